@@ -102,6 +102,8 @@ typedef uint16_t swa_bf16; /* bf16 bit pattern */
 #define SWA_ERR_FP16_RANGE -14    /* device: an input magnitude overflowed the fp16 operand copy */
 #define SWA_ERR_SCRATCH_LAYOUT -15 /* head dim 512: device cannot hold the per-SM tile scratch (see below) */
 #define SWA_ERR_BAD_PLAN -16      /* shared-prefix plan: prompt_len or chosen_len out of range */
+#define SWA_ERR_BAD_ROPE -17      /* norm and rotation: rot_dim, eps, weight_offset or a token stride out of range */
+#define SWA_ERR_BAD_CACHE -18     /* cache rows or prefix_len out of range */
 
 /*
  * Workspace bytes swa_attn_fwd needs for this shape (may be 0; a NULL
@@ -210,6 +212,117 @@ int swa_attn_bwd_sinks(const swa_bf16* q, const swa_bf16* k, const swa_bf16* v, 
                        const float* lse, const swa_bf16* dO, float* dq, float* dk, float* dv, float* dsinks, int B,
                        int Hq, int Hkv, int Lq, int Lk, int D, int window, int causal, float scale, void* workspace,
                        size_t workspace_bytes, void* stream);
+
+/*
+ * Attention of a generation step for a batch that shares a prefix: every
+ * request's queries see the keys of one prefix, stored once for the whole
+ * batch, and of the request's own cache behind it.
+ *
+ *   q         [B, Hq, Lq, D]          bf16, the step's Lq query rows a request
+ *   k_prefix  [Hkv, prefix_rows, D]   bf16, the first prefix_len rows of each
+ *   v_prefix                          head are the prefix; rows behind them are
+ *                                     not read.  prefix_len = 0: may be NULL
+ *   k_own     [B, Hkv, own_rows, D]   bf16, request b's keys at its first
+ *   v_own                             own_len[b] rows; rows behind are not read
+ *   own_len   [B] int32, device       read when the kernels run (a captured
+ *                                     call replays with the lengths of then)
+ *   sinks     [Hq] fp32, device       one sink logit a head (see
+ *                                     swa_attn_fwd_sinks), or NULL
+ *   o         [B, Hq, Lq, D]          bf16
+ *   lse       [B, Hq, Lq]             fp32
+ *
+ * Request b's sequence is [prefix; its own_len[b] keys] and its queries are
+ * that sequence's last Lq positions (the step's own keys are in the cache
+ * before the call): row i sits at a = prefix_len + own_len[b] - Lq + i and
+ * sees the keys j <= a, with a - j < window when window > 0.  This is
+ * swa_attn_fwd_ex on the concatenated sequence of each request, but the
+ * prefix's keys are read once for all requests that fit one block of 64 query
+ * rows, and the requests' lengths differ.
+ *
+ * A row that sees no key (a < 0) gets o = 0 and lse = -inf (with a sink
+ * logit c: lse = c).  A negative own_len[b] marks an empty place of the
+ * batch: its o and lse rows are left as they were.  A length above own_rows
+ * counts as own_rows.  Rows within the lengths must be finite.
+ *
+ * P is rounded to bf16 for the product with v (K and V are read as they are,
+ * as in the decode step of swa_attn_fwd_ex), and o to bf16, the type that a
+ * step's output projection reads; scores, maxima, sums and partial outputs
+ * are fp32.  The result does not depend on what else runs, but it does on the
+ * other requests' lengths, in its last bits: they move the places where the
+ * key ranges are split.  Equal calls give equal bits.
+ *
+ * workspace: at least swa_attn_fwd_workspace_bytes_shared(...) bytes,
+ * 256-byte aligned, with any content; calls that may overlap need separate
+ * ones.  Alignment, streams, status word and other errors are as for
+ * swa_attn_fwd.  SWA_ERR_BAD_CACHE: prefix_len outside [0, prefix_rows] or
+ * own_rows < 1.
+ */
+size_t swa_attn_fwd_workspace_bytes_shared(int B, int Hq, int Hkv, int Lq, int prefix_len, int own_rows, int D,
+                                           int window);
+int swa_attn_fwd_shared(const swa_bf16* q, const swa_bf16* k_prefix, const swa_bf16* v_prefix, const swa_bf16* k_own,
+                        const swa_bf16* v_own, const int32_t* own_len, const float* sinks, swa_bf16* o, float* lse,
+                        int B, int Hq, int Hkv, int Lq, int prefix_len, int prefix_rows, int own_rows, int D,
+                        int window, float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Queries and keys for the calls above from one projection's output: each
+ * head's row normalised, scaled and rotated by its position, and laid out
+ * [B, H, L, D]; values laid out beside them.  For a row x of D elements at
+ * position p, with w = weight + weight_offset (1 where the weight is NULL):
+ *
+ *   u = x (mean(x^2) + eps)^(-1/2) w
+ *   y = u with the pairs of its first rot_dim elements turned by the angles
+ *       p * inv_freq[i] (radians): (u_a cos - u_b sin, u_b cos + u_a sin)
+ *
+ * Pair i is (a, b) = (i, i + rot_dim / 2), or (2 i, 2 i + 1) when interleaved
+ * is not 0; elements from rot_dim on are not turned.
+ *
+ *   q, k, v      bf16, token-major: token t = b * L + l starts at t * stride
+ *                elements (three strides, for a fused projection's slices:
+ *                multiples of 8, at least heads * D), its heads D apart.
+ *                k and v may each be NULL (layers that share another's keys)
+ *   wq, wk       [D] fp32 or NULL
+ *   inv_freq     [rot_dim / 2] fp64; not read when rot_dim = 0
+ *   positions    [B, L] int32, or NULL for pos0 + l (plus kv_len[b] - L)
+ *   kv_len       [B] int32 or NULL.  NULL: k_out and v_out are
+ *                [B, Hkv, kv_rows, D] with token l at row l (kv_rows >= L).
+ *                Otherwise request b's tokens are the last L of its first
+ *                kv_len[b] cache rows: token l goes to row kv_len[b] - L + l
+ *                (rows outside [0, kv_rows) are not written) and, without
+ *                positions, sits at position pos0 + that row
+ *   q_out        [B, Hq, L, D] bf16
+ *
+ * All of them device memory, data 16-byte aligned; outputs may not overlap
+ * inputs.  Angles are exact to 2^-31 of a turn at any position (they are
+ * formed modulo one turn in 64-bit integers from the fp64 frequencies); the
+ * norm, the sums and the rotation are fp32, rounded to bf16 once.  With
+ * kv_len this is the cache update of a generation step whose attention is
+ * swa_attn_fwd_shared with own_len = kv_len and pos0 = prefix_len.
+ * D in {64, 128, 256, 512}; rot_dim a multiple of 16 in [0, D]; eps > 0.
+ * Asynchronous on `stream`; errors as for swa_attn_fwd, and SWA_ERR_BAD_ROPE,
+ * SWA_ERR_BAD_CACHE (kv_rows).
+ *
+ * The backward takes the gradients of q_out, k_out and v_out in fp32 as
+ * swa_attn_bwd writes them (dq [B, Hq, L, D], dk and dv [B, Hkv, L, D]), and
+ * the forward's q, k, weights and positions; it writes the gradients of q, k
+ * and v in bf16 at the same token-major layout (its own three strides), and
+ * of the scales in fp32 (dwq, dwk: [D], or NULL where not wanted).  dk with
+ * k, and dv, may be NULL.  Deterministic: no floating-point atomics.
+ * workspace: swa_attn_qk_rope_bwd_workspace_bytes(B, L, D) bytes, 256-byte
+ * aligned, any content.
+ */
+int swa_attn_qk_rope_fwd(const swa_bf16* q, const swa_bf16* k, const swa_bf16* v, long long q_stride,
+                         long long k_stride, long long v_stride, const float* wq, const float* wk,
+                         const double* inv_freq, const int32_t* positions, const int32_t* kv_len, swa_bf16* q_out,
+                         swa_bf16* k_out, swa_bf16* v_out, int B, int Hq, int Hkv, int L, int D, int kv_rows,
+                         int rot_dim, int interleaved, int pos0, float eps, float weight_offset, void* stream);
+size_t swa_attn_qk_rope_bwd_workspace_bytes(int B, int L, int D);
+int swa_attn_qk_rope_bwd(const swa_bf16* q, const swa_bf16* k, long long q_stride, long long k_stride,
+                         const float* wq, const float* wk, const double* inv_freq, const int32_t* positions,
+                         const float* dq, const float* dk, const float* dv, swa_bf16* dq_in, swa_bf16* dk_in,
+                         swa_bf16* dv_in, long long dq_stride, long long dk_stride, long long dv_stride, float* dwq,
+                         float* dwk, int B, int Hq, int Hkv, int L, int D, int rot_dim, int interleaved, int pos0,
+                         float eps, float weight_offset, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Sequence sharding (context parallelism) with a halo: a sequence split into

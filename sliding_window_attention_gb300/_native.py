@@ -37,6 +37,11 @@ EXPORTED = (
     "swa_attn_add_rows_f32",
     "swa_attn_fwd_sinks",
     "swa_attn_bwd_sinks",
+    "swa_attn_fwd_workspace_bytes_shared",
+    "swa_attn_fwd_shared",
+    "swa_attn_qk_rope_fwd",
+    "swa_attn_qk_rope_bwd_workspace_bytes",
+    "swa_attn_qk_rope_bwd",
 )
 
 _lock = threading.Lock()
@@ -110,6 +115,19 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.swa_attn_fwd_sinks.restype = I
         lib.swa_attn_bwd_sinks.argtypes = [P, P, P, P, P, P, P, P, P, P, P] + shape_ex + [F, P, Z, P]
         lib.swa_attn_bwd_sinks.restype = I
+        # shared prefix: B, Hq, Hkv, Lq, prefix_len, [prefix_rows,] own_rows, D, window
+        lib.swa_attn_fwd_workspace_bytes_shared.argtypes = [I] * 8
+        lib.swa_attn_fwd_workspace_bytes_shared.restype = Z
+        lib.swa_attn_fwd_shared.argtypes = [P] * 9 + [I] * 9 + [F, P, Z, P]
+        lib.swa_attn_fwd_shared.restype = I
+        # per-head norm and rotation: B, Hq, Hkv, L, D, [kv_rows,] rot_dim, interleaved, pos0, eps, weight_offset
+        LL = ctypes.c_longlong
+        lib.swa_attn_qk_rope_fwd.argtypes = [P] * 3 + [LL] * 3 + [P] * 8 + [I] * 9 + [F, F, P]
+        lib.swa_attn_qk_rope_fwd.restype = I
+        lib.swa_attn_qk_rope_bwd_workspace_bytes.argtypes = [I, I, I]
+        lib.swa_attn_qk_rope_bwd_workspace_bytes.restype = Z
+        lib.swa_attn_qk_rope_bwd.argtypes = [P] * 2 + [LL] * 2 + [P] * 10 + [LL] * 3 + [P] * 2 + [I] * 8 + [F, F, P, Z, P]
+        lib.swa_attn_qk_rope_bwd.restype = I
         _lib = lib
         return lib
 
@@ -381,3 +399,263 @@ def backward(q, k, v, o, lse, dO, window: int, scale: float, stream=None, causal
         ws = _workspace(bwd_workspace_bytes_ex(B, Hq, Hkv, Lq, Lk, D, window, causal), q.device)
         swa_attn_bwd_ex(q, k, v, o, lse, dO, dq, dk, dv, window, causal, scale, ws, stream)
     return dq, dk, dv
+
+
+# ---------------------------------------------------------------------------
+# attention over a shared prefix and per-request caches; per-head norm and rotation
+
+
+def _expect(name, t, dtype, shape, device):
+    """t is a dense CUDA tensor of this type and shape on `device` (an index)."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                         f"got {t.dtype} {tuple(t.shape)}{'' if t.is_contiguous() else ' (strided)'}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on the current CUDA device, like the other tensors (got {t.device})")
+
+
+def _current_device(t, name):
+    import torch
+
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device (got {t.device})")
+    return t.get_device()
+
+
+def fwd_workspace_bytes_shared(B, Hq, Hkv, Lq, prefix_len, own_rows, D, window) -> int:
+    return int(load().swa_attn_fwd_workspace_bytes_shared(B, Hq, Hkv, Lq, prefix_len, own_rows, D, window))
+
+
+def swa_attn_fwd_shared(q, k_prefix, v_prefix, k_own, v_own, own_len, sinks, o, lse, window: int, scale: float,
+                        prefix_len=None, workspace=None, stream=None) -> None:
+    """Attention of a generation step over a prefix shared by the batch and
+    each request's own cache (see include/swa_attn.h).  q bf16 [B,Hq,Lq,D];
+    k_prefix, v_prefix bf16 [Hkv,prefix_rows,D] (prefix_len of the rows, all
+    by default); k_own, v_own bf16 [B,Hkv,own_rows,D]; own_len int32 [B];
+    sinks fp32 [Hq] or None; o bf16 like q and lse fp32 [B,Hq,Lq] are
+    caller-allocated outputs."""
+    import torch
+
+    B, Hq, Lq, D = q.shape
+    Hkv, own_rows = k_own.shape[1], k_own.shape[2]
+    prefix_rows = k_prefix.shape[1]
+    dev = _current_device(q, "q")
+    bf16 = torch.bfloat16
+    _expect("q", q, bf16, (B, Hq, Lq, D), dev)
+    _expect("k_prefix", k_prefix, bf16, (Hkv, prefix_rows, D), dev)
+    _expect("v_prefix", v_prefix, bf16, (Hkv, prefix_rows, D), dev)
+    _expect("k_own", k_own, bf16, (B, Hkv, own_rows, D), dev)
+    _expect("v_own", v_own, bf16, (B, Hkv, own_rows, D), dev)
+    _expect("own_len", own_len, torch.int32, (B,), dev)
+    _expect("o", o, bf16, (B, Hq, Lq, D), dev)
+    _expect("lse", lse, torch.float32, (B, Hq, Lq), dev)
+    if sinks is not None:
+        _expect("sinks", sinks, torch.float32, (Hq,), dev)
+    P = prefix_rows if prefix_len is None else int(prefix_len)
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    rc = load().swa_attn_fwd_shared(q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), k_own.data_ptr(),
+                                    v_own.data_ptr(), own_len.data_ptr(), None if sinks is None else sinks.data_ptr(),
+                                    o.data_ptr(), lse.data_ptr(), B, Hq, Hkv, Lq, P, prefix_rows, own_rows, D,
+                                    int(window), float(scale), _ptr(workspace), nbytes, _stream_ptr(stream))
+    if rc:
+        raise SwaError(rc, "swa_attn_fwd_shared")
+
+
+def forward_shared(q, k_prefix, v_prefix, k_own, v_own, own_len, window: int, scale: float, prefix_len=None,
+                   sinks=None, stream=None):
+    """Return (o bf16 [B,Hq,Lq,D], lse fp32 [B,Hq,Lq]) of swa_attn_fwd_shared."""
+    import torch
+
+    B, Hq, Lq, D = q.shape
+    P = k_prefix.shape[1] if prefix_len is None else int(prefix_len)
+    o = torch.empty_like(q)
+    lse = torch.empty((B, Hq, Lq), dtype=torch.float32, device=q.device)
+    ws = _workspace(fwd_workspace_bytes_shared(B, Hq, k_own.shape[1], Lq, P, k_own.shape[2], D, window), q.device)
+    swa_attn_fwd_shared(q, k_prefix, v_prefix, k_own, v_own, own_len, sinks, o, lse, window, scale, P, ws, stream)
+    return o, lse
+
+
+def _token_rows(name, t, B, L, D, device):
+    """(heads, elements between tokens) of a bf16 [B, L, H, D] tensor whose
+    heads are dense within a token (a fused projection's slice)."""
+    import torch
+
+    if t.dtype != torch.bfloat16 or t.dim() != 4 or t.shape[0] != B or t.shape[1] != L or t.shape[3] != D:
+        raise ValueError(f"{name} must be a bf16 tensor [{B}, {L}, heads, {D}], got {t.dtype} {tuple(t.shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on the current CUDA device, like the other tensors (got {t.device})")
+    H = t.shape[2]
+    sb, sl, sh, sd = t.stride()
+    tok = sl if L > 1 else (sb if B > 1 else H * D)
+    if sd != 1 or (H > 1 and sh != D) or (B > 1 and L > 1 and sb != L * sl) or tok < H * D or tok % 8:
+        raise ValueError(f"{name} must hold each token's heads densely, with one stride (a multiple of 8 elements) "
+                         f"between tokens; got strides {t.stride()} of shape {tuple(t.shape)}")
+    return H, tok
+
+
+def _rope_common(q, wq, wk, inv_freq, positions):
+    import torch
+
+    if q.dim() != 4:
+        raise ValueError("q must be [B, L, heads, D]")
+    dev = _current_device(q, "q")
+    B, L, _, D = q.shape
+    for name, w in (("wq", wq), ("wk", wk)):
+        if w is not None:
+            _expect(name, w, torch.float32, (D,), dev)
+    rot = 0
+    if inv_freq is not None:
+        _expect("inv_freq", inv_freq, torch.float64, inv_freq.shape[:1], dev)
+        rot = 2 * inv_freq.shape[0]
+    if positions is not None:
+        _expect("positions", positions, torch.int32, (B, L), dev)
+    return dev, B, L, D, rot
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def swa_attn_qk_rope_fwd(q, k, v, wq, wk, inv_freq, q_out, k_out, v_out, eps: float, positions=None, kv_len=None,
+                         pos0: int = 0, weight_offset: float = 0.0, interleaved: bool = False, stream=None) -> None:
+    """Per-head RMS norm, scale and rotation of q and k, and the layout change
+    of v, through the C ABI (see include/swa_attn.h).  q, k, v: bf16
+    [B,L,heads,D] (slices of a fused projection, or dense); k, v may be None.
+    wq, wk fp32 [D] or None; inv_freq fp64 [rot_dim / 2] or None;
+    q_out bf16 [B,Hq,L,D], k_out and v_out bf16 [B,Hkv,kv_rows,D]."""
+    import torch
+
+    dev, B, L, D, rot = _rope_common(q, wq, wk, inv_freq, positions)
+    Hq, q_tok = _token_rows("q", q, B, L, D, dev)
+    _expect("q_out", q_out, torch.bfloat16, (B, Hq, L, D), dev)
+    Hkv, k_tok, v_tok, rows = 1, 0, 0, L
+    if k is not None:
+        Hkv, k_tok = _token_rows("k", k, B, L, D, dev)
+        rows = k_out.shape[2]
+        _expect("k_out", k_out, torch.bfloat16, (B, Hkv, rows, D), dev)
+    if v is not None:
+        Hv, v_tok = _token_rows("v", v, B, L, D, dev)
+        if k is not None and Hv != Hkv:
+            raise ValueError(f"k has {Hkv} heads and v has {Hv}")
+        Hkv = Hv
+        rows = v_out.shape[2] if k is None else rows
+        _expect("v_out", v_out, torch.bfloat16, (B, Hkv, rows, D), dev)
+    if kv_len is not None:
+        _expect("kv_len", kv_len, torch.int32, (B,), dev)
+    rc = load().swa_attn_qk_rope_fwd(q.data_ptr(), _addr(k), _addr(v), q_tok, k_tok, v_tok, _addr(wq), _addr(wk),
+                                     _addr(inv_freq), _addr(positions), _addr(kv_len), q_out.data_ptr(),
+                                     None if k is None else k_out.data_ptr(), None if v is None else v_out.data_ptr(),
+                                     B, Hq, Hkv, L, D, rows, rot, 1 if interleaved else 0, int(pos0), float(eps),
+                                     float(weight_offset), _stream_ptr(stream))
+    if rc:
+        raise SwaError(rc, "swa_attn_qk_rope_fwd")
+
+
+def qk_rope(q, k, v, wq, wk, inv_freq, eps: float, positions=None, pos0: int = 0, weight_offset: float = 0.0,
+            interleaved: bool = False, stream=None):
+    """Return (q [B,Hq,L,D], k [B,Hkv,L,D], v [B,Hkv,L,D]) for the attention
+    from a projection's bf16 q, k, v [B,L,heads,D]: q and k normalised per
+    head, scaled and rotated by position.  k and v may be None."""
+    import torch
+
+    B, L, Hq, D = q.shape
+    out = [None if t is None else torch.empty((B, t.shape[2], L, D), dtype=q.dtype, device=q.device)
+           for t in (q, k, v)]
+    swa_attn_qk_rope_fwd(q, k, v, wq, wk, inv_freq, *out, eps, positions, None, pos0, weight_offset, interleaved,
+                         stream)
+    return tuple(out)
+
+
+def qk_rope_append(q, k, v, wq, wk, inv_freq, k_cache, v_cache, kv_len, eps: float, positions=None, pos0: int = 0,
+                   weight_offset: float = 0.0, interleaved: bool = False, stream=None):
+    """The same for a generation step: k and v go into rows kv_len[b] - L ..
+    kv_len[b] - 1 of each request's cache [B,Hkv,kv_rows,D] (kv_len int32 [B]
+    counts the step's tokens), which also give their positions, from pos0.
+    Return q [B,Hq,L,D]."""
+    import torch
+
+    B, L, Hq, D = q.shape
+    q_out = torch.empty((B, Hq, L, D), dtype=q.dtype, device=q.device)
+    swa_attn_qk_rope_fwd(q, k, v, wq, wk, inv_freq, q_out, k_cache, v_cache, eps, positions, kv_len, pos0,
+                         weight_offset, interleaved, stream)
+    return q_out
+
+
+def qk_rope_bwd_workspace_bytes(B, L, D) -> int:
+    return int(load().swa_attn_qk_rope_bwd_workspace_bytes(B, L, D))
+
+
+def swa_attn_qk_rope_bwd(q, k, wq, wk, inv_freq, dq, dk, dv, dq_in, dk_in, dv_in, dwq, dwk, eps: float,
+                         positions=None, pos0: int = 0, weight_offset: float = 0.0, interleaved: bool = False,
+                         workspace=None, stream=None) -> None:
+    """Backward of swa_attn_qk_rope_fwd (without kv_len): fp32 dq [B,Hq,L,D],
+    dk, dv [B,Hkv,L,D] to bf16 dq_in, dk_in, dv_in [B,L,heads,D] (which may be
+    slices of a fused buffer) and fp32 dwq, dwk [D] (None: not wanted)."""
+    import torch
+
+    dev, B, L, D, rot = _rope_common(q, wq, wk, inv_freq, positions)
+    f32 = torch.float32
+    Hq, q_tok = _token_rows("q", q, B, L, D, dev)
+    _expect("dq", dq, f32, (B, Hq, L, D), dev)
+
+    def grad_rows(name, t, H):
+        heads, tok = _token_rows(name, t, B, L, D, dev)
+        if heads != H:
+            raise ValueError(f"{name} must have {H} heads, got {heads}")
+        return tok
+
+    gq_tok = grad_rows("dq_in", dq_in, Hq)
+    Hkv, k_tok, gk_tok, gv_tok = 1, 0, 0, 0
+    if k is not None:
+        Hkv, k_tok = _token_rows("k", k, B, L, D, dev)
+        _expect("dk", dk, f32, (B, Hkv, L, D), dev)
+        gk_tok = grad_rows("dk_in", dk_in, Hkv)
+    if dv is not None:
+        Hkv = dv.shape[1] if k is None else Hkv
+        _expect("dv", dv, f32, (B, Hkv, L, D), dev)
+        gv_tok = grad_rows("dv_in", dv_in, Hkv)
+    for name, w in (("dwq", dwq), ("dwk", dwk)):
+        if w is not None:
+            _expect(name, w, f32, (D,), dev)
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    rc = load().swa_attn_qk_rope_bwd(q.data_ptr(), _addr(k), q_tok, k_tok, _addr(wq), _addr(wk), _addr(inv_freq),
+                                     _addr(positions), dq.data_ptr(), None if k is None else dk.data_ptr(), _addr(dv),
+                                     dq_in.data_ptr(), None if k is None else dk_in.data_ptr(),
+                                     None if dv is None else dv_in.data_ptr(), gq_tok, gk_tok, gv_tok, _addr(dwq),
+                                     _addr(dwk), B, Hq, Hkv, L, D, rot, 1 if interleaved else 0, int(pos0),
+                                     float(eps), float(weight_offset), _ptr(workspace), nbytes, _stream_ptr(stream))
+    if rc:
+        raise SwaError(rc, "swa_attn_qk_rope_bwd")
+
+
+def qk_rope_backward(q, k, wq, wk, inv_freq, dq, dk, dv, eps: float, positions=None, pos0: int = 0,
+                     weight_offset: float = 0.0, interleaved: bool = False, stream=None):
+    """Return (d, dwq, dwk): d bf16 [B,L,Hq + Hkv + Hkv,D] is the gradient of
+    the fused projection output (q, k and v heads in that order; the k or v
+    part is left out with k or dv None), dwq and dwk fp32 [D] (None for a
+    None weight)."""
+    import torch
+
+    B, L, Hq, D = q.shape
+    Hk = 0 if k is None else k.shape[2]
+    Hv = 0 if dv is None else dv.shape[1]
+    d = torch.empty((B, L, Hq + Hk + Hv, D), dtype=q.dtype, device=q.device)
+    dwq = None if wq is None else torch.empty_like(wq)
+    dwk = None if wk is None or k is None else torch.empty_like(wk)
+    ws = _workspace(qk_rope_bwd_workspace_bytes(B, L, D), q.device)
+    swa_attn_qk_rope_bwd(q, k, wq, wk, inv_freq, dq, dk, dv, d[:, :, :Hq], d[:, :, Hq:Hq + Hk] if Hk else None,
+                         d[:, :, Hq + Hk:] if Hv else None, dwq, dwk, eps, positions, pos0, weight_offset,
+                         interleaved, ws, stream)
+    return d, dwq, dwk
+
+
+def prefix_positions(B: int, L: int, prompt_len: int, chosen_len: int, device):
+    """Positions int32 [B, L] of a shared-prefix sequence [prompt; chosen;
+    rejected]: the rejected response starts again behind the prompt, as the
+    window of swa_attn_fwd_prefix measures it."""
+    import torch
+
+    p = torch.arange(L, dtype=torch.int32, device=device)
+    if chosen_len > 0:
+        p[prompt_len + chosen_len:] -= chosen_len
+    return p.expand(B, L).contiguous()

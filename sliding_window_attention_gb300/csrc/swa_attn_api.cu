@@ -416,6 +416,11 @@ const char* swa_attn_strerror(int code) {
       return "shared-prefix plan needs prompt_len >= 0, chosen_len >= 0 and prompt_len + chosen_len <= L";
     case SWA_ERR_SCRATCH_LAYOUT:
       return "head dim 512 needs at most one CTA per SM and SM ids below 192 for its per-SM tile scratch";
+    case SWA_ERR_BAD_ROPE:
+      return "rot_dim must be a multiple of 16 in [0, D], eps > 0, weight_offset finite, token strides multiples of 8 "
+             "that hold a token's heads";
+    case SWA_ERR_BAD_CACHE:
+      return "cache rows must be >= 1 (>= L without kv_len) and prefix_len in [0, prefix_rows]";
     case SWA_ERR_NOALLOC_LIMIT:
       return "B*Hq*L exceeds the fixed scratch of swa_attn_bwd_noalloc (2,097,152 rows); use swa_attn_bwd";
     default: return "unknown error code";
@@ -539,6 +544,176 @@ int swa_attn_bwd_sinks(const swa_bf16* q, const swa_bf16* k, const swa_bf16* v, 
   swa::Geom g = make_geom(B, Hq, Hkv, Lq, Lk, D, window, causal, scale);
   g.sinks = sinks;
   return bwd_run(g, q, k, v, o, lse, dO, dq, dk, dv, workspace, workspace_bytes, stream, dsinks);
+}
+
+// Checks of the norm-and-rotation calls shared by the forward and the
+// backward: shapes, strides (in elements) and the rotation's arguments.
+static int check_rope(int B, int Hq, int Hkv, int L, int D, int rot_dim, float eps, float weight_offset,
+                      const double* inv_freq) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || L < 1) return SWA_ERR_BAD_SHAPE;
+  if (D != 64 && D != 128 && D != 256 && D != 512) return SWA_ERR_BAD_HEAD_DIM;
+  if (rot_dim < 0 || rot_dim > D || rot_dim % 16 != 0 || !isfinite(eps) || !(eps > 0.f) || !isfinite(weight_offset))
+    return SWA_ERR_BAD_ROPE;
+  if (rot_dim > 0 && !inv_freq) return SWA_ERR_NULL_POINTER;
+  if ((double)B * L > 2.0e9 || (double)B * L * ((double)Hq + 2.0 * Hkv) * D > 9.0e15) return SWA_ERR_TOO_LARGE;
+  return SWA_OK;
+}
+static bool stride_ok(long long stride, int heads, int D) { return stride % 8 == 0 && stride >= (long long)heads * D; }
+
+static swa::RopeArgs rope_args(const swa_bf16* q, const swa_bf16* k, long long q_stride, long long k_stride,
+                               const float* wq, const float* wk, const double* inv_freq, const int32_t* positions,
+                               const int32_t* kv_len, int B, int Hq, int Hkv, int L, int D, int rot_dim,
+                               int interleaved, int pos0, float eps, float weight_offset) {
+  swa::RopeArgs a;
+  a.q = q;
+  a.k = k;
+  a.q_tok = q_stride;
+  a.k_tok = k_stride;
+  a.wq = wq;
+  a.wk = wk;
+  a.inv_freq = inv_freq;
+  a.positions = positions;
+  a.kv_len = kv_len;
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.L = L;
+  a.D = D;
+  a.rot_dim = rot_dim;
+  a.interleaved = interleaved ? 1 : 0;
+  a.pos0 = pos0;
+  a.eps = eps;
+  a.weight_offset = weight_offset;
+  return a;
+}
+
+int swa_attn_qk_rope_fwd(const swa_bf16* q, const swa_bf16* k, const swa_bf16* v, long long q_stride,
+                         long long k_stride, long long v_stride, const float* wq, const float* wk,
+                         const double* inv_freq, const int32_t* positions, const int32_t* kv_len, swa_bf16* q_out,
+                         swa_bf16* k_out, swa_bf16* v_out, int B, int Hq, int Hkv, int L, int D, int kv_rows,
+                         int rot_dim, int interleaved, int pos0, float eps, float weight_offset, void* stream) {
+  if (!q || !q_out || (k && !k_out) || (v && !v_out)) return SWA_ERR_NULL_POINTER;
+  int rc = check_rope(B, Hq, Hkv, L, D, rot_dim, eps, weight_offset, inv_freq);
+  if (rc) return rc;
+  if (!stride_ok(q_stride, Hq, D) || (k && !stride_ok(k_stride, Hkv, D)) || (v && !stride_ok(v_stride, Hkv, D)))
+    return SWA_ERR_BAD_ROPE;
+  if ((k || v) && (kv_rows < 1 || (!kv_len && kv_rows < L))) return SWA_ERR_BAD_CACHE;
+  if ((double)B * Hkv * kv_rows * D > 9.0e15) return SWA_ERR_TOO_LARGE;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) || !aligned(k_out, 16) ||
+      !aligned(v_out, 16) || !aligned(wq, 4) || !aligned(wk, 4) || !aligned(inv_freq, 8) || !aligned(positions, 4) ||
+      !aligned(kv_len, 4))
+    return SWA_ERR_MISALIGNED;
+  if ((rc = check_device())) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const swa::RopeArgs a = rope_args(q, k, q_stride, k_stride, wq, wk, inv_freq, positions, kv_len, B, Hq, Hkv, L, D,
+                                    rot_dim, interleaved, pos0, eps, weight_offset);
+  const cudaError_t e = launch("qk_rope_fwd", s, [&] {
+    return swa::launch_qk_rope_fwd(a, v, v_stride, q_out, k_out, v_out, kv_rows, s);
+  });
+  return e == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
+}
+
+size_t swa_attn_qk_rope_bwd_workspace_bytes(int B, int L, int D) {
+  if (B < 1 || L < 1 || D < 1 || (double)B * L > 2.0e9) return 0;
+  return round_up((size_t)swa::qk_rope_bwd_ctas((long long)B * L) * 2 * D * sizeof(float), 256);
+}
+
+int swa_attn_qk_rope_bwd(const swa_bf16* q, const swa_bf16* k, long long q_stride, long long k_stride,
+                         const float* wq, const float* wk, const double* inv_freq, const int32_t* positions,
+                         const float* dq, const float* dk, const float* dv, swa_bf16* dq_in, swa_bf16* dk_in,
+                         swa_bf16* dv_in, long long dq_stride, long long dk_stride, long long dv_stride, float* dwq,
+                         float* dwk, int B, int Hq, int Hkv, int L, int D, int rot_dim, int interleaved, int pos0,
+                         float eps, float weight_offset, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q || !dq || !dq_in || (k && (!dk || !dk_in)) || (dv && !dv_in) || (dwk && !k)) return SWA_ERR_NULL_POINTER;
+  int rc = check_rope(B, Hq, Hkv, L, D, rot_dim, eps, weight_offset, inv_freq);
+  if (rc) return rc;
+  if (!stride_ok(q_stride, Hq, D) || !stride_ok(dq_stride, Hq, D) ||
+      (k && (!stride_ok(k_stride, Hkv, D) || !stride_ok(dk_stride, Hkv, D))) || (dv && !stride_ok(dv_stride, Hkv, D)))
+    return SWA_ERR_BAD_ROPE;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16) ||
+      !aligned(dq_in, 16) || !aligned(dk_in, 16) || !aligned(dv_in, 16) || !aligned(wq, 4) || !aligned(wk, 4) ||
+      !aligned(dwq, 4) || !aligned(dwk, 4) || !aligned(inv_freq, 8) || !aligned(positions, 4) ||
+      !aligned(workspace, 256))
+    return SWA_ERR_MISALIGNED;
+  if (!workspace || workspace_bytes < swa_attn_qk_rope_bwd_workspace_bytes(B, L, D)) return SWA_ERR_WORKSPACE;
+  if ((rc = check_device())) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const swa::RopeArgs a = rope_args(q, k, q_stride, k_stride, wq, wk, inv_freq, positions, nullptr, B, Hq, Hkv, L, D,
+                                    rot_dim, interleaved, pos0, eps, weight_offset);
+  const cudaError_t e = launch("qk_rope_bwd", s, [&] {
+    return swa::launch_qk_rope_bwd(a, dq, dk, dv, dq_in, dk_in, dv_in, dq_stride, dk_stride, dv_stride, dwq, dwk,
+                                   static_cast<float*>(workspace), s);
+  });
+  return e == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
+}
+
+// The geometry of a shared-prefix call (shape-checked).
+static swa::SharedGeom shared_geom(int B, int Hq, int Hkv, int Lq, int prefix_len, int prefix_rows, int own_rows,
+                                   int D, int window, float scale) {
+  swa::SharedGeom g;
+  g.B = B;
+  g.Hq = Hq;
+  g.Hkv = Hkv;
+  g.G = Hq / Hkv;
+  g.Lq = Lq;
+  g.M = g.G * Lq;
+  g.P = prefix_len;
+  g.prefix_rows = prefix_rows;
+  g.own_rows = own_rows;
+  g.D = D;
+  // no two positions are further apart than the keys there are
+  g.W = (long long)window >= (long long)prefix_len + own_rows ? 0 : window;
+  g.scale = scale;
+  return g;
+}
+static int check_shared(int B, int Hq, int Hkv, int Lq, int prefix_len, int prefix_rows, int own_rows, int D,
+                        int window, float scale) {
+  const int rc = check_shape(B, Hq, Hkv, Lq, Lq, D, window, scale);
+  if (rc) return rc;
+  if (prefix_len < 0 || prefix_len > prefix_rows || own_rows < 1) return SWA_ERR_BAD_CACHE;
+  if ((long long)prefix_rows + own_rows > 2000000000LL || (long long)(Hq / Hkv) * Lq > 1000000LL ||
+      !swa::shared_fits(shared_geom(B, Hq, Hkv, Lq, prefix_len, prefix_rows, own_rows, D, window, scale)))
+    return SWA_ERR_TOO_LARGE;
+  return SWA_OK;
+}
+
+size_t swa_attn_fwd_workspace_bytes_shared(int B, int Hq, int Hkv, int Lq, int prefix_len, int own_rows, int D,
+                                           int window) {
+  if (check_shared(B, Hq, Hkv, Lq, prefix_len, prefix_len, own_rows, D, window, 1.f)) return 0;
+  return swa::shared_workspace_bytes(shared_geom(B, Hq, Hkv, Lq, prefix_len, prefix_len, own_rows, D, window, 1.f));
+}
+
+int swa_attn_fwd_shared(const swa_bf16* q, const swa_bf16* k_prefix, const swa_bf16* v_prefix, const swa_bf16* k_own,
+                        const swa_bf16* v_own, const int32_t* own_len, const float* sinks, swa_bf16* o, float* lse,
+                        int B, int Hq, int Hkv, int Lq, int prefix_len, int prefix_rows, int own_rows, int D,
+                        int window, float scale, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q || !k_own || !v_own || !own_len || !o || !lse || (prefix_len > 0 && (!k_prefix || !v_prefix)))
+    return SWA_ERR_NULL_POINTER;
+  int rc = check_shared(B, Hq, Hkv, Lq, prefix_len, prefix_rows, own_rows, D, window, scale);
+  if (rc) return rc;
+  if (!aligned(q, 16) || !aligned(k_prefix, 16) || !aligned(v_prefix, 16) || !aligned(k_own, 16) ||
+      !aligned(v_own, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(own_len, 4) || !aligned(sinks, 4) ||
+      !aligned(workspace, 256))
+    return SWA_ERR_MISALIGNED;
+  const swa::SharedGeom g = shared_geom(B, Hq, Hkv, Lq, prefix_len, prefix_rows, own_rows, D, window, scale);
+  if (!workspace || workspace_bytes < swa::shared_workspace_bytes(g)) return SWA_ERR_WORKSPACE;
+  if ((rc = check_device())) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int* status = status_ptr_for_current_device(&rc);
+  if (!status) return rc;
+  swa::SharedArgs a;
+  a.q = q;
+  a.kp = k_prefix;
+  a.vp = v_prefix;
+  a.ko = k_own;
+  a.vo = v_own;
+  a.own_len = own_len;
+  a.sinks = sinks;
+  a.o = o;
+  a.lse = lse;
+  const cudaError_t e =
+      launch("fwd_shared", s, [&] { return swa::launch_fwd_shared(g, a, workspace, status, s); });
+  return e == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
 }
 
 int swa_attn_selftest_timeout(void* stream) {

@@ -265,8 +265,14 @@ cudaError_t make_tmap_f16(CUtensorMap* m, const void* ptr, int D, int L, int hea
 // The same tensor as a 4-D map whose box (64, box_rows, nchunk, 1) loads
 // nchunk 64-column chunks (consecutive [box_rows x 128 B] swizzled blocks)
 // with one TMA instruction; coordinates (0, row, first chunk, head).
+// head_rows > 0: heads are that many rows apart (L of them are read).
 cudaError_t make_tmap_f16_chunks(CUtensorMap* m, const void* ptr, int D, int L, int heads, int box_rows,
-                                 int nchunk);
+                                 int nchunk, int head_rows = 0);
+// A dense [batch, heads, M, D] 16-bit tensor whose box (64, box_rows, 1, 1,
+// nb) packs one head's rows of nb batch entries; coordinates (0, row, chunk,
+// head, first entry).
+cudaError_t make_tmap_rows_5d(CUtensorMap* m, const void* ptr, int D, int M, int heads, int batch, int box_rows,
+                              int nb);
 
 // 3-D fp32 tensor map over an output [heads, L, D] for the D = 512 epilogues:
 // 32 x 32 boxes (128-byte rows) with 128-byte swizzle; TMA stores clip rows
@@ -328,5 +334,56 @@ cudaError_t launch_bwd_dq_tc512(const Geom& g, const uint16_t* q16, const uint16
 cudaError_t launch_bwd_dq_tc(const Geom& g, const uint16_t* q16, const uint16_t* k16, const uint16_t* v16,
                              const uint16_t* g16, const float* stats, int Lpad, float* dq, int* status,
                              cudaStream_t s);
+
+// ---- attention over a shared prefix and per-request caches (shared_prefix.cu) ----
+struct SharedGeom {
+  int B, Hq, Hkv, G, Lq, M;        // M = G * Lq query rows of a request and kv head
+  int P, prefix_rows, own_rows;    // prefix keys, rows between its heads, cache rows of a request
+  int D, W;                        // W = 0: no window
+  float scale;
+};
+// How the query rows are blocked.  Prefix blocks: rows of nb whole requests
+// (nmb == 1), or one of nmb blocks of a request's rows; own blocks of 16 rows.
+struct SharedSplit {
+  int np;          // rows a prefix block may have (the kernel's N): 16 or 64
+  int mb, nb;      // rows of one request in a block, requests in a block
+  int nmb, nrb;    // blocks of a request's rows, prefix blocks of a kv head
+  int nomb;        // own row blocks of a request and kv head
+  int prow, orow;  // rows of a partial's slot (prefix, own)
+};
+struct SharedArgs {
+  const uint16_t *q, *kp, *vp, *ko, *vo;
+  const int* own_len;
+  const float* sinks;
+  uint16_t* o;
+  float* lse;
+};
+SharedSplit shared_split(const SharedGeom& g);
+bool shared_fits(const SharedGeom& g);  // unit and row counts within the kernel's 32-bit indexes
+size_t shared_workspace_bytes(const SharedGeom& g);
+cudaError_t launch_fwd_shared(const SharedGeom& g, const SharedArgs& a, void* ws, int* status, cudaStream_t s);
+
+// ---- per-head norm and rotation of q and k (qk_rope.cu) ----
+// Token-major bf16 inputs (head h of a token at h * D past the token's row)
+// and where the rotation's angles come from; k null: queries only.
+struct RopeArgs {
+  const uint16_t *q, *k;
+  long long q_tok, k_tok;    // elements between tokens
+  const float *wq, *wk;      // [D] or null (unit scale)
+  const double* inv_freq;    // [rot_dim / 2], radians a position
+  const int* positions;      // [B, L] or null: pos0 + index
+  const int* kv_len;         // [B] or null: the tokens are the last L of kv_len[b]
+  int B, Hq, Hkv, L, D, rot_dim, interleaved, pos0;
+  float eps, weight_offset;
+};
+// q to [B, Hq, L, D]; k and v (null: left out) to [B, Hkv, kv_rows, D], rows
+// outside [0, kv_rows) not written.
+cudaError_t launch_qk_rope_fwd(const RopeArgs& a, const uint16_t* v, long long v_tok, uint16_t* qo, uint16_t* ko,
+                               uint16_t* vo, int kv_rows, cudaStream_t s);
+// CTAs of the backward, each of which writes 2 D floats of `part`.
+int qk_rope_bwd_ctas(long long tokens);
+cudaError_t launch_qk_rope_bwd(const RopeArgs& a, const float* dq, const float* dk, const float* dv, uint16_t* gq,
+                               uint16_t* gk, uint16_t* gv, long long gq_tok, long long gk_tok, long long gv_tok,
+                               float* dwq, float* dwk, float* part, cudaStream_t s);
 
 }  // namespace swa

@@ -877,15 +877,32 @@ cudaError_t make_tmap_f16(CUtensorMap* m, const void* ptr, int D, int L, int hea
 // 32 KB instruction sustains about 81 B/clk per SM against 67 for two 16 KB
 // instructions under one barrier (46 for one 16 KB instruction).
 cudaError_t make_tmap_f16_chunks(CUtensorMap* m, const void* ptr, int D, int L, int heads, int box_rows,
-                                 int nchunk) {
+                                 int nchunk, int head_rows) {
   auto enc = encode_fn();
   if (!enc) return cudaErrorNotSupported;
   if (nchunk < 1 || nchunk > D / 64) return cudaErrorInvalidValue;
   cuuint64_t dims[4] = {64, (cuuint64_t)L, (cuuint64_t)(D / 64), (cuuint64_t)heads};
-  cuuint64_t strides[3] = {(cuuint64_t)D * 2, 128, (cuuint64_t)D * L * 2};
+  cuuint64_t strides[3] = {(cuuint64_t)D * 2, 128, (cuuint64_t)D * (head_rows > 0 ? head_rows : L) * 2};
   cuuint32_t box[4] = {64, (cuuint32_t)box_rows, (cuuint32_t)nchunk, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// 5-D view (64 elements, M rows, D / 64 chunks, heads, batch) of a dense
+// [batch, heads, M, D] tensor: a box (64, box_rows, 1, 1, nb) packs one
+// head's rows of nb batch entries behind one another.
+cudaError_t make_tmap_rows_5d(CUtensorMap* m, const void* ptr, int D, int M, int heads, int batch, int box_rows,
+                              int nb) {
+  auto enc = encode_fn();
+  if (!enc) return cudaErrorNotSupported;
+  cuuint64_t dims[5] = {64, (cuuint64_t)M, (cuuint64_t)(D / 64), (cuuint64_t)heads, (cuuint64_t)batch};
+  cuuint64_t strides[4] = {(cuuint64_t)D * 2, 128, (cuuint64_t)D * M * 2, (cuuint64_t)D * M * heads * 2};
+  cuuint32_t box[5] = {64, (cuuint32_t)box_rows, 1, 1, (cuuint32_t)nb};
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, const_cast<void*>(ptr), dims, strides, box, estr,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
