@@ -7,6 +7,7 @@ missing or was not built, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -57,6 +58,8 @@ class SwaError(RuntimeError):
 def load(path: str | None = None) -> ctypes.CDLL:
     """Load the shared library (once).  Raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -164,8 +167,10 @@ def _stream_ptr(stream):
     if stream is None:
         import torch
 
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        # the handle alone: torch.cuda.current_stream() builds a Stream object
+        # around it, which took 2.9 us of a call's 10 to 20 on the GB300's host
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _dims(q, k, D=None):
@@ -403,15 +408,20 @@ def backward(q, k, v, o, lse, dO, window: int, scale: float, stream=None, causal
 
 # ---------------------------------------------------------------------------
 # attention over a shared prefix and per-request caches; per-head norm and rotation
+#
+# A generation step calls these with tensors of a few KB, where the host's
+# time is what counts: the checks are one pass over (name, tensor, type,
+# shape), and workspace sizes are remembered by shape.
 
 
-def _expect(name, t, dtype, shape, device):
-    """t is a dense CUDA tensor of this type and shape on `device` (an index)."""
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
-                         f"got {t.dtype} {tuple(t.shape)}{'' if t.is_contiguous() else ' (strided)'}")
-    if t.get_device() != device:
-        raise ValueError(f"{name} must be on the current CUDA device, like the other tensors (got {t.device})")
+def _check(device, specs):
+    """Every tensor dense, on `device` (an index) and of its type and shape."""
+    for name, t, dtype, shape in specs:
+        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                             f"got {t.dtype} {tuple(t.shape)}{'' if t.is_contiguous() else ' (strided)'}")
+        if t.get_device() != device:
+            raise ValueError(f"{name} must be on the current CUDA device, like the other tensors (got {t.device})")
 
 
 def _current_device(t, name):
@@ -422,8 +432,36 @@ def _current_device(t, name):
     return t.get_device()
 
 
+@functools.lru_cache(maxsize=256)
 def fwd_workspace_bytes_shared(B, Hq, Hkv, Lq, prefix_len, own_rows, D, window) -> int:
     return int(load().swa_attn_fwd_workspace_bytes_shared(B, Hq, Hkv, Lq, prefix_len, own_rows, D, window))
+
+
+def _check_shared(q, k_prefix, v_prefix, k_own, v_own, own_len, sinks):
+    import torch
+
+    B, Hq, Lq, D = q.shape
+    _, Hkv, own_rows, _ = k_own.shape
+    prefix_rows = k_prefix.shape[1]
+    dev, bf16 = _current_device(q, "q"), torch.bfloat16
+    prefix, own = (Hkv, prefix_rows, D), (B, Hkv, own_rows, D)
+    _check(dev, (("q", q, bf16, (B, Hq, Lq, D)), ("k_prefix", k_prefix, bf16, prefix),
+                 ("v_prefix", v_prefix, bf16, prefix), ("k_own", k_own, bf16, own), ("v_own", v_own, bf16, own),
+                 ("own_len", own_len, torch.int32, (B,))))
+    if sinks is not None:
+        _check(dev, (("sinks", sinks, torch.float32, (Hq,)),))
+    return dev, B, Hq, Hkv, Lq, D, prefix_rows, own_rows
+
+
+def _run_shared(dims, q, k_prefix, v_prefix, k_own, v_own, own_len, sinks, o, lse, window, scale, P, ws, nbytes,
+                stream):
+    _, B, Hq, Hkv, Lq, D, prefix_rows, own_rows = dims
+    rc = load().swa_attn_fwd_shared(q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), k_own.data_ptr(),
+                                    v_own.data_ptr(), own_len.data_ptr(), None if sinks is None else sinks.data_ptr(),
+                                    o.data_ptr(), lse.data_ptr(), B, Hq, Hkv, Lq, P, prefix_rows, own_rows, D, window,
+                                    scale, None if ws is None else ws.data_ptr(), nbytes, _stream_ptr(stream))
+    if rc:
+        raise SwaError(rc, "swa_attn_fwd_shared")
 
 
 def swa_attn_fwd_shared(q, k_prefix, v_prefix, k_own, v_own, own_len, sinks, o, lse, window: int, scale: float,
@@ -436,29 +474,12 @@ def swa_attn_fwd_shared(q, k_prefix, v_prefix, k_own, v_own, own_len, sinks, o, 
     caller-allocated outputs."""
     import torch
 
-    B, Hq, Lq, D = q.shape
-    Hkv, own_rows = k_own.shape[1], k_own.shape[2]
-    prefix_rows = k_prefix.shape[1]
-    dev = _current_device(q, "q")
-    bf16 = torch.bfloat16
-    _expect("q", q, bf16, (B, Hq, Lq, D), dev)
-    _expect("k_prefix", k_prefix, bf16, (Hkv, prefix_rows, D), dev)
-    _expect("v_prefix", v_prefix, bf16, (Hkv, prefix_rows, D), dev)
-    _expect("k_own", k_own, bf16, (B, Hkv, own_rows, D), dev)
-    _expect("v_own", v_own, bf16, (B, Hkv, own_rows, D), dev)
-    _expect("own_len", own_len, torch.int32, (B,), dev)
-    _expect("o", o, bf16, (B, Hq, Lq, D), dev)
-    _expect("lse", lse, torch.float32, (B, Hq, Lq), dev)
-    if sinks is not None:
-        _expect("sinks", sinks, torch.float32, (Hq,), dev)
-    P = prefix_rows if prefix_len is None else int(prefix_len)
+    dims = _check_shared(q, k_prefix, v_prefix, k_own, v_own, own_len, sinks)
+    _check(dims[0], (("o", o, torch.bfloat16, q.shape), ("lse", lse, torch.float32, q.shape[:3])))
+    P = k_prefix.shape[1] if prefix_len is None else int(prefix_len)
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    rc = load().swa_attn_fwd_shared(q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), k_own.data_ptr(),
-                                    v_own.data_ptr(), own_len.data_ptr(), None if sinks is None else sinks.data_ptr(),
-                                    o.data_ptr(), lse.data_ptr(), B, Hq, Hkv, Lq, P, prefix_rows, own_rows, D,
-                                    int(window), float(scale), _ptr(workspace), nbytes, _stream_ptr(stream))
-    if rc:
-        raise SwaError(rc, "swa_attn_fwd_shared")
+    _run_shared(dims, q, k_prefix, v_prefix, k_own, v_own, own_len, sinks, o, lse, int(window), float(scale), P,
+                workspace, nbytes, stream)
 
 
 def forward_shared(q, k_prefix, v_prefix, k_own, v_own, own_len, window: int, scale: float, prefix_len=None,
@@ -466,12 +487,16 @@ def forward_shared(q, k_prefix, v_prefix, k_own, v_own, own_len, window: int, sc
     """Return (o bf16 [B,Hq,Lq,D], lse fp32 [B,Hq,Lq]) of swa_attn_fwd_shared."""
     import torch
 
-    B, Hq, Lq, D = q.shape
-    P = k_prefix.shape[1] if prefix_len is None else int(prefix_len)
+    dims = _check_shared(q, k_prefix, v_prefix, k_own, v_own, own_len, sinks)
+    dev, B, Hq, Hkv, Lq, D, prefix_rows, own_rows = dims
+    P, window = prefix_rows if prefix_len is None else int(prefix_len), int(window)
+    nbytes = fwd_workspace_bytes_shared(B, Hq, Hkv, Lq, P, own_rows, D, window)
+    device = q.device
     o = torch.empty_like(q)
-    lse = torch.empty((B, Hq, Lq), dtype=torch.float32, device=q.device)
-    ws = _workspace(fwd_workspace_bytes_shared(B, Hq, k_own.shape[1], Lq, P, k_own.shape[2], D, window), q.device)
-    swa_attn_fwd_shared(q, k_prefix, v_prefix, k_own, v_own, own_len, sinks, o, lse, window, scale, P, ws, stream)
+    lse = torch.empty((B, Hq, Lq), dtype=torch.float32, device=device)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    _run_shared(dims, q, k_prefix, v_prefix, k_own, v_own, own_len, sinks, o, lse, window, float(scale), P, ws,
+                nbytes, stream)
     return o, lse
 
 
@@ -480,16 +505,17 @@ def _token_rows(name, t, B, L, D, device):
     heads are dense within a token (a fused projection's slice)."""
     import torch
 
-    if t.dtype != torch.bfloat16 or t.dim() != 4 or t.shape[0] != B or t.shape[1] != L or t.shape[3] != D:
-        raise ValueError(f"{name} must be a bf16 tensor [{B}, {L}, heads, {D}], got {t.dtype} {tuple(t.shape)}")
+    shape = t.shape
+    if t.dtype is not torch.bfloat16 or len(shape) != 4 or shape[0] != B or shape[1] != L or shape[3] != D:
+        raise ValueError(f"{name} must be a bf16 tensor [{B}, {L}, heads, {D}], got {t.dtype} {tuple(shape)}")
     if t.get_device() != device:
         raise ValueError(f"{name} must be on the current CUDA device, like the other tensors (got {t.device})")
-    H = t.shape[2]
+    H = shape[2]
     sb, sl, sh, sd = t.stride()
     tok = sl if L > 1 else (sb if B > 1 else H * D)
     if sd != 1 or (H > 1 and sh != D) or (B > 1 and L > 1 and sb != L * sl) or tok < H * D or tok % 8:
         raise ValueError(f"{name} must hold each token's heads densely, with one stride (a multiple of 8 elements) "
-                         f"between tokens; got strides {t.stride()} of shape {tuple(t.shape)}")
+                         f"between tokens; got strides {t.stride()} of shape {tuple(shape)}")
     return H, tok
 
 
@@ -500,16 +526,11 @@ def _rope_common(q, wq, wk, inv_freq, positions):
         raise ValueError("q must be [B, L, heads, D]")
     dev = _current_device(q, "q")
     B, L, _, D = q.shape
-    for name, w in (("wq", wq), ("wk", wk)):
-        if w is not None:
-            _expect(name, w, torch.float32, (D,), dev)
-    rot = 0
-    if inv_freq is not None:
-        _expect("inv_freq", inv_freq, torch.float64, inv_freq.shape[:1], dev)
-        rot = 2 * inv_freq.shape[0]
-    if positions is not None:
-        _expect("positions", positions, torch.int32, (B, L), dev)
-    return dev, B, L, D, rot
+    f32 = torch.float32
+    _check(dev, [s for s in (("wq", wq, f32, (D,)), ("wk", wk, f32, (D,)),
+                             ("inv_freq", inv_freq, torch.float64, None if inv_freq is None else inv_freq.shape[:1]),
+                             ("positions", positions, torch.int32, (B, L))) if s[1] is not None])
+    return dev, B, L, D, 0 if inv_freq is None else 2 * inv_freq.shape[0]
 
 
 def _addr(t):
@@ -526,27 +547,29 @@ def swa_attn_qk_rope_fwd(q, k, v, wq, wk, inv_freq, q_out, k_out, v_out, eps: fl
     import torch
 
     dev, B, L, D, rot = _rope_common(q, wq, wk, inv_freq, positions)
+    bf16 = torch.bfloat16
     Hq, q_tok = _token_rows("q", q, B, L, D, dev)
-    _expect("q_out", q_out, torch.bfloat16, (B, Hq, L, D), dev)
+    outs = [("q_out", q_out, bf16, (B, Hq, L, D))]
     Hkv, k_tok, v_tok, rows = 1, 0, 0, L
     if k is not None:
         Hkv, k_tok = _token_rows("k", k, B, L, D, dev)
         rows = k_out.shape[2]
-        _expect("k_out", k_out, torch.bfloat16, (B, Hkv, rows, D), dev)
+        outs.append(("k_out", k_out, bf16, (B, Hkv, rows, D)))
     if v is not None:
         Hv, v_tok = _token_rows("v", v, B, L, D, dev)
         if k is not None and Hv != Hkv:
             raise ValueError(f"k has {Hkv} heads and v has {Hv}")
         Hkv = Hv
         rows = v_out.shape[2] if k is None else rows
-        _expect("v_out", v_out, torch.bfloat16, (B, Hkv, rows, D), dev)
+        outs.append(("v_out", v_out, bf16, (B, Hkv, rows, D)))
     if kv_len is not None:
-        _expect("kv_len", kv_len, torch.int32, (B,), dev)
+        outs.append(("kv_len", kv_len, torch.int32, (B,)))
+    _check(dev, outs)
     rc = load().swa_attn_qk_rope_fwd(q.data_ptr(), _addr(k), _addr(v), q_tok, k_tok, v_tok, _addr(wq), _addr(wk),
                                      _addr(inv_freq), _addr(positions), _addr(kv_len), q_out.data_ptr(),
                                      None if k is None else k_out.data_ptr(), None if v is None else v_out.data_ptr(),
-                                     B, Hq, Hkv, L, D, rows, rot, 1 if interleaved else 0, int(pos0), float(eps),
-                                     float(weight_offset), _stream_ptr(stream))
+                                     B, Hq, Hkv, L, D, rows, rot, 1 if interleaved else 0, pos0, eps, weight_offset,
+                                     _stream_ptr(stream))
     if rc:
         raise SwaError(rc, "swa_attn_qk_rope_fwd")
 
@@ -558,9 +581,9 @@ def qk_rope(q, k, v, wq, wk, inv_freq, eps: float, positions=None, pos0: int = 0
     head, scaled and rotated by position.  k and v may be None."""
     import torch
 
-    B, L, Hq, D = q.shape
-    out = [None if t is None else torch.empty((B, t.shape[2], L, D), dtype=q.dtype, device=q.device)
-           for t in (q, k, v)]
+    B, L, _, D = q.shape
+    dtype, device = q.dtype, q.device
+    out = [None if t is None else torch.empty((B, t.shape[2], L, D), dtype=dtype, device=device) for t in (q, k, v)]
     swa_attn_qk_rope_fwd(q, k, v, wq, wk, inv_freq, *out, eps, positions, None, pos0, weight_offset, interleaved,
                          stream)
     return tuple(out)
@@ -581,8 +604,40 @@ def qk_rope_append(q, k, v, wq, wk, inv_freq, k_cache, v_cache, kv_len, eps: flo
     return q_out
 
 
+@functools.lru_cache(maxsize=256)
 def qk_rope_bwd_workspace_bytes(B, L, D) -> int:
     return int(load().swa_attn_qk_rope_bwd_workspace_bytes(B, L, D))
+
+
+def _check_rope_bwd(q, k, wq, wk, inv_freq, dq, dk, dv, positions):
+    import torch
+
+    dev, B, L, D, rot = _rope_common(q, wq, wk, inv_freq, positions)
+    f32 = torch.float32
+    Hq, q_tok = _token_rows("q", q, B, L, D, dev)
+    grads = [("dq", dq, f32, (B, Hq, L, D))]
+    Hkv, k_tok = 1, 0
+    if k is not None:
+        Hkv, k_tok = _token_rows("k", k, B, L, D, dev)
+        grads.append(("dk", dk, f32, (B, Hkv, L, D)))
+    if dv is not None:
+        Hkv = dv.shape[1] if k is None else Hkv
+        grads.append(("dv", dv, f32, (B, Hkv, L, D)))
+    _check(dev, grads)
+    return dev, B, L, D, rot, Hq, Hkv, q_tok, k_tok
+
+
+def _run_rope_bwd(dims, q, k, wq, wk, inv_freq, dq, dk, dv, outs, toks, dwq, dwk, eps, positions, pos0,
+                  weight_offset, interleaved, ws, nbytes, stream):
+    """outs, toks: addresses of the q, k and v gradients' first rows and the elements between their tokens."""
+    _, B, L, D, rot, Hq, Hkv, q_tok, k_tok = dims
+    rc = load().swa_attn_qk_rope_bwd(q.data_ptr(), _addr(k), q_tok, k_tok, _addr(wq), _addr(wk), _addr(inv_freq),
+                                     _addr(positions), dq.data_ptr(), None if k is None else dk.data_ptr(), _addr(dv),
+                                     *outs, *toks, _addr(dwq), _addr(dwk), B, Hq, Hkv, L, D, rot,
+                                     1 if interleaved else 0, pos0, eps, weight_offset, _addr(ws), nbytes,
+                                     _stream_ptr(stream))
+    if rc:
+        raise SwaError(rc, "swa_attn_qk_rope_bwd")
 
 
 def swa_attn_qk_rope_bwd(q, k, wq, wk, inv_freq, dq, dk, dv, dq_in, dk_in, dv_in, dwq, dwk, eps: float,
@@ -593,39 +648,20 @@ def swa_attn_qk_rope_bwd(q, k, wq, wk, inv_freq, dq, dk, dv, dq_in, dk_in, dv_in
     slices of a fused buffer) and fp32 dwq, dwk [D] (None: not wanted)."""
     import torch
 
-    dev, B, L, D, rot = _rope_common(q, wq, wk, inv_freq, positions)
-    f32 = torch.float32
-    Hq, q_tok = _token_rows("q", q, B, L, D, dev)
-    _expect("dq", dq, f32, (B, Hq, L, D), dev)
-
-    def grad_rows(name, t, H):
-        heads, tok = _token_rows(name, t, B, L, D, dev)
+    dims = _check_rope_bwd(q, k, wq, wk, inv_freq, dq, dk, dv, positions)
+    dev, B, L, D, _, Hq, Hkv, _, _ = dims
+    outs, toks = [], []
+    for name, t, H in (("dq_in", dq_in, Hq), ("dk_in", None if k is None else dk_in, Hkv),
+                       ("dv_in", None if dv is None else dv_in, Hkv)):
+        heads, tok = (H, 0) if t is None else _token_rows(name, t, B, L, D, dev)
         if heads != H:
             raise ValueError(f"{name} must have {H} heads, got {heads}")
-        return tok
-
-    gq_tok = grad_rows("dq_in", dq_in, Hq)
-    Hkv, k_tok, gk_tok, gv_tok = 1, 0, 0, 0
-    if k is not None:
-        Hkv, k_tok = _token_rows("k", k, B, L, D, dev)
-        _expect("dk", dk, f32, (B, Hkv, L, D), dev)
-        gk_tok = grad_rows("dk_in", dk_in, Hkv)
-    if dv is not None:
-        Hkv = dv.shape[1] if k is None else Hkv
-        _expect("dv", dv, f32, (B, Hkv, L, D), dev)
-        gv_tok = grad_rows("dv_in", dv_in, Hkv)
-    for name, w in (("dwq", dwq), ("dwk", dwk)):
-        if w is not None:
-            _expect(name, w, f32, (D,), dev)
+        outs.append(_addr(t))
+        toks.append(tok)
+    _check(dev, [(n, w, torch.float32, (D,)) for n, w in (("dwq", dwq), ("dwk", dwk)) if w is not None])
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    rc = load().swa_attn_qk_rope_bwd(q.data_ptr(), _addr(k), q_tok, k_tok, _addr(wq), _addr(wk), _addr(inv_freq),
-                                     _addr(positions), dq.data_ptr(), None if k is None else dk.data_ptr(), _addr(dv),
-                                     dq_in.data_ptr(), None if k is None else dk_in.data_ptr(),
-                                     None if dv is None else dv_in.data_ptr(), gq_tok, gk_tok, gv_tok, _addr(dwq),
-                                     _addr(dwk), B, Hq, Hkv, L, D, rot, 1 if interleaved else 0, int(pos0),
-                                     float(eps), float(weight_offset), _ptr(workspace), nbytes, _stream_ptr(stream))
-    if rc:
-        raise SwaError(rc, "swa_attn_qk_rope_bwd")
+    _run_rope_bwd(dims, q, k, wq, wk, inv_freq, dq, dk, dv, outs, toks, dwq, dwk, eps, positions, pos0,
+                  weight_offset, interleaved, workspace, nbytes, stream)
 
 
 def qk_rope_backward(q, k, wq, wk, inv_freq, dq, dk, dv, eps: float, positions=None, pos0: int = 0,
@@ -636,16 +672,20 @@ def qk_rope_backward(q, k, wq, wk, inv_freq, dq, dk, dv, eps: float, positions=N
     None weight)."""
     import torch
 
-    B, L, Hq, D = q.shape
-    Hk = 0 if k is None else k.shape[2]
-    Hv = 0 if dv is None else dv.shape[1]
-    d = torch.empty((B, L, Hq + Hk + Hv, D), dtype=q.dtype, device=q.device)
+    dims = _check_rope_bwd(q, k, wq, wk, inv_freq, dq, dk, dv, positions)
+    _, B, L, D, _, Hq, Hkv, _, _ = dims
+    device = q.device
+    Hk, Hv = (0 if k is None else Hkv), (0 if dv is None else Hkv)
+    H = Hq + Hk + Hv
+    d = torch.empty((B, L, H, D), dtype=torch.bfloat16, device=device)
     dwq = None if wq is None else torch.empty_like(wq)
     dwk = None if wk is None or k is None else torch.empty_like(wk)
-    ws = _workspace(qk_rope_bwd_workspace_bytes(B, L, D), q.device)
-    swa_attn_qk_rope_bwd(q, k, wq, wk, inv_freq, dq, dk, dv, d[:, :, :Hq], d[:, :, Hq:Hq + Hk] if Hk else None,
-                         d[:, :, Hq + Hk:] if Hv else None, dwq, dwk, eps, positions, pos0, weight_offset,
-                         interleaved, ws, stream)
+    nbytes = qk_rope_bwd_workspace_bytes(B, L, D)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    at, row = d.data_ptr(), 2 * D  # bytes of a head's row
+    outs = (at, at + Hq * row if Hk else None, at + (Hq + Hk) * row if Hv else None)
+    _run_rope_bwd(dims, q, k, wq, wk, inv_freq, dq, dk, dv, outs, (H * D,) * 3, dwq, dwk, eps, positions, pos0,
+                  weight_offset, interleaved, ws, nbytes, stream)
     return d, dwq, dwk
 
 

@@ -27,11 +27,13 @@
 #include <stdint.h>
 
 #include "swa_internal.h"
+#include "tc_ptx.cuh"
 
 namespace swa {
 namespace {
 
 constexpr int kThr = 256, kWarps = kThr / 32;
+constexpr long long kStagedTokens = 1024;  // from here on the forward stages its rows through shared memory
 
 // A row is held by LPR lanes, E elements each in NV vectors of 8 (16 bytes of
 // bf16): vector j of lane l holds elements 256 j + 8 l ... + 7, so that every
@@ -114,13 +116,14 @@ struct LaneRot {
   int src[C::NV], srcv[C::NV];
 
   __device__ __forceinline__ void place(int lane, int pairs) {
-    if (INTER) return;
+    if constexpr (!INTER) {
 #pragma unroll
-    for (int j = 0; j < C::NV; ++j) {
-      const int d = 256 * j + 8 * (lane % C::LPR);
-      const int pd = d < pairs ? d + pairs : (d < 2 * pairs ? d - pairs : d);
-      src[j] = (lane & ~(C::LPR - 1)) | ((pd % (C::LPR * 8)) >> 3);
-      srcv[j] = C::NV > 1 ? pd / 256 : 0;
+      for (int j = 0; j < C::NV; ++j) {
+        const int d = 256 * j + 8 * (lane % C::LPR);
+        const int pd = d < pairs ? d + pairs : (d < 2 * pairs ? d - pairs : d);
+        src[j] = (lane & ~(C::LPR - 1)) | ((pd % (C::LPR * 8)) >> 3);
+        srcv[j] = C::NV > 1 ? pd / 256 : 0;
+      }
     }
   }
   __device__ __forceinline__ void load(const float2* cs, int lane, int pairs) {
@@ -291,147 +294,374 @@ __global__ void __launch_bounds__(kThr) qk_rope_fwd_kernel(const RopeFwd p) {
   }
 }
 
-struct RopeBwd {
-  const uint16_t *q, *k;                 // the forward's inputs; k may be null
-  long long q_tok, k_tok;
-  const float *wq, *wk;                  // [D] or null
-  RopePos pos;
-  const float *dq, *dk, *dv;             // [B, H, L, D]; dk, dv may be null
-  uint16_t *gq, *gk, *gv;                // gradient rows, token-major
-  long long gq_tok, gk_tok, gv_tok;
-  float* part;                           // [gridDim.x][2][D] partial dw
-  int B, L, Hq, Hkv;
-  float eps, off;
+// ---------------------------------------------------------------------------
+// Long sequences: rows staged through shared memory by TMA.
+//
+// Both directions move a few bytes a multiplication, so what bounds them is
+// the memory's latency: the bytes in flight.  A producer thread keeps a ring of
+// stages filled -- a stage is 512 / D heads of 8 consecutive tokens, x as the
+// projection laid it out ([token][head][D]) and, in the backward, dy as the
+// attention did ([head][token][D]); the boxes of two tensor maps -- and eight
+// consumer warps, one a token, work from there.  A stage's units (token group,
+// block of heads) form one list that the CTAs share out evenly.
+//
+// A lane holds E = 8 (16 at D = 512) elements of a row in NG groups of 4, D / NG
+// apart: with the whole head rotated in halves an element's partner is then in
+// the same lane, and a warp's loads of a group are contiguous.
+constexpr int kTok = 8;  // tokens of a stage, one a consumer warp
+
+template <int D>
+struct StCfg {
+  static constexpr int HB = 512 / D;        // heads of a stage
+  static constexpr int E = D == 512 ? 16 : 8;
+  static constexpr int NG = E / 4, GS = D / NG;
+  static constexpr int LPR = D / E, RPW = 32 / LPR, ITER = HB / RPW;
+  static constexpr int XB = kTok * 512 * 2, YB = kTok * 512 * 4;
 };
 
-// Persistent: a CTA walks blocks of kWarps consecutive tokens, a warp a
-// token; the scales' gradients stay in registers until the end and leave as
-// one partial sum a CTA, so their order of summation is fixed by the launch.
+// The order of a CTA's stages: units [u0, u1) of groups x (Hq, Hkv, Hkv heads in blocks).
+struct StList {
+  int nq, nk, nv, per;     // blocks of q, k, v heads, and of a group
+  int groups, gl;          // token groups, of a batch entry
+  __device__ __forceinline__ void split(int cta, int ctas, int& u0, int& u1) const {
+    const long long u = (long long)groups * per;
+    u0 = (int)(u * cta / ctas);
+    u1 = (int)(u * (cta + 1) / ctas);
+  }
+};
+
+struct StRope {
+  StList list;
+  RopePos pos;
+  const float *wq, *wk;
+  uint16_t *qo, *ko, *vo;         // forward outputs
+  uint16_t *gq, *gk, *gv;         // backward outputs, token-major
+  long long gq_tok, gk_tok, gv_tok;
+  float* part;                    // [gridDim.x][2][D] partial dw
+  int B, L, Hq, Hkv, kv_rows;
+  float eps, off;
+  int* status;
+};
+
+// The partners' elements of a row in shared memory whose own elements are in
+// registers (own[E]); ld(d, v) loads elements d .. d + 3.
+template <int D, bool INTER, typename F>
+__device__ __forceinline__ void row_partners(const float (&own)[StCfg<D>::E], float (&other)[StCfg<D>::E], int d4,
+                                             int pairs, F&& ld) {
+  using C = StCfg<D>;
+  if constexpr (INTER) {
+#pragma unroll
+    for (int e = 0; e < C::E; ++e) other[e] = own[e ^ 1];
+  } else {
+    if (2 * pairs == D) {
+#pragma unroll
+      for (int e = 0; e < C::E; ++e) other[e] = own[(e + C::E / 2) % C::E];
+    } else {
+#pragma unroll
+      for (int g = 0; g < C::NG; ++g) {
+        const int d = C::GS * g + d4;
+        ld(d < pairs ? d + pairs : (d < 2 * pairs ? d - pairs : d), other + 4 * g);
+      }
+    }
+  }
+}
+// cos, and +-sin as y_e = cos u_e + s_e u_partner(e), of the lane's elements.
 template <int D, bool INTER>
-__global__ void __launch_bounds__(kThr) qk_rope_bwd_kernel(const RopeBwd p) {
-  using C = RowCfg<D>;
-  constexpr int NV = C::NV, E = C::E, LPR = C::LPR, RPW = C::RPW;
-  extern __shared__ uint64_t sm[];
-  uint64_t* step = sm;
-  float2* cs = reinterpret_cast<float2*>(sm + p.pos.pairs);
-  const int pairs = p.pos.pairs, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long n_tok = (long long)p.B * p.L;
-  const int sub = lane / LPR, d0 = 8 * (lane % LPR);
-  for (int i = threadIdx.x; i < pairs; i += kThr) step[i] = turn_step(p.pos.inv_freq[i]);
-  LaneRot<D, INTER> rot;
-  rot.place(lane, pairs);
-  float accq[E], acck[E];
+__device__ __forceinline__ void lane_angles(const float2* cs, int d4, int pairs, float (&c)[StCfg<D>::E],
+                                            float (&s)[StCfg<D>::E]) {
+  using C = StCfg<D>;
 #pragma unroll
-  for (int e = 0; e < E; ++e) accq[e] = acck[e] = 0.f;
+  for (int g = 0; g < C::NG; ++g) {
+    const int d = C::GS * g + d4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool in = d < 2 * pairs, lo = INTER ? (i & 1) == 0 : d < pairs;
+      const float2 v = in ? cs[INTER ? (d + i) / 2 : (lo ? d + i : d - pairs + i)] : make_float2(1.f, 0.f);
+      c[4 * g + i] = v.x;
+      s[4 * g + i] = lo ? -v.y : v.y;
+    }
+  }
+}
+__device__ __forceinline__ void ld_bf4(const uint16_t* p, float* x) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  x[0] = bf_lo(v.x);
+  x[1] = bf_hi(v.x);
+  x[2] = bf_lo(v.y);
+  x[3] = bf_hi(v.y);
+}
+__device__ __forceinline__ void ld_f4(const float* p, float* x) {
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  x[0] = v.x;
+  x[1] = v.y;
+  x[2] = v.z;
+  x[3] = v.w;
+}
+__device__ __forceinline__ uint2 pack4(const float* x) { return make_uint2(bf_pack(x[0], x[1]), bf_pack(x[2], x[3])); }
 
-  for (long long tok0 = (long long)blockIdx.x * kWarps; tok0 < n_tok; tok0 += (long long)gridDim.x * kWarps) {
-    __syncthreads();  // step[] is written; the last block's cs[] is consumed
-    fill_cs(p.pos, tok0, kWarps, n_tok, p.L, step, cs);
-    __syncthreads();
-    const long long tok = tok0 + warp;
-    if (tok >= n_tok) continue;
-    const int b = (int)(tok / p.L), l = (int)(tok % p.L);
-    rot.load(cs + warp * pairs, lane, pairs);
+// Shared memory of a staged kernel: NS stages, then weights, turn steps, the
+// warps' cos / sin tables and the barriers.
+template <int D, bool BWD>
+struct StSmem {
+  using C = StCfg<D>;
+  static constexpr int STAGE = C::XB + (BWD ? C::YB : 0);
+  static constexpr int NS = BWD ? (D == 512 ? 8 : 4) : 8;
+  static constexpr int OFF_W = NS * STAGE;              // [2][D] scales
+  static constexpr int OFF_STEP = OFF_W + 2 * D * 4;    // [D / 2]
+  static constexpr int OFF_CS = OFF_STEP + D / 2 * 8;   // [kTok][D / 2]
+  static constexpr int OFF_BAR = OFF_CS + kTok * D / 2 * 8;
+  static constexpr size_t BYTES = (size_t)OFF_BAR + 256 + 128;
+  static constexpr int CTAS = BWD && D == 512 ? 1 : 2;  // per SM
+  static_assert(CTAS * BYTES <= 228 * 1024 - CTAS * 1024, "shared memory");
+  static_assert(!BWD || NS * STAGE >= kTok * D * 4, "the scales' gradients are reduced in the stages");
+};
 
-    auto rows = [&](const uint16_t* x, const float* w, const float* dy, uint16_t* out, int H, float (&acc)[E]) {
-      float we[E];
+template <int D, bool INTER, bool BWD>
+__global__ void __launch_bounds__(kThr + 32, StSmem<D, BWD>::CTAS)
+    qk_rope_staged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                          const __grid_constant__ CUtensorMap tmV,   // forward: v's rows
+                          const __grid_constant__ CUtensorMap tmDQ, const __grid_constant__ CUtensorMap tmDK,
+                          const __grid_constant__ CUtensorMap tmDV, const __grid_constant__ StRope p) {
+  using C = StCfg<D>;
+  using M = StSmem<D, BWD>;
+  constexpr int E = C::E, NG = C::NG, GS = C::GS, HB = C::HB, NS = M::NS;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  float* sw = reinterpret_cast<float*>(base + M::OFF_W);
+  uint64_t* step = reinterpret_cast<uint64_t*>(base + M::OFF_STEP);
+  uint64_t* full = reinterpret_cast<uint64_t*>(base + M::OFF_BAR);  // [NS]
+  uint64_t* empty = full + NS;                                      // [NS]
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + NS);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, pairs = p.pos.pairs;
+  const StList& ls = p.list;
+  int u0, u1;
+  ls.split(blockIdx.x, gridDim.x, u0, u1);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS; ++i) {
+      tc::mbar_init(full + i, 1);
+      tc::mbar_init(empty + i, kTok);
+    }
+    *abort_flag = 0;
+    tc::fence_mbar_init();
+  }
+  for (int i = threadIdx.x; i < pairs; i += kThr + 32) step[i] = turn_step(p.pos.inv_freq[i]);
+  for (int i = threadIdx.x; i < 2 * D; i += kThr + 32) {
+    const float* w = i < D ? p.wq : p.wk;
+    sw[i] = w ? w[i < D ? i : i - D] + p.off : 1.f;
+  }
+  __syncthreads();
+
+  float accq[BWD ? E : 1], acck[BWD ? E : 1];
 #pragma unroll
-      for (int e = 0; e < E; ++e) we[e] = w ? w[256 * (e >> 3) + d0 + (e & 7)] + p.off : 1.f;
-#pragma unroll 2
-      for (int hg = 0; hg < H; hg += RPW) {
-        const int h = hg + sub;
-        const bool in = h < H;
-        float f[E], g[E], gp[E];
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          const uint4 raw = in ? __ldcs(reinterpret_cast<const uint4*>(x + (size_t)h * D + 256 * j + d0)) : make_uint4(0, 0, 0, 0);
-          const float4* dyp = reinterpret_cast<const float4*>(dy + (size_t)h * p.L * D + 256 * j + d0);
-          const float4 a = in ? __ldcs(dyp) : make_float4(0.f, 0.f, 0.f, 0.f);
-          const float4 c = in ? __ldcs(dyp + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
-          unpack8(raw, f + 8 * j);
-          g[8 * j] = a.x; g[8 * j + 1] = a.y; g[8 * j + 2] = a.z; g[8 * j + 3] = a.w;
-          g[8 * j + 4] = c.x; g[8 * j + 5] = c.y; g[8 * j + 6] = c.z; g[8 * j + 7] = c.w;
-        }
-        // the rotation's transpose: c_e dy_e - s_e dy_partner(e)
-        if constexpr (INTER) {
-#pragma unroll
-          for (int e = 0; e < E; ++e) gp[e] = g[e ^ 1];
-        } else {
-          rot.partners(g, gp, pairs);
-        }
-        float ss = 0.f, dot = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          g[e] = fmaf(rot.c[e], g[e], -rot.s[e] * gp[e]);
-          ss = fmaf(f[e], f[e], ss);
-          dot = fmaf(g[e] * we[e], f[e], dot);
-        }
-        ss = row_sum<LPR>(ss);
-        dot = row_sum<LPR>(dot);
-        const float r = rsqrtf(ss * (1.f / D) + p.eps);
-        const float m = dot * r * r * (1.f / D);  // mean(h n) r
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          acc[e] = fmaf(g[e] * r, f[e], acc[e]);
-          g[e] = r * (g[e] * we[e] - f[e] * m);
-        }
-        if (in) {
-#pragma unroll
-          for (int j = 0; j < NV; ++j) *reinterpret_cast<uint4*>(out + (size_t)h * D + 256 * j + d0) = pack8(g + 8 * j);
+  for (int e = 0; e < (BWD ? E : 1); ++e) accq[e] = acck[e] = 0.f;
+
+  if (warp == kTok) {
+    // ------------------------------------------------------------ producer
+    if (tc::elect_one()) {
+      int n = 0;
+      for (int u = u0; u < u1; ++u, ++n) {
+        const int s = n % NS, grp = u / ls.per, i = u - grp * ls.per;
+        if (n >= NS && !tc::mbar_wait(empty + s, ((n / NS) & 1) ^ 1, abort_flag)) break;
+        const int b = grp / ls.gl, l0 = (grp - b * ls.gl) * kTok;
+        const int kind = i < ls.nq ? 0 : (i < ls.nq + ls.nk ? 1 : 2);
+        const int h0 = (i - (kind > 0 ? ls.nq : 0) - (kind > 1 ? ls.nk : 0)) * HB;
+        unsigned char* x = base + s * M::STAGE;
+        // D = 512 rows are two halves of 256 (a box is at most 256 wide)
+        const bool has_x = !BWD || kind < 2;
+        tc::mbar_arrive_expect_tx(full + s, (has_x ? C::XB : 0) + (BWD ? C::YB : 0));
+        if (has_x) tc::tma_load_4d(x, kind == 0 ? &tmQ : (kind == 1 ? &tmK : &tmV), full + s, 0, D == 512 ? 2 * h0 : h0, l0, b);
+        if (BWD) {
+          const CUtensorMap* m = kind == 0 ? &tmDQ : (kind == 1 ? &tmDK : &tmDV);
+          if (D == 512) tc::tma_load_5d(x + C::XB, m, full + s, 0, 0, l0, h0, b);
+          else tc::tma_load_4d(x + C::XB, m, full + s, 0, l0, h0, b);
         }
       }
-    };
-    rows(p.q + tok * p.q_tok, p.wq, p.dq + ((size_t)b * p.Hq * p.L + l) * D, p.gq + tok * p.gq_tok, p.Hq, accq);
-    if (p.k) rows(p.k + tok * p.k_tok, p.wk, p.dk + ((size_t)b * p.Hkv * p.L + l) * D, p.gk + tok * p.gk_tok, p.Hkv, acck);
-    if (p.dv) {
-      for (int h = sub; h < p.Hkv; h += RPW)
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          const float4* dvp = reinterpret_cast<const float4*>(p.dv + (((size_t)b * p.Hkv + h) * p.L + l) * D + 256 * j + d0);
-          const float4 a = __ldcs(dvp), c = __ldcs(dvp + 1);
-          const float y[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
-          *reinterpret_cast<uint4*>(p.gv + tok * p.gv_tok + (size_t)h * D + 256 * j + d0) = pack8(y);
+      if (*abort_flag) tc::drain_ring(full, NS, n);
+    }
+  } else {
+    // ------------------------------------------------------------ one token a warp
+    float2* cs = reinterpret_cast<float2*>(base + M::OFF_CS) + warp * (D / 2);
+    const int sub = lane / C::LPR, d4 = 4 * (lane % C::LPR);
+    float a[E], q[E];  // forward: cos w and +-sin w of the partner; backward: cos, +-sin
+    float we[BWD ? E : 1];
+    int last_grp = -1, last_kind = -1, b = 0, l = 0, kv_row = 0;
+    bool live = false, kv_ok = false;
+    int n = 0;
+    for (int u = u0; u < u1; ++u, ++n) {
+      const int s = n % NS, grp = u / ls.per, i = u - grp * ls.per;
+      const int kind = i < ls.nq ? 0 : (i < ls.nq + ls.nk ? 1 : 2);
+      const int h0 = (i - (kind > 0 ? ls.nq : 0) - (kind > 1 ? ls.nk : 0)) * HB;
+      if (grp != last_grp) {
+        b = grp / ls.gl;
+        l = (grp - b * ls.gl) * kTok + warp;
+        live = l < p.L;
+        kv_row = p.pos.kv_len ? (live ? p.pos.kv_len[b] - p.L + l : -1) : l;
+        kv_ok = kv_row >= 0 && kv_row < p.kv_rows;
+        __syncwarp();
+        if (live) {
+          const long long pos = token_pos(p.pos, b, l, p.L);
+          for (int k = lane; k < pairs; k += 32) cs[k] = turn_cs(pos, step[k]);
         }
+        __syncwarp();
+        last_kind = -1;
+        last_grp = grp;
+      }
+      if (kind != last_kind && kind < 2) {
+        const float* w = sw + kind * D;
+        lane_angles<D, INTER>(cs, d4, pairs, a, q);
+        float wv[E];
+#pragma unroll
+        for (int g = 0; g < NG; ++g) ld_f4(w + GS * g + d4, wv + 4 * g);
+        if constexpr (BWD) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) we[e] = wv[e];
+        } else {
+          float wp[E];
+          row_partners<D, INTER>(wv, wp, d4, pairs, [&](int d, float* v) { ld_f4(w + d, v); });
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            a[e] *= wv[e];
+            q[e] *= wp[e];
+          }
+        }
+        last_kind = kind;
+      }
+      if (!__all_sync(0xffffffffu, tc::mbar_wait(full + s, (n / NS) & 1, abort_flag))) break;
+      const int H = kind == 0 ? p.Hq : p.Hkv;
+      const uint16_t* xs = reinterpret_cast<const uint16_t*>(base + s * M::STAGE) + warp * 512;  // [head][D] of the token
+      const float* ys = reinterpret_cast<const float*>(base + s * M::STAGE + C::XB) + warp * D;  // [head][token][D]
+      if (live) {
+#pragma unroll
+        for (int it = 0; it < C::ITER; ++it) {
+          const int r = it * C::RPW + sub, h = h0 + r;
+          const bool in = h < H;
+          if constexpr (!BWD) {
+            const uint16_t* x = xs + r * D;
+            if (kind == 2) {
+              if (in && kv_ok) {
+                uint16_t* out = p.vo + (((size_t)b * p.Hkv + h) * p.kv_rows + kv_row) * D;
+#pragma unroll
+                for (int g = 0; g < NG; ++g)
+                  *reinterpret_cast<uint2*>(out + GS * g + d4) = *reinterpret_cast<const uint2*>(x + GS * g + d4);
+              }
+              continue;
+            }
+            float f[E], o[E];
+#pragma unroll
+            for (int g = 0; g < NG; ++g) ld_bf4(x + GS * g + d4, f + 4 * g);
+            row_partners<D, INTER>(f, o, d4, pairs, [&](int d, float* v) { ld_bf4(x + d, v); });
+            float ss = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) ss = fmaf(f[e], f[e], ss);
+            const float rn = rsqrtf(row_sum<C::LPR>(ss) * (1.f / D) + p.eps);
+#pragma unroll
+            for (int e = 0; e < E; ++e) f[e] = rn * fmaf(f[e], a[e], o[e] * q[e]);
+            if (in && (kind == 0 || kv_ok)) {
+              uint16_t* out = kind == 0 ? p.qo + (((size_t)b * p.Hq + h) * p.L + l) * D
+                                        : p.ko + (((size_t)b * p.Hkv + h) * p.kv_rows + kv_row) * D;
+#pragma unroll
+              for (int g = 0; g < NG; ++g) *reinterpret_cast<uint2*>(out + GS * g + d4) = pack4(f + 4 * g);
+            }
+          } else {
+            const float* y = ys + r * (kTok * D);
+            const long long tok = (long long)b * p.L + l;
+            float g4[E];
+#pragma unroll
+            for (int g = 0; g < NG; ++g) ld_f4(y + GS * g + d4, g4 + 4 * g);
+            if (kind == 2) {
+              if (in) {
+                uint16_t* out = p.gv + tok * p.gv_tok + (size_t)h * D;
+#pragma unroll
+                for (int g = 0; g < NG; ++g) *reinterpret_cast<uint2*>(out + GS * g + d4) = pack4(g4 + 4 * g);
+              }
+              continue;
+            }
+            const uint16_t* x = xs + r * D;
+            float f[E], o[E];
+            row_partners<D, INTER>(g4, o, d4, pairs, [&](int d, float* v) { ld_f4(y + d, v); });
+#pragma unroll
+            for (int g = 0; g < NG; ++g) ld_bf4(x + GS * g + d4, f + 4 * g);
+            float ss = 0.f, dot = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+              g4[e] = fmaf(a[e], g4[e], -q[e] * o[e]);  // the rotation's transpose
+              ss = fmaf(f[e], f[e], ss);
+              dot = fmaf(g4[e] * we[e], f[e], dot);
+            }
+            ss = row_sum<C::LPR>(ss);
+            dot = row_sum<C::LPR>(dot);
+            const float rn = rsqrtf(ss * (1.f / D) + p.eps);
+            const float m = dot * rn * rn * (1.f / D);  // mean(h n) r
+            if (in) {
+#pragma unroll
+              for (int e = 0; e < E; ++e) {
+                const float t = g4[e] * rn * f[e];
+                if (kind == 0) accq[e] += t;
+                else acck[e] += t;
+                g4[e] = rn * fmaf(g4[e], we[e], -f[e] * m);
+              }
+              uint16_t* out = (kind == 0 ? p.gq + tok * p.gq_tok : p.gk + tok * p.gk_tok) + (size_t)h * D;
+#pragma unroll
+              for (int g = 0; g < NG; ++g) *reinterpret_cast<uint2*>(out + GS * g + d4) = pack4(g4 + 4 * g);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(empty + s);
     }
   }
 
-  // this CTA's dw: the warp's row slots, then the warps, in a fixed order
   __syncthreads();
-  float* red = reinterpret_cast<float*>(sm);  // [kWarps][D]
+  if (*abort_flag) {
+    if (threadIdx.x == 0) atomicCAS(p.status, 0, kStatusTimeout);
+    return;
+  }
+  if constexpr (BWD) {
+    // this CTA's dw: a warp's row slots, then the warps, in a fixed order (in
+    // the stages' memory: every load has been consumed)
+    float* red = reinterpret_cast<float*>(base);  // [kTok][D]
+    const int sub = lane / C::LPR, d4 = 4 * (lane % C::LPR);
 #pragma unroll
-  for (int kind = 0; kind < 2; ++kind) {
+    for (int kind = 0; kind < 2; ++kind) {
+      if (warp < kTok) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      float v = kind ? acck[e] : accq[e];
+        for (int e = 0; e < E; ++e) {
+          float v = kind ? acck[e] : accq[e];
 #pragma unroll
-      for (int o = LPR; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (sub == 0) red[warp * D + 256 * (e >> 3) + d0 + (e & 7)] = v;
+          for (int o = C::LPR; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+          if (sub == 0) red[warp * D + GS * (e >> 2) + d4 + (e & 3)] = v;
+        }
+      }
+      __syncthreads();
+      for (int d = threadIdx.x; d < D; d += kThr + 32) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kTok; ++w) v += red[w * D + d];
+        p.part[((size_t)blockIdx.x * 2 + kind) * D + d] = v;
+      }
+      __syncthreads();
     }
-    __syncthreads();
-    for (int d = threadIdx.x; d < D; d += kThr) {
-      float v = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) v += red[w * D + d];
-      p.part[((size_t)blockIdx.x * 2 + kind) * D + d] = v;
-    }
-    __syncthreads();
   }
 }
 
-// dw[kind][d] = sum of the CTAs' partials, 8 strided sums a column, then those.
-__global__ void __launch_bounds__(256) qk_rope_dw_kernel(const float* part, float* dwq, float* dwk, int D, int n) {
-  __shared__ float red[8][32];
-  const int col = blockIdx.x * 32 + (threadIdx.x & 31), grp = threadIdx.x >> 5;  // column of [2][D]
+// dw[kind][d] = sum of the CTAs' partials: 32 strided sums a column, then those.
+__global__ void __launch_bounds__(1024) qk_rope_dw_kernel(const float* part, float* dwq, float* dwk, int D, int n) {
+  __shared__ float red[32][33];
+  const int x = threadIdx.x & 31, grp = threadIdx.x >> 5, col = blockIdx.x * 32 + x;  // column of [2][D]
+  tc::grid_dependency_wait();
   float v = 0.f;
-#pragma unroll 8
-  for (int c = grp; c < n; c += 8) v += part[(size_t)c * 2 * D + col];
-  red[grp][threadIdx.x & 31] = v;
+#pragma unroll 5
+  for (int c = grp; c < n; c += 32) v += part[(size_t)c * 2 * D + col];
+  red[grp][x] = v;
   __syncthreads();
-  if (grp == 0) {
+  v = red[x][grp];
 #pragma unroll
-    for (int g = 1; g < 8; ++g) v += red[g][threadIdx.x];
-    float* out = col < D ? dwq : dwk;
-    if (out) out[col < D ? col : col - D] = v;
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (x == 0) {
+    const int c = blockIdx.x * 32 + grp;
+    float* out = c < D ? dwq : dwk;
+    if (out) out[c < D ? c : c - D] = v;
   }
 }
 
@@ -442,18 +672,6 @@ cudaError_t rope_fwd_d(const RopeFwd& p, cudaStream_t s) {
   const size_t smem = (size_t)p.pos.pairs * 8 * (1 + p.T);
   if (p.pos.interleaved) qk_rope_fwd_kernel<D, true><<<grid, kThr, smem, s>>>(p);
   else qk_rope_fwd_kernel<D, false><<<grid, kThr, smem, s>>>(p);
-  return cudaGetLastError();
-}
-
-template <int D>
-cudaError_t rope_bwd_d(const RopeBwd& p, int grid, float* dwq, float* dwk, cudaStream_t s) {
-  const size_t cs = (size_t)p.pos.pairs * 8 * (1 + kWarps), red = (size_t)kWarps * D * 4;
-  const size_t smem = cs > red ? cs : red;
-  if (p.pos.interleaved) qk_rope_bwd_kernel<D, true><<<grid, kThr, smem, s>>>(p);
-  else qk_rope_bwd_kernel<D, false><<<grid, kThr, smem, s>>>(p);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || (!dwq && !dwk)) return e;
-  qk_rope_dw_kernel<<<2 * D / 32, 256, 0, s>>>(p.part, dwq, dwk, D, grid);
   return cudaGetLastError();
 }
 
@@ -468,17 +686,110 @@ RopePos rope_pos(const RopeArgs& a) {
   return r;
 }
 
-constexpr int kBwdCtasPerSm = 2;
+StRope staged_params(const RopeArgs& a, bool v, int* status) {
+  StRope p = {};
+  const int hb = 512 / a.D;
+  p.list.nq = (a.Hq + hb - 1) / hb;
+  p.list.nk = a.k ? (a.Hkv + hb - 1) / hb : 0;
+  p.list.nv = v ? (a.Hkv + hb - 1) / hb : 0;
+  p.list.per = p.list.nq + p.list.nk + p.list.nv;
+  p.list.gl = (a.L + kTok - 1) / kTok;
+  p.list.groups = a.B * p.list.gl;
+  p.pos = rope_pos(a);
+  p.wq = a.wq;
+  p.wk = a.wk;
+  p.B = a.B;
+  p.L = a.L;
+  p.Hq = a.Hq;
+  p.Hkv = a.Hkv;
+  p.eps = a.eps;
+  p.off = a.weight_offset;
+  p.status = status;
+  return p;
+}
+
+template <int D, bool BWD>
+int staged_ctas(const StList& l) {
+  const long long u = (long long)l.groups * l.per, most = 152 * StSmem<D, BWD>::CTAS;
+  return (int)(u < most ? u : most);
+}
+template <int D, bool INTER, bool BWD>
+cudaError_t staged_launch(const StRope& p, const CUtensorMap (&m)[6], int grid, cudaStream_t s) {
+  auto kern = qk_rope_staged_kernel<D, INTER, BWD>;
+  const size_t smem = StSmem<D, BWD>::BYTES;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kThr + 32, smem, s>>>(m[0], m[1], m[2], m[3], m[4], m[5], p);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t staged_fwd(const RopeArgs& a, const uint16_t* v, long long v_tok, const StRope& p, cudaStream_t s) {
+  CUtensorMap m[6];
+  cudaError_t e = make_tmap_tokens(&m[0], a.q, D, a.Hq, a.L, a.B, a.q_tok, kTok, StCfg<D>::HB);
+  if (e == cudaSuccess && a.k) e = make_tmap_tokens(&m[1], a.k, D, a.Hkv, a.L, a.B, a.k_tok, kTok, StCfg<D>::HB);
+  if (e == cudaSuccess && v) e = make_tmap_tokens(&m[2], v, D, a.Hkv, a.L, a.B, v_tok, kTok, StCfg<D>::HB);
+  if (e != cudaSuccess) return e;
+  if (!a.k) m[1] = m[0];  // not read
+  if (!v) m[2] = m[0];
+  m[3] = m[4] = m[5] = m[0];
+  const int grid = staged_ctas<D, false>(p.list);
+  return a.interleaved ? staged_launch<D, true, false>(p, m, grid, s) : staged_launch<D, false, false>(p, m, grid, s);
+}
+
+template <int D>
+cudaError_t staged_bwd(const RopeArgs& a, const float* dq, const float* dk, const float* dv, const StRope& p,
+                       float* dwq, float* dwk, cudaStream_t s) {
+  CUtensorMap m[6];
+  cudaError_t e = make_tmap_tokens(&m[0], a.q, D, a.Hq, a.L, a.B, a.q_tok, kTok, StCfg<D>::HB);
+  if (e == cudaSuccess) e = make_tmap_f32_tokens(&m[3], dq, D, a.Hq, a.L, a.B, kTok, StCfg<D>::HB);
+  if (e == cudaSuccess && a.k) e = make_tmap_tokens(&m[1], a.k, D, a.Hkv, a.L, a.B, a.k_tok, kTok, StCfg<D>::HB);
+  if (e == cudaSuccess && a.k) e = make_tmap_f32_tokens(&m[4], dk, D, a.Hkv, a.L, a.B, kTok, StCfg<D>::HB);
+  if (e == cudaSuccess && dv) e = make_tmap_f32_tokens(&m[5], dv, D, a.Hkv, a.L, a.B, kTok, StCfg<D>::HB);
+  if (e != cudaSuccess) return e;
+  if (!a.k) {  // not read
+    m[1] = m[0];
+    m[4] = m[3];
+  }
+  if (!dv) m[5] = m[3];
+  m[2] = m[0];
+  const int grid = staged_ctas<D, true>(p.list);
+  e = a.interleaved ? staged_launch<D, true, true>(p, m, grid, s) : staged_launch<D, false, true>(p, m, grid, s);
+  if (e != cudaSuccess || (!dwq && !dwk)) return e;
+  // the partials' sum, launched as a programmatic dependent of the main kernel
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * D / 32);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, qk_rope_dw_kernel, static_cast<const float*>(p.part), dwq, dwk, D, grid);
+}
 
 }  // namespace
 
-int qk_rope_bwd_ctas(long long tokens) {
-  const long long blocks = (tokens + kWarps - 1) / kWarps;
-  return (int)(blocks < 152 * kBwdCtasPerSm ? blocks : 152 * kBwdCtasPerSm);
-}
+size_t qk_rope_bwd_part_floats(int D) { return (size_t)152 * 2 * 2 * D; }
 
 cudaError_t launch_qk_rope_fwd(const RopeArgs& a, const uint16_t* v, long long v_tok, uint16_t* qo, uint16_t* ko,
-                               uint16_t* vo, int kv_rows, cudaStream_t s) {
+                               uint16_t* vo, int kv_rows, int* status, cudaStream_t s) {
+  const long long n_tok = (long long)a.B * a.L;
+  if (a.L >= kTok && n_tok >= kStagedTokens) {
+    StRope p = staged_params(a, v != nullptr, status);
+    p.qo = qo;
+    p.ko = ko;
+    p.vo = vo;
+    p.kv_rows = kv_rows;
+    switch (a.D) {
+      case 64: return staged_fwd<64>(a, v, v_tok, p, s);
+      case 128: return staged_fwd<128>(a, v, v_tok, p, s);
+      case 256: return staged_fwd<256>(a, v, v_tok, p, s);
+      case 512: return staged_fwd<512>(a, v, v_tok, p, s);
+      default: return cudaErrorInvalidValue;
+    }
+  }
   RopeFwd p;
   p.q = a.q;
   p.k = a.k;
@@ -499,7 +810,6 @@ cudaError_t launch_qk_rope_fwd(const RopeArgs& a, const uint16_t* v, long long v
   p.kv_rows = kv_rows;
   p.eps = a.eps;
   p.off = a.weight_offset;
-  const long long n_tok = (long long)a.B * a.L;
   p.T = n_tok >= 4096 ? 4 : 1;
   switch (a.D) {
     case 64: return rope_fwd_d<64>(p, s);
@@ -512,18 +822,8 @@ cudaError_t launch_qk_rope_fwd(const RopeArgs& a, const uint16_t* v, long long v
 
 cudaError_t launch_qk_rope_bwd(const RopeArgs& a, const float* dq, const float* dk, const float* dv, uint16_t* gq,
                                uint16_t* gk, uint16_t* gv, long long gq_tok, long long gk_tok, long long gv_tok,
-                               float* dwq, float* dwk, float* part, cudaStream_t s) {
-  RopeBwd p;
-  p.q = a.q;
-  p.k = a.k;
-  p.q_tok = a.q_tok;
-  p.k_tok = a.k_tok;
-  p.wq = a.wq;
-  p.wk = a.wk;
-  p.pos = rope_pos(a);
-  p.dq = dq;
-  p.dk = dk;
-  p.dv = dv;
+                               float* dwq, float* dwk, float* part, int* status, cudaStream_t s) {
+  StRope p = staged_params(a, dv != nullptr, status);
   p.gq = gq;
   p.gk = gk;
   p.gv = gv;
@@ -531,18 +831,11 @@ cudaError_t launch_qk_rope_bwd(const RopeArgs& a, const float* dq, const float* 
   p.gk_tok = gk_tok;
   p.gv_tok = gv_tok;
   p.part = part;
-  p.B = a.B;
-  p.L = a.L;
-  p.Hq = a.Hq;
-  p.Hkv = a.Hkv;
-  p.eps = a.eps;
-  p.off = a.weight_offset;
-  const int grid = qk_rope_bwd_ctas((long long)a.B * a.L);
   switch (a.D) {
-    case 64: return rope_bwd_d<64>(p, grid, dwq, dwk, s);
-    case 128: return rope_bwd_d<128>(p, grid, dwq, dwk, s);
-    case 256: return rope_bwd_d<256>(p, grid, dwq, dwk, s);
-    case 512: return rope_bwd_d<512>(p, grid, dwq, dwk, s);
+    case 64: return staged_bwd<64>(a, dq, dk, dv, p, dwq, dwk, s);
+    case 128: return staged_bwd<128>(a, dq, dk, dv, p, dwq, dwk, s);
+    case 256: return staged_bwd<256>(a, dq, dk, dv, p, dwq, dwk, s);
+    case 512: return staged_bwd<512>(a, dq, dk, dv, p, dwq, dwk, s);
     default: return cudaErrorInvalidValue;
   }
 }

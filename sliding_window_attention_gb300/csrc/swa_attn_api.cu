@@ -555,7 +555,7 @@ static int check_rope(int B, int Hq, int Hkv, int L, int D, int rot_dim, float e
   if (rot_dim < 0 || rot_dim > D || rot_dim % 16 != 0 || !isfinite(eps) || !(eps > 0.f) || !isfinite(weight_offset))
     return SWA_ERR_BAD_ROPE;
   if (rot_dim > 0 && !inv_freq) return SWA_ERR_NULL_POINTER;
-  if ((double)B * L > 2.0e9 || (double)B * L * ((double)Hq + 2.0 * Hkv) * D > 9.0e15) return SWA_ERR_TOO_LARGE;
+  if ((double)B * L * (Hq + 2.0 * Hkv) > 2.0e9 || (double)B * L * ((double)Hq + 2.0 * Hkv) * D > 9.0e15) return SWA_ERR_TOO_LARGE;
   return SWA_OK;
 }
 static bool stride_ok(long long stride, int heads, int D) { return stride % 8 == 0 && stride >= (long long)heads * D; }
@@ -605,17 +605,19 @@ int swa_attn_qk_rope_fwd(const swa_bf16* q, const swa_bf16* k, const swa_bf16* v
     return SWA_ERR_MISALIGNED;
   if ((rc = check_device())) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int* status = status_ptr_for_current_device(&rc);
+  if (!status) return rc;
   const swa::RopeArgs a = rope_args(q, k, q_stride, k_stride, wq, wk, inv_freq, positions, kv_len, B, Hq, Hkv, L, D,
                                     rot_dim, interleaved, pos0, eps, weight_offset);
   const cudaError_t e = launch("qk_rope_fwd", s, [&] {
-    return swa::launch_qk_rope_fwd(a, v, v_stride, q_out, k_out, v_out, kv_rows, s);
+    return swa::launch_qk_rope_fwd(a, v, v_stride, q_out, k_out, v_out, kv_rows, status, s);
   });
   return e == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
 }
 
 size_t swa_attn_qk_rope_bwd_workspace_bytes(int B, int L, int D) {
   if (B < 1 || L < 1 || D < 1 || (double)B * L > 2.0e9) return 0;
-  return round_up((size_t)swa::qk_rope_bwd_ctas((long long)B * L) * 2 * D * sizeof(float), 256);
+  return round_up(swa::qk_rope_bwd_part_floats(D) * sizeof(float), 256);
 }
 
 int swa_attn_qk_rope_bwd(const swa_bf16* q, const swa_bf16* k, long long q_stride, long long k_stride,
@@ -638,11 +640,13 @@ int swa_attn_qk_rope_bwd(const swa_bf16* q, const swa_bf16* k, long long q_strid
   if (!workspace || workspace_bytes < swa_attn_qk_rope_bwd_workspace_bytes(B, L, D)) return SWA_ERR_WORKSPACE;
   if ((rc = check_device())) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int* status = status_ptr_for_current_device(&rc);
+  if (!status) return rc;
   const swa::RopeArgs a = rope_args(q, k, q_stride, k_stride, wq, wk, inv_freq, positions, nullptr, B, Hq, Hkv, L, D,
                                     rot_dim, interleaved, pos0, eps, weight_offset);
   const cudaError_t e = launch("qk_rope_bwd", s, [&] {
     return swa::launch_qk_rope_bwd(a, dq, dk, dv, dq_in, dk_in, dv_in, dq_stride, dk_stride, dv_stride, dwq, dwk,
-                                   static_cast<float*>(workspace), s);
+                                   static_cast<float*>(workspace), status, s);
   });
   return e == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
 }

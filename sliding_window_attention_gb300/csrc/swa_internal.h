@@ -274,6 +274,17 @@ cudaError_t make_tmap_f16_chunks(CUtensorMap* m, const void* ptr, int D, int L, 
 cudaError_t make_tmap_rows_5d(CUtensorMap* m, const void* ptr, int D, int M, int heads, int batch, int box_rows,
                               int nb);
 
+// Token-major bf16 rows [batch, L, tok elements], H heads of D dense in each:
+// box of `toks` tokens x `hb` heads as [token][head][D].  Coordinates (0,
+// head, token, batch entry), at D = 512 (0, 2 head, token, batch entry): a
+// row is two halves of 256.
+cudaError_t make_tmap_tokens(CUtensorMap* m, const void* ptr, int D, int H, int L, int batch, long long tok, int toks,
+                             int hb);
+// A dense fp32 [batch, H, L, D] tensor: box of hb heads x toks tokens as
+// [head][token][D].  Coordinates (0, token, head, batch entry), at D = 512 (0,
+// 0, token, head, batch entry).
+cudaError_t make_tmap_f32_tokens(CUtensorMap* m, const void* ptr, int D, int H, int L, int batch, int toks, int hb);
+
 // 3-D fp32 tensor map over an output [heads, L, D] for the D = 512 epilogues:
 // 32 x 32 boxes (128-byte rows) with 128-byte swizzle; TMA stores clip rows
 // at or beyond L.
@@ -379,11 +390,11 @@ struct RopeArgs {
 // q to [B, Hq, L, D]; k and v (null: left out) to [B, Hkv, kv_rows, D], rows
 // outside [0, kv_rows) not written.
 cudaError_t launch_qk_rope_fwd(const RopeArgs& a, const uint16_t* v, long long v_tok, uint16_t* qo, uint16_t* ko,
-                               uint16_t* vo, int kv_rows, cudaStream_t s);
-// CTAs of the backward, each of which writes 2 D floats of `part`.
-int qk_rope_bwd_ctas(long long tokens);
+                               uint16_t* vo, int kv_rows, int* status, cudaStream_t s);
+// Floats of the backward's `part`: 2 D for each CTA it may launch.
+size_t qk_rope_bwd_part_floats(int D);
 cudaError_t launch_qk_rope_bwd(const RopeArgs& a, const float* dq, const float* dk, const float* dv, uint16_t* gq,
                                uint16_t* gk, uint16_t* gv, long long gq_tok, long long gk_tok, long long gv_tok,
-                               float* dwq, float* dwk, float* part, cudaStream_t s);
+                               float* dwq, float* dwk, float* part, int* status, cudaStream_t s);
 
 }  // namespace swa

@@ -908,6 +908,46 @@ cudaError_t make_tmap_rows_5d(CUtensorMap* m, const void* ptr, int D, int M, int
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+cudaError_t make_tmap_tokens(CUtensorMap* m, const void* ptr, int D, int H, int L, int batch, long long tok, int toks,
+                             int hb) {
+  auto enc = encode_fn();
+  if (!enc) return cudaErrorNotSupported;
+  const int cut = D > 256 ? D / 256 : 1, w = D / cut;  // a box is at most 256 wide
+  cuuint64_t dims[4] = {(cuuint64_t)w, (cuuint64_t)H * cut, (cuuint64_t)L, (cuuint64_t)batch};
+  cuuint64_t strides[3] = {(cuuint64_t)w * 2, (cuuint64_t)tok * 2, (cuuint64_t)tok * L * 2};
+  cuuint32_t box[4] = {(cuuint32_t)w, (cuuint32_t)(hb * cut), (cuuint32_t)toks, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t make_tmap_f32_tokens(CUtensorMap* m, const void* ptr, int D, int H, int L, int batch, int toks, int hb) {
+  auto enc = encode_fn();
+  if (!enc) return cudaErrorNotSupported;
+  const int cut = D > 256 ? D / 256 : 1, w = D / cut, n = cut > 1 ? 5 : 4;
+  const cuuint64_t row = (cuuint64_t)D * 4;
+  cuuint64_t dims[5] = {(cuuint64_t)w, (cuuint64_t)L, (cuuint64_t)H, (cuuint64_t)batch, 1};
+  cuuint64_t strides[4] = {row, row * L, row * L * H, 0};
+  cuuint32_t box[5] = {(cuuint32_t)w, (cuuint32_t)toks, (cuuint32_t)hb, 1, 1};
+  if (cut > 1) {
+    const cuuint64_t d5[5] = {(cuuint64_t)w, (cuuint64_t)cut, (cuuint64_t)L, (cuuint64_t)H, (cuuint64_t)batch};
+    const cuuint64_t s5[4] = {(cuuint64_t)w * 4, row, row * L, row * L * H};
+    const cuuint32_t b5[5] = {(cuuint32_t)w, (cuuint32_t)cut, (cuuint32_t)toks, (cuuint32_t)hb, 1};
+    for (int i = 0; i < 5; ++i) {
+      dims[i] = d5[i];
+      box[i] = b5[i];
+      if (i < 4) strides[i] = s5[i];
+    }
+  }
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, n, const_cast<void*>(ptr), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 cudaError_t make_tmap_f32_out(CUtensorMap* m, void* ptr, int D, int L, int heads) {
   auto enc = encode_fn();
   if (!enc) return cudaErrorNotSupported;
