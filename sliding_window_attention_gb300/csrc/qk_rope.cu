@@ -298,11 +298,11 @@ __global__ void __launch_bounds__(kThr) qk_rope_fwd_kernel(const RopeFwd p) {
 // Long sequences: rows staged through shared memory by TMA.
 //
 // Both directions move a few bytes a multiplication, so what bounds them is
-// the memory's latency: the bytes in flight.  A producer thread keeps a ring of
+// the memory's latency: the bytes in flight.  A CTA keeps a ring of
 // stages filled -- a stage is 512 / D heads of 8 consecutive tokens, x as the
 // projection laid it out ([token][head][D]) and, in the backward, dy as the
-// attention did ([head][token][D]); the boxes of two tensor maps -- and eight
-// consumer warps, one a token, work from there.  A stage's units (token group,
+// attention did ([head][token][D]); the boxes of two tensor maps -- and its
+// eight warps, one a token, work from there.  A stage's units (token group,
 // block of heads) form one list that the CTAs share out evenly.
 //
 // A lane holds E = 8 (16 at D = 512) elements of a row in NG groups of 4, D / NG
@@ -343,60 +343,79 @@ struct StRope {
   int* status;
 };
 
-// The partners' elements of a row in shared memory whose own elements are in
-// registers (own[E]); ld(d, v) loads elements d .. d + 3.
-template <int D, bool INTER, typename F>
-__device__ __forceinline__ void row_partners(const float (&own)[StCfg<D>::E], float (&other)[StCfg<D>::E], int d4,
-                                             int pairs, F&& ld) {
+// How a pair is laid out: neighbours; the halves of the whole head (both in
+// one lane); the halves of its first 2 * pairs elements (the partner's row
+// group is read from shared memory).
+enum : int { kInter = 0, kHalves = 1, kPart = 2 };
+
+// Elements are held as pairs of neighbours (.f32x2 arithmetic: one
+// instruction for two elements).
+__device__ __forceinline__ void ld_bf4(const uint16_t* p, uint64_t* x) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  x[0] = tc::f2_pack(bf_lo(v.x), bf_hi(v.x));
+  x[1] = tc::f2_pack(bf_lo(v.y), bf_hi(v.y));
+}
+__device__ __forceinline__ void ld_f4(const float* p, uint64_t* x) {
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  x[0] = tc::f2_pack(v.x, v.y);
+  x[1] = tc::f2_pack(v.z, v.w);
+}
+__device__ __forceinline__ uint32_t bf_pack2(uint64_t x) {
+  const float2 v = tc::f2_unpack(x);
+  return bf_pack(v.x, v.y);
+}
+__device__ __forceinline__ uint64_t f2_dup(float x) { return tc::f2_pack(x, x); }
+__device__ __forceinline__ float f2_sum(uint64_t x) {
+  const float2 v = tc::f2_unpack(x);
+  return v.x + v.y;
+}
+
+// The partners' elements of a row whose own elements are in registers; ld(d,
+// v) loads elements d .. d + 3 of the row.
+template <int D, int MODE, typename F>
+__device__ __forceinline__ void row_partners(const uint64_t (&own)[StCfg<D>::E / 2], uint64_t (&other)[StCfg<D>::E / 2],
+                                             int d4, int pairs, F&& ld) {
   using C = StCfg<D>;
-  if constexpr (INTER) {
+  constexpr int W = C::E / 2;
+  if constexpr (MODE == kInter) {
 #pragma unroll
-    for (int e = 0; e < C::E; ++e) other[e] = own[e ^ 1];
+    for (int e = 0; e < W; ++e) {
+      const float2 v = tc::f2_unpack(own[e]);
+      other[e] = tc::f2_pack(v.y, v.x);
+    }
+  } else if constexpr (MODE == kHalves) {
+#pragma unroll
+    for (int e = 0; e < W; ++e) other[e] = own[(e + W / 2) % W];
   } else {
-    if (2 * pairs == D) {
 #pragma unroll
-      for (int e = 0; e < C::E; ++e) other[e] = own[(e + C::E / 2) % C::E];
-    } else {
-#pragma unroll
-      for (int g = 0; g < C::NG; ++g) {
-        const int d = C::GS * g + d4;
-        ld(d < pairs ? d + pairs : (d < 2 * pairs ? d - pairs : d), other + 4 * g);
-      }
+    for (int g = 0; g < C::NG; ++g) {
+      const int d = C::GS * g + d4;
+      ld(d < pairs ? d + pairs : (d < 2 * pairs ? d - pairs : d), other + 2 * g);
     }
   }
 }
 // cos, and +-sin as y_e = cos u_e + s_e u_partner(e), of the lane's elements.
-template <int D, bool INTER>
-__device__ __forceinline__ void lane_angles(const float2* cs, int d4, int pairs, float (&c)[StCfg<D>::E],
-                                            float (&s)[StCfg<D>::E]) {
+template <int D, int MODE>
+__device__ __forceinline__ void lane_angles(const float2* cs, int d4, int pairs, uint64_t (&c)[StCfg<D>::E / 2],
+                                            uint64_t (&s)[StCfg<D>::E / 2]) {
   using C = StCfg<D>;
 #pragma unroll
   for (int g = 0; g < C::NG; ++g) {
     const int d = C::GS * g + d4;
+    float2 v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const bool in = d < 2 * pairs, lo = INTER ? (i & 1) == 0 : d < pairs;
-      const float2 v = in ? cs[INTER ? (d + i) / 2 : (lo ? d + i : d - pairs + i)] : make_float2(1.f, 0.f);
-      c[4 * g + i] = v.x;
-      s[4 * g + i] = lo ? -v.y : v.y;
+      const bool in = d < 2 * pairs, lo = MODE == kInter ? (i & 1) == 0 : d < pairs;
+      v[i] = in ? cs[MODE == kInter ? (d + i) / 2 : (lo ? d + i : d - pairs + i)] : make_float2(1.f, 0.f);
+      if (lo) v[i].y = -v[i].y;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      c[2 * g + i] = tc::f2_pack(v[2 * i].x, v[2 * i + 1].x);
+      s[2 * g + i] = tc::f2_pack(v[2 * i].y, v[2 * i + 1].y);
     }
   }
 }
-__device__ __forceinline__ void ld_bf4(const uint16_t* p, float* x) {
-  const uint2 v = *reinterpret_cast<const uint2*>(p);
-  x[0] = bf_lo(v.x);
-  x[1] = bf_hi(v.x);
-  x[2] = bf_lo(v.y);
-  x[3] = bf_hi(v.y);
-}
-__device__ __forceinline__ void ld_f4(const float* p, float* x) {
-  const float4 v = *reinterpret_cast<const float4*>(p);
-  x[0] = v.x;
-  x[1] = v.y;
-  x[2] = v.z;
-  x[3] = v.w;
-}
-__device__ __forceinline__ uint2 pack4(const float* x) { return make_uint2(bf_pack(x[0], x[1]), bf_pack(x[2], x[3])); }
 
 // Shared memory of a staged kernel: NS stages, then weights, turn steps, the
 // warps' cos / sin tables and the barriers.
@@ -415,15 +434,15 @@ struct StSmem {
   static_assert(!BWD || NS * STAGE >= kTok * D * 4, "the scales' gradients are reduced in the stages");
 };
 
-template <int D, bool INTER, bool BWD>
-__global__ void __launch_bounds__(kThr + 32, StSmem<D, BWD>::CTAS)
+template <int D, int MODE, bool BWD>
+__global__ void __launch_bounds__(kThr, StSmem<D, BWD>::CTAS)
     qk_rope_staged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                           const __grid_constant__ CUtensorMap tmV,   // forward: v's rows
                           const __grid_constant__ CUtensorMap tmDQ, const __grid_constant__ CUtensorMap tmDK,
                           const __grid_constant__ CUtensorMap tmDV, const __grid_constant__ StRope p) {
   using C = StCfg<D>;
   using M = StSmem<D, BWD>;
-  constexpr int E = C::E, NG = C::NG, GS = C::GS, HB = C::HB, NS = M::NS;
+  constexpr int E = C::E, W = E / 2, NG = C::NG, GS = C::GS, HB = C::HB, NS = M::NS, IT = C::ITER;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
   float* sw = reinterpret_cast<float*>(base + M::OFF_W);
@@ -444,174 +463,232 @@ __global__ void __launch_bounds__(kThr + 32, StSmem<D, BWD>::CTAS)
     *abort_flag = 0;
     tc::fence_mbar_init();
   }
-  for (int i = threadIdx.x; i < pairs; i += kThr + 32) step[i] = turn_step(p.pos.inv_freq[i]);
-  for (int i = threadIdx.x; i < 2 * D; i += kThr + 32) {
+  for (int i = threadIdx.x; i < pairs; i += kThr) step[i] = turn_step(p.pos.inv_freq[i]);
+  for (int i = threadIdx.x; i < 2 * D; i += kThr) {
     const float* w = i < D ? p.wq : p.wk;
     sw[i] = w ? w[i < D ? i : i - D] + p.off : 1.f;
   }
   __syncthreads();
 
-  float accq[BWD ? E : 1], acck[BWD ? E : 1];
+  uint64_t accq[BWD ? W : 1], acck[BWD ? W : 1];  // dw of the lane's elements
 #pragma unroll
-  for (int e = 0; e < (BWD ? E : 1); ++e) accq[e] = acck[e] = 0.f;
+  for (int e = 0; e < (BWD ? W : 1); ++e) accq[e] = acck[e] = f2_dup(0.f);
 
-  if (warp == kTok) {
-    // ------------------------------------------------------------ producer
-    if (tc::elect_one()) {
-      int n = 0;
-      for (int u = u0; u < u1; ++u, ++n) {
-        const int s = n % NS, grp = u / ls.per, i = u - grp * ls.per;
-        if (n >= NS && !tc::mbar_wait(empty + s, ((n / NS) & 1) ^ 1, abort_flag)) break;
-        const int b = grp / ls.gl, l0 = (grp - b * ls.gl) * kTok;
-        const int kind = i < ls.nq ? 0 : (i < ls.nq + ls.nk ? 1 : 2);
-        const int h0 = (i - (kind > 0 ? ls.nq : 0) - (kind > 1 ? ls.nk : 0)) * HB;
-        unsigned char* x = base + s * M::STAGE;
-        // D = 512 rows are two halves of 256 (a box is at most 256 wide)
-        const bool has_x = !BWD || kind < 2;
-        tc::mbar_arrive_expect_tx(full + s, (has_x ? C::XB : 0) + (BWD ? C::YB : 0));
-        if (has_x) tc::tma_load_4d(x, kind == 0 ? &tmQ : (kind == 1 ? &tmK : &tmV), full + s, 0, D == 512 ? 2 * h0 : h0, l0, b);
-        if (BWD) {
-          const CUtensorMap* m = kind == 0 ? &tmDQ : (kind == 1 ? &tmDK : &tmDV);
-          if (D == 512) tc::tma_load_5d(x + C::XB, m, full + s, 0, 0, l0, h0, b);
-          else tc::tma_load_4d(x + C::XB, m, full + s, 0, l0, h0, b);
-        }
-      }
-      if (*abort_flag) tc::drain_ring(full, NS, n);
+  // Stage n (unit u0 + n) is loaded by lane 0 of warp n % kTok, once every
+  // warp has consumed stage n - NS; a warp gets to that after its own stage
+  // n - NS + 1, so it seldom waits.
+  int loaded = -1;  // the last stage this thread loaded
+  auto load = [&](int n) {
+    const int s = n % NS, u = u0 + n, grp = u / ls.per, i = u - grp * ls.per;
+    if (n >= NS && !tc::mbar_wait(empty + s, ((n / NS) & 1) ^ 1, abort_flag)) return;
+    const int b = grp / ls.gl, l0 = (grp - b * ls.gl) * kTok;
+    const int kind = i < ls.nq ? 0 : (i < ls.nq + ls.nk ? 1 : 2);
+    const int h0 = (i - (kind > 0 ? ls.nq : 0) - (kind > 1 ? ls.nk : 0)) * HB;
+    unsigned char* x = base + s * M::STAGE;
+    // D = 512 rows are two halves of 256 (a box is at most 256 wide)
+    const bool has_x = !BWD || kind < 2;
+    tc::mbar_arrive_expect_tx(full + s, (has_x ? C::XB : 0) + (BWD ? C::YB : 0));
+    if (has_x) tc::tma_load_4d(x, kind == 0 ? &tmQ : (kind == 1 ? &tmK : &tmV), full + s, 0, D == 512 ? 2 * h0 : h0, l0, b);
+    if (BWD) {
+      const CUtensorMap* m = kind == 0 ? &tmDQ : (kind == 1 ? &tmDK : &tmDV);
+      if (D == 512) tc::tma_load_5d(x + C::XB, m, full + s, 0, 0, l0, h0, b);
+      else tc::tma_load_4d(x + C::XB, m, full + s, 0, l0, h0, b);
     }
-  } else {
-    // ------------------------------------------------------------ one token a warp
+    loaded = n;
+  };
+  {
+    if (lane == 0 && warp < NS && warp < u1 - u0) load(warp);
+    __syncwarp();
+    // one token a warp
     float2* cs = reinterpret_cast<float2*>(base + M::OFF_CS) + warp * (D / 2);
     const int sub = lane / C::LPR, d4 = 4 * (lane % C::LPR);
-    float a[E], q[E];  // forward: cos w and +-sin w of the partner; backward: cos, +-sin
-    float we[BWD ? E : 1];
-    int last_grp = -1, last_kind = -1, b = 0, l = 0, kv_row = 0;
-    bool live = false, kv_ok = false;
-    int n = 0;
-    for (int u = u0; u < u1; ++u, ++n) {
-      const int s = n % NS, grp = u / ls.per, i = u - grp * ls.per;
-      const int kind = i < ls.nq ? 0 : (i < ls.nq + ls.nk ? 1 : 2);
-      const int h0 = (i - (kind > 0 ? ls.nq : 0) - (kind > 1 ? ls.nk : 0)) * HB;
-      if (grp != last_grp) {
-        b = grp / ls.gl;
-        l = (grp - b * ls.gl) * kTok + warp;
-        live = l < p.L;
-        kv_row = p.pos.kv_len ? (live ? p.pos.kv_len[b] - p.L + l : -1) : l;
-        kv_ok = kv_row >= 0 && kv_row < p.kv_rows;
+    int u = u0, slot = 0, grp = u0 / ls.per, skip = u0 - grp * ls.per;  // blocks of the group before this CTA's
+    uint32_t phase = 0;
+    bool ok = true;
+    // The stages of one kind's nb head blocks: f(stage, first head) works on one.
+    auto blocks = [&](int nb, auto&& f) {
+      int blk = min(skip, nb);
+      skip -= blk;
+      for (; blk < nb && u < u1; ++blk, ++u) {
+        if (!__all_sync(0xffffffffu, tc::mbar_wait(full + slot, phase, abort_flag))) {
+          ok = false;
+          return;
+        }
+        f(base + slot * M::STAGE, blk * HB);
         __syncwarp();
-        if (live) {
-          const long long pos = token_pos(p.pos, b, l, p.L);
-          for (int k = lane; k < pairs; k += 32) cs[k] = turn_cs(pos, step[k]);
+        if (lane == 0) {
+          tc::mbar_arrive(empty + slot);
+          const int n = u - u0 + NS - 1;
+          if (n % kTok == warp && n >= NS && n < u1 - u0) load(n);
         }
         __syncwarp();
-        last_kind = -1;
-        last_grp = grp;
-      }
-      if (kind != last_kind && kind < 2) {
-        const float* w = sw + kind * D;
-        lane_angles<D, INTER>(cs, d4, pairs, a, q);
-        float wv[E];
-#pragma unroll
-        for (int g = 0; g < NG; ++g) ld_f4(w + GS * g + d4, wv + 4 * g);
-        if constexpr (BWD) {
-#pragma unroll
-          for (int e = 0; e < E; ++e) we[e] = wv[e];
-        } else {
-          float wp[E];
-          row_partners<D, INTER>(wv, wp, d4, pairs, [&](int d, float* v) { ld_f4(w + d, v); });
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            a[e] *= wv[e];
-            q[e] *= wp[e];
-          }
+        if (++slot == NS) {
+          slot = 0;
+          phase ^= 1;
         }
-        last_kind = kind;
       }
-      if (!__all_sync(0xffffffffu, tc::mbar_wait(full + s, (n / NS) & 1, abort_flag))) break;
-      const int H = kind == 0 ? p.Hq : p.Hkv;
-      const uint16_t* xs = reinterpret_cast<const uint16_t*>(base + s * M::STAGE) + warp * 512;  // [head][D] of the token
-      const float* ys = reinterpret_cast<const float*>(base + s * M::STAGE + C::XB) + warp * D;  // [head][token][D]
+    };
+    for (; ok && u < u1; ++grp) {
+      const int b = grp / ls.gl, l = (grp - b * ls.gl) * kTok + warp;
+      const bool live = l < p.L;
+      const long long tok = (long long)b * p.L + l;
+      __syncwarp();
       if (live) {
-#pragma unroll
-        for (int it = 0; it < C::ITER; ++it) {
-          const int r = it * C::RPW + sub, h = h0 + r;
-          const bool in = h < H;
-          if constexpr (!BWD) {
-            const uint16_t* x = xs + r * D;
-            if (kind == 2) {
-              if (in && kv_ok) {
-                uint16_t* out = p.vo + (((size_t)b * p.Hkv + h) * p.kv_rows + kv_row) * D;
-#pragma unroll
-                for (int g = 0; g < NG; ++g)
-                  *reinterpret_cast<uint2*>(out + GS * g + d4) = *reinterpret_cast<const uint2*>(x + GS * g + d4);
-              }
-              continue;
-            }
-            float f[E], o[E];
-#pragma unroll
-            for (int g = 0; g < NG; ++g) ld_bf4(x + GS * g + d4, f + 4 * g);
-            row_partners<D, INTER>(f, o, d4, pairs, [&](int d, float* v) { ld_bf4(x + d, v); });
-            float ss = 0.f;
-#pragma unroll
-            for (int e = 0; e < E; ++e) ss = fmaf(f[e], f[e], ss);
-            const float rn = rsqrtf(row_sum<C::LPR>(ss) * (1.f / D) + p.eps);
-#pragma unroll
-            for (int e = 0; e < E; ++e) f[e] = rn * fmaf(f[e], a[e], o[e] * q[e]);
-            if (in && (kind == 0 || kv_ok)) {
-              uint16_t* out = kind == 0 ? p.qo + (((size_t)b * p.Hq + h) * p.L + l) * D
-                                        : p.ko + (((size_t)b * p.Hkv + h) * p.kv_rows + kv_row) * D;
-#pragma unroll
-              for (int g = 0; g < NG; ++g) *reinterpret_cast<uint2*>(out + GS * g + d4) = pack4(f + 4 * g);
-            }
-          } else {
-            const float* y = ys + r * (kTok * D);
-            const long long tok = (long long)b * p.L + l;
-            float g4[E];
-#pragma unroll
-            for (int g = 0; g < NG; ++g) ld_f4(y + GS * g + d4, g4 + 4 * g);
-            if (kind == 2) {
-              if (in) {
-                uint16_t* out = p.gv + tok * p.gv_tok + (size_t)h * D;
-#pragma unroll
-                for (int g = 0; g < NG; ++g) *reinterpret_cast<uint2*>(out + GS * g + d4) = pack4(g4 + 4 * g);
-              }
-              continue;
-            }
-            const uint16_t* x = xs + r * D;
-            float f[E], o[E];
-            row_partners<D, INTER>(g4, o, d4, pairs, [&](int d, float* v) { ld_f4(y + d, v); });
-#pragma unroll
-            for (int g = 0; g < NG; ++g) ld_bf4(x + GS * g + d4, f + 4 * g);
-            float ss = 0.f, dot = 0.f;
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-              g4[e] = fmaf(a[e], g4[e], -q[e] * o[e]);  // the rotation's transpose
-              ss = fmaf(f[e], f[e], ss);
-              dot = fmaf(g4[e] * we[e], f[e], dot);
-            }
-            ss = row_sum<C::LPR>(ss);
-            dot = row_sum<C::LPR>(dot);
-            const float rn = rsqrtf(ss * (1.f / D) + p.eps);
-            const float m = dot * rn * rn * (1.f / D);  // mean(h n) r
-            if (in) {
-#pragma unroll
-              for (int e = 0; e < E; ++e) {
-                const float t = g4[e] * rn * f[e];
-                if (kind == 0) accq[e] += t;
-                else acck[e] += t;
-                g4[e] = rn * fmaf(g4[e], we[e], -f[e] * m);
-              }
-              uint16_t* out = (kind == 0 ? p.gq + tok * p.gq_tok : p.gk + tok * p.gk_tok) + (size_t)h * D;
-#pragma unroll
-              for (int g = 0; g < NG; ++g) *reinterpret_cast<uint2*>(out + GS * g + d4) = pack4(g4 + 4 * g);
-            }
-          }
-        }
+        const long long pos = token_pos(p.pos, b, l, p.L);
+        for (int k = lane; k < pairs; k += 32) cs[k] = turn_cs(pos, step[k]);
       }
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(empty + s);
+      uint64_t a[W], q[W];  // cos and +-sin (forward: times the element's and its partner's scale)
+      if constexpr (!BWD) {
+        // q or k rows: out = the token's row of head 0, heads `pitch` elements apart
+        auto rows = [&](int nb, int H, const float* w, uint16_t* out, long long pitch, bool store) {
+          lane_angles<D, MODE>(cs, d4, pairs, a, q);
+          {
+            uint64_t wv[W], wp[W];
+#pragma unroll
+            for (int g = 0; g < NG; ++g) ld_f4(w + GS * g + d4, wv + 2 * g);
+            row_partners<D, MODE>(wv, wp, d4, pairs, [&](int d, uint64_t* v) { ld_f4(w + d, v); });
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+              a[e] = tc::f2_mul(a[e], wv[e]);
+              q[e] = tc::f2_mul(q[e], wp[e]);
+            }
+          }
+          blocks(nb, [&](const unsigned char* st, int h0) {
+            const uint16_t* xs = reinterpret_cast<const uint16_t*>(st) + warp * 512 + sub * D;  // [head][D] of the token
+            uint64_t f[IT][W], o[IT][W];
+            float ss[IT];
+#pragma unroll
+            for (int it = 0; it < IT; ++it) {
+              const uint16_t* x = xs + it * C::RPW * D;
+#pragma unroll
+              for (int g = 0; g < NG; ++g) ld_bf4(x + GS * g + d4, f[it] + 2 * g);
+              row_partners<D, MODE>(f[it], o[it], d4, pairs, [&](int d, uint64_t* v) { ld_bf4(x + d, v); });
+              uint64_t t = tc::f2_mul(f[it][0], f[it][0]);
+#pragma unroll
+              for (int e = 1; e < W; ++e) t = tc::f2_fma(f[it][e], f[it][e], t);
+              ss[it] = f2_sum(t);
+            }
+#pragma unroll
+            for (int k = C::LPR / 2; k > 0; k >>= 1)
+#pragma unroll
+              for (int it = 0; it < IT; ++it) ss[it] += __shfl_xor_sync(0xffffffffu, ss[it], k);
+#pragma unroll
+            for (int it = 0; it < IT; ++it) {
+              const int h = h0 + it * C::RPW + sub;
+              const uint64_t rn = f2_dup(rsqrtf(ss[it] * (1.f / D) + p.eps));
+#pragma unroll
+              for (int e = 0; e < W; ++e)
+                f[it][e] = tc::f2_mul(rn, tc::f2_fma(f[it][e], a[e], tc::f2_mul(o[it][e], q[e])));
+              if (store && h < H) {
+                uint16_t* dst = out + h * pitch + d4;
+#pragma unroll
+                for (int g = 0; g < NG; ++g)
+                  *reinterpret_cast<uint2*>(dst + GS * g) = make_uint2(bf_pack2(f[it][2 * g]), bf_pack2(f[it][2 * g + 1]));
+              }
+            }
+          });
+        };
+        const int kv_row = p.pos.kv_len ? (live ? p.pos.kv_len[b] - p.L + l : -1) : l;
+        const bool kv_ok = live && kv_row >= 0 && kv_row < p.kv_rows;  // rows outside the cache are not written
+        const long long kv_at = ((long long)b * p.Hkv * p.kv_rows + kv_row) * D, kv_pitch = (long long)p.kv_rows * D;
+        rows(ls.nq, p.Hq, sw, p.qo + ((long long)b * p.Hq * p.L + l) * D, (long long)p.L * D, live);
+        if (ok && ls.nk) rows(ls.nk, p.Hkv, sw + D, p.ko + kv_at, kv_pitch, kv_ok);
+        if (ok && ls.nv)
+          blocks(ls.nv, [&](const unsigned char* st, int h0) {
+            const uint16_t* xs = reinterpret_cast<const uint16_t*>(st) + warp * 512 + sub * D;
+#pragma unroll
+            for (int it = 0; it < IT; ++it) {
+              const int h = h0 + it * C::RPW + sub;
+              if (!kv_ok || h >= p.Hkv) continue;
+#pragma unroll
+              for (int g = 0; g < NG; ++g)
+                *reinterpret_cast<uint2*>(p.vo + kv_at + h * kv_pitch + GS * g + d4) =
+                    *reinterpret_cast<const uint2*>(xs + it * C::RPW * D + GS * g + d4);
+            }
+          });
+      } else {
+        lane_angles<D, MODE>(cs, d4, pairs, a, q);
+#pragma unroll
+        for (int e = 0; e < W; ++e) q[e] = tc::f2_mul(q[e], f2_dup(-1.f));  // the rotation's transpose
+        auto rows = [&](int nb, int H, const float* w, uint16_t* out, uint64_t (&acc)[W]) {
+          uint64_t we[W];
+#pragma unroll
+          for (int g = 0; g < NG; ++g) ld_f4(w + GS * g + d4, we + 2 * g);
+          blocks(nb, [&](const unsigned char* st, int h0) {
+            const uint16_t* xs = reinterpret_cast<const uint16_t*>(st) + warp * 512 + sub * D;  // [head][D] of the token
+            const float* ys = reinterpret_cast<const float*>(st + C::XB) + (sub * kTok + warp) * D;  // [head][token][D]
+            uint64_t f[IT][W], y[IT][W];
+            float ss[IT], dot[IT];
+#pragma unroll
+            for (int it = 0; it < IT; ++it) {
+              const uint16_t* x = xs + it * C::RPW * D;
+              const float* dy = ys + it * C::RPW * kTok * D;
+              uint64_t o[W];
+#pragma unroll
+              for (int g = 0; g < NG; ++g) {
+                ld_f4(dy + GS * g + d4, y[it] + 2 * g);
+                ld_bf4(x + GS * g + d4, f[it] + 2 * g);
+              }
+              row_partners<D, MODE>(y[it], o, d4, pairs, [&](int d, uint64_t* v) { ld_f4(dy + d, v); });
+              uint64_t t = f2_dup(0.f), v = f2_dup(0.f);
+#pragma unroll
+              for (int e = 0; e < W; ++e) {
+                y[it][e] = tc::f2_fma(a[e], y[it][e], tc::f2_mul(q[e], o[e]));
+                t = tc::f2_fma(f[it][e], f[it][e], t);
+                v = tc::f2_fma(tc::f2_mul(y[it][e], we[e]), f[it][e], v);
+              }
+              ss[it] = f2_sum(t);
+              dot[it] = f2_sum(v);
+            }
+#pragma unroll
+            for (int k = C::LPR / 2; k > 0; k >>= 1)
+#pragma unroll
+              for (int it = 0; it < IT; ++it) {
+                ss[it] += __shfl_xor_sync(0xffffffffu, ss[it], k);
+                dot[it] += __shfl_xor_sync(0xffffffffu, dot[it], k);
+              }
+#pragma unroll
+            for (int it = 0; it < IT; ++it) {
+              const int h = h0 + it * C::RPW + sub;
+              if (!live || h >= H) continue;
+              const float r = rsqrtf(ss[it] * (1.f / D) + p.eps);
+              const uint64_t rn = f2_dup(r), m = f2_dup(-dot[it] * r * r * (1.f / D));  // -mean(h n) r
+              uint16_t* dst = out + (long long)h * D + d4;
+#pragma unroll
+              for (int e = 0; e < W; ++e) {
+                acc[e] = tc::f2_fma(tc::f2_mul(y[it][e], rn), f[it][e], acc[e]);
+                y[it][e] = tc::f2_mul(rn, tc::f2_fma(f[it][e], m, tc::f2_mul(y[it][e], we[e])));
+              }
+#pragma unroll
+              for (int g = 0; g < NG; ++g)
+                *reinterpret_cast<uint2*>(dst + GS * g) = make_uint2(bf_pack2(y[it][2 * g]), bf_pack2(y[it][2 * g + 1]));
+            }
+          });
+        };
+        rows(ls.nq, p.Hq, sw, p.gq + tok * p.gq_tok, accq);
+        if (ok && ls.nk) rows(ls.nk, p.Hkv, sw + D, p.gk + tok * p.gk_tok, acck);
+        if (ok && ls.nv)
+          blocks(ls.nv, [&](const unsigned char* st, int h0) {
+            const float* ys = reinterpret_cast<const float*>(st + C::XB) + (sub * kTok + warp) * D;
+#pragma unroll
+            for (int it = 0; it < IT; ++it) {
+              const int h = h0 + it * C::RPW + sub;
+              if (!live || h >= p.Hkv) continue;
+              uint16_t* dst = p.gv + tok * p.gv_tok + (long long)h * D + d4;
+#pragma unroll
+              for (int g = 0; g < NG; ++g) {
+                uint64_t v[2];
+                ld_f4(ys + it * C::RPW * kTok * D + GS * g + d4, v);
+                *reinterpret_cast<uint2*>(dst + GS * g) = make_uint2(bf_pack2(v[0]), bf_pack2(v[1]));
+              }
+            }
+          });
+      }
     }
   }
 
+  if (*abort_flag && loaded >= 0) tc::mbar_wait_drain(full + loaded % NS, (loaded / NS) & 1);  // a load may be in flight
   __syncthreads();
   if (*abort_flag) {
     if (threadIdx.x == 0) atomicCAS(p.status, 0, kStatusTimeout);
@@ -624,17 +701,16 @@ __global__ void __launch_bounds__(kThr + 32, StSmem<D, BWD>::CTAS)
     const int sub = lane / C::LPR, d4 = 4 * (lane % C::LPR);
 #pragma unroll
     for (int kind = 0; kind < 2; ++kind) {
-      if (warp < kTok) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          float v = kind ? acck[e] : accq[e];
+      for (int e = 0; e < E; ++e) {
+        const float2 pr = tc::f2_unpack(kind ? acck[e / 2] : accq[e / 2]);
+        float v = e & 1 ? pr.y : pr.x;
 #pragma unroll
-          for (int o = C::LPR; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-          if (sub == 0) red[warp * D + GS * (e >> 2) + d4 + (e & 3)] = v;
-        }
+        for (int o = C::LPR; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (sub == 0) red[warp * D + GS * (e >> 2) + d4 + (e & 3)] = v;
       }
       __syncthreads();
-      for (int d = threadIdx.x; d < D; d += kThr + 32) {
+      for (int d = threadIdx.x; d < D; d += kThr) {
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < kTok; ++w) v += red[w * D + d];
@@ -713,14 +789,20 @@ int staged_ctas(const StList& l) {
   const long long u = (long long)l.groups * l.per, most = 152 * StSmem<D, BWD>::CTAS;
   return (int)(u < most ? u : most);
 }
-template <int D, bool INTER, bool BWD>
-cudaError_t staged_launch(const StRope& p, const CUtensorMap (&m)[6], int grid, cudaStream_t s) {
-  auto kern = qk_rope_staged_kernel<D, INTER, BWD>;
+template <int D, int MODE, bool BWD>
+cudaError_t staged_mode(const StRope& p, const CUtensorMap (&m)[6], int grid, cudaStream_t s) {
+  auto kern = qk_rope_staged_kernel<D, MODE, BWD>;
   const size_t smem = StSmem<D, BWD>::BYTES;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kern<<<grid, kThr + 32, smem, s>>>(m[0], m[1], m[2], m[3], m[4], m[5], p);
+  kern<<<grid, kThr, smem, s>>>(m[0], m[1], m[2], m[3], m[4], m[5], p);
   return cudaGetLastError();
+}
+
+template <int D, bool BWD>
+cudaError_t staged_launch(const StRope& p, const CUtensorMap (&m)[6], int grid, cudaStream_t s) {
+  if (p.pos.interleaved) return staged_mode<D, kInter, BWD>(p, m, grid, s);
+  return 2 * p.pos.pairs == D ? staged_mode<D, kHalves, BWD>(p, m, grid, s) : staged_mode<D, kPart, BWD>(p, m, grid, s);
 }
 
 template <int D>
@@ -734,7 +816,7 @@ cudaError_t staged_fwd(const RopeArgs& a, const uint16_t* v, long long v_tok, co
   if (!v) m[2] = m[0];
   m[3] = m[4] = m[5] = m[0];
   const int grid = staged_ctas<D, false>(p.list);
-  return a.interleaved ? staged_launch<D, true, false>(p, m, grid, s) : staged_launch<D, false, false>(p, m, grid, s);
+  return staged_launch<D, false>(p, m, grid, s);
 }
 
 template <int D>
@@ -754,7 +836,7 @@ cudaError_t staged_bwd(const RopeArgs& a, const float* dq, const float* dk, cons
   if (!dv) m[5] = m[3];
   m[2] = m[0];
   const int grid = staged_ctas<D, true>(p.list);
-  e = a.interleaved ? staged_launch<D, true, true>(p, m, grid, s) : staged_launch<D, false, true>(p, m, grid, s);
+  e = staged_launch<D, true>(p, m, grid, s);
   if (e != cudaSuccess || (!dwq && !dwk)) return e;
   // the partials' sum, launched as a programmatic dependent of the main kernel
   cudaLaunchConfig_t cfg = {};
