@@ -399,20 +399,40 @@ template <int D, int MODE>
 __device__ __forceinline__ void lane_angles(const float2* cs, int d4, int pairs, uint64_t (&c)[StCfg<D>::E / 2],
                                             uint64_t (&s)[StCfg<D>::E / 2]) {
   using C = StCfg<D>;
+  // pairs i, i + 1 as {cos, sin, cos, sin}; beyond the rotated part {1, 0}
+  auto two = [&](int i, bool in) {
+    return in ? *reinterpret_cast<const float4*>(cs + i) : make_float4(1.f, 0.f, 1.f, 0.f);
+  };
+  if constexpr (MODE == kHalves) {
+    constexpr int H = C::E / 4;  // words of the lower half
 #pragma unroll
-  for (int g = 0; g < C::NG; ++g) {
-    const int d = C::GS * g + d4;
-    float2 v[4];
+    for (int g = 0; g < C::NG / 2; ++g)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool in = d < 2 * pairs, lo = MODE == kInter ? (i & 1) == 0 : d < pairs;
-      v[i] = in ? cs[MODE == kInter ? (d + i) / 2 : (lo ? d + i : d - pairs + i)] : make_float2(1.f, 0.f);
-      if (lo) v[i].y = -v[i].y;
-    }
+      for (int i = 0; i < 2; ++i) {
+        const float4 v = two(C::GS * g + d4 + 2 * i, true);
+        c[2 * g + i] = c[H + 2 * g + i] = tc::f2_pack(v.x, v.z);
+        s[2 * g + i] = tc::f2_pack(-v.y, -v.w);
+        s[H + 2 * g + i] = tc::f2_pack(v.y, v.w);
+      }
+  } else {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      c[2 * g + i] = tc::f2_pack(v[2 * i].x, v[2 * i + 1].x);
-      s[2 * g + i] = tc::f2_pack(v[2 * i].y, v[2 * i + 1].y);
+    for (int g = 0; g < C::NG; ++g) {
+      const int d = C::GS * g + d4;
+      const bool in = d < 2 * pairs, lo = d < pairs;
+      if constexpr (MODE == kInter) {
+        const float4 v = two(d / 2, in);
+        c[2 * g] = tc::f2_pack(v.x, v.x);
+        s[2 * g] = tc::f2_pack(-v.y, v.y);
+        c[2 * g + 1] = tc::f2_pack(v.z, v.z);
+        s[2 * g + 1] = tc::f2_pack(-v.w, v.w);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float4 v = two((lo ? d : d - pairs) + 2 * i, in);
+          c[2 * g + i] = tc::f2_pack(v.x, v.z);
+          s[2 * g + i] = lo ? tc::f2_pack(-v.y, -v.w) : tc::f2_pack(v.y, v.w);
+        }
+      }
     }
   }
 }
@@ -423,14 +443,15 @@ template <int D, bool BWD>
 struct StSmem {
   using C = StCfg<D>;
   static constexpr int STAGE = C::XB + (BWD ? C::YB : 0);
-  static constexpr int NS = BWD ? (D == 512 ? 8 : 4) : 8;
+  static constexpr int NS = BWD && D == 512 ? 8 : 4;
   static constexpr int OFF_W = NS * STAGE;              // [2][D] scales
   static constexpr int OFF_STEP = OFF_W + 2 * D * 4;    // [D / 2]
   static constexpr int OFF_CS = OFF_STEP + D / 2 * 8;   // [kTok][D / 2]
   static constexpr int OFF_BAR = OFF_CS + kTok * D / 2 * 8;
   static constexpr size_t BYTES = (size_t)OFF_BAR + 256 + 128;
-  static constexpr int CTAS = BWD && D == 512 ? 1 : 2;  // per SM
+  static constexpr int CTAS = BWD ? (D == 512 ? 1 : 2) : 3;  // per SM
   static_assert(CTAS * BYTES <= 228 * 1024 - CTAS * 1024, "shared memory");
+  static_assert(NS <= kTok, "each warp loads one of the first stages");
   static_assert(!BWD || NS * STAGE >= kTok * D * 4, "the scales' gradients are reduced in the stages");
 };
 
@@ -463,11 +484,6 @@ __global__ void __launch_bounds__(kThr, StSmem<D, BWD>::CTAS)
     *abort_flag = 0;
     tc::fence_mbar_init();
   }
-  for (int i = threadIdx.x; i < pairs; i += kThr) step[i] = turn_step(p.pos.inv_freq[i]);
-  for (int i = threadIdx.x; i < 2 * D; i += kThr) {
-    const float* w = i < D ? p.wq : p.wk;
-    sw[i] = w ? w[i < D ? i : i - D] + p.off : 1.f;
-  }
   __syncthreads();
 
   uint64_t accq[BWD ? W : 1], acck[BWD ? W : 1];  // dw of the lane's elements
@@ -496,9 +512,16 @@ __global__ void __launch_bounds__(kThr, StSmem<D, BWD>::CTAS)
     }
     loaded = n;
   };
+  if (lane == 0 && warp < NS && warp < u1 - u0) load(warp);
+  for (int i = threadIdx.x; i < pairs; i += kThr) step[i] = turn_step(p.pos.inv_freq[i]);
+  for (int i = threadIdx.x; i < 2 * D; i += kThr) {
+    const float* w = i < D ? p.wq : p.wk;
+    sw[i] = w ? w[i < D ? i : i - D] + p.off : 1.f;
+  }
+  __syncthreads();
+
+
   {
-    if (lane == 0 && warp < NS && warp < u1 - u0) load(warp);
-    __syncwarp();
     // one token a warp
     float2* cs = reinterpret_cast<float2*>(base + M::OFF_CS) + warp * (D / 2);
     const int sub = lane / C::LPR, d4 = 4 * (lane % C::LPR);
@@ -540,9 +563,10 @@ __global__ void __launch_bounds__(kThr, StSmem<D, BWD>::CTAS)
       __syncwarp();
       uint64_t a[W], q[W];  // cos and +-sin (forward: times the element's and its partner's scale)
       if constexpr (!BWD) {
+        uint64_t c[W], sn[W];
+        lane_angles<D, MODE>(cs, d4, pairs, c, sn);
         // q or k rows: out = the token's row of head 0, heads `pitch` elements apart
         auto rows = [&](int nb, int H, const float* w, uint16_t* out, long long pitch, bool store) {
-          lane_angles<D, MODE>(cs, d4, pairs, a, q);
           {
             uint64_t wv[W], wp[W];
 #pragma unroll
@@ -550,8 +574,8 @@ __global__ void __launch_bounds__(kThr, StSmem<D, BWD>::CTAS)
             row_partners<D, MODE>(wv, wp, d4, pairs, [&](int d, uint64_t* v) { ld_f4(w + d, v); });
 #pragma unroll
             for (int e = 0; e < W; ++e) {
-              a[e] = tc::f2_mul(a[e], wv[e]);
-              q[e] = tc::f2_mul(q[e], wp[e]);
+              a[e] = tc::f2_mul(c[e], wv[e]);
+              q[e] = tc::f2_mul(sn[e], wp[e]);
             }
           }
           blocks(nb, [&](const unsigned char* st, int h0) {

@@ -10,14 +10,18 @@
 //   o = sum 2^(m - M) O / sum 2^(m - M) l,   lse = (M + log2 sum 2^(m - M) l) ln 2.
 //
 // Work.  The unit is one key tile (T = 128 keys) of one segment.  A segment is
-// the product of one block of query rows with one kv head's prefix (up to NP
+// the product of one block of query rows with one kv head's prefix (up to N
 // rows, packed from as many requests as fit, so the prefix is read once for
 // all of them), or with one request's own cache (up to 16 rows: the G * Lq
-// rows of a kv head).  One CTA per SM takes an equal run of units, however
-// ragged the lengths: every CTA sums the device-side lengths itself, no host
-// sees them and no counter has to be reset between calls.  A CTA's share of a
-// segment leaves one partial (m, l, O) in the slot cta + segment, which no
-// other pair of them has; a second kernel merges a row's partials.
+// rows of a kv head).  One CTA per SM works first on pieces of the prefix,
+// then on a run of the requests' own tiles, sized so that all CTAs get the
+// same number of units however ragged the lengths are: every CTA sums the
+// device-side lengths itself, no host sees them, and no counter has to be
+// reset between calls.  The pieces of one key range with all its row blocks
+// are neighbouring CTAs' work at the same time, so a tile's second and later
+// reads find it in L2.  Each piece, and each CTA's share of an own segment,
+// leaves one partial (m, l, O) in a slot of its own; a second kernel merges a
+// row's partials.
 //
 // Products are transposed, as in the decode kernel: S^T (128 keys x N rows) =
 // K_tile Q^T and O^T (D x N rows) += V_tile^T P^T, so the keys fill the MMA's
@@ -43,15 +47,17 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThr = 192;   // warp 0 TMA, warp 1 MMA, warps 2-5 softmax (thread = key = TMEM lane)
 constexpr int T = 128;      // keys per tile
 constexpr int kOwnRows = 16;  // query rows of an own segment (MMA N)
 constexpr int kSMs = 152;   // one CTA per SM
+constexpr int kPieces = 2 * kSMs;  // prefix pieces (or as many as there are segments)
 constexpr int kSmemMax = 232448;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 8.0f;
-constexpr int kPlanInts = 4;  // plan words in front of the per-request offsets
+// plan words: {prefix tiles, splits of the prefix, -, -}, each CTA's first own
+// unit (and their number), then each request's first own tile
+constexpr int kPlanStart = 4, kPlanOff = kPlanStart + kSMs + 1;
 
 struct SharedParams {
   SharedGeom g;
@@ -60,36 +66,71 @@ struct SharedParams {
   const float* sinks;  // [Hq] or null
   uint16_t* o;         // bf16 [B, Hq, Lq, D]
   float* lse;          // [B, Hq, Lq]
-  int* plan;           // {prefix tiles, units, CTAs with work, prefix start}, then own tiles before each request
-  float *pp_ml, *pp_o;  // prefix partials: [slot][rows][2] and [slot][rows][D]
-  float *po_ml, *po_o;  // own partials
+  int* plan;
+  float *pp_ml, *pp_o;  // prefix partials: [piece][rows][2] and [piece][rows][D]
+  float *po_ml, *po_o;  // own partials: [slot][rows]...
   int* status;
 };
 
-// First own key any of a request's rows sees, and the tiles from there to
-// the end of its cache; a negative length is an empty place of the batch.
+// The tiles of a request's own cache that any of its rows sees; a negative
+// length is an empty place of the batch.
 __device__ __forceinline__ int own_tiles(const SharedGeom& g, int len) {
   const int n = min(len, g.own_rows);
   const int lo = g.W > 0 ? max(0, n - g.Lq - g.W + 1) : 0;
   return n > lo ? (n - lo + T - 1) / T : 0;
 }
 
-// A place in a CTA's run of units.
-struct Walk {
+// A place in a CTA's prefix pieces.  Piece p is key range s of kv head h for
+// row block blk, p = (h splits + s) nrb + blk; a CTA has every gridDim.x-th.
+struct PrefixWalk {
   const SharedParams* p;
-  int left;        // units from here to the end of the run (0: done)
-  int own;         // this segment: a request's own cache, or the prefix
-  int seg;         // index among the segments of its kind
-  int h, b, blk;   // kv head; request (own); row block
-  int t, nt, n;    // tile of the segment, its tiles, own length
-  int key_lo;      // prefix: first key of tile 0
-  bool first;      // first tile of this CTA's visit of the segment
+  int splits, tiles, extra;  // ranges of a segment: `tiles` tiles, the first `extra` of them one more
+  int key_lo;                // first key of tile 0
+  int slot, t, t1;           // piece, tile, end of the piece's tiles
+  int h, blk;
+  bool first;                // first tile of the piece
+  __device__ __forceinline__ void begin(int piece) {
+    slot = piece;
+    const int hs = slot / p->s.nrb;
+    blk = slot - hs * p->s.nrb;
+    h = hs / splits;
+    const int s = hs - h * splits;
+    t = s * tiles + min(s, extra);
+    t1 = t + tiles + (s < extra ? 1 : 0);
+    first = true;
+  }
+  __device__ __forceinline__ int key0() const { return key_lo + T * t; }
+  __device__ __forceinline__ bool last() const { return t == t1 - 1; }
+  __device__ __forceinline__ void next() {
+    first = false;
+    if (++t == t1) begin(slot + gridDim.x);  // past the last piece: not used
+  }
+};
 
-  __device__ __forceinline__ void set_own() {
+// A place in a CTA's run of own units: request, kv head, row block, tile.
+struct OwnWalk {
+  const SharedParams* p;
+  int left;        // units from here to the end of the run
+  int b, h, blk, seg, slot;
+  int t, nt, n;    // tile of the segment, its tiles, own length
+  bool first;      // first tile of this CTA's visit of the segment
+  __device__ __forceinline__ void set_request() {
     n = min(p->own_len[b], p->g.own_rows);
     nt = own_tiles(p->g, n);
   }
-  __device__ __forceinline__ int key0() const { return own ? n - T * (nt - t) : key_lo + T * t; }
+  // unit r of request b0's segments
+  __device__ __forceinline__ void begin(int b0, int r, int units) {
+    b = b0;
+    set_request();
+    const int in = r / nt;
+    t = r - in * nt;
+    h = in / p->s.nomb;
+    blk = in - h * p->s.nomb;
+    slot = blockIdx.x + b * p->g.Hkv * p->s.nomb + in;
+    left = units;
+    first = true;
+  }
+  __device__ __forceinline__ int key0() const { return n - T * (nt - t); }
   __device__ __forceinline__ bool last() const { return left == 1 || t == nt - 1; }
   __device__ __forceinline__ void next() {
     first = false;
@@ -97,82 +138,77 @@ struct Walk {
     if (--left == 0 || t < nt) return;
     first = true;
     t = 0;
-    if (!own) {
-      ++seg;
-      if (++blk == p->s.nrb) {
-        blk = 0;
-        ++h;
-      }
-      if (h < p->g.Hkv) return;
-      own = 1;
-      h = 0;
-      b = -1;
-    } else {
-      if (++blk < p->s.nomb) {
-        ++seg;
-        return;
-      }
-      blk = 0;
-      if (++h < p->g.Hkv) {
-        ++seg;
-        return;
-      }
-      h = 0;
-    }
+    ++slot;
+    if (++blk < p->s.nomb) return;
+    blk = 0;
+    if (++h < p->g.Hkv) return;
+    h = 0;
     do {  // the next request with keys (there is one: units are left)
       ++b;
-      set_own();
+      set_request();
+      slot += nt == 0 ? p->g.Hkv * p->s.nomb : 0;
     } while (nt == 0);
-    seg = b * p->g.Hkv * p->s.nomb;
   }
 };
 
-template <int D, int NP>
+// Shared memory of one phase: N query rows a block (own caches: 16).
+template <int D, int N, bool OWN>
 struct ShCfg {
   static constexpr int NCH = D / 64;             // 64-column chunks of a row
   static constexpr int CPS = NCH < 2 ? NCH : 2;  // chunks per ring slot
   static constexpr int SPT = NCH / CPS;          // slots per tile and tensor
   static constexpr int NDC = (D + 127) / 128;    // 128-column blocks of O^T
+  static constexpr int GROUPS = N > 64 ? N / 64 : 1;  // softmax warpgroups, 64 rows each
+  static constexpr int NG = N / GROUPS;               // rows of one
   static constexpr int SLOT = CPS * T * 128;
-  static constexpr int QP = NP * D * 2, QO = kOwnRows * D * 2;
-  static constexpr int QD = (D == 512 && NP > 16) ? 1 : 2;  // buffers of own queries
-  static constexpr int PB = NP > 16 ? NP * T * 2 : kOwnRows * T * 2;  // one P^T buffer
-  // behind the ring: prefix queries, own queries, P^T, then the small arrays
-  static constexpr int SMALL = 2 * 4 * NP * 4 + 3 * NP * 4 + NP * 8 + 64 + 512;
+  static constexpr int QB = N * D * 2;           // one block of queries
+  static constexpr int QD = OWN ? 2 : 1;         // blocks buffered (own segments are short)
+  static constexpr int PB = N * T * 2;           // P^T
+  // per warpgroup: [2][4][NG] exchanged maxima / sums, thresholds, references,
+  // rescale factors, row ranges, bounds and growth tags
+  static constexpr int SMALL = 2 * 4 * NG * 4 + 3 * NG * 4 + NG * 8 + 64;
   // at head dim 64 the second product's 128 rows read one chunk past a slot
   // (rows 64-127 of O^T, never used): the last slot's must stay in bounds
   static constexpr int TAIL = D == 64 ? T * 128 : 0;
-  static constexpr int FIXED = QP + QD * QO + 2 * PB + SMALL + TAIL;
-  static constexpr int FIT = (kSmemMax - 1024 - FIXED) / SLOT;
+  static constexpr int FIXED = QB * QD + PB + GROUPS * SMALL + TAIL;
+  static constexpr int FIT = (kSmemMax - 1024 - 1024 - FIXED) / SLOT;
   static constexpr int NSLOT = FIT > 8 ? 8 : FIT;
-  static constexpr int OFF_QP = NSLOT * SLOT;
-  static constexpr int OFF_QO = OFF_QP + QP;
-  static constexpr int OFF_P = OFF_QO + QD * QO;
-  static constexpr int OFF_RED = OFF_P + 2 * PB;       // [2][4 warps][NP] exchanged maxima / sums
-  static constexpr int OFF_THR = OFF_RED + 2 * 4 * NP * 4;  // [NP] reference maximum + kRescaleLog2
-  static constexpr int OFF_USE = OFF_THR + NP * 4;     // [NP] reference maximum (0 where there is none)
-  static constexpr int OFF_ALPHA = OFF_USE + NP * 4;   // [NP] rescale factors
-  static constexpr int OFF_RNG = OFF_ALPHA + NP * 4;   // [NP] visible keys (first, last) of each row
-  static constexpr int OFF_BND = OFF_RNG + NP * 8;     // [4][2] bounds over a warp's rows, [2] growth tags
-  static constexpr int OFF_BAR = OFF_BND + 64;
-  static constexpr size_t SMEM = (size_t)OFF_BAR + 512 + TAIL + 1024;
-  static constexpr uint32_t S_COL = 0, O_COL = 2 * NP;  // TMEM columns
-  static constexpr uint32_t TCOLS = O_COL + NDC * NP <= 128 ? 128 : (O_COL + NDC * NP <= 256 ? 256 : 512);
-  static_assert(NSLOT >= 2 && SMEM + 256 <= (size_t)kSmemMax, "shared memory");
-  static_assert(O_COL + NDC * NP <= 512, "TMEM columns");
-  static_assert(NP == 16 || NP == 64, "row block");
+  static constexpr int OFF_Q = NSLOT * SLOT;
+  static constexpr int OFF_P = OFF_Q + QD * QB;
+  static constexpr int OFF_SMALL = OFF_P + PB;
+  static constexpr int BYTES = OFF_SMALL + GROUPS * SMALL + TAIL;
+  // within a warpgroup's small arrays
+  static constexpr int RED = 0, THR = 2 * 4 * NG * 4, USE = THR + NG * 4, ALPHA = USE + NG * 4, RNG = ALPHA + NG * 4,
+                       BND = RNG + NG * 8;
+  static constexpr uint32_t S_COL = 0, O_COL = 2 * N;  // TMEM columns
+  static constexpr uint32_t COLS = O_COL + NDC * N;
+  static_assert(NSLOT >= 2, "shared memory");
+  static_assert(COLS <= 512, "TMEM columns");
+  static_assert(NG == 16 || NG == 64, "rows of a warpgroup");
+};
+template <int D, int NP>
+struct ShKernel {
+  using A = ShCfg<D, NP, false>;
+  using B = ShCfg<D, kOwnRows, true>;
+  static constexpr int THREADS = 64 + 128 * A::GROUPS;
+  static constexpr int BODY = (A::BYTES > B::BYTES ? A::BYTES : B::BYTES);
+  static constexpr int OFF_BAR = (BODY + 15) / 16 * 16;  // barriers of the two phases, 384 bytes each
+  static constexpr size_t SMEM = (size_t)OFF_BAR + 768 + 1024;
+  static constexpr uint32_t COLS = A::COLS > B::COLS ? A::COLS : B::COLS;
+  static constexpr uint32_t TCOLS = COLS <= 128 ? 128 : (COLS <= 256 ? 256 : 512);
+  static_assert(SMEM + 512 <= (size_t)kSmemMax, "shared memory");
 };
 
 // Column reduction over the warp's 32 lanes by halving: each step keeps one
-// half of the columns and hands the other half over, so N columns take N
-// shuffles (5 N for a butterfly a column).  N = 64: lane l ends with columns
-// 2 l, 2 l + 1 in v[0], v[1]; N = 16: lanes 2 c, 2 c + 1 with column c in v[0].
+// half of the columns and hands the other half over, so N columns take about
+// N shuffles (5 N for a butterfly a column).  N = 32: lane l ends with column
+// l in v[0]; N = 16: lanes 2 c, 2 c + 1 with column c.
 template <int N, bool MAX>
 __device__ __forceinline__ void column_reduce(float (&v)[N], int lane) {
   auto op = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
   int o = 16;
 #pragma unroll
-  for (int h = N / 2; h >= (N == 64 ? 2 : 1); h >>= 1, o >>= 1) {
+  for (int h = N / 2; h >= 1; h >>= 1, o >>= 1) {
     const bool up = lane & o;
 #pragma unroll
     for (int i = 0; i < h; ++i) {
@@ -184,7 +220,7 @@ __device__ __forceinline__ void column_reduce(float (&v)[N], int lane) {
 }
 template <int N>
 __device__ __forceinline__ void column_post(const float (&v)[N], float* dst, int lane) {
-  if (N == 64) *reinterpret_cast<float2*>(dst + 2 * lane) = make_float2(v[0], v[1]);
+  if (N == 32) dst[lane] = v[0];
   else if ((lane & 1) == 0) dst[lane >> 1] = v[0];
 }
 
@@ -193,62 +229,99 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// What the softmax warps share.
+// Waits for a phase as mbar_wait does, in a third of its code: the roles wait
+// in some twenty places, and the code that a CTA runs once is fetched at the
+// memory's latency (an unrolled 200 KB version of this kernel spent most of a
+// short call on instruction fetches).
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint32_t t0 = (uint32_t)clock();
+  do {
+    if (mbar_try_wait(bar, parity)) return true;
+  } while (!*abort && (uint32_t)clock() - t0 < 4000000000u);  // ~2 s, within the counter's 32 bits
+  *abort = 1;
+  return false;
+}
+
+// A phase's barriers (its own, so that none has to be set up twice).
+struct Bars {
+  uint64_t *slot_full, *slot_empty;  // [8]
+  uint64_t *q_full, *q_empty;        // [2] a visit's queries
+  uint64_t *s_full;                  // [2] S^T(n) in TMEM
+  uint64_t *p_full;                  // [1] P^T(n) written (and O^T rescaled)
+  uint64_t *o_done;                  // [1] PV(n) finished
+  uint64_t *xch;                     // [2] a softmax warpgroup's exchanges
+  uint64_t *drain;                   // [1]
+  __device__ __forceinline__ explicit Bars(uint64_t* b)
+      : slot_full(b), slot_empty(b + 8), q_full(b + 16), q_empty(b + 18), s_full(b + 20), p_full(b + 22),
+        o_done(b + 23), xch(b + 24), drain(b + 26) {}
+  static constexpr int kCount = 27;
+  // arrivals that complete a phase of barrier i
+  static __device__ __forceinline__ int arrivals(int i, int groups) {
+    return i == 22 ? 4 * groups : (i == 24 || i == 25 ? 4 : 1);
+  }
+};
+
+// What a softmax warpgroup works with.
 struct SoftCtx {
   unsigned char* base;
-  uint64_t *s_full, *p_full, *o_done, *xch;
+  unsigned char* small;  // this warpgroup's small arrays
+  Bars bar;
   volatile int* abort;
   uint32_t tmem;
-  int n;   // tiles done by this CTA
+  int group;
+  int n;   // tiles done in this phase
   int xc;  // exchanges done
 };
 
-// Every softmax thread arrives and waits (bounded); what was written to
-// shared memory before is visible after.
+// Every softmax warp of the group arrives and waits (bounded); what was
+// written to shared memory before is visible after.
 __device__ __forceinline__ bool exchange(SoftCtx& c) {
-  mbar_arrive(c.xch);
-  const bool ok = mbar_wait(c.xch, c.xc & 1, c.abort);
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(c.bar.xch + c.group);
+  const bool ok = wait(c.bar.xch + c.group, c.xc & 1, c.abort);
   ++c.xc;
   return __all_sync(0xffffffffu, ok);
 }
 
 // One visit of a segment: its tiles' softmax, then the partial result.
-// N = 16: every thread keeps all rows' running maxima in registers, and each
-// tile exchanges its column maxima.  N = 64: the maxima live in shared memory,
-// and a tile exchanges only whether any score outgrew its row's reference by
-// more than 2^kRescaleLog2 (rare after a visit's first tiles).
-template <int D, int NP, int N>
+// 16 rows: every thread keeps all rows' running maxima in registers, and each
+// tile exchanges its column maxima.  64 rows a warpgroup: the maxima live in
+// shared memory, and a tile exchanges only whether any score outgrew its row's
+// reference by more than 2^kRescaleLog2 (rare after a visit's first tiles).
+template <int D, int N, bool OWN, typename Walk>
 __device__ bool softmax_visit(const SharedParams& p, Walk& w, SoftCtx& c) {
-  using C = ShCfg<D, NP>;
-  constexpr int NDC = C::NDC;
+  using C = ShCfg<D, N, OWN>;
+  constexpr int NDC = C::NDC, NG = C::NG;
   const SharedGeom& g = p.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q4 = warp & 3, t = 32 * q4 + lane;
-  const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
+  const uint32_t lane_off = (uint32_t)(32 * q4) << 16, col0 = (uint32_t)(NG * c.group);
   const float sl2 = g.scale * kLog2e;
-  float* red = reinterpret_cast<float*>(c.base + C::OFF_RED);
-  float* thr = reinterpret_cast<float*>(c.base + C::OFF_THR);
-  float* use = reinterpret_cast<float*>(c.base + C::OFF_USE);
-  float* alp = reinterpret_cast<float*>(c.base + C::OFF_ALPHA);
-  int2* rng = reinterpret_cast<int2*>(c.base + C::OFF_RNG);
-  int* bnd = reinterpret_cast<int*>(c.base + C::OFF_BND);
+  float* red = reinterpret_cast<float*>(c.small + C::RED);
+  float* thr = reinterpret_cast<float*>(c.small + C::THR);
+  float* use = reinterpret_cast<float*>(c.small + C::USE);
+  float* alp = reinterpret_cast<float*>(c.small + C::ALPHA);
+  int2* rng = reinterpret_cast<int2*>(c.small + C::RNG);
+  int* bnd = reinterpret_cast<int*>(c.small + C::BND);
   volatile int* grow_tag = bnd + 8;
-  const Walk at = w;  // this visit
+  const int blk = w.blk, slot = w.slot;
 
   // visible keys of row t (own cache: own indices), and bounds over all rows
   {
     int lo = 0, hi = INT32_MAX;  // rows that are no query mask nothing: their columns are never read
     bool row = false;
-    if (t < N) {
-      if (at.own) {
-        const int m = at.blk * kOwnRows + t, i = m % g.Lq;
+    if (t < NG) {
+      const int r = NG * c.group + t;  // row of the block
+      if constexpr (OWN) {
+        const int m = blk * kOwnRows + r;
         row = m < g.M;
         if (row) {
-          hi = at.n - g.Lq + i;
+          hi = w.n - g.Lq + m % g.Lq;
           lo = g.W > 0 ? max(0, hi - g.W + 1) : 0;
         }
       } else {
-        const int b = at.blk / p.s.nmb * p.s.nb + t / p.s.mb, m = at.blk % p.s.nmb * NP + t % p.s.mb;
-        const int len = (t < p.s.prow && b < g.B && m < g.M) ? p.own_len[b] : -1;
+        const int b = blk / p.s.nmb * p.s.nb + r / p.s.mb, m = blk % p.s.nmb * N + r % p.s.mb;
+        const int len = (r < p.s.prow && b < g.B && m < g.M) ? p.own_len[b] : -1;
         row = len >= 0;
         if (row) {
           const int a = g.P + min(len, g.own_rows) - g.Lq + m % g.Lq;
@@ -270,114 +343,117 @@ __device__ bool softmax_visit(const SharedParams& p, Walk& w, SoftCtx& c) {
   const int lo_all = max(max(bnd[0], bnd[2]), max(bnd[4], bnd[6]));
   const int hi_all = min(min(bnd[1], bnd[3]), min(bnd[5], bnd[7]));
 
-  float l_part[N], m_run[N == 16 ? 16 : 1];  // N = 64: thread t holds row t's reference maximum
+  float l_part[NG], m_run[NG == 16 ? 16 : 1];  // 64 rows: thread t holds row t's reference maximum
 #pragma unroll
-  for (int q = 0; q < N; ++q) l_part[q] = 0.f;
-  if constexpr (N == 16) {
+  for (int q = 0; q < NG; ++q) l_part[q] = 0.f;
 #pragma unroll
-    for (int q = 0; q < N; ++q) m_run[q] = -INFINITY;
-  } else {
-    m_run[0] = -INFINITY;
-  }
+  for (int q = 0; q < (NG == 16 ? 16 : 1); ++q) m_run[q] = -INFINITY;
 
   bool more = true;
+#pragma unroll 1
   while (more) {
     const int n = c.n, key0 = w.key0();
     const bool first = w.first;
     more = !w.last();
-    if (!__all_sync(0xffffffffu, mbar_wait(c.s_full + (n & 1), (n >> 1) & 1, c.abort))) return false;
+    if (!__all_sync(0xffffffffu, wait(c.bar.s_full + (n & 1), (n >> 1) & 1, c.abort))) return false;
     tc_fence_after();
-    uint32_t sr[N];
-    if constexpr (N == 16) {
-      tmem_ld16(c.tmem + lane_off + C::S_COL + NP * (n & 1), sr);
-    } else {
-      tmem_ld32(c.tmem + lane_off + C::S_COL + NP * (n & 1), *reinterpret_cast<uint32_t(*)[32]>(sr));
-      tmem_ld32(c.tmem + lane_off + C::S_COL + NP * (n & 1) + 32, *reinterpret_cast<uint32_t(*)[32]>(sr + 32));
-    }
-    tmem_wait_ld();
-    float x[N];
-    if (key0 >= lo_all && key0 + T - 1 <= hi_all) {
+    const uint32_t s_at = c.tmem + lane_off + C::S_COL + N * (n & 1) + col0;
+    const bool all = key0 >= lo_all && key0 + T - 1 <= hi_all;  // no row masks a key of this tile
+    const int key = key0 + t;
+    // 16 rows' scores, in log2 units; masked ones are -inf
+    auto scores = [&](int q0, float (&x)[16]) {
+      uint32_t sr[16];
+      tmem_ld16(s_at + q0, sr);
+      tmem_wait_ld();
 #pragma unroll
-      for (int q = 0; q < N; ++q) x[q] = __uint_as_float(sr[q]) * sl2;
-    } else {
-      const int key = key0 + t;
+      for (int q = 0; q < 16; ++q) x[q] = __uint_as_float(sr[q]) * sl2;
+      if (!all) {
 #pragma unroll
-      for (int q = 0; q < N; ++q) {
-        const int2 r = rng[q];
-        x[q] = (key >= r.x && key <= r.y) ? __uint_as_float(sr[q]) * sl2 : -INFINITY;
+        for (int q = 0; q < 16; ++q) {
+          const int2 r = rng[q0 + q];
+          if (key < r.x || key > r.y) x[q] = -INFINITY;
+        }
       }
-    }
-    bool waited = false;  // for PV(n - 1)
-    if constexpr (N == 16) {
-      float mx[N];
+    };
+    // O^T's columns of 16 rows times their factors
+    auto rescale = [&](int q0, const float (&f)[16]) {
+#pragma unroll 1
+      for (int h = 0; h < NDC; ++h) {
+        const uint32_t o_at = c.tmem + lane_off + C::O_COL + N * h + col0 + q0;
+        uint32_t ov[16];
+        tmem_ld16(o_at, ov);
+        tmem_wait_ld();
 #pragma unroll
-      for (int q = 0; q < N; ++q) mx[q] = x[q];
-      column_reduce<N, true>(mx, lane);
-      float* rb = red + (c.xc & 1) * 4 * NP;
-      column_post<N>(mx, rb + q4 * NP, lane);
+        for (int q = 0; q < 16; ++q) ov[q] = __float_as_uint(__uint_as_float(ov[q]) * f[q]);
+        tmem_st16(o_at, ov);
+      }
+    };
+    uint32_t pk[NG / 2];  // P, two rows a word
+    bool grow = false;
+    float x[NG == 16 ? 16 : 1], alpha[NG == 16 ? 16 : 1];
+    if constexpr (NG == 16) {
+      float mx[16];
+      scores(0, x);
+#pragma unroll
+      for (int q = 0; q < 16; ++q) mx[q] = x[q];
+      column_reduce<16, true>(mx, lane);
+      float* rb = red + (c.xc & 1) * 4 * NG;
+      column_post<16>(mx, rb + q4 * NG, lane);
       if (!exchange(c)) return false;
-      bool grow = false;
-      float alpha[N];
 #pragma unroll
-      for (int q = 0; q < N; ++q) {
-        const float tm = fmaxf(fmaxf(rb[q], rb[NP + q]), fmaxf(rb[2 * NP + q], rb[3 * NP + q]));
-        alpha[q] = 1.f;
-        if (tm > m_run[q] + kRescaleLog2) {  // the reference maximum moves (lazily)
-          if (m_run[q] != -INFINITY) {
-            alpha[q] = exp2f(m_run[q] - tm);
-            grow = true;
+      for (int q = 0; q < 16; q += 4) {
+        float4 v = *reinterpret_cast<const float4*>(rb + q);
+#pragma unroll
+        for (int i = 1; i < 4; ++i) {
+          const float4 u = *reinterpret_cast<const float4*>(rb + i * NG + q);
+          v = make_float4(fmaxf(v.x, u.x), fmaxf(v.y, u.y), fmaxf(v.z, u.z), fmaxf(v.w, u.w));
+        }
+        const float tm[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          alpha[q + e] = 1.f;
+          if (tm[e] > m_run[q + e] + kRescaleLog2) {  // the reference maximum moves (lazily)
+            if (m_run[q + e] != -INFINITY) {
+              alpha[q + e] = fast_exp2(m_run[q + e] - tm[e]);
+              grow = true;
+            }
+            m_run[q + e] = tm[e];
           }
-          m_run[q] = tm;
         }
-      }
-      if (grow) {  // uniform: every thread holds the same maxima
-        if (n > 0 && !__all_sync(0xffffffffu, mbar_wait(c.o_done, (n - 1) & 1, c.abort))) return false;
-        waited = true;
-        tc_fence_after();
-#pragma unroll
-        for (int h = 0; h < NDC; ++h) {
-          uint32_t ov[16];
-          tmem_ld16(c.tmem + lane_off + C::O_COL + NP * h, ov);
-          tmem_wait_ld();
-#pragma unroll
-          for (int q = 0; q < N; ++q) ov[q] = __float_as_uint(__uint_as_float(ov[q]) * alpha[q]);
-          tmem_st16(c.tmem + lane_off + C::O_COL + NP * h, ov);
-        }
-        tmem_wait_st();
-#pragma unroll
-        for (int q = 0; q < N; ++q) l_part[q] *= alpha[q];
-      }
-#pragma unroll
-      for (int q = 0; q < N; ++q) {
-        x[q] = fast_exp2(x[q] - (m_run[q] == -INFINITY ? 0.f : m_run[q]));
-        l_part[q] += x[q];
       }
     } else {
-      bool grow = first;
+      grow = first;
       if (!first) {
         bool over = false;
+#pragma unroll 1
+        for (int q0 = 0; q0 < NG; q0 += 16) {
+          float y[16];
+          scores(q0, y);
 #pragma unroll
-        for (int q = 0; q < N; q += 4) {
-          const float4 v = *reinterpret_cast<const float4*>(thr + q);
-          over |= x[q] > v.x || x[q + 1] > v.y || x[q + 2] > v.z || x[q + 3] > v.w;
+          for (int q = 0; q < 16; q += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(thr + q0 + q);
+            over |= y[q] > v.x || y[q + 1] > v.y || y[q + 2] > v.z || y[q + 3] > v.w;
+          }
         }
         if (__any_sync(0xffffffffu, over) && lane == 0) grow_tag[n & 1] = n + 1;
         if (!exchange(c)) return false;
         grow = grow_tag[n & 1] == n + 1;
       }
       if (grow) {
-        float mx[N];
-#pragma unroll
-        for (int q = 0; q < N; ++q) mx[q] = x[q];
-        column_reduce<N, true>(mx, lane);
-        float* rb = red + (c.xc & 1) * 4 * NP;
-        column_post<N>(mx, rb + q4 * NP, lane);
+        float* rb = red + (c.xc & 1) * 4 * NG;
+#pragma unroll 1
+        for (int q0 = 0; q0 < NG; q0 += 16) {
+          float y[16];
+          scores(q0, y);
+          column_reduce<16, true>(y, lane);
+          column_post<16>(y, rb + q4 * NG + q0, lane);
+        }
         if (!exchange(c)) return false;
-        if (t < N) {
-          const float tm = fmaxf(fmaxf(rb[t], rb[NP + t]), fmaxf(rb[2 * NP + t], rb[3 * NP + t]));
+        if (t < NG) {
+          const float tm = fmaxf(fmaxf(rb[t], rb[NG + t]), fmaxf(rb[2 * NG + t], rb[3 * NG + t]));
           float a = 1.f;
           if (tm > m_run[0] + kRescaleLog2) {
-            if (m_run[0] != -INFINITY) a = exp2f(m_run[0] - tm);
+            if (m_run[0] != -INFINITY) a = fast_exp2(m_run[0] - tm);
             m_run[0] = tm;
             use[t] = tm;
             thr[t] = tm + kRescaleLog2;
@@ -387,102 +463,136 @@ __device__ bool softmax_visit(const SharedParams& p, Walk& w, SoftCtx& c) {
           alp[t] = a;
         }
         if (!exchange(c)) return false;
-        if (!first) {
-          if (!__all_sync(0xffffffffu, mbar_wait(c.o_done, (n - 1) & 1, c.abort))) return false;
-          waited = true;
-          tc_fence_after();
-#pragma unroll 1
-          for (int h = 0; h < NDC; ++h)
+        grow = !first;
+      }
+    }
+    // P = 2^(score - reference), and the row sums
+    if constexpr (NG == 16) {
+      if (grow) {
 #pragma unroll
-            for (int hf = 0; hf < N / 32; ++hf) {
-              uint32_t ov[32];
-              tmem_ld32(c.tmem + lane_off + C::O_COL + NP * h + 32 * hf, ov);
-              tmem_wait_ld();
+        for (int q = 0; q < 16; ++q) l_part[q] *= alpha[q];
+      }
 #pragma unroll
-              for (int q = 0; q < 32; ++q) ov[q] = __float_as_uint(__uint_as_float(ov[q]) * alp[32 * hf + q]);
-              tmem_st32(c.tmem + lane_off + C::O_COL + NP * h + 32 * hf, ov);
-            }
-          tmem_wait_st();
+      for (int q = 0; q < 16; q += 2) {
+        const float e0 = fast_exp2(x[q] - (m_run[q] == -INFINITY ? 0.f : m_run[q]));
+        const float e1 = fast_exp2(x[q + 1] - (m_run[q + 1] == -INFINITY ? 0.f : m_run[q + 1]));
+        l_part[q] += e0;
+        l_part[q + 1] += e1;
+        pk[q / 2] = pack_bf16(e0, e1);
+      }
+    } else {
+      if (grow) {
 #pragma unroll
-          for (int q = 0; q < N; ++q) l_part[q] *= alp[q];
+        for (int q = 0; q < NG; q += 4) {
+          const float4 v = *reinterpret_cast<const float4*>(alp + q);
+          l_part[q] *= v.x;
+          l_part[q + 1] *= v.y;
+          l_part[q + 2] *= v.z;
+          l_part[q + 3] *= v.w;
         }
       }
 #pragma unroll
-      for (int q = 0; q < N; q += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(use + q);
-        x[q] = fast_exp2(x[q] - v.x);
-        x[q + 1] = fast_exp2(x[q + 1] - v.y);
-        x[q + 2] = fast_exp2(x[q + 2] - v.z);
-        x[q + 3] = fast_exp2(x[q + 3] - v.w);
+      for (int q0 = 0; q0 < NG; q0 += 16) {
+        float y[16];
+        scores(q0, y);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) l_part[q + e] += x[q + e];
+        for (int q = 0; q < 16; q += 4) {
+          const float4 v = *reinterpret_cast<const float4*>(use + q0 + q);
+          const float e0 = fast_exp2(y[q] - v.x), e1 = fast_exp2(y[q + 1] - v.y);
+          const float e2 = fast_exp2(y[q + 2] - v.z), e3 = fast_exp2(y[q + 3] - v.w);
+          l_part[q0 + q] += e0;
+          l_part[q0 + q + 1] += e1;
+          l_part[q0 + q + 2] += e2;
+          l_part[q0 + q + 3] += e3;
+          pk[(q0 + q) / 2] = pack_bf16(e0, e1);
+          pk[(q0 + q) / 2 + 1] = pack_bf16(e2, e3);
+        }
       }
     }
-    // PV(n - 1) has finished, so PV(n - 2), the last reader of P buffer n & 1, has too
-    if (!waited && n > 0 && !__all_sync(0xffffffffu, mbar_wait(c.o_done, (n - 1) & 1, c.abort))) return false;
-    unsigned char* pb = c.base + C::OFF_P + (n & 1) * C::PB;
-    if constexpr (N == 16) {
-      // K-major B operand: row q, key t -> chunk t / 64, 128-byte swizzle
-      pb += (t >> 6) * kOwnRows * 128;
-      const int kc = t & 63;
+    // PV(n - 1) has finished with P^T's buffer, and with O^T before it is rescaled
+    if (n > 0 && !__all_sync(0xffffffffu, wait(c.bar.o_done, (n - 1) & 1, c.abort))) return false;
+    if (grow) {  // uniform over the warpgroup
+      tc_fence_after();
+      if constexpr (NG == 16) {
+        rescale(0, alpha);
+      } else {
+#pragma unroll 1
+        for (int q0 = 0; q0 < NG; q0 += 16) {
+          float f[16];
 #pragma unroll
-      for (int q = 0; q < N; ++q)
-        *reinterpret_cast<__nv_bfloat16*>(pb + q * 128 + (((kc >> 3) ^ (q & 7)) << 4) + (kc & 7) * 2) =
-            __float2bfloat16_rn(x[q]);
+          for (int q = 0; q < 16; ++q) f[q] = alp[q0 + q];
+          rescale(q0, f);
+        }
+      }
+      tmem_wait_st();
+    }
+    unsigned char* pb = c.base + C::OFF_P;
+    if constexpr (NG == 16) {
+      // K-major B operand: row q, key t -> chunk t / 64, 128-byte swizzle
+      pb += (t >> 6) * kOwnRows * 128 + (t & 7) * 2;
+      const int kc = (t & 63) >> 3;
+#pragma unroll
+      for (int q = 0; q < 16; ++q)
+        *reinterpret_cast<uint16_t*>(pb + q * 128 + ((kc ^ (q & 7)) << 4)) = (uint16_t)(pk[q / 2] >> (16 * (q & 1)));
     } else {
-      // MN-major B operand: key t's 64 rows are one 128-byte swizzled line
+      // MN-major B operand: key t's 64 rows of this group are one 128-byte swizzled line
+      pb += c.group * T * 128 + t * 128;
 #pragma unroll
       for (int u = 0; u < 8; ++u)
-        *reinterpret_cast<uint4*>(pb + t * 128 + ((u ^ (t & 7)) << 4)) =
-            make_uint4(pack_bf16(x[8 * u], x[8 * u + 1]), pack_bf16(x[8 * u + 2], x[8 * u + 3]),
-                       pack_bf16(x[8 * u + 4], x[8 * u + 5]), pack_bf16(x[8 * u + 6], x[8 * u + 7]));
+        *reinterpret_cast<uint4*>(pb + ((u ^ (t & 7)) << 4)) =
+            make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
     }
     fence_proxy_async_smem();  // generic writes -> the tensor core's reads
     tc_fence_before();
-    mbar_arrive(c.p_full + (n & 1));
+    __syncwarp();
+    if (lane == 0) mbar_arrive(c.bar.p_full);
     ++c.n;
     w.next();
   }
 
   // the visit's partial: row sums over the 128 threads, then O^T
-  column_reduce<N, false>(l_part, lane);
-  float* rb = red + (c.xc & 1) * 4 * NP;
-  column_post<N>(l_part, rb + q4 * NP, lane);
-  if (!exchange(c)) return false;
-  if (!__all_sync(0xffffffffu, mbar_wait(c.o_done, (c.n - 1) & 1, c.abort))) return false;
-  tc_fence_after();
-  const size_t slot = (size_t)blockIdx.x + at.seg;
-  const int stride = at.own ? p.s.orow : p.s.prow;  // rows of a slot
-  int rows;                                         // of which this segment has
-  if (at.own) rows = min(kOwnRows, g.M - at.blk * kOwnRows);
-  else if (p.s.nmb > 1) rows = min(NP, g.M - at.blk % p.s.nmb * NP);
-  else rows = min(p.s.nb, g.B - at.blk * p.s.nb) * g.M;
-  float* out = (at.own ? p.po_o : p.pp_o) + slot * stride * D;
-  float* ml = (at.own ? p.po_ml : p.pp_ml) + slot * stride * 2;
-  if (t < rows) {
-    float m;
-    if constexpr (N == 16) {
-      m = m_run[0];
+  float* rb = red + (c.xc & 1) * 4 * NG;
 #pragma unroll
-      for (int q = 1; q < N; ++q) m = t == q ? m_run[q] : m;
-    } else {
-      m = m_run[0];
+  for (int q0 = 0; q0 < NG; q0 += 16) {
+    float v[16];
+#pragma unroll
+    for (int q = 0; q < 16; ++q) v[q] = l_part[q0 + q];
+    column_reduce<16, false>(v, lane);
+    column_post<16>(v, rb + q4 * NG + q0, lane);
+  }
+  if (!exchange(c)) return false;
+  if (!__all_sync(0xffffffffu, wait(c.bar.o_done, (c.n - 1) & 1, c.abort))) return false;
+  tc_fence_after();
+  const int stride = OWN ? p.s.orow : p.s.prow;  // rows of a slot
+  int rows;                                      // of which this segment has, and this group from row NG * group on
+  if (OWN) rows = min(kOwnRows, g.M - blk * kOwnRows);
+  else if (p.s.nmb > 1) rows = min(N, g.M - blk % p.s.nmb * N);
+  else rows = min(p.s.nb, g.B - blk * p.s.nb) * g.M;
+  rows -= NG * c.group;
+  const size_t at = (size_t)slot * stride + NG * c.group;
+  float* out = (OWN ? p.po_o : p.pp_o) + at * D;
+  float* ml = (OWN ? p.po_ml : p.pp_ml) + at * 2;
+  if (t < min(rows, NG)) {
+    float m = m_run[0];
+    if constexpr (NG == 16) {
+#pragma unroll
+      for (int q = 1; q < NG; ++q) m = t == q ? m_run[q] : m;
     }
     *reinterpret_cast<float2*>(ml + 2 * t) =
-        make_float2(m, (rb[t] + rb[NP + t]) + (rb[2 * NP + t] + rb[3 * NP + t]));
+        make_float2(m, (rb[t] + rb[NG + t]) + (rb[2 * NG + t] + rb[3 * NG + t]));
   }
 #pragma unroll 1
   for (int h = 0; h < NDC; ++h) {
-    const int d = 128 * h + t;
-#pragma unroll
-    for (int part = 0; part < N / 16; ++part) {
+    float* dst = out + 128 * h + t;
+#pragma unroll 1
+    for (int q0 = 0; q0 < min(rows, NG); q0 += 16) {
       uint32_t ov[16];
-      tmem_ld16(c.tmem + lane_off + C::O_COL + NP * h + 16 * part, ov);  // warp-collective
+      tmem_ld16(c.tmem + lane_off + C::O_COL + N * h + col0 + q0, ov);  // warp-collective
       tmem_wait_ld();
-      if (d < D) {
+      if (128 * h + t < D) {
 #pragma unroll
         for (int q = 0; q < 16; ++q)
-          if (16 * part + q < rows) out[(size_t)(16 * part + q) * D + d] = __uint_as_float(ov[q]);
+          if (q0 + q < rows) dst[(q0 + q) * D] = __uint_as_float(ov[q]);
       }
     }
   }
@@ -490,40 +600,169 @@ __device__ bool softmax_visit(const SharedParams& p, Walk& w, SoftCtx& c) {
   return true;
 }
 
+// One phase of a CTA's work: `total` tiles from walk `w0` on, all warp roles.
+template <int D, int N, bool OWN, typename Walk>
+__device__ void run_phase(const SharedParams& p, unsigned char* base, uint64_t* bar_mem, volatile int* abort_flag,
+                          uint32_t tmem, const CUtensorMap* tmQ, const CUtensorMap* tmK, const CUtensorMap* tmV,
+                          const Walk& w0, int total) {
+  using C = ShCfg<D, N, OWN>;
+  constexpr int NCH = C::NCH, CPS = C::CPS, SPT = C::SPT, NSLOT = C::NSLOT, QD = C::QD;
+  const SharedGeom& g = p.g;
+  const Bars bar(bar_mem);
+  const int warp = threadIdx.x / 32;
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer
+    if (elect_one()) {
+      Walk wk = w0, wv = w0;
+      int issued = 0, nq = 0;
+      auto load_tile = [&](Walk& w, const CUtensorMap* m) -> bool {
+        const int key0 = w.key0();
+        int head = w.h;
+        if constexpr (OWN) head += w.b * g.Hkv;
+#pragma unroll 1
+        for (int sp = 0; sp < SPT; ++sp, ++issued) {
+          const int s = issued % NSLOT;
+          if (issued >= NSLOT && !wait(bar.slot_empty + s, ((issued / NSLOT) & 1) ^ 1, abort_flag)) return false;
+          mbar_arrive_expect_tx(bar.slot_full + s, C::SLOT);
+          tma_load_4d(base + s * C::SLOT, m, bar.slot_full + s, 0, key0, sp * CPS, head);
+        }
+        w.next();
+        return true;
+      };
+      auto load_k = [&]() -> bool {
+        if (wk.first) {
+          const int s = nq % QD;
+          if (nq >= QD && !wait(bar.q_empty + s, ((nq / QD) & 1) ^ 1, abort_flag)) return false;
+          unsigned char* q = base + C::OFF_Q + s * C::QB;
+          if constexpr (OWN) {
+            mbar_arrive_expect_tx(bar.q_full + s, C::QB);
+            tma_load_4d(q, tmQ, bar.q_full + s, 0, wk.blk * kOwnRows, 0, wk.b * g.Hkv + wk.h);
+          } else {
+            mbar_arrive_expect_tx(bar.q_full + s, NCH * p.s.prow * 128);
+#pragma unroll 1
+            for (int c = 0; c < NCH; ++c)
+              tma_load_5d(q + c * N * 128, tmQ, bar.q_full + s, 0, wk.blk % p.s.nmb * N, c, wk.h,
+                          wk.blk / p.s.nmb * p.s.nb);
+          }
+          ++nq;
+        }
+        return load_tile(wk, tmK);
+      };
+      // slots in MMA order: K(0), K(1), then per tile n: V(n), K(n + 2)
+      bool ok = true;
+#pragma unroll 1
+      for (int n = -2; ok && n < total; ++n) ok = (n < 0 || load_tile(wv, tmV)) && (n + 2 >= total || load_k());
+      if (*abort_flag) {  // unwinding: the loads in flight land before shared memory is released
+        drain_ring(bar.q_full, QD, nq);
+        drain_ring(bar.slot_full, NSLOT, issued);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (elect_one()) {
+      const uint32_t idS = idesc_f16(T, N, 1, 1, 0, 0);                // K x Q^T, both K-major
+      const uint32_t idPV = idesc_f16(T, N, 1, 1, 1, N > 16 ? 1 : 0);  // V^T (MN-major) x P^T
+      Walk ws = w0, wv = w0;
+      int used = 0, nq = 0;
+      auto issue_s = [&](int n) -> bool {  // S^T(n) into buffer n & 1
+        const int qs = nq % QD;
+        if (ws.first && !wait(bar.q_full + qs, (nq / QD) & 1, abort_flag)) return false;
+        uint64_t qd = smem_desc_sw128(smem_u32(base + C::OFF_Q + qs * C::QB), 16, 1024);
+#pragma unroll 1
+        for (int sp = 0; sp < SPT; ++sp, ++used) {
+          const int s = used % NSLOT;
+          if (!wait(bar.slot_full + s, (used / NSLOT) & 1, abort_flag)) return false;
+          tc_fence_after();
+          uint64_t kd = smem_desc_sw128(smem_u32(base + s * C::SLOT), 16, 1024);
+#pragma unroll 1
+          for (int cc = 0; cc < CPS; ++cc) {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              mma_ss(tmem + C::S_COL + N * (n & 1), desc_add(kd, ks * 32), desc_add(qd, ks * 32), idS,
+                     (sp | cc | ks) ? 1u : 0u);
+            kd = desc_add(kd, T * 128);
+            qd = desc_add(qd, N * 128);
+          }
+          mma_commit(bar.slot_empty + s);
+        }
+        mma_commit(bar.s_full + (n & 1));
+        if (ws.last()) {  // the visit's queries are read
+          mma_commit(bar.q_empty + qs);
+          ++nq;
+        }
+        ws.next();
+        return true;
+      };
+      const uint64_t pd = smem_desc_sw128(smem_u32(base + C::OFF_P), N > 16 ? T * 128 : 16, 1024);
+      bool ok = true;
+#pragma unroll 1
+      for (int n = -2; ok && n < total; ++n) {
+        if (n >= 0) {
+          if (!wait(bar.p_full, n & 1, abort_flag)) break;
+          tc_fence_after();
+          const uint32_t acc = wv.first ? 0u : 1u;
+          // O^T block h (head-dim columns [128 h, 128 h + 128)) += V^T . P^T: one slot a block
+#pragma unroll 1
+          for (int h = 0; h < SPT; ++h, ++used) {
+            const int s = used % NSLOT;
+            if (!wait(bar.slot_full + s, (used / NSLOT) & 1, abort_flag)) { ok = false; break; }
+            tc_fence_after();
+            const uint64_t vd = smem_desc_sw128(smem_u32(base + s * C::SLOT), T * 128, 1024);  // MN-major
+#pragma unroll
+            for (int ks = 0; ks < T / 16; ++ks)
+              mma_ss(tmem + C::O_COL + N * h, desc_add(vd, ks * 2048),
+                     N > 16 ? desc_add(pd, ks * 2048) : desc_add(pd, (ks >> 2) * kOwnRows * 128 + (ks & 3) * 32),
+                     idPV, (acc || ks > 0) ? 1u : 0u);
+            mma_commit(bar.slot_empty + s);
+          }
+          if (!ok) break;
+          mma_commit(bar.o_done);
+          wv.next();
+        }
+        if (n + 2 < total) ok = issue_s(n + 2);  // after PV(n): S buffer n & 1 is free
+      }
+      mma_commit(bar.drain);
+      mbar_wait_drain(bar.drain, 0);
+    }
+  } else if ((warp - 2) / 4 < C::GROUPS) {
+    // ------------------------------------------------------------ softmax
+    const int group = (warp - 2) / 4;
+    SoftCtx c{base, base + C::OFF_SMALL + group * C::SMALL, bar, abort_flag, tmem, group, 0, 0};
+    Walk w = w0;
+    bool ok = true;
+#pragma unroll 1
+    while (ok && c.n < total) ok = softmax_visit<D, N, OWN>(p, w, c);
+  }
+  __syncwarp();
+}
+
 template <int D, int NP>
-__global__ void __launch_bounds__(kThr, 1)
+__global__ void __launch_bounds__(ShKernel<D, NP>::THREADS, 1)
     shared_kernel(const __grid_constant__ CUtensorMap tmQP, const __grid_constant__ CUtensorMap tmQO,
                   const __grid_constant__ CUtensorMap tmKP, const __grid_constant__ CUtensorMap tmVP,
                   const __grid_constant__ CUtensorMap tmKO, const __grid_constant__ CUtensorMap tmVO,
                   const __grid_constant__ SharedParams p) {
-  using C = ShCfg<D, NP>;
-  constexpr int NCH = C::NCH, CPS = C::CPS, SPT = C::SPT, NSLOT = C::NSLOT, QD = C::QD;
+  using K = ShKernel<D, NP>;
+  using A = typename K::A;
+  constexpr int THR = K::THREADS, NW = THR / 32;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ int scan_sum[6], scan_min[6], start_b, start_r;
+  __shared__ int scan_sum[NW], scan_min[NW], start_b, start_r;
+  __shared__ unsigned scan_best[NW];
   unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(base + C::OFF_BAR);
-  uint64_t* slot_full = bars;                  // [NSLOT]
-  uint64_t* slot_empty = slot_full + NSLOT;    // [NSLOT]
-  uint64_t* qp_full = slot_empty + NSLOT;      // [1] prefix queries of a visit
-  uint64_t* qp_empty = qp_full + 1;            // [1]
-  uint64_t* qo_full = qp_empty + 1;            // [QD] own queries
-  uint64_t* qo_empty = qo_full + QD;           // [QD]
-  uint64_t* s_full = qo_empty + QD;            // [2] S^T(n) in TMEM
-  uint64_t* p_full = s_full + 2;               // [2] P^T(n) written (and O^T rescaled)
-  uint64_t* o_done = p_full + 2;               // [1] PV(n) finished
-  uint64_t* xch = o_done + 1;                  // [1] softmax threads' exchanges
-  uint64_t* mma_drain = xch + 1;               // [1]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_drain + 1);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + K::OFF_BAR);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 32);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint64_t* bars2 = bars + 48;
 
   const SharedGeom& g = p.g;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   grid_launch_dependents();  // the merge waits for this grid's end
 
-  // ---- this CTA's run of units, from the lengths on the device
+  // ---- the lengths: own tiles in all, the shortest live request
   {
     int sum = 0, mn = INT32_MAX;
-    for (int b = threadIdx.x; b < g.B; b += kThr) {
+#pragma unroll 1
+    for (int b = threadIdx.x; b < g.B; b += THR) {
       const int len = p.own_len[b];
       sum += own_tiles(g, len);
       if (len >= 0) mn = min(mn, min(len, g.own_rows));
@@ -535,35 +774,87 @@ __global__ void __launch_bounds__(kThr, 1)
       scan_min[warp] = mn;
     }
   }
-  if (threadIdx.x == 0) start_b = -1;
+  if (threadIdx.x == 0) {
+    start_b = -1;
+    *abort_flag = 0;
+    prefetch_tmap(&tmKP);
+    prefetch_tmap(&tmKO);
+  }
+  if (threadIdx.x < 64 && lane < Bars::kCount) {
+    mbar_init((warp ? bars2 : bars) + lane, Bars::arrivals(lane, warp ? 1 : A::GROUPS));
+    fence_mbar_init();
+  }
+  // rows of the prefix query block that no box fills stay zero
+#pragma unroll 1
+  for (int i = threadIdx.x; i < A::QB / 16; i += THR) reinterpret_cast<uint4*>(base + A::OFF_Q)[i] = make_uint4(0, 0, 0, 0);
+  if (threadIdx.x < 2 * A::GROUPS)  // growth tags
+    reinterpret_cast<int*>(base + A::OFF_SMALL + (threadIdx.x >> 1) * A::SMALL + A::BND)[8 + (threadIdx.x & 1)] = 0;
+  fence_proxy_async_smem();
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, K::TCOLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
   int tiles = 0, mn = INT32_MAX;
 #pragma unroll
-  for (int i = 0; i < 6; ++i) {
+  for (int i = 0; i < NW; ++i) {
     tiles += scan_sum[i];
     mn = min(mn, scan_min[i]);
   }
-  // prefix keys that some row sees start at key_lo (none without a live request)
+
+  // ---- the split.  Prefix keys that some row sees start at key_lo (there are
+  // none without a live request); tp tiles of nseg segments, in ns ranges each
+  const int ctas = gridDim.x, cta = blockIdx.x;
   const int key_lo = mn == INT32_MAX ? g.P : (g.W > 0 ? min(g.P, max(0, g.P + mn - g.Lq - g.W + 1)) : 0);
   const int tp = (g.P - key_lo + T - 1) / T;
-  const int hn = g.Hkv * p.s.nomb;
-  const int up = g.Hkv * p.s.nrb * tp, units = up + tiles * hn;
-  const int ctas = min((int)gridDim.x, units);
-  const int cta = blockIdx.x;
-  if (cta == 0 && threadIdx.x == 0) {
-    p.plan[0] = tp;
-    p.plan[1] = units;
-    p.plan[2] = ctas;
-    p.plan[3] = key_lo;
+  const int nseg = tp > 0 ? g.Hkv * p.s.nrb : 0, hn = g.Hkv * p.s.nomb, own_units = tiles * hn;
+  // ns: the one that makes the longest CTA's units fewest, a piece counting one
+  // unit more than its tiles (its queries' load and its partial's store)
+  const int most = nseg ? min(tp, max(1, kPieces / nseg)) : 0;
+  {
+    unsigned mine = ~0u;
+#pragma unroll 1
+    for (int i = 1 + threadIdx.x; i <= most; i += THR) {
+      const int np = nseg * i, k = (np + ctas - 1) / ctas;
+      const int all = (nseg * tp + np + own_units + ctas - 1) / ctas;
+      mine = min(mine, (unsigned)min(max(k * ((tp + i - 1) / i + 1), all), 0x3fffff) << 9 | i);
+    }
+    mine = __reduce_min_sync(0xffffffffu, mine);
+    if (lane == 0) scan_best[warp] = mine;
   }
-  if (cta >= ctas && cta != 0) return;
-  const int u0 = ctas ? (int)((long long)units * cta / ctas) : 0;
-  const int u1 = ctas ? (int)((long long)units * (cta + 1) / ctas) : 0;
-  // the request that unit u0 belongs to (own units only); CTA 0 writes every
-  // request's offset for the merge
-  if (u0 >= up || cta == 0) {
+  __syncthreads();
+  unsigned best = ~0u;
+#pragma unroll
+  for (int i = 0; i < NW; ++i) best = min(best, scan_best[i]);
+  const int ns = nseg ? best & 511 : 1, pieces = nseg * ns;
+  // own runs fill the CTAs up to the same number of units: the first `rich`
+  // CTAs have `rounds` pieces, the others one less
+  const int rounds = (pieces + ctas - 1) / ctas, rich = pieces - (rounds > 0 ? rounds - 1 : 0) * ctas;
+  const int pl = pieces ? (tp + ns - 1) / ns + 1 : 0, even = (own_units + pieces * pl + ctas - 1) / ctas;
+  const int qa = max(0, even - rounds * pl);  // own units of a rich CTA, and of another
+  const int qb = qa > 0 || rich == ctas ? even - (rounds - 1) * pl : (own_units + ctas - rich - 1) / (ctas - rich);
+  auto own_start = [&](int c) {
+    const long long u = c < rich ? (long long)c * qa : (long long)rich * qa + (long long)(c - rich) * qb;
+    return c >= ctas || u > own_units ? own_units : (int)u;
+  };
+  const int o0 = own_start(cta), o1 = own_start(cta + 1);
+  if (cta == 0) {  // for the merge
+    if (threadIdx.x == 0) {
+      p.plan[0] = tp;
+      p.plan[1] = ns;
+    }
+#pragma unroll 1
+    for (int c = threadIdx.x; c <= ctas; c += THR) p.plan[kPlanStart + c] = own_start(c);
+  }
+  // the request that own unit o0 belongs to; CTA 0 also writes every request's
+  // first tile for the merge
+  if (o0 < o1 || cta == 0) {
     int before = 0;
-    for (int c0 = 0; c0 < g.B; c0 += kThr) {
+#pragma unroll 1
+    for (int c0 = 0; c0 < g.B; c0 += THR) {
       const int b = c0 + threadIdx.x;
       const int nt = b < g.B ? own_tiles(g, p.own_len[b]) : 0;
       int inc = nt;
@@ -576,215 +867,49 @@ __global__ void __launch_bounds__(kThr, 1)
       if (lane == 31) scan_sum[warp] = inc;
       __syncthreads();
       int off = before + inc - nt;
-      for (int i = 0; i < 6; ++i) {
+      for (int i = 0; i < NW; ++i) {
         if (i < warp) off += scan_sum[i];
         before += scan_sum[i];
       }
-      if (cta == 0 && b < g.B) p.plan[kPlanInts + b] = off;
-      const int v = u0 - up;
-      if (nt > 0 && v >= off * hn && v < (off + nt) * hn) {
+      if (cta == 0 && b < g.B) p.plan[kPlanOff + b] = off;
+      if (nt > 0 && o0 >= off * hn && o0 < (off + nt) * hn) {
         start_b = b;
-        start_r = v - off * hn;
+        start_r = o0 - off * hn;
       }
     }
+    __syncthreads();
   }
-  if (ctas == 0) return;
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < NSLOT; ++s) {
-      mbar_init(slot_full + s, 1);
-      mbar_init(slot_empty + s, 1);
+  // ---- the prefix pieces, then the own run
+  if (cta < pieces) {
+    PrefixWalk w;
+    w.p = &p;
+    w.splits = ns;
+    w.tiles = tp / ns;
+    w.extra = tp - ns * w.tiles;
+    w.key_lo = key_lo;
+    int total = 0;
+#pragma unroll 1
+    for (int i = cta; i < pieces; i += ctas) {
+      w.begin(i);
+      total += w.t1 - w.t;
     }
-    mbar_init(qp_full, 1);
-    mbar_init(qp_empty, 1);
-    for (int s = 0; s < QD; ++s) {
-      mbar_init(qo_full + s, 1);
-      mbar_init(qo_empty + s, 1);
-    }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(s_full + s, 1);
-      mbar_init(p_full + s, 128);
-    }
-    mbar_init(o_done, 1);
-    mbar_init(xch, 128);
-    mbar_init(mma_drain, 1);
-    *abort_flag = 0;
-    fence_mbar_init();
+    w.begin(cta);
+    run_phase<D, NP, false>(p, base, bars, abort_flag, tmem, &tmQP, &tmKP, &tmVP, w, total);
   }
-  // rows of the prefix query block that no box fills stay zero
-  for (int i = threadIdx.x; i < C::QP / 16; i += kThr) reinterpret_cast<uint4*>(base + C::OFF_QP)[i] = make_uint4(0, 0, 0, 0);
-  if (threadIdx.x < 2) reinterpret_cast<int*>(base + C::OFF_BND)[8 + threadIdx.x] = 0;  // growth tags
-  fence_proxy_async_smem();
-  if (warp == 1) {
-    tmem_alloc(tmem_slot, C::TCOLS);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-
-  Walk w0;
-  w0.p = &p;
-  w0.left = u1 - u0;
-  w0.key_lo = key_lo;
-  w0.first = true;
-  w0.n = 0;
-  if (u0 < up) {
-    w0.own = 0;
-    w0.seg = u0 / tp;
-    w0.t = u0 - w0.seg * tp;
-    w0.nt = tp;
-    w0.h = w0.seg / p.s.nrb;
-    w0.blk = w0.seg - w0.h * p.s.nrb;
-    w0.b = 0;
-  } else {
-    w0.own = 1;
-    w0.b = start_b;
-    w0.set_own();
-    const int in = start_r / w0.nt;  // (kv head, row block)
-    w0.t = start_r - in * w0.nt;
-    w0.h = in / p.s.nomb;
-    w0.blk = in - w0.h * p.s.nomb;
-    w0.seg = w0.b * hn + in;
-  }
-  const int total = w0.left;
-
-  if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer
-    if (elect_one()) {
-      prefetch_tmap(&tmKP);
-      prefetch_tmap(&tmVP);
-      prefetch_tmap(&tmKO);
-      prefetch_tmap(&tmVO);
-      Walk wk = w0, wv = w0;
-      int issued = 0, np = 0, no = 0;
-      auto load_tile = [&](Walk& w, const CUtensorMap* mp, const CUtensorMap* mo) -> bool {
-        const int key0 = w.key0();
-        for (int sp = 0; sp < SPT; ++sp, ++issued) {
-          const int s = issued % NSLOT;
-          if (issued >= NSLOT && !mbar_wait(slot_empty + s, ((issued / NSLOT) & 1) ^ 1, abort_flag)) return false;
-          mbar_arrive_expect_tx(slot_full + s, C::SLOT);
-          tma_load_4d(base + s * C::SLOT, w.own ? mo : mp, slot_full + s, 0, key0, sp * CPS,
-                      w.own ? w.b * g.Hkv + w.h : w.h);
-        }
-        w.next();
-        return true;
-      };
-      auto load_k = [&]() -> bool {
-        if (wk.first && !wk.own) {
-          if (np > 0 && !mbar_wait(qp_empty, (np - 1) & 1, abort_flag)) return false;
-          mbar_arrive_expect_tx(qp_full, NCH * p.s.prow * 128);
-          for (int c = 0; c < NCH; ++c)
-            tma_load_5d(base + C::OFF_QP + c * NP * 128, &tmQP, qp_full, 0, wk.blk % p.s.nmb * NP, c, wk.h,
-                        wk.blk / p.s.nmb * p.s.nb);
-          ++np;
-        } else if (wk.first) {
-          const int s = no % QD;
-          if (no >= QD && !mbar_wait(qo_empty + s, ((no / QD) & 1) ^ 1, abort_flag)) return false;
-          mbar_arrive_expect_tx(qo_full + s, C::QO);
-          tma_load_4d(base + C::OFF_QO + s * C::QO, &tmQO, qo_full + s, 0, wk.blk * kOwnRows, 0, wk.b * g.Hkv + wk.h);
-          ++no;
-        }
-        return load_tile(wk, &tmKP, &tmKO);
-      };
-      // slots in MMA order: K(0), K(1), then per tile n: V(n), K(n + 2)
-      bool ok = load_k() && (total < 2 || load_k());
-      for (int n = 0; ok && n < total; ++n) ok = load_tile(wv, &tmVP, &tmVO) && (n + 2 >= total || load_k());
-      if (*abort_flag) {  // unwinding: the loads in flight land before shared memory is released
-        if (np > 0) mbar_wait_drain(qp_full, (np - 1) & 1);
-        drain_ring(qo_full, QD, no);
-        drain_ring(slot_full, NSLOT, issued);
-      }
+  if (o0 < o1) {
+    if (cta < pieces) {  // the shared memory and the accumulators change hands
+      fence_proxy_async_smem();  // the small arrays' generic accesses, before loads that land there
+      tc_fence_before();
+      __syncthreads();
+      tc_fence_after();
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    if (elect_one()) {
-      const uint32_t idSp = idesc_f16(T, NP, 1, 1, 0, 0), idSo = idesc_f16(T, kOwnRows, 1, 1, 0, 0);  // K x Q^T, both K-major
-      const uint32_t idPVp = idesc_f16(T, NP, 1, 1, 1, NP > 16 ? 1 : 0);  // V^T (MN-major) x P^T
-      const uint32_t idPVo = idesc_f16(T, kOwnRows, 1, 1, 1, 0);
-      Walk ws = w0, wv = w0;
-      int used = 0, np = 0, no = 0;
-      auto issue_s = [&](int n) -> bool {  // S^T(n) into buffer n & 1
-        const int own = ws.own, qs = own ? (no % QD) : 0;
-        uint64_t* qf = own ? qo_full + qs : qp_full;
-        if (ws.first && !mbar_wait(qf, own ? (no / QD) & 1 : np & 1, abort_flag)) return false;
-        const uint64_t qd = smem_desc_sw128(smem_u32(base + (own ? C::OFF_QO + qs * C::QO : C::OFF_QP)), 16, 1024);
-        const uint32_t qpitch = (own ? kOwnRows : NP) * 128, idS = own ? idSo : idSp;
-        for (int sp = 0; sp < SPT; ++sp, ++used) {
-          const int s = used % NSLOT;
-          if (!mbar_wait(slot_full + s, (used / NSLOT) & 1, abort_flag)) return false;
-          tc_fence_after();
-          const uint64_t kd = smem_desc_sw128(smem_u32(base + s * C::SLOT), 16, 1024);
-#pragma unroll
-          for (int cc = 0; cc < CPS; ++cc) {
-            const int c = sp * CPS + cc;
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              mma_ss(tmem + C::S_COL + NP * (n & 1), desc_add(kd, cc * T * 128 + ks * 32),
-                     desc_add(qd, c * qpitch + ks * 32), idS, (c | ks) ? 1u : 0u);
-          }
-          mma_commit(slot_empty + s);
-        }
-        mma_commit(s_full + (n & 1));
-        if (ws.last()) {  // the visit's queries are read
-          mma_commit(own ? qo_empty + qs : qp_empty);
-          if (own) ++no;
-          else ++np;
-        }
-        ws.next();
-        return true;
-      };
-      bool ok = issue_s(0) && (total < 2 || issue_s(1));
-      for (int n = 0; ok && n < total; ++n) {
-        if (!mbar_wait(p_full + (n & 1), (n >> 1) & 1, abort_flag)) { ok = false; break; }
-        tc_fence_after();
-        const int own = wv.own;
-        const uint32_t acc = wv.first ? 0u : 1u;
-        const uint64_t pd = (NP > 16 && !own) ? smem_desc_sw128(smem_u32(base + C::OFF_P + (n & 1) * C::PB), T * 128, 1024)
-                                              : smem_desc_sw128(smem_u32(base + C::OFF_P + (n & 1) * C::PB), 16, 1024);
-        // O^T block h (head-dim columns [128 h, 128 h + 128)) += V^T . P^T: one slot a block
-        for (int h = 0; h < SPT; ++h, ++used) {
-          const int s = used % NSLOT;
-          if (!mbar_wait(slot_full + s, (used / NSLOT) & 1, abort_flag)) { ok = false; break; }
-          tc_fence_after();
-          const uint64_t vd = smem_desc_sw128(smem_u32(base + s * C::SLOT), T * 128, 1024);  // MN-major
-          if (NP > 16 && !own) {
-#pragma unroll
-            for (int ks = 0; ks < T / 16; ++ks)
-              mma_ss(tmem + C::O_COL + NP * h, desc_add(vd, ks * 2048), desc_add(pd, ks * 2048), idPVp,
-                     (acc || ks > 0) ? 1u : 0u);
-          } else {
-#pragma unroll
-            for (int ks = 0; ks < T / 16; ++ks)
-              mma_ss(tmem + C::O_COL + NP * h, desc_add(vd, ks * 2048),
-                     desc_add(pd, (ks >> 2) * kOwnRows * 128 + (ks & 3) * 32), idPVo, (acc || ks > 0) ? 1u : 0u);
-          }
-          mma_commit(slot_empty + s);
-        }
-        if (!ok) break;
-        mma_commit(o_done);
-        wv.next();
-        if (n + 2 < total && !issue_s(n + 2)) { ok = false; break; }  // after PV(n): S buffer n & 1 is free
-      }
-      mma_commit(mma_drain);
-      mbar_wait_drain(mma_drain, 0);
+    if (!*abort_flag) {
+      OwnWalk w;
+      w.p = &p;
+      w.begin(start_b, start_r, o1 - o0);
+      run_phase<D, kOwnRows, true>(p, base, bars2, abort_flag, tmem, &tmQO, &tmKO, &tmVO, w, o1 - o0);
     }
-  } else {
-    // ------------------------------------------------------------ softmax
-    SoftCtx c;
-    c.base = base;
-    c.s_full = s_full;
-    c.p_full = p_full;
-    c.o_done = o_done;
-    c.xch = xch;
-    c.abort = abort_flag;
-    c.tmem = tmem;
-    c.n = 0;
-    c.xc = 0;
-    Walk w = w0;
-    bool ok = true;
-    while (ok && w.left > 0) ok = w.own ? softmax_visit<D, NP, kOwnRows>(p, w, c) : softmax_visit<D, NP, NP>(p, w, c);
   }
 
   __syncwarp();
@@ -793,78 +918,115 @@ __global__ void __launch_bounds__(kThr, 1)
   if (*abort_flag && threadIdx.x == 0) atomicCAS(p.status, 0, kStatusTimeout);
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, C::TCOLS);
+    tmem_dealloc(tmem, K::TCOLS);
   }
 }
 
-// Merge of one query row's partials: those of its prefix block and of its own
-// cache, one for each CTA that had a run of the segment.  Rows without a key
+// Merge of one query row's partials: those of its prefix block's pieces, and
+// of its own cache, one for each CTA that had a part of the segment.  Rows without a key
 // get o = 0 and lse = -inf (or the sink's logit); rows of an empty place of
 // the batch are not written.
 template <int D>
 struct MergeCfg {
   static constexpr int VEC = D >= 128 ? 4 : 2, THREADS = D / VEC;
 };
-constexpr int kMaxParts = 2 * kSMs;
+constexpr int kMaxParts = kPieces + kSMs;
 
 template <int D>
-__global__ void __launch_bounds__(MergeCfg<D>::THREADS) shared_merge_kernel(const SharedParams p) {
-  constexpr int VEC = MergeCfg<D>::VEC;
+__global__ void __launch_bounds__(MergeCfg<D>::THREADS) shared_merge_kernel(const __grid_constant__ SharedParams p) {
+  constexpr int VEC = MergeCfg<D>::VEC, AHEAD = 8;
   __shared__ float wts[kMaxParts];
+  __shared__ int owner[kSMs], n_own;  // the CTAs that have a part of the row's own segment
   __shared__ float stat[2];
   const SharedGeom& g = p.g;
   const SharedSplit& s = p.s;
   const int row = blockIdx.x;  // (b Hkv + kv head) M + m
   const int bkv = row / g.M, m = row - bkv * g.M, b = bkv / g.Hkv, h = bkv - b * g.Hkv;
+  const int lane = threadIdx.x & 31;
   grid_dependency_wait();
-  const int len = p.own_len[b];
+  // the lengths and the plan, in one round of loads
+  const int len = p.own_len[b], tp = p.plan[0], ns = p.plan[1], off = p.plan[kPlanOff + b];
+  int start[(kSMs + 31) / 32 + 1];
+  if (threadIdx.x < 32) {
+#pragma unroll
+    for (int i = 0; i <= kSMs / 32; ++i) start[i] = 32 * i + lane <= kSMs ? p.plan[kPlanStart + 32 * i + lane] : INT32_MAX;
+  }
   if (len < 0) return;
-  const int tp = p.plan[0], units = p.plan[1], ctas = p.plan[2];
-  const int nt = own_tiles(g, len), hn = g.Hkv * s.nomb;
-  // CTAs c whose run holds a unit u: floor(units c / ctas) <= u
-  auto cta_of = [&](int u) { return (int)((((long long)u + 1) * ctas - 1) / units); };
-  int np = 0, no = 0;
-  const float *pml = nullptr, *po = nullptr, *oml = nullptr, *oo = nullptr;
-  if (tp > 0) {
-    const int rb = s.nmb > 1 ? b * s.nmb + m / s.np : b / s.nb;
-    const int q = s.nmb > 1 ? m % s.np : b % s.nb * g.M + m;
-    const int seg = h * s.nrb + rb;
-    const int c0 = cta_of(seg * tp);
-    np = cta_of(seg * tp + tp - 1) - c0 + 1;
-    const size_t at = (size_t)(c0 + seg) * s.prow + q;
-    pml = p.pp_ml + at * 2;
-    po = p.pp_o + at * D;
+  // the row's partials: np of its prefix block, ns pieces, then those of the
+  // CTAs whose own run meets its segment
+  const int np = tp > 0 ? ns : 0;
+  const int rb = s.nmb > 1 ? b * s.nmb + m / s.np : b / s.nb;
+  const int q = s.nmb > 1 ? m % s.np : b % s.nb * g.M + m;
+  const size_t p_at = ((size_t)h * ns * s.nrb + rb) * s.prow + q, p_step = (size_t)s.nrb * s.prow;
+  const int in = h * s.nomb + m / kOwnRows, nt = own_tiles(g, len), hn = g.Hkv * s.nomb;
+  const int u0 = off * hn + in * nt, u1 = u0 + nt;
+  const size_t o_at = (size_t)(b * hn + in) * s.orow + m % kOwnRows;
+  if (threadIdx.x < 32) {
+    int no = 0;
+    start[kSMs / 32 + 1] = INT32_MAX;
+#pragma unroll
+    for (int i = 0; i <= kSMs / 32; ++i) {
+      // lane 31's next start is lane 0's of the next group
+      int next = __shfl_down_sync(0xffffffffu, start[i], 1);
+      const int wrap = __shfl_sync(0xffffffffu, start[i + 1], 0);
+      if (lane == 31) next = wrap;
+      const bool hit = 32 * i + lane < kSMs && max(start[i], u0) < min(next, u1);
+      const unsigned bits = __ballot_sync(0xffffffffu, hit);
+      if (hit) owner[no + __popc(bits & ((1u << lane) - 1))] = 32 * i + lane;
+      no += __popc(bits);
+    }
+    if (lane == 0) n_own = no;
   }
-  if (nt > 0) {
-    const int in = h * s.nomb + m / kOwnRows;
-    const int u = g.Hkv * s.nrb * tp + p.plan[kPlanInts + b] * hn + in * nt;
-    const int c0 = cta_of(u);
-    no = cta_of(u + nt - 1) - c0 + 1;
-    const size_t at = (size_t)(c0 + b * hn + in) * s.orow + m % kOwnRows;
-    oml = p.po_ml + at * 2;
-    oo = p.po_o + at * D;
-  }
-  const int n = np + no;
-  auto ml_of = [&](int i) {
-    return *reinterpret_cast<const float2*>(i < np ? pml + (size_t)i * s.prow * 2 : oml + (size_t)(i - np) * s.orow * 2);
+  __syncthreads();
+  const int n = np + n_own;
+  auto row_of = [&](int i) {  // partial i: its row among the prefix's or the own partials
+    return i < np ? p_at + i * p_step : o_at + (size_t)owner[i - np] * s.orow;
   };
+  const int d = threadIdx.x * VEC;
+  auto load = [&](int i, float (&v)[VEC]) {
+    const float* src = (i < np ? p.pp_o : p.po_o) + row_of(i) * D + d;
+    if constexpr (VEC == 4) {
+      const float4 u = *reinterpret_cast<const float4*>(src);
+      v[0] = u.x;
+      v[1] = u.y;
+      v[2] = u.z;
+      v[3] = u.w;
+    } else {
+      const float2 u = *reinterpret_cast<const float2*>(src);
+      v[0] = u.x;
+      v[1] = u.y;
+    }
+  };
+  float ahead[AHEAD][VEC];  // the first partials' loads are under way while the weights form
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) ahead[i][e] = 0.f;
+    if (i < n) load(i, ahead[i]);
+  }
   if (threadIdx.x < 32) {
     float mx = -INFINITY;
-    for (int i = threadIdx.x; i < n; i += 32) mx = fmaxf(mx, ml_of(i).x);
+#pragma unroll 1
+    for (int i = lane; i < n; i += 32) {
+      const float2 v = *reinterpret_cast<const float2*>((i < np ? p.pp_ml : p.po_ml) + row_of(i) * 2);
+      wts[i] = v.x;
+      mx = fmaxf(mx, v.x);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     float l = 0.f;
-    for (int i = threadIdx.x; i < n; i += 32) {
-      const float2 v = ml_of(i);
+#pragma unroll 1
+    for (int i = lane; i < n; i += 32) {
+      const float m2 = wts[i], li = (i < np ? p.pp_ml : p.po_ml)[row_of(i) * 2 + 1];
       // a part without a visible key adds nothing (its l is 0; NaN scores leave
       // no maximum either, and a NaN l)
-      const float w = v.x == -INFINITY ? 0.f : exp2f(v.x - mx);
+      const float w = m2 == -INFINITY ? 0.f : exp2f(m2 - mx);
       wts[i] = w;
-      l += v.x == -INFINITY ? v.y : w * v.y;
+      l += m2 == -INFINITY ? li : w * li;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if (threadIdx.x == 0) {
+    if (lane == 0) {
       stat[0] = mx;
       stat[1] = l;
     }
@@ -884,26 +1046,18 @@ __global__ void __launch_bounds__(MergeCfg<D>::THREADS) shared_merge_kernel(cons
   float acc[VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
-  const int d = threadIdx.x * VEC;
-  auto add = [&](const float* src, int cnt, int stride, const float* wt) {
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i)
+    if (i < n)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) acc[e] = fmaf(wts[i], ahead[i][e], acc[e]);
 #pragma unroll 4
-    for (int i = 0; i < cnt; ++i) {
-      const float w = wt[i];
-      if constexpr (VEC == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(src + (size_t)i * stride * D + d);
-        acc[0] = fmaf(w, v.x, acc[0]);
-        acc[1] = fmaf(w, v.y, acc[1]);
-        acc[2] = fmaf(w, v.z, acc[2]);
-        acc[3] = fmaf(w, v.w, acc[3]);
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(src + (size_t)i * stride * D + d);
-        acc[0] = fmaf(w, v.x, acc[0]);
-        acc[1] = fmaf(w, v.y, acc[1]);
-      }
-    }
-  };
-  add(po, np, s.prow, wts);
-  add(oo, no, s.orow, wts + np);
+  for (int i = AHEAD; i < n; ++i) {
+    float v[VEC];
+    load(i, v);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) acc[e] = fmaf(wts[i], v[e], acc[e]);
+  }
   uint16_t* dst = p.o + (size_t)row * D + d;
 #pragma unroll
   for (int e = 0; e < VEC; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
@@ -916,10 +1070,11 @@ struct SharedWs {
 SharedWs shared_ws(const SharedGeom& g) {
   const SharedSplit s = shared_split(g);
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  const size_t ps = (size_t)(kSMs + (long long)g.Hkv * s.nrb) * s.prow, os = (size_t)(kSMs + (long long)g.B * g.Hkv * s.nomb) * s.orow;
+  const long long nseg = (long long)g.Hkv * s.nrb;
+  const size_t ps = (size_t)(nseg > kPieces ? nseg : kPieces) * s.prow, os = (size_t)(kSMs + (long long)g.B * g.Hkv * s.nomb) * s.orow;
   SharedWs w;
   w.plan = 0;
-  w.pp_ml = w.plan + up(((size_t)g.B + kPlanInts) * 4);
+  w.pp_ml = w.plan + up(((size_t)g.B + kPlanOff) * 4);
   w.pp_o = w.pp_ml + (g.P > 0 ? up(ps * 8) : 0);
   w.po_ml = w.pp_o + (g.P > 0 ? up(ps * g.D * 4) : 0);
   w.po_o = w.po_ml + up(os * 8);
@@ -929,18 +1084,19 @@ SharedWs shared_ws(const SharedGeom& g) {
 
 template <int D, int NP>
 cudaError_t shared_d(const SharedGeom& g, const SharedArgs& a, void* ws, int* status, cudaStream_t st) {
-  using C = ShCfg<D, NP>;
+  using K = ShKernel<D, NP>;
+  constexpr int CPS = K::A::CPS;
   const SharedSplit s = shared_split(g);
   CUtensorMap tqp, tqo, tkp, tvp, tko, tvo;
   cudaError_t e;
   if ((e = make_tmap_rows_5d(&tqp, a.q, D, g.M, g.Hkv, g.B, s.mb, s.nb)) != cudaSuccess) return e;
-  if ((e = make_tmap_f16_chunks(&tqo, a.q, D, g.M, g.B * g.Hkv, kOwnRows, C::NCH)) != cudaSuccess) return e;
-  if ((e = make_tmap_f16_chunks(&tko, a.ko, D, g.own_rows, g.B * g.Hkv, T, C::CPS)) != cudaSuccess) return e;
-  if ((e = make_tmap_f16_chunks(&tvo, a.vo, D, g.own_rows, g.B * g.Hkv, T, C::CPS)) != cudaSuccess) return e;
+  if ((e = make_tmap_f16_chunks(&tqo, a.q, D, g.M, g.B * g.Hkv, kOwnRows, D / 64)) != cudaSuccess) return e;
+  if ((e = make_tmap_f16_chunks(&tko, a.ko, D, g.own_rows, g.B * g.Hkv, T, CPS)) != cudaSuccess) return e;
+  if ((e = make_tmap_f16_chunks(&tvo, a.vo, D, g.own_rows, g.B * g.Hkv, T, CPS)) != cudaSuccess) return e;
   if (g.P > 0) {
     // rows at or beyond the prefix's length read as zero
-    if ((e = make_tmap_f16_chunks(&tkp, a.kp, D, g.P, g.Hkv, T, C::CPS, g.prefix_rows)) != cudaSuccess) return e;
-    if ((e = make_tmap_f16_chunks(&tvp, a.vp, D, g.P, g.Hkv, T, C::CPS, g.prefix_rows)) != cudaSuccess) return e;
+    if ((e = make_tmap_f16_chunks(&tkp, a.kp, D, g.P, g.Hkv, T, CPS, g.prefix_rows)) != cudaSuccess) return e;
+    if ((e = make_tmap_f16_chunks(&tvp, a.vp, D, g.P, g.Hkv, T, CPS, g.prefix_rows)) != cudaSuccess) return e;
   } else {
     tkp = tko;  // not used: the prefix has no tiles
     tvp = tvo;
@@ -961,9 +1117,9 @@ cudaError_t shared_d(const SharedGeom& g, const SharedArgs& a, void* ws, int* st
   p.po_o = reinterpret_cast<float*>(wb + w.po_o);
   p.status = status;
   auto kern = shared_kernel<D, NP>;
-  if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM)) != cudaSuccess)
+  if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::SMEM)) != cudaSuccess)
     return e;
-  kern<<<kSMs, kThr, C::SMEM, st>>>(tqp, tqo, tkp, tvp, tko, tvo, p);
+  kern<<<kSMs, K::THREADS, K::SMEM, st>>>(tqp, tqo, tkp, tvp, tko, tvo, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // the merge, launched as a programmatic dependent: its blocks are placed
   // while the main grid runs and start when that has completed
@@ -981,14 +1137,22 @@ cudaError_t shared_d(const SharedGeom& g, const SharedArgs& a, void* ws, int* st
 
 template <int D>
 cudaError_t shared_np(const SharedGeom& g, const SharedArgs& a, void* ws, int* status, cudaStream_t st) {
-  return shared_split(g).np == 16 ? shared_d<D, 16>(g, a, ws, status, st) : shared_d<D, 64>(g, a, ws, status, st);
+  switch (shared_split(g).np) {
+    case 16: return shared_d<D, 16>(g, a, ws, status, st);
+    case 64: return shared_d<D, 64>(g, a, ws, status, st);
+    default:
+      if constexpr (D <= 256) return shared_d<D, 128>(g, a, ws, status, st);
+      else return cudaErrorInvalidValue;
+  }
 }
 
 }  // namespace
 
 SharedSplit shared_split(const SharedGeom& g) {
   SharedSplit s;
-  s.np = (long long)g.B * g.M <= 16 ? 16 : 64;
+  // (at D = 512 the accumulators of 128 rows would not fit beside the scores)
+  const long long r = (long long)g.B * g.M;
+  s.np = r <= 16 ? 16 : (r <= 64 || g.D == 512 ? 64 : 128);
   s.mb = g.M < s.np ? g.M : s.np;
   s.nmb = (g.M + s.np - 1) / s.np;
   s.nb = g.M <= s.np ? s.np / g.M : 1;
@@ -1004,7 +1168,7 @@ bool shared_fits(const SharedGeom& g) {
   const SharedSplit s = shared_split(g);
   const double tp = (g.P + T - 1) / T, to = (g.own_rows + T - 1) / T;
   const double units = (double)g.Hkv * s.nrb * tp + (double)g.B * g.Hkv * s.nomb * to;
-  return units < 1.0e9 && (double)g.B * g.Hkv * g.M < 1.0e9 && (double)g.B * g.Hkv * s.nomb < 1.0e9;
+  return units + kPieces < 1.0e9 && (double)g.B * g.Hkv * g.M < 1.0e9 && (double)g.B * g.Hkv * s.nomb < 1.0e9;
 }
 
 size_t shared_workspace_bytes(const SharedGeom& g) { return shared_ws(g).total; }

@@ -356,7 +356,7 @@ struct SharedGeom {
 // How the query rows are blocked.  Prefix blocks: rows of nb whole requests
 // (nmb == 1), or one of nmb blocks of a request's rows; own blocks of 16 rows.
 struct SharedSplit {
-  int np;          // rows a prefix block may have (the kernel's N): 16 or 64
+  int np;          // rows a prefix block may have (the kernel's N): 16, 64 or 128
   int mb, nb;      // rows of one request in a block, requests in a block
   int nmb, nrb;    // blocks of a request's rows, prefix blocks of a kv head
   int nomb;        // own row blocks of a request and kv head
