@@ -54,7 +54,11 @@ constexpr int kPieces = 2 * kSMs;  // prefix pieces (or as many as there are seg
 constexpr int kSmemMax = 232448;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRescaleLog2 = 8.0f;
+// P, its sums and O are bf16 and fp32, whose exponents reach 2^127: a row's
+// reference maximum (that of its first tile with a visible key) only moves
+// when a score outgrows it by more than 2^32, which leaves 2^63 for the sum
+// over 2^31 keys and loses no bit, since their precision is relative.
+constexpr float kGrowLog2 = 32.0f;
 // plan words: {prefix tiles, splits of the prefix, -, -}, each CTA's first own
 // unit (and their number), then each request's first own tile
 constexpr int kPlanStart = 4, kPlanOff = kPlanStart + kSMs + 1;
@@ -158,21 +162,26 @@ struct ShCfg {
   static constexpr int CPS = NCH < 2 ? NCH : 2;  // chunks per ring slot
   static constexpr int SPT = NCH / CPS;          // slots per tile and tensor
   static constexpr int NDC = (D + 127) / 128;    // 128-column blocks of O^T
-  static constexpr int GROUPS = N > 64 ? N / 64 : 1;  // softmax warpgroups, 64 rows each
-  static constexpr int NG = N / GROUPS;               // rows of one
+  static constexpr int NG = N > 16 ? 32 : 16;    // rows of a softmax warpgroup
+  static constexpr int GROUPS = N / NG;
   static constexpr int SLOT = CPS * T * 128;
   static constexpr int QB = N * D * 2;           // one block of queries
   static constexpr int QD = OWN ? 2 : 1;         // blocks buffered (own segments are short)
   static constexpr int PB = N * T * 2;           // P^T
   // per warpgroup: [2][4][NG] exchanged maxima / sums, thresholds, references,
-  // rescale factors, row ranges, bounds and growth tags
+  // rescale factors, row ranges, bounds and tags
   static constexpr int SMALL = 2 * 4 * NG * 4 + 3 * NG * 4 + NG * 8 + 64;
   // at head dim 64 the second product's 128 rows read one chunk past a slot
   // (rows 64-127 of O^T, never used): the last slot's must stay in bounds
   static constexpr int TAIL = D == 64 ? T * 128 : 0;
   static constexpr int FIXED = QB * QD + PB + GROUPS * SMALL + TAIL;
   static constexpr int FIT = (kSmemMax - 1024 - 1024 - FIXED) / SLOT;
-  static constexpr int NSLOT = FIT > 8 ? 8 : FIT;
+  // own caches stream from HBM on every SM: 128 KB in flight on each saturate
+  // it, and more only lengthen the queues (4 slots of 32 KB against 6: 54.4 and
+  // 55.8 us at 32 caches of up to 1,024 keys, D = 256; 3 slots: 56.0, and at
+  // D = 512, where a tile has 8, 140 us against 118)
+  static constexpr int MOST = OWN && CPS == 2 ? 4 : 8;
+  static constexpr int NSLOT = FIT > MOST ? MOST : FIT;
   static constexpr int OFF_Q = NSLOT * SLOT;
   static constexpr int OFF_P = OFF_Q + QD * QB;
   static constexpr int OFF_SMALL = OFF_P + PB;
@@ -182,9 +191,9 @@ struct ShCfg {
                        BND = RNG + NG * 8;
   static constexpr uint32_t S_COL = 0, O_COL = 2 * N;  // TMEM columns
   static constexpr uint32_t COLS = O_COL + NDC * N;
-  static_assert(NSLOT >= 2, "shared memory");
+  static_assert(NSLOT >= 2 && NSLOT <= 8, "ring slots (the barriers hold 8)");
   static_assert(COLS <= 512, "TMEM columns");
-  static_assert(NG == 16 || NG == 64, "rows of a warpgroup");
+  static_assert(GROUPS <= 4, "softmax warpgroups");
 };
 template <int D, int NP>
 struct ShKernel {
@@ -245,20 +254,20 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
 
 // A phase's barriers (its own, so that none has to be set up twice).
 struct Bars {
-  uint64_t *slot_full, *slot_empty;  // [8]
-  uint64_t *q_full, *q_empty;        // [2] a visit's queries
-  uint64_t *s_full;                  // [2] S^T(n) in TMEM
-  uint64_t *p_full;                  // [1] P^T(n) written (and O^T rescaled)
-  uint64_t *o_done;                  // [1] PV(n) finished
-  uint64_t *xch;                     // [2] a softmax warpgroup's exchanges
-  uint64_t *drain;                   // [1]
-  __device__ __forceinline__ explicit Bars(uint64_t* b)
-      : slot_full(b), slot_empty(b + 8), q_full(b + 16), q_empty(b + 18), s_full(b + 20), p_full(b + 22),
-        o_done(b + 23), xch(b + 24), drain(b + 26) {}
-  static constexpr int kCount = 27;
+  uint64_t* b;
+  __device__ __forceinline__ uint64_t* slot_full(int i) const { return b + i; }        // [8]
+  __device__ __forceinline__ uint64_t* slot_empty(int i) const { return b + 8 + i; }   // [8]
+  __device__ __forceinline__ uint64_t* q_full(int i) const { return b + 16 + i; }      // [2] a visit's queries
+  __device__ __forceinline__ uint64_t* q_empty(int i) const { return b + 18 + i; }     // [2]
+  __device__ __forceinline__ uint64_t* s_full(int i) const { return b + 20 + i; }      // [2] S^T(n) in TMEM
+  __device__ __forceinline__ uint64_t* p_full() const { return b + 22; }  // P^T(n) written (and O^T rescaled)
+  __device__ __forceinline__ uint64_t* o_done() const { return b + 23; }  // PV(n) finished
+  __device__ __forceinline__ uint64_t* drain() const { return b + 24; }
+  __device__ __forceinline__ uint64_t* xch(int i) const { return b + 25 + i; }  // [4] a softmax warpgroup's exchanges
+  static constexpr int kCount = 29;
   // arrivals that complete a phase of barrier i
   static __device__ __forceinline__ int arrivals(int i, int groups) {
-    return i == 22 ? 4 * groups : (i == 24 || i == 25 ? 4 : 1);
+    return i == 22 ? 4 * groups : (i >= 25 ? 4 : 1);
   }
 };
 
@@ -278,17 +287,16 @@ struct SoftCtx {
 // written to shared memory before is visible after.
 __device__ __forceinline__ bool exchange(SoftCtx& c) {
   __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(c.bar.xch + c.group);
-  const bool ok = wait(c.bar.xch + c.group, c.xc & 1, c.abort);
+  if ((threadIdx.x & 31) == 0) mbar_arrive(c.bar.xch(c.group));
+  const bool ok = wait(c.bar.xch(c.group), c.xc & 1, c.abort);
   ++c.xc;
   return __all_sync(0xffffffffu, ok);
 }
 
-// One visit of a segment: its tiles' softmax, then the partial result.
-// 16 rows: every thread keeps all rows' running maxima in registers, and each
-// tile exchanges its column maxima.  64 rows a warpgroup: the maxima live in
-// shared memory, and a tile exchanges only whether any score outgrew its row's
-// reference by more than 2^kRescaleLog2 (rare after a visit's first tiles).
+// One visit of a segment: its tiles' softmax, then the partial result.  The
+// rows' reference maxima live in shared memory; a tile only exchanges whether
+// any score outgrew its row's threshold, which after a visit's first tile is
+// rare (it also happens when a window first lets a row see a key).
 template <int D, int N, bool OWN, typename Walk>
 __device__ bool softmax_visit(const SharedParams& p, Walk& w, SoftCtx& c) {
   using C = ShCfg<D, N, OWN>;
@@ -303,7 +311,8 @@ __device__ bool softmax_visit(const SharedParams& p, Walk& w, SoftCtx& c) {
   float* alp = reinterpret_cast<float*>(c.small + C::ALPHA);
   int2* rng = reinterpret_cast<int2*>(c.small + C::RNG);
   int* bnd = reinterpret_cast<int*>(c.small + C::BND);
-  volatile int* grow_tag = bnd + 8;
+  volatile int* grow_tag = bnd + 8;   // [2] tile (plus one) at which some score outgrew its threshold
+  volatile int* scale_tag = bnd + 10;  // [1] tile (plus one) at which some row with earlier keys did
   const int blk = w.blk, slot = w.slot;
 
   // visible keys of row t (own cache: own indices), and bounds over all rows
@@ -343,11 +352,9 @@ __device__ bool softmax_visit(const SharedParams& p, Walk& w, SoftCtx& c) {
   const int lo_all = max(max(bnd[0], bnd[2]), max(bnd[4], bnd[6]));
   const int hi_all = min(min(bnd[1], bnd[3]), min(bnd[5], bnd[7]));
 
-  float l_part[NG], m_run[NG == 16 ? 16 : 1];  // 64 rows: thread t holds row t's reference maximum
+  float l_part[NG], m_row = -INFINITY;  // thread t < NG holds row t's reference
 #pragma unroll
   for (int q = 0; q < NG; ++q) l_part[q] = 0.f;
-#pragma unroll
-  for (int q = 0; q < (NG == 16 ? 16 : 1); ++q) m_run[q] = -INFINITY;
 
   bool more = true;
 #pragma unroll 1
@@ -355,133 +362,64 @@ __device__ bool softmax_visit(const SharedParams& p, Walk& w, SoftCtx& c) {
     const int n = c.n, key0 = w.key0();
     const bool first = w.first;
     more = !w.last();
-    if (!__all_sync(0xffffffffu, wait(c.bar.s_full + (n & 1), (n >> 1) & 1, c.abort))) return false;
+    if (!__all_sync(0xffffffffu, wait(c.bar.s_full(n & 1), (n >> 1) & 1, c.abort))) return false;
     tc_fence_after();
-    const uint32_t s_at = c.tmem + lane_off + C::S_COL + N * (n & 1) + col0;
-    const bool all = key0 >= lo_all && key0 + T - 1 <= hi_all;  // no row masks a key of this tile
-    const int key = key0 + t;
-    // 16 rows' scores, in log2 units; masked ones are -inf
-    auto scores = [&](int q0, float (&x)[16]) {
-      uint32_t sr[16];
-      tmem_ld16(s_at + q0, sr);
-      tmem_wait_ld();
+    uint32_t sr[NG];
+    if constexpr (NG == 16) tmem_ld16(c.tmem + lane_off + C::S_COL + N * (n & 1) + col0, sr);
+    else tmem_ld32(c.tmem + lane_off + C::S_COL + N * (n & 1) + col0, sr);
+    tmem_wait_ld();
+    float x[NG];
 #pragma unroll
-      for (int q = 0; q < 16; ++q) x[q] = __uint_as_float(sr[q]) * sl2;
-      if (!all) {
+    for (int q = 0; q < NG; ++q) x[q] = __uint_as_float(sr[q]) * sl2;
+    if (!(key0 >= lo_all && key0 + T - 1 <= hi_all)) {
+      const int key = key0 + t;
 #pragma unroll
-        for (int q = 0; q < 16; ++q) {
-          const int2 r = rng[q0 + q];
-          if (key < r.x || key > r.y) x[q] = -INFINITY;
-        }
-      }
-    };
-    // O^T's columns of 16 rows times their factors
-    auto rescale = [&](int q0, const float (&f)[16]) {
-#pragma unroll 1
-      for (int h = 0; h < NDC; ++h) {
-        const uint32_t o_at = c.tmem + lane_off + C::O_COL + N * h + col0 + q0;
-        uint32_t ov[16];
-        tmem_ld16(o_at, ov);
-        tmem_wait_ld();
-#pragma unroll
-        for (int q = 0; q < 16; ++q) ov[q] = __float_as_uint(__uint_as_float(ov[q]) * f[q]);
-        tmem_st16(o_at, ov);
-      }
-    };
-    uint32_t pk[NG / 2];  // P, two rows a word
-    bool grow = false;
-    float x[NG == 16 ? 16 : 1], alpha[NG == 16 ? 16 : 1];
-    if constexpr (NG == 16) {
-      float mx[16];
-      scores(0, x);
-#pragma unroll
-      for (int q = 0; q < 16; ++q) mx[q] = x[q];
-      column_reduce<16, true>(mx, lane);
-      float* rb = red + (c.xc & 1) * 4 * NG;
-      column_post<16>(mx, rb + q4 * NG, lane);
-      if (!exchange(c)) return false;
-#pragma unroll
-      for (int q = 0; q < 16; q += 4) {
-        float4 v = *reinterpret_cast<const float4*>(rb + q);
-#pragma unroll
-        for (int i = 1; i < 4; ++i) {
-          const float4 u = *reinterpret_cast<const float4*>(rb + i * NG + q);
-          v = make_float4(fmaxf(v.x, u.x), fmaxf(v.y, u.y), fmaxf(v.z, u.z), fmaxf(v.w, u.w));
-        }
-        const float tm[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          alpha[q + e] = 1.f;
-          if (tm[e] > m_run[q + e] + kRescaleLog2) {  // the reference maximum moves (lazily)
-            if (m_run[q + e] != -INFINITY) {
-              alpha[q + e] = fast_exp2(m_run[q + e] - tm[e]);
-              grow = true;
-            }
-            m_run[q + e] = tm[e];
-          }
-        }
-      }
-    } else {
-      grow = first;
-      if (!first) {
-        bool over = false;
-#pragma unroll 1
-        for (int q0 = 0; q0 < NG; q0 += 16) {
-          float y[16];
-          scores(q0, y);
-#pragma unroll
-          for (int q = 0; q < 16; q += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(thr + q0 + q);
-            over |= y[q] > v.x || y[q + 1] > v.y || y[q + 2] > v.z || y[q + 3] > v.w;
-          }
-        }
-        if (__any_sync(0xffffffffu, over) && lane == 0) grow_tag[n & 1] = n + 1;
-        if (!exchange(c)) return false;
-        grow = grow_tag[n & 1] == n + 1;
-      }
-      if (grow) {
-        float* rb = red + (c.xc & 1) * 4 * NG;
-#pragma unroll 1
-        for (int q0 = 0; q0 < NG; q0 += 16) {
-          float y[16];
-          scores(q0, y);
-          column_reduce<16, true>(y, lane);
-          column_post<16>(y, rb + q4 * NG + q0, lane);
-        }
-        if (!exchange(c)) return false;
-        if (t < NG) {
-          const float tm = fmaxf(fmaxf(rb[t], rb[NG + t]), fmaxf(rb[2 * NG + t], rb[3 * NG + t]));
-          float a = 1.f;
-          if (tm > m_run[0] + kRescaleLog2) {
-            if (m_run[0] != -INFINITY) a = fast_exp2(m_run[0] - tm);
-            m_run[0] = tm;
-            use[t] = tm;
-            thr[t] = tm + kRescaleLog2;
-          } else if (first) {
-            use[t] = 0.f;  // no visible key yet
-          }
-          alp[t] = a;
-        }
-        if (!exchange(c)) return false;
-        grow = !first;
+      for (int q = 0; q < NG; ++q) {
+        const int2 r = rng[q];
+        if (key < r.x || key > r.y) x[q] = -INFINITY;
       }
     }
-    // P = 2^(score - reference), and the row sums
-    if constexpr (NG == 16) {
-      if (grow) {
+    bool grow = first, scale = false;
+    if (!first) {
+      bool over = false;
 #pragma unroll
-        for (int q = 0; q < 16; ++q) l_part[q] *= alpha[q];
+      for (int q = 0; q < NG; q += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(thr + q);
+        over |= x[q] > v.x || x[q + 1] > v.y || x[q + 2] > v.z || x[q + 3] > v.w;
       }
+      if (__any_sync(0xffffffffu, over) && lane == 0) grow_tag[n & 1] = n + 1;
+      if (!exchange(c)) return false;
+      grow = grow_tag[n & 1] == n + 1;
+    }
+    if (grow) {
+      float* rb = red + (c.xc & 1) * 4 * NG;
+      {
+        float mx[NG];
 #pragma unroll
-      for (int q = 0; q < 16; q += 2) {
-        const float e0 = fast_exp2(x[q] - (m_run[q] == -INFINITY ? 0.f : m_run[q]));
-        const float e1 = fast_exp2(x[q + 1] - (m_run[q + 1] == -INFINITY ? 0.f : m_run[q + 1]));
-        l_part[q] += e0;
-        l_part[q + 1] += e1;
-        pk[q / 2] = pack_bf16(e0, e1);
+        for (int q = 0; q < NG; ++q) mx[q] = x[q];
+        column_reduce<NG, true>(mx, lane);
+        column_post<NG>(mx, rb + q4 * NG, lane);
       }
-    } else {
-      if (grow) {
+      if (!exchange(c)) return false;
+      if (t < NG) {
+        const float tm = fmaxf(fmaxf(rb[t], rb[NG + t]), fmaxf(rb[2 * NG + t], rb[3 * NG + t]));
+        float a = 1.f;
+        if (tm > (m_row == -INFINITY ? m_row : m_row + kGrowLog2)) {
+          if (m_row != -INFINITY) {
+            a = fast_exp2(m_row - tm);
+            *scale_tag = n + 1;
+          }
+          m_row = tm;
+          use[t] = tm;
+          thr[t] = tm + kGrowLog2;
+        } else if (first) {
+          use[t] = 0.f;  // no visible key yet
+        }
+        alp[t] = a;
+      }
+      if (!exchange(c)) return false;
+      scale = *scale_tag == n + 1;
+      if (scale) {
 #pragma unroll
         for (int q = 0; q < NG; q += 4) {
           const float4 v = *reinterpret_cast<const float4*>(alp + q);
@@ -491,38 +429,35 @@ __device__ bool softmax_visit(const SharedParams& p, Walk& w, SoftCtx& c) {
           l_part[q + 3] *= v.w;
         }
       }
+    }
+    // P = 2^(score - reference), two rows a word, and the row sums
+    uint32_t pk[NG / 2];
 #pragma unroll
-      for (int q0 = 0; q0 < NG; q0 += 16) {
-        float y[16];
-        scores(q0, y);
-#pragma unroll
-        for (int q = 0; q < 16; q += 4) {
-          const float4 v = *reinterpret_cast<const float4*>(use + q0 + q);
-          const float e0 = fast_exp2(y[q] - v.x), e1 = fast_exp2(y[q + 1] - v.y);
-          const float e2 = fast_exp2(y[q + 2] - v.z), e3 = fast_exp2(y[q + 3] - v.w);
-          l_part[q0 + q] += e0;
-          l_part[q0 + q + 1] += e1;
-          l_part[q0 + q + 2] += e2;
-          l_part[q0 + q + 3] += e3;
-          pk[(q0 + q) / 2] = pack_bf16(e0, e1);
-          pk[(q0 + q) / 2 + 1] = pack_bf16(e2, e3);
-        }
-      }
+    for (int q = 0; q < NG; q += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(use + q);
+      const float e0 = fast_exp2(x[q] - v.x), e1 = fast_exp2(x[q + 1] - v.y);
+      const float e2 = fast_exp2(x[q + 2] - v.z), e3 = fast_exp2(x[q + 3] - v.w);
+      l_part[q] += e0;
+      l_part[q + 1] += e1;
+      l_part[q + 2] += e2;
+      l_part[q + 3] += e3;
+      pk[q / 2] = pack_bf16(e0, e1);
+      pk[q / 2 + 1] = pack_bf16(e2, e3);
     }
     // PV(n - 1) has finished with P^T's buffer, and with O^T before it is rescaled
-    if (n > 0 && !__all_sync(0xffffffffu, wait(c.bar.o_done, (n - 1) & 1, c.abort))) return false;
-    if (grow) {  // uniform over the warpgroup
+    if (n > 0 && !__all_sync(0xffffffffu, wait(c.bar.o_done(), (n - 1) & 1, c.abort))) return false;
+    if (scale) {  // uniform over the warpgroup
       tc_fence_after();
-      if constexpr (NG == 16) {
-        rescale(0, alpha);
-      } else {
 #pragma unroll 1
-        for (int q0 = 0; q0 < NG; q0 += 16) {
-          float f[16];
+      for (int i = 0; i < NDC * (NG / 16); ++i) {
+        const int q0 = NG == 16 ? 0 : 16 * (i & 1);
+        const uint32_t o_at = c.tmem + lane_off + C::O_COL + N * (NG == 16 ? i : i >> 1) + col0 + q0;
+        uint32_t ov[16];
+        tmem_ld16(o_at, ov);
+        tmem_wait_ld();
 #pragma unroll
-          for (int q = 0; q < 16; ++q) f[q] = alp[q0 + q];
-          rescale(q0, f);
-        }
+        for (int q = 0; q < 16; ++q) ov[q] = __float_as_uint(__uint_as_float(ov[q]) * alp[q0 + q]);
+        tmem_st16(o_at, ov);
       }
       tmem_wait_st();
     }
@@ -535,33 +470,28 @@ __device__ bool softmax_visit(const SharedParams& p, Walk& w, SoftCtx& c) {
       for (int q = 0; q < 16; ++q)
         *reinterpret_cast<uint16_t*>(pb + q * 128 + ((kc ^ (q & 7)) << 4)) = (uint16_t)(pk[q / 2] >> (16 * (q & 1)));
     } else {
-      // MN-major B operand: key t's 64 rows of this group are one 128-byte swizzled line
-      pb += c.group * T * 128 + t * 128;
+      // MN-major B operand: a key's 64 rows (two groups') are one 128-byte swizzled line
+      pb += (c.group >> 1) * T * 128 + t * 128;
+      const int u0 = 4 * (c.group & 1);
 #pragma unroll
-      for (int u = 0; u < 8; ++u)
-        *reinterpret_cast<uint4*>(pb + ((u ^ (t & 7)) << 4)) =
+      for (int u = 0; u < 4; ++u)
+        *reinterpret_cast<uint4*>(pb + (((u0 + u) ^ (t & 7)) << 4)) =
             make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
     }
     fence_proxy_async_smem();  // generic writes -> the tensor core's reads
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(c.bar.p_full);
+    if (lane == 0) mbar_arrive(c.bar.p_full());
     ++c.n;
     w.next();
   }
 
   // the visit's partial: row sums over the 128 threads, then O^T
   float* rb = red + (c.xc & 1) * 4 * NG;
-#pragma unroll
-  for (int q0 = 0; q0 < NG; q0 += 16) {
-    float v[16];
-#pragma unroll
-    for (int q = 0; q < 16; ++q) v[q] = l_part[q0 + q];
-    column_reduce<16, false>(v, lane);
-    column_post<16>(v, rb + q4 * NG + q0, lane);
-  }
+  column_reduce<NG, false>(l_part, lane);
+  column_post<NG>(l_part, rb + q4 * NG, lane);
   if (!exchange(c)) return false;
-  if (!__all_sync(0xffffffffu, wait(c.bar.o_done, (c.n - 1) & 1, c.abort))) return false;
+  if (!__all_sync(0xffffffffu, wait(c.bar.o_done(), (c.n - 1) & 1, c.abort))) return false;
   tc_fence_after();
   const int stride = OWN ? p.s.orow : p.s.prow;  // rows of a slot
   int rows;                                      // of which this segment has, and this group from row NG * group on
@@ -572,15 +502,9 @@ __device__ bool softmax_visit(const SharedParams& p, Walk& w, SoftCtx& c) {
   const size_t at = (size_t)slot * stride + NG * c.group;
   float* out = (OWN ? p.po_o : p.pp_o) + at * D;
   float* ml = (OWN ? p.po_ml : p.pp_ml) + at * 2;
-  if (t < min(rows, NG)) {
-    float m = m_run[0];
-    if constexpr (NG == 16) {
-#pragma unroll
-      for (int q = 1; q < NG; ++q) m = t == q ? m_run[q] : m;
-    }
+  if (t < min(rows, NG))
     *reinterpret_cast<float2*>(ml + 2 * t) =
-        make_float2(m, (rb[t] + rb[NG + t]) + (rb[2 * NG + t] + rb[3 * NG + t]));
-  }
+        make_float2(m_row, (rb[t] + rb[NG + t]) + (rb[2 * NG + t] + rb[3 * NG + t]));
 #pragma unroll 1
   for (int h = 0; h < NDC; ++h) {
     float* dst = out + 128 * h + t;
@@ -608,7 +532,7 @@ __device__ void run_phase(const SharedParams& p, unsigned char* base, uint64_t* 
   using C = ShCfg<D, N, OWN>;
   constexpr int NCH = C::NCH, CPS = C::CPS, SPT = C::SPT, NSLOT = C::NSLOT, QD = C::QD;
   const SharedGeom& g = p.g;
-  const Bars bar(bar_mem);
+  const Bars bar{bar_mem};
   const int warp = threadIdx.x / 32;
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
@@ -622,9 +546,9 @@ __device__ void run_phase(const SharedParams& p, unsigned char* base, uint64_t* 
 #pragma unroll 1
         for (int sp = 0; sp < SPT; ++sp, ++issued) {
           const int s = issued % NSLOT;
-          if (issued >= NSLOT && !wait(bar.slot_empty + s, ((issued / NSLOT) & 1) ^ 1, abort_flag)) return false;
-          mbar_arrive_expect_tx(bar.slot_full + s, C::SLOT);
-          tma_load_4d(base + s * C::SLOT, m, bar.slot_full + s, 0, key0, sp * CPS, head);
+          if (issued >= NSLOT && !wait(bar.slot_empty(s), ((issued / NSLOT) & 1) ^ 1, abort_flag)) return false;
+          mbar_arrive_expect_tx(bar.slot_full(s), C::SLOT);
+          tma_load_4d(base + s * C::SLOT, m, bar.slot_full(s), 0, key0, sp * CPS, head);
         }
         w.next();
         return true;
@@ -632,16 +556,16 @@ __device__ void run_phase(const SharedParams& p, unsigned char* base, uint64_t* 
       auto load_k = [&]() -> bool {
         if (wk.first) {
           const int s = nq % QD;
-          if (nq >= QD && !wait(bar.q_empty + s, ((nq / QD) & 1) ^ 1, abort_flag)) return false;
+          if (nq >= QD && !wait(bar.q_empty(s), ((nq / QD) & 1) ^ 1, abort_flag)) return false;
           unsigned char* q = base + C::OFF_Q + s * C::QB;
           if constexpr (OWN) {
-            mbar_arrive_expect_tx(bar.q_full + s, C::QB);
-            tma_load_4d(q, tmQ, bar.q_full + s, 0, wk.blk * kOwnRows, 0, wk.b * g.Hkv + wk.h);
+            mbar_arrive_expect_tx(bar.q_full(s), C::QB);
+            tma_load_4d(q, tmQ, bar.q_full(s), 0, wk.blk * kOwnRows, 0, wk.b * g.Hkv + wk.h);
           } else {
-            mbar_arrive_expect_tx(bar.q_full + s, NCH * p.s.prow * 128);
+            mbar_arrive_expect_tx(bar.q_full(s), NCH * p.s.prow * 128);
 #pragma unroll 1
             for (int c = 0; c < NCH; ++c)
-              tma_load_5d(q + c * N * 128, tmQ, bar.q_full + s, 0, wk.blk % p.s.nmb * N, c, wk.h,
+              tma_load_5d(q + c * N * 128, tmQ, bar.q_full(s), 0, wk.blk % p.s.nmb * N, c, wk.h,
                           wk.blk / p.s.nmb * p.s.nb);
           }
           ++nq;
@@ -653,8 +577,8 @@ __device__ void run_phase(const SharedParams& p, unsigned char* base, uint64_t* 
 #pragma unroll 1
       for (int n = -2; ok && n < total; ++n) ok = (n < 0 || load_tile(wv, tmV)) && (n + 2 >= total || load_k());
       if (*abort_flag) {  // unwinding: the loads in flight land before shared memory is released
-        drain_ring(bar.q_full, QD, nq);
-        drain_ring(bar.slot_full, NSLOT, issued);
+        drain_ring(bar.q_full(0), QD, nq);
+        drain_ring(bar.slot_full(0), NSLOT, issued);
       }
     }
   } else if (warp == 1) {
@@ -666,12 +590,12 @@ __device__ void run_phase(const SharedParams& p, unsigned char* base, uint64_t* 
       int used = 0, nq = 0;
       auto issue_s = [&](int n) -> bool {  // S^T(n) into buffer n & 1
         const int qs = nq % QD;
-        if (ws.first && !wait(bar.q_full + qs, (nq / QD) & 1, abort_flag)) return false;
+        if (ws.first && !wait(bar.q_full(qs), (nq / QD) & 1, abort_flag)) return false;
         uint64_t qd = smem_desc_sw128(smem_u32(base + C::OFF_Q + qs * C::QB), 16, 1024);
 #pragma unroll 1
         for (int sp = 0; sp < SPT; ++sp, ++used) {
           const int s = used % NSLOT;
-          if (!wait(bar.slot_full + s, (used / NSLOT) & 1, abort_flag)) return false;
+          if (!wait(bar.slot_full(s), (used / NSLOT) & 1, abort_flag)) return false;
           tc_fence_after();
           uint64_t kd = smem_desc_sw128(smem_u32(base + s * C::SLOT), 16, 1024);
 #pragma unroll 1
@@ -683,11 +607,11 @@ __device__ void run_phase(const SharedParams& p, unsigned char* base, uint64_t* 
             kd = desc_add(kd, T * 128);
             qd = desc_add(qd, N * 128);
           }
-          mma_commit(bar.slot_empty + s);
+          mma_commit(bar.slot_empty(s));
         }
-        mma_commit(bar.s_full + (n & 1));
+        mma_commit(bar.s_full(n & 1));
         if (ws.last()) {  // the visit's queries are read
-          mma_commit(bar.q_empty + qs);
+          mma_commit(bar.q_empty(qs));
           ++nq;
         }
         ws.next();
@@ -698,14 +622,14 @@ __device__ void run_phase(const SharedParams& p, unsigned char* base, uint64_t* 
 #pragma unroll 1
       for (int n = -2; ok && n < total; ++n) {
         if (n >= 0) {
-          if (!wait(bar.p_full, n & 1, abort_flag)) break;
+          if (!wait(bar.p_full(), n & 1, abort_flag)) break;
           tc_fence_after();
           const uint32_t acc = wv.first ? 0u : 1u;
           // O^T block h (head-dim columns [128 h, 128 h + 128)) += V^T . P^T: one slot a block
 #pragma unroll 1
           for (int h = 0; h < SPT; ++h, ++used) {
             const int s = used % NSLOT;
-            if (!wait(bar.slot_full + s, (used / NSLOT) & 1, abort_flag)) { ok = false; break; }
+            if (!wait(bar.slot_full(s), (used / NSLOT) & 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
             const uint64_t vd = smem_desc_sw128(smem_u32(base + s * C::SLOT), T * 128, 1024);  // MN-major
 #pragma unroll
@@ -713,16 +637,16 @@ __device__ void run_phase(const SharedParams& p, unsigned char* base, uint64_t* 
               mma_ss(tmem + C::O_COL + N * h, desc_add(vd, ks * 2048),
                      N > 16 ? desc_add(pd, ks * 2048) : desc_add(pd, (ks >> 2) * kOwnRows * 128 + (ks & 3) * 32),
                      idPV, (acc || ks > 0) ? 1u : 0u);
-            mma_commit(bar.slot_empty + s);
+            mma_commit(bar.slot_empty(s));
           }
           if (!ok) break;
-          mma_commit(bar.o_done);
+          mma_commit(bar.o_done());
           wv.next();
         }
         if (n + 2 < total) ok = issue_s(n + 2);  // after PV(n): S buffer n & 1 is free
       }
-      mma_commit(bar.drain);
-      mbar_wait_drain(bar.drain, 0);
+      mma_commit(bar.drain());
+      mbar_wait_drain(bar.drain(), 0);
     }
   } else if ((warp - 2) / 4 < C::GROUPS) {
     // ------------------------------------------------------------ softmax
@@ -787,8 +711,8 @@ __global__ void __launch_bounds__(ShKernel<D, NP>::THREADS, 1)
   // rows of the prefix query block that no box fills stay zero
 #pragma unroll 1
   for (int i = threadIdx.x; i < A::QB / 16; i += THR) reinterpret_cast<uint4*>(base + A::OFF_Q)[i] = make_uint4(0, 0, 0, 0);
-  if (threadIdx.x < 2 * A::GROUPS)  // growth tags
-    reinterpret_cast<int*>(base + A::OFF_SMALL + (threadIdx.x >> 1) * A::SMALL + A::BND)[8 + (threadIdx.x & 1)] = 0;
+  if (threadIdx.x < 4 * A::GROUPS)  // tags of the prefix phase
+    reinterpret_cast<int*>(base + A::OFF_SMALL + (threadIdx.x >> 2) * A::SMALL + A::BND)[8 + (threadIdx.x & 3)] = 0;
   fence_proxy_async_smem();
   if (warp == 1) {
     tmem_alloc(tmem_slot, K::TCOLS);
@@ -904,6 +828,9 @@ __global__ void __launch_bounds__(ShKernel<D, NP>::THREADS, 1)
       __syncthreads();
       tc_fence_after();
     }
+    if (threadIdx.x < 4)  // tags of this phase
+      reinterpret_cast<int*>(base + K::B::OFF_SMALL + K::B::BND)[8 + threadIdx.x] = 0;
+    __syncthreads();
     if (!*abort_flag) {
       OwnWalk w;
       w.p = &p;
