@@ -410,8 +410,33 @@ def backward(q, k, v, o, lse, dO, window: int, scale: float, stream=None, causal
 # attention over a shared prefix and per-request caches; per-head norm and rotation
 #
 # A generation step calls these with tensors of a few KB, where the host's
-# time is what counts: the checks are one pass over (name, tensor, type,
-# shape), and workspace sizes are remembered by shape.
+# time is what counts: the calls that allocate their outputs go through
+# csrc/marshal.cpp, which returns None for anything unusual; the path below then
+# runs the call or says what is wrong with it.  Its checks are one pass over
+# (name, tensor, type, shape), and workspace sizes are remembered by shape.
+
+
+_fast = None  # csrc/marshal.cpp, once a call needs it
+
+
+def _marshal():
+    """The marshalling module, bound to the library that load() returned."""
+    global _fast
+    lib = load()
+    with _lock:
+        if _fast is None:
+            import torch  # noqa: F401  its libraries are the module's
+
+            try:
+                from . import _marshal as m
+            except ImportError as e:
+                raise RuntimeError("the binding's marshalling module is missing: build the CUDA library first "
+                                   "(python -c 'import __graft_entry__ as g; g.build()')") from e
+            m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+                lib.swa_attn_fwd_workspace_bytes_shared, lib.swa_attn_fwd_shared, lib.swa_attn_qk_rope_fwd,
+                lib.swa_attn_qk_rope_bwd_workspace_bytes, lib.swa_attn_qk_rope_bwd)))
+            _fast = m
+        return _fast
 
 
 def _check(device, specs):
@@ -485,6 +510,13 @@ def swa_attn_fwd_shared(q, k_prefix, v_prefix, k_own, v_own, own_len, sinks, o, 
 def forward_shared(q, k_prefix, v_prefix, k_own, v_own, own_len, window: int, scale: float, prefix_len=None,
                    sinks=None, stream=None):
     """Return (o bf16 [B,Hq,Lq,D], lse fp32 [B,Hq,Lq]) of swa_attn_fwd_shared."""
+    if stream is None:
+        r = (_fast or _marshal()).forward_shared(q, k_prefix, v_prefix, k_own, v_own, own_len, window, scale,
+                                                 prefix_len, sinks)
+        if r.__class__ is tuple:
+            return r
+        if r is not None:
+            raise SwaError(r, "swa_attn_fwd_shared")
     import torch
 
     dims = _check_shared(q, k_prefix, v_prefix, k_own, v_own, own_len, sinks)
@@ -551,6 +583,8 @@ def swa_attn_qk_rope_fwd(q, k, v, wq, wk, inv_freq, q_out, k_out, v_out, eps: fl
     Hq, q_tok = _token_rows("q", q, B, L, D, dev)
     outs = [("q_out", q_out, bf16, (B, Hq, L, D))]
     Hkv, k_tok, v_tok, rows = 1, 0, 0, L
+    if (k is not None and k_out is None) or (v is not None and v_out is None):
+        raise ValueError("k needs k_out and v needs v_out")
     if k is not None:
         Hkv, k_tok = _token_rows("k", k, B, L, D, dev)
         rows = k_out.shape[2]
@@ -568,8 +602,8 @@ def swa_attn_qk_rope_fwd(q, k, v, wq, wk, inv_freq, q_out, k_out, v_out, eps: fl
     rc = load().swa_attn_qk_rope_fwd(q.data_ptr(), _addr(k), _addr(v), q_tok, k_tok, v_tok, _addr(wq), _addr(wk),
                                      _addr(inv_freq), _addr(positions), _addr(kv_len), q_out.data_ptr(),
                                      None if k is None else k_out.data_ptr(), None if v is None else v_out.data_ptr(),
-                                     B, Hq, Hkv, L, D, rows, rot, 1 if interleaved else 0, pos0, eps, weight_offset,
-                                     _stream_ptr(stream))
+                                     B, Hq, Hkv, L, D, rows, rot, 1 if interleaved else 0, int(pos0), float(eps),
+                                     float(weight_offset), _stream_ptr(stream))
     if rc:
         raise SwaError(rc, "swa_attn_qk_rope_fwd")
 
@@ -579,6 +613,13 @@ def qk_rope(q, k, v, wq, wk, inv_freq, eps: float, positions=None, pos0: int = 0
     """Return (q [B,Hq,L,D], k [B,Hkv,L,D], v [B,Hkv,L,D]) for the attention
     from a projection's bf16 q, k, v [B,L,heads,D]: q and k normalised per
     head, scaled and rotated by position.  k and v may be None."""
+    if stream is None:
+        r = (_fast or _marshal()).qk_rope(q, k, v, wq, wk, inv_freq, None, None, None, eps, positions, pos0,
+                                          weight_offset, interleaved)
+        if r.__class__ is tuple:
+            return r
+        if r is not None:
+            raise SwaError(r, "swa_attn_qk_rope_fwd")
     import torch
 
     B, L, _, D = q.shape
@@ -595,6 +636,13 @@ def qk_rope_append(q, k, v, wq, wk, inv_freq, k_cache, v_cache, kv_len, eps: flo
     kv_len[b] - 1 of each request's cache [B,Hkv,kv_rows,D] (kv_len int32 [B]
     counts the step's tokens), which also give their positions, from pos0.
     Return q [B,Hq,L,D]."""
+    if stream is None:
+        r = (_fast or _marshal()).qk_rope(q, k, v, wq, wk, inv_freq, k_cache, v_cache, kv_len, eps, positions, pos0,
+                                          weight_offset, interleaved)
+        if r.__class__ is tuple:
+            return r[0]
+        if r is not None:
+            raise SwaError(r, "swa_attn_qk_rope_fwd")
     import torch
 
     B, L, Hq, D = q.shape
@@ -634,8 +682,8 @@ def _run_rope_bwd(dims, q, k, wq, wk, inv_freq, dq, dk, dv, outs, toks, dwq, dwk
     rc = load().swa_attn_qk_rope_bwd(q.data_ptr(), _addr(k), q_tok, k_tok, _addr(wq), _addr(wk), _addr(inv_freq),
                                      _addr(positions), dq.data_ptr(), None if k is None else dk.data_ptr(), _addr(dv),
                                      *outs, *toks, _addr(dwq), _addr(dwk), B, Hq, Hkv, L, D, rot,
-                                     1 if interleaved else 0, pos0, eps, weight_offset, _addr(ws), nbytes,
-                                     _stream_ptr(stream))
+                                     1 if interleaved else 0, int(pos0), float(eps), float(weight_offset), _addr(ws),
+                                     nbytes, _stream_ptr(stream))
     if rc:
         raise SwaError(rc, "swa_attn_qk_rope_bwd")
 
@@ -670,6 +718,13 @@ def qk_rope_backward(q, k, wq, wk, inv_freq, dq, dk, dv, eps: float, positions=N
     the fused projection output (q, k and v heads in that order; the k or v
     part is left out with k or dv None), dwq and dwk fp32 [D] (None for a
     None weight)."""
+    if stream is None:
+        r = (_fast or _marshal()).qk_rope_backward(q, k, wq, wk, inv_freq, dq, dk, dv, eps, positions, pos0,
+                                                   weight_offset, interleaved)
+        if r.__class__ is tuple:
+            return r
+        if r is not None:
+            raise SwaError(r, "swa_attn_qk_rope_bwd")
     import torch
 
     dims = _check_rope_bwd(q, k, wq, wk, inv_freq, dq, dk, dv, positions)

@@ -1,4 +1,5 @@
-"""Build libswa_attn.so in-tree with nvcc for sm_103a.
+"""Build libswa_attn.so in-tree with nvcc for sm_103a, and the binding's
+argument marshalling (csrc/marshal.cpp) with g++ against PyTorch's headers.
 
 Each .cu under csrc/ is compiled to an object in parallel, then linked into
 sliding_window_attention_gb300/libswa_attn.so.  Rebuilds only what changed
@@ -11,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -28,6 +30,23 @@ def _nvcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libswa_attn.so")
+
+
+MARSHAL = os.path.join(PKG, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
+
+
+def _marshal_cmd(src: str, out: str):
+    """g++ on the marshalling module.  The torch and CUDA symbols that it uses
+    come from the libraries `import torch` has loaded."""
+    import torch
+
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-w",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", sysconfig.get_paths()["include"],
+            "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"), "-I", cuda, src, "-o", out,
+            "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
 
 
 def _headers():
@@ -51,6 +70,15 @@ def build(verbose: bool = False, force: bool = False) -> str:
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    src = os.path.join(CSRC, "marshal.cpp")
+    marshal_tmp = MARSHAL + f".tmp{os.getpid()}"
+    marshal_due = force or not os.path.exists(MARSHAL) or \
+        os.path.getmtime(MARSHAL) < max(os.path.getmtime(src), os.path.getmtime(os.path.join(ROOT, "include", "swa_attn.h")))
+    if marshal_due:
+        cmd = _marshal_cmd(src, marshal_tmp)
+        if verbose:
+            print(" ".join(cmd), file=sys.stderr)
+        procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -61,7 +89,9 @@ def build(verbose: bool = False, force: bool = False) -> str:
             print(text, file=sys.stderr)
     if failed:
         msg = "\n".join(f"--- {s}\n{t}" for s, t in failed)
-        raise RuntimeError(f"nvcc failed:\n{msg}")
+        raise RuntimeError(f"compilation failed:\n{msg}")
+    if marshal_due:
+        os.replace(marshal_tmp, MARSHAL)
     if force or not os.path.exists(SO) or any(os.path.getmtime(o) > os.path.getmtime(SO) for o in objs):
         tmp = SO + f".tmp{os.getpid()}"
         cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]

@@ -386,6 +386,42 @@ def test_training_chain_matches_64_bits():
         assert rel <= 1e-2, f"{name}: {rel:.2e}"
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("has_k,has_v", [(True, True), (True, False), (False, True), (False, False)])
+def test_both_marshalling_paths_give_the_same(has_k, has_v):
+    """A call on the current stream is marshalled in C++, one with a stream of its own (or with numpy scalars) in
+    Python: equal bits, equal outputs left out."""
+    import numpy as np
+
+    import sliding_window_attention_gb300 as swa
+
+    B, L, Hq, Hkv, D = 3, 5, 4, 2, 64
+    (q, k, v), g = fused(B, L, Hq, Hkv, D, 41, 8)
+    w, f, dq, dk, dv = cuda(1 + 0.2 * torch.randn(D, generator=g), freqs(16),
+                            *(torch.randn((B, h, L, D), generator=g) for h in (Hq, Hkv, Hkv)))
+    q, k, v = dev_rows((q, k, v), 8)
+    k, v = k if has_k else None, v if has_v else None
+    s = torch.cuda.current_stream()
+    for kw in (dict(pos0=7, weight_offset=0.5, interleaved=True), dict(), dict(positions=torch.arange(
+            15, dtype=torch.int32, device="cuda").view(3, 5))):
+        calls = [swa.qk_rope(q, k, v, w, w, f, EPS, **kw, **x) for x in (dict(), dict(stream=s))]
+        if "pos0" in kw:
+            calls.append(swa.qk_rope(q, k, v, w, w, f, np.float64(EPS), **dict(kw, pos0=np.int64(7))))
+        kc = [torch.zeros((B, Hkv, 9, D), dtype=BF, device="cuda") for _ in range(4)]
+        n = torch.tensor([5, 9, 7], dtype=torch.int32, device="cuda")
+        appends = [swa.qk_rope_append(q, k, v, w, w, f, kc[2 * i] if has_k else None, kc[2 * i + 1] if has_v else None,
+                                      n, EPS, **kw, **x) for i, x in enumerate((dict(), dict(stream=s)))]
+        grads = [swa.qk_rope_backward(q, k, w, w, f, dq, dk if has_k else None, dv if has_v else None, EPS, **kw, **x)
+                 for x in (dict(), dict(stream=s))]
+        torch.cuda.synchronize()
+        for outs in (calls, grads):
+            for other in outs[1:]:
+                for a, b in zip(outs[0], other):
+                    assert (a is None and b is None) or torch.equal(a, b)
+        assert torch.equal(*appends) and torch.equal(kc[0], kc[2]) and torch.equal(kc[1], kc[3])
+        assert (calls[0][1] is not None) == has_k and (calls[0][2] is not None) == has_v
+
+
 # --------------------------------------------------------------------------- refusals (no GPU)
 
 
@@ -463,5 +499,10 @@ def test_binding_refuses_wrong_layouts():
         a = {**dict(q=q, k=k, v=v, wq=w, wk=w, f=f, positions=None), **bad}
         with pytest.raises(ValueError):
             swa.qk_rope(a["q"], a["k"], a["v"], a["wq"], a["wk"], a["f"], EPS, positions=a["positions"])
-    with pytest.raises(swa.SwaError):
-        swa.qk_rope(q, k, v, w, w, freqs(36).cuda(), EPS)  # rot_dim 72 > D
+    for kw in (dict(), dict(stream=torch.cuda.current_stream())):
+        with pytest.raises(swa.SwaError):
+            swa.qk_rope(q, k, v, w, w, freqs(36).cuda(), EPS, **kw)  # rot_dim 72 > D
+        with pytest.raises(swa.SwaError):
+            swa.qk_rope(q, k, v, w, w, f, 0.0, **kw)
+        with pytest.raises(ValueError):
+            swa.qk_rope_append(q, k, v, w, w, f, None, None, torch.ones(2, dtype=torch.int32, device="cuda"), EPS, **kw)

@@ -241,6 +241,22 @@ def test_repeats_streams_and_workspaces():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("sinks", [False, True])
+def test_both_marshalling_paths_give_the_same(sinks):
+    """On the current stream (marshalled in C++) and on a stream of the call's own (in Python): equal bits."""
+    import sliding_window_attention_gb300 as swa
+
+    a = {n: None if t is None else t.cuda() for n, t in make(3, 4, 2, 2, 128, 90, 20, 9, sinks, prefix_rows=100).items()}
+    n = torch.tensor([20, 3, 11], dtype=torch.int32, device="cuda")
+    x = (a["q"], a["kp"], a["vp"], a["ko"], a["vo"], n)
+    for kw in (dict(), dict(prefix_len=90), dict(prefix_len=0)):
+        got = [swa.forward_shared(*x, 17, 0.1, sinks=a["sinks"], **kw, **s)
+               for s in (dict(), dict(stream=torch.cuda.current_stream()))]
+        torch.cuda.synchronize()
+        assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+@pytest.mark.gpu
 def test_captured_step_follows_the_lengths():
     """Append and attend, captured once: every replay takes the lengths and tokens of its moment."""
     import sliding_window_attention_gb300 as swa
