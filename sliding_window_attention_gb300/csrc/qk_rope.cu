@@ -32,19 +32,7 @@
 namespace swa {
 namespace {
 
-constexpr int kThr = 256, kWarps = kThr / 32;
-constexpr long long kStagedTokens = 1024;  // from here on the forward stages its rows through shared memory
-
-// A row is held by LPR lanes, E elements each in NV vectors of 8 (16 bytes of
-// bf16): vector j of lane l holds elements 256 j + 8 l ... + 7, so that every
-// vector load of a warp is one contiguous run.
-template <int D>
-struct RowCfg {
-  static constexpr int NV = D == 512 ? 2 : 1;
-  static constexpr int E = 8 * NV;
-  static constexpr int LPR = D / E;     // lanes of a row
-  static constexpr int RPW = 32 / LPR;  // rows of a warp at once
-};
+constexpr int kThr = 256;
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
@@ -52,24 +40,6 @@ __device__ __forceinline__ uint32_t bf_pack(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ void unpack8(const uint4& v, float* x) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = bf_lo(w[i]);
-    x[2 * i + 1] = bf_hi(w[i]);
-  }
-}
-__device__ __forceinline__ uint4 pack8(const float* x) {
-  return make_uint4(bf_pack(x[0], x[1]), bf_pack(x[2], x[3]), bf_pack(x[4], x[5]), bf_pack(x[6], x[7]));
-}
-template <int LPR>
-__device__ __forceinline__ float row_sum(float v) {
-#pragma unroll
-  for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
 // Frequency (radians a position) as a fraction of a turn, mod 1, in units of 2^-64.
 __device__ __forceinline__ uint64_t turn_step(double f) {
   double t = f * 0.15915494309189533577;  // 1 / (2 pi)
@@ -97,213 +67,16 @@ __device__ __forceinline__ long long token_pos(const RopePos& a, int b, int l, i
   return (long long)a.pos0 + l + (a.kv_len ? (long long)a.kv_len[b] - L : 0);
 }
 
-// cos / sin of T consecutive tokens from `tok0`, as cs[t * pairs + i].
-__device__ __forceinline__ void fill_cs(const RopePos& a, long long tok0, int T, long long n_tok, int L,
-                                        const uint64_t* step, float2* cs) {
-  for (int idx = threadIdx.x; idx < T * a.pairs; idx += kThr) {
-    const int t = idx / a.pairs, i = idx - t * a.pairs;
-    const long long tok = tok0 + t;
-    if (tok < n_tok) cs[idx] = turn_cs(token_pos(a, (int)(tok / L), (int)(tok % L), L), step[i]);
-  }
-}
-
-// One lane's share of a token's rotation: y_e = c_e u_e + s_e u_partner(e).
-template <int D, bool INTER>
-struct LaneRot {
-  using C = RowCfg<D>;
-  float c[C::E], s[C::E];
-  // half-split pairs: the lane (and vector) that holds each vector's partners
-  int src[C::NV], srcv[C::NV];
-
-  __device__ __forceinline__ void place(int lane, int pairs) {
-    if constexpr (!INTER) {
-#pragma unroll
-      for (int j = 0; j < C::NV; ++j) {
-        const int d = 256 * j + 8 * (lane % C::LPR);
-        const int pd = d < pairs ? d + pairs : (d < 2 * pairs ? d - pairs : d);
-        src[j] = (lane & ~(C::LPR - 1)) | ((pd % (C::LPR * 8)) >> 3);
-        srcv[j] = C::NV > 1 ? pd / 256 : 0;
-      }
-    }
-  }
-  __device__ __forceinline__ void load(const float2* cs, int lane, int pairs) {
-#pragma unroll
-    for (int j = 0; j < C::NV; ++j) {
-      const int d = 256 * j + 8 * (lane % C::LPR);
-      if (INTER) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bool in = d + 2 * i < 2 * pairs;
-          const float2 v = in ? cs[d / 2 + i] : make_float2(1.f, 0.f);
-          c[8 * j + 2 * i] = c[8 * j + 2 * i + 1] = v.x;
-          s[8 * j + 2 * i] = -v.y;
-          s[8 * j + 2 * i + 1] = v.y;
-        }
-      } else {
-        const bool lo = d < pairs, in = d < 2 * pairs;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 v = in ? cs[(lo ? d : d - pairs) + i] : make_float2(1.f, 0.f);
-          c[8 * j + i] = v.x;
-          s[8 * j + i] = lo ? -v.y : v.y;
-        }
-      }
-    }
-  }
-  // The partners' values of one register array (as many words a vector as given).
-  template <int W, typename T>
-  __device__ __forceinline__ void partners(const T (&x)[W], T (&xp)[W], int pairs) const {
-    constexpr int PV = W / C::NV;
-    if (C::NV > 1 && 4 * pairs > D) {
-      // a pair may span the two vectors (always, when the whole head is rotated)
-      if (2 * pairs == D) {
-#pragma unroll
-        for (int i = 0; i < W; ++i) xp[i] = x[(i + PV) % W];
-        return;
-      }
-#pragma unroll
-      for (int j = 0; j < C::NV; ++j)
-#pragma unroll
-        for (int i = 0; i < PV; ++i) {
-          const T a = __shfl_sync(0xffffffffu, x[i], src[j]), b = __shfl_sync(0xffffffffu, x[PV * (C::NV - 1) + i], src[j]);
-          xp[PV * j + i] = srcv[j] ? b : a;
-        }
-      return;
-    }
-#pragma unroll
-    for (int i = 0; i < PV; ++i) xp[i] = __shfl_sync(0xffffffffu, x[i], src[0]);
-    if (C::NV > 1) {
-#pragma unroll
-      for (int i = PV; i < W; ++i) xp[i] = x[i];  // beyond the rotated part
-    }
-  }
-};
-
-struct RopeFwd {
-  const uint16_t *q, *k, *v;             // token-major rows; k, v may be null
-  long long q_tok, k_tok, v_tok;         // elements between tokens
-  const float *wq, *wk;                  // [D] or null
-  RopePos pos;
-  uint16_t *qo, *ko, *vo;                // [B, Hq, L, D], [B, Hkv, kv_rows, D]
-  int B, L, Hq, Hkv, kv_rows, T;         // T tokens a CTA (1, 2, 4 or 8)
-  float eps, off;
-};
-
-// A warp takes one token and a share of its heads: the token's rotation
-// stays in registers over all of them.  8 / T warps share a token.
-template <int D, bool INTER>
-__global__ void __launch_bounds__(kThr) qk_rope_fwd_kernel(const RopeFwd p) {
-  using C = RowCfg<D>;
-  constexpr int NV = C::NV, E = C::E, LPR = C::LPR, RPW = C::RPW, U = 4 / NV;  // U row groups in flight
-  extern __shared__ uint64_t sm[];
-  uint64_t* step = sm;
-  float2* cs = reinterpret_cast<float2*>(sm + p.pos.pairs);
-  const int pairs = p.pos.pairs, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long n_tok = (long long)p.B * p.L, tok0 = (long long)blockIdx.x * p.T;
-  for (int i = threadIdx.x; i < pairs; i += kThr) step[i] = turn_step(p.pos.inv_freq[i]);
-  __syncthreads();
-  fill_cs(p.pos, tok0, p.T, n_tok, p.L, step, cs);
-  __syncthreads();
-  const int t = warp % p.T, share = warp / p.T, shares = kWarps / p.T;
-  const long long tok = tok0 + t;
-  if (tok >= n_tok) return;
-  const int b = (int)(tok / p.L), l = (int)(tok % p.L);
-  const int sub = lane / LPR, d0 = 8 * (lane % LPR);
-  LaneRot<D, INTER> rot;
-  rot.place(lane, pairs);
-
-  const int kv_row = p.pos.kv_len ? p.pos.kv_len[b] - p.L + l : l;
-  const bool kv_ok = kv_row >= 0 && kv_row < p.kv_rows;  // rows outside the cache are not written
-
-  // rows of one kind (q or k)
-  auto rows = [&](const uint16_t* x, const float* w, uint16_t* out, int H, long long head_stride, bool store) {
-    float ca[E], sb[E];  // c_e w_e and s_e w_partner(e)
-    rot.load(cs + t * pairs, lane, pairs);
-    {
-      float we[E], wp[E];
-#pragma unroll
-      for (int e = 0; e < E; ++e) we[e] = w ? w[256 * (e >> 3) + d0 + (e & 7)] + p.off : 1.f;
-      if constexpr (INTER) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) wp[e] = we[e ^ 1];
-      } else {
-        rot.partners(we, wp, pairs);
-      }
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        ca[e] = rot.c[e] * we[e];
-        sb[e] = rot.s[e] * wp[e];
-      }
-    }
-    for (int h0 = share * RPW; h0 < H; h0 += U * shares * RPW) {
-      uint4 raw[U][NV];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = h0 + u * shares * RPW + sub;
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-          raw[u][j] = h < H ? __ldcs(reinterpret_cast<const uint4*>(x + (size_t)h * D + 256 * j + d0)) : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = h0 + u * shares * RPW + sub;
-        if (h0 + u * shares * RPW >= H) break;  // uniform over the warp
-        float f[E], y[E];
-        uint32_t words[4 * NV], other[4 * NV];
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          unpack8(raw[u][j], f + 8 * j);
-          words[4 * j] = raw[u][j].x;
-          words[4 * j + 1] = raw[u][j].y;
-          words[4 * j + 2] = raw[u][j].z;
-          words[4 * j + 3] = raw[u][j].w;
-        }
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) ss = fmaf(f[e], f[e], ss);
-        const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
-        if constexpr (INTER) {
-#pragma unroll
-          for (int e = 0; e < E; ++e) y[e] = r * fmaf(f[e], ca[e], f[e ^ 1] * sb[e]);
-        } else {
-          rot.partners(words, other, pairs);
-#pragma unroll
-          for (int i = 0; i < 4 * NV; ++i) {
-            y[2 * i] = r * fmaf(f[2 * i], ca[2 * i], bf_lo(other[i]) * sb[2 * i]);
-            y[2 * i + 1] = r * fmaf(f[2 * i + 1], ca[2 * i + 1], bf_hi(other[i]) * sb[2 * i + 1]);
-          }
-        }
-        if (store && h < H) {
-#pragma unroll
-          for (int j = 0; j < NV; ++j)
-            *reinterpret_cast<uint4*>(out + h * head_stride + 256 * j + d0) = pack8(y + 8 * j);
-        }
-      }
-    }
-  };
-  rows(p.q + tok * p.q_tok, p.wq, p.qo + (((size_t)b * p.Hq) * p.L + l) * D, p.Hq, (long long)p.L * D, true);
-  const size_t kv_off = ((size_t)b * p.Hkv * p.kv_rows + (kv_ok ? kv_row : 0)) * D;
-  if (p.k) rows(p.k + tok * p.k_tok, p.wk, p.ko + kv_off, p.Hkv, (long long)p.kv_rows * D, kv_ok);
-  if (p.v && kv_ok) {
-    const uint16_t* x = p.v + tok * p.v_tok;
-    for (int h = share * RPW + sub; h < p.Hkv; h += shares * RPW)
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-        *reinterpret_cast<uint4*>(p.vo + kv_off + (size_t)h * p.kv_rows * D + 256 * j + d0) =
-            __ldcs(reinterpret_cast<const uint4*>(x + (size_t)h * D + 256 * j + d0));
-  }
-}
-
-// ---------------------------------------------------------------------------
-// Long sequences: rows staged through shared memory by TMA.
-//
-// Both directions move a few bytes a multiplication, so what bounds them is
-// the memory's latency: the bytes in flight.  A CTA keeps a ring of
-// stages filled -- a stage is 512 / D heads of 8 consecutive tokens, x as the
-// projection laid it out ([token][head][D]) and, in the backward, dy as the
-// attention did ([head][token][D]); the boxes of two tensor maps -- and its
-// eight warps, one a token, work from there.  A stage's units (token group,
-// block of heads) form one list that the CTAs share out evenly.
+// Rows staged through shared memory by TMA.  Both directions do a few
+// multiplications a byte, so what bounds them is the memory's latency: the
+// bytes in flight.  A CTA keeps a ring of stages filled -- a stage is 512 / D
+// heads of 8 consecutive tokens, x as the projection laid it out
+// ([token][head][D]) and, in the backward, dy as the attention did
+// ([head][token][D]); the boxes of two tensor maps -- and its eight warps, one
+// a token, work from there.  The stages' units (token group, block of heads)
+// form one list that the CTAs share out evenly.  The forward's groups run over
+// the whole batch's tokens, so that a generation step of 64 requests is 8
+// groups; the backward's stay within a batch entry (dy's layout).
 //
 // A lane holds E = 8 (16 at D = 512) elements of a row in NG groups of 4, D / NG
 // apart: with the whole head rotated in halves an element's partner is then in
@@ -322,7 +95,7 @@ struct StCfg {
 // The order of a CTA's stages: units [u0, u1) of groups x (Hq, Hkv, Hkv heads in blocks).
 struct StList {
   int nq, nk, nv, per;     // blocks of q, k, v heads, and of a group
-  int groups, gl;          // token groups, of a batch entry
+  int groups, gl;          // token groups, and (backward) those of a batch entry
   __device__ __forceinline__ void split(int cta, int ctas, int& u0, int& u1) const {
     const long long u = (long long)groups * per;
     u0 = (int)(u * cta / ctas);
@@ -473,6 +246,7 @@ __global__ void __launch_bounds__(kThr, StSmem<D, BWD>::CTAS)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + NS);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, pairs = p.pos.pairs;
   const StList& ls = p.list;
+  if (BWD) tc::grid_launch_dependents();  // the scales' sum waits for this grid's end
   int u0, u1;
   ls.split(blockIdx.x, gridDim.x, u0, u1);
 
@@ -497,7 +271,7 @@ __global__ void __launch_bounds__(kThr, StSmem<D, BWD>::CTAS)
   auto load = [&](int n) {
     const int s = n % NS, u = u0 + n, grp = u / ls.per, i = u - grp * ls.per;
     if (n >= NS && !tc::mbar_wait(empty + s, ((n / NS) & 1) ^ 1, abort_flag)) return;
-    const int b = grp / ls.gl, l0 = (grp - b * ls.gl) * kTok;
+    const int b = BWD ? grp / ls.gl : 0, l0 = (grp - b * ls.gl) * kTok;  // forward: tokens of the whole batch
     const int kind = i < ls.nq ? 0 : (i < ls.nq + ls.nk ? 1 : 2);
     const int h0 = (i - (kind > 0 ? ls.nq : 0) - (kind > 1 ? ls.nk : 0)) * HB;
     unsigned char* x = base + s * M::STAGE;
@@ -552,8 +326,10 @@ __global__ void __launch_bounds__(kThr, StSmem<D, BWD>::CTAS)
       }
     };
     for (; ok && u < u1; ++grp) {
-      const int b = grp / ls.gl, l = (grp - b * ls.gl) * kTok + warp;
-      const bool live = l < p.L;
+      // this warp's token
+      const int t = grp * kTok + warp, b = BWD ? grp / ls.gl : t / p.L;
+      const int l = BWD ? t - b * ls.gl * kTok : t - b * p.L;
+      const bool live = b < p.B && l < p.L;
       const long long tok = (long long)b * p.L + l;
       __syncwarp();
       if (live) {
@@ -765,16 +541,6 @@ __global__ void __launch_bounds__(1024) qk_rope_dw_kernel(const float* part, flo
   }
 }
 
-template <int D>
-cudaError_t rope_fwd_d(const RopeFwd& p, cudaStream_t s) {
-  const long long n_tok = (long long)p.B * p.L;
-  const unsigned grid = (unsigned)((n_tok + p.T - 1) / p.T);
-  const size_t smem = (size_t)p.pos.pairs * 8 * (1 + p.T);
-  if (p.pos.interleaved) qk_rope_fwd_kernel<D, true><<<grid, kThr, smem, s>>>(p);
-  else qk_rope_fwd_kernel<D, false><<<grid, kThr, smem, s>>>(p);
-  return cudaGetLastError();
-}
-
 RopePos rope_pos(const RopeArgs& a) {
   RopePos r;
   r.inv_freq = a.inv_freq;
@@ -786,15 +552,15 @@ RopePos rope_pos(const RopeArgs& a) {
   return r;
 }
 
-StRope staged_params(const RopeArgs& a, bool v, int* status) {
+StRope staged_params(const RopeArgs& a, bool v, bool bwd, int* status) {
   StRope p = {};
   const int hb = 512 / a.D;
   p.list.nq = (a.Hq + hb - 1) / hb;
   p.list.nk = a.k ? (a.Hkv + hb - 1) / hb : 0;
   p.list.nv = v ? (a.Hkv + hb - 1) / hb : 0;
   p.list.per = p.list.nq + p.list.nk + p.list.nv;
-  p.list.gl = (a.L + kTok - 1) / kTok;
-  p.list.groups = a.B * p.list.gl;
+  p.list.gl = bwd ? (a.L + kTok - 1) / kTok : 0;
+  p.list.groups = bwd ? a.B * p.list.gl : (int)(((long long)a.B * a.L + kTok - 1) / kTok);
   p.pos = rope_pos(a);
   p.wq = a.wq;
   p.wk = a.wk;
@@ -832,9 +598,10 @@ cudaError_t staged_launch(const StRope& p, const CUtensorMap (&m)[6], int grid, 
 template <int D>
 cudaError_t staged_fwd(const RopeArgs& a, const uint16_t* v, long long v_tok, const StRope& p, cudaStream_t s) {
   CUtensorMap m[6];
-  cudaError_t e = make_tmap_tokens(&m[0], a.q, D, a.Hq, a.L, a.B, a.q_tok, kTok, StCfg<D>::HB);
-  if (e == cudaSuccess && a.k) e = make_tmap_tokens(&m[1], a.k, D, a.Hkv, a.L, a.B, a.k_tok, kTok, StCfg<D>::HB);
-  if (e == cudaSuccess && v) e = make_tmap_tokens(&m[2], v, D, a.Hkv, a.L, a.B, v_tok, kTok, StCfg<D>::HB);
+  const int toks = a.B * a.L;
+  cudaError_t e = make_tmap_tokens(&m[0], a.q, D, a.Hq, toks, 1, a.q_tok, kTok, StCfg<D>::HB);
+  if (e == cudaSuccess && a.k) e = make_tmap_tokens(&m[1], a.k, D, a.Hkv, toks, 1, a.k_tok, kTok, StCfg<D>::HB);
+  if (e == cudaSuccess && v) e = make_tmap_tokens(&m[2], v, D, a.Hkv, toks, 1, v_tok, kTok, StCfg<D>::HB);
   if (e != cudaSuccess) return e;
   if (!a.k) m[1] = m[0];  // not read
   if (!v) m[2] = m[0];
@@ -881,47 +648,16 @@ size_t qk_rope_bwd_part_floats(int D) { return (size_t)152 * 2 * 2 * D; }
 
 cudaError_t launch_qk_rope_fwd(const RopeArgs& a, const uint16_t* v, long long v_tok, uint16_t* qo, uint16_t* ko,
                                uint16_t* vo, int kv_rows, int* status, cudaStream_t s) {
-  const long long n_tok = (long long)a.B * a.L;
-  if (a.L >= kTok && n_tok >= kStagedTokens) {
-    StRope p = staged_params(a, v != nullptr, status);
-    p.qo = qo;
-    p.ko = ko;
-    p.vo = vo;
-    p.kv_rows = kv_rows;
-    switch (a.D) {
-      case 64: return staged_fwd<64>(a, v, v_tok, p, s);
-      case 128: return staged_fwd<128>(a, v, v_tok, p, s);
-      case 256: return staged_fwd<256>(a, v, v_tok, p, s);
-      case 512: return staged_fwd<512>(a, v, v_tok, p, s);
-      default: return cudaErrorInvalidValue;
-    }
-  }
-  RopeFwd p;
-  p.q = a.q;
-  p.k = a.k;
-  p.v = v;
-  p.q_tok = a.q_tok;
-  p.k_tok = a.k_tok;
-  p.v_tok = v_tok;
-  p.wq = a.wq;
-  p.wk = a.wk;
-  p.pos = rope_pos(a);
+  StRope p = staged_params(a, v != nullptr, false, status);
   p.qo = qo;
   p.ko = ko;
   p.vo = vo;
-  p.B = a.B;
-  p.L = a.L;
-  p.Hq = a.Hq;
-  p.Hkv = a.Hkv;
   p.kv_rows = kv_rows;
-  p.eps = a.eps;
-  p.off = a.weight_offset;
-  p.T = n_tok >= 4096 ? 4 : 1;
   switch (a.D) {
-    case 64: return rope_fwd_d<64>(p, s);
-    case 128: return rope_fwd_d<128>(p, s);
-    case 256: return rope_fwd_d<256>(p, s);
-    case 512: return rope_fwd_d<512>(p, s);
+    case 64: return staged_fwd<64>(a, v, v_tok, p, s);
+    case 128: return staged_fwd<128>(a, v, v_tok, p, s);
+    case 256: return staged_fwd<256>(a, v, v_tok, p, s);
+    case 512: return staged_fwd<512>(a, v, v_tok, p, s);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -929,7 +665,7 @@ cudaError_t launch_qk_rope_fwd(const RopeArgs& a, const uint16_t* v, long long v
 cudaError_t launch_qk_rope_bwd(const RopeArgs& a, const float* dq, const float* dk, const float* dv, uint16_t* gq,
                                uint16_t* gk, uint16_t* gv, long long gq_tok, long long gk_tok, long long gv_tok,
                                float* dwq, float* dwk, float* part, int* status, cudaStream_t s) {
-  StRope p = staged_params(a, dv != nullptr, status);
+  StRope p = staged_params(a, dv != nullptr, true, status);
   p.gq = gq;
   p.gk = gk;
   p.gv = gv;
