@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kThr, StSmem<D, BWD>::CTAS)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + NS);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, pairs = p.pos.pairs;
   const StList& ls = p.list;
-  if (BWD) tc::grid_launch_dependents();  // the scales' sum waits for this grid's end
+  tc::grid_launch_dependents();  // dependents wait for this grid's end
   int u0, u1;
   ls.split(blockIdx.x, gridDim.x, u0, u1);
 
@@ -264,6 +264,7 @@ __global__ void __launch_bounds__(kThr, StSmem<D, BWD>::CTAS)
     tc::fence_mbar_init();
   }
   __syncthreads();
+  tc::grid_dependency_wait();
 
   uint64_t accq[BWD ? W : 1], acck[BWD ? W : 1];  // dw of the lane's elements
 #pragma unroll
@@ -530,6 +531,7 @@ __global__ void __launch_bounds__(kThr, StSmem<D, BWD>::CTAS)
 __global__ void __launch_bounds__(1024) qk_rope_dw_kernel(const float* part, float* dwq, float* dwk, int D, int n) {
   __shared__ float red[32][33];
   const int x = threadIdx.x & 31, grp = threadIdx.x >> 5, col = blockIdx.x * 32 + x;  // column of [2][D]
+  tc::grid_launch_dependents();
   tc::grid_dependency_wait();
   float v = 0.f;
 #pragma unroll 5
@@ -590,8 +592,7 @@ cudaError_t staged_mode(const StRope& p, const CUtensorMap (&m)[6], int grid, cu
   const size_t smem = StSmem<D, BWD>::BYTES;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kern<<<grid, kThr, smem, s>>>(m[0], m[1], m[2], m[3], m[4], m[5], p);
-  return cudaGetLastError();
+  return launch_dependent(kern, dim3(grid), dim3(kThr), smem, s, m[0], m[1], m[2], m[3], m[4], m[5], p);
 }
 
 template <int D, bool BWD>
@@ -634,17 +635,7 @@ cudaError_t staged_bwd(const RopeArgs& a, const float* dq, const float* dk, cons
   const int grid = staged_ctas<D, true>(p.list);
   e = staged_launch<D, true>(p, m, grid, s);
   if (e != cudaSuccess || (!dwq && !dwk)) return e;
-  // the partials' sum, launched as a programmatic dependent of the main kernel
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * D / 32);
-  cfg.blockDim = dim3(1024);
-  cfg.stream = s;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, qk_rope_dw_kernel, static_cast<const float*>(p.part), dwq, dwk, D, grid);
+  return launch_dependent(qk_rope_dw_kernel, dim3(2 * D / 32), dim3(1024), 0, s, p.part, dwq, dwk, D, grid);
 }
 
 }  // namespace

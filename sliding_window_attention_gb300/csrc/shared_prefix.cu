@@ -682,22 +682,6 @@ __global__ void __launch_bounds__(ShKernel<D, NP>::THREADS, 1)
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   grid_launch_dependents();  // the merge waits for this grid's end
 
-  // ---- the lengths: own tiles in all, the shortest live request
-  {
-    int sum = 0, mn = INT32_MAX;
-#pragma unroll 1
-    for (int b = threadIdx.x; b < g.B; b += THR) {
-      const int len = p.own_len[b];
-      sum += own_tiles(g, len);
-      if (len >= 0) mn = min(mn, min(len, g.own_rows));
-    }
-    sum = __reduce_add_sync(0xffffffffu, sum);
-    mn = __reduce_min_sync(0xffffffffu, mn);
-    if (lane == 0) {
-      scan_sum[warp] = sum;
-      scan_min[warp] = mn;
-    }
-  }
   if (threadIdx.x == 0) {
     start_b = -1;
     *abort_flag = 0;
@@ -717,6 +701,23 @@ __global__ void __launch_bounds__(ShKernel<D, NP>::THREADS, 1)
   if (warp == 1) {
     tmem_alloc(tmem_slot, K::TCOLS);
     tmem_relinquish();
+  }
+  grid_dependency_wait();
+  // ---- the lengths: own tiles in all, the shortest live request
+  {
+    int sum = 0, mn = INT32_MAX;
+#pragma unroll 1
+    for (int b = threadIdx.x; b < g.B; b += THR) {
+      const int len = p.own_len[b];
+      sum += own_tiles(g, len);
+      if (len >= 0) mn = min(mn, min(len, g.own_rows));
+    }
+    sum = __reduce_add_sync(0xffffffffu, sum);
+    mn = __reduce_min_sync(0xffffffffu, mn);
+    if (lane == 0) {
+      scan_sum[warp] = sum;
+      scan_min[warp] = mn;
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -870,6 +871,7 @@ __global__ void __launch_bounds__(MergeCfg<D>::THREADS) shared_merge_kernel(cons
   const int row = blockIdx.x;  // (b Hkv + kv head) M + m
   const int bkv = row / g.M, m = row - bkv * g.M, b = bkv / g.Hkv, h = bkv - b * g.Hkv;
   const int lane = threadIdx.x & 31;
+  grid_launch_dependents();
   grid_dependency_wait();
   // the lengths and the plan, in one round of loads
   const int len = p.own_len[b], tp = p.plan[0], ns = p.plan[1], off = p.plan[kPlanOff + b];
@@ -1046,20 +1048,12 @@ cudaError_t shared_d(const SharedGeom& g, const SharedArgs& a, void* ws, int* st
   auto kern = shared_kernel<D, NP>;
   if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::SMEM)) != cudaSuccess)
     return e;
-  kern<<<kSMs, K::THREADS, K::SMEM, st>>>(tqp, tqo, tkp, tvp, tko, tvo, p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  // the merge, launched as a programmatic dependent: its blocks are placed
-  // while the main grid runs and start when that has completed
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(g.B * g.Hkv * g.M));
-  cfg.blockDim = dim3(MergeCfg<D>::THREADS);
-  cfg.stream = st;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, shared_merge_kernel<D>, p);
+  // both are programmatic dependents of what runs before them: the main grid's
+  // set-up and the merge's placement fall into its predecessor's end
+  if ((e = launch_dependent(kern, dim3(kSMs), dim3(K::THREADS), K::SMEM, st, tqp, tqo, tkp, tvp, tko, tvo, p)) !=
+      cudaSuccess)
+    return e;
+  return launch_dependent(shared_merge_kernel<D>, dim3((unsigned)(g.B * g.Hkv * g.M)), dim3(MergeCfg<D>::THREADS), 0, st, p);
 }
 
 template <int D>

@@ -346,6 +346,25 @@ cudaError_t launch_bwd_dq_tc(const Geom& g, const uint16_t* q16, const uint16_t*
                              const uint16_t* g16, const float* stats, int Lpad, float* dq, int* status,
                              cudaStream_t s);
 
+// Launches `kern` as a programmatic dependent of the work before it on `s`:
+// its CTAs may be placed before that has completed, and it has to call
+// grid_dependency_wait() (tc_ptx.cuh) before it touches global memory.
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kern)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                             Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<Params>(args)...);
+}
+
 // ---- attention over a shared prefix and per-request caches (shared_prefix.cu) ----
 struct SharedGeom {
   int B, Hq, Hkv, G, Lq, M;        // M = G * Lq query rows of a request and kv head
