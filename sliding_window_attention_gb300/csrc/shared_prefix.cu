@@ -680,7 +680,6 @@ __global__ void __launch_bounds__(ShKernel<D, NP>::THREADS, 1)
 
   const SharedGeom& g = p.g;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-  grid_launch_dependents();  // the merge waits for this grid's end
 
   if (threadIdx.x == 0) {
     start_b = -1;
@@ -698,11 +697,14 @@ __global__ void __launch_bounds__(ShKernel<D, NP>::THREADS, 1)
   if (threadIdx.x < 4 * A::GROUPS)  // tags of the prefix phase
     reinterpret_cast<int*>(base + A::OFF_SMALL + (threadIdx.x >> 2) * A::SMALL + A::BND)[8 + (threadIdx.x & 3)] = 0;
   fence_proxy_async_smem();
+  grid_dependency_wait();
+  // Tensor memory is taken after the predecessor's end and before a dependent
+  // may be placed: a grid that held columns while it waits for another that has
+  // yet to allocate its own, on the same SM, would wait for ever.
   if (warp == 1) {
     tmem_alloc(tmem_slot, K::TCOLS);
     tmem_relinquish();
   }
-  grid_dependency_wait();
   // ---- the lengths: own tiles in all, the shortest live request
   {
     int sum = 0, mn = INT32_MAX;
@@ -722,6 +724,7 @@ __global__ void __launch_bounds__(ShKernel<D, NP>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_launch_dependents();  // the merge waits for this grid's end
   const uint32_t tmem = *tmem_slot;
   int tiles = 0, mn = INT32_MAX;
 #pragma unroll
