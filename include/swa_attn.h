@@ -236,8 +236,9 @@ int swa_attn_bwd_sinks(const swa_bf16* q, const swa_bf16* k, const swa_bf16* v, 
  * before the call): row i sits at a = prefix_len + own_len[b] - Lq + i and
  * sees the keys j <= a, with a - j < window when window > 0.  This is
  * swa_attn_fwd_ex on the concatenated sequence of each request, but the
- * prefix's keys are read once for all requests that fit one block of 64 query
- * rows, and the requests' lengths differ.
+ * requests' lengths differ, and a prefix key is loaded once for every block of
+ * up to 128 query rows (64 at D = 512) of the whole batch's B * (Hq / Hkv) * Lq
+ * rows of a key head; blocks of one key range run side by side and meet in L2.
  *
  * A row that sees no key (a < 0) gets o = 0 and lse = -inf (with a sink
  * logit c: lse = c).  A negative own_len[b] marks an empty place of the
@@ -253,9 +254,9 @@ int swa_attn_bwd_sinks(const swa_bf16* q, const swa_bf16* k, const swa_bf16* v, 
  *
  * workspace: at least swa_attn_fwd_workspace_bytes_shared(...) bytes,
  * 256-byte aligned, with any content; calls that may overlap need separate
- * ones.  Alignment, streams, status word and other errors are as for
- * swa_attn_fwd.  SWA_ERR_BAD_CACHE: prefix_len outside [0, prefix_rows] or
- * own_rows < 1.
+ * ones.  Make the first call on a device outside stream capture.  Alignment,
+ * streams, status word and other errors are as for swa_attn_fwd.
+ * SWA_ERR_BAD_CACHE: prefix_len outside [0, prefix_rows] or own_rows < 1.
  */
 size_t swa_attn_fwd_workspace_bytes_shared(int B, int Hq, int Hkv, int Lq, int prefix_len, int own_rows, int D,
                                            int window);

@@ -449,6 +449,14 @@ def _check(device, specs):
             raise ValueError(f"{name} must be on the current CUDA device, like the other tensors (got {t.device})")
 
 
+def _int32(name, v) -> int:
+    """v as the int of a C argument (ctypes drops the bits above 32)."""
+    v = int(v)
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise ValueError(f"{name} does not fit 32 bits: {v}")
+    return v
+
+
 def _current_device(t, name):
     import torch
 
@@ -501,34 +509,39 @@ def swa_attn_fwd_shared(q, k_prefix, v_prefix, k_own, v_own, own_len, sinks, o, 
 
     dims = _check_shared(q, k_prefix, v_prefix, k_own, v_own, own_len, sinks)
     _check(dims[0], (("o", o, torch.bfloat16, q.shape), ("lse", lse, torch.float32, q.shape[:3])))
-    P = k_prefix.shape[1] if prefix_len is None else int(prefix_len)
+    P = k_prefix.shape[1] if prefix_len is None else _int32("prefix_len", prefix_len)
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _run_shared(dims, q, k_prefix, v_prefix, k_own, v_own, own_len, sinks, o, lse, int(window), float(scale), P,
-                workspace, nbytes, stream)
+    _run_shared(dims, q, k_prefix, v_prefix, k_own, v_own, own_len, sinks, o, lse, _int32("window", window),
+                float(scale), P, workspace, nbytes, stream)
 
 
 def forward_shared(q, k_prefix, v_prefix, k_own, v_own, own_len, window: int, scale: float, prefix_len=None,
                    sinks=None, stream=None):
-    """Return (o bf16 [B,Hq,Lq,D], lse fp32 [B,Hq,Lq]) of swa_attn_fwd_shared."""
-    if stream is None:
-        r = (_fast or _marshal()).forward_shared(q, k_prefix, v_prefix, k_own, v_own, own_len, window, scale,
-                                                 prefix_len, sinks)
-        if r.__class__ is tuple:
-            return r
-        if r is not None:
-            raise SwaError(r, "swa_attn_fwd_shared")
+    """Return (o bf16 [B,Hq,Lq,D], lse fp32 [B,Hq,Lq]) of swa_attn_fwd_shared,
+    allocated on the stream that the call runs on."""
     import torch
+
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return forward_shared(q, k_prefix, v_prefix, k_own, v_own, own_len, window, scale, prefix_len, sinks)
+    r = (_fast or _marshal()).forward_shared(q, k_prefix, v_prefix, k_own, v_own, own_len, window, scale, prefix_len,
+                                             sinks)
+    if r.__class__ is tuple:
+        return r
+    if r is not None:
+        raise SwaError(r, "swa_attn_fwd_shared")
 
     dims = _check_shared(q, k_prefix, v_prefix, k_own, v_own, own_len, sinks)
     dev, B, Hq, Hkv, Lq, D, prefix_rows, own_rows = dims
-    P, window = prefix_rows if prefix_len is None else int(prefix_len), int(window)
+    P = prefix_rows if prefix_len is None else _int32("prefix_len", prefix_len)
+    window = _int32("window", window)
     nbytes = fwd_workspace_bytes_shared(B, Hq, Hkv, Lq, P, own_rows, D, window)
     device = q.device
     o = torch.empty_like(q)
     lse = torch.empty((B, Hq, Lq), dtype=torch.float32, device=device)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
     _run_shared(dims, q, k_prefix, v_prefix, k_own, v_own, own_len, sinks, o, lse, window, float(scale), P, ws,
-                nbytes, stream)
+                nbytes, None)
     return o, lse
 
 
@@ -602,8 +615,8 @@ def swa_attn_qk_rope_fwd(q, k, v, wq, wk, inv_freq, q_out, k_out, v_out, eps: fl
     rc = load().swa_attn_qk_rope_fwd(q.data_ptr(), _addr(k), _addr(v), q_tok, k_tok, v_tok, _addr(wq), _addr(wk),
                                      _addr(inv_freq), _addr(positions), _addr(kv_len), q_out.data_ptr(),
                                      None if k is None else k_out.data_ptr(), None if v is None else v_out.data_ptr(),
-                                     B, Hq, Hkv, L, D, rows, rot, 1 if interleaved else 0, int(pos0), float(eps),
-                                     float(weight_offset), _stream_ptr(stream))
+                                     B, Hq, Hkv, L, D, rows, rot, 1 if interleaved else 0, _int32("pos0", pos0),
+                                     float(eps), float(weight_offset), _stream_ptr(stream))
     if rc:
         raise SwaError(rc, "swa_attn_qk_rope_fwd")
 
@@ -613,20 +626,21 @@ def qk_rope(q, k, v, wq, wk, inv_freq, eps: float, positions=None, pos0: int = 0
     """Return (q [B,Hq,L,D], k [B,Hkv,L,D], v [B,Hkv,L,D]) for the attention
     from a projection's bf16 q, k, v [B,L,heads,D]: q and k normalised per
     head, scaled and rotated by position.  k and v may be None."""
-    if stream is None:
-        r = (_fast or _marshal()).qk_rope(q, k, v, wq, wk, inv_freq, None, None, None, eps, positions, pos0,
-                                          weight_offset, interleaved)
-        if r.__class__ is tuple:
-            return r
-        if r is not None:
-            raise SwaError(r, "swa_attn_qk_rope_fwd")
     import torch
 
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return qk_rope(q, k, v, wq, wk, inv_freq, eps, positions, pos0, weight_offset, interleaved)
+    r = (_fast or _marshal()).qk_rope(q, k, v, wq, wk, inv_freq, None, None, None, eps, positions, pos0,
+                                      weight_offset, interleaved)
+    if r.__class__ is tuple:
+        return r
+    if r is not None:
+        raise SwaError(r, "swa_attn_qk_rope_fwd")
     B, L, _, D = q.shape
     dtype, device = q.dtype, q.device
     out = [None if t is None else torch.empty((B, t.shape[2], L, D), dtype=dtype, device=device) for t in (q, k, v)]
-    swa_attn_qk_rope_fwd(q, k, v, wq, wk, inv_freq, *out, eps, positions, None, pos0, weight_offset, interleaved,
-                         stream)
+    swa_attn_qk_rope_fwd(q, k, v, wq, wk, inv_freq, *out, eps, positions, None, pos0, weight_offset, interleaved)
     return tuple(out)
 
 
@@ -636,19 +650,23 @@ def qk_rope_append(q, k, v, wq, wk, inv_freq, k_cache, v_cache, kv_len, eps: flo
     kv_len[b] - 1 of each request's cache [B,Hkv,kv_rows,D] (kv_len int32 [B]
     counts the step's tokens), which also give their positions, from pos0.
     Return q [B,Hq,L,D]."""
-    if stream is None:
-        r = (_fast or _marshal()).qk_rope(q, k, v, wq, wk, inv_freq, k_cache, v_cache, kv_len, eps, positions, pos0,
-                                          weight_offset, interleaved)
-        if r.__class__ is tuple:
-            return r[0]
-        if r is not None:
-            raise SwaError(r, "swa_attn_qk_rope_fwd")
     import torch
+
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return qk_rope_append(q, k, v, wq, wk, inv_freq, k_cache, v_cache, kv_len, eps, positions, pos0,
+                                  weight_offset, interleaved)
+    r = (_fast or _marshal()).qk_rope(q, k, v, wq, wk, inv_freq, k_cache, v_cache, kv_len, eps, positions, pos0,
+                                      weight_offset, interleaved)
+    if r.__class__ is tuple:
+        return r[0]
+    if r is not None:
+        raise SwaError(r, "swa_attn_qk_rope_fwd")
 
     B, L, Hq, D = q.shape
     q_out = torch.empty((B, Hq, L, D), dtype=q.dtype, device=q.device)
     swa_attn_qk_rope_fwd(q, k, v, wq, wk, inv_freq, q_out, k_cache, v_cache, eps, positions, kv_len, pos0,
-                         weight_offset, interleaved, stream)
+                         weight_offset, interleaved)
     return q_out
 
 
@@ -682,8 +700,8 @@ def _run_rope_bwd(dims, q, k, wq, wk, inv_freq, dq, dk, dv, outs, toks, dwq, dwk
     rc = load().swa_attn_qk_rope_bwd(q.data_ptr(), _addr(k), q_tok, k_tok, _addr(wq), _addr(wk), _addr(inv_freq),
                                      _addr(positions), dq.data_ptr(), None if k is None else dk.data_ptr(), _addr(dv),
                                      *outs, *toks, _addr(dwq), _addr(dwk), B, Hq, Hkv, L, D, rot,
-                                     1 if interleaved else 0, int(pos0), float(eps), float(weight_offset), _addr(ws),
-                                     nbytes, _stream_ptr(stream))
+                                     1 if interleaved else 0, _int32("pos0", pos0), float(eps), float(weight_offset),
+                                     _addr(ws), nbytes, _stream_ptr(stream))
     if rc:
         raise SwaError(rc, "swa_attn_qk_rope_bwd")
 
@@ -718,14 +736,18 @@ def qk_rope_backward(q, k, wq, wk, inv_freq, dq, dk, dv, eps: float, positions=N
     the fused projection output (q, k and v heads in that order; the k or v
     part is left out with k or dv None), dwq and dwk fp32 [D] (None for a
     None weight)."""
-    if stream is None:
-        r = (_fast or _marshal()).qk_rope_backward(q, k, wq, wk, inv_freq, dq, dk, dv, eps, positions, pos0,
-                                                   weight_offset, interleaved)
-        if r.__class__ is tuple:
-            return r
-        if r is not None:
-            raise SwaError(r, "swa_attn_qk_rope_bwd")
     import torch
+
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return qk_rope_backward(q, k, wq, wk, inv_freq, dq, dk, dv, eps, positions, pos0, weight_offset,
+                                    interleaved)
+    r = (_fast or _marshal()).qk_rope_backward(q, k, wq, wk, inv_freq, dq, dk, dv, eps, positions, pos0,
+                                               weight_offset, interleaved)
+    if r.__class__ is tuple:
+        return r
+    if r is not None:
+        raise SwaError(r, "swa_attn_qk_rope_bwd")
 
     dims = _check_rope_bwd(q, k, wq, wk, inv_freq, dq, dk, dv, positions)
     _, B, L, D, _, Hq, Hkv, _, _ = dims
@@ -740,7 +762,7 @@ def qk_rope_backward(q, k, wq, wk, inv_freq, dq, dk, dv, eps: float, positions=N
     at, row = d.data_ptr(), 2 * D  # bytes of a head's row
     outs = (at, at + Hq * row if Hk else None, at + (Hq + Hk) * row if Hv else None)
     _run_rope_bwd(dims, q, k, wq, wk, inv_freq, dq, dk, dv, outs, (H * D,) * 3, dwq, dwk, eps, positions, pos0,
-                  weight_offset, interleaved, ws, nbytes, stream)
+                  weight_offset, interleaved, ws, nbytes, None)
     return d, dwq, dwk
 
 

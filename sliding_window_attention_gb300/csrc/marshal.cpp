@@ -62,6 +62,14 @@ float real(PyObject* o) {
   }
   return (float)v;
 }
+int truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) {
+    PyErr_Clear();
+    throw NotThisWay{};
+  }
+  return v;
+}
 int dim32(int64_t v) {
   if (v != (int)v) throw NotThisWay{};
   return (int)v;
@@ -111,6 +119,17 @@ PyObject* tuple(std::initializer_list<at::Tensor> ts) {
   return r;
 }
 
+// Other threads may run Python while this one allocates and launches: a full
+// launch queue makes it wait, and what the queue waits for may need Python.
+template <typename F>
+int unlocked(F&& f) {
+  struct NoGil {
+    PyThreadState* state = PyEval_SaveThread();
+    ~NoGil() { PyEval_RestoreThread(state); }
+  } no_gil;
+  return f();
+}
+
 // Runs f with n arguments; no C++ exception leaves.
 template <typename F>
 PyObject* call(Py_ssize_t n, Py_ssize_t want, F&& f) {
@@ -147,12 +166,16 @@ PyObject* forward_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
     expect(len, at::kInt, {B}, dev);
     expect(sinks, at::kFloat, {Hq}, dev);
     const size_t bytes = g_shared_ws(B, Hq, Hkv, Lq, P, rows, D, window);
-    at::Tensor o = empty(q->sizes(), q, at::kBFloat16), lse = empty({B, Hq, Lq}, q, at::kFloat);
-    at::Tensor ws = empty({(int64_t)bytes}, q, at::kByte);
-    const int rc = g_shared(ptr<swa_bf16>(q), ptr<swa_bf16>(kp), ptr<swa_bf16>(vp), ptr<swa_bf16>(ko), ptr<swa_bf16>(vo),
-                            ptr<int32_t>(len), ptr<float>(sinks), ptr<swa_bf16>(&o), ptr<float>(&lse), B, Hq, Hkv, Lq, P,
-                            prefix_rows, rows, D, window, scale, ws.data_ptr(), bytes,
-                            c10::cuda::getCurrentCUDAStream(dev).stream());
+    at::Tensor o, lse;
+    const int rc = unlocked([&] {
+      o = empty(q->sizes(), q, at::kBFloat16);
+      lse = empty({B, Hq, Lq}, q, at::kFloat);
+      at::Tensor ws = empty({(int64_t)bytes}, q, at::kByte);
+      return g_shared(ptr<swa_bf16>(q), ptr<swa_bf16>(kp), ptr<swa_bf16>(vp), ptr<swa_bf16>(ko), ptr<swa_bf16>(vo),
+                      ptr<int32_t>(len), ptr<float>(sinks), ptr<swa_bf16>(&o), ptr<float>(&lse), B, Hq, Hkv, Lq, P,
+                      prefix_rows, rows, D, window, scale, ws.data_ptr(), bytes,
+                      c10::cuda::getCurrentCUDAStream(dev).stream());
+    });
     return rc ? PyLong_FromLong(rc) : tuple({o, lse});
   });
 }
@@ -209,18 +232,20 @@ PyObject* qk_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (r.k) expect(kc, at::kBFloat16, {r.B, Hkv, rows, r.D}, r.dev);
       if (v) expect(vc, at::kBFloat16, {r.B, Hkv, rows, r.D}, r.dev);
       expect(len, at::kInt, {r.B}, r.dev);
-    } else {
-      if (r.k) k_out = empty({r.B, Hkv, r.L, r.D}, r.q, at::kBFloat16);
-      if (v) v_out = empty({r.B, Hkv, r.L, r.D}, r.q, at::kBFloat16);
     }
-    q_out = empty({r.B, r.Hq, r.L, r.D}, r.q, at::kBFloat16);
-    swa_bf16* ko = r.k ? (len ? ptr<swa_bf16>(kc) : ptr<swa_bf16>(&k_out)) : nullptr;
-    swa_bf16* vo = v ? (len ? ptr<swa_bf16>(vc) : ptr<swa_bf16>(&v_out)) : nullptr;
-    const int rc = g_rope(ptr<swa_bf16>(r.q), ptr<swa_bf16>(r.k), ptr<swa_bf16>(v), r.q_tok, r.k_tok, v_tok,
-                          ptr<float>(r.wq), ptr<float>(r.wk), ptr<double>(r.freq), ptr<int32_t>(r.pos),
-                          ptr<int32_t>(len), ptr<swa_bf16>(&q_out), ko, vo, r.B, r.Hq, Hkv, r.L, r.D, rows, r.rot,
-                          PyObject_IsTrue(a[13]), int32(a[11]), real(a[9]), real(a[12]),
-                          c10::cuda::getCurrentCUDAStream(r.dev).stream());
+    const int interleaved = truth(a[13]), pos0 = int32(a[11]);
+    const float eps = real(a[9]), off = real(a[12]);
+    const int rc = unlocked([&] {
+      if (!len && r.k) k_out = empty({r.B, Hkv, r.L, r.D}, r.q, at::kBFloat16);
+      if (!len && v) v_out = empty({r.B, Hkv, r.L, r.D}, r.q, at::kBFloat16);
+      q_out = empty({r.B, r.Hq, r.L, r.D}, r.q, at::kBFloat16);
+      swa_bf16* ko = r.k ? ptr<swa_bf16>(len ? kc : &k_out) : nullptr;
+      swa_bf16* vo = v ? ptr<swa_bf16>(len ? vc : &v_out) : nullptr;
+      return g_rope(ptr<swa_bf16>(r.q), ptr<swa_bf16>(r.k), ptr<swa_bf16>(v), r.q_tok, r.k_tok, v_tok,
+                    ptr<float>(r.wq), ptr<float>(r.wk), ptr<double>(r.freq), ptr<int32_t>(r.pos), ptr<int32_t>(len),
+                    ptr<swa_bf16>(&q_out), ko, vo, r.B, r.Hq, Hkv, r.L, r.D, rows, r.rot, interleaved, pos0, eps, off,
+                    c10::cuda::getCurrentCUDAStream(r.dev).stream());
+    });
     return rc ? PyLong_FromLong(rc) : tuple({q_out, k_out, v_out});
   });
 }
@@ -237,20 +262,24 @@ PyObject* qk_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     expect(dk, at::kFloat, {r.B, Hkv, r.L, r.D}, r.dev);
     expect(dv, at::kFloat, {r.B, Hkv, r.L, r.D}, r.dev);
     const int Hk = r.k ? Hkv : 0, H = r.Hq + Hk + (dv ? Hkv : 0);
-    at::Tensor d = empty({r.B, r.L, H, r.D}, r.q, at::kBFloat16), dwq, dwk;
-    if (r.wq) dwq = empty({r.D}, r.q, at::kFloat);
-    if (r.wk && r.k) dwk = empty({r.D}, r.q, at::kFloat);
+    const int interleaved = truth(a[12]), pos0 = int32(a[10]);
+    const float eps = real(a[8]), off = real(a[11]);
     const size_t bytes = g_rope_bwd_ws(r.B, r.L, r.D);
-    at::Tensor ws = empty({(int64_t)bytes}, r.q, at::kByte);
-    swa_bf16* out = ptr<swa_bf16>(&d);
     const long long tok = (long long)H * r.D;
-    const int rc = g_rope_bwd(
-        ptr<swa_bf16>(r.q), ptr<swa_bf16>(r.k), r.q_tok, r.k_tok, ptr<float>(r.wq), ptr<float>(r.wk),
-        ptr<double>(r.freq), ptr<int32_t>(r.pos), ptr<float>(dq), ptr<float>(dk), ptr<float>(dv), out,
-        Hk ? out + (size_t)r.Hq * r.D : nullptr, dv ? out + (size_t)(r.Hq + Hk) * r.D : nullptr, tok, tok, tok,
-        dwq.defined() ? ptr<float>(&dwq) : nullptr, dwk.defined() ? ptr<float>(&dwk) : nullptr, r.B, r.Hq, Hkv, r.L,
-        r.D, r.rot, PyObject_IsTrue(a[12]), int32(a[10]), real(a[8]), real(a[11]), ws.data_ptr(), bytes,
-        c10::cuda::getCurrentCUDAStream(r.dev).stream());
+    at::Tensor d, dwq, dwk;
+    const int rc = unlocked([&] {
+      d = empty({r.B, r.L, H, r.D}, r.q, at::kBFloat16);
+      if (r.wq) dwq = empty({r.D}, r.q, at::kFloat);
+      if (r.wk && r.k) dwk = empty({r.D}, r.q, at::kFloat);
+      at::Tensor ws = empty({(int64_t)bytes}, r.q, at::kByte);
+      swa_bf16* out = ptr<swa_bf16>(&d);
+      return g_rope_bwd(ptr<swa_bf16>(r.q), ptr<swa_bf16>(r.k), r.q_tok, r.k_tok, ptr<float>(r.wq), ptr<float>(r.wk),
+                        ptr<double>(r.freq), ptr<int32_t>(r.pos), ptr<float>(dq), ptr<float>(dk), ptr<float>(dv), out,
+                        Hk ? out + (size_t)r.Hq * r.D : nullptr, dv ? out + (size_t)(r.Hq + Hk) * r.D : nullptr, tok,
+                        tok, tok, dwq.defined() ? ptr<float>(&dwq) : nullptr, dwk.defined() ? ptr<float>(&dwk) : nullptr,
+                        r.B, r.Hq, Hkv, r.L, r.D, r.rot, interleaved, pos0, eps, off, ws.data_ptr(), bytes,
+                        c10::cuda::getCurrentCUDAStream(r.dev).stream());
+    });
     return rc ? PyLong_FromLong(rc) : tuple({d, dwq, dwk});
   });
 }

@@ -555,7 +555,7 @@ static int check_rope(int B, int Hq, int Hkv, int L, int D, int rot_dim, float e
   if (rot_dim < 0 || rot_dim > D || rot_dim % 16 != 0 || !isfinite(eps) || !(eps > 0.f) || !isfinite(weight_offset))
     return SWA_ERR_BAD_ROPE;
   if (rot_dim > 0 && !inv_freq) return SWA_ERR_NULL_POINTER;
-  if ((double)B * L * (Hq + 2.0 * Hkv) > 2.0e9 || (double)B * L * ((double)Hq + 2.0 * Hkv) * D > 9.0e15) return SWA_ERR_TOO_LARGE;
+  if ((double)B * L * (Hq + 2.0 * Hkv) > 2.0e9) return SWA_ERR_TOO_LARGE;
   return SWA_OK;
 }
 static bool stride_ok(long long stride, int heads, int D) { return stride % 8 == 0 && stride >= (long long)heads * D; }
@@ -637,6 +637,7 @@ int swa_attn_qk_rope_bwd(const swa_bf16* q, const swa_bf16* k, long long q_strid
       !aligned(dwq, 4) || !aligned(dwk, 4) || !aligned(inv_freq, 8) || !aligned(positions, 4) ||
       !aligned(workspace, 256))
     return SWA_ERR_MISALIGNED;
+  if ((double)B * ((L + 7LL) / 8 * 8) > 2.0e9) return SWA_ERR_TOO_LARGE;  // tokens in groups of 8 of one batch entry
   if (!workspace || workspace_bytes < swa_attn_qk_rope_bwd_workspace_bytes(B, L, D)) return SWA_ERR_WORKSPACE;
   if ((rc = check_device())) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

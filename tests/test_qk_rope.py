@@ -345,6 +345,37 @@ def test_side_stream_and_graph():
 
 
 @pytest.mark.gpu
+def test_offsets_beyond_32_bits():
+    """More than 2^32 bytes and 2^31 elements on both sides: the last tokens' rows, and rows far inside a cache."""
+    import sliding_window_attention_gb300 as swa
+
+    H, D, L = 4, 512, (1 << 31) // (4 * 512) + 1003
+    g = torch.Generator().manual_seed(2)
+    x = torch.empty((1, L, H, D), dtype=BF, device="cuda")
+    x[:, -9:] = torch.randn((9, H, D), generator=g).to(BF)
+    f = freqs(64)
+    tail = torch.arange(L - 9, L)[None]
+    y = swa.qk_rope(x, None, None, None, None, f.cuda(), EPS)[0]
+    check_rows("q", y[:, :, -9:], *forward_ref(x[:, -9:].cpu(), None, 0.0, tail, f, False))
+    dy = torch.zeros((1, H, L, D), dtype=torch.float32, device="cuda")
+    dy[:, :, -9:] = torch.randn((H, 9, D), generator=g)
+    d, _, _ = swa.qk_rope_backward(x, None, None, None, f.cuda(), dy, None, None, EPS)
+    xr, gr = x[:, -9:].cpu().double(), turn(dy[:, :, -9:].cpu().double().transpose(1, 2), tail, f, False, -1.0)
+    r = 1 / (xr.square().mean(-1, keepdim=True) + EPS).sqrt()
+    n = xr * r
+    size = pair_size(dy[:, :, -9:].cpu().double().transpose(1, 2), 64, False)
+    ref = r * (gr - n * (gr * n).mean(-1, keepdim=True))
+    check_rows("dq", d[:, -9:], ref, r * (size + n.abs() * (size * n.abs()).mean(-1, keepdim=True)))
+    del d, dy
+    k = x[:, -2:, :1].contiguous()
+    kc = y.view(1, 1, H * L, D)  # a cache of 2^31 elements and more
+    at = H * L - 5
+    swa.qk_rope_append(x[:, -2:].contiguous(), k, k, None, None, f.cuda(), kc, kc.clone(),
+                       torch.tensor([at], dtype=torch.int32, device="cuda"), EPS)
+    check_rows("k", kc[:, :, at - 2:at], *forward_ref(k.cpu(), None, 0.0, torch.tensor([[at - 2, at - 1]]), f, False))
+
+
+@pytest.mark.gpu
 def test_training_chain_matches_64_bits():
     """Projection output -> rotation -> shared-prefix attention -> its backward -> rotation's backward,
     against 64-bit autograd of the whole; the attention's bar (1e-2 in relative Frobenius norm) covers the
@@ -389,8 +420,8 @@ def test_training_chain_matches_64_bits():
 @pytest.mark.gpu
 @pytest.mark.parametrize("has_k,has_v", [(True, True), (True, False), (False, True), (False, False)])
 def test_both_marshalling_paths_give_the_same(has_k, has_v):
-    """A call on the current stream is marshalled in C++, one with a stream of its own (or with numpy scalars) in
-    Python: equal bits, equal outputs left out."""
+    """A call with numpy scalars is marshalled in Python, others in C++; a call with a stream runs there: equal
+    bits, equal outputs left out."""
     import numpy as np
 
     import sliding_window_attention_gb300 as swa
@@ -401,24 +432,26 @@ def test_both_marshalling_paths_give_the_same(has_k, has_v):
                             *(torch.randn((B, h, L, D), generator=g) for h in (Hq, Hkv, Hkv)))
     q, k, v = dev_rows((q, k, v), 8)
     k, v = k if has_k else None, v if has_v else None
-    s = torch.cuda.current_stream()
+    s = torch.cuda.Stream()
+    n = torch.tensor([5, 9, 7], dtype=torch.int32, device="cuda")
     for kw in (dict(pos0=7, weight_offset=0.5, interleaved=True), dict(), dict(positions=torch.arange(
             15, dtype=torch.int32, device="cuda").view(3, 5))):
-        calls = [swa.qk_rope(q, k, v, w, w, f, EPS, **kw, **x) for x in (dict(), dict(stream=s))]
-        if "pos0" in kw:
-            calls.append(swa.qk_rope(q, k, v, w, w, f, np.float64(EPS), **dict(kw, pos0=np.int64(7))))
-        kc = [torch.zeros((B, Hkv, 9, D), dtype=BF, device="cuda") for _ in range(4)]
-        n = torch.tensor([5, 9, 7], dtype=torch.int32, device="cuda")
+        kc = [torch.zeros((B, Hkv, 9, D), dtype=BF, device="cuda") for _ in range(6)]
+        torch.cuda.synchronize()
+        ways = (kw, dict(kw, stream=s), dict(kw, pos0=np.int64(kw.get("pos0", 0))))
+        calls = [swa.qk_rope(q, k, v, w, w, f, EPS, **x) for x in ways]
         appends = [swa.qk_rope_append(q, k, v, w, w, f, kc[2 * i] if has_k else None, kc[2 * i + 1] if has_v else None,
-                                      n, EPS, **kw, **x) for i, x in enumerate((dict(), dict(stream=s)))]
-        grads = [swa.qk_rope_backward(q, k, w, w, f, dq, dk if has_k else None, dv if has_v else None, EPS, **kw, **x)
-                 for x in (dict(), dict(stream=s))]
+                                      n, EPS, **x) for i, x in enumerate(ways)]
+        grads = [swa.qk_rope_backward(q, k, w, w, f, dq, dk if has_k else None, dv if has_v else None, EPS, **x)
+                 for x in ways]
         torch.cuda.synchronize()
         for outs in (calls, grads):
             for other in outs[1:]:
                 for a, b in zip(outs[0], other):
                     assert (a is None and b is None) or torch.equal(a, b)
-        assert torch.equal(*appends) and torch.equal(kc[0], kc[2]) and torch.equal(kc[1], kc[3])
+        for i in (1, 2):
+            assert torch.equal(appends[0], appends[i])
+            assert torch.equal(kc[0], kc[2 * i]) and torch.equal(kc[1], kc[2 * i + 1])
         assert (calls[0][1] is not None) == has_k and (calls[0][2] is not None) == has_v
 
 
@@ -464,6 +497,7 @@ def test_c_abi_refuses_bad_arguments():
     for name in ("q", "dq", "gq", "dk", "gk", "gv", "f", "k"):
         assert bwd(**{name: None}) == -1, name
     assert bwd(gks=8) == -17 and bwd(rot=24) == -17 and bwd(D=32) == -4 and bwd(L=0) == -2
+    assert bwd(B=2 ** 29, L=1) == -10  # 2^32 tokens once counted in groups of 8
     assert bwd(dq=0x7008) == -7 and bwd(ws=0x10010) == -7 and bwd(dwk=0xe001) == -7
     need = lib.swa_attn_qk_rope_bwd_workspace_bytes(1, 4, 64)
     assert need == 304 * 2 * 64 * 4 and bwd(wsb=need - 1) == -8 and bwd(ws=None) == -8
@@ -485,6 +519,8 @@ def test_binding_refuses_host_tensors():
 
 @pytest.mark.gpu
 def test_binding_refuses_wrong_layouts():
+    import numpy as np
+
     import sliding_window_attention_gb300 as swa
 
     (q, k, v), _ = fused(2, 4, 2, 1, 64, 1)
@@ -499,10 +535,18 @@ def test_binding_refuses_wrong_layouts():
         a = {**dict(q=q, k=k, v=v, wq=w, wk=w, f=f, positions=None), **bad}
         with pytest.raises(ValueError):
             swa.qk_rope(a["q"], a["k"], a["v"], a["wq"], a["wk"], a["f"], EPS, positions=a["positions"])
-    for kw in (dict(), dict(stream=torch.cuda.current_stream())):
+    for kw in (dict(), dict(pos0=np.int64(0))):
         with pytest.raises(swa.SwaError):
             swa.qk_rope(q, k, v, w, w, freqs(36).cuda(), EPS, **kw)  # rot_dim 72 > D
         with pytest.raises(swa.SwaError):
             swa.qk_rope(q, k, v, w, w, f, 0.0, **kw)
         with pytest.raises(ValueError):
             swa.qk_rope_append(q, k, v, w, w, f, None, None, torch.ones(2, dtype=torch.int32, device="cuda"), EPS, **kw)
+    for pos0 in (2 ** 31, -2 ** 31 - 1, 2 ** 80):
+        with pytest.raises(ValueError, match="pos0 does not fit"):
+            swa.qk_rope(q, k, v, w, w, f, EPS, pos0=pos0)
+        with pytest.raises(ValueError, match="pos0 does not fit"):
+            swa.qk_rope_backward(q, k, w, w, f, q.float().transpose(1, 2).contiguous(),
+                                 k.float().transpose(1, 2).contiguous(), None, EPS, pos0=pos0)
+    with pytest.raises(RuntimeError):  # a truth value that there is none of
+        swa.qk_rope(q, k, v, w, w, f, EPS, interleaved=torch.zeros(2))

@@ -182,6 +182,64 @@ def test_extreme_values():
 
 
 @pytest.mark.gpu
+def test_two_threads_on_two_streams():
+    """Calls of two threads at once, each on its own stream: each call's own bits."""
+    import threading
+
+    import sliding_window_attention_gb300 as swa
+
+    cases = []
+    for lens, shape in (([90, 1, 37], (8, 2, 1, 128, 300, 90)), ([130] * 20, (4, 2, 2, 64, 513, 200))):
+        a = make(len(lens), *shape, seed=5)
+        cases.append([a[n].cuda() for n in ("q", "kp", "vp", "ko", "vo")] + [torch.tensor(lens, dtype=torch.int32).cuda()])
+    alone = [swa.forward_shared(*x, 0, 0.2) for x in cases]
+    torch.cuda.synchronize()
+    got, streams = [[], []], [torch.cuda.Stream() for _ in cases]
+
+    def calls(i):
+        for _ in range(50):
+            got[i].append(swa.forward_shared(*cases[i], 0, 0.2, stream=streams[i]))
+
+    threads = [threading.Thread(target=calls, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for want, outs in zip(alone, got):
+        assert len(outs) == 50
+        for o, lse in outs:
+            assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.gpu
+def test_a_cache_beyond_32_bits():
+    """Caches of more than 2^32 bytes and 2^31 elements, against 64 bits on the GPU in parts."""
+    import sliding_window_attention_gb300 as swa
+
+    B, Hq, D, rows = 2, 2, 128, (1 << 30) // 128 + 777
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q = torch.randn((B, Hq, 1, D), device="cuda", generator=g).to(BF)
+    ko, vo = (torch.randn((B, 1, rows, D), device="cuda", generator=g, dtype=BF) for _ in range(2))
+    kp, vp = (torch.randn((1, 200, D), device="cuda", generator=g).to(BF) for _ in range(2))
+    lens = [rows, rows - 1000]
+    o, lse = swa.forward_shared(q, kp, vp, ko, vo, torch.tensor(lens, dtype=torch.int32, device="cuda"), 0, 0.3)
+    for b, n in enumerate(lens):
+        z, num, mag = (torch.zeros((Hq, c), dtype=torch.float64, device="cuda") for c in (1, D, D))
+        for i in range(0, n, 1 << 20):
+            e = torch.exp(q[b, :, 0].double() @ ko[b, 0, i:min(n, i + (1 << 20))].double().T * 0.3)
+            v = vo[b, 0, i:min(n, i + (1 << 20))].double()
+            z += e.sum(1, keepdim=True)
+            num += e @ v
+            mag += e @ v.abs()
+        e = torch.exp(q[b, :, 0].double() @ kp[0].double().T * 0.3)
+        z, num, mag = z + e.sum(1, keepdim=True), num + e @ vp[0].double(), mag + e @ vp[0].double().abs()
+        ref = num / z
+        assert ((o[b, :, 0].double() - ref).abs() <= (2.0 ** -8 + 2.0 ** -11) * mag / z + 2.0 ** -8 * ref.abs()).all()
+        assert ((lse[b, :, 0].double() - z[:, 0].log()).abs() <= 2.0 ** -12).all()
+
+
+@pytest.mark.gpu
 def test_empty_places_keep_their_rows():
     import sliding_window_attention_gb300 as swa
 
@@ -243,17 +301,20 @@ def test_repeats_streams_and_workspaces():
 @pytest.mark.gpu
 @pytest.mark.parametrize("sinks", [False, True])
 def test_both_marshalling_paths_give_the_same(sinks):
-    """On the current stream (marshalled in C++) and on a stream of the call's own (in Python): equal bits."""
+    """With numpy scalars (marshalled in Python), others (in C++), and on a stream of the call's own: equal bits."""
+    import numpy as np
+
     import sliding_window_attention_gb300 as swa
 
     a = {n: None if t is None else t.cuda() for n, t in make(3, 4, 2, 2, 128, 90, 20, 9, sinks, prefix_rows=100).items()}
     n = torch.tensor([20, 3, 11], dtype=torch.int32, device="cuda")
     x = (a["q"], a["kp"], a["vp"], a["ko"], a["vo"], n)
     for kw in (dict(), dict(prefix_len=90), dict(prefix_len=0)):
-        got = [swa.forward_shared(*x, 17, 0.1, sinks=a["sinks"], **kw, **s)
-               for s in (dict(), dict(stream=torch.cuda.current_stream()))]
+        got = [swa.forward_shared(*x, w, 0.1, sinks=a["sinks"], **kw, **s)
+               for w, s in ((17, dict()), (17, dict(stream=torch.cuda.Stream())), (np.int64(17), dict()))]
         torch.cuda.synchronize()
-        assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+        for o, lse in got[1:]:
+            assert torch.equal(got[0][0], o) and torch.equal(got[0][1], lse)
 
 
 @pytest.mark.gpu
@@ -362,3 +423,6 @@ def test_binding_refuses_wrong_tensors():
         swa.forward_shared(*ok.values(), 0, 0.1, sinks=torch.zeros(2, device="cuda"))
     with pytest.raises(swa.SwaError):
         swa.forward_shared(*ok.values(), 0, 0.1, prefix_len=11)
+    for kw in (dict(prefix_len=2 ** 32), dict(window=-2 ** 40)):
+        with pytest.raises(ValueError, match="does not fit 32 bits"):
+            swa.forward_shared(*ok.values(), **{**dict(window=0, scale=0.1), **kw})
