@@ -13,7 +13,8 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -101,8 +102,10 @@ T* ptr(const at::Tensor* t) {
   return t ? static_cast<T*>(t->data_ptr()) : nullptr;
 }
 at::Tensor empty(at::IntArrayRef shape, const at::Tensor* like, at::ScalarType type) {
-  return at::empty(shape, like->options().dtype(type).requires_grad(false));
+  return at::Tensor(at::detail::empty_cuda(shape, type, like->device(), std::nullopt));
 }
+// The call's scratch: freed on return, to be used again behind the call on its stream.
+c10::DataPtr scratch(size_t bytes) { return c10::cuda::CUDACachingAllocator::get()->allocate(bytes); }
 PyObject* wrap(const at::Tensor& t) { return t.defined() ? THPVariable_Wrap(t) : Py_NewRef(Py_None); }
 PyObject* tuple(std::initializer_list<at::Tensor> ts) {
   PyObject* r = PyTuple_New((Py_ssize_t)ts.size());
@@ -170,10 +173,10 @@ PyObject* forward_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int rc = unlocked([&] {
       o = empty(q->sizes(), q, at::kBFloat16);
       lse = empty({B, Hq, Lq}, q, at::kFloat);
-      at::Tensor ws = empty({(int64_t)bytes}, q, at::kByte);
+      const c10::DataPtr ws = scratch(bytes);
       return g_shared(ptr<swa_bf16>(q), ptr<swa_bf16>(kp), ptr<swa_bf16>(vp), ptr<swa_bf16>(ko), ptr<swa_bf16>(vo),
                       ptr<int32_t>(len), ptr<float>(sinks), ptr<swa_bf16>(&o), ptr<float>(&lse), B, Hq, Hkv, Lq, P,
-                      prefix_rows, rows, D, window, scale, ws.data_ptr(), bytes,
+                      prefix_rows, rows, D, window, scale, ws.get(), bytes,
                       c10::cuda::getCurrentCUDAStream(dev).stream());
     });
     return rc ? PyLong_FromLong(rc) : tuple({o, lse});
@@ -271,13 +274,13 @@ PyObject* qk_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
       d = empty({r.B, r.L, H, r.D}, r.q, at::kBFloat16);
       if (r.wq) dwq = empty({r.D}, r.q, at::kFloat);
       if (r.wk && r.k) dwk = empty({r.D}, r.q, at::kFloat);
-      at::Tensor ws = empty({(int64_t)bytes}, r.q, at::kByte);
+      const c10::DataPtr ws = scratch(bytes);
       swa_bf16* out = ptr<swa_bf16>(&d);
       return g_rope_bwd(ptr<swa_bf16>(r.q), ptr<swa_bf16>(r.k), r.q_tok, r.k_tok, ptr<float>(r.wq), ptr<float>(r.wk),
                         ptr<double>(r.freq), ptr<int32_t>(r.pos), ptr<float>(dq), ptr<float>(dk), ptr<float>(dv), out,
                         Hk ? out + (size_t)r.Hq * r.D : nullptr, dv ? out + (size_t)(r.Hq + Hk) * r.D : nullptr, tok,
                         tok, tok, dwq.defined() ? ptr<float>(&dwq) : nullptr, dwk.defined() ? ptr<float>(&dwk) : nullptr,
-                        r.B, r.Hq, Hkv, r.L, r.D, r.rot, interleaved, pos0, eps, off, ws.data_ptr(), bytes,
+                        r.B, r.Hq, Hkv, r.L, r.D, r.rot, interleaved, pos0, eps, off, ws.get(), bytes,
                         c10::cuda::getCurrentCUDAStream(r.dev).stream());
     });
     return rc ? PyLong_FromLong(rc) : tuple({d, dwq, dwk});
