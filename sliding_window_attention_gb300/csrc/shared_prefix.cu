@@ -59,9 +59,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 // when a score outgrows it by more than 2^32, which leaves 2^63 for the sum
 // over 2^31 keys and loses no bit, since their precision is relative.
 constexpr float kGrowLog2 = 32.0f;
-// plan words: {prefix tiles, splits of the prefix, -, -}, each CTA's first own
-// unit (and their number), then each request's first own tile
-constexpr int kPlanStart = 4, kPlanOff = kPlanStart + kSMs + 1;
+// plan words: prefix tiles, ranges of a prefix segment, the own runs (four
+// words), then from kPlanOff on each request's first own tile
+constexpr int kPlanOff = 8;
 
 struct SharedParams {
   SharedGeom g;
@@ -83,6 +83,20 @@ __device__ __forceinline__ int own_tiles(const SharedGeom& g, int len) {
   const int lo = g.W > 0 ? max(0, n - g.Lq - g.W + 1) : 0;
   return n > lo ? (n - lo + T - 1) / T : 0;
 }
+
+// The CTAs' runs of own units: `rich` CTAs with qa each, then the others with
+// qb each; the last CTA's ends with the units.
+struct OwnRuns {
+  int rich, qa, qb, units;
+  __device__ __forceinline__ int start(int c) const {
+    const long long u = c < rich ? (long long)c * qa : (long long)rich * qa + (long long)(c - rich) * qb;
+    return c >= kSMs || u > units ? units : (int)u;
+  }
+  __device__ __forceinline__ int owner(int u) const {  // of unit u < units
+    const long long r = (long long)rich * qa;
+    return u < r ? u / qa : min(rich + (int)(u - r) / qb, kSMs - 1);
+  }
+};
 
 // A place in a CTA's prefix pieces.  Piece p is key range s of kv head h for
 // row block blk, p = (h splits + s) nrb + blk; a CTA has every gridDim.x-th.
@@ -735,7 +749,8 @@ __global__ void __launch_bounds__(ShKernel<D, NP>::THREADS, 1)
 
   // ---- the split.  Prefix keys that some row sees start at key_lo (there are
   // none without a live request); tp tiles of nseg segments, in ns ranges each
-  const int ctas = gridDim.x, cta = blockIdx.x;
+  constexpr int ctas = kSMs;
+  const int cta = blockIdx.x;
   const int key_lo = mn == INT32_MAX ? g.P : (g.W > 0 ? min(g.P, max(0, g.P + mn - g.Lq - g.W + 1)) : 0);
   const int tp = (g.P - key_lo + T - 1) / T;
   const int nseg = tp > 0 ? g.Hkv * p.s.nrb : 0, hn = g.Hkv * p.s.nomb, own_units = tiles * hn;
@@ -764,18 +779,11 @@ __global__ void __launch_bounds__(ShKernel<D, NP>::THREADS, 1)
   const int pl = pieces ? (tp + ns - 1) / ns + 1 : 0, even = (own_units + pieces * pl + ctas - 1) / ctas;
   const int qa = max(0, even - rounds * pl);  // own units of a rich CTA, and of another
   const int qb = qa > 0 || rich == ctas ? even - (rounds - 1) * pl : (own_units + ctas - rich - 1) / (ctas - rich);
-  auto own_start = [&](int c) {
-    const long long u = c < rich ? (long long)c * qa : (long long)rich * qa + (long long)(c - rich) * qb;
-    return c >= ctas || u > own_units ? own_units : (int)u;
-  };
-  const int o0 = own_start(cta), o1 = own_start(cta + 1);
-  if (cta == 0) {  // for the merge
-    if (threadIdx.x == 0) {
-      p.plan[0] = tp;
-      p.plan[1] = ns;
-    }
-#pragma unroll 1
-    for (int c = threadIdx.x; c <= ctas; c += THR) p.plan[kPlanStart + c] = own_start(c);
+  const OwnRuns runs{rich, qa, qb, own_units};
+  const int o0 = runs.start(cta), o1 = runs.start(cta + 1);
+  if (cta == 0 && threadIdx.x == 0) {  // for the merge
+    *reinterpret_cast<int4*>(p.plan) = make_int4(tp, ns, rich, qa);
+    *reinterpret_cast<int4*>(p.plan + 4) = make_int4(qb, own_units, 0, 0);
   }
   // the request that own unit o0 belongs to; CTA 0 also writes every request's
   // first tile for the merge
@@ -854,118 +862,94 @@ __global__ void __launch_bounds__(ShKernel<D, NP>::THREADS, 1)
 }
 
 // Merge of one query row's partials: those of its prefix block's pieces, and
-// of its own cache, one for each CTA that had a part of the segment.  Rows without a key
-// get o = 0 and lse = -inf (or the sink's logit); rows of an empty place of
-// the batch are not written.
-template <int D>
-struct MergeCfg {
-  static constexpr int VEC = D >= 128 ? 4 : 2, THREADS = D / VEC;
-};
-constexpr int kMaxParts = kPieces + kSMs;
-
-template <int D>
-__global__ void __launch_bounds__(MergeCfg<D>::THREADS) shared_merge_kernel(const __grid_constant__ SharedParams p) {
-  constexpr int VEC = MergeCfg<D>::VEC, AHEAD = 8;
-  __shared__ float wts[kMaxParts];
-  __shared__ int owner[kSMs], n_own;  // the CTAs that have a part of the row's own segment
-  __shared__ float stat[2];
+// of its own cache, one for each CTA that had a part of the segment (they are
+// neighbours).  Rows without a key get o = 0 and lse = -inf (or the sink's
+// logit); rows of an empty place of the batch are not written.
+//
+// A row's partials are a few KB spread over L2, so the memory's latency is what
+// this takes: D / 4 threads read a partial, THREADS / (D / 4) partials are read
+// at once, with AHEAD loads a thread under way before the weights are known,
+// and every warp forms the weights by itself.  THREADS: 256 where that is at
+// most two CTAs an SM, else 128 (a call's time with 256 and 128: 256 rows of
+// some 40 partials, D = 128: 15.1 and 17.0 us; 1,024 rows of as many, D = 64:
+// 19.2 and 16.3; 2,048 rows of 11, D = 512: 122 and 119).
+template <int D, int THREADS>
+__global__ void __launch_bounds__(THREADS) shared_merge_kernel(const __grid_constant__ SharedParams p) {
+  constexpr int LANES = D / 4, GR = THREADS / LANES, AHEAD = 1024 / THREADS;
+  __shared__ float4 part[GR][LANES];
   const SharedGeom& g = p.g;
   const SharedSplit& s = p.s;
   const int row = blockIdx.x;  // (b Hkv + kv head) M + m
   const int bkv = row / g.M, m = row - bkv * g.M, b = bkv / g.Hkv, h = bkv - b * g.Hkv;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, grp = threadIdx.x / LANES, d = threadIdx.x % LANES;
   grid_launch_dependents();
-  grid_dependency_wait();
-  // the lengths and the plan, in one round of loads
-  const int len = p.own_len[b], tp = p.plan[0], ns = p.plan[1], off = p.plan[kPlanOff + b];
-  int start[(kSMs + 31) / 32 + 1];
-  if (threadIdx.x < 32) {
-#pragma unroll
-    for (int i = 0; i <= kSMs / 32; ++i) start[i] = 32 * i + lane <= kSMs ? p.plan[kPlanStart + 32 * i + lane] : INT32_MAX;
-  }
-  if (len < 0) return;
-  // the row's partials: np of its prefix block, ns pieces, then those of the
-  // CTAs whose own run meets its segment
-  const int np = tp > 0 ? ns : 0;
+  // the main grid lets this one start once it has waited for what wrote the lengths
+  const int len = __ldcg(p.own_len + b);
+  const float* sink = p.sinks ? p.sinks + h * g.G + m / g.Lq : nullptr;
+  const int nt = own_tiles(g, len), hn = g.Hkv * s.nomb, in = h * s.nomb + m / kOwnRows;
   const int rb = s.nmb > 1 ? b * s.nmb + m / s.np : b / s.nb;
   const int q = s.nmb > 1 ? m % s.np : b % s.nb * g.M + m;
-  const size_t p_at = ((size_t)h * ns * s.nrb + rb) * s.prow + q, p_step = (size_t)s.nrb * s.prow;
-  const int in = h * s.nomb + m / kOwnRows, nt = own_tiles(g, len), hn = g.Hkv * s.nomb;
-  const int u0 = off * hn + in * nt, u1 = u0 + nt;
-  const size_t o_at = (size_t)(b * hn + in) * s.orow + m % kOwnRows;
-  if (threadIdx.x < 32) {
-    int no = 0;
-    start[kSMs / 32 + 1] = INT32_MAX;
-#pragma unroll
-    for (int i = 0; i <= kSMs / 32; ++i) {
-      // lane 31's next start is lane 0's of the next group
-      int next = __shfl_down_sync(0xffffffffu, start[i], 1);
-      const int wrap = __shfl_sync(0xffffffffu, start[i + 1], 0);
-      if (lane == 31) next = wrap;
-      const bool hit = 32 * i + lane < kSMs && max(start[i], u0) < min(next, u1);
-      const unsigned bits = __ballot_sync(0xffffffffu, hit);
-      if (hit) owner[no + __popc(bits & ((1u << lane) - 1))] = 32 * i + lane;
-      no += __popc(bits);
-    }
-    if (lane == 0) n_own = no;
-  }
-  __syncthreads();
-  const int n = np + n_own;
+  const size_t o_seg = (size_t)(b * hn + in) * s.orow + m % kOwnRows, p_step = (size_t)s.nrb * s.prow;
+  grid_dependency_wait();
+  if (len < 0) return;
+  const int4 pl = *reinterpret_cast<const int4*>(p.plan), pr = *reinterpret_cast<const int4*>(p.plan + 4);
+  const int off = p.plan[kPlanOff + b];
+  // the row's partials: np of its prefix block, ns pieces, then those of the
+  // CTAs whose own run meets its segment
+  const int np = pl.x > 0 ? pl.y : 0;
+  const OwnRuns runs{pl.z, pl.w, pr.x, pr.y};
+  const int u0 = off * hn + in * nt, c0 = nt > 0 ? runs.owner(u0) : 0, n = np + (nt > 0 ? runs.owner(u0 + nt - 1) - c0 + 1 : 0);
+  const size_t p_at = ((size_t)h * pl.y * s.nrb + rb) * s.prow + q, o_at = o_seg + (size_t)c0 * s.orow;
   auto row_of = [&](int i) {  // partial i: its row among the prefix's or the own partials
-    return i < np ? p_at + i * p_step : o_at + (size_t)owner[i - np] * s.orow;
+    return i < np ? p_at + i * p_step : o_at + (size_t)(i - np) * s.orow;
   };
-  const int d = threadIdx.x * VEC;
-  auto load = [&](int i, float (&v)[VEC]) {
-    const float* src = (i < np ? p.pp_o : p.po_o) + row_of(i) * D + d;
-    if constexpr (VEC == 4) {
-      const float4 u = *reinterpret_cast<const float4*>(src);
-      v[0] = u.x;
-      v[1] = u.y;
-      v[2] = u.z;
-      v[3] = u.w;
-    } else {
-      const float2 u = *reinterpret_cast<const float2*>(src);
-      v[0] = u.x;
-      v[1] = u.y;
-    }
-  };
-  float ahead[AHEAD][VEC];  // the first partials' loads are under way while the weights form
+  auto ml_of = [&](int i) { return *reinterpret_cast<const float2*>((i < np ? p.pp_ml : p.po_ml) + row_of(i) * 2); };
+  auto o_of = [&](int i) { return *reinterpret_cast<const float4*>((i < np ? p.pp_o : p.po_o) + row_of(i) * D + 4 * d); };
+  // all first loads are under way before any is used
+  const float2 first = lane < n ? ml_of(lane) : make_float2(-INFINITY, 0.f);
+  float4 v[AHEAD];
+  float mi[AHEAD];
 #pragma unroll
   for (int i = 0; i < AHEAD; ++i) {
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) ahead[i][e] = 0.f;
-    if (i < n) load(i, ahead[i]);
-  }
-  if (threadIdx.x < 32) {
-    float mx = -INFINITY;
-#pragma unroll 1
-    for (int i = lane; i < n; i += 32) {
-      const float2 v = *reinterpret_cast<const float2*>((i < np ? p.pp_ml : p.po_ml) + row_of(i) * 2);
-      wts[i] = v.x;
-      mx = fmaxf(mx, v.x);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    float l = 0.f;
-#pragma unroll 1
-    for (int i = lane; i < n; i += 32) {
-      const float m2 = wts[i], li = (i < np ? p.pp_ml : p.po_ml)[row_of(i) * 2 + 1];
-      // a part without a visible key adds nothing (its l is 0; NaN scores leave
-      // no maximum either, and a NaN l)
-      const float w = m2 == -INFINITY ? 0.f : exp2f(m2 - mx);
-      wts[i] = w;
-      l += m2 == -INFINITY ? li : w * li;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if (lane == 0) {
-      stat[0] = mx;
-      stat[1] = l;
+    const int j = grp + GR * i;
+    if (j < n) {
+      v[i] = o_of(j);
+      mi[i] = ml_of(j).x;
     }
   }
+  // a part without a visible key adds nothing (its l is 0; NaN scores leave no
+  // maximum either, and a NaN l)
+  float mx = first.x;
+#pragma unroll 1
+  for (int i = lane + 32; i < n; i += 32) mx = fmaxf(mx, ml_of(i).x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  auto weight = [&](float x) { return x == -INFINITY ? 0.f : exp2f(x - mx); };
+  float l = first.x == -INFINITY ? first.y : weight(first.x) * first.y;
+#pragma unroll 1
+  for (int i = lane + 32; i < n; i += 32) {
+    const float2 t = ml_of(i);
+    l += t.x == -INFINITY ? t.y : weight(t.x) * t.y;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](float w, const float4& u) {
+    acc.x = fmaf(w, u.x, acc.x);
+    acc.y = fmaf(w, u.y, acc.y);
+    acc.z = fmaf(w, u.z, acc.z);
+    acc.w = fmaf(w, u.w, acc.w);
+  };
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i)
+    if (grp + GR * i < n) add(weight(mi[i]), v[i]);
+#pragma unroll 4
+  for (int j = grp + GR * AHEAD; j < n; j += GR) add(weight(ml_of(j).x), o_of(j));
+  part[grp][d] = acc;
   __syncthreads();
-  const float mx = stat[0], l = stat[1];
-  const float* sink = p.sinks ? p.sinks + h * g.G + m / g.Lq : nullptr;
+  if (grp > 0) return;
+#pragma unroll
+  for (int i = 1; i < GR; ++i) add(1.f, part[i][d]);
   float inv, lse;
   if (mx == -INFINITY && l == 0.f) {
     inv = 0.f;
@@ -975,25 +959,9 @@ __global__ void __launch_bounds__(MergeCfg<D>::THREADS) shared_merge_kernel(cons
     lse = (mx + log2f(l)) * kLn2;
     if (sink) inv = sink_finish(*sink, mx, l, &lse);
   }
-  float acc[VEC];
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
-#pragma unroll
-  for (int i = 0; i < AHEAD; ++i)
-    if (i < n)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) acc[e] = fmaf(wts[i], ahead[i][e], acc[e]);
-#pragma unroll 4
-  for (int i = AHEAD; i < n; ++i) {
-    float v[VEC];
-    load(i, v);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) acc[e] = fmaf(wts[i], v[e], acc[e]);
-  }
-  uint16_t* dst = p.o + (size_t)row * D + d;
-#pragma unroll
-  for (int e = 0; e < VEC; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
-  if (threadIdx.x == 0) p.lse[row] = lse;
+  *reinterpret_cast<uint2*>(p.o + (size_t)row * D + 4 * d) =
+      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  if (d == 0) p.lse[row] = lse;
 }
 
 struct SharedWs {
@@ -1056,7 +1024,9 @@ cudaError_t shared_d(const SharedGeom& g, const SharedArgs& a, void* ws, int* st
   if ((e = launch_dependent(kern, dim3(kSMs), dim3(K::THREADS), K::SMEM, st, tqp, tqo, tkp, tvp, tko, tvo, p)) !=
       cudaSuccess)
     return e;
-  return launch_dependent(shared_merge_kernel<D>, dim3((unsigned)(g.B * g.Hkv * g.M)), dim3(MergeCfg<D>::THREADS), 0, st, p);
+  const unsigned rows = (unsigned)(g.B * g.Hkv * g.M);
+  if (rows <= 2 * kSMs) return launch_dependent(shared_merge_kernel<D, 256>, dim3(rows), dim3(256), 0, st, p);
+  return launch_dependent(shared_merge_kernel<D, 128>, dim3(rows), dim3(128), 0, st, p);
 }
 
 template <int D>
