@@ -14,14 +14,25 @@
 // rows, packed from as many requests as fit, so the prefix is read once for
 // all of them), or with one request's own cache (up to 16 rows: the G * Lq
 // rows of a kv head).  One CTA per SM works first on pieces of the prefix,
-// then on a run of the requests' own tiles, sized so that all CTAs get the
-// same number of units however ragged the lengths are: every CTA sums the
-// device-side lengths itself, no host sees them, and no counter has to be
-// reset between calls.  The pieces of one key range with all its row blocks
-// are neighbouring CTAs' work at the same time, so a tile's second and later
-// reads find it in L2.  Each piece, and each CTA's share of an own segment,
-// leaves one partial (m, l, O) in a slot of its own; a second kernel merges a
-// row's partials.
+// then on a run of the requests' own tiles, so that all CTAs take the same
+// time however ragged the lengths are: every CTA sums the device-side lengths
+// itself, no host sees them, and no counter has to be reset between calls.
+// Pieces of one key range with all its row blocks are neighbouring CTAs' work
+// at the same time, so a tile's second and later reads find it in L2 (64
+// requests of 32 heads over 16,384 keys, D = 512: 139 MB from HBM and 127 us;
+// with pieces that drift apart 1.2 GB and 208 us).  Each piece, and each CTA's
+// share of an own segment, leaves one partial (m, l, O) in a slot of its own; a
+// second kernel merges a row's partials.
+//
+// Bounds, of 64 requests of 32 heads (4 of them kv) over 16,384 prefix keys and
+// up to 1,024 of their own, D = 512 (112 us): the prefix's tiles, 2.5 us each on
+// 128 of the CTAs, are bound by shared memory (a tile's operands are 393 KB of
+// MMA reads and 256 KB of TMA writes: 2.5 us at 128 bytes a clock); the own
+// caches by HBM (32 caches of up to 1,024 keys at D = 256: 6.0 TB/s).  At D <=
+// 128 a prefix tile is bound by the softmax's latency (1.2 us for 64 rows, 2.5
+// for 128), and a short call by what comes before and behind: lengths 0.5 us,
+// split 0.7, first tile 1.3, merge 1.8 (4 requests over 1,024 keys, D = 128: 7.9
+// us, of which 1.6 are tiles).
 //
 // Products are transposed, as in the decode kernel: S^T (128 keys x N rows) =
 // K_tile Q^T and O^T (D x N rows) += V_tile^T P^T, so the keys fill the MMA's
@@ -38,6 +49,8 @@
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "swa_internal.h"
 #include "tc_ptx.cuh"
@@ -71,6 +84,7 @@ struct SharedParams {
   uint16_t* o;         // bf16 [B, Hq, Lq, D]
   float* lse;          // [B, Hq, Lq]
   int* plan;
+  int most;            // ranges that a prefix segment is split into at most
   float *pp_ml, *pp_o;  // prefix partials: [piece][rows][2] and [piece][rows][D]
   float *po_ml, *po_o;  // own partials: [slot][rows]...
   int* status;
@@ -109,9 +123,11 @@ struct PrefixWalk {
   bool first;                // first tile of the piece
   __device__ __forceinline__ void begin(int piece) {
     slot = piece;
-    const int hs = slot / p->s.nrb;
-    blk = slot - hs * p->s.nrb;
-    h = hs / splits;
+    const int nrb = p->s.nrb, hs = nrb > 1 ? slot / nrb : slot;
+    blk = slot - hs * nrb;
+    // hs < 2^20 where there are splits (they make at most kPieces pieces), and a
+    // quotient's distance from the next is 1 / (2 splits) at least
+    h = splits > 1 ? (int)__fdividef(hs + 0.5f, (float)splits) : hs;
     const int s = hs - h * splits;
     t = s * tiles + min(s, extra);
     t1 = t + tiles + (s < extra ? 1 : 0);
@@ -150,6 +166,13 @@ struct OwnWalk {
   }
   __device__ __forceinline__ int key0() const { return n - T * (nt - t); }
   __device__ __forceinline__ bool last() const { return left == 1 || t == nt - 1; }
+  __device__ __forceinline__ int skip() {  // over the rest of the visit; its tiles
+    const int k = min(left, nt - t);
+    t += k - 1;
+    left -= k - 1;
+    next();
+    return k;
+  }
   __device__ __forceinline__ void next() {
     first = false;
     ++t;
@@ -169,57 +192,76 @@ struct OwnWalk {
   }
 };
 
-// Shared memory of one phase: N query rows a block (own caches: 16).
-template <int D, int N, bool OWN>
-struct ShCfg {
+// One phase's blocks of N query rows (own caches: 16).
+template <int D, int N>
+struct ShPhase {
+  static constexpr int NG = N > 16 ? 32 : 16;  // rows of a softmax warpgroup
+  static constexpr int QB = N * D * 2;         // a block of queries
+  static constexpr int PB = N * T * 2;         // P^T
+  // a softmax warpgroup's small arrays: [2][4][NG] exchanged maxima / sums, thresholds, references, rescale
+  // factors, row ranges, bounds and tags
+  static constexpr int RED = 0, THR = 2 * 4 * NG * 4, USE = THR + NG * 4, ALPHA = USE + NG * 4, RNG = ALPHA + NG * 4,
+                       BND = RNG + NG * 8, SMALL = BND + 64;
+};
+// The kernel with prefix blocks of N rows.  Shared memory: one ring of slots for
+// both phases, the prefix blocks' queries and P^T, and the own caches', which
+// take over the same bytes where these are large enough.
+template <int D, int N>
+struct ShKernel {
+  using A = ShPhase<D, N>;
+  using B = ShPhase<D, kOwnRows>;
   static constexpr int NCH = D / 64;             // 64-column chunks of a row
   static constexpr int CPS = NCH < 2 ? NCH : 2;  // chunks per ring slot
   static constexpr int SPT = NCH / CPS;          // slots per tile and tensor
   static constexpr int NDC = (D + 127) / 128;    // 128-column blocks of O^T
-  static constexpr int NG = N > 16 ? 32 : 16;    // rows of a softmax warpgroup
-  static constexpr int GROUPS = N / NG;
   static constexpr int SLOT = CPS * T * 128;
-  static constexpr int QB = N * D * 2;           // one block of queries
-  static constexpr int QD = OWN ? 2 : 1;         // blocks buffered (own segments are short)
-  static constexpr int PB = N * T * 2;           // P^T
-  // per warpgroup: [2][4][NG] exchanged maxima / sums, thresholds, references,
-  // rescale factors, row ranges, bounds and tags
-  static constexpr int SMALL = 2 * 4 * NG * 4 + 3 * NG * 4 + NG * 8 + 64;
+  static constexpr int GROUPS = N / A::NG;       // softmax warpgroups of the prefix; own segments take turns in two
+  // What work takes, in quarter microseconds: a prefix tile, an own tile, what a
+  // piece adds to its tiles, what an own run adds
+  static constexpr int WP = N == 128 ? (D == 256 ? 12 : D == 128 ? 10 : 9)
+                                     : (D == 512 ? 11 : D == 256 ? (N == 64 ? 7 : 9) : (N == 64 ? 5 : 4));
+  static constexpr int WO = D == 512 ? 11 : D == 256 ? (N == 128 ? 12 : 7) : D == 128 ? (N == 128 ? 9 : 4) : (N == 128 ? 5 : 4);
+  static constexpr int VP = D == 512 ? 14 : 6, WV = 4;
+  static constexpr int THREADS = 64 + 128 * (GROUPS > 2 ? GROUPS : 2);
+  // few rows: at most 128 registers a thread, so that merge CTAs are placed
+  // beside this one's while they run (with more rows it would spill)
+  static constexpr int BOUND = N == 16 ? 512 : THREADS;
+  static constexpr bool SHARE_Q = A::QB >= 2 * B::QB, SHARE_P = A::PB >= 2 * B::PB;
   // at head dim 64 the second product's 128 rows read one chunk past a slot
   // (rows 64-127 of O^T, never used): the last slot's must stay in bounds
   static constexpr int TAIL = D == 64 ? T * 128 : 0;
-  static constexpr int FIXED = QB * QD + PB + GROUPS * SMALL + TAIL;
-  static constexpr int FIT = (kSmemMax - 1024 - 1024 - FIXED) / SLOT;
+  static constexpr int FIXED = A::QB + A::PB + (SHARE_Q ? 0 : 2 * B::QB) + (SHARE_P ? 0 : 2 * B::PB) +
+                               GROUPS * A::SMALL + 2 * B::SMALL;
+  static constexpr int FIT = (kSmemMax - 1024 - 1024 - FIXED - TAIL) / SLOT;
+  static constexpr int NSLOT = FIT > 8 ? 8 : FIT;
   // own caches stream from HBM on every SM: 128 KB in flight on each saturate
   // it, and more only lengthen the queues (4 slots of 32 KB against 6: 54.4 and
   // 55.8 us at 32 caches of up to 1,024 keys, D = 256; 3 slots: 56.0, and at
   // D = 512, where a tile has 8, 140 us against 118)
-  static constexpr int MOST = OWN && CPS == 2 ? 4 : 8;
-  static constexpr int NSLOT = FIT > MOST ? MOST : FIT;
-  static constexpr int OFF_Q = NSLOT * SLOT;
-  static constexpr int OFF_P = OFF_Q + QD * QB;
-  static constexpr int OFF_SMALL = OFF_P + PB;
-  static constexpr int BYTES = OFF_SMALL + GROUPS * SMALL + TAIL;
-  // within a warpgroup's small arrays
-  static constexpr int RED = 0, THR = 2 * 4 * NG * 4, USE = THR + NG * 4, ALPHA = USE + NG * 4, RNG = ALPHA + NG * 4,
-                       BND = RNG + NG * 8;
-  static constexpr uint32_t S_COL = 0, O_COL = 2 * N;  // TMEM columns
-  static constexpr uint32_t COLS = O_COL + NDC * N;
+  static constexpr int OWN_AHEAD = CPS == 2 && NSLOT > 4 ? 4 : NSLOT;
+  static constexpr int OFF_Q = NSLOT * SLOT, OFF_P = OFF_Q + A::QB, END_P = OFF_P + A::PB;
+  static constexpr int OFF_QO = SHARE_Q ? OFF_Q : END_P;
+  static constexpr int END_QO = SHARE_Q ? END_P : END_P + 2 * B::QB;
+  static constexpr int OFF_PO = SHARE_P ? OFF_P : END_QO;
+  static constexpr int OFF_SMALL = SHARE_P ? END_QO : END_QO + 2 * B::PB;
+  static constexpr int OFF_SMALL_O = OFF_SMALL + GROUPS * A::SMALL;
+  static constexpr int BODY = OFF_SMALL_O + 2 * B::SMALL;
+  static constexpr int OFF_BAR = ((BODY > OFF_Q + TAIL ? BODY : OFF_Q + TAIL) + 15) / 16 * 16;
+  static constexpr int OFF_ABORT = OFF_BAR + 48 * 8 + 8;  // behind the barriers and the TMEM address
+  static constexpr size_t SMEM = (size_t)OFF_BAR + 512 + 1024;
+  // TMEM columns: S^T twice and O^T of the prefix.  The own segments' O^T (one
+  // for each warpgroup) and S^T lie where the prefix's scores were, which have
+  // all been read before the first own product is issued, or behind.
+  static constexpr uint32_t S_COL = 0, O_COL = 2 * N, A_END = O_COL + NDC * N;
+  static constexpr bool O_IN_S = 2 * N >= 32 * NDC, S_IN_S = 2 * N >= 32 * NDC + 32;
+  static constexpr uint32_t O_OWN = O_IN_S ? 0 : A_END, S_OWN = S_IN_S ? 32 * NDC : (O_IN_S ? A_END : A_END + 32 * NDC);
+  static constexpr uint32_t COLS = S_IN_S ? A_END : S_OWN + 32;
+  static constexpr uint32_t TCOLS = COLS <= 128 ? 128 : (COLS <= 256 ? 256 : 512);
   static_assert(NSLOT >= 2 && NSLOT <= 8, "ring slots (the barriers hold 8)");
   static_assert(COLS <= 512, "TMEM columns");
   static_assert(GROUPS <= 4, "softmax warpgroups");
-};
-template <int D, int NP>
-struct ShKernel {
-  using A = ShCfg<D, NP, false>;
-  using B = ShCfg<D, kOwnRows, true>;
-  static constexpr int THREADS = 64 + 128 * A::GROUPS;
-  static constexpr int BODY = (A::BYTES > B::BYTES ? A::BYTES : B::BYTES);
-  static constexpr int OFF_BAR = (BODY + 15) / 16 * 16;  // barriers of the two phases, 384 bytes each
-  static constexpr size_t SMEM = (size_t)OFF_BAR + 768 + 1024;
-  static constexpr uint32_t COLS = A::COLS > B::COLS ? A::COLS : B::COLS;
-  static constexpr uint32_t TCOLS = COLS <= 128 ? 128 : (COLS <= 256 ? 256 : 512);
   static_assert(SMEM + 512 <= (size_t)kSmemMax, "shared memory");
+  static_assert(OFF_QO % 1024 == 0 && OFF_PO % 1024 == 0 && OFF_P % 1024 == 0, "swizzled tiles");
 };
 
 // Column reduction over the warp's 32 lanes by halving: each step keeps one
@@ -266,65 +308,87 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
   return false;
 }
 
-// A phase's barriers (its own, so that none has to be set up twice).
+// Barriers.  The ring's are shared by both phases; each has its own for the
+// rest, the own segments' one set a warpgroup.
 struct Bars {
   uint64_t* b;
-  __device__ __forceinline__ uint64_t* slot_full(int i) const { return b + i; }        // [8]
-  __device__ __forceinline__ uint64_t* slot_empty(int i) const { return b + 8 + i; }   // [8]
-  __device__ __forceinline__ uint64_t* q_full(int i) const { return b + 16 + i; }      // [2] a visit's queries
-  __device__ __forceinline__ uint64_t* q_empty(int i) const { return b + 18 + i; }     // [2]
-  __device__ __forceinline__ uint64_t* s_full(int i) const { return b + 20 + i; }      // [2] S^T(n) in TMEM
-  __device__ __forceinline__ uint64_t* p_full() const { return b + 22; }  // P^T(n) written (and O^T rescaled)
-  __device__ __forceinline__ uint64_t* o_done() const { return b + 23; }  // PV(n) finished
-  __device__ __forceinline__ uint64_t* drain() const { return b + 24; }
-  __device__ __forceinline__ uint64_t* xch(int i) const { return b + 25 + i; }  // [4] a softmax warpgroup's exchanges
-  static constexpr int kCount = 29;
+  __device__ __forceinline__ uint64_t* slot_full(int i) const { return b + i; }       // [8]
+  __device__ __forceinline__ uint64_t* slot_empty(int i) const { return b + 8 + i; }  // [8]
+  __device__ __forceinline__ uint64_t* drain() const { return b + 16; }
+  template <bool OWN>
+  __device__ __forceinline__ uint64_t* q_full(int i) const { return b + (OWN ? 27 : 17) + i; }  // a visit's queries (own: [2])
+  template <bool OWN>
+  __device__ __forceinline__ uint64_t* q_empty(int i) const { return b + (OWN ? 29 : 18) + i; }
+  template <bool OWN>
+  __device__ __forceinline__ uint64_t* s_full(int g) const { return b + (OWN ? 31 + 2 * g : 19); }  // [2] S^T in TMEM
+  template <bool OWN>
+  __device__ __forceinline__ uint64_t* p_full(int g) const { return b + (OWN ? 35 + g : 21); }  // P^T written (O^T rescaled)
+  template <bool OWN>
+  __device__ __forceinline__ uint64_t* o_done(int g) const { return b + (OWN ? 37 + g : 22); }  // PV finished
+  template <bool OWN>
+  __device__ __forceinline__ uint64_t* xch(int g) const { return b + (OWN ? 39 : 23) + g; }  // a warpgroup's exchanges
+  static constexpr int kCount = 41;
   // arrivals that complete a phase of barrier i
   static __device__ __forceinline__ int arrivals(int i, int groups) {
-    return i == 22 ? 4 * groups : (i >= 25 ? 4 : 1);
+    return i == 21 ? 4 * groups : ((i >= 23 && i < 27) || i == 35 || i == 36 || i >= 39 ? 4 : 1);
   }
 };
 
-// What a softmax warpgroup works with.
+// A softmax warpgroup's place in a phase.
+template <int D, int NP, bool OWN>
 struct SoftCtx {
+  using K = ShKernel<D, NP>;
+  using C = typename std::conditional<OWN, typename K::B, typename K::A>::type;
   unsigned char* base;
-  unsigned char* small;  // this warpgroup's small arrays
-  Bars bar;
-  volatile int* abort;
-  uint32_t tmem;
+  uint32_t at;   // TMEM: this thread's lane
   int group;
-  int n;   // tiles done in this phase
-  int xc;  // exchanges done
+  int n;         // the phase's tiles so far: S^T(n) is in buffer n & 1
+  int k;         // of which this warpgroup has done k
+  uint32_t sph;  // phases of s_full
+  int xc;        // exchanges done
+  __device__ __forceinline__ Bars bar() const { return Bars{reinterpret_cast<uint64_t*>(base + K::OFF_BAR)}; }
+  __device__ __forceinline__ volatile int* abort() const { return reinterpret_cast<volatile int*>(base + K::OFF_ABORT); }
+  template <typename V>
+  __device__ __forceinline__ V* small(int off) const {
+    return reinterpret_cast<V*>(base + (OWN ? K::OFF_SMALL_O : K::OFF_SMALL) + group * C::SMALL + off);
+  }
+  __device__ __forceinline__ unsigned char* pt() const {  // P^T
+    return base + (OWN ? K::OFF_PO + group * C::PB : K::OFF_P);
+  }
+  __device__ __forceinline__ uint32_t s_at() const { return at + (OWN ? K::S_OWN : K::S_COL + C::NG * group); }
+  __device__ __forceinline__ uint32_t o_at() const {
+    return at + (OWN ? K::O_OWN + group * kOwnRows * K::NDC : K::O_COL + C::NG * group);
+  }
+  // Every softmax warp of the group arrives and waits (bounded); what was
+  // written to shared memory before is visible after.
+  __device__ __forceinline__ bool exchange() {
+    __syncwarp();
+    uint64_t* b = bar().template xch<OWN>(group);
+    if ((threadIdx.x & 31) == 0) mbar_arrive(b);
+    const bool ok = wait(b, xc & 1, abort());
+    ++xc;
+    return __all_sync(0xffffffffu, ok);
+  }
 };
-
-// Every softmax warp of the group arrives and waits (bounded); what was
-// written to shared memory before is visible after.
-__device__ __forceinline__ bool exchange(SoftCtx& c) {
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(c.bar.xch(c.group));
-  const bool ok = wait(c.bar.xch(c.group), c.xc & 1, c.abort);
-  ++c.xc;
-  return __all_sync(0xffffffffu, ok);
-}
 
 // One visit of a segment: its tiles' softmax, then the partial result.  The
 // rows' reference maxima live in shared memory; a tile only exchanges whether
 // any score outgrew its row's threshold, which after a visit's first tile is
 // rare (it also happens when a window first lets a row see a key).
-template <int D, int N, bool OWN, typename Walk>
-__device__ bool softmax_visit(const SharedParams& p, Walk& w, SoftCtx& c) {
-  using C = ShCfg<D, N, OWN>;
-  constexpr int NDC = C::NDC, NG = C::NG;
+template <int D, int NP, bool OWN, typename Walk>
+__device__ bool softmax_visit(const SharedParams& p, Walk& w, SoftCtx<D, NP, OWN>& c) {
+  using C = typename SoftCtx<D, NP, OWN>::C;
+  constexpr int N = OWN ? kOwnRows : NP, NDC = (D + 127) / 128, NG = C::NG;
   const SharedGeom& g = p.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q4 = warp & 3, t = 32 * q4 + lane;
-  const uint32_t lane_off = (uint32_t)(32 * q4) << 16, col0 = (uint32_t)(NG * c.group);
+  const int row0 = OWN ? 0 : NG * c.group;  // this warpgroup's first row of the block
   const float sl2 = g.scale * kLog2e;
-  float* red = reinterpret_cast<float*>(c.small + C::RED);
-  float* thr = reinterpret_cast<float*>(c.small + C::THR);
-  float* use = reinterpret_cast<float*>(c.small + C::USE);
-  float* alp = reinterpret_cast<float*>(c.small + C::ALPHA);
-  int2* rng = reinterpret_cast<int2*>(c.small + C::RNG);
-  int* bnd = reinterpret_cast<int*>(c.small + C::BND);
+  float* red = c.template small<float>(C::RED);
+  float* thr = c.template small<float>(C::THR);
+  float* use = c.template small<float>(C::USE);
+  float* alp = c.template small<float>(C::ALPHA);
+  int2* rng = c.template small<int2>(C::RNG);
+  int* bnd = c.template small<int>(C::BND);
   volatile int* grow_tag = bnd + 8;   // [2] tile (plus one) at which some score outgrew its threshold
   volatile int* scale_tag = bnd + 10;  // [1] tile (plus one) at which some row with earlier keys did
   const int blk = w.blk, slot = w.slot;
@@ -334,7 +398,7 @@ __device__ bool softmax_visit(const SharedParams& p, Walk& w, SoftCtx& c) {
     int lo = 0, hi = INT32_MAX;  // rows that are no query mask nothing: their columns are never read
     bool row = false;
     if (t < NG) {
-      const int r = NG * c.group + t;  // row of the block
+      const int r = row0 + t;  // row of the block
       if constexpr (OWN) {
         const int m = blk * kOwnRows + r;
         row = m < g.M;
@@ -362,7 +426,7 @@ __device__ bool softmax_visit(const SharedParams& p, Walk& w, SoftCtx& c) {
       bnd[q4 * 2 + 1] = hi_w;
     }
   }
-  if (!exchange(c)) return false;
+  if (!c.exchange()) return false;
   const int lo_all = max(max(bnd[0], bnd[2]), max(bnd[4], bnd[6]));
   const int hi_all = min(min(bnd[1], bnd[3]), min(bnd[5], bnd[7]));
 
@@ -373,14 +437,15 @@ __device__ bool softmax_visit(const SharedParams& p, Walk& w, SoftCtx& c) {
   bool more = true;
 #pragma unroll 1
   while (more) {
-    const int n = c.n, key0 = w.key0();
+    const int n = c.k, buf = c.n & 1, key0 = w.key0();
     const bool first = w.first;
     more = !w.last();
-    if (!__all_sync(0xffffffffu, wait(c.bar.s_full(n & 1), (n >> 1) & 1, c.abort))) return false;
+    if (!__all_sync(0xffffffffu, wait(c.bar().template s_full<OWN>(c.group) + buf, (c.sph >> buf) & 1, c.abort()))) return false;
+    c.sph ^= 1u << buf;
     tc_fence_after();
     uint32_t sr[NG];
-    if constexpr (NG == 16) tmem_ld16(c.tmem + lane_off + C::S_COL + N * (n & 1) + col0, sr);
-    else tmem_ld32(c.tmem + lane_off + C::S_COL + N * (n & 1) + col0, sr);
+    if constexpr (NG == 16) tmem_ld16(c.s_at() + N * buf, sr);
+    else tmem_ld32(c.s_at() + N * buf, sr);
     tmem_wait_ld();
     float x[NG];
 #pragma unroll
@@ -402,7 +467,7 @@ __device__ bool softmax_visit(const SharedParams& p, Walk& w, SoftCtx& c) {
         over |= x[q] > v.x || x[q + 1] > v.y || x[q + 2] > v.z || x[q + 3] > v.w;
       }
       if (__any_sync(0xffffffffu, over) && lane == 0) grow_tag[n & 1] = n + 1;
-      if (!exchange(c)) return false;
+      if (!c.exchange()) return false;
       grow = grow_tag[n & 1] == n + 1;
     }
     if (grow) {
@@ -414,7 +479,7 @@ __device__ bool softmax_visit(const SharedParams& p, Walk& w, SoftCtx& c) {
         column_reduce<NG, true>(mx, lane);
         column_post<NG>(mx, rb + q4 * NG, lane);
       }
-      if (!exchange(c)) return false;
+      if (!c.exchange()) return false;
       if (t < NG) {
         const float tm = fmaxf(fmaxf(rb[t], rb[NG + t]), fmaxf(rb[2 * NG + t], rb[3 * NG + t]));
         float a = 1.f;
@@ -431,7 +496,7 @@ __device__ bool softmax_visit(const SharedParams& p, Walk& w, SoftCtx& c) {
         }
         alp[t] = a;
       }
-      if (!exchange(c)) return false;
+      if (!c.exchange()) return false;
       scale = *scale_tag == n + 1;
       if (scale) {
 #pragma unroll
@@ -459,13 +524,13 @@ __device__ bool softmax_visit(const SharedParams& p, Walk& w, SoftCtx& c) {
       pk[q / 2 + 1] = pack_bf16(e2, e3);
     }
     // PV(n - 1) has finished with P^T's buffer, and with O^T before it is rescaled
-    if (n > 0 && !__all_sync(0xffffffffu, wait(c.bar.o_done(), (n - 1) & 1, c.abort))) return false;
+    if (n > 0 && !__all_sync(0xffffffffu, wait(c.bar().template o_done<OWN>(c.group), (n - 1) & 1, c.abort()))) return false;
     if (scale) {  // uniform over the warpgroup
       tc_fence_after();
 #pragma unroll 1
       for (int i = 0; i < NDC * (NG / 16); ++i) {
         const int q0 = NG == 16 ? 0 : 16 * (i & 1);
-        const uint32_t o_at = c.tmem + lane_off + C::O_COL + N * (NG == 16 ? i : i >> 1) + col0 + q0;
+        const uint32_t o_at = c.o_at() + N * (NG == 16 ? i : i >> 1) + q0;
         uint32_t ov[16];
         tmem_ld16(o_at, ov);
         tmem_wait_ld();
@@ -475,7 +540,7 @@ __device__ bool softmax_visit(const SharedParams& p, Walk& w, SoftCtx& c) {
       }
       tmem_wait_st();
     }
-    unsigned char* pb = c.base + C::OFF_P;
+    unsigned char* pb = c.pt();
     if constexpr (NG == 16) {
       // K-major B operand: row q, key t -> chunk t / 64, 128-byte swizzle
       pb += (t >> 6) * kOwnRows * 128 + (t & 7) * 2;
@@ -495,8 +560,9 @@ __device__ bool softmax_visit(const SharedParams& p, Walk& w, SoftCtx& c) {
     fence_proxy_async_smem();  // generic writes -> the tensor core's reads
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(c.bar.p_full());
+    if (lane == 0) mbar_arrive(c.bar().template p_full<OWN>(c.group));
     ++c.n;
+    ++c.k;
     w.next();
   }
 
@@ -504,16 +570,16 @@ __device__ bool softmax_visit(const SharedParams& p, Walk& w, SoftCtx& c) {
   float* rb = red + (c.xc & 1) * 4 * NG;
   column_reduce<NG, false>(l_part, lane);
   column_post<NG>(l_part, rb + q4 * NG, lane);
-  if (!exchange(c)) return false;
-  if (!__all_sync(0xffffffffu, wait(c.bar.o_done(), (c.n - 1) & 1, c.abort))) return false;
+  if (!c.exchange()) return false;
+  if (!__all_sync(0xffffffffu, wait(c.bar().template o_done<OWN>(c.group), (c.k - 1) & 1, c.abort()))) return false;
   tc_fence_after();
   const int stride = OWN ? p.s.orow : p.s.prow;  // rows of a slot
   int rows;                                      // of which this segment has, and this group from row NG * group on
   if (OWN) rows = min(kOwnRows, g.M - blk * kOwnRows);
   else if (p.s.nmb > 1) rows = min(N, g.M - blk % p.s.nmb * N);
   else rows = min(p.s.nb, g.B - blk * p.s.nb) * g.M;
-  rows -= NG * c.group;
-  const size_t at = (size_t)slot * stride + NG * c.group;
+  rows -= row0;
+  const size_t at = (size_t)slot * stride + row0;
   float* out = (OWN ? p.po_o : p.pp_o) + at * D;
   float* ml = (OWN ? p.po_ml : p.pp_ml) + at * 2;
   if (t < min(rows, NG))
@@ -525,7 +591,7 @@ __device__ bool softmax_visit(const SharedParams& p, Walk& w, SoftCtx& c) {
 #pragma unroll 1
     for (int q0 = 0; q0 < min(rows, NG); q0 += 16) {
       uint32_t ov[16];
-      tmem_ld16(c.tmem + lane_off + C::O_COL + N * h + col0 + q0, ov);  // warp-collective
+      tmem_ld16(c.o_at() + N * h + q0, ov);  // warp-collective
       tmem_wait_ld();
       if (128 * h + t < D) {
 #pragma unroll
@@ -538,178 +604,171 @@ __device__ bool softmax_visit(const SharedParams& p, Walk& w, SoftCtx& c) {
   return true;
 }
 
-// One phase of a CTA's work: `total` tiles from walk `w0` on, all warp roles.
+// The roles' parts of one phase: `total` tiles from walk `w0` on.  Each role
+// goes from the prefix to the own caches by itself, so the ring never empties
+// in between (3 us a CTA that had work in both, when they met there).
+//
+// The TMA producer.  `issued`: slots loaded since the kernel began; nq: the
+// phase's blocks of queries.
 template <int D, int N, bool OWN, typename Walk>
-__device__ void run_phase(const SharedParams& p, unsigned char* base, uint64_t* bar_mem, volatile int* abort_flag,
-                          uint32_t tmem, const CUtensorMap* tmQ, const CUtensorMap* tmK, const CUtensorMap* tmV,
-                          const Walk& w0, int total) {
-  using C = ShCfg<D, N, OWN>;
-  constexpr int NCH = C::NCH, CPS = C::CPS, SPT = C::SPT, NSLOT = C::NSLOT, QD = C::QD;
+__device__ __forceinline__ bool produce(const SharedParams& p, unsigned char* base, const Bars& bar, volatile int* abort,
+                                        const CUtensorMap* tmQ, const CUtensorMap* tmK, const CUtensorMap* tmV,
+                                        const Walk& w0, int total, int& issued, int& nq) {
+  using K = ShKernel<D, N>;
+  constexpr int NCH = K::NCH, CPS = K::CPS, SPT = K::SPT, NSLOT = K::NSLOT, QD = OWN ? 2 : 1;
+  constexpr int AHEAD = OWN ? K::OWN_AHEAD : NSLOT;
   const SharedGeom& g = p.g;
-  const Bars bar{bar_mem};
-  const int warp = threadIdx.x / 32;
-  if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer
-    if (elect_one()) {
-      Walk wk = w0, wv = w0;
-      int issued = 0, nq = 0;
-      auto load_tile = [&](Walk& w, const CUtensorMap* m) -> bool {
-        const int key0 = w.key0();
-        int head = w.h;
-        if constexpr (OWN) head += w.b * g.Hkv;
+  Walk wk = w0, wv = w0;
+  auto load_tile = [&](Walk& w, const CUtensorMap* m) -> bool {
+    const int key0 = w.key0();
+    int head = w.h;
+    if constexpr (OWN) head += w.b * g.Hkv;
 #pragma unroll 1
-        for (int sp = 0; sp < SPT; ++sp, ++issued) {
-          const int s = issued % NSLOT;
-          if (issued >= NSLOT && !wait(bar.slot_empty(s), ((issued / NSLOT) & 1) ^ 1, abort_flag)) return false;
-          mbar_arrive_expect_tx(bar.slot_full(s), C::SLOT);
-          tma_load_4d(base + s * C::SLOT, m, bar.slot_full(s), 0, key0, sp * CPS, head);
-        }
-        w.next();
-        return true;
-      };
-      auto load_k = [&]() -> bool {
-        if (wk.first) {
-          const int s = nq % QD;
-          if (nq >= QD && !wait(bar.q_empty(s), ((nq / QD) & 1) ^ 1, abort_flag)) return false;
-          unsigned char* q = base + C::OFF_Q + s * C::QB;
-          if constexpr (OWN) {
-            mbar_arrive_expect_tx(bar.q_full(s), C::QB);
-            tma_load_4d(q, tmQ, bar.q_full(s), 0, wk.blk * kOwnRows, 0, wk.b * g.Hkv + wk.h);
-          } else {
-            mbar_arrive_expect_tx(bar.q_full(s), NCH * p.s.prow * 128);
-#pragma unroll 1
-            for (int c = 0; c < NCH; ++c)
-              tma_load_5d(q + c * N * 128, tmQ, bar.q_full(s), 0, wk.blk % p.s.nmb * N, c, wk.h,
-                          wk.blk / p.s.nmb * p.s.nb);
-          }
-          ++nq;
-        }
-        return load_tile(wk, tmK);
-      };
-      // slots in MMA order: K(0), K(1), then per tile n: V(n), K(n + 2)
-      bool ok = true;
-#pragma unroll 1
-      for (int n = -2; ok && n < total; ++n) ok = (n < 0 || load_tile(wv, tmV)) && (n + 2 >= total || load_k());
-      if (*abort_flag) {  // unwinding: the loads in flight land before shared memory is released
-        drain_ring(bar.q_full(0), QD, nq);
-        drain_ring(bar.slot_full(0), NSLOT, issued);
-      }
+    for (int sp = 0; sp < SPT; ++sp, ++issued) {
+      const int s = issued % NSLOT, old = issued - AHEAD;  // the load that has to have been used
+      if (old >= 0 && !wait(bar.slot_empty(old % NSLOT), (old / NSLOT) & 1, abort)) return false;
+      mbar_arrive_expect_tx(bar.slot_full(s), K::SLOT);
+      tma_load_4d(base + s * K::SLOT, m, bar.slot_full(s), 0, key0, sp * CPS, head);
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    if (elect_one()) {
-      const uint32_t idS = idesc_f16(T, N, 1, 1, 0, 0);                // K x Q^T, both K-major
-      const uint32_t idPV = idesc_f16(T, N, 1, 1, 1, N > 16 ? 1 : 0);  // V^T (MN-major) x P^T
-      Walk ws = w0, wv = w0;
-      int used = 0, nq = 0;
-      auto issue_s = [&](int n) -> bool {  // S^T(n) into buffer n & 1
-        const int qs = nq % QD;
-        if (ws.first && !wait(bar.q_full(qs), (nq / QD) & 1, abort_flag)) return false;
-        uint64_t qd = smem_desc_sw128(smem_u32(base + C::OFF_Q + qs * C::QB), 16, 1024);
+    w.next();
+    return true;
+  };
+  auto load_k = [&]() -> bool {
+    if (wk.first) {
+      const int s = nq % QD;
+      if (nq >= QD && !wait(bar.q_empty<OWN>(s), ((nq / QD) & 1) ^ 1, abort)) return false;
+      mbar_arrive_expect_tx(bar.q_full<OWN>(s), OWN ? K::B::QB : NCH * p.s.prow * 128);
+      if constexpr (OWN) {
+        tma_load_4d(base + K::OFF_QO + s * K::B::QB, tmQ, bar.q_full<OWN>(s), 0, wk.blk * kOwnRows, 0, wk.b * g.Hkv + wk.h);
+      } else {
 #pragma unroll 1
-        for (int sp = 0; sp < SPT; ++sp, ++used) {
-          const int s = used % NSLOT;
-          if (!wait(bar.slot_full(s), (used / NSLOT) & 1, abort_flag)) return false;
-          tc_fence_after();
-          uint64_t kd = smem_desc_sw128(smem_u32(base + s * C::SLOT), 16, 1024);
-#pragma unroll 1
-          for (int cc = 0; cc < CPS; ++cc) {
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              mma_ss(tmem + C::S_COL + N * (n & 1), desc_add(kd, ks * 32), desc_add(qd, ks * 32), idS,
-                     (sp | cc | ks) ? 1u : 0u);
-            kd = desc_add(kd, T * 128);
-            qd = desc_add(qd, N * 128);
-          }
-          mma_commit(bar.slot_empty(s));
-        }
-        mma_commit(bar.s_full(n & 1));
-        if (ws.last()) {  // the visit's queries are read
-          mma_commit(bar.q_empty(qs));
-          ++nq;
-        }
-        ws.next();
-        return true;
-      };
-      const uint64_t pd = smem_desc_sw128(smem_u32(base + C::OFF_P), N > 16 ? T * 128 : 16, 1024);
-      bool ok = true;
-#pragma unroll 1
-      for (int n = -2; ok && n < total; ++n) {
-        if (n >= 0) {
-          if (!wait(bar.p_full(), n & 1, abort_flag)) break;
-          tc_fence_after();
-          const uint32_t acc = wv.first ? 0u : 1u;
-          // O^T block h (head-dim columns [128 h, 128 h + 128)) += V^T . P^T: one slot a block
-#pragma unroll 1
-          for (int h = 0; h < SPT; ++h, ++used) {
-            const int s = used % NSLOT;
-            if (!wait(bar.slot_full(s), (used / NSLOT) & 1, abort_flag)) { ok = false; break; }
-            tc_fence_after();
-            const uint64_t vd = smem_desc_sw128(smem_u32(base + s * C::SLOT), T * 128, 1024);  // MN-major
-#pragma unroll
-            for (int ks = 0; ks < T / 16; ++ks)
-              mma_ss(tmem + C::O_COL + N * h, desc_add(vd, ks * 2048),
-                     N > 16 ? desc_add(pd, ks * 2048) : desc_add(pd, (ks >> 2) * kOwnRows * 128 + (ks & 3) * 32),
-                     idPV, (acc || ks > 0) ? 1u : 0u);
-            mma_commit(bar.slot_empty(s));
-          }
-          if (!ok) break;
-          mma_commit(bar.o_done());
-          wv.next();
-        }
-        if (n + 2 < total) ok = issue_s(n + 2);  // after PV(n): S buffer n & 1 is free
+        for (int c = 0; c < NCH; ++c)
+          tma_load_5d(base + K::OFF_Q + c * N * 128, tmQ, bar.q_full<OWN>(s), 0, wk.blk % p.s.nmb * N, c, wk.h,
+                      wk.blk / p.s.nmb * p.s.nb);
       }
-      mma_commit(bar.drain());
-      mbar_wait_drain(bar.drain(), 0);
+      ++nq;
     }
-  } else if ((warp - 2) / 4 < C::GROUPS) {
-    // ------------------------------------------------------------ softmax
-    const int group = (warp - 2) / 4;
-    SoftCtx c{base, base + C::OFF_SMALL + group * C::SMALL, bar, abort_flag, tmem, group, 0, 0};
-    Walk w = w0;
-    bool ok = true;
+    return load_tile(wk, tmK);
+  };
+  // slots in MMA order: K(0), K(1), then per tile n: V(n), K(n + 2)
+  bool ok = true;
 #pragma unroll 1
-    while (ok && c.n < total) ok = softmax_visit<D, N, OWN>(p, w, c);
+  for (int n = -2; ok && n < total; ++n) ok = (n < 0 || load_tile(wv, tmV)) && (n + 2 >= total || load_k());
+  return ok;
+}
+
+// The MMA issuer.  `used`: slots consumed since the kernel began.
+template <int D, int NP, bool OWN, typename Walk>
+__device__ __forceinline__ bool multiply(const SharedParams& p, unsigned char* base, const Bars& bar, volatile int* abort,
+                                         uint32_t tmem, const Walk& w0, int total, int& used) {
+  using K = ShKernel<D, NP>;
+  using C = typename std::conditional<OWN, typename K::B, typename K::A>::type;
+  constexpr int N = OWN ? kOwnRows : NP, CPS = K::CPS, SPT = K::SPT, NSLOT = K::NSLOT, QD = OWN ? 2 : 1;
+  const uint32_t idS = idesc_f16(T, N, 1, 1, 0, 0);                // K x Q^T, both K-major
+  const uint32_t idPV = idesc_f16(T, N, 1, 1, 1, N > 16 ? 1 : 0);  // V^T (MN-major) x P^T
+  const uint32_t s_at = tmem + (OWN ? K::S_OWN : K::S_COL), o_at = tmem + (OWN ? K::O_OWN : K::O_COL);
+  Walk ws = w0, wv = w0;
+  int nq = 0, gs = 0, gv = 0;  // own: the warpgroup of the walks' visits
+  uint32_t pph = 0;            // phases of p_full
+  auto issue_s = [&](int n) -> bool {  // S^T(n) into buffer n & 1
+    const int qs = nq % QD;
+    if (ws.first && !wait(bar.q_full<OWN>(qs), (nq / QD) & 1, abort)) return false;
+    uint64_t qd = smem_desc_sw128(smem_u32(base + (OWN ? K::OFF_QO : K::OFF_Q) + qs * C::QB), 16, 1024);
+#pragma unroll 1
+    for (int sp = 0; sp < SPT; ++sp, ++used) {
+      const int s = used % NSLOT;
+      if (!wait(bar.slot_full(s), (used / NSLOT) & 1, abort)) return false;
+      tc_fence_after();
+      uint64_t kd = smem_desc_sw128(smem_u32(base + s * K::SLOT), 16, 1024);
+#pragma unroll 1
+      for (int cc = 0; cc < CPS; ++cc) {
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          mma_ss(s_at + N * (n & 1), desc_add(kd, ks * 32), desc_add(qd, ks * 32), idS, (sp | cc | ks) ? 1u : 0u);
+        kd = desc_add(kd, T * 128);
+        qd = desc_add(qd, N * 128);
+      }
+      mma_commit(bar.slot_empty(s));
+    }
+    mma_commit(bar.s_full<OWN>(gs) + (n & 1));
+    if (ws.last()) {  // the visit's queries are read
+      mma_commit(bar.q_empty<OWN>(qs));
+      ++nq;
+      if (OWN) gs ^= 1;
+    }
+    ws.next();
+    return true;
+  };
+#pragma unroll 1
+  for (int n = -2; n < total; ++n) {
+    if (n >= 0) {
+      if (!wait(bar.p_full<OWN>(gv), (pph >> gv) & 1, abort)) return false;
+      pph ^= 1u << gv;
+      tc_fence_after();
+      const uint32_t acc = wv.first ? 0u : 1u, o = o_at + (OWN ? gv * kOwnRows * K::NDC : 0);
+      const uint64_t pd = smem_desc_sw128(smem_u32(base + (OWN ? K::OFF_PO + gv * C::PB : K::OFF_P)), N > 16 ? T * 128 : 16, 1024);
+      // O^T block h (head-dim columns [128 h, 128 h + 128)) += V^T . P^T: one slot a block
+#pragma unroll 1
+      for (int h = 0; h < SPT; ++h, ++used) {
+        const int s = used % NSLOT;
+        if (!wait(bar.slot_full(s), (used / NSLOT) & 1, abort)) return false;
+        tc_fence_after();
+        const uint64_t vd = smem_desc_sw128(smem_u32(base + s * K::SLOT), T * 128, 1024);  // MN-major
+#pragma unroll
+        for (int ks = 0; ks < T / 16; ++ks)
+          mma_ss(o + N * h, desc_add(vd, ks * 2048),
+                 N > 16 ? desc_add(pd, ks * 2048) : desc_add(pd, (ks >> 2) * kOwnRows * 128 + (ks & 3) * 32), idPV,
+                 (acc || ks > 0) ? 1u : 0u);
+        mma_commit(bar.slot_empty(s));
+      }
+      mma_commit(bar.o_done<OWN>(gv));
+      if (OWN && wv.last()) gv ^= 1;
+      wv.next();
+    }
+    if (n + 2 < total && !issue_s(n + 2)) return false;  // after PV(n): S buffer n & 1 is free
   }
-  __syncwarp();
+  return true;
 }
 
 template <int D, int NP>
-__global__ void __launch_bounds__(ShKernel<D, NP>::THREADS, 1)
+__global__ void __launch_bounds__(ShKernel<D, NP>::BOUND, 1)
     shared_kernel(const __grid_constant__ CUtensorMap tmQP, const __grid_constant__ CUtensorMap tmQO,
                   const __grid_constant__ CUtensorMap tmKP, const __grid_constant__ CUtensorMap tmVP,
                   const __grid_constant__ CUtensorMap tmKO, const __grid_constant__ CUtensorMap tmVO,
                   const __grid_constant__ SharedParams p) {
   using K = ShKernel<D, NP>;
   using A = typename K::A;
+  using B = typename K::B;
   constexpr int THR = K::THREADS, NW = THR / 32;
   extern __shared__ unsigned char smem_raw[];
   __shared__ int scan_sum[NW], scan_min[NW], start_b, start_r;
-  __shared__ unsigned scan_best[NW];
+  __shared__ int4 scan_best[NW];
   unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(base + K::OFF_BAR);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 32);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  uint64_t* bars2 = bars + 48;
+  const Bars bar{reinterpret_cast<uint64_t*>(base + K::OFF_BAR)};
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar.b + 48);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(base + K::OFF_ABORT);
 
   const SharedGeom& g = p.g;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    start_b = -1;
     *abort_flag = 0;
     prefetch_tmap(&tmKP);
     prefetch_tmap(&tmKO);
   }
-  if (threadIdx.x < 64 && lane < Bars::kCount) {
-    mbar_init((warp ? bars2 : bars) + lane, Bars::arrivals(lane, warp ? 1 : A::GROUPS));
+  if (threadIdx.x < Bars::kCount) {
+    mbar_init(bar.b + threadIdx.x, Bars::arrivals(threadIdx.x, K::GROUPS));
     fence_mbar_init();
   }
   // rows of the prefix query block that no box fills stay zero
 #pragma unroll 1
-  for (int i = threadIdx.x; i < A::QB / 16; i += THR) reinterpret_cast<uint4*>(base + A::OFF_Q)[i] = make_uint4(0, 0, 0, 0);
-  if (threadIdx.x < 4 * A::GROUPS)  // tags of the prefix phase
-    reinterpret_cast<int*>(base + A::OFF_SMALL + (threadIdx.x >> 2) * A::SMALL + A::BND)[8 + (threadIdx.x & 3)] = 0;
+  for (int i = threadIdx.x; i < A::QB / 16; i += THR) reinterpret_cast<uint4*>(base + K::OFF_Q)[i] = make_uint4(0, 0, 0, 0);
+  if (threadIdx.x < 4 * (K::GROUPS + 2)) {  // the warpgroups' tags
+    const int grp = threadIdx.x >> 2;
+    unsigned char* small = grp < K::GROUPS ? base + K::OFF_SMALL + grp * A::SMALL + A::BND
+                                           : base + K::OFF_SMALL_O + (grp - K::GROUPS) * B::SMALL + B::BND;
+    reinterpret_cast<int*>(small)[8 + (threadIdx.x & 3)] = 0;
+  }
   fence_proxy_async_smem();
   grid_dependency_wait();
   // Tensor memory is taken after the predecessor's end and before a dependent
@@ -720,13 +779,17 @@ __global__ void __launch_bounds__(ShKernel<D, NP>::THREADS, 1)
     tmem_relinquish();
   }
   // ---- the lengths: own tiles in all, the shortest live request
+  int nt0;  // tiles of request threadIdx.x
   {
-    int sum = 0, mn = INT32_MAX;
+    const int len = threadIdx.x < g.B ? p.own_len[threadIdx.x] : -1;
+    int mn = len >= 0 ? min(len, g.own_rows) : INT32_MAX;
+    nt0 = own_tiles(g, len);
+    int sum = nt0;
 #pragma unroll 1
-    for (int b = threadIdx.x; b < g.B; b += THR) {
-      const int len = p.own_len[b];
-      sum += own_tiles(g, len);
-      if (len >= 0) mn = min(mn, min(len, g.own_rows));
+    for (int b = THR + threadIdx.x; b < g.B; b += THR) {
+      const int n = p.own_len[b];
+      sum += own_tiles(g, n);
+      if (n >= 0) mn = min(mn, min(n, g.own_rows));
     }
     sum = __reduce_add_sync(0xffffffffu, sum);
     mn = __reduce_min_sync(0xffffffffu, mn);
@@ -754,31 +817,39 @@ __global__ void __launch_bounds__(ShKernel<D, NP>::THREADS, 1)
   const int key_lo = mn == INT32_MAX ? g.P : (g.W > 0 ? min(g.P, max(0, g.P + mn - g.Lq - g.W + 1)) : 0);
   const int tp = (g.P - key_lo + T - 1) / T;
   const int nseg = tp > 0 ? g.Hkv * p.s.nrb : 0, hn = g.Hkv * p.s.nomb, own_units = tiles * hn;
-  // ns: the one that makes the longest CTA's units fewest, a piece counting one
-  // unit more than its tiles (its queries' load and its partial's store)
-  const int most = nseg ? min(tp, max(1, kPieces / nseg)) : 0;
-  {
-    unsigned mine = ~0u;
-#pragma unroll 1
-    for (int i = 1 + threadIdx.x; i <= most; i += THR) {
-      const int np = nseg * i, k = (np + ctas - 1) / ctas;
-      const int all = (nseg * tp + np + own_units + ctas - 1) / ctas;
-      mine = min(mine, (unsigned)min(max(k * ((tp + i - 1) / i + 1), all), 0x3fffff) << 9 | i);
-    }
-    mine = __reduce_min_sync(0xffffffffu, mine);
-    if (lane == 0) scan_best[warp] = mine;
+  // Ranges: the number that makes the longest CTA's time shortest.  Pieces go to
+  // the CTAs in rounds, the first `rich` CTAs have k of them and the others one
+  // less; the own units either level all CTAs (qa for a rich one) or, where the
+  // others are done with all of them as soon, stay with those (qb each).
+  const int most = nseg ? min(tp, p.most) : 1;
+  static_assert(THR >= kPieces, "one candidate a thread");
+  if (32 * warp < most) {
+    const int i = min(1 + (int)threadIdx.x, most);
+    const int np = nseg * i, k = (np + ctas - 1) / ctas, rich = np - (k > 0 ? k - 1 : 0) * ctas, t = tp / i;
+    const float pl = k > 0 ? (float)(K::WP * (t + (t * i < tp)) + K::VP) : 0.f, kp = k * pl;
+    const float even = (K::WO * (float)own_units + (float)nseg * (K::WP * (float)tp + (float)(K::VP * i))) * (1.f / ctas);
+    const int level = rich == ctas ? (own_units + ctas - 1) / ctas : (int)ceilf(fmaxf(0.f, even - kp) * (1.f / K::WO));
+    const int alone = rich == ctas ? 0 : (own_units + ctas - rich - 1) / (ctas - rich);
+    const float both = kp + (float)(K::WV + K::WO * level);
+    const float apart = rich == ctas ? INFINITY : fmaxf(kp, kp - pl + (float)(K::WV + K::WO * alone));
+    const bool join = level > 0 && both < apart;
+    const float cost = own_units == 0 ? kp : (join ? both : apart);
+    const unsigned mine = (unsigned)fminf(cost, 4.0e6f) << 9 | i, least = __reduce_min_sync(0xffffffffu, mine);
+    if (mine == least) scan_best[warp] = make_int4((int)least, join ? level : 0, alone, t);  // (equal where i is)
   }
   __syncthreads();
-  unsigned best = ~0u;
-#pragma unroll
-  for (int i = 0; i < NW; ++i) best = min(best, scan_best[i]);
-  const int ns = nseg ? best & 511 : 1, pieces = nseg * ns;
-  // own runs fill the CTAs up to the same number of units: the first `rich`
-  // CTAs have `rounds` pieces, the others one less
+  int4 best = scan_best[0];
+#pragma unroll 1
+  for (int i = 1; 32 * i < most; ++i) {
+    const int4 v = scan_best[i];
+    if ((unsigned)v.x < (unsigned)best.x) best = v;
+  }
+  const int ns = best.x & 511, pieces = nseg * ns;
   const int rounds = (pieces + ctas - 1) / ctas, rich = pieces - (rounds > 0 ? rounds - 1 : 0) * ctas;
-  const int pl = pieces ? (tp + ns - 1) / ns + 1 : 0, even = (own_units + pieces * pl + ctas - 1) / ctas;
-  const int qa = max(0, even - rounds * pl);  // own units of a rich CTA, and of another
-  const int qb = qa > 0 || rich == ctas ? even - (rounds - 1) * pl : (own_units + ctas - rich - 1) / (ctas - rich);
+  const int per = best.w, extra = tp - ns * per;  // tiles of a piece, and how many have one more
+  const int qa = best.y;                          // own units of a rich CTA, and (qb) of another
+  int qb = best.z;
+  if (qa > 0) qb = rich == ctas ? 0 : (own_units - min(own_units, rich * qa) + ctas - rich - 1) / (ctas - rich);
   const OwnRuns runs{rich, qa, qb, own_units};
   const int o0 = runs.start(cta), o1 = runs.start(cta + 1);
   if (cta == 0 && threadIdx.x == 0) {  // for the merge
@@ -792,20 +863,22 @@ __global__ void __launch_bounds__(ShKernel<D, NP>::THREADS, 1)
 #pragma unroll 1
     for (int c0 = 0; c0 < g.B; c0 += THR) {
       const int b = c0 + threadIdx.x;
-      const int nt = b < g.B ? own_tiles(g, p.own_len[b]) : 0;
+      const int nt = c0 == 0 ? nt0 : (b < g.B ? own_tiles(g, p.own_len[b]) : 0);
       int inc = nt;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += v;
       }
-      __syncthreads();
+      if (c0 > 0) __syncthreads();  // (before the first, scan_best's)
       if (lane == 31) scan_sum[warp] = inc;
       __syncthreads();
       int off = before + inc - nt;
+#pragma unroll
       for (int i = 0; i < NW; ++i) {
-        if (i < warp) off += scan_sum[i];
-        before += scan_sum[i];
+        const int v = scan_sum[i];
+        if (i < warp) off += v;
+        before += v;
       }
       if (cta == 0 && b < g.B) p.plan[kPlanOff + b] = off;
       if (nt > 0 && o0 >= off * hn && o0 < (off + nt) * hn) {
@@ -817,37 +890,68 @@ __global__ void __launch_bounds__(ShKernel<D, NP>::THREADS, 1)
   }
 
   // ---- the prefix pieces, then the own run
+  PrefixWalk wp;
+  int total = 0;  // tiles of this CTA's pieces
   if (cta < pieces) {
-    PrefixWalk w;
-    w.p = &p;
-    w.splits = ns;
-    w.tiles = tp / ns;
-    w.extra = tp - ns * w.tiles;
-    w.key_lo = key_lo;
-    int total = 0;
+    wp.p = &p;
+    wp.splits = ns;
+    wp.tiles = per;
+    wp.extra = extra;
+    wp.key_lo = key_lo;
 #pragma unroll 1
     for (int i = cta; i < pieces; i += ctas) {
-      w.begin(i);
-      total += w.t1 - w.t;
+      wp.begin(i);
+      total += wp.t1 - wp.t;
     }
-    w.begin(cta);
-    run_phase<D, NP, false>(p, base, bars, abort_flag, tmem, &tmQP, &tmKP, &tmVP, w, total);
+    wp.begin(cta);
   }
-  if (o0 < o1) {
-    if (cta < pieces) {  // the shared memory and the accumulators change hands
-      fence_proxy_async_smem();  // the small arrays' generic accesses, before loads that land there
-      tc_fence_before();
-      __syncthreads();
-      tc_fence_after();
+  auto own_walk = [&]() {
+    OwnWalk w;
+    w.p = &p;
+    w.begin(start_b, start_r, o1 - o0);
+    return w;
+  };
+  if (warp == 0) {
+    if (elect_one()) {
+      int issued = 0, nqa = 0, nqb = 0;
+      bool ok = total == 0 || produce<D, NP, false>(p, base, bar, abort_flag, &tmQP, &tmKP, &tmVP, wp, total, issued, nqa);
+      if (ok && o0 < o1) {
+        // the own queries take over the prefix's bytes once its last scores are formed
+        if (K::SHARE_Q && nqa > 0) ok = wait(bar.q_empty<false>(0), (nqa - 1) & 1, abort_flag);
+        if (ok) produce<D, NP, true>(p, base, bar, abort_flag, &tmQO, &tmKO, &tmVO, own_walk(), o1 - o0, issued, nqb);
+      }
+      if (*abort_flag) {  // unwinding: the loads in flight land before shared memory is released
+        drain_ring(bar.q_full<false>(0), 1, nqa);
+        drain_ring(bar.q_full<true>(0), 2, nqb);
+        drain_ring(bar.slot_full(0), K::NSLOT, issued);
+      }
     }
-    if (threadIdx.x < 4)  // tags of this phase
-      reinterpret_cast<int*>(base + K::B::OFF_SMALL + K::B::BND)[8 + threadIdx.x] = 0;
-    __syncthreads();
-    if (!*abort_flag) {
-      OwnWalk w;
-      w.p = &p;
-      w.begin(start_b, start_r, o1 - o0);
-      run_phase<D, kOwnRows, true>(p, base, bars2, abort_flag, tmem, &tmQO, &tmKO, &tmVO, w, o1 - o0);
+  } else if (warp == 1) {
+    if (elect_one()) {
+      int used = 0;
+      const bool ok = total == 0 || multiply<D, NP, false>(p, base, bar, abort_flag, tmem, wp, total, used);
+      if (ok && o0 < o1) multiply<D, NP, true>(p, base, bar, abort_flag, tmem, own_walk(), o1 - o0, used);
+      mma_commit(bar.drain());
+      mbar_wait_drain(bar.drain(), 0);
+    }
+  } else {
+    const int group = (warp - 2) / 4;
+    const uint32_t at = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    bool ok = true;
+    if (group < K::GROUPS && total > 0) {
+      SoftCtx<D, NP, false> c{base, at, group, 0, 0, 0, 0};
+#pragma unroll 1
+      while (ok && c.n < total) ok = softmax_visit(p, wp, c);
+    }
+    if (ok && group < 2 && o0 < o1) {  // the own segments in turn
+      SoftCtx<D, NP, true> c{base, at, group, 0, 0, 0, 0};
+      OwnWalk w = own_walk();
+      if (group == 1) c.n += w.skip();
+#pragma unroll 1
+      while (ok && w.left > 0) {
+        ok = softmax_visit(p, w, c);
+        if (ok && w.left > 0) c.n += w.skip();
+      }
     }
   }
 
@@ -985,7 +1089,7 @@ SharedWs shared_ws(const SharedGeom& g) {
 template <int D, int NP>
 cudaError_t shared_d(const SharedGeom& g, const SharedArgs& a, void* ws, int* status, cudaStream_t st) {
   using K = ShKernel<D, NP>;
-  constexpr int CPS = K::A::CPS;
+  constexpr int CPS = K::CPS;
   const SharedSplit s = shared_split(g);
   CUtensorMap tqp, tqo, tkp, tvp, tko, tvo;
   cudaError_t e;
@@ -1016,6 +1120,8 @@ cudaError_t shared_d(const SharedGeom& g, const SharedArgs& a, void* ws, int* st
   p.po_ml = reinterpret_cast<float*>(wb + w.po_ml);
   p.po_o = reinterpret_cast<float*>(wb + w.po_o);
   p.status = status;
+  const long long nseg = (long long)g.Hkv * s.nrb;
+  p.most = nseg < kPieces ? (int)(kPieces / nseg) : 1;
   auto kern = shared_kernel<D, NP>;
   if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::SMEM)) != cudaSuccess)
     return e;
