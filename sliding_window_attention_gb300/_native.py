@@ -519,9 +519,9 @@ def forward_shared(q, k_prefix, v_prefix, k_own, v_own, own_len, window: int, sc
                    sinks=None, stream=None):
     """Return (o bf16 [B,Hq,Lq,D], lse fp32 [B,Hq,Lq]) of swa_attn_fwd_shared,
     allocated on the stream that the call runs on."""
-    import torch
-
     if stream is not None:
+        import torch
+
         with torch.cuda.stream(stream):
             return forward_shared(q, k_prefix, v_prefix, k_own, v_own, own_len, window, scale, prefix_len, sinks)
     r = (_fast or _marshal()).forward_shared(q, k_prefix, v_prefix, k_own, v_own, own_len, window, scale, prefix_len,
@@ -530,6 +530,7 @@ def forward_shared(q, k_prefix, v_prefix, k_own, v_own, own_len, window: int, sc
         return r
     if r is not None:
         raise SwaError(r, "swa_attn_fwd_shared")
+    import torch
 
     dims = _check_shared(q, k_prefix, v_prefix, k_own, v_own, own_len, sinks)
     dev, B, Hq, Hkv, Lq, D, prefix_rows, own_rows = dims
@@ -626,9 +627,9 @@ def qk_rope(q, k, v, wq, wk, inv_freq, eps: float, positions=None, pos0: int = 0
     """Return (q [B,Hq,L,D], k [B,Hkv,L,D], v [B,Hkv,L,D]) for the attention
     from a projection's bf16 q, k, v [B,L,heads,D]: q and k normalised per
     head, scaled and rotated by position.  k and v may be None."""
-    import torch
-
     if stream is not None:
+        import torch
+
         with torch.cuda.stream(stream):
             return qk_rope(q, k, v, wq, wk, inv_freq, eps, positions, pos0, weight_offset, interleaved)
     r = (_fast or _marshal()).qk_rope(q, k, v, wq, wk, inv_freq, None, None, None, eps, positions, pos0,
@@ -637,6 +638,8 @@ def qk_rope(q, k, v, wq, wk, inv_freq, eps: float, positions=None, pos0: int = 0
         return r
     if r is not None:
         raise SwaError(r, "swa_attn_qk_rope_fwd")
+    import torch
+
     B, L, _, D = q.shape
     dtype, device = q.dtype, q.device
     out = [None if t is None else torch.empty((B, t.shape[2], L, D), dtype=dtype, device=device) for t in (q, k, v)]
@@ -650,9 +653,9 @@ def qk_rope_append(q, k, v, wq, wk, inv_freq, k_cache, v_cache, kv_len, eps: flo
     kv_len[b] - 1 of each request's cache [B,Hkv,kv_rows,D] (kv_len int32 [B]
     counts the step's tokens), which also give their positions, from pos0.
     Return q [B,Hq,L,D]."""
-    import torch
-
     if stream is not None:
+        import torch
+
         with torch.cuda.stream(stream):
             return qk_rope_append(q, k, v, wq, wk, inv_freq, k_cache, v_cache, kv_len, eps, positions, pos0,
                                   weight_offset, interleaved)
@@ -662,6 +665,7 @@ def qk_rope_append(q, k, v, wq, wk, inv_freq, k_cache, v_cache, kv_len, eps: flo
         return r[0]
     if r is not None:
         raise SwaError(r, "swa_attn_qk_rope_fwd")
+    import torch
 
     B, L, Hq, D = q.shape
     q_out = torch.empty((B, Hq, L, D), dtype=q.dtype, device=q.device)
@@ -736,9 +740,9 @@ def qk_rope_backward(q, k, wq, wk, inv_freq, dq, dk, dv, eps: float, positions=N
     the fused projection output (q, k and v heads in that order; the k or v
     part is left out with k or dv None), dwq and dwk fp32 [D] (None for a
     None weight)."""
-    import torch
-
     if stream is not None:
+        import torch
+
         with torch.cuda.stream(stream):
             return qk_rope_backward(q, k, wq, wk, inv_freq, dq, dk, dv, eps, positions, pos0, weight_offset,
                                     interleaved)
@@ -748,6 +752,7 @@ def qk_rope_backward(q, k, wq, wk, inv_freq, dq, dk, dv, eps: float, positions=N
         return r
     if r is not None:
         raise SwaError(r, "swa_attn_qk_rope_bwd")
+    import torch
 
     dims = _check_rope_bwd(q, k, wq, wk, inv_freq, dq, dk, dv, positions)
     _, B, L, D, _, Hq, Hkv, _, _ = dims
