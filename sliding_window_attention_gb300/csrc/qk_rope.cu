@@ -229,6 +229,7 @@ struct StSmem {
   static constexpr size_t BYTES = (size_t)OFF_BAR + 256 + 128;
   static constexpr int CTAS = BWD ? (D == 512 ? 1 : 2) : (D == 512 ? 2 : 3);  // per SM (at D = 512, 3 would spill)
   static_assert(CTAS * BYTES <= 228 * 1024 - CTAS * 1024, "shared memory");
+  static_assert(D / 2 <= kThr, "a frequency a thread");
   static_assert(NS <= kTok, "each warp loads one of the first stages");
   static_assert(!BWD || NS * STAGE >= kTok * D * 4, "the scales' gradients are reduced in the stages");
 };
@@ -292,14 +293,24 @@ __global__ void __launch_bounds__(kThr, StSmem<D, BWD>::CTAS)
     }
     loaded = n;
   };
-  if (lane == 0 && warp < NS && warp < u1 - u0) load(warp);
-  for (int i = threadIdx.x; i < pairs; i += kThr) step[i] = turn_step(p.pos.inv_freq[i]);
-  for (int i = threadIdx.x; i < 2 * D; i += kThr) {
+  // Frequencies and scales are asked for before the stages: behind the first
+  // stages of every CTA (29 MB) they would take 4 us.
+  constexpr int WN = (2 * D + kThr - 1) / kThr;
+  const double freq = threadIdx.x < pairs ? p.pos.inv_freq[threadIdx.x] : 0.0;
+  float wr[WN];
+#pragma unroll
+  for (int j = 0; j < WN; ++j) {
+    const int i = threadIdx.x + j * kThr;
     const float* w = i < D ? p.wq : p.wk;
-    sw[i] = w ? w[i < D ? i : i - D] + p.off : 1.f;
+    wr[j] = i < 2 * D && w ? w[i < D ? i : i - D] + p.off : 1.f;
   }
+  asm volatile("" ::: "memory");
+  if (lane == 0 && warp < NS && warp < u1 - u0) load(warp);
+  if (threadIdx.x < pairs) step[threadIdx.x] = turn_step(freq);
+#pragma unroll
+  for (int j = 0; j < WN; ++j)
+    if (threadIdx.x + j * kThr < 2 * D) sw[threadIdx.x + j * kThr] = wr[j];
   __syncthreads();
-
 
   {
     // one token a warp
@@ -527,15 +538,21 @@ __global__ void __launch_bounds__(kThr, StSmem<D, BWD>::CTAS)
   }
 }
 
-// dw[kind][d] = sum of the CTAs' partials: 32 strided sums a column, then those.
+// dw[kind][d] = sum of the CTAs' partials (at most 2 a SM): 32 strided sums a column, then those.
+constexpr int kDwLoads = (2 * 152 + 31) / 32;
 __global__ void __launch_bounds__(1024) qk_rope_dw_kernel(const float* part, float* dwq, float* dwk, int D, int n) {
   __shared__ float red[32][33];
   const int x = threadIdx.x & 31, grp = threadIdx.x >> 5, col = blockIdx.x * 32 + x;  // column of [2][D]
   tc::grid_launch_dependents();
   tc::grid_dependency_wait();
-  float v = 0.f;
-#pragma unroll 5
-  for (int c = grp; c < n; c += 32) v += part[(size_t)c * 2 * D + col];
+  float t[kDwLoads], v = 0.f;  // every load of a thread is under way at once
+#pragma unroll
+  for (int i = 0; i < kDwLoads; ++i) {
+    const int c = grp + 32 * i;
+    t[i] = c < n ? part[(size_t)c * 2 * D + col] : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < kDwLoads; ++i) v += t[i];
   red[grp][x] = v;
   __syncthreads();
   v = red[x][grp];
