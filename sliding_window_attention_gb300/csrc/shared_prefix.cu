@@ -976,10 +976,12 @@ __global__ void __launch_bounds__(ShKernel<D, NP>::BOUND, 1)
 // and every warp forms the weights by itself.  THREADS: 256 where that is at
 // most two CTAs an SM, else 128 (a call's time with 256 and 128: 256 rows of
 // some 40 partials, D = 128: 15.1 and 17.0 us; 1,024 rows of as many, D = 64:
-// 19.2 and 16.3; 2,048 rows of 11, D = 512: 122 and 119).
+// 19.2 and 16.3; 2,048 rows of 6, D = 512: 122 and 119).  AHEAD: at D = 512,
+// where a thread's registers bound the rows in flight, 6 (110 us) rather than 8
+// (112); in CTAs of 256 threads 4 (15.1 us) rather than 8 (15.6).
 template <int D, int THREADS>
 __global__ void __launch_bounds__(THREADS) shared_merge_kernel(const __grid_constant__ SharedParams p) {
-  constexpr int LANES = D / 4, GR = THREADS / LANES, AHEAD = 1024 / THREADS;
+  constexpr int LANES = D / 4, GR = THREADS / LANES, AHEAD = THREADS == 256 ? 4 : (D == 512 ? 6 : 8);
   __shared__ float4 part[GR][LANES];
   const SharedGeom& g = p.g;
   const SharedSplit& s = p.s;

@@ -182,6 +182,68 @@ def test_extreme_values():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,Hq,Hkv,Lq,D,P,rows,window", [
+    (700, 64, 8, 1, 64, 70, 3, 0),      # more prefix segments than pieces, more requests than a CTA's threads
+    (1500, 2, 1, 1, 128, 129, 130, 0),  # rounds of 128 rows over three times a CTA's threads
+    (650, 1, 1, 1, 512, 65, 140, 50),
+    (330, 1, 1, 3, 256, 1, 2, 0),
+])
+def test_many_requests(B, Hq, Hkv, Lq, D, P, rows, window):
+    a = make(B, Hq, Hkv, Lq, D, P, rows, 3)
+    lens = [(i * 37) % (rows + 2) - 1 for i in range(B)]  # empty places and lengths of zero among them
+    got = run(a, lens, P, window, 0.2)
+    ref = reference(a, lens, P, window, 0.2)
+    check(got, ref)
+
+
+@pytest.mark.gpu
+def test_only_empty_places():
+    import sliding_window_attention_gb300 as swa
+
+    a = {n: None if t is None else t.cuda() for n, t in make(5, 4, 2, 2, 128, 300, 40, 1).items()}
+    lens = torch.full((5,), -1, dtype=torch.int32, device="cuda")
+    o, lse = torch.full_like(a["q"], 7), torch.full((5, 4, 2), 7.0, device="cuda")
+    ws = torch.empty(swa.fwd_workspace_bytes_shared(5, 4, 2, 2, 300, 40, 128, 0), dtype=torch.uint8, device="cuda")
+    swa.swa_attn_fwd_shared(a["q"], a["kp"], a["vp"], a["ko"], a["vo"], lens, None, o, lse, 0, 0.1, workspace=ws)
+    torch.cuda.synchronize()
+    assert swa.swa_attn_get_status() == 0 and (o == 7).all() and (lse == 7).all()
+
+
+@pytest.mark.gpu
+def test_steps_back_to_back():
+    """Appends, attention and growing lengths with nothing between them on the stream, against the same steps one by
+    one: a kernel that starts before its predecessor has ended must not read what that one still writes."""
+    import sliding_window_attention_gb300 as swa
+
+    B, Hq, Hkv, D, P, rows, steps = 6, 8, 2, 128, 200, 64, 40
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn((steps, B, 1, Hq + 2 * Hkv, D), device="cuda", generator=g).to(BF)
+    kp, vp = (torch.randn((Hkv, P, D), device="cuda", generator=g).to(BF) for _ in range(2))
+    f = (10000.0 ** (-torch.arange(D // 2, dtype=torch.float64) / (D // 2))).cuda()
+    w = torch.ones(D, device="cuda")
+
+    def chain(wait):
+        kc, vc = (torch.zeros((B, Hkv, rows, D), dtype=BF, device="cuda") for _ in range(2))
+        n = torch.tensor([1, 5, 9, 13, 17, 21], dtype=torch.int32, device="cuda")
+        outs = []
+        torch.cuda.synchronize()
+        for i in range(steps):
+            q, k, v = x[i].split((Hq, Hkv, Hkv), 2)
+            q = swa.qk_rope_append(q, k, v, w, w, f, kc, vc, n, 1e-6, pos0=P)
+            outs.append(swa.forward_shared(q, kp, vp, kc, vc, n, 0, 0.1))
+            n += 1
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return outs, kc, vc
+
+    (outs, kc, vc), (want, kw, vw) = chain(False), chain(True)
+    assert torch.equal(kc, kw) and torch.equal(vc, vw)
+    for (o, lse), (po, pl) in zip(outs, want):
+        assert torch.equal(o, po) and torch.equal(lse, pl)
+
+
+@pytest.mark.gpu
 def test_two_threads_on_two_streams():
     """Calls of two threads at once, each on its own stream: each call's own bits."""
     import threading
