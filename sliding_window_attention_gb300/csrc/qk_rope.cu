@@ -607,7 +607,8 @@ template <int D, int MODE, bool BWD>
 cudaError_t staged_mode(const StRope& p, const CUtensorMap (&m)[6], int grid, cudaStream_t s) {
   auto kern = qk_rope_staged_kernel<D, MODE, BWD>;
   const size_t smem = StSmem<D, BWD>::BYTES;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = allow_smem(kern, (int)smem, done);
   if (e != cudaSuccess) return e;
   return launch_dependent(kern, dim3(grid), dim3(kThr), smem, s, m[0], m[1], m[2], m[3], m[4], m[5], p);
 }

@@ -25,7 +25,7 @@
 // second kernel merges a row's partials.
 //
 // Bounds, of 64 requests of 32 heads (4 of them kv) over 16,384 prefix keys and
-// up to 1,024 of their own, D = 512 (112 us): the prefix's tiles, 2.5 us each on
+// up to 1,024 of their own, D = 512 (110 us): the prefix's tiles, 2.5 us each on
 // 128 of the CTAs, are bound by shared memory (a tile's operands are 393 KB of
 // MMA reads and 256 KB of TMA writes: 2.5 us at 128 bytes a clock); the own
 // caches by HBM (32 caches of up to 1,024 keys at D = 256: 6.0 TB/s).  At D <=
@@ -1125,8 +1125,8 @@ cudaError_t shared_d(const SharedGeom& g, const SharedArgs& a, void* ws, int* st
   const long long nseg = (long long)g.Hkv * s.nrb;
   p.most = nseg < kPieces ? (int)(kPieces / nseg) : 1;
   auto kern = shared_kernel<D, NP>;
-  if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::SMEM)) != cudaSuccess)
-    return e;
+  static std::atomic<unsigned long long> done{0};
+  if ((e = allow_smem(kern, (int)K::SMEM, done)) != cudaSuccess) return e;
   // both are programmatic dependents of what runs before them: the main grid's
   // set-up and the merge's placement fall into its predecessor's end
   if ((e = launch_dependent(kern, dim3(kSMs), dim3(K::THREADS), K::SMEM, st, tqp, tqo, tkp, tvp, tko, tvo, p)) !=

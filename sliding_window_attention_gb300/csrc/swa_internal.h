@@ -2,6 +2,7 @@
 // translation units.  Not installed; not part of the public ABI.
 #pragma once
 
+#include <atomic>
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -363,6 +364,20 @@ cudaError_t launch_dependent(void (*kern)(Params...), dim3 grid, dim3 block, siz
   cfg.attrs = &at;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, static_cast<Params>(args)...);
+}
+
+// Lets `kern` use `bytes` of dynamic shared memory, once a device (bit d of
+// `done`: device d has it).  The call takes 0.2 us of a small launch's 1.7.
+template <typename K>
+cudaError_t allow_smem(K kern, int bytes, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 // ---- attention over a shared prefix and per-request caches (shared_prefix.cu) ----
