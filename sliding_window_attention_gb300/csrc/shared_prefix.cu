@@ -830,8 +830,8 @@ __global__ void __launch_bounds__(ShKernel<D, NP>::BOUND, 1)
     const float even = (K::WO * (float)own_units + (float)nseg * (K::WP * (float)tp + (float)(K::VP * i))) * (1.f / ctas);
     const int level = rich == ctas ? (own_units + ctas - 1) / ctas : (int)ceilf(fmaxf(0.f, even - kp) * (1.f / K::WO));
     const int alone = rich == ctas ? 0 : (own_units + ctas - rich - 1) / (ctas - rich);
-    const float both = kp + (float)(K::WV + K::WO * level);
-    const float apart = rich == ctas ? INFINITY : fmaxf(kp, kp - pl + (float)(K::WV + K::WO * alone));
+    const float both = kp + K::WV + (float)K::WO * (float)level;
+    const float apart = rich == ctas ? INFINITY : fmaxf(kp, kp - pl + K::WV + (float)K::WO * (float)alone);
     const bool join = level > 0 && both < apart;
     const float cost = own_units == 0 ? kp : (join ? both : apart);
     const unsigned mine = (unsigned)fminf(cost, 4.0e6f) << 9 | i, least = __reduce_min_sync(0xffffffffu, mine);
