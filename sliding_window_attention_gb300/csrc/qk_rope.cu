@@ -113,6 +113,7 @@ struct StRope {
   float* part;                    // [gridDim.x][2][D] partial dw
   int B, L, Hq, Hkv, kv_rows;
   float eps, off;
+  int pass;                       // inputs are the first to leave L2
   int* status;
 };
 
@@ -275,6 +276,7 @@ __global__ void __launch_bounds__(kThr, StSmem<D, BWD>::CTAS)
   // warp has consumed stage n - NS; a warp gets to that after its own stage
   // n - NS + 1, so it seldom waits.
   int loaded = -1;  // the last stage this thread loaded
+  const uint64_t policy = tc::l2_policy(p.pass);
   auto load = [&](int n) {
     const int s = n % NS, u = u0 + n, grp = u / ls.per, i = u - grp * ls.per;
     if (n >= NS && !tc::mbar_wait(empty + s, ((n / NS) & 1) ^ 1, abort_flag)) return;
@@ -285,11 +287,11 @@ __global__ void __launch_bounds__(kThr, StSmem<D, BWD>::CTAS)
     // D = 512 rows are two halves of 256 (a box is at most 256 wide)
     const bool has_x = !BWD || kind < 2;
     tc::mbar_arrive_expect_tx(full + s, (has_x ? C::XB : 0) + (BWD ? C::YB : 0));
-    if (has_x) tc::tma_load_4d(x, kind == 0 ? &tmQ : (kind == 1 ? &tmK : &tmV), full + s, 0, D == 512 ? 2 * h0 : h0, l0, b);
+    if (has_x) tc::tma_load_4d(x, kind == 0 ? &tmQ : (kind == 1 ? &tmK : &tmV), full + s, 0, D == 512 ? 2 * h0 : h0, l0, b, policy);
     if (BWD) {
       const CUtensorMap* m = kind == 0 ? &tmDQ : (kind == 1 ? &tmDK : &tmDV);
-      if (D == 512) tc::tma_load_5d(x + C::XB, m, full + s, 0, 0, l0, h0, b);
-      else tc::tma_load_4d(x + C::XB, m, full + s, 0, l0, h0, b);
+      if (D == 512) tc::tma_load_5d(x + C::XB, m, full + s, 0, 0, l0, h0, b, policy);
+      else tc::tma_load_4d(x + C::XB, m, full + s, 0, l0, h0, b, policy);
     }
     loaded = n;
   };
@@ -595,6 +597,14 @@ StRope staged_params(const RopeArgs& a, bool v, bool bwd, int* status) {
   p.eps = a.eps;
   p.off = a.weight_offset;
   p.status = status;
+  // Where the outputs take at most half of L2, and inputs and outputs more than
+  // it can hold beside other data, the inputs give way: the outputs then stay for
+  // the kernel that reads them next and are not written out meanwhile.  Backward,
+  // 8 + 4 + 4 heads, D = 128, with and without, at 8,192 tokens (34 MB of outputs):
+  // 21.8 and 25.0 us; forward, 32 + 16 + 16 heads, D = 256, at 2,048 (67 MB): 20.8
+  // and 22.6; backward at 24,576 (100 MB): 64.7 and 62.0; at 2,048 (8 MB): 10.0 and 9.3.
+  const double out = (double)a.B * a.L * (a.Hq + (a.k ? a.Hkv : 0) + (v ? a.Hkv : 0)) * a.D * 2, in = bwd ? 2.75 * out : out;
+  p.pass = out <= 68.0e6 && in + out > 48.0e6;
   return p;
 }
 
