@@ -81,14 +81,20 @@ __device__ __forceinline__ long long token_pos(const RopePos& a, int b, int l, i
 // A lane holds E = 8 (16 at D = 512) elements of a row in NG groups of 4, D / NG
 // apart: with the whole head rotated in halves an element's partner is then in
 // the same lane, and a warp's loads of a group are contiguous.
-constexpr int kTok = 8;  // tokens of a stage, one a consumer warp
+//
+// With few heads a stage of 512 / D heads is mostly empty, so there is a second
+// form with a quarter of the heads and four tokens a warp (TPW), which serves
+// the shapes whose stages it makes fewer (65,536 tokens, 2 + 1 + 1 heads, D = 64:
+// forward 29.7 us, with one token a warp 54.6; backward 34.6 and 71.4).
+constexpr int kTok = 8;  // consumer warps, each with TPW tokens of a stage
 
-template <int D>
+template <int D, int TPW>
 struct StCfg {
-  static constexpr int HB = 512 / D;        // heads of a stage
+  static constexpr int HB = 512 / D / TPW;  // heads of a stage
   static constexpr int E = D == 512 ? 16 : 8;
   static constexpr int NG = E / 4, GS = D / NG;
-  static constexpr int LPR = D / E, RPW = 32 / LPR, ITER = HB / RPW;
+  static constexpr int LPR = D / E, RPW = 32 / LPR, ITER = HB * TPW / RPW;  // a warp's rows: RPW at a time
+  static constexpr int TOKS = kTok * TPW;
   static constexpr int XB = kTok * 512 * 2, YB = kTok * 512 * 4;
 };
 
@@ -147,9 +153,9 @@ __device__ __forceinline__ float f2_sum(uint64_t x) {
 // The partners' elements of a row whose own elements are in registers; ld(d,
 // v) loads elements d .. d + 3 of the row.
 template <int D, int MODE, typename F>
-__device__ __forceinline__ void row_partners(const uint64_t (&own)[StCfg<D>::E / 2], uint64_t (&other)[StCfg<D>::E / 2],
+__device__ __forceinline__ void row_partners(const uint64_t (&own)[StCfg<D, 1>::E / 2], uint64_t (&other)[StCfg<D, 1>::E / 2],
                                              int d4, int pairs, F&& ld) {
-  using C = StCfg<D>;
+  using C = StCfg<D, 1>;
   constexpr int W = C::E / 2;
   if constexpr (MODE == kInter) {
 #pragma unroll
@@ -170,9 +176,9 @@ __device__ __forceinline__ void row_partners(const uint64_t (&own)[StCfg<D>::E /
 }
 // cos, and +-sin as y_e = cos u_e + s_e u_partner(e), of the lane's elements.
 template <int D, int MODE>
-__device__ __forceinline__ void lane_angles(const float2* cs, int d4, int pairs, uint64_t (&c)[StCfg<D>::E / 2],
-                                            uint64_t (&s)[StCfg<D>::E / 2]) {
-  using C = StCfg<D>;
+__device__ __forceinline__ void lane_angles(const float2* cs, int d4, int pairs, uint64_t (&c)[StCfg<D, 1>::E / 2],
+                                            uint64_t (&s)[StCfg<D, 1>::E / 2]) {
+  using C = StCfg<D, 1>;
   // pairs i, i + 1 as {cos, sin, cos, sin}; beyond the rotated part {1, 0}
   auto two = [&](int i, bool in) {
     return in ? *reinterpret_cast<const float4*>(cs + i) : make_float4(1.f, 0.f, 1.f, 0.f);
@@ -213,37 +219,38 @@ __device__ __forceinline__ void lane_angles(const float2* cs, int d4, int pairs,
 
 // Shared memory of a staged kernel: NS stages, then weights, turn steps, the
 // warps' cos / sin tables and the barriers.
-template <int D, bool BWD>
+template <int D, bool BWD, int TPW>
 struct StSmem {
-  using C = StCfg<D>;
+  using C = StCfg<D, TPW>;
   static constexpr int STAGE = C::XB + (BWD ? C::YB : 0);
   // stages and CTAs an SM: 96 KB (forward) and 192 KB (backward) in flight;
   // measured at 30,553 tokens, D = 256, 2 x 8 stages of 8 KB take 349 us, 2 x 4
   // 327, 3 x 4 324, 4 x 4 351 (and 3 x 4 is best at 8,192 tokens, D = 128: 13.1
   // us against 14.3 and 15.8); the backward at 16,384 tokens, D = 512, takes 382
   // us with 8 stages of 24 KB, 389 with 5, 518 with 3
-  static constexpr int NS = BWD && D == 512 ? 8 : 4;
+  static constexpr int NS = BWD ? (D == 512 ? 8 : (TPW > 1 && D == 128 ? 3 : 4)) : (TPW > 1 ? 6 : 4);
   static constexpr int OFF_W = NS * STAGE;              // [2][D] scales
   static constexpr int OFF_STEP = OFF_W + 2 * D * 4;    // [D / 2]
-  static constexpr int OFF_CS = OFF_STEP + D / 2 * 8;   // [kTok][D / 2]
-  static constexpr int OFF_BAR = OFF_CS + kTok * D / 2 * 8;
+  static constexpr int OFF_CS = OFF_STEP + D / 2 * 8;   // [tokens][D / 2]
+  static constexpr int OFF_BAR = OFF_CS + C::TOKS * D / 2 * 8;
   static constexpr size_t BYTES = (size_t)OFF_BAR + 256 + 128;
-  static constexpr int CTAS = BWD ? (D == 512 ? 1 : 2) : (D == 512 ? 2 : 3);  // per SM (at D = 512, 3 would spill)
+  static constexpr int CTAS = BWD ? (D == 512 ? 1 : 2) : (D == 512 || TPW > 1 ? 2 : 3);  // per SM (there 3 would spill)
   static_assert(CTAS * BYTES <= 228 * 1024 - CTAS * 1024, "shared memory");
   static_assert(D / 2 <= kThr, "a frequency a thread");
   static_assert(NS <= kTok, "each warp loads one of the first stages");
   static_assert(!BWD || NS * STAGE >= kTok * D * 4, "the scales' gradients are reduced in the stages");
 };
 
-template <int D, int MODE, bool BWD>
-__global__ void __launch_bounds__(kThr, StSmem<D, BWD>::CTAS)
+template <int D, int MODE, bool BWD, int TPW>
+__global__ void __launch_bounds__(kThr, StSmem<D, BWD, TPW>::CTAS)
     qk_rope_staged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                           const __grid_constant__ CUtensorMap tmV,   // forward: v's rows
                           const __grid_constant__ CUtensorMap tmDQ, const __grid_constant__ CUtensorMap tmDK,
                           const __grid_constant__ CUtensorMap tmDV, const __grid_constant__ StRope p) {
-  using C = StCfg<D>;
-  using M = StSmem<D, BWD>;
+  using C = StCfg<D, TPW>;
+  using M = StSmem<D, BWD, TPW>;
   constexpr int E = C::E, W = E / 2, NG = C::NG, GS = C::GS, HB = C::HB, NS = M::NS, IT = C::ITER;
+  constexpr int AI = TPW > 1 ? IT : 1;  // tokens of a lane
   extern __shared__ unsigned char smem_raw[];
   unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
   float* sw = reinterpret_cast<float*>(base + M::OFF_W);
@@ -280,7 +287,7 @@ __global__ void __launch_bounds__(kThr, StSmem<D, BWD>::CTAS)
   auto load = [&](int n) {
     const int s = n % NS, u = u0 + n, grp = u / ls.per, i = u - grp * ls.per;
     if (n >= NS && !tc::mbar_wait(empty + s, ((n / NS) & 1) ^ 1, abort_flag)) return;
-    const int b = BWD ? grp / ls.gl : 0, l0 = (grp - b * ls.gl) * kTok;  // forward: tokens of the whole batch
+    const int b = BWD ? grp / ls.gl : 0, l0 = (grp - b * ls.gl) * C::TOKS;  // forward: tokens of the whole batch
     const int kind = i < ls.nq ? 0 : (i < ls.nq + ls.nk ? 1 : 2);
     const int h0 = (i - (kind > 0 ? ls.nq : 0) - (kind > 1 ? ls.nk : 0)) * HB;
     unsigned char* x = base + s * M::STAGE;
@@ -315,8 +322,7 @@ __global__ void __launch_bounds__(kThr, StSmem<D, BWD>::CTAS)
   __syncthreads();
 
   {
-    // one token a warp
-    float2* cs = reinterpret_cast<float2*>(base + M::OFF_CS) + warp * (D / 2);
+    float2* cs = reinterpret_cast<float2*>(base + M::OFF_CS) + warp * TPW * (D / 2);
     const int sub = lane / C::LPR, d4 = 4 * (lane % C::LPR);
     int u = u0, slot = 0, grp = u0 / ls.per, skip = u0 - grp * ls.per;  // blocks of the group before this CTA's
     uint32_t phase = 0;
@@ -345,36 +351,51 @@ __global__ void __launch_bounds__(kThr, StSmem<D, BWD>::CTAS)
       }
     };
     for (; ok && u < u1; ++grp) {
-      // this warp's token
-      const int t = grp * kTok + warp, b = BWD ? grp / ls.gl : t / p.L;
-      const int l = BWD ? t - b * ls.gl * kTok : t - b * p.L;
-      const bool live = b < p.B && l < p.L;
-      const long long tok = (long long)b * p.L + l;
+      // token i of this warp: its batch entry and place there
+      auto token = [&](int i, int& b, int& l) {
+        const int t = grp * C::TOKS + warp * TPW + i;
+        b = BWD ? grp / ls.gl : t / p.L;
+        l = BWD ? t - b * ls.gl * C::TOKS : t - b * p.L;
+        return b < p.B && l < p.L;
+      };
       __syncwarp();
-      if (live) {
+#pragma unroll 1
+      for (int i = 0; i < TPW; ++i) {
+        int b, l;
+        if (!token(i, b, l)) break;
         const long long pos = token_pos(p.pos, b, l, p.L);
-        for (int k = lane; k < pairs; k += 32) cs[k] = turn_cs(pos, step[k]);
+        for (int k = lane; k < pairs; k += 32) cs[i * (D / 2) + k] = turn_cs(pos, step[k]);
       }
       __syncwarp();
-      uint64_t a[W], q[W];  // cos and +-sin (forward: times the element's and its partner's scale)
+      // this lane's tokens: of its row in each round (TPW > 1), or the warp's
+      bool live[AI];
+      int tb[AI], tl[AI];
+#pragma unroll
+      for (int i = 0; i < AI; ++i) live[i] = token(TPW > 1 ? (i * C::RPW + sub) / HB : 0, tb[i], tl[i]);
+      auto table = [&](int i) { return cs + (TPW > 1 ? (i * C::RPW + sub) / HB * (D / 2) : 0); };
+      auto head = [&](int it) { return TPW > 1 ? (it * C::RPW + sub) % HB : it * C::RPW + sub; };
+      uint64_t a[AI][W], q[AI][W];  // cos and +-sin (forward: times the element's and its partner's scale)
       if constexpr (!BWD) {
-        uint64_t c[W], sn[W];
-        lane_angles<D, MODE>(cs, d4, pairs, c, sn);
-        // q or k rows: out = the token's row of head 0, heads `pitch` elements apart
-        auto rows = [&](int nb, int H, const float* w, uint16_t* out, long long pitch, bool store) {
+        // q or k rows: at = the tokens' rows of head 0, heads `pitch` elements apart
+        auto rows = [&](int nb, int H, const float* w, uint16_t* out, const long long (&at)[AI], long long pitch,
+                        const bool (&store)[AI]) {
           {
             uint64_t wv[W], wp[W];
 #pragma unroll
             for (int g = 0; g < NG; ++g) ld_f4(w + GS * g + d4, wv + 2 * g);
             row_partners<D, MODE>(wv, wp, d4, pairs, [&](int d, uint64_t* v) { ld_f4(w + d, v); });
 #pragma unroll
-            for (int e = 0; e < W; ++e) {
-              a[e] = tc::f2_mul(c[e], wv[e]);
-              q[e] = tc::f2_mul(sn[e], wp[e]);
+            for (int i = 0; i < AI; ++i) {
+              lane_angles<D, MODE>(table(i), d4, pairs, a[i], q[i]);
+#pragma unroll
+              for (int e = 0; e < W; ++e) {
+                a[i][e] = tc::f2_mul(a[i][e], wv[e]);
+                q[i][e] = tc::f2_mul(q[i][e], wp[e]);
+              }
             }
           }
           blocks(nb, [&](const unsigned char* st, int h0) {
-            const uint16_t* xs = reinterpret_cast<const uint16_t*>(st) + warp * 512 + sub * D;  // [head][D] of the token
+            const uint16_t* xs = reinterpret_cast<const uint16_t*>(st) + warp * 512 + sub * D;  // [token][head][D]
             uint64_t f[IT][W], o[IT][W];
             float ss[IT];
 #pragma unroll
@@ -394,13 +415,13 @@ __global__ void __launch_bounds__(kThr, StSmem<D, BWD>::CTAS)
               for (int it = 0; it < IT; ++it) ss[it] += __shfl_xor_sync(0xffffffffu, ss[it], k);
 #pragma unroll
             for (int it = 0; it < IT; ++it) {
-              const int h = h0 + it * C::RPW + sub;
+              const int h = h0 + head(it), i = TPW > 1 ? it : 0;
               const uint64_t rn = f2_dup(rsqrtf(ss[it] * (1.f / D) + p.eps));
 #pragma unroll
               for (int e = 0; e < W; ++e)
-                f[it][e] = tc::f2_mul(rn, tc::f2_fma(f[it][e], a[e], tc::f2_mul(o[it][e], q[e])));
-              if (store && h < H) {
-                uint16_t* dst = out + h * pitch + d4;
+                f[it][e] = tc::f2_mul(rn, tc::f2_fma(f[it][e], a[i][e], tc::f2_mul(o[it][e], q[i][e])));
+              if (store[i] && h < H) {
+                uint16_t* dst = out + at[i] + h * pitch + d4;
 #pragma unroll
                 for (int g = 0; g < NG; ++g)
                   *reinterpret_cast<uint2*>(dst + GS * g) = make_uint2(bf_pack2(f[it][2 * g]), bf_pack2(f[it][2 * g + 1]));
@@ -408,41 +429,58 @@ __global__ void __launch_bounds__(kThr, StSmem<D, BWD>::CTAS)
             }
           });
         };
-        const int kv_row = p.pos.kv_len ? (live ? p.pos.kv_len[b] - p.L + l : -1) : l;
-        const bool kv_ok = live && kv_row >= 0 && kv_row < p.kv_rows;  // rows outside the cache are not written
-        const long long kv_at = ((long long)b * p.Hkv * p.kv_rows + kv_row) * D, kv_pitch = (long long)p.kv_rows * D;
-        rows(ls.nq, p.Hq, sw, p.qo + ((long long)b * p.Hq * p.L + l) * D, (long long)p.L * D, live);
-        if (ok && ls.nk) rows(ls.nk, p.Hkv, sw + D, p.ko + kv_at, kv_pitch, kv_ok);
+        bool kv_ok[AI];
+        long long q_at[AI], kv_at[AI];
+#pragma unroll
+        for (int i = 0; i < AI; ++i) {
+          const int b = tb[i], l = tl[i], row = p.pos.kv_len ? (live[i] ? p.pos.kv_len[b] - p.L + l : -1) : l;
+          kv_ok[i] = live[i] && row >= 0 && row < p.kv_rows;  // rows outside the cache are not written
+          q_at[i] = ((long long)b * p.Hq * p.L + l) * D;
+          kv_at[i] = ((long long)b * p.Hkv * p.kv_rows + row) * D;
+        }
+        const long long kv_pitch = (long long)p.kv_rows * D;
+        rows(ls.nq, p.Hq, sw, p.qo, q_at, (long long)p.L * D, live);
+        if (ok && ls.nk) rows(ls.nk, p.Hkv, sw + D, p.ko, kv_at, kv_pitch, kv_ok);
         if (ok && ls.nv)
           blocks(ls.nv, [&](const unsigned char* st, int h0) {
             const uint16_t* xs = reinterpret_cast<const uint16_t*>(st) + warp * 512 + sub * D;
 #pragma unroll
             for (int it = 0; it < IT; ++it) {
-              const int h = h0 + it * C::RPW + sub;
-              if (!kv_ok || h >= p.Hkv) continue;
+              const int h = h0 + head(it), i = TPW > 1 ? it : 0;
+              if (!kv_ok[i] || h >= p.Hkv) continue;
 #pragma unroll
               for (int g = 0; g < NG; ++g)
-                *reinterpret_cast<uint2*>(p.vo + kv_at + h * kv_pitch + GS * g + d4) =
+                *reinterpret_cast<uint2*>(p.vo + kv_at[i] + h * kv_pitch + GS * g + d4) =
                     *reinterpret_cast<const uint2*>(xs + it * C::RPW * D + GS * g + d4);
             }
           });
       } else {
-        lane_angles<D, MODE>(cs, d4, pairs, a, q);
+        // rows of dy: [head][token][D]
+        auto dy_at = [&](const unsigned char* st, int it) {
+          const int tok = warp * TPW + (TPW > 1 ? (it * C::RPW + sub) / HB : 0);
+          return reinterpret_cast<const float*>(st + C::XB) + (head(it) * C::TOKS + tok) * D;
+        };
+        long long tok[AI];
 #pragma unroll
-        for (int e = 0; e < W; ++e) q[e] = tc::f2_mul(q[e], f2_dup(-1.f));  // the rotation's transpose
-        auto rows = [&](int nb, int H, const float* w, uint16_t* out, uint64_t (&acc)[W]) {
+        for (int i = 0; i < AI; ++i) {
+          tok[i] = (long long)tb[i] * p.L + tl[i];
+          lane_angles<D, MODE>(table(i), d4, pairs, a[i], q[i]);
+#pragma unroll
+          for (int e = 0; e < W; ++e) q[i][e] = tc::f2_mul(q[i][e], f2_dup(-1.f));  // the rotation's transpose
+        }
+        auto rows = [&](int nb, int H, const float* w, uint16_t* out, long long pitch, uint64_t (&acc)[W]) {
           uint64_t we[W];
 #pragma unroll
           for (int g = 0; g < NG; ++g) ld_f4(w + GS * g + d4, we + 2 * g);
           blocks(nb, [&](const unsigned char* st, int h0) {
-            const uint16_t* xs = reinterpret_cast<const uint16_t*>(st) + warp * 512 + sub * D;  // [head][D] of the token
-            const float* ys = reinterpret_cast<const float*>(st + C::XB) + (sub * kTok + warp) * D;  // [head][token][D]
+            const uint16_t* xs = reinterpret_cast<const uint16_t*>(st) + warp * 512 + sub * D;  // [token][head][D]
             uint64_t f[IT][W], y[IT][W];
             float ss[IT], dot[IT];
 #pragma unroll
             for (int it = 0; it < IT; ++it) {
               const uint16_t* x = xs + it * C::RPW * D;
-              const float* dy = ys + it * C::RPW * kTok * D;
+              const float* dy = dy_at(st, it);
+              const int i = TPW > 1 ? it : 0;
               uint64_t o[W];
 #pragma unroll
               for (int g = 0; g < NG; ++g) {
@@ -453,7 +491,7 @@ __global__ void __launch_bounds__(kThr, StSmem<D, BWD>::CTAS)
               uint64_t t = f2_dup(0.f), v = f2_dup(0.f);
 #pragma unroll
               for (int e = 0; e < W; ++e) {
-                y[it][e] = tc::f2_fma(a[e], y[it][e], tc::f2_mul(q[e], o[e]));
+                y[it][e] = tc::f2_fma(a[i][e], y[it][e], tc::f2_mul(q[i][e], o[e]));
                 t = tc::f2_fma(f[it][e], f[it][e], t);
                 v = tc::f2_fma(tc::f2_mul(y[it][e], we[e]), f[it][e], v);
               }
@@ -469,11 +507,11 @@ __global__ void __launch_bounds__(kThr, StSmem<D, BWD>::CTAS)
               }
 #pragma unroll
             for (int it = 0; it < IT; ++it) {
-              const int h = h0 + it * C::RPW + sub;
-              if (!live || h >= H) continue;
+              const int h = h0 + head(it), i = TPW > 1 ? it : 0;
+              if (!live[i] || h >= H) continue;
               const float r = rsqrtf(ss[it] * (1.f / D) + p.eps);
               const uint64_t rn = f2_dup(r), m = f2_dup(-dot[it] * r * r * (1.f / D));  // -mean(h n) r
-              uint16_t* dst = out + (long long)h * D + d4;
+              uint16_t* dst = out + tok[i] * pitch + (long long)h * D + d4;
 #pragma unroll
               for (int e = 0; e < W; ++e) {
                 acc[e] = tc::f2_fma(tc::f2_mul(y[it][e], rn), f[it][e], acc[e]);
@@ -485,20 +523,19 @@ __global__ void __launch_bounds__(kThr, StSmem<D, BWD>::CTAS)
             }
           });
         };
-        rows(ls.nq, p.Hq, sw, p.gq + tok * p.gq_tok, accq);
-        if (ok && ls.nk) rows(ls.nk, p.Hkv, sw + D, p.gk + tok * p.gk_tok, acck);
+        rows(ls.nq, p.Hq, sw, p.gq, p.gq_tok, accq);
+        if (ok && ls.nk) rows(ls.nk, p.Hkv, sw + D, p.gk, p.gk_tok, acck);
         if (ok && ls.nv)
           blocks(ls.nv, [&](const unsigned char* st, int h0) {
-            const float* ys = reinterpret_cast<const float*>(st + C::XB) + (sub * kTok + warp) * D;
 #pragma unroll
             for (int it = 0; it < IT; ++it) {
-              const int h = h0 + it * C::RPW + sub;
-              if (!live || h >= p.Hkv) continue;
-              uint16_t* dst = p.gv + tok * p.gv_tok + (long long)h * D + d4;
+              const int h = h0 + head(it), i = TPW > 1 ? it : 0;
+              if (!live[i] || h >= p.Hkv) continue;
+              uint16_t* dst = p.gv + tok[i] * p.gv_tok + (long long)h * D + d4;
 #pragma unroll
               for (int g = 0; g < NG; ++g) {
                 uint64_t v[2];
-                ld_f4(ys + it * C::RPW * kTok * D + GS * g + d4, v);
+                ld_f4(dy_at(st, it) + GS * g + d4, v);
                 *reinterpret_cast<uint2*>(dst + GS * g) = make_uint2(bf_pack2(v[0]), bf_pack2(v[1]));
               }
             }
@@ -578,15 +615,32 @@ RopePos rope_pos(const RopeArgs& a) {
   return r;
 }
 
+// The stages' units with TPW tokens a warp.
+StList stage_list(const RopeArgs& a, bool v, bool bwd, int tpw) {
+  StList l;
+  const int hb = 512 / a.D / tpw, toks = kTok * tpw;
+  l.nq = (a.Hq + hb - 1) / hb;
+  l.nk = a.k ? (a.Hkv + hb - 1) / hb : 0;
+  l.nv = v ? (a.Hkv + hb - 1) / hb : 0;
+  l.per = l.nq + l.nk + l.nv;
+  l.gl = bwd ? (a.L + toks - 1) / toks : 0;
+  l.groups = bwd ? a.B * l.gl : (int)(((long long)a.B * a.L + toks - 1) / toks);
+  return l;
+}
+// Four tokens a warp where that halves the stages and leaves one for every CTA
+// (forward: two; 8,192 tokens, 2 + 1 + 1 heads, D = 64: 8.3 us, else 10.1; but at
+// 4,096 tokens 7.5, else 7.1), or makes a quarter fewer of very many (30,000
+// tokens, 8 + 4 + 4 heads, D = 64: 24.2 us, else 28.1; but at 4,096 8.6, else 7.2).
+int tokens_a_warp(const RopeArgs& a, bool v, bool bwd) {
+  if (a.D > 128) return 1;
+  const StList one = stage_list(a, v, bwd, 1), four = stage_list(a, v, bwd, 4);
+  const long long u1 = (long long)one.groups * one.per, u4 = (long long)four.groups * four.per;
+  const bool fewer = 2 * u4 <= u1 ? u4 >= (bwd ? 2 : 4) * 152 : 4 * u4 <= 3 * u1 && u4 >= 16 * 152;
+  return fewer && four.groups < (1 << 26) ? 4 : 1;  // (32-bit token indexes)
+}
+
 StRope staged_params(const RopeArgs& a, bool v, bool bwd, int* status) {
   StRope p = {};
-  const int hb = 512 / a.D;
-  p.list.nq = (a.Hq + hb - 1) / hb;
-  p.list.nk = a.k ? (a.Hkv + hb - 1) / hb : 0;
-  p.list.nv = v ? (a.Hkv + hb - 1) / hb : 0;
-  p.list.per = p.list.nq + p.list.nk + p.list.nv;
-  p.list.gl = bwd ? (a.L + kTok - 1) / kTok : 0;
-  p.list.groups = bwd ? a.B * p.list.gl : (int)(((long long)a.B * a.L + kTok - 1) / kTok);
   p.pos = rope_pos(a);
   p.wq = a.wq;
   p.wk = a.wk;
@@ -600,59 +654,65 @@ StRope staged_params(const RopeArgs& a, bool v, bool bwd, int* status) {
   // Where the outputs take at most half of L2, and inputs and outputs more than
   // it can hold beside other data, the inputs give way: the outputs then stay for
   // the kernel that reads them next and are not written out meanwhile.  Backward,
-  // 8 + 4 + 4 heads, D = 128, with and without, at 8,192 tokens (34 MB of outputs):
-  // 21.8 and 25.0 us; forward, 32 + 16 + 16 heads, D = 256, at 2,048 (67 MB): 20.8
-  // and 22.6; backward at 24,576 (100 MB): 64.7 and 62.0; at 2,048 (8 MB): 10.0 and 9.3.
+  // 32 + 4 + 4 heads, D = 512, with and without, at 1,024 tokens (42 MB of outputs):
+  // 28.7 and 32.3 us; forward, 32 + 16 + 16 heads, D = 256, at 2,048 (67 MB): 20.8
+  // and 22.6; backward, 8 + 4 + 4 heads, D = 128, at 24,576 (100 MB): 64.7 and 62.0; at
+  // 2,048 (8 MB): 10.0 and 9.3.
   const double out = (double)a.B * a.L * (a.Hq + (a.k ? a.Hkv : 0) + (v ? a.Hkv : 0)) * a.D * 2, in = bwd ? 2.75 * out : out;
   p.pass = out <= 68.0e6 && in + out > 48.0e6;
   return p;
 }
 
-template <int D, bool BWD>
+template <int D, bool BWD, int TPW>
 int staged_ctas(const StList& l) {
-  const long long u = (long long)l.groups * l.per, most = 152 * StSmem<D, BWD>::CTAS;
+  const long long u = (long long)l.groups * l.per, most = 152 * StSmem<D, BWD, TPW>::CTAS;
   return (int)(u < most ? u : most);
 }
-template <int D, int MODE, bool BWD>
+template <int D, int MODE, bool BWD, int TPW>
 cudaError_t staged_mode(const StRope& p, const CUtensorMap (&m)[6], int grid, cudaStream_t s) {
-  auto kern = qk_rope_staged_kernel<D, MODE, BWD>;
-  const size_t smem = StSmem<D, BWD>::BYTES;
+  auto kern = qk_rope_staged_kernel<D, MODE, BWD, TPW>;
+  const size_t smem = StSmem<D, BWD, TPW>::BYTES;
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = allow_smem(kern, (int)smem, done);
   if (e != cudaSuccess) return e;
   return launch_dependent(kern, dim3(grid), dim3(kThr), smem, s, m[0], m[1], m[2], m[3], m[4], m[5], p);
 }
 
-template <int D, bool BWD>
+template <int D, bool BWD, int TPW>
 cudaError_t staged_launch(const StRope& p, const CUtensorMap (&m)[6], int grid, cudaStream_t s) {
-  if (p.pos.interleaved) return staged_mode<D, kInter, BWD>(p, m, grid, s);
-  return 2 * p.pos.pairs == D ? staged_mode<D, kHalves, BWD>(p, m, grid, s) : staged_mode<D, kPart, BWD>(p, m, grid, s);
+  if (p.pos.interleaved) return staged_mode<D, kInter, BWD, TPW>(p, m, grid, s);
+  return 2 * p.pos.pairs == D ? staged_mode<D, kHalves, BWD, TPW>(p, m, grid, s)
+                              : staged_mode<D, kPart, BWD, TPW>(p, m, grid, s);
 }
 
-template <int D>
-cudaError_t staged_fwd(const RopeArgs& a, const uint16_t* v, long long v_tok, const StRope& p, cudaStream_t s) {
+template <int D, int TPW>
+cudaError_t staged_fwd(const RopeArgs& a, const uint16_t* v, long long v_tok, StRope& p, cudaStream_t s) {
+  using C = StCfg<D, TPW>;
+  p.list = stage_list(a, v != nullptr, false, TPW);
   CUtensorMap m[6];
   const int toks = a.B * a.L;
-  cudaError_t e = make_tmap_tokens(&m[0], a.q, D, a.Hq, toks, 1, a.q_tok, kTok, StCfg<D>::HB);
-  if (e == cudaSuccess && a.k) e = make_tmap_tokens(&m[1], a.k, D, a.Hkv, toks, 1, a.k_tok, kTok, StCfg<D>::HB);
-  if (e == cudaSuccess && v) e = make_tmap_tokens(&m[2], v, D, a.Hkv, toks, 1, v_tok, kTok, StCfg<D>::HB);
+  cudaError_t e = make_tmap_tokens(&m[0], a.q, D, a.Hq, toks, 1, a.q_tok, C::TOKS, C::HB);
+  if (e == cudaSuccess && a.k) e = make_tmap_tokens(&m[1], a.k, D, a.Hkv, toks, 1, a.k_tok, C::TOKS, C::HB);
+  if (e == cudaSuccess && v) e = make_tmap_tokens(&m[2], v, D, a.Hkv, toks, 1, v_tok, C::TOKS, C::HB);
   if (e != cudaSuccess) return e;
   if (!a.k) m[1] = m[0];  // not read
   if (!v) m[2] = m[0];
   m[3] = m[4] = m[5] = m[0];
-  const int grid = staged_ctas<D, false>(p.list);
-  return staged_launch<D, false>(p, m, grid, s);
+  const int grid = staged_ctas<D, false, TPW>(p.list);
+  return staged_launch<D, false, TPW>(p, m, grid, s);
 }
 
-template <int D>
-cudaError_t staged_bwd(const RopeArgs& a, const float* dq, const float* dk, const float* dv, const StRope& p,
-                       float* dwq, float* dwk, cudaStream_t s) {
+template <int D, int TPW>
+cudaError_t staged_bwd(const RopeArgs& a, const float* dq, const float* dk, const float* dv, StRope& p, float* dwq,
+                       float* dwk, cudaStream_t s) {
+  using C = StCfg<D, TPW>;
+  p.list = stage_list(a, dv != nullptr, true, TPW);
   CUtensorMap m[6];
-  cudaError_t e = make_tmap_tokens(&m[0], a.q, D, a.Hq, a.L, a.B, a.q_tok, kTok, StCfg<D>::HB);
-  if (e == cudaSuccess) e = make_tmap_f32_tokens(&m[3], dq, D, a.Hq, a.L, a.B, kTok, StCfg<D>::HB);
-  if (e == cudaSuccess && a.k) e = make_tmap_tokens(&m[1], a.k, D, a.Hkv, a.L, a.B, a.k_tok, kTok, StCfg<D>::HB);
-  if (e == cudaSuccess && a.k) e = make_tmap_f32_tokens(&m[4], dk, D, a.Hkv, a.L, a.B, kTok, StCfg<D>::HB);
-  if (e == cudaSuccess && dv) e = make_tmap_f32_tokens(&m[5], dv, D, a.Hkv, a.L, a.B, kTok, StCfg<D>::HB);
+  cudaError_t e = make_tmap_tokens(&m[0], a.q, D, a.Hq, a.L, a.B, a.q_tok, C::TOKS, C::HB);
+  if (e == cudaSuccess) e = make_tmap_f32_tokens(&m[3], dq, D, a.Hq, a.L, a.B, C::TOKS, C::HB);
+  if (e == cudaSuccess && a.k) e = make_tmap_tokens(&m[1], a.k, D, a.Hkv, a.L, a.B, a.k_tok, C::TOKS, C::HB);
+  if (e == cudaSuccess && a.k) e = make_tmap_f32_tokens(&m[4], dk, D, a.Hkv, a.L, a.B, C::TOKS, C::HB);
+  if (e == cudaSuccess && dv) e = make_tmap_f32_tokens(&m[5], dv, D, a.Hkv, a.L, a.B, C::TOKS, C::HB);
   if (e != cudaSuccess) return e;
   if (!a.k) {  // not read
     m[1] = m[0];
@@ -660,8 +720,8 @@ cudaError_t staged_bwd(const RopeArgs& a, const float* dq, const float* dk, cons
   }
   if (!dv) m[5] = m[3];
   m[2] = m[0];
-  const int grid = staged_ctas<D, true>(p.list);
-  e = staged_launch<D, true>(p, m, grid, s);
+  const int grid = staged_ctas<D, true, TPW>(p.list);
+  e = staged_launch<D, true, TPW>(p, m, grid, s);
   if (e != cudaSuccess || (!dwq && !dwk)) return e;
   return launch_dependent(qk_rope_dw_kernel, dim3(2 * D / 32), dim3(1024), 0, s, p.part, dwq, dwk, D, grid);
 }
@@ -677,11 +737,12 @@ cudaError_t launch_qk_rope_fwd(const RopeArgs& a, const uint16_t* v, long long v
   p.ko = ko;
   p.vo = vo;
   p.kv_rows = kv_rows;
+  const bool few = tokens_a_warp(a, v != nullptr, false) == 4;
   switch (a.D) {
-    case 64: return staged_fwd<64>(a, v, v_tok, p, s);
-    case 128: return staged_fwd<128>(a, v, v_tok, p, s);
-    case 256: return staged_fwd<256>(a, v, v_tok, p, s);
-    case 512: return staged_fwd<512>(a, v, v_tok, p, s);
+    case 64: return few ? staged_fwd<64, 4>(a, v, v_tok, p, s) : staged_fwd<64, 1>(a, v, v_tok, p, s);
+    case 128: return few ? staged_fwd<128, 4>(a, v, v_tok, p, s) : staged_fwd<128, 1>(a, v, v_tok, p, s);
+    case 256: return staged_fwd<256, 1>(a, v, v_tok, p, s);
+    case 512: return staged_fwd<512, 1>(a, v, v_tok, p, s);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -697,11 +758,12 @@ cudaError_t launch_qk_rope_bwd(const RopeArgs& a, const float* dq, const float* 
   p.gk_tok = gk_tok;
   p.gv_tok = gv_tok;
   p.part = part;
+  const bool few = tokens_a_warp(a, dv != nullptr, true) == 4;
   switch (a.D) {
-    case 64: return staged_bwd<64>(a, dq, dk, dv, p, dwq, dwk, s);
-    case 128: return staged_bwd<128>(a, dq, dk, dv, p, dwq, dwk, s);
-    case 256: return staged_bwd<256>(a, dq, dk, dv, p, dwq, dwk, s);
-    case 512: return staged_bwd<512>(a, dq, dk, dv, p, dwq, dwk, s);
+    case 64: return few ? staged_bwd<64, 4>(a, dq, dk, dv, p, dwq, dwk, s) : staged_bwd<64, 1>(a, dq, dk, dv, p, dwq, dwk, s);
+    case 128: return few ? staged_bwd<128, 4>(a, dq, dk, dv, p, dwq, dwk, s) : staged_bwd<128, 1>(a, dq, dk, dv, p, dwq, dwk, s);
+    case 256: return staged_bwd<256, 1>(a, dq, dk, dv, p, dwq, dwk, s);
+    case 512: return staged_bwd<512, 1>(a, dq, dk, dv, p, dwq, dwk, s);
     default: return cudaErrorInvalidValue;
   }
 }

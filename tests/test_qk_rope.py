@@ -119,6 +119,14 @@ CASES = [
     (1, 1030, 3, 2, 512, 512, False, True, 0.0, 0, 8),
     (1, 1025, 2, 1, 512, 384, False, True, 0.0, 5, 0),
     (5, 210, 1, 1, 512, 0, False, True, 0.0, 0, 0),
+    # many tokens of few heads (several tokens a warp)
+    (1, 7001, 2, 1, 64, 64, False, True, 0.0, 0, 0),
+    (3, 2403, 2, 1, 64, 32, True, True, 1.0, 3, 8),
+    (2, 5003, 1, 1, 128, 128, False, True, 0.0, 999983, 0),
+    (1, 9005, 2, 1, 128, 96, False, False, 0.5, 0, 16),
+    (5, 1301, 8, 4, 64, 64, False, True, 0.0, 30553, 0),
+    (700, 33, 2, 1, 64, 48, False, True, 0.0, 0, 0),
+    (1, 12000, 1, 1, 128, 128, True, True, 0.0, 0, 0),
 ]
 
 
