@@ -25,10 +25,10 @@
 // second kernel merges a row's partials.
 //
 // Bounds, of 64 requests of 32 heads (4 of them kv) over 16,384 prefix keys and
-// up to 1,024 of their own, D = 512 (110 us): the prefix's tiles, 2.5 us each on
+// up to 1,024 of their own, D = 512 (105 us): the prefix's tiles, 2.5 us each on
 // 128 of the CTAs, are bound by shared memory (a tile's operands are 393 KB of
 // MMA reads and 256 KB of TMA writes: 2.5 us at 128 bytes a clock); the own
-// caches by HBM (32 caches of up to 1,024 keys at D = 256: 6.0 TB/s).  At D <=
+// caches by HBM (32 caches of up to 1,024 keys at D = 256: 5.9 TB/s of a whole call).  At D <=
 // 128 a prefix tile is bound by the softmax's latency (1.2 us for 64 rows, 2.5
 // for 128), and a short call by what comes before and behind: lengths 0.5 us,
 // split 0.7, first tile 1.3, merge 1.8 (4 requests over 1,024 keys, D = 128: 7.9
@@ -84,6 +84,7 @@ struct SharedParams {
   uint16_t* o;         // bf16 [B, Hq, Lq, D]
   float* lse;          // [B, Hq, Lq]
   int* plan;
+  int prefix_pass;     // whether the prefix gives way in L2
   int most;            // ranges that a prefix segment is split into at most
   float *pp_ml, *pp_o;  // prefix partials: [piece][rows][2] and [piece][rows][D]
   float *po_ml, *po_o;  // own partials: [slot][rows]...
@@ -619,6 +620,12 @@ __device__ __forceinline__ bool produce(const SharedParams& p, unsigned char* ba
   constexpr int AHEAD = OWN ? K::OWN_AHEAD : NSLOT;
   const SharedGeom& g = p.g;
   Walk wk = w0, wv = w0;
+  // K and V are the first to leave L2, so that the partials stay there: own
+  // caches are read once a call, and a prefix of more than a quarter of L2 would
+  // not last until the next (64 requests over 16,384 prefix keys, D = 512: 105 us,
+  // else 109; 32 of up to 1,024 own keys, D = 256: 48.5, else 50.9; but 32 over a
+  // prefix of 17 MB, D = 128, that is kept: 14.5, else 15.7).
+  const uint64_t policy = l2_policy(OWN || p.prefix_pass);
   auto load_tile = [&](Walk& w, const CUtensorMap* m) -> bool {
     const int key0 = w.key0();
     int head = w.h;
@@ -628,7 +635,7 @@ __device__ __forceinline__ bool produce(const SharedParams& p, unsigned char* ba
       const int s = issued % NSLOT, old = issued - AHEAD;  // the load that has to have been used
       if (old >= 0 && !wait(bar.slot_empty(old % NSLOT), (old / NSLOT) & 1, abort)) return false;
       mbar_arrive_expect_tx(bar.slot_full(s), K::SLOT);
-      tma_load_4d(base + s * K::SLOT, m, bar.slot_full(s), 0, key0, sp * CPS, head);
+      tma_load_4d(base + s * K::SLOT, m, bar.slot_full(s), 0, key0, sp * CPS, head, policy);
     }
     w.next();
     return true;
@@ -1123,6 +1130,7 @@ cudaError_t shared_d(const SharedGeom& g, const SharedArgs& a, void* ws, int* st
   p.po_o = reinterpret_cast<float*>(wb + w.po_o);
   p.status = status;
   const long long nseg = (long long)g.Hkv * s.nrb;
+  p.prefix_pass = (double)g.Hkv * g.P * D * 4 > 32.0e6;
   p.most = nseg < kPieces ? (int)(kPieces / nseg) : 1;
   auto kern = shared_kernel<D, NP>;
   static std::atomic<unsigned long long> done{0};
