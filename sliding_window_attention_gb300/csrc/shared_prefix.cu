@@ -5,7 +5,7 @@
 // For request b with own length n, query row i (of Lq) sits at position
 // a = P + n - Lq + i behind the P prefix keys and sees the keys j <= a of
 // [prefix; own cache] with a - j < W (W = 0: all of them).  A softmax over two
-// key sets splits exactly: each set (and each part of one) gives its maximum
+// key sets splits exactly: each set (and each part of one) gives its reference
 // m, its sum l of 2^(s - m) and its unnormalised O, and with M = max m
 //   o = sum 2^(m - M) O / sum 2^(m - M) l,   lse = (M + log2 sum 2^(m - M) l) ln 2.
 //
@@ -67,11 +67,13 @@ constexpr int kPieces = 2 * kSMs;  // prefix pieces (or as many as there are seg
 constexpr int kSmemMax = 232448;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// P, its sums and O are bf16 and fp32, whose exponents reach 2^127: a row's
-// reference maximum (that of its first tile with a visible key) only moves
-// when a score outgrows it by more than 2^32, which leaves 2^63 for the sum
-// over 2^31 keys and loses no bit, since their precision is relative.
-constexpr float kGrowLog2 = 32.0f;
+// A row's reference is 2^16 above the largest score of its first tile with a
+// visible key, and only moves when a score outgrows it.  So P = 2^(score -
+// reference) is never above 1, and O never larger than with the maximum itself
+// as the reference: values of any size that the products' sum can hold are
+// safe.  What lies below costs nothing down to 2^-110 of the largest weight
+// (P, its sums and O are bf16 and fp32, whose precision is relative).
+constexpr float kRoomLog2 = 16.0f;
 // plan words: prefix tiles, ranges of a prefix segment, the own runs (four
 // words), then from kPlanOff on each request's first own tile
 constexpr int kPlanOff = 8;
@@ -373,9 +375,9 @@ struct SoftCtx {
 };
 
 // One visit of a segment: its tiles' softmax, then the partial result.  The
-// rows' reference maxima live in shared memory; a tile only exchanges whether
-// any score outgrew its row's threshold, which after a visit's first tile is
-// rare (it also happens when a window first lets a row see a key).
+// rows' references live in shared memory; a tile only exchanges whether any
+// score outgrew its row's, which after a visit's first tile is rare (it also
+// happens when a window first lets a row see a key).
 template <int D, int NP, bool OWN, typename Walk>
 __device__ bool softmax_visit(const SharedParams& p, Walk& w, SoftCtx<D, NP, OWN>& c) {
   using C = typename SoftCtx<D, NP, OWN>::C;
@@ -390,7 +392,7 @@ __device__ bool softmax_visit(const SharedParams& p, Walk& w, SoftCtx<D, NP, OWN
   float* alp = c.template small<float>(C::ALPHA);
   int2* rng = c.template small<int2>(C::RNG);
   int* bnd = c.template small<int>(C::BND);
-  volatile int* grow_tag = bnd + 8;   // [2] tile (plus one) at which some score outgrew its threshold
+  volatile int* grow_tag = bnd + 8;   // [2] tile (plus one) at which some score outgrew its reference
   volatile int* scale_tag = bnd + 10;  // [1] tile (plus one) at which some row with earlier keys did
   const int blk = w.blk, slot = w.slot;
 
@@ -484,14 +486,15 @@ __device__ bool softmax_visit(const SharedParams& p, Walk& w, SoftCtx<D, NP, OWN
       if (t < NG) {
         const float tm = fmaxf(fmaxf(rb[t], rb[NG + t]), fmaxf(rb[2 * NG + t], rb[3 * NG + t]));
         float a = 1.f;
-        if (tm > (m_row == -INFINITY ? m_row : m_row + kGrowLog2)) {
+        if (tm > m_row) {
+          const float up = tm + kRoomLog2;
           if (m_row != -INFINITY) {
-            a = fast_exp2(m_row - tm);
+            a = fast_exp2(m_row - up);
             *scale_tag = n + 1;
           }
-          m_row = tm;
-          use[t] = tm;
-          thr[t] = tm + kGrowLog2;
+          m_row = up;
+          use[t] = up;
+          thr[t] = up;
         } else if (first) {
           use[t] = 0.f;  // no visible key yet
         }

@@ -182,6 +182,22 @@ def test_extreme_values():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,D", [(2, 64), (30, 64), (70, 64), (2, 128), (2, 256), (2, 512)])
+def test_large_values_behind_scores_that_grow(B, D):
+    """Every second tile's scores are 2^28.9 above those of the tile before it, and v is of the order of 2^100: the
+    products with v must not leave fp32's range where the definition does not (128 such keys' sum is below 2^110)."""
+    H, P, rows = 64, 1024, 256
+    a = make(B, H, H, 1, D, P, rows, 12)
+    a["q"] = torch.ones_like(a["q"])
+    high = torch.arange(P) // 128 % 2 * (20.0 / D)  # scores of 20 / D rounded to bf16, D times
+    a["kp"] = high[None, :, None].to(BF).expand(H, P, D).contiguous()
+    a["ko"] = high[None, None, :rows, None].to(BF).expand(B, H, rows, D).contiguous()
+    a["vp"], a["vo"] = a["vp"] * 2.0 ** 100, a["vo"] * 2.0 ** 100
+    lens = [256 if b % 3 else 128 for b in range(B)]
+    check(run(a, lens, P, 0, 1.0), reference(a, lens, P, 0, 1.0))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("B,Hq,Hkv,Lq,D,P,rows,window", [
     (700, 64, 8, 1, 64, 70, 3, 0),      # more prefix segments than pieces, more requests than a CTA's threads
     (1500, 2, 1, 1, 128, 129, 130, 0),  # rounds of 128 rows over three times a CTA's threads
