@@ -653,6 +653,8 @@ def qk_rope_append(q, k, v, wq, wk, inv_freq, k_cache, v_cache, kv_len, eps: flo
     kv_len[b] - 1 of each request's cache [B,Hkv,kv_rows,D] (kv_len int32 [B]
     counts the step's tokens), which also give their positions, from pos0.
     Return q [B,Hq,L,D]."""
+    if kv_len is None:
+        raise ValueError("qk_rope_append needs kv_len, the lengths of the caches that it appends to")
     if stream is not None:
         import torch
 

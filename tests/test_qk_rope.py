@@ -558,3 +558,32 @@ def test_binding_refuses_wrong_layouts():
                                  k.float().transpose(1, 2).contiguous(), None, EPS, pos0=pos0)
     with pytest.raises(RuntimeError):  # a truth value that there is none of
         swa.qk_rope(q, k, v, w, w, f, EPS, interleaved=torch.zeros(2))
+
+
+def test_append_refuses_missing_lengths():
+    """Without lengths there are no rows to append to: refused on either marshalling path, before anything is looked at."""
+    import numpy as np
+
+    import sliding_window_attention_gb300 as swa
+
+    (q, k, v), _ = fused(2, 1, 2, 1, 64, 1)
+    c = torch.zeros((2, 1, 4, 64), dtype=BF)
+    for pos0 in (0, np.int64(0)):
+        with pytest.raises(ValueError, match="kv_len"):
+            swa.qk_rope_append(q, k, v, None, None, freqs(32), c, c.clone(), None, EPS, pos0=pos0)
+
+
+@pytest.mark.gpu
+def test_append_without_lengths_leaves_the_caches():
+    import numpy as np
+
+    import sliding_window_attention_gb300 as swa
+
+    (q, k, v), _ = fused(2, 1, 2, 1, 64, 1)
+    q, k, v = dev_rows((q, k, v), 0)
+    kc, vc = (torch.zeros((2, 1, 4, 64), dtype=BF, device="cuda") for _ in range(2))
+    for kw in (dict(), dict(pos0=np.int64(0)), dict(stream=torch.cuda.Stream())):
+        with pytest.raises(ValueError, match="kv_len"):
+            swa.qk_rope_append(q, k, v, None, None, freqs(32).cuda(), kc, vc, None, EPS, **kw)
+    torch.cuda.synchronize()
+    assert not kc.any() and not vc.any()
