@@ -449,6 +449,16 @@ def _check(device, specs):
             raise ValueError(f"{name} must be on the current CUDA device, like the other tensors (got {t.device})")
 
 
+def _scratch_bytes(workspace, device) -> int:
+    """Bytes of a caller's workspace on `device` (an index); none (0) is for the library to refuse."""
+    if workspace is None:
+        return 0
+    if not workspace.is_contiguous() or workspace.get_device() != device:
+        raise ValueError(f"workspace must be contiguous and on the current CUDA device, got {tuple(workspace.shape)} "
+                         f"strides {workspace.stride()} on {workspace.device}")
+    return workspace.numel() * workspace.element_size()
+
+
 def _int32(name, v) -> int:
     """v as the int of a C argument (ctypes drops the bits above 32)."""
     v = int(v)
@@ -510,7 +520,7 @@ def swa_attn_fwd_shared(q, k_prefix, v_prefix, k_own, v_own, own_len, sinks, o, 
     dims = _check_shared(q, k_prefix, v_prefix, k_own, v_own, own_len, sinks)
     _check(dims[0], (("o", o, torch.bfloat16, q.shape), ("lse", lse, torch.float32, q.shape[:3])))
     P = k_prefix.shape[1] if prefix_len is None else _int32("prefix_len", prefix_len)
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    nbytes = _scratch_bytes(workspace, dims[0])
     _run_shared(dims, q, k_prefix, v_prefix, k_own, v_own, own_len, sinks, o, lse, _int32("window", window),
                 float(scale), P, workspace, nbytes, stream)
 
@@ -731,7 +741,7 @@ def swa_attn_qk_rope_bwd(q, k, wq, wk, inv_freq, dq, dk, dv, dq_in, dk_in, dv_in
         outs.append(_addr(t))
         toks.append(tok)
     _check(dev, [(n, w, torch.float32, (D,)) for n, w in (("dwq", dwq), ("dwk", dwk)) if w is not None])
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    nbytes = _scratch_bytes(workspace, dev)
     _run_rope_bwd(dims, q, k, wq, wk, inv_freq, dq, dk, dv, outs, toks, dwq, dwk, eps, positions, pos0,
                   weight_offset, interleaved, workspace, nbytes, stream)
 

@@ -504,3 +504,34 @@ def test_binding_refuses_wrong_tensors():
     for kw in (dict(prefix_len=2 ** 32), dict(window=-2 ** 40)):
         with pytest.raises(ValueError, match="does not fit 32 bits"):
             swa.forward_shared(*ok.values(), **{**dict(window=0, scale=0.1), **kw})
+
+
+def test_a_workspace_has_its_bytes_on_the_device():
+    """Host memory, or a tensor whose elements share bytes, has not what its size says."""
+    from sliding_window_attention_gb300 import _native
+
+    assert _native._scratch_bytes(None, 0) == 0
+    for ws in (torch.empty(4096, dtype=torch.uint8), torch.empty(1, dtype=torch.uint8).expand(1 << 30)):
+        with pytest.raises(ValueError, match="workspace"):
+            _native._scratch_bytes(ws, 0)
+    assert _native._scratch_bytes(torch.empty(16, dtype=torch.float32), -1) == 64  # (-1: the host's index)
+    with pytest.raises(ValueError, match="workspace"):
+        _native._scratch_bytes(torch.empty(1, dtype=torch.uint8).expand(1 << 30), -1)
+
+
+@pytest.mark.gpu
+def test_binding_refuses_such_workspaces():
+    import sliding_window_attention_gb300 as swa
+
+    a = {n: None if t is None else t.cuda() for n, t in make(2, 4, 2, 1, 64, 10, 8, 1).items()}
+    n = torch.tensor([1, 2], dtype=torch.int32, device="cuda")
+    o, lse = torch.empty_like(a["q"]), torch.empty((2, 4, 1), device="cuda")
+    need = swa.fwd_workspace_bytes_shared(2, 4, 2, 1, 10, 8, 64, 0)
+    x = torch.zeros((1, 3, 2, 64), dtype=BF, device="cuda")
+    dy, dw = torch.zeros((1, 2, 3, 64), device="cuda"), torch.ones(64, device="cuda")
+    for ws in (torch.empty(need, dtype=torch.uint8), torch.empty(1, dtype=torch.uint8, device="cuda").expand(need)):
+        with pytest.raises(ValueError, match="workspace"):
+            swa.swa_attn_fwd_shared(a["q"], a["kp"], a["vp"], a["ko"], a["vo"], n, None, o, lse, 0, 0.1, workspace=ws)
+        with pytest.raises(ValueError, match="workspace"):
+            swa.swa_attn_qk_rope_bwd(x, None, dw, None, None, dy, None, None, x.clone(), None, None, dw.clone(), None,
+                                     1e-6, workspace=ws)
