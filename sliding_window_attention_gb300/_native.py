@@ -425,7 +425,7 @@ def _marshal():
     lib = load()
     with _lock:
         if _fast is None:
-            import torch  # noqa: F401  its libraries are the module's
+            import torch  # its libraries are the module's
 
             try:
                 from . import _marshal as m
@@ -434,7 +434,7 @@ def _marshal():
                                    "(python -c 'import __graft_entry__ as g; g.build()')") from e
             m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
                 lib.swa_attn_fwd_workspace_bytes_shared, lib.swa_attn_fwd_shared, lib.swa_attn_qk_rope_fwd,
-                lib.swa_attn_qk_rope_bwd_workspace_bytes, lib.swa_attn_qk_rope_bwd)))
+                lib.swa_attn_qk_rope_bwd_workspace_bytes, lib.swa_attn_qk_rope_bwd)), torch.OutOfMemoryError)
             _fast = m
         return _fast
 

@@ -17,6 +17,7 @@
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <c10/util/Exception.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
@@ -31,6 +32,7 @@ decltype(&swa_attn_fwd_shared) g_shared;
 decltype(&swa_attn_qk_rope_fwd) g_rope;
 decltype(&swa_attn_qk_rope_bwd_workspace_bytes) g_rope_bwd_ws;
 decltype(&swa_attn_qk_rope_bwd) g_rope_bwd;
+PyObject* g_out_of_memory;  // torch.OutOfMemoryError
 
 // Thrown (and turned into None) where the Python path has to take the call.
 struct NotThisWay {};
@@ -144,7 +146,10 @@ PyObject* call(Py_ssize_t n, Py_ssize_t want, F&& f) {
     return f();
   } catch (const NotThisWay&) {
     Py_RETURN_NONE;
-  } catch (const std::exception& e) {  // torch: out of memory, a tensor without storage
+  } catch (const c10::OutOfMemoryError& e) {
+    PyErr_SetString(g_out_of_memory, e.what_without_backtrace());
+    return nullptr;
+  } catch (const std::exception& e) {  // torch: a tensor without storage
     PyErr_SetString(PyExc_RuntimeError, e.what());
     return nullptr;
   }
@@ -287,10 +292,10 @@ PyObject* qk_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// The five entry points' addresses, in the order of the globals above.
+// The five entry points' addresses, in the order of the globals above, and torch.OutOfMemoryError.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 5) {
-    PyErr_SetString(PyExc_TypeError, "5 addresses expected");
+  if (n != 6 || !PyExceptionClass_Check(a[5])) {
+    PyErr_SetString(PyExc_TypeError, "5 addresses and an exception class expected");
     return nullptr;
   }
   void* p[5];
@@ -306,6 +311,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g_rope = reinterpret_cast<decltype(g_rope)>(p[2]);
   g_rope_bwd_ws = reinterpret_cast<decltype(g_rope_bwd_ws)>(p[3]);
   g_rope_bwd = reinterpret_cast<decltype(g_rope_bwd)>(p[4]);
+  Py_XSETREF(g_out_of_memory, Py_NewRef(a[5]));
   Py_RETURN_NONE;
 }
 

@@ -587,3 +587,33 @@ def test_append_without_lengths_leaves_the_caches():
             swa.qk_rope_append(q, k, v, None, None, freqs(32).cuda(), kc, vc, None, EPS, **kw)
     torch.cuda.synchronize()
     assert not kc.any() and not vc.any()
+
+
+@pytest.mark.gpu
+def test_running_out_of_memory_keeps_its_type():
+    """A call whose outputs do not fit raises what PyTorch's own allocations raise, on either marshalling path.  The
+    allocator's limit for this process is what runs out, not the device's memory."""
+    import numpy as np
+
+    import sliding_window_attention_gb300 as swa
+
+    q = torch.randn((1, 400000, 2, 64), device="cuda").to(BF)  # 102 MB, more than any piece that the allocator keeps
+    dy = torch.zeros((1, 2, 400000, 64), device="cuda")
+    f = freqs(32).cuda()
+    many, cache = (torch.zeros((400000, 1, 1, 64), dtype=BF, device="cuda") for _ in range(2))
+    n, prefix = torch.zeros(400000, dtype=torch.int32, device="cuda"), cache[:5].view(1, 5, 64)
+    calls = [lambda **kw: swa.qk_rope(q, None, None, None, None, f, EPS, **kw),
+             lambda **kw: swa.qk_rope_backward(q, None, None, None, f, dy, None, None, EPS, **kw),
+             lambda pos0=0: swa.forward_shared(many, prefix, prefix, cache, cache, n, type(pos0)(0), 0.1)]
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    total = torch.cuda.get_device_properties(torch.cuda.current_device()).total_memory
+    torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + (1 << 20)) / total)
+    try:
+        for call in calls:
+            for pos0 in (0, np.int64(0)):
+                with pytest.raises(torch.OutOfMemoryError):
+                    call(pos0=pos0)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert calls[0]()[0].shape == (1, 2, 400000, 64)
