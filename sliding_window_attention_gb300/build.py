@@ -1,5 +1,6 @@
 """Build libswa_attn.so in-tree with nvcc for sm_103a, and the binding's
-argument marshalling (csrc/marshal.cpp) with g++ against PyTorch's headers.
+argument marshalling (csrc/marshal.cpp) with g++ against PyTorch's headers
+(left out where PyTorch is not installed: the library needs none of it).
 
 Each .cu under csrc/ is compiled to an object in parallel, then linked into
 sliding_window_attention_gb300/libswa_attn.so.  Rebuilds only what changed
@@ -8,6 +9,7 @@ sliding_window_attention_gb300/libswa_attn.so.  Rebuilds only what changed
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -33,6 +35,27 @@ def _nvcc() -> str:
 
 
 MARSHAL = os.path.join(PKG, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
+
+
+MARSHAL_SRC = os.path.join(CSRC, "marshal.cpp")
+
+
+def _torch_version():
+    """The installed PyTorch's version, None without one."""
+    if importlib.util.find_spec("torch") is None:
+        return None
+    import torch
+
+    return torch.__version__
+
+
+def _marshal_due(version, force: bool = False) -> bool:
+    """Whether the module has to be built for this PyTorch."""
+    if version is None:
+        return False
+    if force or not os.path.exists(MARSHAL):
+        return True
+    return os.path.getmtime(MARSHAL) < max(os.path.getmtime(s) for s in (MARSHAL_SRC, os.path.join(ROOT, "include", "swa_attn.h")))
 
 
 def _marshal_cmd(src: str, out: str):
@@ -70,15 +93,14 @@ def build(verbose: bool = False, force: bool = False) -> str:
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-    src = os.path.join(CSRC, "marshal.cpp")
     marshal_tmp = MARSHAL + f".tmp{os.getpid()}"
-    marshal_due = force or not os.path.exists(MARSHAL) or \
-        os.path.getmtime(MARSHAL) < max(os.path.getmtime(src), os.path.getmtime(os.path.join(ROOT, "include", "swa_attn.h")))
+    torch_version = _torch_version()
+    marshal_due = _marshal_due(torch_version, force)
     if marshal_due:
-        cmd = _marshal_cmd(src, marshal_tmp)
+        cmd = _marshal_cmd(MARSHAL_SRC, marshal_tmp)
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
-        procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+        procs.append((MARSHAL_SRC, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
