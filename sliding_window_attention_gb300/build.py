@@ -49,12 +49,20 @@ def _torch_version():
     return torch.__version__
 
 
+def _marshal_stamp() -> str:
+    """The file that names the PyTorch that the module was built against."""
+    return os.path.join(BUILD, os.path.basename(MARSHAL) + ".torch")
+
+
 def _marshal_due(version, force: bool = False) -> bool:
     """Whether the module has to be built for this PyTorch."""
     if version is None:
         return False
-    if force or not os.path.exists(MARSHAL):
+    if force or not os.path.exists(MARSHAL) or not os.path.exists(_marshal_stamp()):
         return True
+    with open(_marshal_stamp()) as f:
+        if f.read() != version:
+            return True
     return os.path.getmtime(MARSHAL) < max(os.path.getmtime(s) for s in (MARSHAL_SRC, os.path.join(ROOT, "include", "swa_attn.h")))
 
 
@@ -114,6 +122,8 @@ def build(verbose: bool = False, force: bool = False) -> str:
         raise RuntimeError(f"compilation failed:\n{msg}")
     if marshal_due:
         os.replace(marshal_tmp, MARSHAL)
+        with open(_marshal_stamp(), "w") as f:
+            f.write(torch_version)
     if force or not os.path.exists(SO) or any(os.path.getmtime(o) > os.path.getmtime(SO) for o in objs):
         tmp = SO + f".tmp{os.getpid()}"
         cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
