@@ -485,12 +485,15 @@ def _check_shared(q, k_prefix, v_prefix, k_own, v_own, own_len, sinks):
 
     B, Hq, Lq, D = q.shape
     _, Hkv, own_rows, _ = k_own.shape
-    prefix_rows = k_prefix.shape[1]
+    if (k_prefix is None) != (v_prefix is None):
+        raise ValueError("k_prefix and v_prefix are given together, or neither")
+    prefix_rows = 0 if k_prefix is None else k_prefix.shape[1]
     dev, bf16 = _current_device(q, "q"), torch.bfloat16
     prefix, own = (Hkv, prefix_rows, D), (B, Hkv, own_rows, D)
-    _check(dev, (("q", q, bf16, (B, Hq, Lq, D)), ("k_prefix", k_prefix, bf16, prefix),
-                 ("v_prefix", v_prefix, bf16, prefix), ("k_own", k_own, bf16, own), ("v_own", v_own, bf16, own),
+    _check(dev, (("q", q, bf16, (B, Hq, Lq, D)), ("k_own", k_own, bf16, own), ("v_own", v_own, bf16, own),
                  ("own_len", own_len, torch.int32, (B,))))
+    if k_prefix is not None:
+        _check(dev, (("k_prefix", k_prefix, bf16, prefix), ("v_prefix", v_prefix, bf16, prefix)))
     if sinks is not None:
         _check(dev, (("sinks", sinks, torch.float32, (Hq,)),))
     return dev, B, Hq, Hkv, Lq, D, prefix_rows, own_rows
@@ -499,7 +502,7 @@ def _check_shared(q, k_prefix, v_prefix, k_own, v_own, own_len, sinks):
 def _run_shared(dims, q, k_prefix, v_prefix, k_own, v_own, own_len, sinks, o, lse, window, scale, P, ws, nbytes,
                 stream):
     _, B, Hq, Hkv, Lq, D, prefix_rows, own_rows = dims
-    rc = load().swa_attn_fwd_shared(q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), k_own.data_ptr(),
+    rc = load().swa_attn_fwd_shared(q.data_ptr(), _addr(k_prefix), _addr(v_prefix), k_own.data_ptr(),
                                     v_own.data_ptr(), own_len.data_ptr(), None if sinks is None else sinks.data_ptr(),
                                     o.data_ptr(), lse.data_ptr(), B, Hq, Hkv, Lq, P, prefix_rows, own_rows, D, window,
                                     scale, None if ws is None else ws.data_ptr(), nbytes, _stream_ptr(stream))
@@ -512,14 +515,14 @@ def swa_attn_fwd_shared(q, k_prefix, v_prefix, k_own, v_own, own_len, sinks, o, 
     """Attention of a generation step over a prefix shared by the batch and
     each request's own cache (see include/swa_attn.h).  q bf16 [B,Hq,Lq,D];
     k_prefix, v_prefix bf16 [Hkv,prefix_rows,D] (prefix_len of the rows, all
-    by default); k_own, v_own bf16 [B,Hkv,own_rows,D]; own_len int32 [B];
+    by default) or None for no prefix; k_own, v_own bf16 [B,Hkv,own_rows,D]; own_len int32 [B];
     sinks fp32 [Hq] or None; o bf16 like q and lse fp32 [B,Hq,Lq] are
     caller-allocated outputs."""
     import torch
 
     dims = _check_shared(q, k_prefix, v_prefix, k_own, v_own, own_len, sinks)
     _check(dims[0], (("o", o, torch.bfloat16, q.shape), ("lse", lse, torch.float32, q.shape[:3])))
-    P = k_prefix.shape[1] if prefix_len is None else _int32("prefix_len", prefix_len)
+    P = dims[6] if prefix_len is None else _int32("prefix_len", prefix_len)
     nbytes = _scratch_bytes(workspace, dims[0])
     _run_shared(dims, q, k_prefix, v_prefix, k_own, v_own, own_len, sinks, o, lse, _int32("window", window),
                 float(scale), P, workspace, nbytes, stream)

@@ -155,14 +155,15 @@ PyObject* call(Py_ssize_t n, Py_ssize_t want, F&& f) {
   }
 }
 
-// (q, k_prefix, v_prefix, k_own, v_own, own_len, window, scale, prefix_len or None, sinks or None) -> (o, lse)
+// (q, k_prefix or None, v_prefix or None, k_own, v_own, own_len, window, scale, prefix_len or None, sinks or None)
+// -> (o, lse)
 PyObject* forward_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return call(n, 10, [&]() -> PyObject* {
-    const at::Tensor *q = tensor(a[0]), *kp = tensor(a[1]), *vp = tensor(a[2]), *ko = tensor(a[3]), *vo = tensor(a[4]),
-                     *len = tensor(a[5]), *sinks = tensor_or_null(a[9]);
-    if (q->dim() != 4 || kp->dim() != 3 || ko->dim() != 4) throw NotThisWay{};
+    const at::Tensor *q = tensor(a[0]), *kp = tensor_or_null(a[1]), *vp = tensor_or_null(a[2]), *ko = tensor(a[3]),
+                     *vo = tensor(a[4]), *len = tensor(a[5]), *sinks = tensor_or_null(a[9]);
+    if (q->dim() != 4 || !kp != !vp || (kp && kp->dim() != 3) || ko->dim() != 4) throw NotThisWay{};
     const int B = dim32(q->size(0)), Hq = dim32(q->size(1)), Lq = dim32(q->size(2)), D = dim32(q->size(3));
-    const int Hkv = dim32(ko->size(1)), rows = dim32(ko->size(2)), prefix_rows = dim32(kp->size(1));
+    const int Hkv = dim32(ko->size(1)), rows = dim32(ko->size(2)), prefix_rows = kp ? dim32(kp->size(1)) : 0;
     const int window = int32(a[6]), P = a[8] == Py_None ? prefix_rows : int32(a[8]);
     const float scale = real(a[7]);
     const int dev = current(q);

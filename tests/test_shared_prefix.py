@@ -535,3 +535,29 @@ def test_binding_refuses_such_workspaces():
         with pytest.raises(ValueError, match="workspace"):
             swa.swa_attn_qk_rope_bwd(x, None, dw, None, None, dy, None, None, x.clone(), None, None, dw.clone(), None,
                                      1e-6, workspace=ws)
+
+
+@pytest.mark.gpu
+def test_no_prefix_at_all():
+    """None for the prefix (a NULL of the C call) is a prefix of no rows, on either marshalling path; one of k and v
+    alone is refused, and so is a length of a prefix that is not there."""
+    import numpy as np
+
+    import sliding_window_attention_gb300 as swa
+
+    a = {n: None if t is None else t.cuda() for n, t in make(3, 4, 2, 1, 128, 0, 40, 2).items()}
+    n = torch.tensor([40, 0, 7], dtype=torch.int32, device="cuda")
+    rest = (a["ko"], a["vo"], n)
+    want = swa.forward_shared(a["q"], a["kp"], a["vp"], *rest, 0, 0.1)
+    check(want, reference(make(3, 4, 2, 1, 128, 0, 40, 2), [40, 0, 7], 0, 0, 0.1))
+    o, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+    ws = torch.empty(swa.fwd_workspace_bytes_shared(3, 4, 2, 1, 0, 40, 128, 0), dtype=torch.uint8, device="cuda")
+    swa.swa_attn_fwd_shared(a["q"], None, None, *rest, None, o, lse, 0, 0.1, workspace=ws)
+    for got in ((o, lse), *(swa.forward_shared(a["q"], None, None, *rest, w, 0.1) for w in (0, np.int64(0)))):
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for w in (0, np.int64(0)):
+        for prefix in ((a["kp"], None), (None, a["vp"])):
+            with pytest.raises(ValueError, match="together"):
+                swa.forward_shared(a["q"], *prefix, *rest, w, 0.1)
+        with pytest.raises(swa.SwaError):
+            swa.forward_shared(a["q"], None, None, *rest, w, 0.1, prefix_len=1)
