@@ -617,3 +617,93 @@ def test_running_out_of_memory_keeps_its_type():
     finally:
         torch.cuda.set_per_process_memory_fraction(1.0)
     assert calls[0]()[0].shape == (1, 2, 400000, 64)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,L,Hq,Hkv,D", [(1, 2000, 8, 4, 128), (2, 500, 4, 2, 512), (1, 9000, 2, 1, 64)])
+def test_adjacent_backwards_take_turns_in_one_workspace(B, L, Hq, Hkv, D):
+    """Backwards of two inputs in turn, captured so that nothing lies between them, with one workspace: partial sums
+    that were overwritten before they had been read would change the scales' gradients."""
+    import sliding_window_attention_gb300 as swa
+
+    calls, x = 12, []
+    for i in range(2):
+        (q, k, v), g = fused(B, L, Hq, Hkv, D, 60 + i)
+        w = 1 + 0.2 * torch.randn(D, generator=g)
+        dy = [torch.randn((B, h, L, D), generator=g) for h in (Hq, Hkv, Hkv)]
+        q, k, _ = dev_rows((q, k, v), 0)
+        x.append((q, k, *cuda(w, w, freqs(D // 2), *dy)))
+    ws = torch.empty(swa.qk_rope_bwd_workspace_bytes(B, L, D), dtype=torch.uint8, device="cuda")
+    outs = [torch.empty((B, L, Hq + 2 * Hkv, D), dtype=BF, device="cuda").split((Hq, Hkv, Hkv), 2) +
+            tuple(torch.empty((2, D), device="cuda")) for _ in range(calls)]
+
+    def run_all(wait):
+        for i in range(calls):
+            swa.swa_attn_qk_rope_bwd(*x[i % 2], *outs[i], EPS, workspace=ws)
+            if wait:
+                torch.cuda.synchronize()
+
+    run_all(True)
+    want = [[t.clone() for t in o] for o in outs[:2]]
+    assert not torch.equal(want[0][3], want[1][3])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run_all(False)
+    for _ in range(5):
+        for o in outs:
+            for t in o:
+                t.fill_(math.nan)
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, o in enumerate(outs):
+            for a, b in zip(o, want[i % 2]):
+                assert torch.equal(a, b), i
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("L,Hq,Hkv,D,W", [(1000, 8, 4, 512, 0), (1500, 4, 2, 256, 300), (2000, 8, 4, 128, 0)])
+def test_attention_backward_then_rotation_backward(L, Hq, Hkv, D, W):
+    """The rotation's backward right behind the attention's, whose dK/dV and dQ passes run side by side: it may read
+    none of dq, dk, dv before both have ended.  Two inputs in turn, captured, in the same gradient buffers, so that
+    what is read too early is the other input's.  Against the same calls waited for."""
+    import sliding_window_attention_gb300 as swa
+
+    calls, x, scale = 6, [], D ** -0.5
+    f = freqs(D // 2).cuda()
+    for i in range(2):
+        (q, k, v), g = fused(1, L, Hq, Hkv, D, 70 + i)
+        rows = dev_rows((q, k, v), 0)
+        qr, kr, vr = swa.qk_rope(*rows, None, None, f, EPS)
+        o, lse = swa.forward(qr, kr, vr, W, scale)
+        x.append((rows, qr, kr, vr, o, lse, torch.randn((1, Hq, L, D), generator=g).to(BF).cuda()))
+    w = torch.ones(D, device="cuda")
+    dq, dk, dv = (torch.empty((1, h, L, D), device="cuda") for h in (Hq, Hkv, Hkv))
+    ws = torch.empty(swa.bwd_workspace_bytes(1, Hq, Hkv, L, D, W), dtype=torch.uint8, device="cuda")
+    ws2 = torch.empty(swa.qk_rope_bwd_workspace_bytes(1, L, D), dtype=torch.uint8, device="cuda")
+    outs = [torch.empty((1, L, Hq + 2 * Hkv, D), dtype=BF, device="cuda").split((Hq, Hkv, Hkv), 2) +
+            tuple(torch.empty((2, D), device="cuda")) for _ in range(calls)]
+
+    def run_all(wait):
+        for i in range(calls):
+            rows, *attn = x[i % 2]
+            swa.swa_attn_bwd(*attn, dq, dk, dv, W, scale, workspace=ws)
+            if wait:
+                torch.cuda.synchronize()
+            swa.swa_attn_qk_rope_bwd(rows[0], rows[1], w, w, f, dq, dk, dv, *outs[i], EPS, workspace=ws2)
+            if wait:
+                torch.cuda.synchronize()
+
+    run_all(True)
+    assert swa.swa_attn_get_status() == 0
+    want = [[t.clone() for t in o] for o in outs[:2]]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run_all(False)
+    for _ in range(4):
+        for t in (dq, dk, dv):
+            t.fill_(math.nan)
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, o in enumerate(outs):
+            for a, b in zip(o, want[i % 2]):
+                assert torch.equal(a, b), i

@@ -561,3 +561,87 @@ def test_no_prefix_at_all():
                 swa.forward_shared(a["q"], *prefix, *rest, w, 0.1)
         with pytest.raises(swa.SwaError):
             swa.forward_shared(a["q"], None, None, *rest, w, 0.1, prefix_len=1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,Hq,Hkv,Lq,D,P,rows", [(6, 8, 4, 1, 128, 900, 64), (40, 8, 2, 1, 128, 2000, 100),
+                                                  (16, 16, 2, 4, 64, 700, 200), (12, 32, 4, 1, 512, 600, 150)])
+def test_adjacent_calls_take_turns_in_one_workspace(B, Hq, Hkv, Lq, D, P, rows):
+    """Calls on two inputs in turn, captured so that nothing lies between them on the stream and no host time keeps
+    them apart, with one workspace: a call that wrote partials or the split before the merge of the one before had
+    read its own would change that one's result.  Against calls that are waited for."""
+    import sliding_window_attention_gb300 as swa
+
+    calls = 12
+    x = []
+    for i in range(2):
+        a = {n: None if t is None else t.cuda() for n, t in make(B, Hq, Hkv, Lq, D, P, rows, 50 + i).items()}
+        n = torch.tensor([(29 * b + 31 * i) % rows + 1 for b in range(B)], dtype=torch.int32, device="cuda")
+        x.append((a["q"], a["kp"], a["vp"], a["ko"], a["vo"], n, None))
+    ws = torch.empty(swa.fwd_workspace_bytes_shared(B, Hq, Hkv, Lq, P, rows, D, 0), dtype=torch.uint8, device="cuda")
+    outs = [(torch.full_like(x[0][0], math.nan), torch.full((B, Hq, Lq), math.nan, device="cuda")) for _ in range(calls)]
+
+    def run_all(wait):
+        for i in range(calls):
+            swa.swa_attn_fwd_shared(*x[i % 2], *outs[i], 0, 0.1, workspace=ws)
+            if wait:
+                torch.cuda.synchronize()
+
+    run_all(True)
+    want = [(o.clone(), lse.clone()) for o, lse in outs[:2]]
+    assert not torch.equal(want[0][0], want[1][0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run_all(False)
+    for _ in range(5):
+        for o, lse in outs:
+            o.fill_(math.nan)
+            lse.fill_(math.nan)
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, (o, lse) in enumerate(outs):
+            assert torch.equal(o, want[i % 2][0]) and torch.equal(lse, want[i % 2][1]), i
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,Hq,Hkv,D,P,rows", [(6, 8, 2, 128, 300, 90), (30, 4, 2, 64, 1000, 200), (8, 32, 4, 512, 400, 140)])
+def test_layers_back_to_back(B, Hq, Hkv, D, P, rows):
+    """Append, attention, append, attention, ... with nothing between them, captured: each append writes the rows that
+    the attention before it has read last, as a model's layers do that share a cache, and takes its queries' buffer
+    again.  Against the same steps waited for one by one."""
+    import sliding_window_attention_gb300 as swa
+
+    steps = 12
+    g = torch.Generator(device="cuda").manual_seed(14)
+    x = torch.randn((steps, B, 1, Hq + 2 * Hkv, D), device="cuda", generator=g).to(BF)
+    kp, vp = (torch.randn((Hkv, P, D), device="cuda", generator=g).to(BF) for _ in range(2))
+    kc, vc = (torch.randn((B, Hkv, rows, D), device="cuda", generator=g).to(BF) for _ in range(2))
+    n = torch.tensor([(37 * b) % rows + 1 for b in range(B)], dtype=torch.int32, device="cuda")
+    f = (10000.0 ** (-torch.arange(D // 2, dtype=torch.float64) / (D // 2))).cuda()
+    q = torch.empty((B, Hq, 1, D), dtype=BF, device="cuda")
+    ws = torch.empty(swa.fwd_workspace_bytes_shared(B, Hq, Hkv, 1, P, rows, D, 0), dtype=torch.uint8, device="cuda")
+    outs = [(torch.empty_like(q), torch.empty((B, Hq, 1), device="cuda")) for _ in range(steps)]
+
+    def run_all(wait):
+        for i in range(steps):
+            xq, xk, xv = x[i].split((Hq, Hkv, Hkv), 2)
+            swa.swa_attn_qk_rope_fwd(xq, xk, xv, None, None, f, q, kc, vc, 1e-6, None, n, P)
+            if wait:
+                torch.cuda.synchronize()
+            swa.swa_attn_fwd_shared(q, kp, vp, kc, vc, n, None, *outs[i], 0, 0.1, workspace=ws)
+            if wait:
+                torch.cuda.synchronize()
+
+    run_all(True)
+    want = [(o.clone(), lse.clone()) for o, lse in outs]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run_all(False)
+    for _ in range(5):
+        for o, lse in outs:
+            o.fill_(math.nan)
+            lse.fill_(math.nan)
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, (o, lse) in enumerate(outs):
+            assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1]), i
