@@ -294,9 +294,11 @@ int swa_attn_fwd_shared(const swa_bf16* q, const swa_bf16* k_prefix, const swa_b
  *   q_out        [B, Hq, L, D] bf16
  *
  * All of them device memory, data 16-byte aligned; outputs may not overlap
- * inputs.  Angles are exact to 2^-31 of a turn at any position (they are
- * formed modulo one turn in 64-bit integers from the fp64 frequencies); the
- * norm, the sums and the rotation are fp32, rounded to bf16 once.  With
+ * inputs.  An angle is within 2^-25 of a turn, and 2^-52 of the turns made,
+ * of the product of position and frequency at any position (it is formed
+ * modulo one turn in 64-bit integers, from the fp64 frequency); the norm, the
+ * sums and the rotation are fp32, rounded to bf16 once (the sum of a row's
+ * squares has to be within fp32's range).  With
  * kv_len this is the cache update of a generation step whose attention is
  * swa_attn_fwd_shared with own_len = kv_len and pos0 = prefix_len.
  * D in {64, 128, 256, 512}; rot_dim a multiple of 16 in [0, D]; eps > 0.

@@ -16,11 +16,13 @@
 // Angles.  position * frequency loses its fraction in fp32 for far positions
 // (half an ulp at 1e6 radians is 0.03), so frequencies come as doubles and a
 // CTA turns each once into a 64-bit fixed-point fraction of a full turn;
-// position times that fraction, modulo 2^64, is the exact phase (integer
-// multiplication wraps as angles do), and sincospif takes its top 32 bits.
+// position times that fraction, modulo 2^64, loses nothing more (integer
+// multiplication wraps as angles do).  The step carries the rounding of two
+// fp64 factors and their product, 2^-52 of the turns made at most, and
+// sincospif takes the phase's top 32 bits as a float: 2^-26 of a turn.
 //
 // All sums, the norm and the rotation are fp32; the only rounding to fewer
-// bits is the one of each output to bf16 (half a step, 2^-9 relative).
+// bits is the one of each output to bf16 (half a step, 2^-8 of the value).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>

@@ -707,3 +707,32 @@ def test_attention_backward_then_rotation_backward(L, Hq, Hkv, D, W):
         for i, o in enumerate(outs):
             for a, b in zip(o, want[i % 2]):
                 assert torch.equal(a, b), i
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("p", [1, 16384, 999983, 2 ** 31 - 1, -2 ** 31])
+def test_angles_are_as_close_as_documented(p):
+    """An angle is within 2^-25 of a turn and 2^-52 of the turns made.  Where the cosine crosses zero, bf16 shows it:
+    for pairs (1, 0) turned to a quarter turn and at most 2^-22 more, the first element is r cos of at most 2^-19,
+    whose half step is 2^-28 r.  (The reference's turns are exact fractions of the fp64 frequencies, with 2 pi to 60
+    digits.)  r carries 2^-18 as elsewhere, and r (0.5 + eps)^(1/2) is 1 but for that."""
+    from fractions import Fraction
+
+    import sliding_window_attention_gb300 as swa
+
+    D, pairs = 512, 256
+    two_pi = Fraction("6.283185307179586476925286766559005768394338798750211641949889")
+    whole = [abs(p) * i // (8 * pairs) for i in range(pairs)]  # turns made, frequencies up to 2 pi / 8
+    f = [float(two_pi * (m + Fraction(1, 4) + Fraction(i % 16, 1 << 26)) / abs(p)) for i, m in enumerate(whole)]
+    x = torch.zeros((1, 1, 1, D), dtype=BF, device="cuda")
+    x[..., :pairs] = 1
+    y = swa.qk_rope(x, None, None, None, None, torch.tensor(f, dtype=torch.float64, device="cuda"), EPS,
+                    positions=torch.tensor([[p]], dtype=torch.int32, device="cuda"))[0][0, 0, 0].double().cpu()
+    r = (0.5 + EPS) ** -0.5
+    for i in range(pairs):
+        turns = p * Fraction(f[i]) / two_pi
+        frac = turns - math.floor(turns)
+        quarter = Fraction(1, 4) if p > 0 else Fraction(3, 4)
+        ref = -r * math.sin(float(two_pi * (frac - quarter))) * (1 if p > 0 else -1)
+        off = 2 * math.pi * (2.0 ** -25 + 2.0 ** -52 * abs(float(turns)))
+        assert abs(ref) <= 2.0 ** -18 and abs(float(y[i]) - ref) <= (HALF_STEP + F32) * abs(ref) + 1.01 * r * off, i
