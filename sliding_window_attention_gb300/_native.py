@@ -792,6 +792,9 @@ def prefix_positions(B: int, L: int, prompt_len: int, chosen_len: int, device):
     window of swa_attn_fwd_prefix measures it."""
     import torch
 
+    if prompt_len < 0 or chosen_len < 0 or prompt_len + chosen_len > L:
+        raise ValueError("a shared-prefix sequence needs prompt_len >= 0, chosen_len >= 0 and prompt_len + chosen_len <= L, "
+                         f"got {prompt_len}, {chosen_len}, {L}")
     p = torch.arange(L, dtype=torch.int32, device=device)
     if chosen_len > 0:
         p[prompt_len + chosen_len:] -= chosen_len

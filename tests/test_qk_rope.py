@@ -736,3 +736,15 @@ def test_angles_are_as_close_as_documented(p):
         ref = -r * math.sin(float(two_pi * (frac - quarter))) * (1 if p > 0 else -1)
         off = 2 * math.pi * (2.0 ** -25 + 2.0 ** -52 * abs(float(turns)))
         assert abs(ref) <= 2.0 ** -18 and abs(float(y[i]) - ref) <= (HALF_STEP + F32) * abs(ref) + 1.01 * r * off, i
+
+
+def test_prefix_positions():
+    """The rejected response starts behind the prompt again; what swa_attn_fwd_prefix refuses is refused."""
+    import sliding_window_attention_gb300 as swa
+
+    assert swa.prefix_positions(2, 7, 2, 3, "cpu").tolist() == [[0, 1, 2, 3, 4, 2, 3]] * 2
+    assert swa.prefix_positions(1, 4, 0, 0, "cpu").tolist() == [[0, 1, 2, 3]]
+    assert swa.prefix_positions(1, 4, 1, 3, "cpu").tolist() == [[0, 1, 2, 3]]
+    for prompt, chosen in ((-5, 3), (2, -1), (5, 3)):
+        with pytest.raises(ValueError, match="shared-prefix"):
+            swa.prefix_positions(1, 7, prompt, chosen, "cpu")
