@@ -623,11 +623,15 @@ __device__ __forceinline__ bool produce(const SharedParams& p, unsigned char* ba
   constexpr int AHEAD = OWN ? K::OWN_AHEAD : NSLOT;
   const SharedGeom& g = p.g;
   Walk wk = w0, wv = w0;
-  // K and V are the first to leave L2, so that the partials stay there: own
-  // caches are read once a call, and a prefix of more than a quarter of L2 would
-  // not last until the next (64 requests over 16,384 prefix keys, D = 512: 105 us,
-  // else 109; 32 of up to 1,024 own keys, D = 256: 48.5, else 50.9; but 32 over a
-  // prefix of 17 MB, D = 128, that is kept: 14.5, else 15.7).
+  // Own caches, which a call reads once, are the first to leave L2, so that the
+  // partials stay there (32 of up to 1,024 keys, D = 256: 48.5 us, else 50.9), and
+  // so is a prefix of which a call sees more than a quarter of L2: 64 requests of
+  // D = 512 over 268 MB take 103.5 us, else 110.6 (after 256 MB of other data, as
+  // between a model's steps, 109.5 and 113.8).  A smaller one may find part of
+  // itself again: three prefixes of 17 MB in turn, 32 requests, D = 128, 14.4 us,
+  // else 15.8; windows that see 17 of 67 MB, D = 256, 47.0, else 47.5.  At 34 MB the
+  // two meet: 17.2 us kept and 18.7 on one prefix over and over, 19.2 and 19.0 on
+  // three in turn.  After other data all of 17 to 67 MB are within 1 % either way.
   const uint64_t policy = l2_policy(OWN || p.prefix_pass);
   auto load_tile = [&](Walk& w, const CUtensorMap* m) -> bool {
     const int key0 = w.key0();
@@ -1133,7 +1137,8 @@ cudaError_t shared_d(const SharedGeom& g, const SharedArgs& a, void* ws, int* st
   p.po_o = reinterpret_cast<float*>(wb + w.po_o);
   p.status = status;
   const long long nseg = (long long)g.Hkv * s.nrb;
-  p.prefix_pass = (double)g.Hkv * g.P * D * 4 > 32.0e6;
+  const long long seen = g.W > 0 && (long long)g.W + g.Lq < g.P ? (long long)g.W + g.Lq : g.P;  // prefix keys, at most
+  p.prefix_pass = (double)g.Hkv * seen * D * 4 > 32.0e6;
   p.most = nseg < kPieces ? (int)(kPieces / nseg) : 1;
   auto kern = shared_kernel<D, NP>;
   static std::atomic<unsigned long long> done{0};
