@@ -25,14 +25,15 @@
 // second kernel merges a row's partials.
 //
 // Bounds, of 64 requests of 32 heads (4 of them kv) over 16,384 prefix keys and
-// up to 1,024 of their own, D = 512 (105 us): the prefix's tiles, 2.5 us each on
-// 128 of the CTAs, are bound by shared memory (a tile's operands are 393 KB of
-// MMA reads and 256 KB of TMA writes: 2.5 us at 128 bytes a clock); the own
-// caches by HBM (32 caches of up to 1,024 keys at D = 256: 5.9 TB/s of a whole call).  At D <=
-// 128 a prefix tile is bound by the softmax's latency (1.2 us for 64 rows, 2.5
-// for 128), and a short call by what comes before and behind: lengths 0.5 us,
-// split 0.7, first tile 1.3, merge 1.8 (4 requests over 1,024 keys, D = 128: 7.9
-// us, of which 1.6 are tiles).
+// up to 1,024 of their own, D = 512 (104 us): the prefix's tiles, 2.2 us each
+// where L2 has them, are bound by shared memory (a tile's operands are 393 KB of
+// MMA reads and 256 KB of TMA writes: 2.5 us if each byte took its turn at 128 a
+// clock); the own caches by HBM (32 caches of up to 1,024 keys at D = 256: 6.0
+// TB/s of a whole call).  At D <= 128 a prefix tile is bound by the softmax's
+// latency (1.3 us for 64 rows, 1.8 for 128 at D = 64 and 2.0 at D = 128), and a
+// short call by what comes before and behind: lengths 0.5 us, split 0.7, first
+// tile 1.3, merge 1.8 (4 requests over 1,024 keys, D = 128: 7.9 us, of which 1.6
+// are tiles).
 //
 // Products are transposed, as in the decode kernel: S^T (128 keys x N rows) =
 // K_tile Q^T and O^T (D x N rows) += V_tile^T P^T, so the keys fill the MMA's
@@ -219,7 +220,8 @@ struct ShKernel {
   static constexpr int NDC = (D + 127) / 128;    // 128-column blocks of O^T
   static constexpr int SLOT = CPS * T * 128;
   static constexpr int GROUPS = N / A::NG;       // softmax warpgroups of the prefix; own segments take turns in two
-  // What work takes, in quarter microseconds: a prefix tile, an own tile, what a
+  // The split's weights, in about quarter microseconds of a full GPU (a tile whose
+  // operands L2 has takes up to a third less): a prefix tile, an own tile, what a
   // piece adds to its tiles, what an own run adds
   static constexpr int WP = N == 128 ? (D == 256 ? 12 : D == 128 ? 10 : 9)
                                      : (D == 512 ? 11 : D == 256 ? (N == 64 ? 7 : 9) : (N == 64 ? 5 : 4));
