@@ -442,6 +442,8 @@ def _marshal():
 def _check(device, specs):
     """Every tensor dense, on `device` (an index) and of its type and shape."""
     for name, t, dtype, shape in specs:
+        if t is None:
+            raise ValueError(f"{name} is missing: a {dtype} tensor of shape {tuple(shape)} is needed")
         if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
                              f"got {t.dtype} {tuple(t.shape)}{'' if t.is_contiguous() else ' (strided)'}")

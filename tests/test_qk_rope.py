@@ -748,3 +748,23 @@ def test_prefix_positions():
     for prompt, chosen in ((-5, 3), (2, -1), (5, 3)):
         with pytest.raises(ValueError, match="shared-prefix"):
             swa.prefix_positions(1, 7, prompt, chosen, "cpu")
+
+
+@pytest.mark.gpu
+def test_missing_gradients_are_named():
+    """Keys without dk, or no dq: a ValueError, like every other refusal of the binding."""
+    import sliding_window_attention_gb300 as swa
+
+    (q, k, v), _ = fused(2, 4, 2, 1, 64, 1)
+    q, k, _ = dev_rows((q, k, v), 0)
+    dq = torch.zeros((2, 2, 4, 64), device="cuda")
+    for grads, name in (((dq, None, None), "dk"), ((None, None, None), "dq")):
+        with pytest.raises(ValueError, match=name + " is missing"):
+            swa.qk_rope_backward(q, k, None, None, None, *grads, EPS)
+
+
+def test_a_missing_tensor_is_named():
+    from sliding_window_attention_gb300 import _native
+
+    with pytest.raises(ValueError, match="dk is missing"):
+        _native._check(-1, (("dk", None, torch.float32, (2, 3)),))
