@@ -609,13 +609,18 @@ def test_running_out_of_memory_keeps_its_type():
     torch.cuda.empty_cache()
     total = torch.cuda.get_device_properties(torch.cuda.current_device()).total_memory
     torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + (1 << 20)) / total)
+    held = []
     try:
+        with pytest.raises(torch.OutOfMemoryError):  # what earlier tests left in the allocator's pool
+            while True:
+                held.append(torch.empty(16 << 20, dtype=torch.uint8, device="cuda"))
         for call in calls:
             for pos0 in (0, np.int64(0)):
                 with pytest.raises(torch.OutOfMemoryError):
                     call(pos0=pos0)
     finally:
         torch.cuda.set_per_process_memory_fraction(1.0)
+        held.clear()
     assert calls[0]()[0].shape == (1, 2, 400000, 64)
 
 
