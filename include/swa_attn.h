@@ -103,7 +103,8 @@ typedef uint16_t swa_bf16; /* bf16 bit pattern */
 #define SWA_ERR_SCRATCH_LAYOUT -15 /* head dim 512: device cannot hold the per-SM tile scratch (see below) */
 #define SWA_ERR_BAD_PLAN -16      /* shared-prefix plan: prompt_len or chosen_len out of range */
 #define SWA_ERR_BAD_ROPE -17      /* norm and rotation: rot_dim, eps, weight_offset or a token stride out of range */
-#define SWA_ERR_BAD_CACHE -18     /* cache rows or prefix_len out of range */
+#define SWA_ERR_BAD_CACHE -18     /* cache rows, prefix_len, a scale's block or a range of rows out of range */
+#define SWA_ERR_BAD_STRIDE -19    /* a stride is no multiple of 8 elements, negative, or too small */
 
 /*
  * Workspace bytes swa_attn_fwd needs for this shape (may be 0; a NULL
@@ -326,6 +327,97 @@ int swa_attn_qk_rope_bwd(const swa_bf16* q, const swa_bf16* k, long long q_strid
                          swa_bf16* dv_in, long long dq_stride, long long dk_stride, long long dv_stride, float* dwq,
                          float* dwk, int B, int Hq, int Hkv, int L, int D, int rot_dim, int interleaved, int pos0,
                          float eps, float weight_offset, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * A cache of keys and values in 8 bits: half the memory, and half the bytes
+ * that a generation step reads.
+ *
+ *   k_cache, v_cache  [B, Hkv, kv_rows, D]  e4m3 codes (bytes)
+ *   k_scale, v_scale  [B, Hkv, NB]          fp32, NB = ceil(kv_rows / block)
+ *
+ * The value at row r is code * scale[r / block]; block is 16, 32, 64 or 128
+ * tokens.  kv_len [B] int32 (device memory, read when the kernels run, so that
+ * a captured call replays with the lengths of then) counts each request's
+ * tokens; a negative length marks an empty place of the batch, one above
+ * kv_rows counts as kv_rows.  D in {64, 128, 256, 512}; device pointers, data
+ * 16-byte and scales 4-byte aligned.  Asynchronous on `stream`; errors as for
+ * swa_attn_fwd, and SWA_ERR_BAD_CACHE (kv_rows, block, rows), SWA_ERR_BAD_STRIDE.
+ *
+ * swa_attn_cache8_append quantises L new tokens a request and writes them:
+ *
+ *   k, v    bf16 [B, Hkv, L, D] by three strides in elements (request, head,
+ *           token; multiples of 8, a head's D elements dense): the outputs of
+ *           swa_attn_qk_rope_fwd, or rows of a projection as they are.  Either
+ *           may be NULL, with its strides, codes and scales then not used
+ *   kv_len  NULL: token l goes to row l (L <= kv_rows).  Otherwise the tokens
+ *           are the last L of each request's first kv_len[b] rows: token l goes
+ *           to row kv_len[b] - L + l; rows outside [0, kv_rows) are not written
+ *
+ * A block's scale is the smallest power of two s >= 2^-64 with max |x| <= 448 s
+ * over the tokens written by the call; codes are x / s rounded to nearest, ties
+ * to even.  A block that already has tokens (rows before the first new one)
+ * keeps its scale if the new tokens fit, max |x| <= 448 s; otherwise it gets
+ * the scale of the new tokens, and its older codes are written again for it.
+ * That only moves their exponents: a value changes when it falls below 2^-6 s,
+ * by at most 2^-10 s.  Older scales have to be positive and finite.  Rows behind the
+ * last new one are left as they were.  A block in which no row is written
+ * keeps its scale; one that begins with a new token gets a new scale whatever
+ * it held.  Tokens must be finite; magnitudes above 2^127 may read back as
+ * infinity.  Equal calls give equal bits.
+ *
+ * swa_attn_cache8_read writes rows row0 .. row0 + rows - 1 of the cache as bf16
+ * [B, Hkv, rows, D] (code * scale, rounded once; exact where the scale is a
+ * power of two and nothing is subnormal), zeros for rows at or behind the
+ * request's length (none with kv_len NULL).  k_out or v_out may be NULL.  With
+ * it a prompt's next chunk runs through swa_attn_fwd_ex.
+ */
+int swa_attn_cache8_append(const swa_bf16* k, const swa_bf16* v, long long k_stride_b, long long k_stride_h,
+                           long long k_stride_t, long long v_stride_b, long long v_stride_h, long long v_stride_t,
+                           const int32_t* kv_len, uint8_t* k_cache, uint8_t* v_cache, float* k_scale, float* v_scale,
+                           int B, int Hkv, int L, int D, int kv_rows, int block, void* stream);
+int swa_attn_cache8_read(const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale, const float* v_scale,
+                         const int32_t* kv_len, swa_bf16* k_out, swa_bf16* v_out, int B, int Hkv, int D, int kv_rows,
+                         int block, int row0, int rows, void* stream);
+
+/*
+ * Attention of a generation step over a cache in 8 bits (as above), each
+ * request with its own length:
+ *
+ *   q      [B, Hq, Lq, D]  bf16, the step's Lq query rows a request
+ *   sinks  [Hq] fp32       one sink logit a head (see swa_attn_fwd_sinks), or NULL
+ *   o      [B, Hq, Lq, D]  bf16
+ *   lse    [B, Hq, Lq]     fp32
+ *
+ * Query row i of request b sits at a = kv_len[b] - Lq + i (the step's own keys
+ * are in the cache before the call) and sees the keys j <= a, with a - j <
+ * window when window > 0.  A row that sees no key (a < 0) gets o = 0 and lse =
+ * -inf (with a sink logit c: lse = c).  A negative kv_len[b] marks an empty
+ * place of the batch: its o and lse rows are left as they were.
+ *
+ * This is swa_attn_fwd_shared without a prefix on the cache's values, but the
+ * tensor cores multiply the codes as they are: q is split into two e4m3 parts
+ * (exact down to 2^-22 of a row's largest element) and the softmax's weights,
+ * times the values' scales, into three e5m2 parts of an fp16 number (2^-11,
+ * and 2^-27 of the row's largest weight for those below).  Products are summed
+ * in fp32, as are the row sums and the partial outputs; o is rounded to bf16
+ * once.  Within a request and head the values' scales that matter may lie up to
+ * 2^100 apart.  Scales are positive and finite; of rows within the lengths they
+ * and the codes must not be NaN, whatever stands behind is not used.  Many
+ * query rows a kv head (Hq / Hkv * Lq) read the cache once for each 16 of them.
+ * The result does not depend on what else runs, but it does on the other
+ * requests' lengths, in its last bits: they move the places where the key
+ * ranges are split.  Equal calls give equal bits.
+ *
+ * workspace: at least swa_attn_fwd_workspace_bytes_cache8(...) bytes, 256-byte
+ * aligned, with any content; calls that may overlap need separate ones.  Make
+ * the first call on a device outside stream capture.  Alignment, streams, status
+ * word and errors are as for swa_attn_fwd, and SWA_ERR_BAD_CACHE.
+ */
+size_t swa_attn_fwd_workspace_bytes_cache8(int B, int Hq, int Hkv, int Lq, int kv_rows, int D, int block, int window);
+int swa_attn_fwd_cache8(const swa_bf16* q, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale,
+                        const float* v_scale, const int32_t* kv_len, const float* sinks, swa_bf16* o, float* lse,
+                        int B, int Hq, int Hkv, int Lq, int kv_rows, int D, int block, int window, float scale,
+                        void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Sequence sharding (context parallelism) with a halo: a sequence split into

@@ -11,13 +11,18 @@ from ._native import (  # noqa: F401
     bwd_workspace_bytes,
     bwd_workspace_bytes_ex,
     bwd_workspace_bytes_prefix,
+    cache8_append,
+    cache8_read,
     forward,
+    forward_cache8,
     forward_shared,
     fwd_workspace_bytes,
+    fwd_workspace_bytes_cache8,
     fwd_workspace_bytes_ex,
     fwd_workspace_bytes_prefix,
     fwd_workspace_bytes_shared,
     load,
+    make_cache8,
     prefix_positions,
     profile_begin,
     profile_end,
@@ -30,7 +35,10 @@ from ._native import (  # noqa: F401
     swa_attn_bwd_ex,
     swa_attn_bwd_prefix,
     swa_attn_bwd_sinks,
+    swa_attn_cache8_append,
+    swa_attn_cache8_read,
     swa_attn_fwd,
+    swa_attn_fwd_cache8,
     swa_attn_fwd_ex,
     swa_attn_fwd_prefix,
     swa_attn_fwd_shared,
@@ -50,4 +58,6 @@ __all__ = [
     "forward_shared", "fwd_workspace_bytes_shared", "swa_attn_fwd_shared", "prefix_positions", "qk_rope",
     "qk_rope_append", "qk_rope_backward", "qk_rope_bwd_workspace_bytes", "swa_attn_qk_rope_fwd",
     "swa_attn_qk_rope_bwd",
+    "cache8_append", "cache8_read", "forward_cache8", "fwd_workspace_bytes_cache8", "make_cache8",
+    "swa_attn_cache8_append", "swa_attn_cache8_read", "swa_attn_fwd_cache8",
 ]

@@ -43,6 +43,10 @@ EXPORTED = (
     "swa_attn_qk_rope_fwd",
     "swa_attn_qk_rope_bwd_workspace_bytes",
     "swa_attn_qk_rope_bwd",
+    "swa_attn_cache8_append",
+    "swa_attn_cache8_read",
+    "swa_attn_fwd_workspace_bytes_cache8",
+    "swa_attn_fwd_cache8",
 )
 
 _lock = threading.Lock()
@@ -131,6 +135,15 @@ def load(path: str | None = None) -> ctypes.CDLL:
         lib.swa_attn_qk_rope_bwd_workspace_bytes.restype = Z
         lib.swa_attn_qk_rope_bwd.argtypes = [P] * 2 + [LL] * 2 + [P] * 10 + [LL] * 3 + [P] * 2 + [I] * 8 + [F, F, P, Z, P]
         lib.swa_attn_qk_rope_bwd.restype = I
+        # a cache in 8 bits: B, Hkv, [L,] D, kv_rows, block[, row0, rows]; attention: B, Hq, Hkv, Lq, kv_rows, D, block, window
+        lib.swa_attn_cache8_append.argtypes = [P] * 2 + [LL] * 6 + [P] * 5 + [I] * 6 + [P]
+        lib.swa_attn_cache8_append.restype = I
+        lib.swa_attn_cache8_read.argtypes = [P] * 7 + [I] * 7 + [P]
+        lib.swa_attn_cache8_read.restype = I
+        lib.swa_attn_fwd_workspace_bytes_cache8.argtypes = [I] * 8
+        lib.swa_attn_fwd_workspace_bytes_cache8.restype = Z
+        lib.swa_attn_fwd_cache8.argtypes = [P] * 9 + [I] * 8 + [F, P, Z, P]
+        lib.swa_attn_fwd_cache8.restype = I
         _lib = lib
         return lib
 
@@ -434,7 +447,9 @@ def _marshal():
                                    "(python -c 'import __graft_entry__ as g; g.build()')") from e
             m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
                 lib.swa_attn_fwd_workspace_bytes_shared, lib.swa_attn_fwd_shared, lib.swa_attn_qk_rope_fwd,
-                lib.swa_attn_qk_rope_bwd_workspace_bytes, lib.swa_attn_qk_rope_bwd)), torch.OutOfMemoryError)
+                lib.swa_attn_qk_rope_bwd_workspace_bytes, lib.swa_attn_qk_rope_bwd,
+                lib.swa_attn_fwd_workspace_bytes_cache8, lib.swa_attn_fwd_cache8, lib.swa_attn_cache8_append,
+                lib.swa_attn_cache8_read)), torch.OutOfMemoryError)
             _fast = m
         return _fast
 
@@ -801,3 +816,195 @@ def prefix_positions(B: int, L: int, prompt_len: int, chosen_len: int, device):
     if chosen_len > 0:
         p[prompt_len + chosen_len:] -= chosen_len
     return p.expand(B, L).contiguous()
+
+
+# ---------------------------------------------------------------------------
+# a cache in 8 bits: quantised as it is written, read back, and the attention over it
+
+
+def make_cache8(B: int, Hkv: int, rows: int, D: int, block: int, device="cuda"):
+    """An empty cache in 8 bits: (k_cache, v_cache) float8_e4m3fn
+    [B,Hkv,rows,D] and (k_scale, v_scale) fp32 [B,Hkv,ceil(rows / block)]."""
+    import torch
+
+    codes = [torch.zeros((B, Hkv, rows, D), dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) for _ in range(2)]
+    scales = [torch.ones((B, Hkv, -(-rows // block)), dtype=torch.float32, device=device) for _ in range(2)]
+    return (*codes, *scales)
+
+
+def _check_cache8(k_cache, v_cache, k_scale, v_scale, kv_len, block, optional_len):
+    """(device, B, Hkv, rows, D, block); k_cache with k_scale, or v_cache with v_scale, may be None."""
+    import torch
+
+    one = k_cache if k_cache is not None else v_cache
+    if one is None:
+        raise ValueError("k_cache or v_cache is needed")
+    if one.dim() != 4:
+        raise ValueError("the caches must be [B, Hkv, rows, D]")
+    block = _int32("block", block)
+    if block not in (16, 32, 64, 128):
+        raise ValueError(f"block must be 16, 32, 64 or 128 tokens, got {block}")
+    dev = _current_device(one, "the cache")
+    B, Hkv, rows, D = one.shape
+    scales = (B, Hkv, -(-rows // block))
+    specs = []
+    for name, codes, scale in (("k", k_cache, k_scale), ("v", v_cache, v_scale)):
+        if codes is not None:
+            specs += [(f"{name}_cache", codes, torch.float8_e4m3fn, (B, Hkv, rows, D)),
+                      (f"{name}_scale", scale, torch.float32, scales)]
+    if kv_len is not None or not optional_len:
+        specs.append(("kv_len", kv_len, torch.int32, (B,)))
+    _check(dev, specs)
+    return dev, B, Hkv, rows, D, block
+
+
+def swa_attn_cache8_append(k, v, k_cache, v_cache, k_scale, v_scale, kv_len, block: int, stream=None) -> None:
+    """Quantise k, v (bf16 [B,Hkv,L,D] with any strides that are multiples of
+    8 elements and D dense; either may be None, with its cache and scales)
+    into rows kv_len[b] - L .. kv_len[b] - 1 of an 8-bit cache, or rows 0 ..
+    L - 1 with kv_len None (see include/swa_attn.h)."""
+    import torch
+
+    one = k if k is not None else v
+    if one is None:
+        raise ValueError("k or v is needed")
+    dev, B, Hkv, rows, D, block = _check_cache8(None if k is None else k_cache, None if v is None else v_cache,
+                                                k_scale, v_scale, kv_len, block, True)
+    if (k is not None and k_cache is None) or (v is not None and v_cache is None):
+        raise ValueError("k needs k_cache and v needs v_cache")
+    strides = []
+    L = one.shape[2] if one.dim() == 4 else 0
+    for name, t in (("k", k), ("v", v)):
+        if t is None:
+            strides += [0, 0, 0]
+            continue
+        if t.dtype is not torch.bfloat16 or t.shape != (B, Hkv, L, D):
+            raise ValueError(f"{name} must be a bf16 tensor [{B}, {Hkv}, {L}, {D}], got {t.dtype} {tuple(t.shape)}")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be on the current CUDA device, like the cache (got {t.device})")
+        if t.stride(3) != 1:
+            raise ValueError(f"{name}'s rows of D elements must be dense, got strides {t.stride()}")
+        strides += t.stride()[:3]
+    rc = load().swa_attn_cache8_append(_addr(k), _addr(v), *strides, _addr(kv_len),
+                                       *(_addr(c) if t is not None else None for t, c in (
+                                           (k, k_cache), (v, v_cache), (k, k_scale), (v, v_scale))),
+                                       B, Hkv, L, D, rows, block, _stream_ptr(stream))
+    if rc:
+        raise SwaError(rc, "swa_attn_cache8_append")
+
+
+def cache8_append(k, v, k_cache, v_cache, k_scale, v_scale, kv_len, block: int, stream=None) -> None:
+    """swa_attn_cache8_append on the current stream (or `stream`)."""
+    if stream is None:
+        r = (_fast or _marshal()).cache8_append(k, v, k_cache, v_cache, k_scale, v_scale, kv_len, block)
+        if r.__class__ is tuple:
+            return
+        if r is not None:
+            raise SwaError(r, "swa_attn_cache8_append")
+    swa_attn_cache8_append(k, v, k_cache, v_cache, k_scale, v_scale, kv_len, block, stream)
+
+
+def swa_attn_cache8_read(k_cache, v_cache, k_scale, v_scale, kv_len, k_out, v_out, block: int, row0: int = 0,
+                         stream=None) -> None:
+    """Rows row0 .. row0 + n - 1 of an 8-bit cache into bf16 k_out, v_out
+    [B,Hkv,n,D] (either may be None), zeros behind each request's length (none
+    with kv_len None)."""
+    import torch
+
+    dev, B, Hkv, rows, D, block = _check_cache8(None if k_out is None else k_cache, None if v_out is None else v_cache,
+                                                k_scale, v_scale, kv_len, block, True)
+    if (k_out is not None and k_cache is None) or (v_out is not None and v_cache is None):
+        raise ValueError("k_out needs k_cache and v_out needs v_cache")
+    n = (k_out if k_out is not None else v_out).shape[2]
+    _check(dev, [(name, t, torch.bfloat16, (B, Hkv, n, D)) for name, t in (("k_out", k_out), ("v_out", v_out))
+                 if t is not None])
+    rc = load().swa_attn_cache8_read(_addr(k_cache), _addr(v_cache), _addr(k_scale), _addr(v_scale), _addr(kv_len),
+                                     _addr(k_out), _addr(v_out), B, Hkv, D, rows, block, _int32("row0", row0), n,
+                                     _stream_ptr(stream))
+    if rc:
+        raise SwaError(rc, "swa_attn_cache8_read")
+
+
+def cache8_read(k_cache, v_cache, k_scale, v_scale, kv_len, block: int, row0: int = 0, rows=None, stream=None):
+    """Return (k, v) bf16 [B,Hkv,rows,D]: rows row0 .. row0 + rows - 1 (to the
+    end by default) of an 8-bit cache, zeros behind each request's length."""
+    if stream is not None:
+        import torch
+
+        with torch.cuda.stream(stream):
+            return cache8_read(k_cache, v_cache, k_scale, v_scale, kv_len, block, row0, rows)
+    r = (_fast or _marshal()).cache8_read(k_cache, v_cache, k_scale, v_scale, kv_len, block, row0, rows)
+    if r.__class__ is tuple:
+        return r
+    if r is not None:
+        raise SwaError(r, "swa_attn_cache8_read")
+    import torch
+
+    _, B, Hkv, all_rows, D, block = _check_cache8(k_cache, v_cache, k_scale, v_scale, kv_len, block, True)
+    row0 = _int32("row0", row0)
+    n = all_rows - row0 if rows is None else _int32("rows", rows)
+    if row0 < 0 or n < 1 or row0 + n > all_rows:
+        raise ValueError(f"rows {row0} .. {row0 + n - 1} are not rows of a cache of {all_rows}")
+    out = [None if c is None else torch.empty((B, Hkv, n, D), dtype=torch.bfloat16, device=c.device)
+           for c in (k_cache, v_cache)]
+    swa_attn_cache8_read(k_cache, v_cache, k_scale, v_scale, kv_len, *out, block, row0)
+    return tuple(out)
+
+
+@functools.lru_cache(maxsize=256)
+def fwd_workspace_bytes_cache8(B, Hq, Hkv, Lq, kv_rows, D, block, window) -> int:
+    return int(load().swa_attn_fwd_workspace_bytes_cache8(B, Hq, Hkv, Lq, kv_rows, D, block, window))
+
+
+def swa_attn_fwd_cache8(q, k_cache, v_cache, k_scale, v_scale, kv_len, sinks, o, lse, block: int, window: int,
+                        scale: float, workspace=None, stream=None) -> None:
+    """Attention of a generation step over an 8-bit cache, each request with
+    its own length (see include/swa_attn.h).  q bf16 [B,Hq,Lq,D]; kv_len int32
+    [B]; sinks fp32 [Hq] or None; o bf16 like q and lse fp32 [B,Hq,Lq] are
+    caller-allocated outputs."""
+    import torch
+
+    if k_cache is None or v_cache is None:
+        raise ValueError("k_cache and v_cache are both needed")
+    if q.dim() != 4:
+        raise ValueError("q must be [B, Hq, Lq, D]")
+    dev, B, Hkv, rows, D, block = _check_cache8(k_cache, v_cache, k_scale, v_scale, kv_len, block, False)
+    _, Hq, Lq, _ = q.shape
+    _check(dev, [("q", q, torch.bfloat16, (B, Hq, Lq, D)), ("o", o, torch.bfloat16, (B, Hq, Lq, D)),
+                 ("lse", lse, torch.float32, (B, Hq, Lq))] +
+           ([] if sinks is None else [("sinks", sinks, torch.float32, (Hq,))]))
+    nbytes = _scratch_bytes(workspace, dev)
+    rc = load().swa_attn_fwd_cache8(_addr(q), _addr(k_cache), _addr(v_cache), _addr(k_scale), _addr(v_scale),
+                                    _addr(kv_len), _addr(sinks), _addr(o), _addr(lse), B, Hq, Hkv, Lq, rows, D, block,
+                                    _int32("window", window), float(scale), _addr(workspace), nbytes,
+                                    _stream_ptr(stream))
+    if rc:
+        raise SwaError(rc, "swa_attn_fwd_cache8")
+
+
+def forward_cache8(q, k_cache, v_cache, k_scale, v_scale, kv_len, block: int, window: int, scale: float, sinks=None,
+                   stream=None):
+    """Return (o bf16 [B,Hq,Lq,D], lse fp32 [B,Hq,Lq]) of swa_attn_fwd_cache8,
+    allocated on the stream that the call runs on."""
+    if stream is not None:
+        import torch
+
+        with torch.cuda.stream(stream):
+            return forward_cache8(q, k_cache, v_cache, k_scale, v_scale, kv_len, block, window, scale, sinks)
+    r = (_fast or _marshal()).forward_cache8(q, k_cache, v_cache, k_scale, v_scale, kv_len, block, window, scale, sinks)
+    if r.__class__ is tuple:
+        return r
+    if r is not None:
+        raise SwaError(r, "swa_attn_fwd_cache8")
+    import torch
+
+    if q.dim() != 4:
+        raise ValueError("q must be [B, Hq, Lq, D]")
+    _, B, Hkv, rows, D, block = _check_cache8(k_cache, v_cache, k_scale, v_scale, kv_len, block, False)
+    window = _int32("window", window)
+    o = torch.empty_like(q)
+    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    nbytes = fwd_workspace_bytes_cache8(B, q.shape[1], Hkv, q.shape[2], rows, D, block, window)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    swa_attn_fwd_cache8(q, k_cache, v_cache, k_scale, v_scale, kv_len, sinks, o, lse, block, window, scale, ws)
+    return o, lse

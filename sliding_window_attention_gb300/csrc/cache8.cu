@@ -1,0 +1,277 @@
+// A cache in 8 bits: keys and values quantised as they are written, and read back.
+//
+// A cache holds e4m3 codes [B, Hkv, rows, D] and one fp32 scale for each block of
+// 16 to 128 tokens of a head, [B, Hkv, ceil(rows / block)]; a value is code times
+// scale.  The scale of a block is the smallest power of two s >= 2^-64 with
+// max |x| <= 448 s over the block's tokens (448 is the largest e4m3 value): a
+// floating code is as exact under a power of two as under max |x| / 448, and
+// moving to a larger one is exact but for what falls below the smallest normal
+// code, 2^-6 s.  So a block that has tokens keeps its scale while the new ones
+// fit; otherwise its scale grows and its older codes are written again.
+//
+// Both kernels are bound by memory: an append reads 2 bytes and writes 1 an
+// element, a read the other way round.  A group of threads has one block: it
+// keeps the block's new rows in registers between the maximum and the codes, so
+// they are read once.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "swa_internal.h"
+#include "tc_ptx.cuh"
+
+namespace swa {
+namespace {
+
+using namespace tc;
+
+struct AppendParams {
+  const uint16_t* x[2];      // k, v: bf16
+  long long sb[2], sh[2], st[2];  // elements between requests, heads, tokens
+  uint8_t* codes[2];
+  float* scales[2];
+  const int* kv_len;         // or null: tokens are rows 0 .. L - 1
+  int B, Hkv, L, ld, rows, lb, nblk;  // ld, lb: log2 of D and of the block
+  int nj;                    // blocks that a request's tokens meet at most
+  int tasks;                 // B * Hkv * nj
+};
+
+__device__ __forceinline__ uint2 quantised8(const uint4& v, float mul, float div) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a = __uint_as_float(w[i] << 16), b = __uint_as_float(w[i] & 0xFFFF0000u);
+    if (div == 0.f) {  // a power of two: its inverse is exact
+      a *= mul;
+      b *= mul;
+    } else {
+      a = __fdiv_rn(a, div);
+      b = __fdiv_rn(b, div);
+    }
+    r[i] = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  }
+  return make_uint2(r[0] | r[1] << 16, r[2] | r[3] << 16);
+}
+__device__ __forceinline__ uint32_t requantised2(uint32_t codes, float mul) {
+  const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3)));
+  return __nv_cvt_float2_to_fp8x2(make_float2(f.x * mul, f.y * mul), __NV_SATFINITE, __NV_E4M3);
+}
+
+// One block's new tokens by a group of GT threads, up to VPT vectors of 8
+// elements each.
+template <int GT, int VPT>
+__global__ void __launch_bounds__(GT > 256 ? GT : 256) append_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int CTA = GT > 256 ? GT : 256, GROUPS = CTA / GT;
+  __shared__ float top[CTA / 32];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int which = blockIdx.y, group = threadIdx.x / GT, tid = threadIdx.x % GT;
+  const int task = blockIdx.x * GROUPS + group;
+  const bool in = task < p.tasks;
+  const int bh = in ? task / p.nj : 0, j = task - bh * p.nj, b = bh / p.Hkv, h = bh - b * p.Hkv;
+  const int n = in ? (p.kv_len ? p.kv_len[b] : p.L) : 0;
+  const long long from = (long long)n - p.L;  // row of token 0
+  const int row0 = from > 0 ? (int)from : 0, blk = (row0 >> p.lb) + j;
+  const long long lo = (long long)blk << p.lb, end = lo + (1 << p.lb);
+  const int a = (int)(lo > row0 ? lo : row0);  // the block's older tokens are rows lo .. a, its new ones a .. hi
+  int hi = n < p.rows ? n : p.rows;
+  if (end < hi) hi = (int)end;
+  const bool any = in && hi > a;
+  const int lv = p.ld - 3, vecs = any ? (hi - a) << lv : 0;  // vectors of the new rows
+  const uint16_t* x = p.x[which] + b * p.sb[which] + h * p.sh[which] + (any ? a - from : 0) * p.st[which];
+  uint4 v[VPT];
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int e = tid + i * GT;
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (e < vecs) v[i] = __ldcs(reinterpret_cast<const uint4*>(x + (e >> lv) * p.st[which] + ((e & ((1 << lv) - 1)) << 3)));
+  }
+  float* scale = p.scales[which] + (size_t)bh * p.nblk + blk;
+  const bool older = any && a > lo;
+  const float was = older ? *scale : 0.f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      amax = fmax3(amax, fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xFFFF0000u)));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  if (GT > 32) {
+    if ((threadIdx.x & 31) == 0) top[threadIdx.x / 32] = amax;
+    __syncthreads();  // (also orders every thread's read of the old scale before it is written)
+#pragma unroll
+    for (int i = 0; i < GT / 32; ++i) amax = fmaxf(amax, top[group * (GT / 32) + i]);
+  } else {
+    __syncwarp();
+  }
+  if (!any) return;
+  const bool keep = older && amax <= 448.f * was;
+  const float now = keep ? was : cache8_two_to(cache8_scale_exponent(amax, kCache8LeastExponent));
+  const bool exact = (__float_as_uint(now) & 0x7FFFFFu) == 0;
+  const float mul = 1.f / now, div = exact ? 0.f : now;
+  uint8_t* codes = p.codes[which] + (((size_t)bh * p.rows) << p.ld);
+  uint2* out = reinterpret_cast<uint2*>(codes + ((size_t)a << p.ld));
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int e = tid + i * GT;
+    if (e < vecs) out[e] = quantised8(v[i], mul, div);
+  }
+  if (keep) return;
+  if (tid == 0) *scale = now;
+  if (older) {  // the older codes move to the new scale
+    uint2* c = reinterpret_cast<uint2*>(codes + ((size_t)lo << p.ld));
+    const int old = (int)(a - lo) << lv;
+    const float f = was * mul;
+    for (int e = tid; e < old; e += GT) {
+      const uint2 u = c[e];
+      c[e] = make_uint2(requantised2(u.x & 0xFFFFu, f) | requantised2(u.x >> 16, f) << 16,
+                        requantised2(u.y & 0xFFFFu, f) | requantised2(u.y >> 16, f) << 16);
+    }
+  }
+}
+
+struct ReadParams {
+  const uint8_t* codes[2];
+  const float* scales[2];
+  uint16_t* out[2];
+  const int* kv_len;  // or null: all rows
+  int Hkv, ld, rows, lb, nblk;
+  int row0, nrows;    // rows row0 .. row0 + nrows - 1 are read
+  int nx;             // CTAs a head
+};
+
+constexpr int kReadThr = 256, kReadVec = 2;  // vectors of 16 codes a thread
+
+__global__ void __launch_bounds__(kReadThr) read_kernel(const __grid_constant__ ReadParams p) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int which = blockIdx.y, bh = blockIdx.x / p.nx, i = blockIdx.x - bh * p.nx;
+  const int len = p.kv_len ? min(p.kv_len[bh / p.Hkv], p.rows) : p.rows;
+  const int lv = p.ld - 4;
+  const long long total = (long long)p.nrows << lv;  // vectors of a head
+  const uint4* in = reinterpret_cast<const uint4*>(p.codes[which]) + (((size_t)bh * p.rows + p.row0) << lv);
+  uint4* out = reinterpret_cast<uint4*>(p.out[which]) + (((size_t)bh * p.nrows) << lv) * 2;
+  const float* scales = p.scales[which] + (size_t)bh * p.nblk;
+  uint4 v[kReadVec];
+  float s[kReadVec];
+#pragma unroll
+  for (int k = 0; k < kReadVec; ++k) {
+    const long long e = ((long long)i * kReadVec + k) * kReadThr + threadIdx.x;
+    const int row = p.row0 + (int)(e >> lv);
+    v[k] = make_uint4(0, 0, 0, 0);
+    s[k] = 0.f;
+    if (e < total && row < len) {
+      v[k] = __ldcs(in + e);
+      s[k] = scales[row >> p.lb];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kReadVec; ++k) {
+    const long long e = ((long long)i * kReadVec + k) * kReadThr + threadIdx.x;
+    if (e >= total) return;
+    const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+    uint32_t r[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const uint32_t two = w[q / 2] >> (16 * (q & 1));
+      const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3)));
+      const __nv_bfloat162 o = __floats2bfloat162_rn(f.x * s[k], f.y * s[k]);
+      r[q] = *reinterpret_cast<const uint32_t*>(&o);
+    }
+    out[2 * e] = make_uint4(r[0], r[1], r[2], r[3]);
+    out[2 * e + 1] = make_uint4(r[4], r[5], r[6], r[7]);
+  }
+}
+
+int log2_of(int x) {
+  int l = 0;
+  while ((1 << l) < x) ++l;
+  return l;
+}
+
+template <int GT, int VPT>
+cudaError_t append_as(const AppendParams& p, int tensors, cudaStream_t st) {
+  constexpr int CTA = GT > 256 ? GT : 256, GROUPS = CTA / GT;
+  return launch_dependent(append_kernel<GT, VPT>, dim3((unsigned)((p.tasks + GROUPS - 1) / GROUPS), (unsigned)tensors),
+                          dim3(CTA), 0, st, p);
+}
+
+}  // namespace
+
+cudaError_t launch_cache8_append(const Cache8AppendArgs& a, cudaStream_t st) {
+  AppendParams p;
+  int tensors = 0;
+  for (int i = 0; i < 2; ++i) {
+    if (!a.x[i]) continue;
+    p.x[tensors] = a.x[i];
+    p.sb[tensors] = a.stride_b[i];
+    p.sh[tensors] = a.stride_h[i];
+    p.st[tensors] = a.stride_t[i];
+    p.codes[tensors] = a.codes[i];
+    p.scales[tensors] = a.scales[i];
+    ++tensors;
+  }
+  for (int i = tensors; i < 2; ++i) {
+    p.x[i] = nullptr;
+    p.codes[i] = nullptr;
+    p.scales[i] = nullptr;
+    p.sb[i] = p.sh[i] = p.st[i] = 0;
+  }
+  p.kv_len = a.kv_len;
+  p.B = a.B;
+  p.Hkv = a.Hkv;
+  p.L = a.L;
+  p.ld = log2_of(a.D);
+  p.rows = a.rows;
+  p.lb = log2_of(a.block);
+  p.nblk = (a.rows + a.block - 1) / a.block;
+  const long long meets = ((long long)a.L + a.block - 2) / a.block + 1;
+  p.nj = (int)(meets < p.nblk ? meets : p.nblk);
+  p.tasks = a.B * a.Hkv * p.nj;
+  // the smallest group whose registers hold the new rows that a block can get
+  const long long vecs = (long long)(a.L < a.block ? a.L : a.block) * a.D / 8;
+  if (vecs <= 32 * 4) return append_as<32, 4>(p, tensors, st);
+  if (vecs <= 64 * 4) return append_as<64, 4>(p, tensors, st);
+  if (vecs <= 128 * 4) return append_as<128, 4>(p, tensors, st);
+  if (vecs <= 256 * 4) return append_as<256, 4>(p, tensors, st);
+  if (vecs <= 512 * 4) return append_as<512, 4>(p, tensors, st);
+  if (vecs <= 512 * 8) return append_as<512, 8>(p, tensors, st);
+  return append_as<1024, 8>(p, tensors, st);
+}
+
+cudaError_t launch_cache8_read(const Cache8ReadArgs& a, cudaStream_t st) {
+  ReadParams p;
+  int tensors = 0;
+  for (int i = 0; i < 2; ++i) {
+    if (!a.codes[i]) continue;
+    p.codes[tensors] = a.codes[i];
+    p.scales[tensors] = a.scales[i];
+    p.out[tensors] = a.out[i];
+    ++tensors;
+  }
+  for (int i = tensors; i < 2; ++i) {
+    p.codes[i] = nullptr;
+    p.scales[i] = nullptr;
+    p.out[i] = nullptr;
+  }
+  p.kv_len = a.kv_len;
+  p.Hkv = a.Hkv;
+  p.ld = log2_of(a.D);
+  p.rows = a.rows;
+  p.lb = log2_of(a.block);
+  p.nblk = (a.rows + a.block - 1) / a.block;
+  p.row0 = a.row0;
+  p.nrows = a.nrows;
+  const long long per = (long long)kReadThr * kReadVec;
+  p.nx = (int)((((long long)a.nrows * a.D / 16) + per - 1) / per);
+  return launch_dependent(read_kernel, dim3((unsigned)((long long)a.B * a.Hkv * p.nx), (unsigned)tensors),
+                          dim3(kReadThr), 0, st, p);
+}
+
+}  // namespace swa

@@ -32,6 +32,10 @@ decltype(&swa_attn_fwd_shared) g_shared;
 decltype(&swa_attn_qk_rope_fwd) g_rope;
 decltype(&swa_attn_qk_rope_bwd_workspace_bytes) g_rope_bwd_ws;
 decltype(&swa_attn_qk_rope_bwd) g_rope_bwd;
+decltype(&swa_attn_fwd_workspace_bytes_cache8) g_cache8_ws;
+decltype(&swa_attn_fwd_cache8) g_cache8;
+decltype(&swa_attn_cache8_append) g_append;
+decltype(&swa_attn_cache8_read) g_read;
 PyObject* g_out_of_memory;  // torch.OutOfMemoryError
 
 // Thrown (and turned into None) where the Python path has to take the call.
@@ -293,14 +297,104 @@ PyObject* qk_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// The five entry points' addresses, in the order of the globals above, and torch.OutOfMemoryError.
+// A cache in 8 bits: codes [B, Hkv, rows, D] and a scale for each block of tokens of a head.
+struct Cache8 {
+  const at::Tensor *k, *v, *ks, *vs;
+  int B, Hkv, rows, D;
+};
+Cache8 cache8(PyObject* k, PyObject* v, PyObject* ks, PyObject* vs, int block, int dev) {
+  Cache8 c{tensor(k), tensor(v), tensor(ks), tensor(vs), 0, 0, 0, 0};
+  if (c.k->dim() != 4 || block < 1) throw NotThisWay{};
+  c.B = dim32(c.k->size(0));
+  c.Hkv = dim32(c.k->size(1));
+  c.rows = dim32(c.k->size(2));
+  c.D = dim32(c.k->size(3));
+  const int64_t nb = ((int64_t)c.rows + block - 1) / block;
+  for (const at::Tensor* t : {c.k, c.v}) expect(t, at::kFloat8_e4m3fn, {c.B, c.Hkv, c.rows, c.D}, dev);
+  for (const at::Tensor* t : {c.ks, c.vs}) expect(t, at::kFloat, {c.B, c.Hkv, nb}, dev);
+  return c;
+}
+
+// (q, k_cache, v_cache, k_scale, v_scale, kv_len, block, window, scale, sinks or None) -> (o, lse)
+PyObject* forward_cache8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 10, [&]() -> PyObject* {
+    const at::Tensor *q = tensor(a[0]), *len = tensor(a[5]), *sinks = tensor_or_null(a[9]);
+    if (q->dim() != 4) throw NotThisWay{};
+    const int dev = current(q), block = int32(a[6]), window = int32(a[7]);
+    const float scale = real(a[8]);
+    const Cache8 c = cache8(a[1], a[2], a[3], a[4], block, dev);
+    const int B = dim32(q->size(0)), Hq = dim32(q->size(1)), Lq = dim32(q->size(2)), D = dim32(q->size(3));
+    if (B != c.B || D != c.D) throw NotThisWay{};
+    expect(q, at::kBFloat16, {B, Hq, Lq, D}, dev);
+    expect(len, at::kInt, {B}, dev);
+    expect(sinks, at::kFloat, {Hq}, dev);
+    const size_t bytes = g_cache8_ws(B, Hq, c.Hkv, Lq, c.rows, D, block, window);
+    at::Tensor o, lse;
+    const int rc = unlocked([&] {
+      o = empty(q->sizes(), q, at::kBFloat16);
+      lse = empty({B, Hq, Lq}, q, at::kFloat);
+      const c10::DataPtr ws = scratch(bytes);
+      return g_cache8(ptr<swa_bf16>(q), ptr<uint8_t>(c.k), ptr<uint8_t>(c.v), ptr<float>(c.ks), ptr<float>(c.vs),
+                      ptr<int32_t>(len), ptr<float>(sinks), ptr<swa_bf16>(&o), ptr<float>(&lse), B, Hq, c.Hkv, Lq,
+                      c.rows, D, block, window, scale, ws.get(), bytes,
+                      c10::cuda::getCurrentCUDAStream(dev).stream());
+    });
+    return rc ? PyLong_FromLong(rc) : tuple({o, lse});
+  });
+}
+
+// (k, v, k_cache, v_cache, k_scale, v_scale, kv_len or None, block) -> (): k, v bf16 [B, Hkv, L, D] by strides
+PyObject* cache8_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 8, [&]() -> PyObject* {
+    const at::Tensor *k = tensor(a[0]), *v = tensor(a[1]), *len = tensor_or_null(a[6]);
+    const int dev = current(k), block = int32(a[7]);
+    const Cache8 c = cache8(a[2], a[3], a[4], a[5], block, dev);
+    if (k->dim() != 4 || k->sizes() != v->sizes() || k->size(0) != c.B || k->size(1) != c.Hkv || k->size(3) != c.D)
+      throw NotThisWay{};
+    for (const at::Tensor* t : {k, v})
+      if (t->scalar_type() != at::kBFloat16 || t->stride(3) != 1 || t->get_device() != dev) throw NotThisWay{};
+    expect(len, at::kInt, {c.B}, dev);
+    const int L = dim32(k->size(2));
+    const int rc = unlocked([&] {
+      return g_append(ptr<swa_bf16>(k), ptr<swa_bf16>(v), k->stride(0), k->stride(1), k->stride(2), v->stride(0),
+                      v->stride(1), v->stride(2), ptr<int32_t>(len), ptr<uint8_t>(c.k), ptr<uint8_t>(c.v),
+                      ptr<float>(c.ks), ptr<float>(c.vs), c.B, c.Hkv, L, c.D, c.rows, block,
+                      c10::cuda::getCurrentCUDAStream(dev).stream());
+    });
+    return rc ? PyLong_FromLong(rc) : PyTuple_New(0);
+  });
+}
+
+// (k_cache, v_cache, k_scale, v_scale, kv_len or None, block, first row, rows or None) -> (k, v) bf16
+PyObject* cache8_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 8, [&]() -> PyObject* {
+    const at::Tensor* len = tensor_or_null(a[4]);
+    const int dev = current(tensor(a[0])), block = int32(a[5]), row0 = int32(a[6]);
+    const Cache8 c = cache8(a[0], a[1], a[2], a[3], block, dev);
+    const int rows = a[7] == Py_None ? dim32((int64_t)c.rows - row0) : int32(a[7]);
+    if (row0 < 0 || rows < 1 || (int64_t)row0 + rows > c.rows) throw NotThisWay{};
+    expect(len, at::kInt, {c.B}, dev);
+    at::Tensor k, v;
+    const int rc = unlocked([&] {
+      k = empty({c.B, c.Hkv, rows, c.D}, c.k, at::kBFloat16);
+      v = empty({c.B, c.Hkv, rows, c.D}, c.k, at::kBFloat16);
+      return g_read(ptr<uint8_t>(c.k), ptr<uint8_t>(c.v), ptr<float>(c.ks), ptr<float>(c.vs), ptr<int32_t>(len),
+                    ptr<swa_bf16>(&k), ptr<swa_bf16>(&v), c.B, c.Hkv, c.D, c.rows, block, row0, rows,
+                    c10::cuda::getCurrentCUDAStream(dev).stream());
+    });
+    return rc ? PyLong_FromLong(rc) : tuple({k, v});
+  });
+}
+
+// The entry points' addresses, in the order of the globals above, and torch.OutOfMemoryError.
+constexpr int kEntries = 9;
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 6 || !PyExceptionClass_Check(a[5])) {
-    PyErr_SetString(PyExc_TypeError, "5 addresses and an exception class expected");
+  if (n != kEntries + 1 || !PyExceptionClass_Check(a[kEntries])) {
+    PyErr_Format(PyExc_TypeError, "%d addresses and an exception class expected", kEntries);
     return nullptr;
   }
-  void* p[5];
-  for (int i = 0; i < 5; ++i) {
+  void* p[kEntries];
+  for (int i = 0; i < kEntries; ++i) {
     p[i] = PyLong_AsVoidPtr(a[i]);
     if (!p[i]) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "null address");
@@ -312,7 +406,11 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g_rope = reinterpret_cast<decltype(g_rope)>(p[2]);
   g_rope_bwd_ws = reinterpret_cast<decltype(g_rope_bwd_ws)>(p[3]);
   g_rope_bwd = reinterpret_cast<decltype(g_rope_bwd)>(p[4]);
-  Py_XSETREF(g_out_of_memory, Py_NewRef(a[5]));
+  g_cache8_ws = reinterpret_cast<decltype(g_cache8_ws)>(p[5]);
+  g_cache8 = reinterpret_cast<decltype(g_cache8)>(p[6]);
+  g_append = reinterpret_cast<decltype(g_append)>(p[7]);
+  g_read = reinterpret_cast<decltype(g_read)>(p[8]);
+  Py_XSETREF(g_out_of_memory, Py_NewRef(a[kEntries]));
   Py_RETURN_NONE;
 }
 
@@ -322,6 +420,9 @@ PyMethodDef kMethods[] = {
     {"forward_shared", FAST(forward_shared), METH_FASTCALL, nullptr},
     {"qk_rope", FAST(qk_rope), METH_FASTCALL, nullptr},
     {"qk_rope_backward", FAST(qk_rope_backward), METH_FASTCALL, nullptr},
+    {"forward_cache8", FAST(forward_cache8), METH_FASTCALL, nullptr},
+    {"cache8_append", FAST(cache8_append), METH_FASTCALL, nullptr},
+    {"cache8_read", FAST(cache8_read), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 

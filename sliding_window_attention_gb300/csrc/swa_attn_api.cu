@@ -420,7 +420,10 @@ const char* swa_attn_strerror(int code) {
       return "rot_dim must be a multiple of 16 in [0, D], eps > 0, weight_offset finite, token strides multiples of 8 "
              "that hold a token's heads";
     case SWA_ERR_BAD_CACHE:
-      return "cache rows must be >= 1 (>= L without kv_len) and prefix_len in [0, prefix_rows]";
+      return "cache rows must be >= 1 (>= L without kv_len), prefix_len in [0, prefix_rows], a scale's block 16, 32, 64 or "
+             "128 tokens, the rows to read within the cache";
+    case SWA_ERR_BAD_STRIDE:
+      return "a stride is no multiple of 8 elements, or too small";
     case SWA_ERR_NOALLOC_LIMIT:
       return "B*Hq*L exceeds the fixed scratch of swa_attn_bwd_noalloc (2,097,152 rows); use swa_attn_bwd";
     default: return "unknown error code";
@@ -718,6 +721,154 @@ int swa_attn_fwd_shared(const swa_bf16* q, const swa_bf16* k_prefix, const swa_b
   a.lse = lse;
   const cudaError_t e =
       launch("fwd_shared", s, [&] { return swa::launch_fwd_shared(g, a, workspace, status, s); });
+  return e == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
+}
+
+// Checks of a cache in 8 bits that its three calls share.
+static bool scale_block_ok(int block) { return block == 16 || block == 32 || block == 64 || block == 128; }
+static int check_cache8(int B, int Hkv, int D, int kv_rows, int block) {
+  if (B < 1 || Hkv < 1) return SWA_ERR_BAD_SHAPE;
+  if (D != 64 && D != 128 && D != 256 && D != 512) return SWA_ERR_BAD_HEAD_DIM;
+  if (kv_rows < 1 || !scale_block_ok(block)) return SWA_ERR_BAD_CACHE;
+  if (B > 65535 || Hkv > 65535 || kv_rows > 2000000000 || (double)B * Hkv * kv_rows * D > 9.0e15) return SWA_ERR_TOO_LARGE;
+  return SWA_OK;
+}
+// Strides of a [B, H, L, D] tensor in elements: D dense, whole vectors apart.
+static bool strides_ok(long long sb, long long sh, long long st, int B, int H, int L, int D) {
+  auto ok = [&](long long s, int n) { return n == 1 || (s % 8 == 0 && s >= D && s < (1LL << 40)); };
+  return ok(sb, B) && ok(sh, H) && ok(st, L);
+}
+
+int swa_attn_cache8_append(const swa_bf16* k, const swa_bf16* v, long long k_stride_b, long long k_stride_h,
+                           long long k_stride_t, long long v_stride_b, long long v_stride_h, long long v_stride_t,
+                           const int32_t* kv_len, uint8_t* k_cache, uint8_t* v_cache, float* k_scale, float* v_scale,
+                           int B, int Hkv, int L, int D, int kv_rows, int block, void* stream) {
+  if ((!k && !v) || (k && (!k_cache || !k_scale)) || (v && (!v_cache || !v_scale))) return SWA_ERR_NULL_POINTER;
+  int rc = check_cache8(B, Hkv, D, kv_rows, block);
+  if (rc) return rc;
+  if (L < 1) return SWA_ERR_BAD_SHAPE;
+  if (!kv_len && L > kv_rows) return SWA_ERR_BAD_CACHE;
+  if ((k && !strides_ok(k_stride_b, k_stride_h, k_stride_t, B, Hkv, L, D)) ||
+      (v && !strides_ok(v_stride_b, v_stride_h, v_stride_t, B, Hkv, L, D)))
+    return SWA_ERR_BAD_STRIDE;
+  if ((double)B * Hkv * (L / block + 2.0) > 1.0e9) return SWA_ERR_TOO_LARGE;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 4) ||
+      !aligned(v_scale, 4) || !aligned(kv_len, 4))
+    return SWA_ERR_MISALIGNED;
+  if ((rc = check_device())) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  swa::Cache8AppendArgs a;
+  a.x[0] = k;
+  a.x[1] = v;
+  a.stride_b[0] = k_stride_b;
+  a.stride_h[0] = k_stride_h;
+  a.stride_t[0] = k_stride_t;
+  a.stride_b[1] = v_stride_b;
+  a.stride_h[1] = v_stride_h;
+  a.stride_t[1] = v_stride_t;
+  a.codes[0] = k_cache;
+  a.codes[1] = v_cache;
+  a.scales[0] = k_scale;
+  a.scales[1] = v_scale;
+  a.kv_len = kv_len;
+  a.B = B;
+  a.Hkv = Hkv;
+  a.L = L;
+  a.D = D;
+  a.rows = kv_rows;
+  a.block = block;
+  const cudaError_t e = launch("cache8_append", s, [&] { return swa::launch_cache8_append(a, s); });
+  return e == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
+}
+
+int swa_attn_cache8_read(const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale, const float* v_scale,
+                         const int32_t* kv_len, swa_bf16* k_out, swa_bf16* v_out, int B, int Hkv, int D, int kv_rows,
+                         int block, int row0, int rows, void* stream) {
+  if ((!k_out && !v_out) || (k_out && (!k_cache || !k_scale)) || (v_out && (!v_cache || !v_scale)))
+    return SWA_ERR_NULL_POINTER;
+  int rc = check_cache8(B, Hkv, D, kv_rows, block);
+  if (rc) return rc;
+  if (row0 < 0 || rows < 1 || (long long)row0 + rows > kv_rows) return SWA_ERR_BAD_CACHE;
+  if ((double)B * Hkv * ((double)rows * D / 8192 + 1.0) > 2.0e9) return SWA_ERR_TOO_LARGE;
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_out, 16) || !aligned(v_out, 16) ||
+      !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(kv_len, 4))
+    return SWA_ERR_MISALIGNED;
+  if ((rc = check_device())) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  swa::Cache8ReadArgs a;
+  a.codes[0] = k_out ? k_cache : nullptr;
+  a.codes[1] = v_out ? v_cache : nullptr;
+  a.scales[0] = k_scale;
+  a.scales[1] = v_scale;
+  a.out[0] = k_out;
+  a.out[1] = v_out;
+  a.kv_len = kv_len;
+  a.B = B;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.rows = kv_rows;
+  a.block = block;
+  a.row0 = row0;
+  a.nrows = rows;
+  const cudaError_t e = launch("cache8_read", s, [&] { return swa::launch_cache8_read(a, s); });
+  return e == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
+}
+
+static int cache8_geom(swa::Cache8Geom& g, int B, int Hq, int Hkv, int Lq, int kv_rows, int D, int block, int window,
+                       float scale) {
+  int rc = check_shape(B, Hq, Hkv, Lq, Lq, D, window, scale);
+  if (rc || (rc = check_cache8(B, Hkv, D, kv_rows, block))) return rc;
+  if ((long long)(Hq / Hkv) * Lq > 1000000LL) return SWA_ERR_TOO_LARGE;
+  g.B = B;
+  g.Hq = Hq;
+  g.Hkv = Hkv;
+  g.G = Hq / Hkv;
+  g.Lq = Lq;
+  g.M = g.G * Lq;
+  g.nmb = swa::cache8_row_blocks(g.M);
+  g.rows = kv_rows;
+  g.lb = block == 16 ? 4 : (block == 32 ? 5 : (block == 64 ? 6 : 7));
+  g.nblk = (kv_rows + block - 1) / block;
+  g.D = D;
+  g.W = window >= kv_rows ? 0 : window;  // no two positions are further apart
+  g.scale = scale;
+  return swa::cache8_fits(g) ? SWA_OK : SWA_ERR_TOO_LARGE;
+}
+
+size_t swa_attn_fwd_workspace_bytes_cache8(int B, int Hq, int Hkv, int Lq, int kv_rows, int D, int block, int window) {
+  swa::Cache8Geom g;
+  if (cache8_geom(g, B, Hq, Hkv, Lq, kv_rows, D, block, window, 1.f)) return 0;
+  return swa::cache8_workspace_bytes(g);
+}
+
+int swa_attn_fwd_cache8(const swa_bf16* q, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale,
+                        const float* v_scale, const int32_t* kv_len, const float* sinks, swa_bf16* o, float* lse,
+                        int B, int Hq, int Hkv, int Lq, int kv_rows, int D, int block, int window, float scale,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !kv_len || !o || !lse) return SWA_ERR_NULL_POINTER;
+  swa::Cache8Geom g;
+  int rc = cache8_geom(g, B, Hq, Hkv, Lq, kv_rows, D, block, window, scale);
+  if (rc) return rc;
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16) || !aligned(k_scale, 4) ||
+      !aligned(v_scale, 4) || !aligned(kv_len, 4) || !aligned(sinks, 4) || !aligned(lse, 4) || !aligned(workspace, 256))
+    return SWA_ERR_MISALIGNED;
+  if (!workspace || workspace_bytes < swa::cache8_workspace_bytes(g)) return SWA_ERR_WORKSPACE;
+  if ((rc = check_device())) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int* status = status_ptr_for_current_device(&rc);
+  if (!status) return rc;
+  swa::Cache8Args a;
+  a.q = q;
+  a.k = k_cache;
+  a.v = v_cache;
+  a.ks = k_scale;
+  a.vs = v_scale;
+  a.kv_len = kv_len;
+  a.sinks = sinks;
+  a.o = o;
+  a.lse = lse;
+  const cudaError_t e =
+      launch("fwd_cache8", s, [&] { return swa::launch_fwd_cache8(g, a, workspace, status, s); });
   return e == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
 }
 

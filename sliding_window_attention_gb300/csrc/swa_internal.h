@@ -431,4 +431,55 @@ cudaError_t launch_qk_rope_bwd(const RopeArgs& a, const float* dq, const float* 
                                uint16_t* gk, uint16_t* gv, long long gq_tok, long long gk_tok, long long gv_tok,
                                float* dwq, float* dwk, float* part, int* status, cudaStream_t s);
 
+// ---- a cache in 8 bits (cache8.cu, cache8_attn.cu) ----
+// e4m3 codes [B, Hkv, rows, D], a scale for each block of tokens of a head.
+constexpr int kCache8LeastExponent = -64;  // the smallest scale that is written is 2^-64
+// Exponent of the smallest power of two s with amax <= 448 s, 2^least at least
+// (amax >= 0; infinity counts as 2^128).
+__device__ __forceinline__ int cache8_scale_exponent(float amax, int least) {
+  const uint32_t u = __float_as_uint(amax);  // amax = 1.m 2^E, and 448 = 1.75 2^8
+  const int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7FFFFFu) > 0x600000u);
+  return e > least ? e : least;
+}
+__device__ __forceinline__ float cache8_two_to(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+struct Cache8AppendArgs {
+  const uint16_t* x[2];  // k, v [B, Hkv, L, D] by strides (in elements), either null
+  long long stride_b[2], stride_h[2], stride_t[2];
+  uint8_t* codes[2];
+  float* scales[2];
+  const int* kv_len;     // or null: the tokens are rows 0 .. L - 1
+  int B, Hkv, L, D, rows, block;
+};
+cudaError_t launch_cache8_append(const Cache8AppendArgs& a, cudaStream_t s);
+struct Cache8ReadArgs {
+  const uint8_t* codes[2];  // k, v, either null
+  const float* scales[2];
+  uint16_t* out[2];         // [B, Hkv, nrows, D]
+  const int* kv_len;        // or null: all rows
+  int B, Hkv, D, rows, block, row0, nrows;
+};
+cudaError_t launch_cache8_read(const Cache8ReadArgs& a, cudaStream_t s);
+struct Cache8Geom {
+  int B, Hq, Hkv, G, Lq, M, nmb;  // M = G * Lq query rows of a request and kv head, in nmb blocks
+  int rows, lb, nblk;             // cache rows, log2 of a scale's block, scales of a head
+  int D, W;                       // W = 0: no window
+  float scale;
+};
+struct Cache8Args {
+  const uint16_t* q;
+  const uint8_t *k, *v;
+  const float *ks, *vs;
+  const int* kv_len;
+  const float* sinks;
+  uint16_t* o;
+  float* lse;
+};
+int cache8_row_blocks(int M);
+bool cache8_fits(const Cache8Geom& g);  // unit and row counts within the kernel's 32-bit indexes
+size_t cache8_workspace_bytes(const Cache8Geom& g);
+cudaError_t launch_fwd_cache8(const Cache8Geom& g, const Cache8Args& a, void* ws, int* status, cudaStream_t s);
+// A 4-D map of bytes (strides in bytes, for dimensions 1 to 3) with the given box and swizzle.
+cudaError_t make_tmap_u8_4d(CUtensorMap* m, const void* ptr, const cuuint64_t (&dims)[4], const cuuint64_t (&strides)[3],
+                            const cuuint32_t (&box)[4], CUtensorMapSwizzle swizzle);
+
 }  // namespace swa

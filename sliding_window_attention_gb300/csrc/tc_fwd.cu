@@ -908,6 +908,17 @@ cudaError_t make_tmap_rows_5d(CUtensorMap* m, const void* ptr, int D, int M, int
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+cudaError_t make_tmap_u8_4d(CUtensorMap* m, const void* ptr, const cuuint64_t (&dims)[4], const cuuint64_t (&strides)[3],
+                            const cuuint32_t (&box)[4], CUtensorMapSwizzle swizzle) {
+  auto enc = encode_fn();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(ptr), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 cudaError_t make_tmap_tokens(CUtensorMap* m, const void* ptr, int D, int H, int L, int batch, long long tok, int toks,
                              int hb) {
   auto enc = encode_fn();
