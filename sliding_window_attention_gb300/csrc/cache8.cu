@@ -15,7 +15,6 @@
 // they are read once.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -38,34 +37,32 @@ struct AppendParams {
   int tasks;                 // B * Hkv * nj
 };
 
-__device__ __forceinline__ uint2 quantised8(const uint4& v, float mul, float div) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t r[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float a = __uint_as_float(w[i] << 16), b = __uint_as_float(w[i] & 0xFFFF0000u);
-    if (div == 0.f) {  // a power of two: its inverse is exact
-      a *= mul;
-      b *= mul;
-    } else {
-      a = __fdiv_rn(a, div);
-      b = __fdiv_rn(b, div);
-    }
-    r[i] = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-  }
-  return make_uint2(r[0] | r[1] << 16, r[2] | r[3] << 16);
+// Four fp32 values to e4m3, nearest, 448 at most.
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
 }
-__device__ __forceinline__ uint32_t requantised2(uint32_t codes, float mul) {
-  const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3)));
-  return __nv_cvt_float2_to_fp8x2(make_float2(f.x * mul, f.y * mul), __NV_SATFINITE, __NV_E4M3);
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t codes) {  // the low two bytes
+  uint32_t h;
+  asm("{\n\t.reg .b16 lo;\n\tmov.b32 {lo, _}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(h) : "r"(codes));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
+__device__ __forceinline__ float2 bf16x2(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+// Pairs of bf16 patterns without their signs: as unsigned numbers they are in the order of the magnitudes.
+__device__ __forceinline__ uint32_t magnitudes(uint32_t w) { return w & 0x7FFF7FFFu; }
 
 // One block's new tokens by a group of GT threads, up to VPT vectors of 8
 // elements each.
 template <int GT, int VPT>
 __global__ void __launch_bounds__(GT > 256 ? GT : 256) append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int CTA = GT > 256 ? GT : 256, GROUPS = CTA / GT;
-  __shared__ float top[CTA / 32];
+  __shared__ uint32_t top[CTA / 32];
   grid_dependency_wait();
   grid_launch_dependents();
   const int which = blockIdx.y, group = threadIdx.x / GT, tid = threadIdx.x % GT;
@@ -83,7 +80,6 @@ __global__ void __launch_bounds__(GT > 256 ? GT : 256) append_kernel(const __gri
   const int lv = p.ld - 3, vecs = any ? (hi - a) << lv : 0;  // vectors of the new rows
   const uint16_t* x = p.x[which] + b * p.sb[which] + h * p.sh[which] + (any ? a - from : 0) * p.st[which];
   uint4 v[VPT];
-  float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int e = tid + i * GT;
@@ -93,45 +89,55 @@ __global__ void __launch_bounds__(GT > 256 ? GT : 256) append_kernel(const __gri
   float* scale = p.scales[which] + (size_t)bh * p.nblk + blk;
   const bool older = any && a > lo;
   const float was = older ? *scale : 0.f;
+  uint32_t most = 0;  // a pair's larger magnitude
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      amax = fmax3(amax, fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xFFFF0000u)));
+    most = __vmaxu2(most, __vmaxu2(magnitudes(v[i].x), magnitudes(v[i].y)));
+    most = __vmaxu2(most, __vmaxu2(magnitudes(v[i].z), magnitudes(v[i].w)));
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  most = max(most & 0xFFFFu, most >> 16);
+  most = __reduce_max_sync(0xffffffffu, most);
   if (GT > 32) {
-    if ((threadIdx.x & 31) == 0) top[threadIdx.x / 32] = amax;
+    if ((threadIdx.x & 31) == 0) top[threadIdx.x / 32] = most;
     __syncthreads();  // (also orders every thread's read of the old scale before it is written)
 #pragma unroll
-    for (int i = 0; i < GT / 32; ++i) amax = fmaxf(amax, top[group * (GT / 32) + i]);
-  } else {
-    __syncwarp();
+    for (int i = 0; i < GT / 32; ++i) most = max(most, top[group * (GT / 32) + i]);
   }
   if (!any) return;
+  const float amax = __uint_as_float(min(most, 0x7F7Fu) << 16);  // (infinity and NaN count as the largest number)
   const bool keep = older && amax <= 448.f * was;
   const float now = keep ? was : cache8_two_to(cache8_scale_exponent(amax, kCache8LeastExponent));
-  const bool exact = (__float_as_uint(now) & 0x7FFFFFu) == 0;
-  const float mul = 1.f / now, div = exact ? 0.f : now;
   uint8_t* codes = p.codes[which] + (((size_t)bh * p.rows) << p.ld);
-  uint2* out = reinterpret_cast<uint2*>(codes + ((size_t)a << p.ld));
+  uint2* out = reinterpret_cast<uint2*>(codes + ((size_t)a << p.ld)) + tid;
+  if ((__float_as_uint(now) & 0x7FFFFFu) == 0) {  // a power of two: its inverse is exact
+    const float mul = 1.f / now;
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int e = tid + i * GT;
-    if (e < vecs) out[e] = quantised8(v[i], mul, div);
+    for (int i = 0; i < VPT; ++i) {
+      const float2 x0 = bf16x2(v[i].x), x1 = bf16x2(v[i].y), x2 = bf16x2(v[i].z), x3 = bf16x2(v[i].w);
+      if (tid + i * GT < vecs)
+        out[i * GT] = make_uint2(e4m3x4(x0.x * mul, x0.y * mul, x1.x * mul, x1.y * mul),
+                                 e4m3x4(x2.x * mul, x2.y * mul, x3.x * mul, x3.y * mul));
+    }
+  } else {  // another quantiser's
+#pragma unroll 1
+    for (int e = tid; e < vecs; e += GT) {
+      const uint4 u = *reinterpret_cast<const uint4*>(x + (e >> lv) * p.st[which] + ((e & ((1 << lv) - 1)) << 3));
+      const float2 x0 = bf16x2(u.x), x1 = bf16x2(u.y), x2 = bf16x2(u.z), x3 = bf16x2(u.w);
+      out[e - tid] = make_uint2(e4m3x4(x0.x / now, x0.y / now, x1.x / now, x1.y / now),
+                                e4m3x4(x2.x / now, x2.y / now, x3.x / now, x3.y / now));
+    }
   }
   if (keep) return;
   if (tid == 0) *scale = now;
   if (older) {  // the older codes move to the new scale
     uint2* c = reinterpret_cast<uint2*>(codes + ((size_t)lo << p.ld));
     const int old = (int)(a - lo) << lv;
-    const float f = was * mul;
+    const float f = was / now;
+#pragma unroll 1
     for (int e = tid; e < old; e += GT) {
       const uint2 u = c[e];
-      c[e] = make_uint2(requantised2(u.x & 0xFFFFu, f) | requantised2(u.x >> 16, f) << 16,
-                        requantised2(u.y & 0xFFFFu, f) | requantised2(u.y >> 16, f) << 16);
+      const float2 x0 = from_e4m3x2(u.x), x1 = from_e4m3x2(u.x >> 16), x2 = from_e4m3x2(u.y), x3 = from_e4m3x2(u.y >> 16);
+      c[e] = make_uint2(e4m3x4(x0.x * f, x0.y * f, x1.x * f, x1.y * f), e4m3x4(x2.x * f, x2.y * f, x3.x * f, x3.y * f));
     }
   }
 }
@@ -146,46 +152,43 @@ struct ReadParams {
   int nx;             // CTAs a head
 };
 
-constexpr int kReadThr = 256, kReadVec = 2;  // vectors of 16 codes a thread
+constexpr int kReadThr = 256, kReadVec = 4;  // vectors of 8 codes a thread
 
 __global__ void __launch_bounds__(kReadThr) read_kernel(const __grid_constant__ ReadParams p) {
   grid_dependency_wait();
   grid_launch_dependents();
   const int which = blockIdx.y, bh = blockIdx.x / p.nx, i = blockIdx.x - bh * p.nx;
   const int len = p.kv_len ? min(p.kv_len[bh / p.Hkv], p.rows) : p.rows;
-  const int lv = p.ld - 4;
-  const long long total = (long long)p.nrows << lv;  // vectors of a head
-  const uint4* in = reinterpret_cast<const uint4*>(p.codes[which]) + (((size_t)bh * p.rows + p.row0) << lv);
-  uint4* out = reinterpret_cast<uint4*>(p.out[which]) + (((size_t)bh * p.nrows) << lv) * 2;
+  const int lv = p.ld - 3;
+  const long long total = (long long)p.nrows << lv, e0 = (long long)i * kReadVec * kReadThr + threadIdx.x;  // vectors of a head
+  const uint2* in = reinterpret_cast<const uint2*>(p.codes[which]) + (((size_t)bh * p.rows + p.row0) << lv) + e0;
+  uint4* out = reinterpret_cast<uint4*>(p.out[which]) + (((size_t)bh * p.nrows) << lv) + e0;
   const float* scales = p.scales[which] + (size_t)bh * p.nblk;
-  uint4 v[kReadVec];
+  uint2 v[kReadVec];
   float s[kReadVec];
 #pragma unroll
   for (int k = 0; k < kReadVec; ++k) {
-    const long long e = ((long long)i * kReadVec + k) * kReadThr + threadIdx.x;
+    const long long e = e0 + k * kReadThr;
     const int row = p.row0 + (int)(e >> lv);
-    v[k] = make_uint4(0, 0, 0, 0);
+    v[k] = make_uint2(0, 0);
     s[k] = 0.f;
     if (e < total && row < len) {
-      v[k] = __ldcs(in + e);
+      v[k] = __ldcs(in + k * kReadThr);
       s[k] = scales[row >> p.lb];
     }
   }
 #pragma unroll
   for (int k = 0; k < kReadVec; ++k) {
-    const long long e = ((long long)i * kReadVec + k) * kReadThr + threadIdx.x;
-    if (e >= total) return;
-    const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-    uint32_t r[8];
+    if (e0 + k * kReadThr >= total) return;
+    const uint32_t w[4] = {v[k].x, v[k].x >> 16, v[k].y, v[k].y >> 16};
+    uint32_t r[4];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const uint32_t two = w[q / 2] >> (16 * (q & 1));
-      const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3)));
+    for (int q = 0; q < 4; ++q) {
+      const float2 f = from_e4m3x2(w[q]);
       const __nv_bfloat162 o = __floats2bfloat162_rn(f.x * s[k], f.y * s[k]);
       r[q] = *reinterpret_cast<const uint32_t*>(&o);
     }
-    out[2 * e] = make_uint4(r[0], r[1], r[2], r[3]);
-    out[2 * e + 1] = make_uint4(r[4], r[5], r[6], r[7]);
+    out[k * kReadThr] = make_uint4(r[0], r[1], r[2], r[3]);
   }
 }
 
@@ -269,7 +272,7 @@ cudaError_t launch_cache8_read(const Cache8ReadArgs& a, cudaStream_t st) {
   p.row0 = a.row0;
   p.nrows = a.nrows;
   const long long per = (long long)kReadThr * kReadVec;
-  p.nx = (int)((((long long)a.nrows * a.D / 16) + per - 1) / per);
+  p.nx = (int)((((long long)a.nrows * a.D / 8) + per - 1) / per);
   return launch_dependent(read_kernel, dim3((unsigned)((long long)a.B * a.Hkv * p.nx), (unsigned)tensors),
                           dim3(kReadThr), 0, st, p);
 }

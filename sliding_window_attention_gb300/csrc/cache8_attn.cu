@@ -74,7 +74,8 @@ struct C8Params {
   const float* sinks;  // [Hq] or null
   uint16_t* o;         // bf16 [B, Hq, Lq, D]
   float* lse;          // [B, Hq, Lq]
-  int4* cuts;          // [kCtas]: segment of the CTA's first unit, the segment's units (begin, end), units in all
+  int4* cuts;          // [kCtas]: the segment that the begin of the CTA's run cuts (-1: none), its partials, their
+                       // first CTA and that one's slot
   float *ml, *po;      // partials [2 kCtas][rows of a block][2] and [..][D]
   int orow;            // rows of a partial's slot
   int* status;
@@ -89,10 +90,11 @@ __device__ __forceinline__ int tiles_of(const Cache8Geom& g, int len) {
 
 // The runs that the units are cut into, one for each CTA while they last; none is empty.
 struct Runs {
-  unsigned units, n;  // (units * kCtas < 2^32)
-  __device__ __forceinline__ explicit Runs(unsigned u) : units(u), n(u < kCtas ? u : kCtas) {}
-  __device__ __forceinline__ unsigned start(unsigned c) const { return c < n ? c * units / n : units; }
-  __device__ __forceinline__ unsigned of(unsigned u) const { return ((u + 1) * n - 1) / units; }  // whose unit u is
+  unsigned units;  // (units * kCtas < 2^32)
+  __device__ __forceinline__ unsigned start(unsigned c) const { return units < kCtas ? min(c, units) : c * units / kCtas; }
+  __device__ __forceinline__ unsigned of(unsigned u) const {  // whose unit u is
+    return units < kCtas ? u : ((u + 1) * kCtas - 1) / units;
+  }
 };
 
 // A place in a CTA's run: request, kv head, row block, tile.
@@ -111,7 +113,7 @@ struct Walk {
     set_request();
     const int in = r / nt;
     t = r - in * nt;
-    h = in / p->g.nmb;
+    h = p->g.nmb == 1 ? in : in / p->g.nmb;
     blk = in - h * p->g.nmb;
     left = units;
     first = true;
@@ -129,8 +131,11 @@ struct Walk {
     blk = 0;
     if (++h < p->g.Hkv) return;
     h = 0;
-    do {  // the next request with keys (there is one: units are left)
-      ++b;
+    do {  // the next request with keys (there is one while units are left and the lengths stay)
+      if (++b >= p->g.B) {
+        left = 0;
+        return;
+      }
       set_request();
     } while (nt == 0);
   }
@@ -149,13 +154,12 @@ struct C8 {
   static constexpr int SLOT = T * LINE;
   static constexpr int QB = NS * D;               // a block of queries: the parts' 32 rows
   static constexpr int PB = NP * T;               // weights
-  // the softmax warps' small arrays: [2][4][16] exchanged maxima / sums, references, rescale factors, row
-  // factors, row ranges, bounds and tags; the row factors of four visits
-  static constexpr int RED = 0, REF = 512, ALPHA = REF + 64, FAC = ALPHA + 64, RNG = FAC + 64, BND = RNG + 128,
-                       QFAC = BND + 64, SMALL = QFAC + 256;
+  // the softmax warps' small arrays: [4][16] exchanged maxima / sums, references, rescale factors, row ranges, and
+  // the row factors of four visits
+  static constexpr int RED = 0, REF = 256, ALPHA = REF + 64, RNG = ALPHA + 64, QFAC = RNG + 128, SMALL = QFAC + 256;
   static constexpr int BARS = 256;
   static constexpr int FIT = (kSmemMax - 1024 - 2 * QB - PB - SMALL - BARS) / SLOT;
-  static constexpr int NSLOT = FIT > 8 ? 8 : FIT;
+  static constexpr int NSLOT = FIT > 4 ? (D == 64 ? 8 : 4) : FIT;
   static constexpr int OFF_Q = NSLOT * SLOT, OFF_P = OFF_Q + 2 * QB, OFF_SMALL = OFF_P + PB, OFF_BAR = OFF_SMALL + SMALL;
   static constexpr size_t SMEM = (size_t)OFF_BAR + BARS + 1024;
   static constexpr uint32_t S_COL = 0, O_COL = 2 * NS;  // TMEM columns: S^T twice, O^T's blocks
@@ -175,10 +179,9 @@ struct Bars {
   __device__ __forceinline__ uint64_t* s_full(int i) const { return b + 20 + i; }     // [2] S^T in TMEM
   __device__ __forceinline__ uint64_t* p_full() const { return b + 22; }              // weights written (O^T rescaled)
   __device__ __forceinline__ uint64_t* o_done() const { return b + 23; }              // the second product finished
-  __device__ __forceinline__ uint64_t* xch() const { return b + 24; }                 // the softmax warps' exchanges
-  __device__ __forceinline__ uint64_t* drain() const { return b + 25; }
-  static constexpr int kCount = 26;
-  static __device__ __forceinline__ int arrivals(int i) { return i == 16 || i == 17 || i == 22 || i == 24 ? 4 : 1; }
+  __device__ __forceinline__ uint64_t* drain() const { return b + 24; }
+  static constexpr int kCount = 25;
+  static __device__ __forceinline__ int arrivals(int i) { return i == 16 || i == 17 || i == 22 ? 4 : 1; }
 };
 
 // Shared-memory matrix descriptors: layout 2 is the 128-byte swizzle, 4 the 64-byte one, 0 none.
@@ -228,71 +231,55 @@ __device__ __forceinline__ void column_reduce(float (&v)[NR], int lane) {
   v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
 }
 
-// Queries of one visit as the B operand of the first product: rows w, w + nw, ...
-// of the block, the parts of row r in rows r and 16 + r, and each row's factor
-// (what its scores are multiplied with, but for the keys' scales) in fac.
+// Queries of one visit as the B operand of the first product: rows 4 w .. 4 w + 3
+// of the block by one warp, eight lanes a row; row r's parts go to rows r and
+// 16 + r, and its factor (what its scores are multiplied with, but for the keys'
+// scales) to fac[r].  Rows from `rows` on are zero.
 template <int D>
-__device__ __forceinline__ void prepare_queries(const C8Params& p, int head, int blk, unsigned char* dst, float* fac,
-                                                int w, int nw, int lane) {
-  constexpr int E = D / 32;  // elements a lane
-  const Cache8Geom& g = p.g;
-  const uint16_t* src = p.q + ((size_t)head * g.M + blk * NR) * D + lane * E;
-  const int rows = min(NR, g.M - blk * NR);
-  const float sign = g.scale < 0.f ? -1.f : 1.f;
-#pragma unroll 2
-  for (int r = w; r < NR; r += nw) {
-    float x[E];
-    if (r < rows) {
-      const uint16_t* s = src + (size_t)r * D;
-      uint32_t v[E / 2];
-      if constexpr (E == 2) v[0] = *reinterpret_cast<const uint32_t*>(s);
-      else if constexpr (E == 4) *reinterpret_cast<uint2*>(v) = *reinterpret_cast<const uint2*>(s);
-      else {
+__device__ __forceinline__ void prepare_queries(const C8Params& p, int head, int blk, int rows, unsigned char* dst,
+                                                float* fac, int w, int lane) {
+  constexpr int V = D / 64;  // vectors of 8 elements a lane
+  const int r = 4 * w + (lane >> 3), l8 = lane & 7;
+  const uint4* src = reinterpret_cast<const uint4*>(p.q + ((size_t)head * p.g.M + blk * NR + r) * D) + l8;
+  auto load = [&](int i) { return r < rows ? src[8 * i] : make_uint4(0, 0, 0, 0); };
+  uint4 v[V];
 #pragma unroll
-        for (int i = 0; i < E / 8; ++i) reinterpret_cast<uint4*>(v)[i] = reinterpret_cast<const uint4*>(s)[i];
-      }
+  for (int i = 0; i < V; ++i) v[i] = load(i);
+  uint32_t top = 0;  // max |x| of pairs of bf16 patterns
 #pragma unroll
-      for (int i = 0; i < E / 2; ++i) {
-        x[2 * i] = __uint_as_float(v[i] << 16);
-        x[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
-      }
-    } else {
+  for (int i = 0; i < V; ++i) {
+    top = __vmaxu2(top, __vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu));
+    top = __vmaxu2(top, __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
+  }
 #pragma unroll
-      for (int i = 0; i < E; ++i) x[i] = 0.f;
-    }
-    float amax = 0.f;
+  for (int o = 4; o > 0; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float amax = __uint_as_float(max(top << 16, top & 0xFFFF0000u));
+  const int e = cache8_scale_exponent(amax, -100);
+  const float mul = copysignf(cache8_two_to(-e), p.g.scale);
+  constexpr int LINE = C8<D>::LINE;
+#pragma unroll(V <= 2 ? V : 1)
+  for (int i = 0; i < V; ++i) {
+    const uint4 u = V <= 2 ? v[i] : load(i);  // (a rolled loop reads them again: the code is run once or twice)
+    const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+    uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int i = 0; i < E; ++i) amax = fmaxf(amax, fabsf(x[i]));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const int e = cache8_scale_exponent(amax, -100);
-    const float mul = sign * cache8_two_to(-e);
-    uint16_t hi[E / 2], lo[E / 2];
-#pragma unroll
-    for (int i = 0; i < E / 2; ++i) {
-      const float a = x[2 * i] * mul, b = x[2 * i + 1] * mul;
-      hi[i] = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-      const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(hi[i], __NV_E4M3);
-      const float2 h = __half22float2(__half2(hr));
-      lo[i] = __nv_cvt_float2_to_fp8x2(make_float2((a - h.x) * 16.f, (b - h.y) * 16.f), __NV_SATFINITE, __NV_E4M3);
+    for (int k = 0; k < 4; ++k) {
+      const float a = __uint_as_float(x[k] << 16) * mul, b = __uint_as_float(x[k] & 0xFFFF0000u) * mul;
+      hi[k] = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+      const float2 h = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi[k], __NV_E4M3)));
+      lo[k] = __nv_cvt_float2_to_fp8x2(make_float2((a - h.x) * 16.f, (b - h.y) * 16.f), __NV_SATFINITE, __NV_E4M3);
     }
     // K-major rows in the swizzle of their line length
-    const int col = lane * E, chunk = col / C8<D>::LINE, at = col % C8<D>::LINE;
-    auto put = [&](int row, const uint16_t* v) {
+    const int col = (8 * i + l8) * 8, at = col % LINE;
+    unsigned char* d = dst + col / LINE * NS * LINE + (at & 15);
+    auto put = [&](int row, const uint32_t* q) {
       const int turn = D < 128 ? (row >> 1) & 3 : row & 7;
-      unsigned char* d = dst + chunk * NS * C8<D>::LINE + row * C8<D>::LINE + (((at >> 4) ^ turn) << 4) + (at & 15);
-      if constexpr (E == 2) *reinterpret_cast<uint16_t*>(d) = v[0];
-      else if constexpr (E == 4) *reinterpret_cast<uint32_t*>(d) = v[0] | (uint32_t)v[1] << 16;
-      else if constexpr (E == 8)
-        *reinterpret_cast<uint2*>(d) = make_uint2(v[0] | (uint32_t)v[1] << 16, v[2] | (uint32_t)v[3] << 16);
-      else
-        *reinterpret_cast<uint4*>(d) = make_uint4(v[0] | (uint32_t)v[1] << 16, v[2] | (uint32_t)v[3] << 16,
-                                                  v[4] | (uint32_t)v[5] << 16, v[6] | (uint32_t)v[7] << 16);
+      *reinterpret_cast<uint2*>(d + row * LINE + (((at >> 4) ^ turn) << 4)) = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
     };
     put(r, hi);
     put(NR + r, lo);
-    if (lane == 0) fac[r] = fabsf(g.scale) * kLog2e * cache8_two_to(e);
   }
+  if (l8 == 0) fac[r] = fabsf(p.g.scale) * kLog2e * cache8_two_to(e);
   fence_proxy_async_smem();
 }
 
@@ -307,173 +294,181 @@ __device__ __forceinline__ float finish_row(const float* sink, float ref, float 
   return 1.f / l;
 }
 
+// Barrier of the four softmax warps; `any`: whether any of their threads says so.
+// Its wait needs no limit: the warps go through all of them whatever their bounded
+// waits on the other roles say.
+__device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool soft_any(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, "
+      "q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
+// The MMA warp has tensor memory, for itself and the softmax warps.
+__device__ __forceinline__ void tmem_sync() { asm volatile("barrier.cta.sync 2, 160;" ::: "memory"); }
+
 // The softmax warps' state over a run.
 struct Soft {
   uint32_t at;   // TMEM: this thread's lane
   int n;         // tiles so far: S^T(n) is in buffer n & 1
-  int xc;        // exchanges done
   int visit;
+  float ks, vs;  // scales of this thread's key of tile n
 };
+__device__ __forceinline__ void load_scales(const C8Params& p, const Walk& w, int t, Soft& c) {
+  const size_t at = (size_t)w.head() * p.g.nblk + (max(w.key0() + t, 0) >> p.g.lb);
+  c.ks = p.ks[at];
+  c.vs = p.vs[at];
+}
 
 // One visit of a segment: its tiles' weights, then the result or the partial.
+// After a wait that ran out everything here goes on with what is there, to the
+// visit's end: the call's results are then undefined, and its status says so.
 template <int D>
-__device__ bool softmax_visit(const C8Params& p, unsigned char* base, const Bars& bar, volatile int* abort, Walk& w,
-                              Soft& c) {
+__device__ __forceinline__ void softmax_visit(const C8Params& p, unsigned char* base, const Bars& bar,
+                                              volatile int* abort, Walk& w, Soft& c) {
   using C = C8<D>;
   const Cache8Geom& g = p.g;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q4 = warp & 3, t = 32 * q4 + lane;
+  const int lane = threadIdx.x & 31, q4 = (threadIdx.x >> 5) & 3, t = 32 * q4 + lane;
   unsigned char* small = base + C::OFF_SMALL;
   float* red = reinterpret_cast<float*>(small + C::RED);
-  float* ref = reinterpret_cast<float*>(small + C::REF);
+  float* nref = reinterpret_cast<float*>(small + C::REF);  // the references' negatives
   float* alp = reinterpret_cast<float*>(small + C::ALPHA);
-  float* fac = reinterpret_cast<float*>(small + C::FAC);
   int2* rng = reinterpret_cast<int2*>(small + C::RNG);
-  int* bnd = reinterpret_cast<int*>(small + C::BND);
-  volatile int* grow_tag = bnd + 8;    // [2] tile (plus one) at which some weight passed the top
-  volatile int* scale_tag = bnd + 10;  // [1] tile (plus one) at which some row with earlier keys did
-  const int blk = w.blk, head = w.head(), rows = min(NR, g.M - blk * NR);
-  auto exchange = [&]() -> bool {  // what was written to shared memory before is visible after
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar.xch());
-    const bool ok = wait(bar.xch(), c.xc & 1, abort);
-    ++c.xc;
-    return __all_sync(0xffffffffu, ok);
-  };
-
-  // the visit's first scores say that its queries' factors have been written
-  if (!__all_sync(0xffffffffu, wait(bar.s_full(c.n & 1), (c.n >> 1) & 1, abort))) return false;
-  // the visit is of the whole segment; row t's visible keys, and bounds over all rows
-  const bool whole = w.t == 0 && w.left >= w.nt;
-  {
-    int lo = 0, hi = INT32_MAX;  // rows that are no query mask nothing: their columns are never read
-    const bool row = t < rows;
-    if (row) {
-      hi = w.n - g.Lq + (blk * NR + t) % g.Lq;
+  const float* fac = reinterpret_cast<const float*>(small + C::QFAC) + (c.visit & 3) * NR;
+  const int blk = w.blk, head = w.head(), len = w.n, rows = min(NR, g.M - blk * NR);
+  const bool whole = w.t == 0 && w.left >= w.nt;  // the visit is of the whole segment
+  if (t < NR) {  // row t's visible keys; rows that are no query mask nothing: their columns are never read
+    int lo = 0, hi = INT32_MAX;
+    if (t < rows) {
+      hi = len - g.Lq + (g.Lq > 1 ? (blk * NR + t) % g.Lq : 0);
       lo = g.W > 0 ? max(0, hi - g.W + 1) : 0;
     }
-    if (t < NR) {
-      rng[t] = make_int2(lo, hi);
-      ref[t] = kUnset;
-      fac[t] = reinterpret_cast<const float*>(small + C::QFAC)[(c.visit & 3) * NR + t];
-    }
-    const int lo_w = __reduce_max_sync(0xffffffffu, lo);
-    const int hi_w = __reduce_min_sync(0xffffffffu, hi);
-    if (lane == 0 && q4 == 0) {
-      bnd[0] = lo_w;
-      bnd[1] = hi_w;
-    }
+    rng[t] = make_int2(lo, hi);
+    nref[t] = -kUnset;
   }
-  if (!exchange()) return false;
-  const int lo_all = bnd[0], hi_all = bnd[1];  // (the rows are all in the first warp)
+  // every row sees the keys from lo_all to hi_all
+  const int lo_all = g.W > 0 ? max(0, len - g.W) : 0, hi_all = len - g.Lq;
+  soft_sync();
 
-  float l_part[NR], m_row = kUnset;  // thread t < 16 holds row t's reference
+  uint64_t l_part[NR / 2];
+  float m_row = kUnset;  // thread t < 16 holds row t's reference
 #pragma unroll
-  for (int q = 0; q < NR; ++q) l_part[q] = 0.f;
-  const float* ks = p.ks + (size_t)head * g.nblk;
-  const float* vs = p.vs + (size_t)head * g.nblk;
-  const int at0 = max(w.key0() + t, 0) >> g.lb;
-  float k_next = ks[at0], v_next = vs[at0];
+  for (int q = 0; q < NR / 2; ++q) l_part[q] = 0;
 
   bool more = true, fresh = true;
 #pragma unroll 1
   while (more) {
     const int n = c.n, buf = n & 1, key0 = w.key0();
     more = !w.last();
-    const float kscale = k_next, vscale = fmaxf(v_next, cache8_two_to(kCache8LeastExponent));
-    if (more) {  // the next tile's scales are under way meanwhile
-      const int a = max(key0 + T + t, 0) >> g.lb;
-      k_next = ks[a];
-      v_next = vs[a];
-    }
-    const float lv = __log2f(vscale), iv = __frcp_rn(vscale);
-    if (!__all_sync(0xffffffffu, wait(bar.s_full(buf), (n >> 1) & 1, abort))) return false;
-    tc_fence_after();
+    const float vscale = fmaxf(c.vs, cache8_two_to(kCache8LeastExponent)), lv = __log2f(vscale);
+    const uint64_t ks2 = f2_pack(c.ks, c.ks), lv2 = f2_pack(lv, lv), iv2 = f2_pack(__fdividef(1.f, vscale), __fdividef(1.f, vscale));
+    w.next();
+    if (w.left > 0) load_scales(p, w, t, c);  // the next tile's are under way meanwhile
     uint32_t sr[NS];
+    wait(bar.s_full(buf), (n >> 1) & 1, abort);
+    __syncwarp();
+    tc_fence_after();
     tmem_ld32(c.at + C::S_COL + NS * buf, sr);
     tmem_wait_ld();
-    float y[NR];
+    uint64_t y[NR / 2], z[NR / 2];  // pairs of rows
+    const uint64_t small16 = f2_pack(0.0625f, 0.0625f);
 #pragma unroll
-    for (int q = 0; q < NR; q += 4) {
-      const float4 f = *reinterpret_cast<const float4*>(fac + q);
-      const float ff[4] = {f.x, f.y, f.z, f.w};
+    for (int q = 0; q < NR / 2; q += 2) {
+      const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(fac + 2 * q);
+      const uint64_t ff[2] = {f.x, f.y};
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        y[q + i] = fmaf(fmaf(__uint_as_float(sr[NR + q + i]), 0.0625f, __uint_as_float(sr[q + i])), ff[i] * kscale, lv);
+      for (int i = 0; i < 2; ++i) {
+        const int r = 2 * (q + i);
+        const uint64_t a = f2_pack(__uint_as_float(sr[r]), __uint_as_float(sr[r + 1]));
+        const uint64_t b = f2_pack(__uint_as_float(sr[NR + r]), __uint_as_float(sr[NR + r + 1]));
+        y[q + i] = f2_fma(f2_fma(b, small16, a), f2_mul(ff[i], ks2), lv2);
+      }
     }
     if (!(key0 >= lo_all && key0 + T - 1 <= hi_all)) {
       const int key = key0 + t;
 #pragma unroll
-      for (int q = 0; q < NR; ++q) {
-        const int2 r = rng[q];
-        if (key < r.x || key > r.y) y[q] = -INFINITY;
+      for (int q = 0; q < NR / 2; ++q) {
+        const int4 r = *reinterpret_cast<const int4*>(rng + 2 * q);
+        float2 v = f2_unpack(y[q]);
+        if (key < r.x || key > r.y) v.x = -INFINITY;
+        if (key < r.z || key > r.w) v.y = -INFINITY;
+        y[q] = f2_pack(v.x, v.y);
       }
     }
-    bool grow = fresh, scale = false;
+    auto less_reference = [&]() {  // z = y - reference
+#pragma unroll
+      for (int q = 0; q < NR / 2; q += 2) {
+        const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(nref + 2 * q);
+        z[q] = f2_add(y[q], f.x);
+        z[q + 1] = f2_add(y[q + 1], f.y);
+      }
+    };
+    bool scale = false, grow = true;
     if (!fresh) {
+      less_reference();
       float over = -INFINITY;
 #pragma unroll
-      for (int q = 0; q < NR; q += 4) {
-        const float4 f = *reinterpret_cast<const float4*>(ref + q);
-        over = fmax3(over, y[q] - f.x, y[q + 1] - f.y);
-        over = fmax3(over, y[q + 2] - f.z, y[q + 3] - f.w);
+      for (int q = 0; q < NR / 2; ++q) {
+        const float2 v = f2_unpack(z[q]);
+        over = fmax3(over, v.x, v.y);
       }
-      if (__any_sync(0xffffffffu, over > kTop) && lane == 0) grow_tag[n & 1] = n + 1;
-      if (!exchange()) return false;
-      grow = grow_tag[n & 1] == n + 1;
+      grow = soft_any(over > kTop);
     }
-    if (grow) {
-      float* rb = red + (c.xc & 1) * 4 * NR;
+    if (grow) {  // some weight passes the top, or the visit begins
       float mx[NR];
 #pragma unroll
-      for (int q = 0; q < NR; ++q) mx[q] = y[q];
+      for (int q = 0; q < NR / 2; ++q) {
+        const float2 v = f2_unpack(y[q]);
+        mx[2 * q] = v.x;
+        mx[2 * q + 1] = v.y;
+      }
       column_reduce<true>(mx, lane);
-      if ((lane & 1) == 0) rb[q4 * NR + (lane >> 1)] = mx[0];
-      if (!exchange()) return false;
+      if ((lane & 1) == 0) red[q4 * NR + (lane >> 1)] = mx[0];
+      soft_sync();
+      bool moved = false;
       if (t < NR) {
-        const float tm = fmaxf(fmaxf(rb[t], rb[NR + t]), fmaxf(rb[2 * NR + t], rb[3 * NR + t]));
+        const float tm = fmaxf(fmaxf(red[t], red[NR + t]), fmaxf(red[2 * NR + t], red[3 * NR + t]));
         float a = 1.f;
         if (tm - m_row > kTop) {  // (a row without a key yet: its reference is the lowest number)
           const float to = tm - kBelow;
           if (m_row != kUnset) {
             a = fast_exp2(m_row - to);
-            *scale_tag = n + 1;
+            moved = true;
           }
           m_row = to;
-          ref[t] = to;
+          nref[t] = -to;
         }
         alp[t] = a;
       }
-      if (!exchange()) return false;
-      scale = *scale_tag == n + 1;
+      scale = soft_any(moved);
       if (scale) {
 #pragma unroll
-        for (int q = 0; q < NR; q += 4) {
-          const float4 v = *reinterpret_cast<const float4*>(alp + q);
-          l_part[q] *= v.x;
-          l_part[q + 1] *= v.y;
-          l_part[q + 2] *= v.z;
-          l_part[q + 3] *= v.w;
-        }
+        for (int q = 0; q < NR / 2; ++q) l_part[q] = f2_mul(l_part[q], *reinterpret_cast<const uint64_t*>(alp + 2 * q));
       }
+      less_reference();
     }
     fresh = false;
     // the weights 2^(y - reference), their row sums, and their three parts: hi is
     // a weight in fp16 rounded to its top byte, mid the rest so, lo the rest of that
     uint32_t part[3][NR / 4];
 #pragma unroll
-    for (int q = 0; q < NR; q += 4) {
-      const float4 f = *reinterpret_cast<const float4*>(ref + q);
-      const float e0 = fast_exp2(y[q] - f.x), e1 = fast_exp2(y[q + 1] - f.y);
-      const float e2 = fast_exp2(y[q + 2] - f.z), e3 = fast_exp2(y[q + 3] - f.w);
-      l_part[q] = fmaf(e0, iv, l_part[q]);
-      l_part[q + 1] = fmaf(e1, iv, l_part[q + 1]);
-      l_part[q + 2] = fmaf(e2, iv, l_part[q + 2]);
-      l_part[q + 3] = fmaf(e3, iv, l_part[q + 3]);
-      uint32_t a = pack_half2(e0, e1), b = pack_half2(e2, e3);
+    for (int q = 0; q < NR / 2; q += 2) {
+      float2 e = f2_unpack(z[q]), f = f2_unpack(z[q + 1]);
+      e.x = fast_exp2(e.x);
+      e.y = fast_exp2(e.y);
+      f.x = fast_exp2(f.x);
+      f.y = fast_exp2(f.y);
+      l_part[q] = f2_fma(f2_pack(e.x, e.y), iv2, l_part[q]);
+      l_part[q + 1] = f2_fma(f2_pack(f.x, f.y), iv2, l_part[q + 1]);
+      uint32_t a = pack_half2(e.x, e.y), b = pack_half2(f.x, f.y);
 #pragma unroll
       for (int i = 0; i < 3; ++i) {
         const uint32_t ra = a + 0x00800080u, rb = b + 0x00800080u;
-        part[i][q / 4] = __byte_perm(ra, rb, 0x7531);
+        part[i][q / 2] = __byte_perm(ra, rb, 0x7531);
         if (i < 2) {
           const uint32_t ta = ra & 0xFF00FF00u, tb = rb & 0xFF00FF00u;
           const __half2 da = __hsub2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<const __half2*>(&ta));
@@ -484,8 +479,9 @@ __device__ bool softmax_visit(const C8Params& p, unsigned char* base, const Bars
       }
     }
     // the second product of tile n - 1 has finished with the weights' buffer, and with O^T before it is rescaled
-    if (n > 0 && !__all_sync(0xffffffffu, wait(bar.o_done(), (n - 1) & 1, abort))) return false;
+    if (n > 0) wait(bar.o_done(), (n - 1) & 1, abort);
     if (scale) {  // uniform over the warps
+      __syncwarp();
       tc_fence_after();
 #pragma unroll 1
       for (int i = 0; i < 3 * C::NCH; ++i) {
@@ -508,19 +504,26 @@ __device__ bool softmax_visit(const C8Params& p, unsigned char* base, const Bars
     __syncwarp();
     if (lane == 0) mbar_arrive(bar.p_full());
     ++c.n;
-    w.next();
   }
   ++c.visit;
 
   // row sums over the 128 threads, then O^T
-  float* rb = red + (c.xc & 1) * 4 * NR;
-  column_reduce<false>(l_part, lane);
-  if ((lane & 1) == 0) rb[q4 * NR + (lane >> 1)] = l_part[0];
-  if (!exchange()) return false;
+  {
+    float l[NR];
+#pragma unroll
+    for (int q = 0; q < NR / 2; ++q) {
+      const float2 v = f2_unpack(l_part[q]);
+      l[2 * q] = v.x;
+      l[2 * q + 1] = v.y;
+    }
+    column_reduce<false>(l, lane);
+    if ((lane & 1) == 0) red[q4 * NR + (lane >> 1)] = l[0];
+  }
+  soft_sync();
   float* mul = alp;  // a whole segment's 1 / sum
   const size_t slot = (size_t)(2 * blockIdx.x + (c.visit > 1 ? 1 : 0)) * p.orow;
   if (t < rows) {
-    const float l = (rb[t] + rb[NR + t]) + (rb[2 * NR + t] + rb[3 * NR + t]);
+    const float l = (red[t] + red[NR + t]) + (red[2 * NR + t] + red[3 * NR + t]);
     if (whole) {
       const int m = blk * NR + t;
       float lse;
@@ -530,8 +533,9 @@ __device__ bool softmax_visit(const C8Params& p, unsigned char* base, const Bars
       *reinterpret_cast<float2*>(p.ml + 2 * (slot + t)) = make_float2(m_row, l);
     }
   }
-  if (whole && !exchange()) return false;
-  if (!__all_sync(0xffffffffu, wait(bar.o_done(), (c.n - 1) & 1, abort))) return false;
+  soft_sync();
+  wait(bar.o_done(), (c.n - 1) & 1, abort);
+  __syncwarp();
   tc_fence_after();
 #pragma unroll 1
   for (int h = 0; h < C::NCH; ++h) {
@@ -543,18 +547,18 @@ __device__ bool softmax_visit(const C8Params& p, unsigned char* base, const Bars
     tmem_wait_ld();
     const int d = T * h + t;
     if (d < D) {
+      uint16_t* o = p.o + ((size_t)head * g.M + blk * NR) * D + d;
+      float* po = p.po + slot * D + d;
 #pragma unroll
       for (int q = 0; q < NR; ++q)
         if (q < rows) {
           const float v = __uint_as_float(hi[q]) + (__uint_as_float(mid[q]) + __uint_as_float(lo[q]));
-          if (whole)
-            p.o[((size_t)head * g.M + blk * NR + q) * D + d] = __bfloat16_as_ushort(__float2bfloat16_rn(v * mul[q]));
-          else p.po[(slot + q) * D + d] = v;
+          if (whole) o[q * D] = __bfloat16_as_ushort(__float2bfloat16_rn(v * mul[q]));
+          else po[q * D] = v;
         }
     }
   }
   tc_fence_before();  // ordered before the next visit's first product by its arrival
-  return true;
 }
 
 template <int D>
@@ -562,13 +566,13 @@ __global__ void __launch_bounds__(kThr, 2)
     cache8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const __grid_constant__ C8Params p) {
   using C = C8<D>;
-  constexpr int NW = kThr / 32, NSLOT = C::NSLOT, NCH = C::NCH;
+  constexpr int NSLOT = C::NSLOT, NCH = C::NCH;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ int scan_sum[NW], start_b, start_r;
   unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const Bars bar{reinterpret_cast<uint64_t*>(base + C::OFF_BAR)};
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar.b + 30);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bar.b + 31);
+  float* qfac = reinterpret_cast<float*>(base + C::OFF_SMALL + C::QFAC);
   const Cache8Geom& g = p.g;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, cta = blockIdx.x;
 
@@ -581,8 +585,7 @@ __global__ void __launch_bounds__(kThr, 2)
     mbar_init(bar.b + threadIdx.x, Bars::arrivals(threadIdx.x));
     fence_mbar_init();
   }
-  if (threadIdx.x >= 32 && threadIdx.x < 36)  // the tags
-    reinterpret_cast<int*>(base + C::OFF_SMALL + C::BND)[8 + threadIdx.x - 32] = 0;
+  __syncthreads();
   grid_dependency_wait();
   // Tensor memory is taken after the predecessor's end and before a dependent
   // may be placed: a grid that held columns while it waits for another that has
@@ -590,80 +593,52 @@ __global__ void __launch_bounds__(kThr, 2)
   if (warp == 1) {
     tmem_alloc(tmem_slot, C::TCOLS);
     tmem_relinquish();
+    grid_launch_dependents();  // the merge waits for this grid's end
   }
-  // ---- the lengths: tiles in all
-  const int nt0 = threadIdx.x < g.B ? tiles_of(g, p.kv_len[threadIdx.x]) : 0;  // of request threadIdx.x
-  {
-    int sum = nt0;
-#pragma unroll 1
-    for (int b = kThr + threadIdx.x; b < g.B; b += kThr) sum += tiles_of(g, p.kv_len[b]);
-    sum = __reduce_add_sync(0xffffffffu, sum);
-    if (lane == 0) scan_sum[warp] = sum;
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  grid_launch_dependents();  // the merge waits for this grid's end
-  const uint32_t tmem = *tmem_slot;
-  int tiles = 0;
-#pragma unroll
-  for (int i = 0; i < NW; ++i) tiles += scan_sum[i];
+  // ---- this CTA's run, by every warp for itself: the tiles of all requests, then
+  // the request that the run's first unit belongs to
+  auto tiles_at = [&](int b) { return b < g.B ? tiles_of(g, p.kv_len[b]) : 0; };
+  const int nt0 = tiles_at(lane);  // of the first 32
+  unsigned tiles = nt0;
+#pragma unroll 2
+  for (int b = lane + 32; b < g.B; b += 32) tiles += tiles_at(b);
+  tiles = __reduce_add_sync(0xffffffffu, tiles);
   const unsigned hn = g.Hkv * g.nmb;
-  const Runs runs(tiles * hn);
-  const unsigned u0 = runs.start(cta), u1 = runs.start(cta + 1);
-  // ---- the request that unit u0 belongs to
-  if (u0 < u1) {
-    int before = 0;
+  const Runs runs{tiles * hn};
+  const unsigned u0 = runs.start(cta);
+  const int units = (int)(runs.start(cta + 1) - u0);
+  Walk first;  // the run's first unit
+  first.p = &p;
+  first.left = 0;
+  if (units > 0) {
+    unsigned before = 0;
 #pragma unroll 1
-    for (int c0 = 0; c0 < g.B; c0 += kThr) {
-      const int b = c0 + threadIdx.x;
-      const int nt = c0 == 0 ? nt0 : (b < g.B ? tiles_of(g, p.kv_len[b]) : 0);
-      int inc = nt;
+    for (int b0 = 0; b0 < g.B; b0 += 32) {
+      const unsigned nt = b0 == 0 ? nt0 : tiles_at(b0 + lane);
+      unsigned inc = nt;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        const unsigned v = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += v;
       }
-      __syncthreads();
-      if (lane == 31) scan_sum[warp] = inc;
-      __syncthreads();
-      int off = before + inc - nt;
-#pragma unroll
-      for (int i = 0; i < NW; ++i) {
-        const int v = scan_sum[i];
-        if (i < warp) off += v;
-        before += v;
+      const unsigned here = __ballot_sync(0xffffffffu, u0 < (before + inc) * hn);
+      if (here) {
+        const int l = __ffs(here) - 1;
+        const unsigned at = before + __shfl_sync(0xffffffffu, inc - nt, l);
+        first.begin(b0 + l, (int)(u0 - at * hn), units);
+        break;
       }
-      if (nt > 0 && u0 >= off * hn && u0 < (off + nt) * hn) {
-        start_b = b;
-        start_r = (int)(u0 - off * hn);
-      }
+      before += __shfl_sync(0xffffffffu, inc, 31);
     }
-    __syncthreads();
   }
-  const int total = (int)(u1 - u0);
-  auto walk = [&]() {
-    Walk w;
-    w.p = &p;
-    w.begin(start_b, start_r, total);
-    return w;
-  };
-  if (threadIdx.x == 0) {  // for the merge
-    int4 cut = make_int4(-1, 0, 0, (int)runs.units);
-    if (total > 0) {
-      const Walk w = walk();
-      const int begin = (int)u0 - w.t;
-      cut = make_int4(w.head() * g.nmb + w.blk, begin, begin + w.nt, (int)runs.units);
-    }
-    p.cuts[cta] = cut;
-  }
+  const int total = first.left;
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (total > 0 && elect_one()) {
       // the cache, which a call reads once (but for further row blocks), gives way in L2
       const uint64_t policy = l2_policy(true);
-      Walk wk = walk(), wv = wk;
+      Walk wk = first, wv = first;
       int issued = 0;
       auto load_tile = [&](Walk& w, const CUtensorMap* m) -> bool {
         const int key0 = w.key0(), head = w.head();
@@ -685,6 +660,9 @@ __global__ void __launch_bounds__(kThr, 2)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
+    tmem_sync();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
     if (total > 0 && elect_one()) {
       constexpr uint32_t idS = idesc_f8(T, NS, 0, 0, 0, 0);  // K x Q^T, both K-major, e4m3
       constexpr uint32_t idO = idesc_f8(T, NP, 0, 1, 1, 1);  // V^T (e4m3) x weights^T (e5m2), both MN-major
@@ -693,7 +671,7 @@ __global__ void __launch_bounds__(kThr, 2)
       const uint64_t kd0 = smem_desc(smem_u32(base), D < 128 ? 0 : 16, 8 * C::LINE, SWZ);
       const uint64_t qd0 = smem_desc(smem_u32(base + C::OFF_Q), 16, 8 * C::LINE, SWZ);
       const uint64_t pd = smem_desc(smem_u32(base + C::OFF_P), 8 * NR, T * NR, 0);
-      Walk ws = walk(), wv = ws;
+      Walk ws = first, wv = first;
       int used = 0, nq = 0;
       auto issue_s = [&](int n) -> bool {  // S^T(n) into buffer n & 1
         const int qs = nq & 1;
@@ -747,32 +725,46 @@ __global__ void __launch_bounds__(kThr, 2)
     }
   } else if (warp < 6) {
     // ------------------------------------------------------------ softmax
+    Walk w = first;
+    Soft c;
+    c.n = c.visit = 0;
     if (total > 0) {
-      Walk w = walk();
-      prepare_queries<D>(p, w.head(), w.blk, base + C::OFF_Q, reinterpret_cast<float*>(base + C::OFF_SMALL + C::QFAC),
-                         warp - 2, 4, lane);
+      load_scales(p, w, 32 * (warp & 3) + lane, c);
+      prepare_queries<D>(p, w.head(), w.blk, min(NR, g.M - w.blk * NR), base + C::OFF_Q, qfac, warp - 2, lane);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar.q_full(0));
-      bool ok = true;
-      Soft c{tmem + ((uint32_t)(32 * (warp & 3)) << 16), 0, 0, 0};
-#pragma unroll 1
-      while (ok && w.left > 0) ok = softmax_visit<D>(p, base, bar, abort_flag, w, c);
     }
+    tmem_sync();
+    tc_fence_after();
+    c.at = *tmem_slot + ((uint32_t)(32 * (warp & 3)) << 16);
+#pragma unroll 1
+    while (w.left > 0) softmax_visit<D>(p, base, bar, abort_flag, w, c);
   } else {
     // ------------------------------------------------------------ the later visits' queries
-    if (total > 0) {
-      Walk w = walk();
-      w.skip();
-#pragma unroll 1
-      for (int v = 1; w.left > 0; ++v) {
-        const int s = v & 1;
-        if (v >= 2 && !__all_sync(0xffffffffu, wait(bar.q_empty(s), ((v >> 1) & 1) ^ 1, abort_flag))) break;
-        prepare_queries<D>(p, w.head(), w.blk, base + C::OFF_Q + s * C::QB,
-                           reinterpret_cast<float*>(base + C::OFF_SMALL + C::QFAC) + (v & 3) * NR, 0, 1, lane);
-        __syncwarp();
-        if (lane < 4) mbar_arrive(bar.q_full(s));
-        w.skip();
+    if (lane == 0) {  // for the merge
+      int4 cut = make_int4(-1, 0, 0, 0);
+      if (total > 0 && first.t > 0) {
+        const unsigned begin = u0 - first.t;
+        const int c0 = (int)runs.of(begin);
+        cut = make_int4(first.head() * g.nmb + first.blk, (int)runs.of(begin + first.nt - 1) - c0 + 1, c0,
+                        2 * c0 + (runs.start(c0) == begin ? 0 : 1));
       }
+      p.cuts[cta] = cut;
+    }
+    Walk w = first;
+    if (total > 0) w.skip();
+#pragma unroll 1
+    for (int v = 1; w.left > 0; ++v) {
+      const int s = v & 1;
+      if (v >= 2 && !__all_sync(0xffffffffu, wait(bar.q_empty(s), ((v >> 1) & 1) ^ 1, abort_flag))) break;
+      // (the softmax reads the factors of visit v - 3 at most: the scores are two tiles ahead of it, the queries two visits)
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i)
+        prepare_queries<D>(p, w.head(), w.blk, min(NR, g.M - w.blk * NR), base + C::OFF_Q + s * C::QB, qfac + (v & 3) * NR, i,
+                           lane);
+      __syncwarp();
+      if (lane < 4) mbar_arrive(bar.q_full(s));
+      w.skip();
     }
     // requests without a key: no unit is theirs
 #pragma unroll 1
@@ -793,87 +785,138 @@ __global__ void __launch_bounds__(kThr, 2)
   if (*abort_flag && threadIdx.x == 0) atomicCAS(p.status, 0, kStatusTimeout);
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, C::TCOLS);
+    tmem_dealloc(*tmem_slot, C::TCOLS);
   }
 }
 
-// Merge of one row of the segment that the begin of run blockIdx.x cuts: the
-// first cut of a segment does it for all of them.  With R = max R_i over the
-// partials, o = sum 2^(R_i - R) O_i / sum 2^(R_i - R) l_i.
-template <int D>
-__global__ void __launch_bounds__(128) cache8_merge_kernel(const __grid_constant__ C8Params p) {
-  constexpr int LANES = D / 4, GR = 128 / LANES, AHEAD = D == 512 ? 6 : 8;
-  __shared__ float4 part[GR][LANES];
+// Merge of the partials of the segment that the begin of run blockIdx.x cuts.  A
+// segment in n runs has n - 1 cuts, whose CTAs take its rows in turn, or pieces of
+// 64 columns of its rows where there are more cuts than those; a CTA's warps share
+// the partials of its pieces.  With R = max R_i over the partials,
+// o = sum 2^(R_i - R) O_i / sum 2^(R_i - R) l_i.
+constexpr int kMergeWarps = 4, kMergeSides = 2;  // warps a CTA, CTAs a cut
+
+// One pass over a CTA's pieces of W columns; n = 0: none (see the kernel).
+template <int D, int W>
+__device__ __forceinline__ void merge_pieces(const C8Params& p, const int4& cut, int rows, float (&part)[kMergeWarps][W],
+                                             float2 (&stat)[kMergeWarps]) {
+  constexpr int LANES = W / 4 < 32 ? W / 4 : 32, SIDE = 32 / LANES;  // lanes on a partial, partials side by side
+  constexpr int N = W / 4 / LANES, AHEAD = 4 / N, PIECES = D / W;    // vectors a lane, partials under way, pieces of a row
   const Cache8Geom& g = p.g;
-  const int cta = blockIdx.x, row = blockIdx.y, lane = threadIdx.x & 31;
-  grid_launch_dependents();
-  grid_dependency_wait();
-  const int4 cut = p.cuts[cta];
-  if (cut.x < 0) return;
-  const Runs runs(cut.w);
-  const unsigned u0 = cut.y, u1 = cut.z;
-  const int c0 = (int)runs.of(u0);
-  if (c0 != cta - 1) return;  // the run begins with the segment (c0 == cta), or an earlier cut is the first
-  const int head = cut.x / g.nmb, blk = cut.x - head * g.nmb, rows = min(NR, g.M - blk * NR);
-  if (row >= rows) return;
-  const int n = (int)runs.of(u1 - 1) - c0 + 1;
-  const int slot0 = 2 * c0 + (runs.start(c0) == u0 ? 0 : 1);
-  auto slot_of = [&](int i) { return (size_t)(i == 0 ? slot0 : 2 * (c0 + i)) * p.orow + row; };
-  auto ml_of = [&](int i) { return *reinterpret_cast<const float2*>(p.ml + 2 * slot_of(i)); };
-  const int grp = threadIdx.x / LANES, d = threadIdx.x % LANES;
-  auto o_of = [&](int i) { return *reinterpret_cast<const float4*>(p.po + slot_of(i) * D + 4 * d); };
-  // all first loads are under way before any is used
-  const float2 first = lane < n ? ml_of(lane) : make_float2(kUnset, 0.f);
-  float4 v[AHEAD];
-  float mi[AHEAD];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l0 = lane % LANES;
+  const int n = cut.y, head = g.nmb == 1 ? cut.x : cut.x / g.nmb, blk = cut.x - head * g.nmb;
+  // pieces first, first + step, .. of `all` (the quotient of numbers below 2^12 is exact)
+  const int all = rows * PIECES, first = kMergeSides * ((int)blockIdx.x - cut.z - 1) + blockIdx.y, step = max(kMergeSides * (n - 1), 1);
+  const int mine = n == 0 ? 4 : (first < all ? (int)__fdividef(all - first + step - 0.5f, (float)step) : 0);
+  const int sh = mine >= kMergeWarps ? 0 : 2 - (32 - __clz(mine - 1)), share = 1 << sh;  // warps on a piece
+  const int k = warp & (share - 1);
+#pragma unroll 1
+  for (int i0 = 0; i0 < mine; i0 += kMergeWarps >> sh) {
+    const int i = i0 + (warp >> sh);
+    const bool on = i < mine;
+    const int piece = first + i * step, row = piece / PIECES, col = (piece - row * PIECES) * W;
+    float acc[4 * N];
 #pragma unroll
-  for (int i = 0; i < AHEAD; ++i) {
-    const int j = grp + GR * i;
-    if (j < n) {
-      v[i] = o_of(j);
-      mi[i] = ml_of(j).x;
+    for (int e = 0; e < 4 * N; ++e) acc[e] = 0.f;
+    float m = kUnset, l = 0.f;
+    if (on) {
+      float4 v[AHEAD][N];
+      float2 ml[AHEAD];
+      auto load = [&](int a, int j) {
+        ml[a] = make_float2(kUnset, 0.f);
+        if (j >= n) return;
+        const size_t at = (size_t)(j == 0 ? cut.w : 2 * (cut.z + j)) * p.orow + row;
+        ml[a] = *reinterpret_cast<const float2*>(p.ml + 2 * at);
+        const float4* src = reinterpret_cast<const float4*>(p.po + at * D + col) + l0;
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[a][e] = src[LANES * e];
+      };
+      const int j0 = k * SIDE + lane / LANES, dj = share * SIDE;
+#pragma unroll 1
+      for (int j = j0; j - j0 % dj < max(n, 1); j += dj * AHEAD) {
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) load(a, j + dj * a);
+        float to = m;
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) to = fmaxf(to, ml[a].x);
+        const float w0 = fast_exp2(m - to);
+        l *= w0;
+#pragma unroll
+        for (int e = 0; e < 4 * N; ++e) acc[e] *= w0;
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a)
+          if (j + dj * a < n) {  // (a part without a visible key: its sum and O are 0)
+            const float w = fast_exp2(ml[a].x - to);
+            l = fmaf(w, ml[a].y, l);
+#pragma unroll
+            for (int e = 0; e < 4 * N; ++e) acc[e] = fmaf(w, reinterpret_cast<const float*>(v[a])[e], acc[e]);
+          }
+        m = to;
+      }
     }
-  }
-  float mx = first.x;
+    auto join = [&](float m2, float l2, auto&& of) {  // with another stream's reference, sum and elements
+      const float to = fmaxf(m, m2), a = fast_exp2(m - to), b = fast_exp2(m2 - to);
+      m = to;
+      l = l * a + l2 * b;
+#pragma unroll
+      for (int e = 0; e < 4 * N; ++e) acc[e] = acc[e] * a + of(e) * b;
+    };
+    if (SIDE == 2) {
+      const float m2 = __shfl_xor_sync(0xffffffffu, m, 16), l2 = __shfl_xor_sync(0xffffffffu, l, 16);
+      join(m2, l2, [&](int e) { return __shfl_xor_sync(0xffffffffu, acc[e], 16); });
+    }
+    auto place = [&](int e) { return 4 * LANES * (e / 4) + 4 * l0 + e % 4; };  // of a lane's element e
+    if (share > 1) {
+      if (lane == 0) stat[warp] = make_float2(m, l);
+#pragma unroll
+      for (int e = 0; e < 4 * N; ++e)
+        if (lane < LANES) part[warp][place(e)] = acc[e];
+      __syncthreads();
+      if (on && k == 0) {
 #pragma unroll 1
-  for (int i = lane + 32; i < n; i += 32) mx = fmaxf(mx, ml_of(i).x);
+        for (int w = warp + 1; w < warp + share; ++w) join(stat[w].x, stat[w].y, [&](int e) { return part[w][place(e)]; });
+      }
+      __syncthreads();
+    }
+    if (!on || k > 0 || lane >= LANES || n == 0) continue;
+    const int r = blk * NR + row;
+    float lse;
+    const float inv = finish_row(p.sinks ? p.sinks + (head % g.Hkv) * g.G + r / g.Lq : nullptr, m, l, &lse);
+    const size_t at = (size_t)head * g.M + r;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  // (a part without a visible key: its sum and O are 0)
-  auto weight = [&](float x) { return exp2f(x - mx); };
-  float l = weight(first.x) * first.y;
-#pragma unroll 1
-  for (int i = lane + 32; i < n; i += 32) {
-    const float2 t = ml_of(i);
-    l += weight(t.x) * t.y;
+    for (int e = 0; e < 4 * N; e += 4) {
+      const __nv_bfloat162 x = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
+      const __nv_bfloat162 y = __floats2bfloat162_rn(acc[e + 2] * inv, acc[e + 3] * inv);
+      *reinterpret_cast<uint2*>(p.o + at * D + col + place(e)) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+    }
+    if (col == 0 && lane == 0) p.lse[at] = lse;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](float w, const float4& u) {
-    acc.x = fmaf(w, u.x, acc.x);
-    acc.y = fmaf(w, u.y, acc.y);
-    acc.z = fmaf(w, u.z, acc.z);
-    acc.w = fmaf(w, u.w, acc.w);
-  };
-#pragma unroll
-  for (int i = 0; i < AHEAD; ++i)
-    if (grp + GR * i < n) add(weight(mi[i]), v[i]);
-#pragma unroll 4
-  for (int j = grp + GR * AHEAD; j < n; j += GR) add(weight(ml_of(j).x), o_of(j));
-  part[grp][d] = acc;
-  __syncthreads();
-  if (grp > 0) return;
-#pragma unroll
-  for (int i = 1; i < GR; ++i) add(1.f, part[i][d]);
-  const int m = blk * NR + row;
-  float lse;
-  const float inv = finish_row(p.sinks ? p.sinks + (head % g.Hkv) * g.G + m / g.Lq : nullptr, mx, l, &lse);
-  const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), b = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-  const size_t at = (size_t)head * g.M + m;
-  *reinterpret_cast<uint2*>(p.o + at * D + 4 * d) =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-  if (d == 0) p.lse[at] = lse;
+}
+
+// What is behind the wait for the main grid is gone through once before it, on no
+// partials: code that a CTA runs once is fetched at the memory's latency, and there
+// is time while the last runs end.
+template <int D>
+__global__ void __launch_bounds__(32 * kMergeWarps, 6) cache8_merge_kernel(const __grid_constant__ C8Params p) {
+  __shared__ union {
+    float whole[kMergeWarps][D], piece[kMergeWarps][64];
+  } part;
+  __shared__ float2 stat[kMergeWarps];
+  grid_launch_dependents();
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    int4 cut = make_int4(0, 0, 0, 0);
+    if (pass) {
+      grid_dependency_wait();
+      cut = p.cuts[blockIdx.x];
+      if (cut.x < 0) return;
+    }
+    const int blk = p.g.nmb == 1 ? 0 : cut.x % p.g.nmb, rows = min(NR, p.g.M - blk * NR);
+    const bool pieces = D == 64 || cut.y > rows * (D / 64);
+    if (pieces || !pass) merge_pieces<D, 64>(p, cut, rows, part.piece, stat);
+    if (D > 64 && !pieces) merge_pieces<D, D>(p, cut, rows, part.whole, stat);
+  }
 }
 
 struct C8Ws {
@@ -929,7 +972,7 @@ cudaError_t cache8_d(const Cache8Geom& g, const Cache8Args& a, void* ws, int* st
   // both are programmatic dependents of what runs before them: the main grid's
   // set-up and the merge's placement fall into its predecessor's end
   if ((e = launch_dependent(kern, dim3(kCtas), dim3(kThr), C::SMEM, st, tk, tv, p)) != cudaSuccess) return e;
-  return launch_dependent(cache8_merge_kernel<D>, dim3(kCtas, p.orow), dim3(128), 0, st, p);
+  return launch_dependent(cache8_merge_kernel<D>, dim3(kCtas, kMergeSides), dim3(32 * kMergeWarps), 0, st, p);
 }
 
 }  // namespace
