@@ -753,15 +753,23 @@ __global__ void __launch_bounds__(kThr, 2)
     }
     Walk w = first;
     if (total > 0) w.skip();
+    int filled = 0x44;  // groups of rows of either buffer that may not be zero
 #pragma unroll 1
     for (int v = 1; w.left > 0; ++v) {
       const int s = v & 1;
       if (v >= 2 && !__all_sync(0xffffffffu, wait(bar.q_empty(s), ((v >> 1) & 1) ^ 1, abort_flag))) break;
       // (the softmax reads the factors of visit v - 3 at most: the scores are two tiles ahead of it, the queries two visits)
+      const int rows = min(NR, g.M - w.blk * NR);
+      // all rows are asked for at once (four at a time would take four times the memory's latency)
+      const unsigned char* q = reinterpret_cast<const unsigned char*>(p.q + ((size_t)w.head() * g.M + w.blk * NR) * D);
 #pragma unroll 1
-      for (int i = 0; i < 4; ++i)
-        prepare_queries<D>(p, w.head(), w.blk, min(NR, g.M - w.blk * NR), base + C::OFF_Q + s * C::QB, qfac + (v & 3) * NR, i,
-                           lane);
+      for (int i = lane; i < rows * (D / 64); i += 32) asm volatile("prefetch.global.L1 [%0];" ::"l"(q + 128 * i));
+      // rows behind the block's are zero once they have been
+      const int groups = (rows + 3) / 4, old = filled >> (4 * s) & 15;  // of four rows
+#pragma unroll 1
+      for (int i = 0; i < max(groups, old); ++i)
+        prepare_queries<D>(p, w.head(), w.blk, rows, base + C::OFF_Q + s * C::QB, qfac + (v & 3) * NR, i, lane);
+      filled = (filled & ~(15 << (4 * s))) | groups << (4 * s);
       __syncwarp();
       if (lane < 4) mbar_arrive(bar.q_full(s));
       w.skip();

@@ -291,3 +291,28 @@ def test_attention(D, B, Hq, Hkv, Lq, rows, window, sinks, block, lens):
     kc, vc = filled(B, Hkv, rows, D, block, 31, 0.3), filled(B, Hkv, rows, D, block, 32)
     s = torch.randn(Hq, generator=g) if sinks else None
     check_attention(q, kc, vc, s, lens, window, 1.0 / math.sqrt(D), block)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,Hq,Hkv,Lq,D,rows,window,block,spread", [
+    (16, 4, 4, 1, 64, 8192, 0, 64, 1),      # equal lengths: every run in several waves
+    (40, 8, 4, 1, 128, 5000, 0, 128, 0),    # ragged ones
+    (3, 16, 8, 3, 256, 20000, 0, 16, 0),    # long segments, cut by many runs
+    (33, 12, 4, 4, 512, 4000, 2500, 32, 0),  # 12 rows, a window
+])
+def test_attention_of_many_tiles(B, Hq, Hkv, Lq, D, rows, window, block, spread):
+    """More tiles than five a CTA: runs that CTAs take over, and their merge."""
+    g = torch.Generator().manual_seed(rows)
+    q = torch.randn(B, Hq, Lq, D, generator=g).to(BF)
+    x = torch.randint(0, 256, (2, B, Hkv, rows, D), generator=g, dtype=torch.uint8)
+    x &= 0xDF  # no NaN, 30 at most
+    kc, vc = (t.view(F8) for t in x)
+    s = torch.exp2(torch.randint(-6, -2, (2, B, Hkv, -(-rows // block)), generator=g).float())
+    lens = [rows] * B if spread else torch.randint(1, rows + 1, (B,), generator=g).tolist()
+    some = sorted({0, B // 2, B - 1})  # (the whole batch in 64 bits on the host would take minutes)
+    got_o, got_lse = attend(q, (kc, s[0]), (vc, s[1]), None, lens, window, 0.25 / math.sqrt(D), block)
+    o, tol, lse, ltol = attention(q[some], x[0][some].view(F8), x[1][some].view(F8), s[0][some], s[1][some], None,
+                                  [lens[b] for b in some], window, 0.25 / math.sqrt(D), block)
+    assert bool(((got_o[some] - o).abs() <= tol).all()) and bool(((got_lse[some] - lse).abs() <= ltol).all())
+    again = attend(q, (kc, s[0]), (vc, s[1]), None, lens, window, 0.25 / math.sqrt(D), block)
+    assert torch.equal(again[0], got_o) and torch.equal(again[1], got_lse)
