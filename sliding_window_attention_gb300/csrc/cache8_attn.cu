@@ -51,9 +51,7 @@ namespace {
 using namespace tc;
 
 constexpr int T = 128;       // keys per tile
-constexpr int NR = 16;       // query rows of a block
-constexpr int NS = 2 * NR;   // columns of S^T: q's two parts
-constexpr int NP = 3 * NR;   // columns of O^T: a weight's three parts
+constexpr int HR = 16;       // query rows that a softmax thread has in registers at a time
 constexpr int kCtas = 304;   // two an SM
 constexpr int kThr = 224;    // TMA, MMA, four softmax warps, one that prepares queries
 constexpr int kSmemMax = 115584;  // dynamic, a CTA: half of an SM's 228 KB less 1 KB that the system keeps and the static
@@ -147,22 +145,27 @@ struct Walk {
   }
 };
 
-template <int D>
+// The kernel with blocks of NR query rows: 16, or 32 where a kv head has more and
+// the accumulators fit (up to D = 256, there with one buffer of scores).
+template <int D, int NR>
 struct C8 {
+  static constexpr int NS = 2 * NR, NP = 3 * NR;  // columns of S^T (q's two parts) and O^T (a weight's three)
+  static constexpr int SBUF = 2 * NS + NP * (D < 128 ? 1 : D / 128) <= 256 ? 2 : 1;
   static constexpr int LINE = D < 128 ? D : 128;  // bytes of a key's line in a slot
   static constexpr int NCH = D / LINE;            // slots per tile and tensor; 128-row blocks of O^T
   static constexpr int SLOT = T * LINE;
-  static constexpr int QB = NS * D;               // a block of queries: the parts' 32 rows
+  static constexpr int QB = NS * D;               // a block of queries
   static constexpr int PB = NP * T;               // weights
-  // the softmax warps' small arrays: [4][16] exchanged maxima / sums, references, rescale factors, row ranges, and
+  // the softmax warps' small arrays: [4][NR] exchanged maxima / sums, references, rescale factors, row ranges, and
   // the row factors of four visits
-  static constexpr int RED = 0, REF = 256, ALPHA = REF + 64, RNG = ALPHA + 64, QFAC = RNG + 128, SMALL = QFAC + 256;
+  static constexpr int RED = 0, REF = 16 * NR, ALPHA = REF + 4 * NR, RNG = ALPHA + 4 * NR, QFAC = RNG + 8 * NR,
+                       SMALL = QFAC + 16 * NR;
   static constexpr int BARS = 256;
   static constexpr int FIT = (kSmemMax - 1024 - 2 * QB - PB - SMALL - BARS) / SLOT;
   static constexpr int NSLOT = FIT > 4 ? (D == 64 ? 8 : 4) : FIT;
   static constexpr int OFF_Q = NSLOT * SLOT, OFF_P = OFF_Q + 2 * QB, OFF_SMALL = OFF_P + PB, OFF_BAR = OFF_SMALL + SMALL;
   static constexpr size_t SMEM = (size_t)OFF_BAR + BARS + 1024;
-  static constexpr uint32_t S_COL = 0, O_COL = 2 * NS;  // TMEM columns: S^T twice, O^T's blocks
+  static constexpr uint32_t S_COL = 0, O_COL = SBUF * NS;  // TMEM columns: S^T's buffers, O^T's blocks
   static constexpr uint32_t COLS = O_COL + NP * NCH;
   static constexpr uint32_t TCOLS = COLS <= 128 ? 128 : 256;  // (two CTAs share the 512)
   static_assert(COLS <= 256, "TMEM columns");
@@ -216,11 +219,11 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
 
 // Column reduction of 16 columns over the warp's lanes by halving: lanes 2 c and 2 c + 1 end with column c in v[0].
 template <bool MAX>
-__device__ __forceinline__ void column_reduce(float (&v)[NR], int lane) {
+__device__ __forceinline__ void column_reduce(float (&v)[HR], int lane) {
   auto op = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
   int o = 16;
 #pragma unroll
-  for (int h = NR / 2; h >= 1; h >>= 1, o >>= 1) {
+  for (int h = HR / 2; h >= 1; h >>= 1, o >>= 1) {
     const bool up = lane & o;
 #pragma unroll
     for (int i = 0; i < h; ++i) {
@@ -233,9 +236,9 @@ __device__ __forceinline__ void column_reduce(float (&v)[NR], int lane) {
 
 // Queries of one visit as the B operand of the first product: rows 4 w .. 4 w + 3
 // of the block by one warp, eight lanes a row; row r's parts go to rows r and
-// 16 + r, and its factor (what its scores are multiplied with, but for the keys'
+// NR + r, and its factor (what its scores are multiplied with, but for the keys'
 // scales) to fac[r].  Rows from `rows` on are zero.
-template <int D>
+template <int D, int NR>
 __device__ __forceinline__ void prepare_queries(const C8Params& p, int head, int blk, int rows, unsigned char* dst,
                                                 float* fac, int w, int lane) {
   constexpr int V = D / 64;  // vectors of 8 elements a lane
@@ -256,7 +259,7 @@ __device__ __forceinline__ void prepare_queries(const C8Params& p, int head, int
   const float amax = __uint_as_float(max(top << 16, top & 0xFFFF0000u));
   const int e = cache8_scale_exponent(amax, -100);
   const float mul = copysignf(cache8_two_to(-e), p.g.scale);
-  constexpr int LINE = C8<D>::LINE;
+  constexpr int LINE = C8<D, NR>::LINE, NS = 2 * NR;
 #pragma unroll(V <= 2 ? V : 1)
   for (int i = 0; i < V; ++i) {
     const uint4 u = V <= 2 ? v[i] : load(i);  // (a rolled loop reads them again: the code is run once or twice)
@@ -327,10 +330,11 @@ __device__ __forceinline__ void load_scales(const C8Params& p, const Walk& w, in
 // One visit of a segment: its tiles' weights, then the result or the partial.
 // After a wait that ran out everything here goes on with what is there, to the
 // visit's end: the call's results are then undefined, and its status says so.
-template <int D>
+template <int D, int NR>
 __device__ __forceinline__ void softmax_visit(const C8Params& p, unsigned char* base, const Bars& bar,
                                               volatile int* abort, Walk& w, Soft& c) {
-  using C = C8<D>;
+  using C = C8<D, NR>;
+  constexpr int NH = NR / HR, NP = C::NP;
   const Cache8Geom& g = p.g;
   const int lane = threadIdx.x & 31, q4 = (threadIdx.x >> 5) & 3, t = 32 * q4 + lane;
   unsigned char* small = base + C::OFF_SMALL;
@@ -354,151 +358,158 @@ __device__ __forceinline__ void softmax_visit(const C8Params& p, unsigned char* 
   const int lo_all = g.W > 0 ? max(0, len - g.W) : 0, hi_all = len - g.Lq;
   soft_sync();
 
-  uint64_t l_part[NR / 2];
-  float m_row = kUnset;  // thread t < 16 holds row t's reference
+  uint64_t l_part[NR / 2];  // pairs of rows
+  float m_row = kUnset;     // thread t < NR holds row t's reference
 #pragma unroll
   for (int q = 0; q < NR / 2; ++q) l_part[q] = 0;
 
   bool more = true, fresh = true;
 #pragma unroll 1
   while (more) {
-    const int n = c.n, buf = n & 1, key0 = w.key0();
+    const int n = c.n, buf = C::SBUF == 2 ? n & 1 : 0, key0 = w.key0();
     more = !w.last();
     const float vscale = fmaxf(c.vs, cache8_two_to(kCache8LeastExponent)), lv = __log2f(vscale);
     const uint64_t ks2 = f2_pack(c.ks, c.ks), lv2 = f2_pack(lv, lv), iv2 = f2_pack(__fdividef(1.f, vscale), __fdividef(1.f, vscale));
     w.next();
     if (w.left > 0) load_scales(p, w, t, c);  // the next tile's are under way meanwhile
-    uint32_t sr[NS];
-    wait(bar.s_full(buf), (n >> 1) & 1, abort);
+    const bool edge = !(key0 >= lo_all && key0 + T - 1 <= hi_all);
+    wait(bar.s_full(buf), (C::SBUF == 2 ? n >> 1 : n) & 1, abort);
     __syncwarp();
     tc_fence_after();
-    tmem_ld32(c.at + C::S_COL + NS * buf, sr);
-    tmem_wait_ld();
-    uint64_t y[NR / 2], z[NR / 2];  // pairs of rows
-    const uint64_t small16 = f2_pack(0.0625f, 0.0625f);
 #pragma unroll
-    for (int q = 0; q < NR / 2; q += 2) {
-      const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(fac + 2 * q);
-      const uint64_t ff[2] = {f.x, f.y};
+    for (int hf = 0; hf < NH; ++hf) {  // 16 rows from row HR * hf on
+      uint32_t hi[HR], lo[HR];
+      tmem_ld16(c.at + C::S_COL + C::NS * buf + HR * hf, hi);
+      tmem_ld16(c.at + C::S_COL + C::NS * buf + NR + HR * hf, lo);
+      tmem_wait_ld();
+      uint64_t y[HR / 2], z[HR / 2];
+      const uint64_t small16 = f2_pack(0.0625f, 0.0625f);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = 2 * (q + i);
-        const uint64_t a = f2_pack(__uint_as_float(sr[r]), __uint_as_float(sr[r + 1]));
-        const uint64_t b = f2_pack(__uint_as_float(sr[NR + r]), __uint_as_float(sr[NR + r + 1]));
-        y[q + i] = f2_fma(f2_fma(b, small16, a), f2_mul(ff[i], ks2), lv2);
-      }
-    }
-    if (!(key0 >= lo_all && key0 + T - 1 <= hi_all)) {
-      const int key = key0 + t;
+      for (int q = 0; q < HR / 2; q += 2) {
+        const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(fac + HR * hf + 2 * q);
+        const uint64_t ff[2] = {f.x, f.y};
 #pragma unroll
-      for (int q = 0; q < NR / 2; ++q) {
-        const int4 r = *reinterpret_cast<const int4*>(rng + 2 * q);
-        float2 v = f2_unpack(y[q]);
-        if (key < r.x || key > r.y) v.x = -INFINITY;
-        if (key < r.z || key > r.w) v.y = -INFINITY;
-        y[q] = f2_pack(v.x, v.y);
-      }
-    }
-    auto less_reference = [&]() {  // z = y - reference
-#pragma unroll
-      for (int q = 0; q < NR / 2; q += 2) {
-        const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(nref + 2 * q);
-        z[q] = f2_add(y[q], f.x);
-        z[q + 1] = f2_add(y[q + 1], f.y);
-      }
-    };
-    bool scale = false, grow = true;
-    if (!fresh) {
-      less_reference();
-      float over = -INFINITY;
-#pragma unroll
-      for (int q = 0; q < NR / 2; ++q) {
-        const float2 v = f2_unpack(z[q]);
-        over = fmax3(over, v.x, v.y);
-      }
-      grow = soft_any(over > kTop);
-    }
-    if (grow) {  // some weight passes the top, or the visit begins
-      float mx[NR];
-#pragma unroll
-      for (int q = 0; q < NR / 2; ++q) {
-        const float2 v = f2_unpack(y[q]);
-        mx[2 * q] = v.x;
-        mx[2 * q + 1] = v.y;
-      }
-      column_reduce<true>(mx, lane);
-      if ((lane & 1) == 0) red[q4 * NR + (lane >> 1)] = mx[0];
-      soft_sync();
-      bool moved = false;
-      if (t < NR) {
-        const float tm = fmaxf(fmaxf(red[t], red[NR + t]), fmaxf(red[2 * NR + t], red[3 * NR + t]));
-        float a = 1.f;
-        if (tm - m_row > kTop) {  // (a row without a key yet: its reference is the lowest number)
-          const float to = tm - kBelow;
-          if (m_row != kUnset) {
-            a = fast_exp2(m_row - to);
-            moved = true;
-          }
-          m_row = to;
-          nref[t] = -to;
+        for (int i = 0; i < 2; ++i) {
+          const int r = 2 * (q + i);
+          const uint64_t a = f2_pack(__uint_as_float(hi[r]), __uint_as_float(hi[r + 1]));
+          const uint64_t b = f2_pack(__uint_as_float(lo[r]), __uint_as_float(lo[r + 1]));
+          y[q + i] = f2_fma(f2_fma(b, small16, a), f2_mul(ff[i], ks2), lv2);
         }
-        alp[t] = a;
       }
-      scale = soft_any(moved);
-      if (scale) {
+      if (edge) {
+        const int key = key0 + t;
 #pragma unroll
-        for (int q = 0; q < NR / 2; ++q) l_part[q] = f2_mul(l_part[q], *reinterpret_cast<const uint64_t*>(alp + 2 * q));
+        for (int q = 0; q < HR / 2; ++q) {
+          const int4 r = *reinterpret_cast<const int4*>(rng + HR * hf + 2 * q);
+          float2 v = f2_unpack(y[q]);
+          if (key < r.x || key > r.y) v.x = -INFINITY;
+          if (key < r.z || key > r.w) v.y = -INFINITY;
+          y[q] = f2_pack(v.x, v.y);
+        }
       }
-      less_reference();
+      auto less_reference = [&]() {  // z = y - reference
+#pragma unroll
+        for (int q = 0; q < HR / 2; q += 2) {
+          const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(nref + HR * hf + 2 * q);
+          z[q] = f2_add(y[q], f.x);
+          z[q + 1] = f2_add(y[q + 1], f.y);
+        }
+      };
+      bool grow = true;
+      if (!fresh) {
+        less_reference();
+        float over = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < HR / 2; ++q) {
+          const float2 v = f2_unpack(z[q]);
+          over = fmax3(over, v.x, v.y);
+        }
+        grow = soft_any(over > kTop);
+      }
+      if (grow) {  // some weight passes the top, or the visit begins
+        float mx[HR];
+#pragma unroll
+        for (int q = 0; q < HR / 2; ++q) {
+          const float2 v = f2_unpack(y[q]);
+          mx[2 * q] = v.x;
+          mx[2 * q + 1] = v.y;
+        }
+        column_reduce<true>(mx, lane);
+        if ((lane & 1) == 0) red[q4 * HR + (lane >> 1)] = mx[0];
+        soft_sync();
+        bool moved = false;
+        const int i = t - HR * hf;
+        if (i >= 0 && i < HR) {
+          const float tm = fmaxf(fmaxf(red[i], red[HR + i]), fmaxf(red[2 * HR + i], red[3 * HR + i]));
+          float a = 1.f;
+          if (tm - m_row > kTop) {  // (a row without a key yet: its reference is the lowest number)
+            const float to = tm - kBelow;
+            if (m_row != kUnset) {
+              a = fast_exp2(m_row - to);
+              moved = true;
+            }
+            m_row = to;
+            nref[t] = -to;
+          }
+          alp[t] = a;
+        }
+        if (soft_any(moved)) {  // sums and O^T of these rows move with their references
+#pragma unroll
+          for (int q = 0; q < HR / 2; ++q)
+            l_part[HR / 2 * hf + q] = f2_mul(l_part[HR / 2 * hf + q], *reinterpret_cast<const uint64_t*>(alp + HR * hf + 2 * q));
+          wait(bar.o_done(), (n - 1) & 1, abort);  // (the row has earlier keys: n > 0)
+          __syncwarp();
+          tc_fence_after();
+#pragma unroll 1
+          for (int j = 0; j < 3 * C::NCH; ++j) {
+            const uint32_t at = c.at + C::O_COL + NR * j + HR * hf;
+            uint32_t ov[HR];
+            tmem_ld16(at, ov);
+            tmem_wait_ld();
+#pragma unroll
+            for (int q = 0; q < HR; ++q) ov[q] = __float_as_uint(__uint_as_float(ov[q]) * alp[HR * hf + q]);
+            tmem_st16(at, ov);
+          }
+          tmem_wait_st();
+        }
+        less_reference();
+      }
+      // the weights 2^(y - reference), their row sums, and their three parts: hi is
+      // a weight in fp16 rounded to its top byte, mid the rest so, lo the rest of that
+      uint32_t part[3][HR / 4];
+#pragma unroll
+      for (int q = 0; q < HR / 2; q += 2) {
+        float2 e = f2_unpack(z[q]), f = f2_unpack(z[q + 1]);
+        e.x = fast_exp2(e.x);
+        e.y = fast_exp2(e.y);
+        f.x = fast_exp2(f.x);
+        f.y = fast_exp2(f.y);
+        uint64_t* l = l_part + HR / 2 * hf + q;
+        l[0] = f2_fma(f2_pack(e.x, e.y), iv2, l[0]);
+        l[1] = f2_fma(f2_pack(f.x, f.y), iv2, l[1]);
+        uint32_t a = pack_half2(e.x, e.y), b = pack_half2(f.x, f.y);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          const uint32_t ra = a + 0x00800080u, rb = b + 0x00800080u;
+          part[i][q / 2] = __byte_perm(ra, rb, 0x7531);
+          if (i < 2) {
+            const uint32_t ta = ra & 0xFF00FF00u, tb = rb & 0xFF00FF00u;
+            const __half2 da = __hsub2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<const __half2*>(&ta));
+            const __half2 db = __hsub2(*reinterpret_cast<__half2*>(&b), *reinterpret_cast<const __half2*>(&tb));
+            a = *reinterpret_cast<const uint32_t*>(&da);
+            b = *reinterpret_cast<const uint32_t*>(&db);
+          }
+        }
+      }
+      // the second product of tile n - 1 has finished with the weights' buffer
+      if (hf == 0 && n > 0) wait(bar.o_done(), (n - 1) & 1, abort);
+      // MN-major operand without swizzle: a key's 16 rows of one part are 16 bytes
+      unsigned char* pb = base + C::OFF_P + (hf * T + t) * HR;
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        *reinterpret_cast<uint4*>(pb + i * T * NR) = make_uint4(part[i][0], part[i][1], part[i][2], part[i][3]);
     }
     fresh = false;
-    // the weights 2^(y - reference), their row sums, and their three parts: hi is
-    // a weight in fp16 rounded to its top byte, mid the rest so, lo the rest of that
-    uint32_t part[3][NR / 4];
-#pragma unroll
-    for (int q = 0; q < NR / 2; q += 2) {
-      float2 e = f2_unpack(z[q]), f = f2_unpack(z[q + 1]);
-      e.x = fast_exp2(e.x);
-      e.y = fast_exp2(e.y);
-      f.x = fast_exp2(f.x);
-      f.y = fast_exp2(f.y);
-      l_part[q] = f2_fma(f2_pack(e.x, e.y), iv2, l_part[q]);
-      l_part[q + 1] = f2_fma(f2_pack(f.x, f.y), iv2, l_part[q + 1]);
-      uint32_t a = pack_half2(e.x, e.y), b = pack_half2(f.x, f.y);
-#pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        const uint32_t ra = a + 0x00800080u, rb = b + 0x00800080u;
-        part[i][q / 2] = __byte_perm(ra, rb, 0x7531);
-        if (i < 2) {
-          const uint32_t ta = ra & 0xFF00FF00u, tb = rb & 0xFF00FF00u;
-          const __half2 da = __hsub2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<const __half2*>(&ta));
-          const __half2 db = __hsub2(*reinterpret_cast<__half2*>(&b), *reinterpret_cast<const __half2*>(&tb));
-          a = *reinterpret_cast<const uint32_t*>(&da);
-          b = *reinterpret_cast<const uint32_t*>(&db);
-        }
-      }
-    }
-    // the second product of tile n - 1 has finished with the weights' buffer, and with O^T before it is rescaled
-    if (n > 0) wait(bar.o_done(), (n - 1) & 1, abort);
-    if (scale) {  // uniform over the warps
-      __syncwarp();
-      tc_fence_after();
-#pragma unroll 1
-      for (int i = 0; i < 3 * C::NCH; ++i) {
-        uint32_t ov[NR];
-        tmem_ld16(c.at + C::O_COL + NR * i, ov);
-        tmem_wait_ld();
-#pragma unroll
-        for (int q = 0; q < NR; ++q) ov[q] = __float_as_uint(__uint_as_float(ov[q]) * alp[q]);
-        tmem_st16(c.at + C::O_COL + NR * i, ov);
-      }
-      tmem_wait_st();
-    }
-    // MN-major operand without swizzle: a key's 16 rows of one part are 16 bytes
-    unsigned char* pb = base + C::OFF_P + t * NR;
-#pragma unroll
-    for (int i = 0; i < 3; ++i)
-      *reinterpret_cast<uint4*>(pb + i * T * NR) = make_uint4(part[i][0], part[i][1], part[i][2], part[i][3]);
     fence_proxy_async_smem();  // generic writes -> the tensor core's reads
     tc_fence_before();
     __syncwarp();
@@ -508,16 +519,17 @@ __device__ __forceinline__ void softmax_visit(const C8Params& p, unsigned char* 
   ++c.visit;
 
   // row sums over the 128 threads, then O^T
-  {
-    float l[NR];
 #pragma unroll
-    for (int q = 0; q < NR / 2; ++q) {
-      const float2 v = f2_unpack(l_part[q]);
+  for (int hf = 0; hf < NH; ++hf) {
+    float l[HR];
+#pragma unroll
+    for (int q = 0; q < HR / 2; ++q) {
+      const float2 v = f2_unpack(l_part[HR / 2 * hf + q]);
       l[2 * q] = v.x;
       l[2 * q + 1] = v.y;
     }
     column_reduce<false>(l, lane);
-    if ((lane & 1) == 0) red[q4 * NR + (lane >> 1)] = l[0];
+    if ((lane & 1) == 0) red[q4 * NR + HR * hf + (lane >> 1)] = l[0];
   }
   soft_sync();
   float* mul = alp;  // a whole segment's 1 / sum
@@ -538,22 +550,23 @@ __device__ __forceinline__ void softmax_visit(const C8Params& p, unsigned char* 
   __syncwarp();
   tc_fence_after();
 #pragma unroll 1
-  for (int h = 0; h < C::NCH; ++h) {
-    uint32_t hi[NR], mid[NR], lo[NR];
-    const uint32_t at = c.at + C::O_COL + NP * h;
+  for (int h = 0; h < C::NCH * NH; ++h) {
+    const int ch = NH == 1 ? h : h / NH, r0 = NH == 1 ? 0 : HR * (h % NH);
+    uint32_t hi[HR], mid[HR], lo[HR];
+    const uint32_t at = c.at + C::O_COL + NP * ch + r0;
     tmem_ld16(at, hi);  // warp-collective
     tmem_ld16(at + NR, mid);
     tmem_ld16(at + 2 * NR, lo);
     tmem_wait_ld();
-    const int d = T * h + t;
+    const int d = T * ch + t;
     if (d < D) {
-      uint16_t* o = p.o + ((size_t)head * g.M + blk * NR) * D + d;
-      float* po = p.po + slot * D + d;
+      uint16_t* o = p.o + ((size_t)head * g.M + blk * NR + r0) * D + d;
+      float* po = p.po + (slot + r0) * D + d;
 #pragma unroll
-      for (int q = 0; q < NR; ++q)
-        if (q < rows) {
+      for (int q = 0; q < HR; ++q)
+        if (r0 + q < rows) {
           const float v = __uint_as_float(hi[q]) + (__uint_as_float(mid[q]) + __uint_as_float(lo[q]));
-          if (whole) o[q * D] = __bfloat16_as_ushort(__float2bfloat16_rn(v * mul[q]));
+          if (whole) o[q * D] = __bfloat16_as_ushort(__float2bfloat16_rn(v * mul[r0 + q]));
           else po[q * D] = v;
         }
     }
@@ -561,12 +574,12 @@ __device__ __forceinline__ void softmax_visit(const C8Params& p, unsigned char* 
   tc_fence_before();  // ordered before the next visit's first product by its arrival
 }
 
-template <int D>
+template <int D, int NR>
 __global__ void __launch_bounds__(kThr, 2)
     cache8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const __grid_constant__ C8Params p) {
-  using C = C8<D>;
-  constexpr int NSLOT = C::NSLOT, NCH = C::NCH;
+  using C = C8<D, NR>;
+  constexpr int NSLOT = C::NSLOT, NCH = C::NCH, NS = C::NS, NP = C::NP, AHEAD = C::SBUF;  // tiles whose scores are ahead
   extern __shared__ unsigned char smem_raw[];
   unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const Bars bar{reinterpret_cast<uint64_t*>(base + C::OFF_BAR)};
@@ -652,10 +665,11 @@ __global__ void __launch_bounds__(kThr, 2)
         w.next();
         return true;
       };
-      // slots in MMA order: K(0), K(1), then per tile n: V(n), K(n + 2)
+      // slots in MMA order, with two tiles ahead: K(0), K(1), then per tile n: V(n), K(n + 2)
       bool ok = true;
 #pragma unroll 1
-      for (int n = -2; ok && n < total; ++n) ok = (n < 0 || load_tile(wv, &tmV)) && (n + 2 >= total || load_tile(wk, &tmK));
+      for (int n = -AHEAD; ok && n < total; ++n)
+        ok = (n < 0 || load_tile(wv, &tmV)) && (n + AHEAD >= total || load_tile(wk, &tmK));
       if (*abort_flag) drain_ring(bar.slot_full(0), NSLOT, issued);  // loads in flight land before shared memory is released
     }
   } else if (warp == 1) {
@@ -670,10 +684,10 @@ __global__ void __launch_bounds__(kThr, 2)
       // 8 lines make a swizzled group.  At D = 64 the second product's rows 64-127 repeat 0-63 and are never read.
       const uint64_t kd0 = smem_desc(smem_u32(base), D < 128 ? 0 : 16, 8 * C::LINE, SWZ);
       const uint64_t qd0 = smem_desc(smem_u32(base + C::OFF_Q), 16, 8 * C::LINE, SWZ);
-      const uint64_t pd = smem_desc(smem_u32(base + C::OFF_P), 8 * NR, T * NR, 0);
+      const uint64_t pd = smem_desc(smem_u32(base + C::OFF_P), 8 * HR, T * HR, 0);
       Walk ws = first, wv = first;
       int used = 0, nq = 0;
-      auto issue_s = [&](int n) -> bool {  // S^T(n) into buffer n & 1
+      auto issue_s = [&](int n) -> bool {  // S^T(n)
         const int qs = nq & 1;
         if (ws.first && !wait(bar.q_full(qs), (nq >> 1) & 1, abort_flag)) return false;
 #pragma unroll 1
@@ -681,13 +695,14 @@ __global__ void __launch_bounds__(kThr, 2)
           const int s = used % NSLOT;
           if (!wait(bar.slot_full(s), (used / NSLOT) & 1, abort_flag)) return false;
           tc_fence_after();
+          const uint32_t s_at = tmem + C::S_COL + (AHEAD == 2 ? NS * (n & 1) : 0);
           const uint64_t kd = desc_add(kd0, s * C::SLOT), qd = desc_add(qd0, qs * C::QB + c * NS * C::LINE);
 #pragma unroll
           for (int k = 0; k < C::LINE / 32; ++k)
-            mma_f8(tmem + C::S_COL + NS * (n & 1), desc_add(kd, k * 32), desc_add(qd, k * 32), idS, (c | k) ? 1u : 0u);
+            mma_f8(s_at, desc_add(kd, k * 32), desc_add(qd, k * 32), idS, (c | k) ? 1u : 0u);
           mma_commit(bar.slot_empty(s));
         }
-        mma_commit(bar.s_full(n & 1));
+        mma_commit(bar.s_full(AHEAD == 2 ? n & 1 : 0));
         if (ws.last()) {  // the visit's queries are read
           mma_commit(bar.q_empty(qs));
           ++nq;
@@ -697,7 +712,7 @@ __global__ void __launch_bounds__(kThr, 2)
       };
       bool ok = true;
 #pragma unroll 1
-      for (int n = -2; ok && n < total; ++n) {
+      for (int n = -AHEAD; ok && n < total; ++n) {
         if (n >= 0) {
           if (!wait(bar.p_full(), n & 1, abort_flag)) break;
           tc_fence_after();
@@ -710,7 +725,7 @@ __global__ void __launch_bounds__(kThr, 2)
             const uint64_t vd = desc_add(kd0, s * C::SLOT);
 #pragma unroll
             for (int k = 0; k < T / 32; ++k)
-              mma_f8(tmem + C::O_COL + NP * c, desc_add(vd, k * 32 * C::LINE), desc_add(pd, k * 32 * NR), idO,
+              mma_f8(tmem + C::O_COL + NP * c, desc_add(vd, k * 32 * C::LINE), desc_add(pd, k * 32 * HR), idO,
                      (acc || k > 0) ? 1u : 0u);
             mma_commit(bar.slot_empty(s));
           }
@@ -718,7 +733,7 @@ __global__ void __launch_bounds__(kThr, 2)
           mma_commit(bar.o_done());
           wv.next();
         }
-        if (n + 2 < total) ok = issue_s(n + 2);  // after the second product of tile n: S buffer n & 1 is free
+        if (n + AHEAD < total) ok = issue_s(n + AHEAD);  // the weights of tile n have been written: its scores' buffer is free
       }
       mma_commit(bar.drain());
       mbar_wait_drain(bar.drain(), 0);
@@ -730,7 +745,9 @@ __global__ void __launch_bounds__(kThr, 2)
     c.n = c.visit = 0;
     if (total > 0) {
       load_scales(p, w, 32 * (warp & 3) + lane, c);
-      prepare_queries<D>(p, w.head(), w.blk, min(NR, g.M - w.blk * NR), base + C::OFF_Q, qfac, warp - 2, lane);
+#pragma unroll 1
+      for (int i = warp - 2; i < NR / 4; i += 4)
+        prepare_queries<D, NR>(p, w.head(), w.blk, min(NR, g.M - w.blk * NR), base + C::OFF_Q, qfac, i, lane);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar.q_full(0));
     }
@@ -738,7 +755,7 @@ __global__ void __launch_bounds__(kThr, 2)
     tc_fence_after();
     c.at = *tmem_slot + ((uint32_t)(32 * (warp & 3)) << 16);
 #pragma unroll 1
-    while (w.left > 0) softmax_visit<D>(p, base, bar, abort_flag, w, c);
+    while (w.left > 0) softmax_visit<D, NR>(p, base, bar, abort_flag, w, c);
   } else {
     // ------------------------------------------------------------ the later visits' queries
     if (lane == 0) {  // for the merge
@@ -753,7 +770,7 @@ __global__ void __launch_bounds__(kThr, 2)
     }
     Walk w = first;
     if (total > 0) w.skip();
-    int filled = 0x44;  // groups of rows of either buffer that may not be zero
+    int filled = NR / 4 * 0x11;  // groups of rows of either buffer that may not be zero
 #pragma unroll 1
     for (int v = 1; w.left > 0; ++v) {
       const int s = v & 1;
@@ -768,7 +785,7 @@ __global__ void __launch_bounds__(kThr, 2)
       const int groups = (rows + 3) / 4, old = filled >> (4 * s) & 15;  // of four rows
 #pragma unroll 1
       for (int i = 0; i < max(groups, old); ++i)
-        prepare_queries<D>(p, w.head(), w.blk, rows, base + C::OFF_Q + s * C::QB, qfac + (v & 3) * NR, i, lane);
+        prepare_queries<D, NR>(p, w.head(), w.blk, rows, base + C::OFF_Q + s * C::QB, qfac + (v & 3) * NR, i, lane);
       filled = (filled & ~(15 << (4 * s))) | groups << (4 * s);
       __syncwarp();
       if (lane < 4) mbar_arrive(bar.q_full(s));
@@ -887,7 +904,7 @@ __device__ __forceinline__ void merge_pieces(const C8Params& p, const int4& cut,
       __syncthreads();
     }
     if (!on || k > 0 || lane >= LANES || n == 0) continue;
-    const int r = blk * NR + row;
+    const int r = blk * g.nr + row;
     float lse;
     const float inv = finish_row(p.sinks ? p.sinks + (head % g.Hkv) * g.G + r / g.Lq : nullptr, m, l, &lse);
     const size_t at = (size_t)head * g.M + r;
@@ -907,8 +924,9 @@ __device__ __forceinline__ void merge_pieces(const C8Params& p, const int4& cut,
 // is time while the last runs end.
 template <int D>
 __global__ void __launch_bounds__(32 * kMergeWarps, 6) cache8_merge_kernel(const __grid_constant__ C8Params p) {
+  constexpr int W = D < 256 ? D : 256;  // columns of a piece where there are few cuts
   __shared__ union {
-    float whole[kMergeWarps][D], piece[kMergeWarps][64];
+    float whole[kMergeWarps][W], piece[kMergeWarps][64];
   } part;
   __shared__ float2 stat[kMergeWarps];
   grid_launch_dependents();
@@ -920,17 +938,22 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 6) cache8_merge_kernel(const
       cut = p.cuts[blockIdx.x];
       if (cut.x < 0) return;
     }
-    const int blk = p.g.nmb == 1 ? 0 : cut.x % p.g.nmb, rows = min(NR, p.g.M - blk * NR);
+    const int blk = p.g.nmb == 1 ? 0 : cut.x % p.g.nmb, rows = min(p.g.nr, p.g.M - blk * p.g.nr);
     const bool pieces = D == 64 || cut.y > rows * (D / 64);
     if (pieces || !pass) merge_pieces<D, 64>(p, cut, rows, part.piece, stat);
-    if (D > 64 && !pieces) merge_pieces<D, D>(p, cut, rows, part.whole, stat);
+    if (D > 64 && !pieces) merge_pieces<D, W>(p, cut, rows, part.whole, stat);
   }
 }
 
 struct C8Ws {
   size_t cuts, ml, po, total;
 };
-int slot_rows(const Cache8Geom& g) { return g.M < NR ? g.M : NR; }
+int slot_rows(const Cache8Geom& g) { return g.M < g.nr ? g.M : g.nr; }
+// Key tiles of a request, at most.
+long long tiles_most(const Cache8Geom& g) {
+  const long long keys = g.W > 0 && (long long)g.W + g.Lq - 1 < g.rows ? (long long)g.W + g.Lq - 1 : g.rows;
+  return (keys + T - 1) / T;
+}
 C8Ws c8_ws(const Cache8Geom& g) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   const size_t rows = (size_t)2 * kCtas * slot_rows(g);
@@ -951,9 +974,9 @@ cudaError_t make_tmap_codes(CUtensorMap* m, const void* ptr, int D, int rows, in
   return make_tmap_u8_4d(m, ptr, dims, strides, box, D < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int D>
+template <int D, int NR>
 cudaError_t cache8_d(const Cache8Geom& g, const Cache8Args& a, void* ws, int* status, cudaStream_t st) {
-  using C = C8<D>;
+  using C = C8<D, NR>;
   CUtensorMap tk, tv;
   cudaError_t e;
   if ((e = make_tmap_codes(&tk, a.k, D, g.rows, g.B * g.Hkv)) != cudaSuccess) return e;
@@ -974,7 +997,7 @@ cudaError_t cache8_d(const Cache8Geom& g, const Cache8Args& a, void* ws, int* st
   p.po = reinterpret_cast<float*>(wb + w.po);
   p.orow = slot_rows(g);
   p.status = status;
-  auto kern = cache8_kernel<D>;
+  auto kern = cache8_kernel<D, NR>;
   static std::atomic<unsigned long long> done{0};
   if ((e = allow_smem(kern, (int)C::SMEM, done)) != cudaSuccess) return e;
   // both are programmatic dependents of what runs before them: the main grid's
@@ -990,15 +1013,26 @@ bool cache8_fits(const Cache8Geom& g) {
   const double units = (double)g.B * g.Hkv * g.nmb * ((g.rows + T - 1) / T);
   return units * kCtas < 4.0e9 && (double)g.B * g.Hkv * g.M < 1.0e9;
 }
-int cache8_row_blocks(int M) { return (M + NR - 1) / NR; }
+// Query rows of a block.  Blocks of 32 cost a tile nearly twice the softmax of 16, but
+// the cache is read once for them: 32 requests of 32 rows over 8,192 keys, D = 128,
+// 50.6 us against 75.6.  With few tiles a CTA the shorter ones spread better (16
+// requests, D = 256: 20.2 and 16.7 us over 1,024 keys, 26.3 and 28.3 over 2,560,
+// which are 4.2 tiles a CTA; D = 64: 14.6 and 13.5 at 2.1, both 17.1 at 4.2, and
+// 17.2 and 15.9 where the lengths fill half of such a cache, whose rows are what
+// the host knows).
+int cache8_block_rows(const Cache8Geom& g) {
+  const long long units = (long long)g.B * g.Hkv * ((g.M + 31) / 32) * tiles_most(g);
+  return g.M <= 16 || g.D == 512 || units < 6 * kCtas ? 16 : 32;
+}
 size_t cache8_workspace_bytes(const Cache8Geom& g) { return c8_ws(g).total; }
 
 cudaError_t launch_fwd_cache8(const Cache8Geom& g, const Cache8Args& a, void* ws, int* status, cudaStream_t st) {
+  const bool few = g.nr == 16;
   switch (g.D) {
-    case 64: return cache8_d<64>(g, a, ws, status, st);
-    case 128: return cache8_d<128>(g, a, ws, status, st);
-    case 256: return cache8_d<256>(g, a, ws, status, st);
-    case 512: return cache8_d<512>(g, a, ws, status, st);
+    case 64: return few ? cache8_d<64, 16>(g, a, ws, status, st) : cache8_d<64, 32>(g, a, ws, status, st);
+    case 128: return few ? cache8_d<128, 16>(g, a, ws, status, st) : cache8_d<128, 32>(g, a, ws, status, st);
+    case 256: return few ? cache8_d<256, 16>(g, a, ws, status, st) : cache8_d<256, 32>(g, a, ws, status, st);
+    case 512: return cache8_d<512, 16>(g, a, ws, status, st);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -825,13 +825,14 @@ static int cache8_geom(swa::Cache8Geom& g, int B, int Hq, int Hkv, int Lq, int k
   g.G = Hq / Hkv;
   g.Lq = Lq;
   g.M = g.G * Lq;
-  g.nmb = swa::cache8_row_blocks(g.M);
   g.rows = kv_rows;
   g.lb = block == 16 ? 4 : (block == 32 ? 5 : (block == 64 ? 6 : 7));
   g.nblk = (kv_rows + block - 1) / block;
   g.D = D;
   g.W = window >= kv_rows ? 0 : window;  // no two positions are further apart
   g.scale = scale;
+  g.nr = swa::cache8_block_rows(g);
+  g.nmb = (g.M + g.nr - 1) / g.nr;
   return swa::cache8_fits(g) ? SWA_OK : SWA_ERR_TOO_LARGE;
 }
 

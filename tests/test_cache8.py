@@ -299,6 +299,9 @@ def test_attention(D, B, Hq, Hkv, Lq, rows, window, sinks, block, lens):
     (40, 8, 4, 1, 128, 5000, 0, 128, 0),    # ragged ones
     (3, 16, 8, 3, 256, 20000, 0, 16, 0),    # long segments, cut by many runs
     (33, 12, 4, 4, 512, 4000, 2500, 32, 0),  # 12 rows, a window
+    (9, 16, 2, 4, 64, 9000, 0, 16, 0),      # 32 rows
+    (6, 16, 2, 3, 128, 12000, 3000, 64, 0),  # 24 rows, a window
+    (5, 20, 2, 5, 256, 7000, 0, 128, 0),    # 50 rows: a block of 32 and one of 18
 ])
 def test_attention_of_many_tiles(B, Hq, Hkv, Lq, D, rows, window, block, spread):
     """More tiles than five a CTA: runs that CTAs take over, and their merge."""
