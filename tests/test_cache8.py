@@ -319,3 +319,390 @@ def test_attention_of_many_tiles(B, Hq, Hkv, Lq, D, rows, window, block, spread)
     assert bool(((got_o[some] - o).abs() <= tol).all()) and bool(((got_lse[some] - lse).abs() <= ltol).all())
     again = attend(q, (kc, s[0]), (vc, s[1]), None, lens, window, 0.25 / math.sqrt(D), block)
     assert torch.equal(again[0], got_o) and torch.equal(again[1], got_lse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,Hq,rising", [(64, 2, True), (128, 8, True), (256, 20, True), (512, 3, False)])
+def test_references_that_move(D, Hq, rising):
+    """Scores that rise (or fall) by some 200 along the cache: references move often, sums and outputs with them."""
+    g = torch.Generator().manual_seed(D)
+    rows, block = 1500, 16
+    q = torch.randn(2, Hq, 1, D, generator=g).to(BF)
+    q[..., 0] = 4.0
+    k = 0.2 * torch.randn(2, 1, rows, D, generator=g)
+    ramp = torch.linspace(-25, 25, rows)
+    k[..., 0] = ramp if rising else -ramp
+    codes = torch.zeros(2, 1, rows, D, dtype=torch.float64)
+    scales = torch.zeros(2, 1, -(-rows // block), dtype=torch.float64)
+    ref_append(k.to(BF), codes, scales, None, block)
+    vc = filled(2, 1, rows, D, block, 41)
+    check_attention(q, (codes.float().to(F8), scales.float()), vc, None, [rows, 1111], 0, 1.0, block)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 512])
+def test_scales_far_apart(D):
+    """Blocks of values and keys whose scales lie 2^60 apart, zeros among them, and the least scale."""
+    g = torch.Generator().manual_seed(D + 1)
+    B, Hkv, rows, block = 2, 2, 400, 32
+    nb = -(-rows // block)
+    q = torch.randn(B, 4, 2, D, generator=g).to(BF)
+    kc, vc = filled(B, Hkv, rows, D, block, 42, 0.2), filled(B, Hkv, rows, D, block, 43, 0.2)
+    vs = vc[1] * torch.exp2(torch.randint(-30, 31, (B, Hkv, nb), generator=g).float())
+    vs[0, 0, :] = 2.0 ** -64
+    ks = kc[1] * torch.exp2(torch.randint(-8, 1, (B, Hkv, nb), generator=g).float())
+    codes = vc[0].float()
+    codes[1, 1, 64:128] = 0
+    check_attention(q, (kc[0], ks), (codes.to(F8), vs), None, [rows, 333], 0, 1.0 / math.sqrt(D), block)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale", [0.0, -0.125, 3.0])
+def test_scales_of_the_softmax(scale):
+    g = torch.Generator().manual_seed(7)
+    q = torch.randn(2, 4, 1, 64, generator=g).to(BF)
+    q[0, 0] = 0
+    q[1, 1] *= 2.0 ** 40  # a row far larger than the others
+    q[1, 2] *= 2.0 ** -40
+    kc, vc = filled(2, 2, 200, 64, 64, 44, 0.2), filled(2, 2, 200, 64, 64, 45, 0.2)
+    check_attention(q, kc, vc, None, [200, 77], 0, scale, 64)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,Lq,window", [(64, 4, 0), (128, 1, 100), (256, 5, 0), (512, 1, 0)])
+def test_what_stands_behind_the_lengths(D, Lq, window):
+    """NaN codes and scales behind the lengths, and in empty places, change nothing; rows of empty places stay."""
+    import sliding_window_attention_gb300 as swa
+
+    g = torch.Generator().manual_seed(D)
+    B, Hq, Hkv, rows, block = 5, 8, 2, 333, 32
+    lens = [0, 1, -7, 200, 1000]
+    q = torch.randn(B, Hq, Lq, D, generator=g).to(BF).cuda()
+    kc, vc = filled(B, Hkv, rows, D, block, 51), filled(B, Hkv, rows, D, block, 52)
+    clean = [kc[0].cuda(), vc[0].cuda(), kc[1].cuda(), vc[1].cuda()]
+    dirty = [t.clone() for t in clean]
+    for b, n in enumerate(lens):
+        n = max(n, 0)
+        for c, s in ((dirty[0], dirty[2]), (dirty[1], dirty[3])):
+            c.view(torch.uint8)[b, :, n:] = 0x7F
+            s[b, :, -(-n // block):] = math.nan
+    n = torch.tensor(lens, dtype=torch.int32).cuda()
+    got = []
+    for cache in (clean, dirty):
+        o = torch.full((B, Hq, Lq, D), 7.0, dtype=BF, device="cuda")
+        lse = torch.full((B, Hq, Lq), 7.0, device="cuda")
+        ws = torch.full((swa.fwd_workspace_bytes_cache8(B, Hq, Hkv, Lq, rows, D, block, window),), 0xFF,
+                        dtype=torch.uint8, device="cuda")
+        swa.swa_attn_fwd_cache8(q, *cache, n, None, o, lse, block, window, 0.1, ws)
+        status_ok()
+        got.append((o, lse))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    assert bool((got[0][0][2] == 7).all()) and bool((got[0][1][2] == 7).all())
+    assert bool((got[0][0][0] == 0).all()) and bool((got[0][1][0] == -math.inf).all())
+    assert bool(got[0][0][[1, 3, 4]].isfinite().all())
+    read = swa.cache8_read(*dirty, n, block)
+    assert bool(read[0].isfinite().all()) and bool(read[1].isfinite().all())
+
+
+@pytest.mark.gpu
+def test_a_step_with_the_calls_around_it():
+    """Rotation, append and attention, step after step, a request ending and a place reused: like
+    forward_shared over bf16 caches that hold what the 8-bit cache's reads give."""
+    import sliding_window_attention_gb300 as swa
+
+    torch.manual_seed(3)
+    B, Hq, Hkv, D, rows, block = 3, 8, 2, 128, 160, 16
+    inv = 10000.0 ** (-torch.arange(D // 2, dtype=torch.float64, device="cuda") / (D // 2))
+    w = torch.ones(D, device="cuda")
+    cache = swa.make_cache8(B, Hkv, rows, D, block)
+    lens = torch.tensor([100, 0, -1], dtype=torch.int32, device="cuda")
+    for step, L in enumerate((1, 3, 1, 2, 1)):
+        if step == 3:
+            lens[1], lens[2] = -1, 0  # the second request ends, a third begins
+        n = torch.where(lens >= 0, lens + L, lens).to(torch.int32)
+        x = torch.randn(B, L, Hq + 2 * Hkv, D, device="cuda").to(BF)
+        xq, xk, xv = x.split((Hq, Hkv, Hkv), 2)
+        pos = ((n - L).clamp(min=0)[:, None] + torch.arange(L, device="cuda")).to(torch.int32).contiguous()
+        q, k, _ = swa.qk_rope(xq, xk, None, w, w, inv, 1e-6, positions=pos)
+        swa.cache8_append(k, xv.transpose(1, 2), *cache, n, block)
+        o, lse = swa.forward_cache8(q, *cache, n, block, 64, 0.09)
+        kb, vb = swa.cache8_read(*cache, n, block)
+        live = n >= 0
+        o2, lse2 = swa.forward_shared(q, None, None, kb, vb, n, 64, 0.09)
+        # both round o (2^-8), one its weights to 2^-8, the other to 2^-11: of sum p |v| at most; scores to 2^-16 of 12
+        assert float((o.float() - o2.float())[live].abs().max()) <= 3.25 * 2.0 ** -8 * float(vb.float().abs().max())
+        assert float((lse - lse2)[live].abs().max()) <= 2.0 ** -9
+        # what was appended reads back within half a step of e4m3, of the block's scale below
+        for got, want, s in ((kb, k, cache[2]), (vb, xv.transpose(1, 2), cache[3])):
+            for b in range(B):
+                if live[b]:
+                    m = int(n[b])
+                    y, z = got[b, :, m - L:m].float(), want[b].float()
+                    step_ = s[b, :, torch.arange(m - L, m, device="cuda") // block][..., None]
+                    assert bool(((y - z).abs() <= torch.maximum(z.abs() * 2.0 ** -4, step_ * 2.0 ** -10)).all())
+        lens = n
+    status_ok()
+
+
+@pytest.mark.gpu
+def test_a_prompt_in_chunks():
+    """A prompt's chunks appended, read back and attended by the training forward: the same as one append of all."""
+    import sliding_window_attention_gb300 as swa
+
+    torch.manual_seed(4)
+    B, Hkv, D, L, block = 1, 2, 64, 300, 64
+    k, v = (torch.randn(B, Hkv, L, D, device="cuda").to(BF) for _ in range(2))
+    one, parts = swa.make_cache8(B, Hkv, L, D, block), swa.make_cache8(B, Hkv, L, D, block)
+    swa.cache8_append(k, v, *one, None, block)
+    for a, b in ((0, 128), (128, 192), (192, 300)):  # at the blocks' borders: no scale has to grow
+        swa.cache8_append(k[:, :, a:b], v[:, :, a:b], *parts, torch.tensor([b], dtype=torch.int32, device="cuda"), block)
+    for x, y in zip(one, parts):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    kb, vb = swa.cache8_read(*parts, None, block)
+    q = torch.randn(B, 4, 108, D, device="cuda").to(BF)
+    o, lse = swa.forward(q, kb, vb, 0, 0.125)  # 108 rows behind 192 keys
+    n = torch.tensor([L], dtype=torch.int32, device="cuda")
+    o8, lse8 = swa.forward_cache8(q, *parts, n, block, 0, 0.125)
+    status_ok()
+    # o is rounded once (2^-8), weights to 2^-11 on either side, scores to 2^-14 with the sums
+    assert float((o - o8.float()).abs().max()) <= (2.0 ** -8 + 2 * 2.0 ** -11 + 2.0 ** -12) * float(vb.float().abs().max())
+    assert float((lse - lse8).abs().max()) <= 2.0 ** -10
+
+
+@pytest.mark.gpu
+def test_captured_and_replayed():
+    """A captured step replays with the lengths and tokens of then; two graphs share a workspace one after the other."""
+    import sliding_window_attention_gb300 as swa
+
+    torch.manual_seed(5)
+    B, Hq, Hkv, D, rows, block = 4, 8, 4, 128, 700, 64
+    cache = swa.make_cache8(B, Hkv, rows, D, block)
+    k, v = (torch.randn(B, Hkv, 1, D, device="cuda").to(BF) for _ in range(2))
+    q = torch.randn(B, Hq, 1, D, device="cuda").to(BF)
+    big = torch.randn(2, B, Hkv, rows, D, device="cuda").to(BF)
+    swa.cache8_append(big[0], big[1], *cache, None, block)
+    n = torch.tensor([5, 700, -1, 300], dtype=torch.int32, device="cuda")
+    o, lse = torch.zeros_like(q), torch.zeros(B, Hq, 1, device="cuda")
+    ws = torch.empty(swa.fwd_workspace_bytes_cache8(B, Hq, Hkv, 1, rows, D, block, 0), dtype=torch.uint8, device="cuda")
+
+    def step(out, l):
+        swa.cache8_append(k, v, *cache, n, block)
+        swa.swa_attn_fwd_cache8(q, *cache, n, None, out, l, block, 0, 0.1, ws)
+
+    step(o, lse)
+    o2, lse2 = torch.zeros_like(q), torch.zeros_like(lse)
+    graphs = []
+    for out, l in ((o, lse), (o2, lse2)):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step(out, l)
+        graphs.append(g)
+    for lens in ([6, 700, 1, 299], [640, -1, 2, 1]):
+        n.copy_(torch.tensor(lens, dtype=torch.int32))
+        for t in (k, v, q):
+            t.copy_(torch.randn_like(t))
+        o.fill_(3)
+        o2.fill_(3)
+        for g in graphs:
+            g.replay()
+        want = swa.forward_cache8(q, *cache, n, block, 0, 0.1)  # (the append again changes nothing)
+        torch.cuda.synchronize()
+        live = n >= 0
+        assert torch.equal(o[live], want[0][live]) and torch.equal(o2[live], want[0][live])
+        assert torch.equal(lse[live], want[1][live]) and bool((o[~live] == 3).all())
+    status_ok()
+
+
+@pytest.mark.gpu
+def test_two_streams_at_once():
+    """Calls of different shapes on two streams, like their results one after the other."""
+    import sliding_window_attention_gb300 as swa
+
+    torch.manual_seed(6)
+    jobs = []
+    for B, Hq, Hkv, Lq, D, rows, block in ((8, 8, 4, 1, 128, 4000, 64), (3, 32, 4, 4, 256, 3000, 32)):
+        cache = swa.make_cache8(B, Hkv, rows, D, block)
+        x = torch.randn(2, B, Hkv, rows, D, device="cuda").to(BF)
+        n = torch.randint(1, rows, (B,), device="cuda", dtype=torch.int32)
+        q = torch.randn(B, Hq, Lq, D, device="cuda").to(BF)
+        swa.cache8_append(x[0], x[1], *cache, None, block)
+        jobs.append((q, cache, n, block, swa.forward_cache8(q, *cache, n, block, 0, 0.1)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    out = [[], []]
+    for _ in range(20):
+        for i, (q, cache, n, block, _w) in enumerate(jobs):
+            out[i].append(swa.forward_cache8(q, *cache, n, block, 0, 0.1, stream=streams[i]))
+    torch.cuda.synchronize()
+    for i, job in enumerate(jobs):
+        for got in out[i]:
+            assert torch.equal(got[0], job[4][0]) and torch.equal(got[1], job[4][1])
+    status_ok()
+
+
+@pytest.mark.gpu
+def test_beyond_four_gigabytes():
+    """Codes behind 2^32 bytes: an append at the end, the read of it, and the attention's window there."""
+    import sliding_window_attention_gb300 as swa
+
+    B, Hkv, D, rows, block, L = 1, 2, 512, 4_400_000, 128, 200
+    assert Hkv * rows * D > 2 ** 32
+    codes = [torch.zeros((B, Hkv, rows, D), dtype=torch.uint8, device="cuda").view(F8) for _ in range(2)]
+    scales = [torch.ones((B, Hkv, -(-rows // block)), device="cuda") for _ in range(2)]
+    torch.manual_seed(8)
+    k, v = (torch.randn(B, Hkv, L, D, device="cuda").to(BF) for _ in range(2))
+    q = torch.randn(B, 4, 1, D, device="cuda").to(BF)
+    end = rows - 3
+    n = torch.tensor([end], dtype=torch.int32, device="cuda")
+    swa.cache8_append(k, v, *codes, *scales, n, block)
+    kb, vb = swa.cache8_read(*codes, *scales, n, block, end - L, L)
+    o, lse = swa.forward_cache8(q, *codes, *scales, n, block, 150, 0.05)
+    # the same tokens at the same places of their blocks in a small cache
+    first = (end - L) % block
+    small = swa.make_cache8(B, Hkv, first + L, D, block)
+    m = torch.tensor([first + L], dtype=torch.int32, device="cuda")
+    swa.cache8_append(k, v, *small, m, block)
+    nb, j0 = small[2].shape[2], (end - L) // block
+    assert torch.equal(scales[0][:, :, j0:j0 + nb], small[2]) and torch.equal(scales[1][:, :, j0:j0 + nb], small[3])
+    k2, v2 = swa.cache8_read(*small, m, block, first, L)
+    o2, lse2 = swa.forward_cache8(q, *small, m, block, 150, 0.05)
+    status_ok()
+    assert torch.equal(kb, k2) and torch.equal(vb, v2) and torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+# ---------------------------------------------------------------- refusals
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from sliding_window_attention_gb300 import build as b
+    from sliding_window_attention_gb300 import _native
+
+    b.build()
+    return _native.load()
+
+
+def codes_of(lib):
+    import os
+    import re
+
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "swa_attn.h")).read()
+    return {m.group(1): int(m.group(2)) for m in re.finditer(r"#define (SWA_\w+) (-?\d+)", text)}
+
+
+def test_append_refuses_before_any_cuda_call(lib):
+    c = codes_of(lib)
+
+    def call(k=0x1000, v=0x2000, sb=4096, sh=1024, st=64, n=0x3000, kc=0x4000, vc=0x5000, ks=0x6000, vs=0x7000, B=2,
+             Hkv=2, L=3, D=64, rows=32, block=16):
+        return lib.swa_attn_cache8_append(k, v, sb, sh, st, sb, sh, st, n, kc, vc, ks, vs, B, Hkv, L, D, rows, block, None)
+
+    assert call(k=0, v=0) == c["SWA_ERR_NULL_POINTER"]
+    assert call(kc=0) == c["SWA_ERR_NULL_POINTER"] and call(vs=0) == c["SWA_ERR_NULL_POINTER"]
+    assert call(B=0) == c["SWA_ERR_BAD_SHAPE"] and call(L=0) == c["SWA_ERR_BAD_SHAPE"]
+    assert call(D=96) == c["SWA_ERR_BAD_HEAD_DIM"]
+    assert call(rows=0) == c["SWA_ERR_BAD_CACHE"] and call(block=48) == c["SWA_ERR_BAD_CACHE"]
+    assert call(n=0, L=33) == c["SWA_ERR_BAD_CACHE"]
+    assert call(st=65) == c["SWA_ERR_BAD_STRIDE"] and call(st=0) == c["SWA_ERR_BAD_STRIDE"]
+    assert call(sh=-64) == c["SWA_ERR_BAD_STRIDE"]
+    for name in ("k", "v", "kc", "vc"):
+        assert call(**{name: 0x8008}) == c["SWA_ERR_MISALIGNED"], name
+    assert call(n=0x3002) == c["SWA_ERR_MISALIGNED"] and call(ks=0x6001) == c["SWA_ERR_MISALIGNED"]
+    assert call(B=60000, Hkv=60000) == c["SWA_ERR_TOO_LARGE"]
+
+
+def test_read_refuses_before_any_cuda_call(lib):
+    c = codes_of(lib)
+
+    def call(kc=0x1000, vc=0x2000, ks=0x3000, vs=0x4000, n=0x5000, ko=0x6000, vo=0x7000, B=2, Hkv=2, D=64, rows=32,
+             block=16, row0=0, count=32):
+        return lib.swa_attn_cache8_read(kc, vc, ks, vs, n, ko, vo, B, Hkv, D, rows, block, row0, count, None)
+
+    assert call(ko=0, vo=0) == c["SWA_ERR_NULL_POINTER"] and call(kc=0) == c["SWA_ERR_NULL_POINTER"]
+    assert call(Hkv=0) == c["SWA_ERR_BAD_SHAPE"] and call(D=1024) == c["SWA_ERR_BAD_HEAD_DIM"]
+    assert call(row0=-1) == c["SWA_ERR_BAD_CACHE"] and call(row0=1) == c["SWA_ERR_BAD_CACHE"]
+    assert call(count=0) == c["SWA_ERR_BAD_CACHE"] and call(block=0) == c["SWA_ERR_BAD_CACHE"]
+    assert call(row0=2 ** 31 - 1, count=2 ** 31 - 1) == c["SWA_ERR_BAD_CACHE"]
+    assert call(vo=0x7008) == c["SWA_ERR_MISALIGNED"]
+
+
+def test_attention_refuses_before_any_cuda_call(lib):
+    import ctypes
+
+    c = codes_of(lib)
+
+    def call(q=0x1000, kc=0x2000, vc=0x3000, ks=0x4000, vs=0x5000, n=0x6000, sinks=0, o=0x7000, lse=0x8000, B=2, Hq=4,
+             Hkv=2, Lq=1, rows=64, D=64, block=16, window=0, scale=0.1, ws=0x100000, nbytes=None):
+        if nbytes is None:
+            nbytes = lib.swa_attn_fwd_workspace_bytes_cache8(B, Hq, Hkv, Lq, rows, D, block, window)
+        return lib.swa_attn_fwd_cache8(q, kc, vc, ks, vs, n, sinks, o, lse, B, Hq, Hkv, Lq, rows, D, block, window,
+                                       ctypes.c_float(scale), ws, nbytes, None)
+
+    for name in ("q", "kc", "vc", "ks", "vs", "n", "o", "lse"):
+        assert call(**{name: 0}) == c["SWA_ERR_NULL_POINTER"], name
+    assert call(Hq=3) == c["SWA_ERR_BAD_GROUPS"] and call(Lq=0) == c["SWA_ERR_BAD_SHAPE"]
+    assert call(D=32) == c["SWA_ERR_BAD_HEAD_DIM"] and call(window=-1) == c["SWA_ERR_BAD_WINDOW"]
+    assert call(scale=math.inf) == c["SWA_ERR_BAD_SCALE"] and call(scale=math.nan) == c["SWA_ERR_BAD_SCALE"]
+    assert call(rows=0) == c["SWA_ERR_BAD_CACHE"] and call(block=24) == c["SWA_ERR_BAD_CACHE"]
+    assert call(ws=0) == c["SWA_ERR_WORKSPACE"] and call(nbytes=1000) == c["SWA_ERR_WORKSPACE"]
+    assert call(ws=0x100010) == c["SWA_ERR_MISALIGNED"] and call(sinks=0x9002) == c["SWA_ERR_MISALIGNED"]
+    assert call(kc=0x2004) == c["SWA_ERR_MISALIGNED"] and call(lse=0x8002) == c["SWA_ERR_MISALIGNED"]
+    assert call(B=60000, rows=10 ** 6) == c["SWA_ERR_TOO_LARGE"]
+    assert lib.swa_attn_fwd_workspace_bytes_cache8(2, 3, 2, 1, 64, 64, 16, 0) == 0
+    assert lib.swa_attn_fwd_workspace_bytes_cache8(2, 4, 2, 1, 64, 64, 16, 0) % 256 == 0
+
+
+def test_binding_refuses_host_tensors(lib):
+    import sliding_window_attention_gb300 as swa
+
+    cache = swa.make_cache8(1, 2, 32, 64, 16, device="cpu")
+    k = torch.zeros(1, 2, 1, 64, dtype=BF)
+    n = torch.ones(1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA device"):
+        swa.cache8_append(k, k, *cache, n, 16)
+    with pytest.raises(ValueError, match="CUDA device"):
+        swa.cache8_read(*cache, n, 16)
+    with pytest.raises(ValueError, match="CUDA device"):
+        swa.forward_cache8(torch.zeros(1, 4, 1, 64, dtype=BF), *cache, n, 16, 0, 0.1)
+
+
+@pytest.mark.gpu
+def test_binding_refuses_wrong_tensors():
+    import sliding_window_attention_gb300 as swa
+
+    k8, v8, ks, vs = swa.make_cache8(2, 2, 48, 64, 16)
+    n = torch.ones(2, dtype=torch.int32, device="cuda")
+    k = torch.zeros(2, 2, 1, 64, dtype=BF, device="cuda")
+    q = torch.zeros(2, 4, 1, 64, dtype=BF, device="cuda")
+    bad = [lambda: swa.cache8_append(k.float(), k, k8, v8, ks, vs, n, 16),
+           lambda: swa.cache8_append(k[:, :1], k, k8, v8, ks, vs, n, 16),
+           lambda: swa.cache8_append(k, k, k8.view(torch.uint8), v8, ks, vs, n, 16),
+           lambda: swa.cache8_append(k, k, k8, v8, ks[..., :2], vs, n, 16),
+           lambda: swa.cache8_append(k, k, k8, v8, ks, vs, n.long(), 16),
+           lambda: swa.cache8_append(k, k, k8, v8, ks, vs, n, 32),
+           lambda: swa.cache8_append(torch.zeros(2, 2, 1, 128, dtype=BF, device="cuda")[..., ::2], k, k8, v8, ks, vs, n,
+                                     16),
+           lambda: swa.cache8_append(None, None, k8, v8, ks, vs, n, 16),
+           lambda: swa.cache8_append(k, k, None, v8, ks, vs, n, 16),
+           lambda: swa.cache8_read(k8, v8, ks, vs.double(), n, 16),
+           lambda: swa.cache8_read(k8, v8, ks, vs, n, 16, 40, 9),
+           lambda: swa.cache8_read(k8, v8, ks, vs, n, 16, -1),
+           lambda: swa.forward_cache8(q.float(), k8, v8, ks, vs, n, 16, 0, 0.1),
+           lambda: swa.forward_cache8(q[:1], k8, v8, ks, vs, n, 16, 0, 0.1),
+           lambda: swa.forward_cache8(q[0], k8, v8, ks, vs, n, 16, 0, 0.1),
+           lambda: swa.forward_cache8(q, k8, v8, ks, vs, None, 16, 0, 0.1),
+           lambda: swa.forward_cache8(q, k8, v8, ks, vs, n, 16, 2 ** 40, 0.1),
+           lambda: swa.forward_cache8(q, k8, v8, ks, vs, n, 16, 0, 0.1, sinks=torch.zeros(3, device="cuda")),
+           lambda: swa.forward_cache8(q.transpose(1, 3).contiguous().transpose(1, 3), k8, v8, ks, vs, n, 16, 0, 0.1)]
+    for i, f in enumerate(bad):
+        with pytest.raises(ValueError):
+            f()
+            pytest.fail(f"call {i} was not refused")
+    wide = torch.zeros(2, 2, 1, 68, dtype=BF, device="cuda")[..., :64]  # heads 68 elements apart
+    for f in (lambda: swa.cache8_append(wide, k, k8, v8, ks, vs, n, 16),
+              lambda: swa.cache8_append(k[:, :1].expand(2, 2, 1, 64), k, k8, v8, ks, vs, n, 16),
+              lambda: swa.forward_cache8(q, k8, v8, ks, vs, n, 16, -3, 0.1),
+              lambda: swa.forward_cache8(q[:, :3].contiguous(), k8, v8, ks, vs, n, 16, 0, 0.1)):
+        with pytest.raises(swa.SwaError):
+            f()
+    status_ok()
