@@ -20,19 +20,32 @@
 // each of them twice more in shared memory, in a kernel that has 23 of the
 // cache's bytes a clock and SM to take.
 //
-// Products are transposed: S^T (128 keys x 32) = K_tile [a b]^T and O^T (D x 48)
-// += V_tile^T [hi mid lo]^T, so that the keys fill the MMA's M dimension whatever
-// the number of query rows is.  One block has up to 16 rows (G * Lq of a kv head).
+// Products are transposed: S^T (128 keys x 2 N) = K_tile [a b]^T and O^T (D x 3 N) +=
+// V_tile^T [hi mid lo]^T, so that the keys fill the MMA's M dimension whatever the
+// number of query rows is.  A block has up to N = 16 or 32 of the G * Lq rows of a kv
+// head; a softmax thread has one key of the tile.
 //
 // Work.  The unit is one tile of 128 keys of one segment (request, kv head, row
 // block).  The units of all requests, by the device-side lengths, are cut into
 // 304 equal runs, one for each CTA, two CTAs an SM.  A segment that lies within
 // one run is finished there; one that runs' ends cut leaves a partial (R, sum,
-// O) for each run, and a second kernel merges those.
+// O) for each run, and a second kernel merges those.  Where a kv head has several
+// row blocks, neighbouring CTAs have the same runs of different blocks, so that a
+// tile's later reads find it in L2 (16 requests of 32 rows over 4,096 keys, D =
+// 512: 52.7 us, and 83.9 with the blocks one after the other).
 //
 // Tiles are aligned to the end of what a request's rows see: one that would
 // reach past it starts earlier (below key 0 the TMA fills zeros), so nothing
 // behind a request's length is loaded.
+//
+// Bounds.  Long caches by HBM: 32 requests of up to 16,384 tokens, D = 512, 155 us,
+// 6.9 TB/s of cache; 64 of up to 8,192, D = 128, 45.7 us, 5.9 TB/s, of which some 9
+// are not the stream's: 1.0 lengths and split, 3 until the first tiles are there,
+// 1 from the last tile's arrival to a run's end, 1.0 until the merge may begin, 1.6
+// merge, 0.5 until the next call's lengths.  Those are what a short call takes (4
+// requests of up to 1,024, D = 128: 7.7 us, and as much on the host).  A tile takes
+// a CTA 0.8 to 1.0 us of softmax, which two CTAs an SM overlap: at D = 64 that, not
+// HBM, bounds calls with 16 rows.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -73,7 +86,7 @@ struct C8Params {
   uint16_t* o;         // bf16 [B, Hq, Lq, D]
   float* lse;          // [B, Hq, Lq]
   int4* cuts;          // [kCtas]: the segment that the begin of the CTA's run cuts (-1: none), its partials, their
-                       // first CTA and that one's slot
+                       // first CTA (the others are g.lanes apart) and that one's slot
   float *ml, *po;      // partials [2 kCtas][rows of a block][2] and [..][D]
   int orow;            // rows of a partial's slot
   int* status;
@@ -86,19 +99,22 @@ __device__ __forceinline__ int tiles_of(const Cache8Geom& g, int len) {
   return n > lo ? (n - lo + T - 1) / T : 0;
 }
 
-// The runs that the units are cut into, one for each CTA while they last; none is empty.
+// The runs that a lane's units are cut into (see Cache8Geom), one for each of its
+// CTAs while they last; none is empty.
 struct Runs {
-  unsigned units;  // (units * kCtas < 2^32)
-  __device__ __forceinline__ unsigned start(unsigned c) const { return units < kCtas ? min(c, units) : c * units / kCtas; }
-  __device__ __forceinline__ unsigned of(unsigned u) const {  // whose unit u is
-    return units < kCtas ? u : ((u + 1) * kCtas - 1) / units;
+  unsigned units, n;  // (units * kCtas < 2^32)
+  __device__ __forceinline__ unsigned start(unsigned r) const {
+    if (units < n) return min(r, units);
+    return n == kCtas ? r * units / kCtas : r * units / n;
   }
+  __device__ __forceinline__ unsigned of(unsigned u) const { return units < n ? u : ((u + 1) * n - 1) / units; }  // whose unit u is
 };
 
 // A place in a CTA's run: request, kv head, row block, tile.
 struct Walk {
   const C8Params* p;
   int left;      // units from here to the end of the run
+  int lane;      // of row blocks: the walk has blocks lane, lane + g.lanes, ..
   int b, h, blk;
   int t, nt, n;  // tile of the segment, its tiles, the request's length
   bool first;    // first tile of this CTA's visit of the segment
@@ -106,15 +122,21 @@ struct Walk {
     n = min(p->kv_len[b], p->g.rows);
     nt = tiles_of(p->g, n);
   }
-  __device__ __forceinline__ void begin(int b0, int r, int units) {  // unit r of request b0's
+  __device__ __forceinline__ void begin(int b0, int len, int r, int units) {  // unit r of request b0's
     b = b0;
-    set_request();
+    n = min(len, p->g.rows);
+    nt = tiles_of(p->g, n);
     const int in = r / nt;
     t = r - in * nt;
-    h = p->g.nmb == 1 ? in : in / p->g.nmb;
-    blk = in - h * p->g.nmb;
+    const int per = blocks();
+    h = per == 1 ? in : in / per;
+    blk = lane + p->g.lanes * (in - h * per);
     left = units;
     first = true;
+  }
+  // the lane's blocks of a head (one, where there are no more blocks than CTAs)
+  __device__ __forceinline__ int blocks() const {
+    return p->g.nmb == p->g.lanes ? 1 : (p->g.nmb - lane + p->g.lanes - 1) / p->g.lanes;
   }
   __device__ __forceinline__ int head() const { return b * p->g.Hkv + h; }
   __device__ __forceinline__ int key0() const { return n - T * (nt - t); }
@@ -125,8 +147,8 @@ struct Walk {
     if (--left == 0 || t < nt) return;
     first = true;
     t = 0;
-    if (++blk < p->g.nmb) return;
-    blk = 0;
+    if ((blk += p->g.lanes) < p->g.nmb) return;
+    blk = lane;
     if (++h < p->g.Hkv) return;
     h = 0;
     do {  // the next request with keys (there is one while units are left and the lengths stay)
@@ -145,12 +167,10 @@ struct Walk {
   }
 };
 
-// The kernel with blocks of NR query rows: 16, or 32 where a kv head has more and
-// the accumulators fit (up to D = 256, there with one buffer of scores).
+// The kernel with blocks of NR query rows: 16, or 32 at D <= 128.
 template <int D, int NR>
 struct C8 {
   static constexpr int NS = 2 * NR, NP = 3 * NR;  // columns of S^T (q's two parts) and O^T (a weight's three)
-  static constexpr int SBUF = 2 * NS + NP * (D < 128 ? 1 : D / 128) <= 256 ? 2 : 1;
   static constexpr int LINE = D < 128 ? D : 128;  // bytes of a key's line in a slot
   static constexpr int NCH = D / LINE;            // slots per tile and tensor; 128-row blocks of O^T
   static constexpr int SLOT = T * LINE;
@@ -165,7 +185,7 @@ struct C8 {
   static constexpr int NSLOT = FIT > 4 ? (D == 64 ? 8 : 4) : FIT;
   static constexpr int OFF_Q = NSLOT * SLOT, OFF_P = OFF_Q + 2 * QB, OFF_SMALL = OFF_P + PB, OFF_BAR = OFF_SMALL + SMALL;
   static constexpr size_t SMEM = (size_t)OFF_BAR + BARS + 1024;
-  static constexpr uint32_t S_COL = 0, O_COL = SBUF * NS;  // TMEM columns: S^T's buffers, O^T's blocks
+  static constexpr uint32_t S_COL = 0, O_COL = 2 * NS;  // TMEM columns: S^T twice, O^T's blocks
   static constexpr uint32_t COLS = O_COL + NP * NCH;
   static constexpr uint32_t TCOLS = COLS <= 128 ? 128 : 256;  // (two CTAs share the 512)
   static_assert(COLS <= 256, "TMEM columns");
@@ -366,14 +386,14 @@ __device__ __forceinline__ void softmax_visit(const C8Params& p, unsigned char* 
   bool more = true, fresh = true;
 #pragma unroll 1
   while (more) {
-    const int n = c.n, buf = C::SBUF == 2 ? n & 1 : 0, key0 = w.key0();
+    const int n = c.n, buf = n & 1, key0 = w.key0();
     more = !w.last();
     const float vscale = fmaxf(c.vs, cache8_two_to(kCache8LeastExponent)), lv = __log2f(vscale);
     const uint64_t ks2 = f2_pack(c.ks, c.ks), lv2 = f2_pack(lv, lv), iv2 = f2_pack(__fdividef(1.f, vscale), __fdividef(1.f, vscale));
     w.next();
     if (w.left > 0) load_scales(p, w, t, c);  // the next tile's are under way meanwhile
     const bool edge = !(key0 >= lo_all && key0 + T - 1 <= hi_all);
-    wait(bar.s_full(buf), (C::SBUF == 2 ? n >> 1 : n) & 1, abort);
+    wait(bar.s_full(buf), (n >> 1) & 1, abort);
     __syncwarp();
     tc_fence_after();
 #pragma unroll
@@ -579,7 +599,7 @@ __global__ void __launch_bounds__(kThr, 2)
     cache8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const __grid_constant__ C8Params p) {
   using C = C8<D, NR>;
-  constexpr int NSLOT = C::NSLOT, NCH = C::NCH, NS = C::NS, NP = C::NP, AHEAD = C::SBUF;  // tiles whose scores are ahead
+  constexpr int NSLOT = C::NSLOT, NCH = C::NCH, NS = C::NS, NP = C::NP;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const Bars bar{reinterpret_cast<uint64_t*>(base + C::OFF_BAR)};
@@ -610,24 +630,27 @@ __global__ void __launch_bounds__(kThr, 2)
   }
   // ---- this CTA's run, by every warp for itself: the tiles of all requests, then
   // the request that the run's first unit belongs to
-  auto tiles_at = [&](int b) { return b < g.B ? tiles_of(g, p.kv_len[b]) : 0; };
-  const int nt0 = tiles_at(lane);  // of the first 32
-  unsigned tiles = nt0;
+  auto length = [&](int b) { return b < g.B ? p.kv_len[b] : -1; };
+  const int len0 = length(lane);  // of the first 32
+  unsigned tiles = tiles_of(g, len0);
 #pragma unroll 2
-  for (int b = lane + 32; b < g.B; b += 32) tiles += tiles_at(b);
+  for (int b = lane + 32; b < g.B; b += 32) tiles += tiles_of(g, length(b));
   tiles = __reduce_add_sync(0xffffffffu, tiles);
-  const unsigned hn = g.Hkv * g.nmb;
-  const Runs runs{tiles * hn};
-  const unsigned u0 = runs.start(cta);
-  const int units = (int)(runs.start(cta + 1) - u0);
   Walk first;  // the run's first unit
   first.p = &p;
   first.left = 0;
+  const unsigned run = g.lanes == 1 ? cta : cta / g.lanes;
+  first.lane = cta - (int)run * g.lanes;
+  const unsigned hn = g.Hkv * first.blocks();
+  const Runs runs{tiles * hn, g.lanes == 1 ? kCtas : kCtas / (unsigned)g.lanes};
+  const unsigned u0 = runs.start(run);
+  const int units = run < runs.n ? (int)(runs.start(run + 1) - u0) : 0;
   if (units > 0) {
     unsigned before = 0;
 #pragma unroll 1
     for (int b0 = 0; b0 < g.B; b0 += 32) {
-      const unsigned nt = b0 == 0 ? nt0 : tiles_at(b0 + lane);
+      const int len = b0 == 0 ? len0 : length(b0 + lane);
+      const unsigned nt = tiles_of(g, len);
       unsigned inc = nt;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -638,7 +661,7 @@ __global__ void __launch_bounds__(kThr, 2)
       if (here) {
         const int l = __ffs(here) - 1;
         const unsigned at = before + __shfl_sync(0xffffffffu, inc - nt, l);
-        first.begin(b0 + l, (int)(u0 - at * hn), units);
+        first.begin(b0 + l, __shfl_sync(0xffffffffu, len, l), (int)(u0 - at * hn), units);
         break;
       }
       before += __shfl_sync(0xffffffffu, inc, 31);
@@ -665,11 +688,11 @@ __global__ void __launch_bounds__(kThr, 2)
         w.next();
         return true;
       };
-      // slots in MMA order, with two tiles ahead: K(0), K(1), then per tile n: V(n), K(n + 2)
+      // slots in MMA order: K(0), K(1), then per tile n: V(n), K(n + 2)
       bool ok = true;
 #pragma unroll 1
-      for (int n = -AHEAD; ok && n < total; ++n)
-        ok = (n < 0 || load_tile(wv, &tmV)) && (n + AHEAD >= total || load_tile(wk, &tmK));
+      for (int n = -2; ok && n < total; ++n)
+        ok = (n < 0 || load_tile(wv, &tmV)) && (n + 2 >= total || load_tile(wk, &tmK));
       if (*abort_flag) drain_ring(bar.slot_full(0), NSLOT, issued);  // loads in flight land before shared memory is released
     }
   } else if (warp == 1) {
@@ -695,14 +718,14 @@ __global__ void __launch_bounds__(kThr, 2)
           const int s = used % NSLOT;
           if (!wait(bar.slot_full(s), (used / NSLOT) & 1, abort_flag)) return false;
           tc_fence_after();
-          const uint32_t s_at = tmem + C::S_COL + (AHEAD == 2 ? NS * (n & 1) : 0);
+          const uint32_t s_at = tmem + C::S_COL + NS * (n & 1);
           const uint64_t kd = desc_add(kd0, s * C::SLOT), qd = desc_add(qd0, qs * C::QB + c * NS * C::LINE);
 #pragma unroll
           for (int k = 0; k < C::LINE / 32; ++k)
             mma_f8(s_at, desc_add(kd, k * 32), desc_add(qd, k * 32), idS, (c | k) ? 1u : 0u);
           mma_commit(bar.slot_empty(s));
         }
-        mma_commit(bar.s_full(AHEAD == 2 ? n & 1 : 0));
+        mma_commit(bar.s_full(n & 1));
         if (ws.last()) {  // the visit's queries are read
           mma_commit(bar.q_empty(qs));
           ++nq;
@@ -712,7 +735,7 @@ __global__ void __launch_bounds__(kThr, 2)
       };
       bool ok = true;
 #pragma unroll 1
-      for (int n = -AHEAD; ok && n < total; ++n) {
+      for (int n = -2; ok && n < total; ++n) {
         if (n >= 0) {
           if (!wait(bar.p_full(), n & 1, abort_flag)) break;
           tc_fence_after();
@@ -733,7 +756,7 @@ __global__ void __launch_bounds__(kThr, 2)
           mma_commit(bar.o_done());
           wv.next();
         }
-        if (n + AHEAD < total) ok = issue_s(n + AHEAD);  // the weights of tile n have been written: its scores' buffer is free
+        if (n + 2 < total) ok = issue_s(n + 2);  // the weights of tile n have been written: its scores' buffer is free
       }
       mma_commit(bar.drain());
       mbar_wait_drain(bar.drain(), 0);
@@ -763,8 +786,9 @@ __global__ void __launch_bounds__(kThr, 2)
       if (total > 0 && first.t > 0) {
         const unsigned begin = u0 - first.t;
         const int c0 = (int)runs.of(begin);
-        cut = make_int4(first.head() * g.nmb + first.blk, (int)runs.of(begin + first.nt - 1) - c0 + 1, c0,
-                        2 * c0 + (runs.start(c0) == begin ? 0 : 1));
+        cut = make_int4(first.head() * g.nmb + first.blk, (int)runs.of(begin + first.nt - 1) - c0 + 1,
+                        c0 * g.lanes + first.lane,
+                        2 * (c0 * g.lanes + first.lane) + (runs.start(c0) == begin ? 0 : 1));
       }
       p.cuts[cta] = cut;
     }
@@ -830,8 +854,9 @@ __device__ __forceinline__ void merge_pieces(const C8Params& p, const int4& cut,
   const Cache8Geom& g = p.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l0 = lane % LANES;
   const int n = cut.y, head = g.nmb == 1 ? cut.x : cut.x / g.nmb, blk = cut.x - head * g.nmb;
+  const int apart = g.lanes == 1 ? (int)blockIdx.x - cut.z : ((int)blockIdx.x - cut.z) / g.lanes;  // runs
   // pieces first, first + step, .. of `all` (the quotient of numbers below 2^12 is exact)
-  const int all = rows * PIECES, first = kMergeSides * ((int)blockIdx.x - cut.z - 1) + blockIdx.y, step = max(kMergeSides * (n - 1), 1);
+  const int all = rows * PIECES, first = kMergeSides * (apart - 1) + blockIdx.y, step = max(kMergeSides * (n - 1), 1);
   const int mine = n == 0 ? 4 : (first < all ? (int)__fdividef(all - first + step - 0.5f, (float)step) : 0);
   const int sh = mine >= kMergeWarps ? 0 : 2 - (32 - __clz(mine - 1)), share = 1 << sh;  // warps on a piece
   const int k = warp & (share - 1);
@@ -850,7 +875,7 @@ __device__ __forceinline__ void merge_pieces(const C8Params& p, const int4& cut,
       auto load = [&](int a, int j) {
         ml[a] = make_float2(kUnset, 0.f);
         if (j >= n) return;
-        const size_t at = (size_t)(j == 0 ? cut.w : 2 * (cut.z + j)) * p.orow + row;
+        const size_t at = (size_t)(j == 0 ? cut.w : 2 * (cut.z + j * g.lanes)) * p.orow + row;
         ml[a] = *reinterpret_cast<const float2*>(p.ml + 2 * at);
         const float4* src = reinterpret_cast<const float4*>(p.po + at * D + col) + l0;
 #pragma unroll
@@ -1013,16 +1038,20 @@ bool cache8_fits(const Cache8Geom& g) {
   const double units = (double)g.B * g.Hkv * g.nmb * ((g.rows + T - 1) / T);
   return units * kCtas < 4.0e9 && (double)g.B * g.Hkv * g.M < 1.0e9;
 }
-// Query rows of a block.  Blocks of 32 cost a tile nearly twice the softmax of 16, but
-// the cache is read once for them: 32 requests of 32 rows over 8,192 keys, D = 128,
-// 50.6 us against 75.6.  With few tiles a CTA the shorter ones spread better (16
-// requests, D = 256: 20.2 and 16.7 us over 1,024 keys, 26.3 and 28.3 over 2,560,
-// which are 4.2 tiles a CTA; D = 64: 14.6 and 13.5 at 2.1, both 17.1 at 4.2, and
-// 17.2 and 15.9 where the lengths fill half of such a cache, whose rows are what
-// the host knows).
-int cache8_block_rows(const Cache8Geom& g) {
+// Query rows of a block.  A tile costs blocks of 32 nearly twice the softmax of 16,
+// and they read it once where two of 16 both do, one of them from L2.  At D = 256 and
+// 512, where HBM is what bounds the calls, that is as fast (16 requests of 32 rows
+// over 5,120 keys, D = 256: 33.5 us, and 36.9 with 32; 32 requests over 8,192: 88.6
+// and 88.3); at D <= 128 it is what bounds them (32 requests over 8,192 keys, D = 128:
+// 66.3 and 51.3 us; D = 64 over 16,384: 58.3 and 46.8).  With few tiles a CTA the
+// blocks of 16 spread better (16 requests, D = 64: 14.1 and 14.7 us over 2,560 keys,
+// 2.1 tiles a CTA, 17.7 and 17.3 over 5,120; 16.0 and 18.0 where the lengths fill half
+// of such a cache, whose rows are what the host knows).
+void cache8_split(Cache8Geom& g) {
   const long long units = (long long)g.B * g.Hkv * ((g.M + 31) / 32) * tiles_most(g);
-  return g.M <= 16 || g.D == 512 || units < 6 * kCtas ? 16 : 32;
+  g.nr = g.M <= 16 || g.D > 128 || units < 6 * kCtas ? 16 : 32;
+  g.nmb = (g.M + g.nr - 1) / g.nr;
+  g.lanes = g.nmb < kCtas ? g.nmb : kCtas;
 }
 size_t cache8_workspace_bytes(const Cache8Geom& g) { return c8_ws(g).total; }
 
@@ -1031,7 +1060,7 @@ cudaError_t launch_fwd_cache8(const Cache8Geom& g, const Cache8Args& a, void* ws
   switch (g.D) {
     case 64: return few ? cache8_d<64, 16>(g, a, ws, status, st) : cache8_d<64, 32>(g, a, ws, status, st);
     case 128: return few ? cache8_d<128, 16>(g, a, ws, status, st) : cache8_d<128, 32>(g, a, ws, status, st);
-    case 256: return few ? cache8_d<256, 16>(g, a, ws, status, st) : cache8_d<256, 32>(g, a, ws, status, st);
+    case 256: return cache8_d<256, 16>(g, a, ws, status, st);
     case 512: return cache8_d<512, 16>(g, a, ws, status, st);
     default: return cudaErrorInvalidValue;
   }

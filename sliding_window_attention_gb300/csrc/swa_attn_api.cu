@@ -831,8 +831,7 @@ static int cache8_geom(swa::Cache8Geom& g, int B, int Hq, int Hkv, int Lq, int k
   g.D = D;
   g.W = window >= kv_rows ? 0 : window;  // no two positions are further apart
   g.scale = scale;
-  g.nr = swa::cache8_block_rows(g);
-  g.nmb = (g.M + g.nr - 1) / g.nr;
+  swa::cache8_split(g);
   return swa::cache8_fits(g) ? SWA_OK : SWA_ERR_TOO_LARGE;
 }
 

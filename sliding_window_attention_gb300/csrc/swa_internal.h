@@ -462,6 +462,8 @@ cudaError_t launch_cache8_read(const Cache8ReadArgs& a, cudaStream_t s);
 struct Cache8Geom {
   int B, Hq, Hkv, G, Lq, M;       // M = G * Lq query rows of a request and kv head
   int nr, nmb;                    // in nmb blocks of up to nr
+  int lanes;                      // CTA c works on blocks c % lanes, c % lanes + lanes, ..: those of one key range are
+                                  // neighbours' work at the same time, and meet in L2
   int rows, lb, nblk;             // cache rows, log2 of a scale's block, scales of a head
   int D, W;                       // W = 0: no window
   float scale;
@@ -475,7 +477,7 @@ struct Cache8Args {
   uint16_t* o;
   float* lse;
 };
-int cache8_block_rows(const Cache8Geom& g);  // nr, from the rest
+void cache8_split(Cache8Geom& g);       // nr, nmb and lanes, from the rest
 bool cache8_fits(const Cache8Geom& g);  // unit and row counts within the kernel's 32-bit indexes
 size_t cache8_workspace_bytes(const Cache8Geom& g);
 cudaError_t launch_fwd_cache8(const Cache8Geom& g, const Cache8Args& a, void* ws, int* status, cudaStream_t s);
