@@ -12,7 +12,15 @@
 // Both kernels are bound by memory: an append reads 2 bytes and writes 1 an
 // element, a read the other way round.  A group of threads has one block: it
 // keeps the block's new rows in registers between the maximum and the codes, so
-// they are read once.
+// they are read once.  Measured: 30,553 tokens of 16 heads, D = 256, appended in
+// 111 us (6.8 TB/s), 2 x 16,384 rows of 4 heads, D = 512, half of them behind the
+// lengths, read in 50.6 us (6.6 TB/s), one token of each of 64 requests appended in
+// 1.7 us (2.5 us of the host's).
+//
+// Maxima are those of bf16 patterns without their signs, two at a time: with fp32
+// maxima and a division that no power of two needs the append was bound by its
+// instructions (151 us).  A read's thread takes 8 codes, so that its 16 bytes and its
+// neighbours' are written as whole lines (16 codes a thread: 59.5 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -237,7 +245,8 @@ cudaError_t launch_cache8_append(const Cache8AppendArgs& a, cudaStream_t st) {
   const long long meets = ((long long)a.L + a.block - 2) / a.block + 1;
   p.nj = (int)(meets < p.nblk ? meets : p.nblk);
   p.tasks = a.B * a.Hkv * p.nj;
-  // the smallest group whose registers hold the new rows that a block can get
+  // the smallest group whose registers hold the new rows that a block can get: 4
+  // vectors a thread leave 8 CTAs an SM, and 8 where a group would pass a CTA
   const long long vecs = (long long)(a.L < a.block ? a.L : a.block) * a.D / 8;
   if (vecs <= 32 * 4) return append_as<32, 4>(p, tensors, st);
   if (vecs <= 64 * 4) return append_as<64, 4>(p, tensors, st);

@@ -22,8 +22,8 @@
 //
 // Products are transposed: S^T (128 keys x 2 N) = K_tile [a b]^T and O^T (D x 3 N) +=
 // V_tile^T [hi mid lo]^T, so that the keys fill the MMA's M dimension whatever the
-// number of query rows is.  A block has up to N = 16 or 32 of the G * Lq rows of a kv
-// head; a softmax thread has one key of the tile.
+// number of query rows is.  A block has up to N = 8, 16 or 32 of the G * Lq rows of a
+// kv head; a softmax thread has one key of the tile.
 //
 // Work.  The unit is one tile of 128 keys of one segment (request, kv head, row
 // block).  The units of all requests, by the device-side lengths, are cut into
@@ -38,14 +38,15 @@
 // reach past it starts earlier (below key 0 the TMA fills zeros), so nothing
 // behind a request's length is loaded.
 //
-// Bounds.  Long caches by HBM: 32 requests of up to 16,384 tokens, D = 512, 155 us,
-// 6.9 TB/s of cache; 64 of up to 8,192, D = 128, 45.7 us, 5.9 TB/s, of which some 9
+// Bounds.  Long caches by HBM: 32 requests of up to 16,384 tokens, D = 512, 153.7 us,
+// 7.0 TB/s of cache; 64 of up to 8,192, D = 128, 44.3 us, 6.1 TB/s, of which some 8
 // are not the stream's: 1.0 lengths and split, 3 until the first tiles are there,
 // 1 from the last tile's arrival to a run's end, 1.0 until the merge may begin, 1.6
 // merge, 0.5 until the next call's lengths.  Those are what a short call takes (4
-// requests of up to 1,024, D = 128: 7.7 us, and as much on the host).  A tile takes
-// a CTA 0.8 to 1.0 us of softmax, which two CTAs an SM overlap: at D = 64 that, not
-// HBM, bounds calls with 16 rows.
+// requests of up to 1,024, D = 128: 7.3 us, and as much on the host).  At D = 64 the
+// softmax of a tile, 0.7 us of a CTA for 8 rows, is as long as its stream (64
+// requests of 16 / 2 heads over 16,384 keys: 49.1 us, 5.5 TB/s; three CTAs an SM,
+// 46.2 us, would cost the other head dims 1 to 4 us).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -64,7 +65,6 @@ namespace {
 using namespace tc;
 
 constexpr int T = 128;       // keys per tile
-constexpr int HR = 16;       // query rows that a softmax thread has in registers at a time
 constexpr int kCtas = 304;   // two an SM
 constexpr int kThr = 224;    // TMA, MMA, four softmax warps, one that prepares queries
 constexpr int kSmemMax = 115584;  // dynamic, a CTA: half of an SM's 228 KB less 1 KB that the system keeps and the static
@@ -167,10 +167,12 @@ struct Walk {
   }
 };
 
-// The kernel with blocks of NR query rows: 16, or 32 at D <= 128.
+// The kernel with blocks of NR query rows: 8, 16, or 32 at D <= 128.
 template <int D, int NR>
 struct C8 {
-  static constexpr int NS = 2 * NR, NP = 3 * NR;  // columns of S^T (q's two parts) and O^T (a weight's three)
+  static constexpr int HR = NR < 16 ? NR : 16;    // rows that a softmax thread has in registers at a time
+  static constexpr int NS = 2 * NR;               // columns of S^T: q's two parts
+  static constexpr int NP = (3 * NR + 15) / 16 * 16;  // of O^T: a weight's three, part i's row r in column NR i + r
   static constexpr int LINE = D < 128 ? D : 128;  // bytes of a key's line in a slot
   static constexpr int NCH = D / LINE;            // slots per tile and tensor; 128-row blocks of O^T
   static constexpr int SLOT = T * LINE;
@@ -187,7 +189,7 @@ struct C8 {
   static constexpr size_t SMEM = (size_t)OFF_BAR + BARS + 1024;
   static constexpr uint32_t S_COL = 0, O_COL = 2 * NS;  // TMEM columns: S^T twice, O^T's blocks
   static constexpr uint32_t COLS = O_COL + NP * NCH;
-  static constexpr uint32_t TCOLS = COLS <= 128 ? 128 : 256;  // (two CTAs share the 512)
+  static constexpr uint32_t TCOLS = COLS <= 64 ? 64 : (COLS <= 128 ? 128 : 256);  // (two CTAs share the 512)
   static_assert(COLS <= 256, "TMEM columns");
   static_assert(NSLOT >= 3 && SMEM <= (size_t)kSmemMax, "shared memory");
 };
@@ -237,9 +239,9 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
   return false;
 }
 
-// Column reduction of 16 columns over the warp's lanes by halving: lanes 2 c and 2 c + 1 end with column c in v[0].
-template <bool MAX>
-__device__ __forceinline__ void column_reduce(float (&v)[HR], int lane) {
+// Column reduction of HR columns over the warp's lanes by halving, into dst[0 .. HR - 1].
+template <int HR, bool MAX>
+__device__ __forceinline__ void column_reduce(float (&v)[HR], float* dst, int lane) {
   auto op = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
   int o = 16;
 #pragma unroll
@@ -251,7 +253,9 @@ __device__ __forceinline__ void column_reduce(float (&v)[HR], int lane) {
       v[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
     }
   }
-  v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
+#pragma unroll
+  for (; o >= 1; o >>= 1) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+  if (lane % (32 / HR) == 0) dst[lane / (32 / HR)] = v[0];
 }
 
 // Queries of one visit as the B operand of the first product: rows 4 w .. 4 w + 3
@@ -354,7 +358,7 @@ template <int D, int NR>
 __device__ __forceinline__ void softmax_visit(const C8Params& p, unsigned char* base, const Bars& bar,
                                               volatile int* abort, Walk& w, Soft& c) {
   using C = C8<D, NR>;
-  constexpr int NH = NR / HR, NP = C::NP;
+  constexpr int HR = C::HR, NH = NR / HR, NP = C::NP;
   const Cache8Geom& g = p.g;
   const int lane = threadIdx.x & 31, q4 = (threadIdx.x >> 5) & 3, t = 32 * q4 + lane;
   unsigned char* small = base + C::OFF_SMALL;
@@ -398,10 +402,11 @@ __device__ __forceinline__ void softmax_visit(const C8Params& p, unsigned char* 
     tc_fence_after();
 #pragma unroll
     for (int hf = 0; hf < NH; ++hf) {  // 16 rows from row HR * hf on
-      uint32_t hi[HR], lo[HR];
-      tmem_ld16(c.at + C::S_COL + C::NS * buf + HR * hf, hi);
-      tmem_ld16(c.at + C::S_COL + C::NS * buf + NR + HR * hf, lo);
+      uint32_t sa[16], sb[16];
+      tmem_ld16(c.at + C::S_COL + C::NS * buf + HR * hf, sa);
+      if (NR > 8) tmem_ld16(c.at + C::S_COL + C::NS * buf + NR + HR * hf, sb);
       tmem_wait_ld();
+      const uint32_t *hi = sa, *lo = NR > 8 ? sb : sa + 8;
       uint64_t y[HR / 2], z[HR / 2];
       const uint64_t small16 = f2_pack(0.0625f, 0.0625f);
 #pragma unroll
@@ -454,8 +459,7 @@ __device__ __forceinline__ void softmax_visit(const C8Params& p, unsigned char* 
           mx[2 * q] = v.x;
           mx[2 * q + 1] = v.y;
         }
-        column_reduce<true>(mx, lane);
-        if ((lane & 1) == 0) red[q4 * HR + (lane >> 1)] = mx[0];
+        column_reduce<HR, true>(mx, red + q4 * HR, lane);
         soft_sync();
         bool moved = false;
         const int i = t - HR * hf;
@@ -481,13 +485,13 @@ __device__ __forceinline__ void softmax_visit(const C8Params& p, unsigned char* 
           __syncwarp();
           tc_fence_after();
 #pragma unroll 1
-          for (int j = 0; j < 3 * C::NCH; ++j) {
-            const uint32_t at = c.at + C::O_COL + NR * j + HR * hf;
-            uint32_t ov[HR];
+          for (int j = 0; j < (NR > 8 ? 3 : 2) * C::NCH; ++j) {
+            const uint32_t at = c.at + C::O_COL + (NR > 8 ? NR : 16) * j + HR * hf;
+            uint32_t ov[16];
             tmem_ld16(at, ov);
             tmem_wait_ld();
 #pragma unroll
-            for (int q = 0; q < HR; ++q) ov[q] = __float_as_uint(__uint_as_float(ov[q]) * alp[HR * hf + q]);
+            for (int q = 0; q < 16; ++q) ov[q] = __float_as_uint(__uint_as_float(ov[q]) * alp[HR * hf + q % HR]);
             tmem_st16(at, ov);
           }
           tmem_wait_st();
@@ -523,11 +527,16 @@ __device__ __forceinline__ void softmax_visit(const C8Params& p, unsigned char* 
       }
       // the second product of tile n - 1 has finished with the weights' buffer
       if (hf == 0 && n > 0) wait(bar.o_done(), (n - 1) & 1, abort);
-      // MN-major operand without swizzle: a key's 16 rows of one part are 16 bytes
-      unsigned char* pb = base + C::OFF_P + (hf * T + t) * HR;
+      // MN-major operand without swizzle: 16 columns of a key are 16 bytes
+      unsigned char* pb = base + C::OFF_P + (hf * T + t) * 16;
+      if constexpr (NR > 8) {
 #pragma unroll
-      for (int i = 0; i < 3; ++i)
-        *reinterpret_cast<uint4*>(pb + i * T * NR) = make_uint4(part[i][0], part[i][1], part[i][2], part[i][3]);
+        for (int i = 0; i < 3; ++i)
+          *reinterpret_cast<uint4*>(pb + i * T * NR) = make_uint4(part[i][0], part[i][1], part[i][2], part[i][3]);
+      } else {
+        *reinterpret_cast<uint4*>(pb) = make_uint4(part[0][0], part[0][1], part[1][0], part[1][1]);
+        *reinterpret_cast<uint4*>(pb + T * 16) = make_uint4(part[2][0], part[2][1], 0, 0);
+      }
     }
     fresh = false;
     fence_proxy_async_smem();  // generic writes -> the tensor core's reads
@@ -548,8 +557,7 @@ __device__ __forceinline__ void softmax_visit(const C8Params& p, unsigned char* 
       l[2 * q] = v.x;
       l[2 * q + 1] = v.y;
     }
-    column_reduce<false>(l, lane);
-    if ((lane & 1) == 0) red[q4 * NR + HR * hf + (lane >> 1)] = l[0];
+    column_reduce<HR, false>(l, red + q4 * NR + HR * hf, lane);
   }
   soft_sync();
   float* mul = alp;  // a whole segment's 1 / sum
@@ -572,12 +580,13 @@ __device__ __forceinline__ void softmax_visit(const C8Params& p, unsigned char* 
 #pragma unroll 1
   for (int h = 0; h < C::NCH * NH; ++h) {
     const int ch = NH == 1 ? h : h / NH, r0 = NH == 1 ? 0 : HR * (h % NH);
-    uint32_t hi[HR], mid[HR], lo[HR];
+    uint32_t oa[16], ob[16], oc[16];
     const uint32_t at = c.at + C::O_COL + NP * ch + r0;
-    tmem_ld16(at, hi);  // warp-collective
-    tmem_ld16(at + NR, mid);
-    tmem_ld16(at + 2 * NR, lo);
+    tmem_ld16(at, oa);  // warp-collective
+    tmem_ld16(at + (NR > 8 ? NR : 16), ob);
+    if (NR > 8) tmem_ld16(at + 2 * NR, oc);
     tmem_wait_ld();
+    const uint32_t *hi = oa, *mid = NR > 8 ? ob : oa + 8, *lo = NR > 8 ? oc : ob;
     const int d = T * ch + t;
     if (d < D) {
       uint16_t* o = p.o + ((size_t)head * g.M + blk * NR + r0) * D + d;
@@ -707,7 +716,7 @@ __global__ void __launch_bounds__(kThr, 2)
       // 8 lines make a swizzled group.  At D = 64 the second product's rows 64-127 repeat 0-63 and are never read.
       const uint64_t kd0 = smem_desc(smem_u32(base), D < 128 ? 0 : 16, 8 * C::LINE, SWZ);
       const uint64_t qd0 = smem_desc(smem_u32(base + C::OFF_Q), 16, 8 * C::LINE, SWZ);
-      const uint64_t pd = smem_desc(smem_u32(base + C::OFF_P), 8 * HR, T * HR, 0);
+      const uint64_t pd = smem_desc(smem_u32(base + C::OFF_P), 8 * 16, T * 16, 0);
       Walk ws = first, wv = first;
       int used = 0, nq = 0;
       auto issue_s = [&](int n) -> bool {  // S^T(n)
@@ -748,7 +757,7 @@ __global__ void __launch_bounds__(kThr, 2)
             const uint64_t vd = desc_add(kd0, s * C::SLOT);
 #pragma unroll
             for (int k = 0; k < T / 32; ++k)
-              mma_f8(tmem + C::O_COL + NP * c, desc_add(vd, k * 32 * C::LINE), desc_add(pd, k * 32 * HR), idO,
+              mma_f8(tmem + C::O_COL + NP * c, desc_add(vd, k * 32 * C::LINE), desc_add(pd, k * 32 * 16), idO,
                      (acc || k > 0) ? 1u : 0u);
             mma_commit(bar.slot_empty(s));
           }
@@ -1031,6 +1040,15 @@ cudaError_t cache8_d(const Cache8Geom& g, const Cache8Args& a, void* ws, int* st
   return launch_dependent(cache8_merge_kernel<D>, dim3(kCtas, kMergeSides), dim3(32 * kMergeWarps), 0, st, p);
 }
 
+template <int D>
+cudaError_t cache8_nr(const Cache8Geom& g, const Cache8Args& a, void* ws, int* status, cudaStream_t st) {
+  if (g.nr == 8) return cache8_d<D, 8>(g, a, ws, status, st);
+  if constexpr (D <= 128) {
+    if (g.nr == 32) return cache8_d<D, 32>(g, a, ws, status, st);
+  }
+  return cache8_d<D, 16>(g, a, ws, status, st);
+}
+
 }  // namespace
 
 // Units (tiles of all segments) times runs within 32 bits.
@@ -1038,7 +1056,8 @@ bool cache8_fits(const Cache8Geom& g) {
   const double units = (double)g.B * g.Hkv * g.nmb * ((g.rows + T - 1) / T);
   return units * kCtas < 4.0e9 && (double)g.B * g.Hkv * g.M < 1.0e9;
 }
-// Query rows of a block.  A tile costs blocks of 32 nearly twice the softmax of 16,
+// Query rows of a block.  Up to 8 rows take half the softmax of 16 (the 49.1 us above
+// are 56.8 with 16; D = 128, 44.3 and 45.9).  A tile costs blocks of 32 twice that of 16,
 // and they read it once where two of 16 both do, one of them from L2.  At D = 256 and
 // 512, where HBM is what bounds the calls, that is as fast (16 requests of 32 rows
 // over 5,120 keys, D = 256: 33.5 us, and 36.9 with 32; 32 requests over 8,192: 88.6
@@ -1049,19 +1068,18 @@ bool cache8_fits(const Cache8Geom& g) {
 // of such a cache, whose rows are what the host knows).
 void cache8_split(Cache8Geom& g) {
   const long long units = (long long)g.B * g.Hkv * ((g.M + 31) / 32) * tiles_most(g);
-  g.nr = g.M <= 16 || g.D > 128 || units < 6 * kCtas ? 16 : 32;
+  g.nr = g.M <= 8 ? 8 : g.M <= 16 || g.D > 128 || units < 6 * kCtas ? 16 : 32;
   g.nmb = (g.M + g.nr - 1) / g.nr;
   g.lanes = g.nmb < kCtas ? g.nmb : kCtas;
 }
 size_t cache8_workspace_bytes(const Cache8Geom& g) { return c8_ws(g).total; }
 
 cudaError_t launch_fwd_cache8(const Cache8Geom& g, const Cache8Args& a, void* ws, int* status, cudaStream_t st) {
-  const bool few = g.nr == 16;
   switch (g.D) {
-    case 64: return few ? cache8_d<64, 16>(g, a, ws, status, st) : cache8_d<64, 32>(g, a, ws, status, st);
-    case 128: return few ? cache8_d<128, 16>(g, a, ws, status, st) : cache8_d<128, 32>(g, a, ws, status, st);
-    case 256: return cache8_d<256, 16>(g, a, ws, status, st);
-    case 512: return cache8_d<512, 16>(g, a, ws, status, st);
+    case 64: return cache8_nr<64>(g, a, ws, status, st);
+    case 128: return cache8_nr<128>(g, a, ws, status, st);
+    case 256: return cache8_nr<256>(g, a, ws, status, st);
+    case 512: return cache8_nr<512>(g, a, ws, status, st);
     default: return cudaErrorInvalidValue;
   }
 }
