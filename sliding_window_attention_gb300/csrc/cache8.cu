@@ -13,7 +13,7 @@
 // element, a read the other way round.  A group of threads has one block: it
 // keeps the block's new rows in registers between the maximum and the codes, so
 // they are read once.  Measured: 30,553 tokens of 16 heads, D = 256, appended in
-// 111 us (6.8 TB/s), 2 x 16,384 rows of 4 heads, D = 512, half of them behind the
+// 110 us (6.8 TB/s), 2 x 16,384 rows of 4 heads, D = 512, half of them behind the
 // lengths, read in 50.6 us (6.6 TB/s), one token of each of 64 requests appended in
 // 1.7 us (2.5 us of the host's).
 //
@@ -42,7 +42,7 @@ struct AppendParams {
   const int* kv_len;         // or null: tokens are rows 0 .. L - 1
   int B, Hkv, L, ld, rows, lb, nblk;  // ld, lb: log2 of D and of the block
   int nj;                    // blocks that a request's tokens meet at most
-  int tasks;                 // B * Hkv * nj
+  int nx;                    // CTAs a head, or 0: groups go through all heads' blocks
 };
 
 // Four fp32 values to e4m3, nearest, 448 at most.
@@ -66,17 +66,28 @@ __device__ __forceinline__ float2 bf16x2(uint32_t w) {
 __device__ __forceinline__ uint32_t magnitudes(uint32_t w) { return w & 0x7FFF7FFFu; }
 
 // One block's new tokens by a group of GT threads, up to VPT vectors of 8
-// elements each.
-template <int GT, int VPT>
-__global__ void __launch_bounds__(GT > 256 ? GT : 256) append_kernel(const __grid_constant__ AppendParams p) {
+// elements each; MORE: rows behind those are read twice, for the maximum and, from
+// L2, for the codes.
+template <int GT, int VPT, bool MORE>
+__global__ void __launch_bounds__(GT > 256 ? GT : 256, GT > 256 ? 2 : (VPT > 4 ? 3 : 6)) append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int CTA = GT > 256 ? GT : 256, GROUPS = CTA / GT;
   __shared__ uint32_t top[CTA / 32];
   grid_dependency_wait();
   grid_launch_dependents();
-  const int which = blockIdx.y, group = threadIdx.x / GT, tid = threadIdx.x % GT;
-  const int task = blockIdx.x * GROUPS + group;
-  const bool in = task < p.tasks;
-  const int bh = in ? task / p.nj : 0, j = task - bh * p.nj, b = bh / p.Hkv, h = bh - b * p.Hkv;
+  const int which = blockIdx.y, group = threadIdx.x / GT, cta = blockIdx.x, tid = threadIdx.x % GT;
+  // a CTA's groups have blocks of one head where there are as many (the quotients
+  // are then the same for all threads, and formed once), or of neighbouring heads
+  int bh, j;
+  if (p.nx > 0) {
+    bh = cta / p.nx;
+    j = (cta - bh * p.nx) * GROUPS + group;
+  } else {
+    const int task = cta * GROUPS + group;
+    bh = task / p.nj;
+    j = task - bh * p.nj;
+  }
+  const bool in = j < p.nj && bh < p.B * p.Hkv;
+  const int b = in ? bh / p.Hkv : 0, h = in ? bh - b * p.Hkv : 0;
   const int n = in ? (p.kv_len ? p.kv_len[b] : p.L) : 0;
   const long long from = (long long)n - p.L;  // row of token 0
   const int row0 = from > 0 ? (int)from : 0, blk = (row0 >> p.lb) + j;
@@ -87,22 +98,30 @@ __global__ void __launch_bounds__(GT > 256 ? GT : 256) append_kernel(const __gri
   const bool any = in && hi > a;
   const int lv = p.ld - 3, vecs = any ? (hi - a) << lv : 0;  // vectors of the new rows
   const uint16_t* x = p.x[which] + b * p.sb[which] + h * p.sh[which] + (any ? a - from : 0) * p.st[which];
+  auto vector = [&](int e) { return x + (e >> lv) * p.st[which] + ((e & ((1 << lv) - 1)) << 3); };
+  uint32_t most = 0;  // the larger magnitude of a pair
+  auto look = [&](const uint4& u) {
+    most = __vmaxu2(most, __vmaxu2(magnitudes(u.x), magnitudes(u.y)));
+    most = __vmaxu2(most, __vmaxu2(magnitudes(u.z), magnitudes(u.w)));
+  };
+  if (MORE) {
+#pragma unroll 8
+    for (int e = tid + VPT * GT; e < vecs; e += GT) look(*reinterpret_cast<const uint4*>(vector(e)));
+  }
   uint4 v[VPT];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int e = tid + i * GT;
     v[i] = make_uint4(0, 0, 0, 0);
-    if (e < vecs) v[i] = __ldcs(reinterpret_cast<const uint4*>(x + (e >> lv) * p.st[which] + ((e & ((1 << lv) - 1)) << 3)));
+    // (a step is whole rows, but for 32 threads and rows of 512)
+    const uint16_t* at = GT >= 64 || p.ld < 9 ? vector(tid) + i * ((GT >> lv) * p.st[which]) : vector(e);
+    if (e < vecs) v[i] = __ldcs(reinterpret_cast<const uint4*>(at));
   }
   float* scale = p.scales[which] + (size_t)bh * p.nblk + blk;
   const bool older = any && a > lo;
   const float was = older ? *scale : 0.f;
-  uint32_t most = 0;  // a pair's larger magnitude
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    most = __vmaxu2(most, __vmaxu2(magnitudes(v[i].x), magnitudes(v[i].y)));
-    most = __vmaxu2(most, __vmaxu2(magnitudes(v[i].z), magnitudes(v[i].w)));
-  }
+  for (int i = 0; i < VPT; ++i) look(v[i]);
   most = max(most & 0xFFFFu, most >> 16);
   most = __reduce_max_sync(0xffffffffu, most);
   if (GT > 32) {
@@ -118,18 +137,26 @@ __global__ void __launch_bounds__(GT > 256 ? GT : 256) append_kernel(const __gri
   uint8_t* codes = p.codes[which] + (((size_t)bh * p.rows) << p.ld);
   uint2* out = reinterpret_cast<uint2*>(codes + ((size_t)a << p.ld)) + tid;
   if ((__float_as_uint(now) & 0x7FFFFFu) == 0) {  // a power of two: its inverse is exact
-    const float mul = 1.f / now;
+    const uint64_t mul2 = f2_pack(1.f / now, 1.f / now);
+    auto times = [&](uint32_t w) {
+      const float2 f = bf16x2(w);
+      return f2_unpack(f2_mul(f2_pack(f.x, f.y), mul2));
+    };
+    auto quantised = [&](const uint4& u) {
+      const float2 x0 = times(u.x), x1 = times(u.y), x2 = times(u.z), x3 = times(u.w);
+      return make_uint2(e4m3x4(x0.x, x0.y, x1.x, x1.y), e4m3x4(x2.x, x2.y, x3.x, x3.y));
+    };
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const float2 x0 = bf16x2(v[i].x), x1 = bf16x2(v[i].y), x2 = bf16x2(v[i].z), x3 = bf16x2(v[i].w);
-      if (tid + i * GT < vecs)
-        out[i * GT] = make_uint2(e4m3x4(x0.x * mul, x0.y * mul, x1.x * mul, x1.y * mul),
-                                 e4m3x4(x2.x * mul, x2.y * mul, x3.x * mul, x3.y * mul));
+    for (int i = 0; i < VPT; ++i)
+      if (tid + i * GT < vecs) out[i * GT] = quantised(v[i]);
+    if (MORE) {
+#pragma unroll 8
+      for (int e = tid + VPT * GT; e < vecs; e += GT) out[e - tid] = quantised(__ldcs(reinterpret_cast<const uint4*>(vector(e))));
     }
   } else {  // another quantiser's
 #pragma unroll 1
     for (int e = tid; e < vecs; e += GT) {
-      const uint4 u = *reinterpret_cast<const uint4*>(x + (e >> lv) * p.st[which] + ((e & ((1 << lv) - 1)) << 3));
+      const uint4 u = *reinterpret_cast<const uint4*>(vector(e));
       const float2 x0 = bf16x2(u.x), x1 = bf16x2(u.y), x2 = bf16x2(u.z), x3 = bf16x2(u.w);
       out[e - tid] = make_uint2(e4m3x4(x0.x / now, x0.y / now, x1.x / now, x1.y / now),
                                 e4m3x4(x2.x / now, x2.y / now, x3.x / now, x3.y / now));
@@ -206,11 +233,13 @@ int log2_of(int x) {
   return l;
 }
 
-template <int GT, int VPT>
-cudaError_t append_as(const AppendParams& p, int tensors, cudaStream_t st) {
+template <int GT, int VPT, bool MORE = false>
+cudaError_t append_as(AppendParams& p, int tensors, cudaStream_t st) {
   constexpr int CTA = GT > 256 ? GT : 256, GROUPS = CTA / GT;
-  return launch_dependent(append_kernel<GT, VPT>, dim3((unsigned)((p.tasks + GROUPS - 1) / GROUPS), (unsigned)tensors),
-                          dim3(CTA), 0, st, p);
+  const long long heads = (long long)p.B * p.Hkv;
+  p.nx = p.nj >= GROUPS ? (p.nj + GROUPS - 1) / GROUPS : 0;
+  const long long ctas = p.nx ? heads * p.nx : (heads * p.nj + GROUPS - 1) / GROUPS;
+  return launch_dependent(append_kernel<GT, VPT, MORE>, dim3((unsigned)ctas, (unsigned)tensors), dim3(CTA), 0, st, p);
 }
 
 }  // namespace
@@ -244,17 +273,19 @@ cudaError_t launch_cache8_append(const Cache8AppendArgs& a, cudaStream_t st) {
   p.nblk = (a.rows + a.block - 1) / a.block;
   const long long meets = ((long long)a.L + a.block - 2) / a.block + 1;
   p.nj = (int)(meets < p.nblk ? meets : p.nblk);
-  p.tasks = a.B * a.Hkv * p.nj;
-  // the smallest group whose registers hold the new rows that a block can get: 4
-  // vectors a thread leave 8 CTAs an SM, and 8 where a group would pass a CTA
+  // the smallest group whose registers hold the new rows that a block can get: 8
+  // vectors a thread (4 of 256 threads are as fast and more of a short prompt's loads
+  // are under way at once; in smaller groups they are not: 4.8 TB/s and 6.4, for what
+  // a thread does for its block weighs more), 2 of a step's few
   const long long vecs = (long long)(a.L < a.block ? a.L : a.block) * a.D / 8;
+  if (vecs <= 32 * 2) return append_as<32, 2>(p, tensors, st);
   if (vecs <= 32 * 4) return append_as<32, 4>(p, tensors, st);
-  if (vecs <= 64 * 4) return append_as<64, 4>(p, tensors, st);
-  if (vecs <= 128 * 4) return append_as<128, 4>(p, tensors, st);
+  if (vecs <= 32 * 8) return append_as<32, 8>(p, tensors, st);
+  if (vecs <= 64 * 8) return append_as<64, 8>(p, tensors, st);
   if (vecs <= 256 * 4) return append_as<256, 4>(p, tensors, st);
-  if (vecs <= 512 * 4) return append_as<512, 4>(p, tensors, st);
+  if (vecs <= 256 * 8) return append_as<256, 8>(p, tensors, st);
   if (vecs <= 512 * 8) return append_as<512, 8>(p, tensors, st);
-  return append_as<1024, 8>(p, tensors, st);
+  return append_as<512, 8, true>(p, tensors, st);  // 128 rows of 512: half of them once more from L2
 }
 
 cudaError_t launch_cache8_read(const Cache8ReadArgs& a, cudaStream_t st) {
