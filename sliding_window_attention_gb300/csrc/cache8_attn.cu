@@ -179,9 +179,9 @@ struct C8 {
   static constexpr int QB = NS * D;               // a block of queries
   static constexpr int PB = NP * T;               // weights
   // the softmax warps' small arrays: [4][NR] exchanged maxima / sums, references, rescale factors, row ranges, and
-  // the row factors of four visits
+  // the row factors of four visits; the visit's tiles and whether another follows
   static constexpr int RED = 0, REF = 16 * NR, ALPHA = REF + 4 * NR, RNG = ALPHA + 4 * NR, QFAC = RNG + 8 * NR,
-                       SMALL = QFAC + 16 * NR;
+                       PLAN = QFAC + 16 * NR, SMALL = PLAN + 16;
   static constexpr int BARS = 256;
   static constexpr int FIT = (kSmemMax - 1024 - 2 * QB - PB - SMALL - BARS) / SLOT;
   static constexpr int NSLOT = FIT > 4 ? (D == 64 ? 8 : 4) : FIT;
@@ -323,7 +323,9 @@ __device__ __forceinline__ float finish_row(const float* sink, float ref, float 
 
 // Barrier of the four softmax warps; `any`: whether any of their threads says so.
 // Its wait needs no limit: the warps go through all of them whatever their bounded
-// waits on the other roles say.
+// waits on the other roles say, and how often is what one thread says to all (a
+// visit's tiles, whether another follows), so that lengths that a faulty program
+// changes while the kernel runs can make them no different.
 __device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
 __device__ __forceinline__ bool soft_any(bool x) {
   uint32_t r;
@@ -343,8 +345,13 @@ struct Soft {
   uint32_t at;   // TMEM: this thread's lane
   int n;         // tiles so far: S^T(n) is in buffer n & 1
   int visit;
+  int2 plan;     // the visit's tiles, units behind them
   float ks, vs;  // scales of this thread's key of tile n
 };
+__device__ __forceinline__ int2 plan_of(const Walk& w) {  // w at a visit's begin, or behind the run
+  const int tiles = min(w.left, w.nt - w.t);
+  return w.left > 0 ? make_int2(tiles, w.left - tiles) : make_int2(0, 0);
+}
 __device__ __forceinline__ void load_scales(const C8Params& p, const Walk& w, int t, Soft& c) {
   const size_t at = (size_t)w.head() * p.g.nblk + (max(w.key0() + t, 0) >> p.g.lb);
   c.ks = p.ks[at];
@@ -380,18 +387,20 @@ __device__ __forceinline__ void softmax_visit(const C8Params& p, unsigned char* 
   }
   // every row sees the keys from lo_all to hi_all
   const int lo_all = g.W > 0 ? max(0, len - g.W) : 0, hi_all = len - g.Lq;
+  int2* plan = reinterpret_cast<int2*>(small + C::PLAN);
+  if (t == 0) *plan = plan_of(w);
   soft_sync();
+  c.plan = *plan;
 
   uint64_t l_part[NR / 2];  // pairs of rows
   float m_row = kUnset;     // thread t < NR holds row t's reference
 #pragma unroll
   for (int q = 0; q < NR / 2; ++q) l_part[q] = 0;
 
-  bool more = true, fresh = true;
+  bool fresh = true;
 #pragma unroll 1
-  while (more) {
+  for (int k = 0; k < c.plan.x; ++k) {
     const int n = c.n, buf = n & 1, key0 = w.key0();
-    more = !w.last();
     const float vscale = fmaxf(c.vs, cache8_two_to(kCache8LeastExponent)), lv = __log2f(vscale);
     const uint64_t ks2 = f2_pack(c.ks, c.ks), lv2 = f2_pack(lv, lv), iv2 = f2_pack(__fdividef(1.f, vscale), __fdividef(1.f, vscale));
     w.next();
@@ -783,11 +792,15 @@ __global__ void __launch_bounds__(kThr, 2)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar.q_full(0));
     }
+    int2* plan = reinterpret_cast<int2*>(base + C::OFF_SMALL + C::PLAN);
+    if (warp == 4 && lane == 0) *plan = make_int2(0, total);
     tmem_sync();
     tc_fence_after();
     c.at = *tmem_slot + ((uint32_t)(32 * (warp & 3)) << 16);
+    c.plan = *plan;
+    soft_sync();  // (before the first visit's is written)
 #pragma unroll 1
-    while (w.left > 0) softmax_visit<D, NR>(p, base, bar, abort_flag, w, c);
+    while (c.plan.y > 0) softmax_visit<D, NR>(p, base, bar, abort_flag, w, c);
   } else {
     // ------------------------------------------------------------ the later visits' queries
     if (lane == 0) {  // for the merge
