@@ -1050,6 +1050,7 @@ cudaError_t cache8_d(const Cache8Geom& g, const Cache8Args& a, void* ws, int* st
   // both are programmatic dependents of what runs before them: the main grid's
   // set-up and the merge's placement fall into its predecessor's end
   if ((e = launch_dependent(kern, dim3(kCtas), dim3(kThr), C::SMEM, st, tk, tv, p)) != cudaSuccess) return e;
+  if (tiles_most(g) == 1) return cudaSuccess;  // a segment of one tile is not cut
   return launch_dependent(cache8_merge_kernel<D>, dim3(kCtas, kMergeSides), dim3(32 * kMergeWarps), 0, st, p);
 }
 
