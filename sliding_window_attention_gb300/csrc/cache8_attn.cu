@@ -99,15 +99,29 @@ __device__ __forceinline__ int tiles_of(const Cache8Geom& g, int len) {
   return n > lo ? (n - lo + T - 1) / T : 0;
 }
 
-// The runs that a lane's units are cut into (see Cache8Geom), one for each of its
-// CTAs while they last; none is empty.
+// a / b, 0 <= a < 2^31, 0 < b: an estimate, the estimate of what it left, and the
+// last one.  (A part of the integer division's code: what a CTA runs once is fetched
+// at the memory's latency.)
+__device__ __forceinline__ int quotient(int a, int b) {
+  const float inv = __fdividef(1.f, (float)b);
+  int q = (int)((float)a * inv);       // off by 2^-21 of it at most
+  int r = a - q * b;
+  const int d = (int)((float)r * inv);  // of at most 2^10: off by one at most
+  q += d;
+  r -= d * b;
+  return q + (r >= b) - (r < 0);
+}
+
+// The runs that a lane's units are cut into (see Cache8Geom), as equal as whole units
+// are: the first `extra` have one more.  Runs behind the units are empty.
 struct Runs {
-  unsigned units, n;  // (units * kCtas < 2^32)
-  __device__ __forceinline__ unsigned start(unsigned r) const {
-    if (units < n) return min(r, units);
-    return n == kCtas ? r * units / kCtas : r * units / n;
+  int base, extra;
+  __device__ __forceinline__ Runs(int units, int n) : base(quotient(units, n)), extra(units - base * n) {}
+  __device__ __forceinline__ int start(int r) const { return r * base + min(r, extra); }
+  __device__ __forceinline__ int of(int u) const {  // whose unit u is
+    const int wide = extra * (base + 1);
+    return u < wide ? u / (base + 1) : extra + (u - wide) / base;
   }
-  __device__ __forceinline__ unsigned of(unsigned u) const { return units < n ? u : ((u + 1) * n - 1) / units; }  // whose unit u is
 };
 
 // A place in a CTA's run: request, kv head, row block, tile.
@@ -126,10 +140,9 @@ struct Walk {
     b = b0;
     n = min(len, p->g.rows);
     nt = tiles_of(p->g, n);
-    const int in = r / nt;
+    const int in = quotient(r, nt), per = blocks();
     t = r - in * nt;
-    const int per = blocks();
-    h = per == 1 ? in : in / per;
+    h = per == 1 ? in : quotient(in, per);
     blk = lane + p->g.lanes * (in - h * per);
     left = units;
     first = true;
@@ -570,7 +583,7 @@ __device__ __forceinline__ void softmax_visit(const C8Params& p, unsigned char* 
   }
   soft_sync();
   float* mul = alp;  // a whole segment's 1 / sum
-  const size_t slot = (size_t)(2 * blockIdx.x + (c.visit > 1 ? 1 : 0)) * p.orow;
+  const size_t slot = (size_t)(2 * (blockIdx.y * gridDim.x + blockIdx.x) + (c.visit > 1 ? 1 : 0)) * p.orow;
   if (t < rows) {
     const float l = (red[t] + red[NR + t]) + (red[2 * NR + t] + red[3 * NR + t]);
     if (whole) {
@@ -625,7 +638,7 @@ __global__ void __launch_bounds__(kThr, 2)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bar.b + 31);
   float* qfac = reinterpret_cast<float*>(base + C::OFF_SMALL + C::QFAC);
   const Cache8Geom& g = p.g;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, cta = blockIdx.x;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, cta = blockIdx.y * gridDim.x + blockIdx.x;
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
@@ -650,36 +663,34 @@ __global__ void __launch_bounds__(kThr, 2)
   // the request that the run's first unit belongs to
   auto length = [&](int b) { return b < g.B ? p.kv_len[b] : -1; };
   const int len0 = length(lane);  // of the first 32
-  unsigned tiles = tiles_of(g, len0);
+  int tiles = tiles_of(g, len0);
 #pragma unroll 2
   for (int b = lane + 32; b < g.B; b += 32) tiles += tiles_of(g, length(b));
   tiles = __reduce_add_sync(0xffffffffu, tiles);
   Walk first;  // the run's first unit
   first.p = &p;
   first.left = 0;
-  const unsigned run = g.lanes == 1 ? cta : cta / g.lanes;
-  first.lane = cta - (int)run * g.lanes;
-  const unsigned hn = g.Hkv * first.blocks();
-  const Runs runs{tiles * hn, g.lanes == 1 ? kCtas : kCtas / (unsigned)g.lanes};
-  const unsigned u0 = runs.start(run);
-  const int units = run < runs.n ? (int)(runs.start(run + 1) - u0) : 0;
+  first.lane = blockIdx.x;
+  const int hn = g.Hkv * first.blocks();
+  const Runs runs(tiles * hn, gridDim.y);
+  const int u0 = runs.start(blockIdx.y), units = runs.start(blockIdx.y + 1) - u0;
   if (units > 0) {
-    unsigned before = 0;
+    int before = 0;
 #pragma unroll 1
     for (int b0 = 0; b0 < g.B; b0 += 32) {
       const int len = b0 == 0 ? len0 : length(b0 + lane);
-      const unsigned nt = tiles_of(g, len);
-      unsigned inc = nt;
+      const int nt = tiles_of(g, len);
+      int inc = nt;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const unsigned v = __shfl_up_sync(0xffffffffu, inc, o);
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += v;
       }
       const unsigned here = __ballot_sync(0xffffffffu, u0 < (before + inc) * hn);
       if (here) {
         const int l = __ffs(here) - 1;
-        const unsigned at = before + __shfl_sync(0xffffffffu, inc - nt, l);
-        first.begin(b0 + l, __shfl_sync(0xffffffffu, len, l), (int)(u0 - at * hn), units);
+        const int at = before + __shfl_sync(0xffffffffu, inc - nt, l);
+        first.begin(b0 + l, __shfl_sync(0xffffffffu, len, l), u0 - at * hn, units);
         break;
       }
       before += __shfl_sync(0xffffffffu, inc, 31);
@@ -806,9 +817,8 @@ __global__ void __launch_bounds__(kThr, 2)
     if (lane == 0) {  // for the merge
       int4 cut = make_int4(-1, 0, 0, 0);
       if (total > 0 && first.t > 0) {
-        const unsigned begin = u0 - first.t;
-        const int c0 = (int)runs.of(begin);
-        cut = make_int4(first.head() * g.nmb + first.blk, (int)runs.of(begin + first.nt - 1) - c0 + 1,
+        const int begin = u0 - first.t, c0 = runs.of(begin);
+        cut = make_int4(first.head() * g.nmb + first.blk, runs.of(begin + first.nt - 1) - c0 + 1,
                         c0 * g.lanes + first.lane,
                         2 * (c0 * g.lanes + first.lane) + (runs.start(c0) == begin ? 0 : 1));
       }
@@ -839,7 +849,7 @@ __global__ void __launch_bounds__(kThr, 2)
     }
     // requests without a key: no unit is theirs
 #pragma unroll 1
-    for (int b = cta; b < g.B; b += kCtas) {
+    for (int b = cta; b < g.B; b += gridDim.x * gridDim.y) {
       const int len = p.kv_len[b];
       if (len < 0 || tiles_of(g, len) > 0) continue;
       const size_t at = (size_t)b * g.Hkv * g.M;
@@ -1047,11 +1057,12 @@ cudaError_t cache8_d(const Cache8Geom& g, const Cache8Args& a, void* ws, int* st
   auto kern = cache8_kernel<D, NR>;
   static std::atomic<unsigned long long> done{0};
   if ((e = allow_smem(kern, (int)C::SMEM, done)) != cudaSuccess) return e;
+  const dim3 grid((unsigned)g.lanes, (unsigned)(kCtas / g.lanes));  // a run's lanes are neighbours
   // both are programmatic dependents of what runs before them: the main grid's
   // set-up and the merge's placement fall into its predecessor's end
-  if ((e = launch_dependent(kern, dim3(kCtas), dim3(kThr), C::SMEM, st, tk, tv, p)) != cudaSuccess) return e;
+  if ((e = launch_dependent(kern, grid, dim3(kThr), C::SMEM, st, tk, tv, p)) != cudaSuccess) return e;
   if (tiles_most(g) == 1) return cudaSuccess;  // a segment of one tile is not cut
-  return launch_dependent(cache8_merge_kernel<D>, dim3(kCtas, kMergeSides), dim3(32 * kMergeWarps), 0, st, p);
+  return launch_dependent(cache8_merge_kernel<D>, dim3(grid.x * grid.y, kMergeSides), dim3(32 * kMergeWarps), 0, st, p);
 }
 
 template <int D>
@@ -1065,10 +1076,10 @@ cudaError_t cache8_nr(const Cache8Geom& g, const Cache8Args& a, void* ws, int* s
 
 }  // namespace
 
-// Units (tiles of all segments) times runs within 32 bits.
+// Units (tiles of all segments) within 32 bits.
 bool cache8_fits(const Cache8Geom& g) {
   const double units = (double)g.B * g.Hkv * g.nmb * ((g.rows + T - 1) / T);
-  return units * kCtas < 4.0e9 && (double)g.B * g.Hkv * g.M < 1.0e9;
+  return units < 2.0e9 && (double)g.B * g.Hkv * g.M < 1.0e9;
 }
 // Query rows of a block.  Up to 8 rows take half the softmax of 16 (the 49.1 us above
 // are 56.8 with 16; D = 128, 44.3 and 45.9).  A tile costs blocks of 32 twice that of 16,
