@@ -401,9 +401,12 @@ int swa_attn_cache8_read(const uint8_t* k_cache, const uint8_t* v_cache, const f
  * and 2^-27 of the row's largest weight for those below).  Products are summed
  * in fp32, as are the row sums and the partial outputs; o is rounded to bf16
  * once.  Within a request and head the values' scales that matter may lie up to
- * 2^100 apart.  Scales are positive and finite; of rows within the lengths they
- * and the codes must not be NaN, whatever stands behind is not used.  Many
- * query rows a kv head (Hq / Hkv * Lq) read the cache once for each 16 of them.
+ * 2^100 apart; a value's scale below 2^-64 (the append writes none) counts as
+ * 2^-64.  Scales are positive and finite; of rows within the lengths they
+ * and the codes must not be NaN, whatever stands behind is not used.  The
+ * Hq / Hkv * Lq query rows of a kv head are taken in blocks of up to 8, 16 or 32,
+ * each of which multiplies the whole cache (side by side, so that L2 serves all
+ * but the first): a prompt's next chunk is better read back.
  * The result does not depend on what else runs, but it does on the other
  * requests' lengths, in its last bits: they move the places where the key
  * ranges are split.  Equal calls give equal bits.

@@ -38,14 +38,14 @@
 // reach past it starts earlier (below key 0 the TMA fills zeros), so nothing
 // behind a request's length is loaded.
 //
-// Bounds.  Long caches by HBM: 32 requests of up to 16,384 tokens, D = 512, 153.7 us,
-// 7.0 TB/s of cache; 64 of up to 8,192, D = 128, 44.3 us, 6.1 TB/s, of which some 8
+// Bounds.  Long caches by HBM: 32 requests of up to 16,384 tokens, D = 512, 151 us,
+// 7.1 TB/s of cache; 64 of up to 8,192, D = 128, 43.5 us, 6.2 TB/s, of which some 8
 // are not the stream's: 1.0 lengths and split, 3 until the first tiles are there,
 // 1 from the last tile's arrival to a run's end, 1.0 until the merge may begin, 1.6
 // merge, 0.5 until the next call's lengths.  Those are what a short call takes (4
-// requests of up to 1,024, D = 128: 7.3 us, and as much on the host).  At D = 64 the
+// requests of up to 1,024, D = 128: 7.8 us, and as much on the host).  At D = 64 the
 // softmax of a tile, 0.7 us of a CTA for 8 rows, is as long as its stream (64
-// requests of 16 / 2 heads over 16,384 keys: 49.1 us, 5.5 TB/s; three CTAs an SM,
+// requests of 16 / 2 heads over 16,384 keys: 48.5 us, 5.5 TB/s; three CTAs an SM,
 // 46.2 us, would cost the other head dims 1 to 4 us).
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -1081,8 +1081,8 @@ bool cache8_fits(const Cache8Geom& g) {
   const double units = (double)g.B * g.Hkv * g.nmb * ((g.rows + T - 1) / T);
   return units < 2.0e9 && (double)g.B * g.Hkv * g.M < 1.0e9;
 }
-// Query rows of a block.  Up to 8 rows take half the softmax of 16 (the 49.1 us above
-// are 56.8 with 16; D = 128, 44.3 and 45.9).  A tile costs blocks of 32 twice that of 16,
+// Query rows of a block.  Up to 8 rows take half the softmax of 16 (the 48.5 us above
+// are 56.8 with 16; D = 128, 43.5 and 45.9).  A tile costs blocks of 32 twice that of 16,
 // and they read it once where two of 16 both do, one of them from L2.  At D = 256 and
 // 512, where HBM is what bounds the calls, that is as fast (16 requests of 32 rows
 // over 5,120 keys, D = 256: 33.5 us, and 36.9 with 32; 32 requests over 8,192: 88.6
