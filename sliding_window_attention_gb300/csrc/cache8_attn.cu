@@ -650,50 +650,60 @@ __global__ void __launch_bounds__(kThr, 2)
     fence_mbar_init();
   }
   __syncthreads();
-  grid_dependency_wait();
-  // Tensor memory is taken after the predecessor's end and before a dependent
-  // may be placed: a grid that held columns while it waits for another that has
-  // yet to allocate its own, on the same SM, would wait for ever.
-  if (warp == 1) {
-    tmem_alloc(tmem_slot, C::TCOLS);
-    tmem_relinquish();
-    grid_launch_dependents();  // the merge waits for this grid's end
-  }
   // ---- this CTA's run, by every warp for itself: the tiles of all requests, then
-  // the request that the run's first unit belongs to
-  auto length = [&](int b) { return b < g.B ? p.kv_len[b] : -1; };
-  const int len0 = length(lane);  // of the first 32
-  int tiles = tiles_of(g, len0);
-#pragma unroll 2
-  for (int b = lane + 32; b < g.B; b += 32) tiles += tiles_of(g, length(b));
-  tiles = __reduce_add_sync(0xffffffffu, tiles);
+  // the request that the run's first unit belongs to.  Gone through twice, first as if
+  // all requests were full: code that a CTA runs once is fetched at the memory's
+  // latency, and there is time before the predecessor's end.
   Walk first;  // the run's first unit
   first.p = &p;
-  first.left = 0;
   first.lane = blockIdx.x;
   const int hn = g.Hkv * first.blocks();
-  const Runs runs(tiles * hn, gridDim.y);
-  const int u0 = runs.start(blockIdx.y), units = runs.start(blockIdx.y + 1) - u0;
-  if (units > 0) {
-    int before = 0;
+  Runs runs(0, 1);
+  int u0 = 0;
 #pragma unroll 1
-    for (int b0 = 0; b0 < g.B; b0 += 32) {
-      const int len = b0 == 0 ? len0 : length(b0 + lane);
-      const int nt = tiles_of(g, len);
-      int inc = nt;
+  for (int pass = 0; pass < 2; ++pass) {
+    if (pass) {
+      grid_dependency_wait();
+      // Tensor memory is taken after the predecessor's end and before a dependent
+      // may be placed: a grid that held columns while it waits for another that has
+      // yet to allocate its own, on the same SM, would wait for ever.
+      if (warp == 1) {
+        tmem_alloc(tmem_slot, C::TCOLS);
+        tmem_relinquish();
+        grid_launch_dependents();  // the merge waits for this grid's end
+      }
+    }
+    auto length = [&](int b) { return b >= g.B ? -1 : pass ? p.kv_len[b] : g.rows; };
+    const int len0 = length(lane);  // of the first 32
+    int tiles = tiles_of(g, len0);
+#pragma unroll 1
+    for (int b = lane + 32; b < g.B; b += 32) tiles += tiles_of(g, length(b));
+    tiles = __reduce_add_sync(0xffffffffu, tiles);
+    first.left = 0;
+    runs = Runs(tiles * hn, gridDim.y);
+    u0 = runs.start(blockIdx.y);
+    const int units = runs.start(blockIdx.y + 1) - u0;
+    if (units > 0) {
+      int before = 0;
+#pragma unroll 1
+      for (int b0 = 0; b0 < g.B; b0 += 32) {
+        const int len = b0 == 0 ? len0 : length(b0 + lane);
+        const int nt = tiles_of(g, len);
+        int inc = nt;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += v;
+        }
+        const unsigned here = __ballot_sync(0xffffffffu, u0 < (before + inc) * hn);
+        if (here) {
+          const int l = __ffs(here) - 1;
+          const int at = before + __shfl_sync(0xffffffffu, inc - nt, l);
+          first.begin(b0 + l, __shfl_sync(0xffffffffu, len, l), u0 - at * hn, units);
+          break;
+        }
+        before += __shfl_sync(0xffffffffu, inc, 31);
       }
-      const unsigned here = __ballot_sync(0xffffffffu, u0 < (before + inc) * hn);
-      if (here) {
-        const int l = __ffs(here) - 1;
-        const int at = before + __shfl_sync(0xffffffffu, inc - nt, l);
-        first.begin(b0 + l, __shfl_sync(0xffffffffu, len, l), u0 - at * hn, units);
-        break;
-      }
-      before += __shfl_sync(0xffffffffu, inc, 31);
     }
   }
   const int total = first.left;
