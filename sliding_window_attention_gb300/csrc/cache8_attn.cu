@@ -23,7 +23,10 @@
 // Products are transposed: S^T (128 keys x 2 N) = K_tile [a b]^T and O^T (D x 3 N) +=
 // V_tile^T [hi mid lo]^T, so that the keys fill the MMA's M dimension whatever the
 // number of query rows is.  A block has up to N = 8, 16 or 32 of the G * Lq rows of a
-// kv head; a softmax thread has one key of the tile.
+// kv head; a softmax thread has one key of the tile and 8 rows at a time.  Blocks of 16
+// and 32 have two groups of four softmax warps, each with half of the rows and with
+// barriers of its own, so that one works while the other waits (32 requests over up to
+// 8,192 keys, D = 128, N = 32: 47.7 us, and 50.4 with one group).
 //
 // Work.  The unit is one tile of 128 keys of one segment (request, kv head, row
 // block).  The units of all requests, by the device-side lengths, are cut into
@@ -66,7 +69,6 @@ using namespace tc;
 
 constexpr int T = 128;       // keys per tile
 constexpr int kCtas = 304;   // two an SM
-constexpr int kThr = 224;    // TMA, MMA, four softmax warps, one that prepares queries
 constexpr int kSmemMax = 115584;  // dynamic, a CTA: half of an SM's 228 KB less 1 KB that the system keeps and the static
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -183,18 +185,22 @@ struct Walk {
 // The kernel with blocks of NR query rows: 8, 16, or 32 at D <= 128.
 template <int D, int NR>
 struct C8 {
-  static constexpr int HR = NR < 16 ? NR : 16;    // rows that a softmax thread has in registers at a time
-  static constexpr int NS = 2 * NR;               // columns of S^T: q's two parts
-  static constexpr int NP = (3 * NR + 15) / 16 * 16;  // of O^T: a weight's three, part i's row r in column NR i + r
+  static constexpr int GROUPS = NR > 8 ? 2 : 1;   // of four softmax warps, each with a part of the rows:
+  static constexpr int NH = NR / 8 / GROUPS;      // so many eights, one after the other
+  // warps: TMA, MMA, softmax, and those that prepare queries (rows of 512: one warp is 40.1 us where two are 36.4, 16
+  // requests of 32 rows over up to 4,096 keys); two CTAs of 12 warps have 80 registers a thread
+  static constexpr int HELPER = 2 + 4 * GROUPS, HELPERS = GROUPS, THR = 32 * (HELPER + HELPERS);
+  static constexpr int NS = 2 * NR;               // columns of S^T: 8 rows' q in its first part, then in its second
+  static constexpr int NP = NR > 8 ? 3 * NR : 32; // of O^T: weights' three parts (see o_col)
   static constexpr int LINE = D < 128 ? D : 128;  // bytes of a key's line in a slot
   static constexpr int NCH = D / LINE;            // slots per tile and tensor; 128-row blocks of O^T
   static constexpr int SLOT = T * LINE;
   static constexpr int QB = NS * D;               // a block of queries
   static constexpr int PB = NP * T;               // weights
-  // the softmax warps' small arrays: [4][NR] exchanged maxima / sums, references, rescale factors, row ranges, and
-  // the row factors of four visits; the visit's tiles and whether another follows
-  static constexpr int RED = 0, REF = 16 * NR, ALPHA = REF + 4 * NR, RNG = ALPHA + 4 * NR, QFAC = RNG + 8 * NR,
-                       PLAN = QFAC + 16 * NR, SMALL = PLAN + 16;
+  // the softmax groups' small arrays: [4][8] exchanged maxima / sums, references, rescale factors, row ranges, the
+  // visit's tiles and whether another follows; and the row factors of four visits
+  static constexpr int RED = 0, REF = 128 * NH, ALPHA = REF + 32 * NH, RNG = ALPHA + 32 * NH, PLAN = RNG + 64 * NH, SOFT = PLAN + 16,
+                       QFAC = GROUPS * SOFT, SMALL = QFAC + 16 * NR;
   static constexpr int BARS = 256;
   static constexpr int FIT = (kSmemMax - 1024 - 2 * QB - PB - SMALL - BARS) / SLOT;
   static constexpr int NSLOT = FIT > 4 ? (D == 64 ? 8 : 4) : FIT;
@@ -206,6 +212,11 @@ struct C8 {
   static_assert(COLS <= 256, "TMEM columns");
   static_assert(NSLOT >= 3 && SMEM <= (size_t)kSmemMax, "shared memory");
 };
+
+// Columns of an eight's weights (and of their products): the first two parts, and 16 for
+// the third parts of two eights between them.
+__device__ __forceinline__ int o_col(int eight) { return 48 * (eight >> 1) + 32 * (eight & 1); }
+__device__ __forceinline__ int lo_col(int eight) { return 48 * (eight >> 1) + 16 + 8 * (eight & 1); }
 
 // Barriers (words from OFF_BAR on).
 struct Bars {
@@ -219,7 +230,9 @@ struct Bars {
   __device__ __forceinline__ uint64_t* o_done() const { return b + 23; }              // the second product finished
   __device__ __forceinline__ uint64_t* drain() const { return b + 24; }
   static constexpr int kCount = 25;
-  static __device__ __forceinline__ int arrivals(int i) { return i == 16 || i == 17 || i == 22 ? 4 : 1; }
+  static __device__ __forceinline__ int arrivals(int i, int groups) {
+    return i == 16 || i == 17 || i == 22 ? 4 * groups : 1;
+  }
 };
 
 // Shared-memory matrix descriptors: layout 2 is the 128-byte swizzle, 4 the 64-byte one, 0 none.
@@ -252,13 +265,13 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
   return false;
 }
 
-// Column reduction of HR columns over the warp's lanes by halving, into dst[0 .. HR - 1].
-template <int HR, bool MAX>
-__device__ __forceinline__ void column_reduce(float (&v)[HR], float* dst, int lane) {
+// Column reduction of 8 columns over the warp's lanes by halving, into dst[0 .. 7].
+template <bool MAX>
+__device__ __forceinline__ void column_reduce(float (&v)[8], float* dst, int lane) {
   auto op = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
   int o = 16;
 #pragma unroll
-  for (int h = HR / 2; h >= 1; h >>= 1, o >>= 1) {
+  for (int h = 4; h >= 1; h >>= 1, o >>= 1) {
     const bool up = lane & o;
 #pragma unroll
     for (int i = 0; i < h; ++i) {
@@ -268,12 +281,12 @@ __device__ __forceinline__ void column_reduce(float (&v)[HR], float* dst, int la
   }
 #pragma unroll
   for (; o >= 1; o >>= 1) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
-  if (lane % (32 / HR) == 0) dst[lane / (32 / HR)] = v[0];
+  if (lane % 4 == 0) dst[lane / 4] = v[0];
 }
 
 // Queries of one visit as the B operand of the first product: rows 4 w .. 4 w + 3
-// of the block by one warp, eight lanes a row; row r's parts go to rows r and
-// NR + r, and its factor (what its scores are multiplied with, but for the keys'
+// of the block by one warp, eight lanes a row; row r's parts go to columns 16 (r / 8)
+// + r % 8 and 8 further, and its factor (what its scores are multiplied with, but for the keys'
 // scales) to fac[r].  Rows from `rows` on are zero.
 template <int D, int NR>
 __device__ __forceinline__ void prepare_queries(const C8Params& p, int head, int blk, int rows, unsigned char* dst,
@@ -316,8 +329,8 @@ __device__ __forceinline__ void prepare_queries(const C8Params& p, int head, int
       const int turn = D < 128 ? (row >> 1) & 3 : row & 7;
       *reinterpret_cast<uint2*>(d + row * LINE + (((at >> 4) ^ turn) << 4)) = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
     };
-    put(r, hi);
-    put(NR + r, lo);
+    put(r + (r & ~7), hi);
+    put(r + (r & ~7) + 8, lo);
   }
   if (l8 == 0) fac[r] = fabsf(p.g.scale) * kLog2e * cache8_two_to(e);
   fence_proxy_async_smem();
@@ -334,24 +347,32 @@ __device__ __forceinline__ float finish_row(const float* sink, float ref, float 
   return 1.f / l;
 }
 
-// Barrier of the four softmax warps; `any`: whether any of their threads says so.
+// Barrier of a group's four softmax warps; `any`: whether any of their threads says so.
 // Its wait needs no limit: the warps go through all of them whatever their bounded
 // waits on the other roles say, and how often is what one thread says to all (a
 // visit's tiles, whether another follows), so that lengths that a faulty program
 // changes while the kernel runs can make them no different.
-__device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
-__device__ __forceinline__ bool soft_any(bool x) {
+__device__ __forceinline__ void soft_sync(int group) {
+  if (group == 0) asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
+  else asm volatile("barrier.cta.sync 3, 128;" ::: "memory");
+}
+template <int ID>
+__device__ __forceinline__ bool any_of(bool x) {
   uint32_t r;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, "
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, "
       "q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)x)
+      : "r"((uint32_t)x), "n"(ID)
       : "memory");
   return r != 0;
 }
+__device__ __forceinline__ bool soft_any(int group, bool x) { return group == 0 ? any_of<1>(x) : any_of<3>(x); }
 // The MMA warp has tensor memory, for itself and the softmax warps.
-__device__ __forceinline__ void tmem_sync() { asm volatile("barrier.cta.sync 2, 160;" ::: "memory"); }
+template <int THR>
+__device__ __forceinline__ void tmem_sync() {
+  asm volatile("barrier.cta.sync 2, %0;" ::"n"(THR) : "memory");
+}
 
 // The softmax warps' state over a run.
 struct Soft {
@@ -378,21 +399,22 @@ template <int D, int NR>
 __device__ __forceinline__ void softmax_visit(const C8Params& p, unsigned char* base, const Bars& bar,
                                               volatile int* abort, Walk& w, Soft& c) {
   using C = C8<D, NR>;
-  constexpr int HR = C::HR, NH = NR / HR, NP = C::NP;
+  constexpr int NP = C::NP, NH = C::NH, R = 8 * NH;
   const Cache8Geom& g = p.g;
   const int lane = threadIdx.x & 31, q4 = (threadIdx.x >> 5) & 3, t = 32 * q4 + lane;
-  unsigned char* small = base + C::OFF_SMALL;
+  const int group = C::GROUPS == 1 ? 0 : threadIdx.x >= 192, r0 = R * group;  // the group's rows: r0 .. r0 + R - 1 of the block's
+  unsigned char* small = base + C::OFF_SMALL + group * C::SOFT;
   float* red = reinterpret_cast<float*>(small + C::RED);
   float* nref = reinterpret_cast<float*>(small + C::REF);  // the references' negatives
   float* alp = reinterpret_cast<float*>(small + C::ALPHA);
   int2* rng = reinterpret_cast<int2*>(small + C::RNG);
-  const float* fac = reinterpret_cast<const float*>(small + C::QFAC) + (c.visit & 3) * NR;
-  const int blk = w.blk, head = w.head(), len = w.n, rows = min(NR, g.M - blk * NR);
+  const float* fac = reinterpret_cast<const float*>(base + C::OFF_SMALL + C::QFAC) + (c.visit & 3) * NR + r0;
+  const int blk = w.blk, head = w.head(), len = w.n, row0 = blk * NR + r0, rows = min(R, g.M - row0);  // (rows < 1: none)
   const bool whole = w.t == 0 && w.left >= w.nt;  // the visit is of the whole segment
-  if (t < NR) {  // row t's visible keys; rows that are no query mask nothing: their columns are never read
+  if (t < R) {  // row t's visible keys; rows that are no query mask nothing: their columns are never read
     int lo = 0, hi = INT32_MAX;
     if (t < rows) {
-      hi = len - g.Lq + (g.Lq > 1 ? (blk * NR + t) % g.Lq : 0);
+      hi = len - g.Lq + (g.Lq > 1 ? (row0 + t) % g.Lq : 0);
       lo = g.W > 0 ? max(0, hi - g.W + 1) : 0;
     }
     rng[t] = make_int2(lo, hi);
@@ -402,13 +424,13 @@ __device__ __forceinline__ void softmax_visit(const C8Params& p, unsigned char* 
   const int lo_all = g.W > 0 ? max(0, len - g.W) : 0, hi_all = len - g.Lq;
   int2* plan = reinterpret_cast<int2*>(small + C::PLAN);
   if (t == 0) *plan = plan_of(w);
-  soft_sync();
+  soft_sync(group);
   c.plan = *plan;
 
-  uint64_t l_part[NR / 2];  // pairs of rows
-  float m_row = kUnset;     // thread t < NR holds row t's reference
+  uint64_t l_part[R / 2];  // pairs of rows
+  float m_row = kUnset;    // thread t < R holds row t's reference
 #pragma unroll
-  for (int q = 0; q < NR / 2; ++q) l_part[q] = 0;
+  for (int q = 0; q < R / 2; ++q) l_part[q] = 0;
 
   bool fresh = true;
 #pragma unroll 1
@@ -423,31 +445,29 @@ __device__ __forceinline__ void softmax_visit(const C8Params& p, unsigned char* 
     __syncwarp();
     tc_fence_after();
 #pragma unroll
-    for (int hf = 0; hf < NH; ++hf) {  // 16 rows from row HR * hf on
-      uint32_t sa[16], sb[16];
-      tmem_ld16(c.at + C::S_COL + C::NS * buf + HR * hf, sa);
-      if (NR > 8) tmem_ld16(c.at + C::S_COL + C::NS * buf + NR + HR * hf, sb);
+    for (int hf = 0; hf < NH; ++hf) {  // 8 rows
+      uint32_t sc[16];  // 8 rows' products with the first part of q, then with the second
+      tmem_ld16(c.at + C::S_COL + C::NS * buf + 16 * (NH * group + hf), sc);
       tmem_wait_ld();
-      const uint32_t *hi = sa, *lo = NR > 8 ? sb : sa + 8;
-      uint64_t y[HR / 2], z[HR / 2];
+      uint64_t y[4], z[4];
       const uint64_t small16 = f2_pack(0.0625f, 0.0625f);
 #pragma unroll
-      for (int q = 0; q < HR / 2; q += 2) {
-        const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(fac + HR * hf + 2 * q);
+      for (int q = 0; q < 4; q += 2) {
+        const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(fac + 8 * hf + 2 * q);
         const uint64_t ff[2] = {f.x, f.y};
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int r = 2 * (q + i);
-          const uint64_t a = f2_pack(__uint_as_float(hi[r]), __uint_as_float(hi[r + 1]));
-          const uint64_t b = f2_pack(__uint_as_float(lo[r]), __uint_as_float(lo[r + 1]));
+          const uint64_t a = f2_pack(__uint_as_float(sc[r]), __uint_as_float(sc[r + 1]));
+          const uint64_t b = f2_pack(__uint_as_float(sc[8 + r]), __uint_as_float(sc[9 + r]));
           y[q + i] = f2_fma(f2_fma(b, small16, a), f2_mul(ff[i], ks2), lv2);
         }
       }
       if (edge) {
         const int key = key0 + t;
 #pragma unroll
-        for (int q = 0; q < HR / 2; ++q) {
-          const int4 r = *reinterpret_cast<const int4*>(rng + HR * hf + 2 * q);
+        for (int q = 0; q < 4; ++q) {
+          const int4 r = *reinterpret_cast<const int4*>(rng + 8 * hf + 2 * q);
           float2 v = f2_unpack(y[q]);
           if (key < r.x || key > r.y) v.x = -INFINITY;
           if (key < r.z || key > r.w) v.y = -INFINITY;
@@ -456,8 +476,8 @@ __device__ __forceinline__ void softmax_visit(const C8Params& p, unsigned char* 
       }
       auto less_reference = [&]() {  // z = y - reference
 #pragma unroll
-        for (int q = 0; q < HR / 2; q += 2) {
-          const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(nref + HR * hf + 2 * q);
+        for (int q = 0; q < 4; q += 2) {
+          const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(nref + 8 * hf + 2 * q);
           z[q] = f2_add(y[q], f.x);
           z[q + 1] = f2_add(y[q + 1], f.y);
         }
@@ -467,26 +487,26 @@ __device__ __forceinline__ void softmax_visit(const C8Params& p, unsigned char* 
         less_reference();
         float over = -INFINITY;
 #pragma unroll
-        for (int q = 0; q < HR / 2; ++q) {
+        for (int q = 0; q < 4; ++q) {
           const float2 v = f2_unpack(z[q]);
           over = fmax3(over, v.x, v.y);
         }
-        grow = soft_any(over > kTop);
+        grow = soft_any(group, over > kTop);
       }
       if (grow) {  // some weight passes the top, or the visit begins
-        float mx[HR];
+        float mx[8];
 #pragma unroll
-        for (int q = 0; q < HR / 2; ++q) {
+        for (int q = 0; q < 4; ++q) {
           const float2 v = f2_unpack(y[q]);
           mx[2 * q] = v.x;
           mx[2 * q + 1] = v.y;
         }
-        column_reduce<HR, true>(mx, red + q4 * HR, lane);
-        soft_sync();
+        column_reduce<true>(mx, red + q4 * 8, lane);
+        soft_sync(group);
         bool moved = false;
-        const int i = t - HR * hf;
-        if (i >= 0 && i < HR) {
-          const float tm = fmaxf(fmaxf(red[i], red[HR + i]), fmaxf(red[2 * HR + i], red[3 * HR + i]));
+        const int i = t - 8 * hf;
+        if (i >= 0 && i < 8) {
+          const float tm = fmaxf(fmaxf(red[i], red[8 + i]), fmaxf(red[16 + i], red[24 + i]));
           float a = 1.f;
           if (tm - m_row > kTop) {  // (a row without a key yet: its reference is the lowest number)
             const float to = tm - kBelow;
@@ -499,22 +519,25 @@ __device__ __forceinline__ void softmax_visit(const C8Params& p, unsigned char* 
           }
           alp[t] = a;
         }
-        if (soft_any(moved)) {  // sums and O^T of these rows move with their references
+        if (soft_any(group, moved)) {  // sums and O^T of these rows move with their references
 #pragma unroll
-          for (int q = 0; q < HR / 2; ++q)
-            l_part[HR / 2 * hf + q] = f2_mul(l_part[HR / 2 * hf + q], *reinterpret_cast<const uint64_t*>(alp + HR * hf + 2 * q));
+          for (int q = 0; q < 4; ++q) l_part[4 * hf + q] = f2_mul(l_part[4 * hf + q], *reinterpret_cast<const uint64_t*>(alp + 8 * hf + 2 * q));
           wait(bar.o_done(), (n - 1) & 1, abort);  // (the row has earlier keys: n > 0)
           __syncwarp();
           tc_fence_after();
 #pragma unroll 1
-          for (int j = 0; j < (NR > 8 ? 3 : 2) * C::NCH; ++j) {
-            const uint32_t at = c.at + C::O_COL + (NR > 8 ? NR : 16) * j + HR * hf;
-            uint32_t ov[16];
-            tmem_ld16(at, ov);
+          for (int j = 0; j < C::NCH; ++j) {
+            const uint32_t at = c.at + C::O_COL + NP * j;
+            uint32_t ov[16], ow[8];
+            tmem_ld16(at + o_col(NH * group + hf), ov);
+            tmem_ld8(at + lo_col(NH * group + hf), ow);
             tmem_wait_ld();
 #pragma unroll
-            for (int q = 0; q < 16; ++q) ov[q] = __float_as_uint(__uint_as_float(ov[q]) * alp[HR * hf + q % HR]);
-            tmem_st16(at, ov);
+            for (int q = 0; q < 16; ++q) ov[q] = __float_as_uint(__uint_as_float(ov[q]) * alp[8 * hf + q % 8]);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) ow[q] = __float_as_uint(__uint_as_float(ow[q]) * alp[8 * hf + q]);
+            tmem_st16(at + o_col(NH * group + hf), ov);
+            tmem_st8(at + lo_col(NH * group + hf), ow);
           }
           tmem_wait_st();
         }
@@ -522,15 +545,15 @@ __device__ __forceinline__ void softmax_visit(const C8Params& p, unsigned char* 
       }
       // the weights 2^(y - reference), their row sums, and their three parts: hi is
       // a weight in fp16 rounded to its top byte, mid the rest so, lo the rest of that
-      uint32_t part[3][HR / 4];
+      uint32_t part[3][2];
 #pragma unroll
-      for (int q = 0; q < HR / 2; q += 2) {
+      for (int q = 0; q < 4; q += 2) {
         float2 e = f2_unpack(z[q]), f = f2_unpack(z[q + 1]);
         e.x = fast_exp2(e.x);
         e.y = fast_exp2(e.y);
         f.x = fast_exp2(f.x);
         f.y = fast_exp2(f.y);
-        uint64_t* l = l_part + HR / 2 * hf + q;
+        uint64_t* l = l_part + 4 * hf + q;
         l[0] = f2_fma(f2_pack(e.x, e.y), iv2, l[0]);
         l[1] = f2_fma(f2_pack(f.x, f.y), iv2, l[1]);
         uint32_t a = pack_half2(e.x, e.y), b = pack_half2(f.x, f.y);
@@ -549,16 +572,11 @@ __device__ __forceinline__ void softmax_visit(const C8Params& p, unsigned char* 
       }
       // the second product of tile n - 1 has finished with the weights' buffer
       if (hf == 0 && n > 0) wait(bar.o_done(), (n - 1) & 1, abort);
-      // MN-major operand without swizzle: 16 columns of a key are 16 bytes
-      unsigned char* pb = base + C::OFF_P + (hf * T + t) * 16;
-      if constexpr (NR > 8) {
-#pragma unroll
-        for (int i = 0; i < 3; ++i)
-          *reinterpret_cast<uint4*>(pb + i * T * NR) = make_uint4(part[i][0], part[i][1], part[i][2], part[i][3]);
-      } else {
-        *reinterpret_cast<uint4*>(pb) = make_uint4(part[0][0], part[0][1], part[1][0], part[1][1]);
-        *reinterpret_cast<uint4*>(pb + T * 16) = make_uint4(part[2][0], part[2][1], 0, 0);
-      }
+      // MN-major operand without swizzle: 16 columns of a key are 16 bytes.  (Columns
+      // of rows that the block has not are multiplied as they are and never read.)
+      unsigned char* pb = base + C::OFF_P + t * 16;
+      *reinterpret_cast<uint4*>(pb + o_col(NH * group + hf) * T) = make_uint4(part[0][0], part[0][1], part[1][0], part[1][1]);
+      *reinterpret_cast<uint2*>(pb + lo_col(NH * group + hf) / 16 * T * 16 + lo_col(NH * group + hf) % 16) = make_uint2(part[2][0], part[2][1]);
     }
     fresh = false;
     fence_proxy_async_smem();  // generic writes -> the tensor core's reads
@@ -572,22 +590,22 @@ __device__ __forceinline__ void softmax_visit(const C8Params& p, unsigned char* 
   // row sums over the 128 threads, then O^T
 #pragma unroll
   for (int hf = 0; hf < NH; ++hf) {
-    float l[HR];
+    float l[8];
 #pragma unroll
-    for (int q = 0; q < HR / 2; ++q) {
-      const float2 v = f2_unpack(l_part[HR / 2 * hf + q]);
+    for (int q = 0; q < 4; ++q) {
+      const float2 v = f2_unpack(l_part[4 * hf + q]);
       l[2 * q] = v.x;
       l[2 * q + 1] = v.y;
     }
-    column_reduce<HR, false>(l, red + q4 * NR + HR * hf, lane);
+    column_reduce<false>(l, red + q4 * R + 8 * hf, lane);
   }
-  soft_sync();
+  soft_sync(group);
   float* mul = alp;  // a whole segment's 1 / sum
-  const size_t slot = (size_t)(2 * (blockIdx.y * gridDim.x + blockIdx.x) + (c.visit > 1 ? 1 : 0)) * p.orow;
+  const size_t slot = (size_t)(2 * (blockIdx.y * gridDim.x + blockIdx.x) + (c.visit > 1 ? 1 : 0)) * p.orow + r0;
   if (t < rows) {
-    const float l = (red[t] + red[NR + t]) + (red[2 * NR + t] + red[3 * NR + t]);
+    const float l = (red[t] + red[R + t]) + (red[2 * R + t] + red[3 * R + t]);
     if (whole) {
-      const int m = blk * NR + t;
+      const int m = row0 + t;
       float lse;
       mul[t] = finish_row(p.sinks ? p.sinks + (head % g.Hkv) * g.G + m / g.Lq : nullptr, m_row, l, &lse);
       p.lse[(size_t)head * g.M + m] = lse;
@@ -595,29 +613,27 @@ __device__ __forceinline__ void softmax_visit(const C8Params& p, unsigned char* 
       *reinterpret_cast<float2*>(p.ml + 2 * (slot + t)) = make_float2(m_row, l);
     }
   }
-  soft_sync();
+  soft_sync(group);
   wait(bar.o_done(), (c.n - 1) & 1, abort);
   __syncwarp();
   tc_fence_after();
 #pragma unroll 1
   for (int h = 0; h < C::NCH * NH; ++h) {
-    const int ch = NH == 1 ? h : h / NH, r0 = NH == 1 ? 0 : HR * (h % NH);
-    uint32_t oa[16], ob[16], oc[16];
-    const uint32_t at = c.at + C::O_COL + NP * ch + r0;
-    tmem_ld16(at, oa);  // warp-collective
-    tmem_ld16(at + (NR > 8 ? NR : 16), ob);
-    if (NR > 8) tmem_ld16(at + 2 * NR, oc);
+    const int ch = h / NH, hf = h % NH;
+    uint32_t oa[16], ob[8];
+    const uint32_t at = c.at + C::O_COL + NP * ch;
+    tmem_ld16(at + o_col(NH * group + hf), oa);  // warp-collective
+    tmem_ld8(at + lo_col(NH * group + hf), ob);
     tmem_wait_ld();
-    const uint32_t *hi = oa, *mid = NR > 8 ? ob : oa + 8, *lo = NR > 8 ? oc : ob;
     const int d = T * ch + t;
     if (d < D) {
-      uint16_t* o = p.o + ((size_t)head * g.M + blk * NR + r0) * D + d;
-      float* po = p.po + (slot + r0) * D + d;
+      uint16_t* o = p.o + ((size_t)head * g.M + row0 + 8 * hf) * D + d;
+      float* po = p.po + (slot + 8 * hf) * D + d;
 #pragma unroll
-      for (int q = 0; q < HR; ++q)
-        if (r0 + q < rows) {
-          const float v = __uint_as_float(hi[q]) + (__uint_as_float(mid[q]) + __uint_as_float(lo[q]));
-          if (whole) o[q * D] = __bfloat16_as_ushort(__float2bfloat16_rn(v * mul[r0 + q]));
+      for (int q = 0; q < 8; ++q)
+        if (8 * hf + q < rows) {
+          const float v = __uint_as_float(oa[q]) + (__uint_as_float(oa[8 + q]) + __uint_as_float(ob[q]));
+          if (whole) o[q * D] = __bfloat16_as_ushort(__float2bfloat16_rn(v * mul[8 * hf + q]));
           else po[q * D] = v;
         }
     }
@@ -626,7 +642,7 @@ __device__ __forceinline__ void softmax_visit(const C8Params& p, unsigned char* 
 }
 
 template <int D, int NR>
-__global__ void __launch_bounds__(kThr, 2)
+__global__ void __launch_bounds__(C8<D, NR>::THR, 2)
     cache8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const __grid_constant__ C8Params p) {
   using C = C8<D, NR>;
@@ -646,7 +662,7 @@ __global__ void __launch_bounds__(kThr, 2)
     prefetch_tmap(&tmV);
   }
   if (threadIdx.x < Bars::kCount) {
-    mbar_init(bar.b + threadIdx.x, Bars::arrivals(threadIdx.x));
+    mbar_init(bar.b + threadIdx.x, Bars::arrivals(threadIdx.x, C::GROUPS));
     fence_mbar_init();
   }
   __syncthreads();
@@ -736,7 +752,7 @@ __global__ void __launch_bounds__(kThr, 2)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    tmem_sync();
+    tmem_sync<32 + 128 * C::GROUPS>();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     if (total > 0 && elect_one()) {
@@ -800,31 +816,31 @@ __global__ void __launch_bounds__(kThr, 2)
       mma_commit(bar.drain());
       mbar_wait_drain(bar.drain(), 0);
     }
-  } else if (warp < 6) {
+  } else if (warp < C::HELPER) {
     // ------------------------------------------------------------ softmax
     Walk w = first;
     Soft c;
     c.n = c.visit = 0;
     if (total > 0) {
       load_scales(p, w, 32 * (warp & 3) + lane, c);
-#pragma unroll 1
-      for (int i = warp - 2; i < NR / 4; i += 4)
-        prepare_queries<D, NR>(p, w.head(), w.blk, min(NR, g.M - w.blk * NR), base + C::OFF_Q, qfac, i, lane);
+      if (warp - 2 < NR / 4)
+        prepare_queries<D, NR>(p, w.head(), w.blk, min(NR, g.M - w.blk * NR), base + C::OFF_Q, qfac, warp - 2, lane);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar.q_full(0));
     }
-    int2* plan = reinterpret_cast<int2*>(base + C::OFF_SMALL + C::PLAN);
-    if (warp == 4 && lane == 0) *plan = make_int2(0, total);
-    tmem_sync();
+    const int group = (warp - 2) / 4;
+    int2* plan = reinterpret_cast<int2*>(base + C::OFF_SMALL + group * C::SOFT + C::PLAN);
+    if ((warp & 3) == 0 && lane == 0) *plan = make_int2(0, total);
+    tmem_sync<32 + 128 * C::GROUPS>();
     tc_fence_after();
     c.at = *tmem_slot + ((uint32_t)(32 * (warp & 3)) << 16);
     c.plan = *plan;
-    soft_sync();  // (before the first visit's is written)
+    soft_sync(group);  // (before the first visit's is written)
 #pragma unroll 1
     while (c.plan.y > 0) softmax_visit<D, NR>(p, base, bar, abort_flag, w, c);
   } else {
     // ------------------------------------------------------------ the later visits' queries
-    if (lane == 0) {  // for the merge
+    if (warp == C::HELPER && lane == 0) {  // for the merge
       int4 cut = make_int4(-1, 0, 0, 0);
       if (total > 0 && first.t > 0) {
         const int begin = u0 - first.t, c0 = runs.of(begin);
@@ -843,23 +859,23 @@ __global__ void __launch_bounds__(kThr, 2)
       if (v >= 2 && !__all_sync(0xffffffffu, wait(bar.q_empty(s), ((v >> 1) & 1) ^ 1, abort_flag))) break;
       // (the softmax reads the factors of visit v - 3 at most: the scores are two tiles ahead of it, the queries two visits)
       const int rows = min(NR, g.M - w.blk * NR);
-      // all rows are asked for at once (four at a time would take four times the memory's latency)
+      // all rows are asked for at once (four at a time would take the memory's latency as often)
       const unsigned char* q = reinterpret_cast<const unsigned char*>(p.q + ((size_t)w.head() * g.M + w.blk * NR) * D);
 #pragma unroll 1
-      for (int i = lane; i < rows * (D / 64); i += 32) asm volatile("prefetch.global.L1 [%0];" ::"l"(q + 128 * i));
+      for (int i = threadIdx.x - 32 * C::HELPER; i < rows * (D / 64); i += 32 * C::HELPERS) asm volatile("prefetch.global.L1 [%0];" ::"l"(q + 128 * i));
       // rows behind the block's are zero once they have been
       const int groups = (rows + 3) / 4, old = filled >> (4 * s) & 15;  // of four rows
 #pragma unroll 1
-      for (int i = 0; i < max(groups, old); ++i)
+      for (int i = warp - C::HELPER; i < max(groups, old); i += C::HELPERS)
         prepare_queries<D, NR>(p, w.head(), w.blk, rows, base + C::OFF_Q + s * C::QB, qfac + (v & 3) * NR, i, lane);
       filled = (filled & ~(15 << (4 * s))) | groups << (4 * s);
       __syncwarp();
-      if (lane < 4) mbar_arrive(bar.q_full(s));
+      if (lane < 4 * C::GROUPS / C::HELPERS) mbar_arrive(bar.q_full(s));
       w.skip();
     }
     // requests without a key: no unit is theirs
 #pragma unroll 1
-    for (int b = cta; b < g.B; b += gridDim.x * gridDim.y) {
+    for (int b = cta; warp == C::HELPER && b < g.B; b += gridDim.x * gridDim.y) {
       const int len = p.kv_len[b];
       if (len < 0 || tiles_of(g, len) > 0) continue;
       const size_t at = (size_t)b * g.Hkv * g.M;
@@ -1070,7 +1086,7 @@ cudaError_t cache8_d(const Cache8Geom& g, const Cache8Args& a, void* ws, int* st
   const dim3 grid((unsigned)g.lanes, (unsigned)(kCtas / g.lanes));  // a run's lanes are neighbours
   // both are programmatic dependents of what runs before them: the main grid's
   // set-up and the merge's placement fall into its predecessor's end
-  if ((e = launch_dependent(kern, grid, dim3(kThr), C::SMEM, st, tk, tv, p)) != cudaSuccess) return e;
+  if ((e = launch_dependent(kern, grid, dim3(C::THR), C::SMEM, st, tk, tv, p)) != cudaSuccess) return e;
   if (tiles_most(g) == 1) return cudaSuccess;  // a segment of one tile is not cut
   return launch_dependent(cache8_merge_kernel<D>, dim3(grid.x * grid.y, kMergeSides), dim3(32 * kMergeWarps), 0, st, p);
 }
@@ -1091,16 +1107,13 @@ bool cache8_fits(const Cache8Geom& g) {
   const double units = (double)g.B * g.Hkv * g.nmb * ((g.rows + T - 1) / T);
   return units < 2.0e9 && (double)g.B * g.Hkv * g.M < 1.0e9;
 }
-// Query rows of a block.  Up to 8 rows take half the softmax of 16 (the 48.5 us above
-// are 56.8 with 16; D = 128, 43.5 and 45.9).  A tile costs blocks of 32 twice that of 16,
-// and they read it once where two of 16 both do, one of them from L2.  At D = 256 and
-// 512, where HBM is what bounds the calls, that is as fast (16 requests of 32 rows
-// over 5,120 keys, D = 256: 33.5 us, and 36.9 with 32; 32 requests over 8,192: 88.6
-// and 88.3); at D <= 128 it is what bounds them (32 requests over 8,192 keys, D = 128:
-// 66.3 and 51.3 us; D = 64 over 16,384: 58.3 and 46.8).  With few tiles a CTA the
-// blocks of 16 spread better (16 requests, D = 64: 14.1 and 14.7 us over 2,560 keys,
-// 2.1 tiles a CTA, 17.7 and 17.3 over 5,120; 16.0 and 18.0 where the lengths fill half
-// of such a cache, whose rows are what the host knows).
+// Query rows of a block.  Up to 8 rows need one group of softmax warps (the 48.4 us
+// above are 59.2 with blocks of 16; D = 128, 43.5 and 45.4).  A tile costs blocks of 32
+// nearly twice that of 16, and they read it once where two of 16 both do, one of them
+// from L2.  At D = 256 and 512, where HBM is what bounds the calls, that is as fast, and
+// the accumulators of 32 rows would not fit beside the scores of two CTAs; at D <= 128
+// it is what bounds them (32 requests over 8,192 keys, D = 128: 65 and 56 us).  With few
+// tiles a CTA the blocks of 16 spread better (SPREAD).
 void cache8_split(Cache8Geom& g) {
   const long long units = (long long)g.B * g.Hkv * ((g.M + 31) / 32) * tiles_most(g);
   g.nr = g.M <= 8 ? 8 : g.M <= 16 || g.D > 128 || units < 6 * kCtas ? 16 : 32;
