@@ -862,7 +862,8 @@ __global__ void __launch_bounds__(C8<D, NR>::THR, 2)
       // all rows are asked for at once (four at a time would take the memory's latency as often)
       const unsigned char* q = reinterpret_cast<const unsigned char*>(p.q + ((size_t)w.head() * g.M + w.blk * NR) * D);
 #pragma unroll 1
-      for (int i = threadIdx.x - 32 * C::HELPER; i < rows * (D / 64); i += 32 * C::HELPERS) asm volatile("prefetch.global.L1 [%0];" ::"l"(q + 128 * i));
+      for (int i = threadIdx.x - 32 * C::HELPER; i < rows * (D / 64); i += 32 * C::HELPERS)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(q + 128 * i));
       // rows behind the block's are zero once they have been
       const int groups = (rows + 3) / 4, old = filled >> (4 * s) & 15;  // of four rows
 #pragma unroll 1
@@ -1102,10 +1103,11 @@ cudaError_t cache8_nr(const Cache8Geom& g, const Cache8Args& a, void* ws, int* s
 
 }  // namespace
 
-// Units (tiles of all segments) within 32 bits.
+// Units (tiles of all segments) within 32 bits; 288 GB hold 18 million tiles, to be
+// multiplied by up to 27 row blocks each.
 bool cache8_fits(const Cache8Geom& g) {
   const double units = (double)g.B * g.Hkv * g.nmb * ((g.rows + T - 1) / T);
-  return units < 2.0e9 && (double)g.B * g.Hkv * g.M < 1.0e9;
+  return units < 5.0e8 && (double)g.B * g.Hkv * g.M < 1.0e9;
 }
 // Query rows of a block.  Up to 8 rows need one group of softmax warps (the 48.4 us
 // above are 59.2 with blocks of 16; D = 128, 43.5 and 45.4).  A tile costs blocks of 32
@@ -1113,7 +1115,10 @@ bool cache8_fits(const Cache8Geom& g) {
 // from L2.  At D = 256 and 512, where HBM is what bounds the calls, that is as fast, and
 // the accumulators of 32 rows would not fit beside the scores of two CTAs; at D <= 128
 // it is what bounds them (32 requests over 8,192 keys, D = 128: 65 and 56 us).  With few
-// tiles a CTA the blocks of 16 spread better (SPREAD).
+// tiles a CTA the blocks of 16 spread better (16 requests, 2 kv heads, D = 64: 12.8 and
+// 14.5 us over 2,560 keys, 2.1 tiles of 32 rows a CTA; 17.1 and 15.9 over 5,120, but 15.3
+// and 17.1 over up to 5,001).  The host knows a cache's rows only; it is taken to be half
+// full.
 void cache8_split(Cache8Geom& g) {
   const long long units = (long long)g.B * g.Hkv * ((g.M + 31) / 32) * tiles_most(g);
   g.nr = g.M <= 8 ? 8 : g.M <= 16 || g.D > 128 || units < 6 * kCtas ? 16 : 32;
