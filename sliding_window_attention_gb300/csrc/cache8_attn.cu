@@ -43,10 +43,10 @@
 //
 // Bounds.  Long caches by HBM: 32 requests of up to 16,384 tokens, D = 512, 151 us,
 // 7.1 TB/s of cache; 64 of up to 8,192, D = 128, 43.5 us, 6.2 TB/s, of which some 8
-// are not the stream's: 1.0 lengths and split, 3 until the first tiles are there,
+// are not the stream's: 0.7 lengths and split, 2.7 until the first tiles are there,
 // 1 from the last tile's arrival to a run's end, 1.0 until the merge may begin, 1.6
 // merge, 0.5 until the next call's lengths.  Those are what a short call takes (4
-// requests of up to 1,024, D = 128: 7.8 us, and as much on the host).  At D = 64 the
+// requests of up to 1,024, D = 128: 7.5 us, and as much on the host).  At D = 64 the
 // softmax of a tile, 0.7 us of a CTA for 8 rows, is as long as its stream (64
 // requests of 16 / 2 heads over 16,384 keys: 48.5 us, 5.5 TB/s; three CTAs an SM,
 // 46.2 us, would cost the other head dims 1 to 4 us).
