@@ -340,6 +340,42 @@ def test_references_that_move(D, Hq, rising):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+def test_references_that_move_apart(D):
+    """28 rows of one block, of which some rise and some fall along a long cache."""
+    g = torch.Generator().manual_seed(D + 5)
+    B, Hq, Hkv, Lq, rows, block = 8, 16, 4, 7, 7300, 64
+    q = torch.randn(B, Hq, Lq, D, generator=g).to(BF)
+    q[..., 0] = torch.tensor([4.0, -4.0, 0.5, 3.0, -1.0, 0.0, 2.0])[(torch.arange(Hq)[:, None] + torch.arange(Lq)) % 7]
+    k = 0.2 * torch.randn(B, Hkv, rows, D, generator=g)
+    k[..., 0] = torch.linspace(-25, 25, rows)
+    codes = torch.zeros(B, Hkv, rows, D, dtype=torch.float64)
+    scales = torch.zeros(B, Hkv, -(-rows // block), dtype=torch.float64)
+    ref_append(k.to(BF), codes, scales, None, block)
+    kc, vc = (codes.float().to(F8), scales.float()), filled(B, Hkv, rows, D, block, 46)
+    lens = torch.randint(rows // 2, rows + 1, (B,), generator=g).tolist()
+    some = [0, B - 1]
+    got_o, got_lse = attend(q, kc, vc, None, lens, 0, 1.0, block)
+    o, tol, lse, ltol = attention(q[some], *(t.view(torch.uint8)[some].view(F8) for t in (kc[0], vc[0])), kc[1][some],
+                                  vc[1][some], None, [lens[b] for b in some], 0, 1.0, block)
+    assert bool(((got_o[some] - o).abs() <= tol).all()) and bool(((got_lse[some] - lse).abs() <= ltol).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,Hq,Hkv,Lq,D,rows,window,sinks,block,lens", [
+    (1, 8, 1, 700, 64, 900, 0, True, 16, [800]),           # 350 blocks: more than CTAs
+    (1, 8, 1, 400, 256, 700, 200, False, 64, [650]),       # 200: one CTA each
+    (2, 4, 1, 1000, 128, 1500, 0, False, 128, [1500, 990]),  # 125 of 32 rows; rows without a key
+])
+def test_attention_of_many_row_blocks(B, Hq, Hkv, Lq, D, rows, window, sinks, block, lens):
+    g = torch.Generator().manual_seed(rows + 1)
+    q = torch.randn(B, Hq, Lq, D, generator=g).to(BF)
+    kc, vc = filled(B, Hkv, rows, D, block, 47, 0.3), filled(B, Hkv, rows, D, block, 48)
+    s = torch.randn(Hq, generator=g) if sinks else None
+    check_attention(q, kc, vc, s, lens, window, 1.0 / math.sqrt(D), block)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("D", [64, 512])
 def test_scales_far_apart(D):
     """Blocks of values and keys whose scales lie 2^60 apart, zeros among them, and the least scale."""
