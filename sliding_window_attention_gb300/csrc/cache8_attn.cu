@@ -29,8 +29,9 @@
 // 8,192 keys, D = 128, N = 32: 47.7 us, and 50.4 with one group).
 //
 // Work.  The unit is one tile of 128 keys of one segment (request, kv head, row
-// block).  The units of all requests, by the device-side lengths, are cut into
-// 304 equal runs, one for each CTA, two CTAs an SM.  A segment that lies within
+// block), and some for each segment, since a CTA's visit of one takes as long as 1 to 3
+// tiles beside them.  The units of all requests, by the device-side lengths, are cut
+// into 304 equal runs, one for each CTA, two CTAs an SM.  A segment that lies within
 // one run is finished there; one that runs' ends cut leaves a partial (R, sum,
 // O) for each run, and a second kernel merges those.  Where a kv head has several
 // row blocks, neighbouring CTAs have the same runs of different blocks, so that a
@@ -126,10 +127,14 @@ struct Runs {
   }
 };
 
+// A segment's units: g.visit of no tile, for what a visit takes but for its tiles
+// (queries, the first references, the last product, the output), and its tiles.
+__device__ __forceinline__ int units_of(const Cache8Geom& g, int tiles) { return tiles > 0 ? tiles + g.visit : 0; }
+
 // A place in a CTA's run: request, kv head, row block, tile.
 struct Walk {
   const C8Params* p;
-  int left;      // units from here to the end of the run
+  int left;      // units from here to the end of the run; none: the run is through
   int lane;      // of row blocks: the walk has blocks lane, lane + g.lanes, ..
   int b, h, blk;
   int t, nt, n;  // tile of the segment, its tiles, the request's length
@@ -142,11 +147,12 @@ struct Walk {
     b = b0;
     n = min(len, p->g.rows);
     nt = tiles_of(p->g, n);
-    const int in = quotient(r, nt), per = blocks();
-    t = r - in * nt;
+    const int in = quotient(r, nt + p->g.visit), per = blocks();
+    t = r - in * (nt + p->g.visit) - p->g.visit;
     h = per == 1 ? in : quotient(in, per);
     blk = lane + p->g.lanes * (in - h * per);
-    left = units;
+    left = max(units + min(t, 0), 0);
+    t = max(t, 0);
     first = true;
   }
   // the lane's blocks of a head (one, where there are no more blocks than CTAs)
@@ -160,6 +166,8 @@ struct Walk {
     first = false;
     ++t;
     if (--left == 0 || t < nt) return;
+    left = max(left - p->g.visit, 0);
+    if (left == 0) return;
     first = true;
     t = 0;
     if ((blk += p->g.lanes) < p->g.nmb) return;
@@ -379,12 +387,12 @@ struct Soft {
   uint32_t at;   // TMEM: this thread's lane
   int n;         // tiles so far: S^T(n) is in buffer n & 1
   int visit;
-  int2 plan;     // the visit's tiles, units behind them
+  int2 plan;     // the visit's tiles, units of the visits behind it
   float ks, vs;  // scales of this thread's key of tile n
 };
 __device__ __forceinline__ int2 plan_of(const Walk& w) {  // w at a visit's begin, or behind the run
   const int tiles = min(w.left, w.nt - w.t);
-  return w.left > 0 ? make_int2(tiles, w.left - tiles) : make_int2(0, 0);
+  return w.left > 0 ? make_int2(tiles, max(w.left - tiles - w.p->g.visit, 0)) : make_int2(0, 0);
 }
 __device__ __forceinline__ void load_scales(const C8Params& p, const Walk& w, int t, Soft& c) {
   const size_t at = (size_t)w.head() * p.g.nblk + (max(w.key0() + t, 0) >> p.g.lb);
@@ -691,12 +699,12 @@ __global__ void __launch_bounds__(C8<D, NR>::THR, 2)
     }
     auto length = [&](int b) { return b >= g.B ? -1 : pass ? p.kv_len[b] : g.rows; };
     const int len0 = length(lane);  // of the first 32
-    int tiles = tiles_of(g, len0);
+    int all = units_of(g, tiles_of(g, len0));
 #pragma unroll 1
-    for (int b = lane + 32; b < g.B; b += 32) tiles += tiles_of(g, length(b));
-    tiles = __reduce_add_sync(0xffffffffu, tiles);
+    for (int b = lane + 32; b < g.B; b += 32) all += units_of(g, tiles_of(g, length(b)));
+    all = __reduce_add_sync(0xffffffffu, all);
     first.left = 0;
-    runs = Runs(tiles * hn, gridDim.y);
+    runs = Runs(all * hn, gridDim.y);
     u0 = runs.start(blockIdx.y);
     const int units = runs.start(blockIdx.y + 1) - u0;
     if (units > 0) {
@@ -704,8 +712,8 @@ __global__ void __launch_bounds__(C8<D, NR>::THR, 2)
 #pragma unroll 1
       for (int b0 = 0; b0 < g.B; b0 += 32) {
         const int len = b0 == 0 ? len0 : length(b0 + lane);
-        const int nt = tiles_of(g, len);
-        int inc = nt;
+        const int own = units_of(g, tiles_of(g, len));
+        int inc = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const int v = __shfl_up_sync(0xffffffffu, inc, o);
@@ -714,7 +722,7 @@ __global__ void __launch_bounds__(C8<D, NR>::THR, 2)
         const unsigned here = __ballot_sync(0xffffffffu, u0 < (before + inc) * hn);
         if (here) {
           const int l = __ffs(here) - 1;
-          const int at = before + __shfl_sync(0xffffffffu, inc - nt, l);
+          const int at = before + __shfl_sync(0xffffffffu, inc - own, l);
           first.begin(b0 + l, __shfl_sync(0xffffffffu, len, l), u0 - at * hn, units);
           break;
         }
@@ -722,11 +730,11 @@ __global__ void __launch_bounds__(C8<D, NR>::THR, 2)
       }
     }
   }
-  const int total = first.left;
+  const bool any = first.left > 0;
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
-    if (total > 0 && elect_one()) {
+    if (any && elect_one()) {
       // the cache, which a call reads once (but for further row blocks), gives way in L2
       const uint64_t policy = l2_policy(true);
       Walk wk = first, wv = first;
@@ -746,8 +754,8 @@ __global__ void __launch_bounds__(C8<D, NR>::THR, 2)
       // slots in MMA order: K(0), K(1), then per tile n: V(n), K(n + 2)
       bool ok = true;
 #pragma unroll 1
-      for (int n = -2; ok && n < total; ++n)
-        ok = (n < 0 || load_tile(wv, &tmV)) && (n + 2 >= total || load_tile(wk, &tmK));
+      for (int n = -2; ok && wv.left > 0; ++n)
+        ok = (n < 0 || load_tile(wv, &tmV)) && (wk.left == 0 || load_tile(wk, &tmK));
       if (*abort_flag) drain_ring(bar.slot_full(0), NSLOT, issued);  // loads in flight land before shared memory is released
     }
   } else if (warp == 1) {
@@ -755,7 +763,7 @@ __global__ void __launch_bounds__(C8<D, NR>::THR, 2)
     tmem_sync<32 + 128 * C::GROUPS>();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    if (total > 0 && elect_one()) {
+    if (any && elect_one()) {
       constexpr uint32_t idS = idesc_f8(T, NS, 0, 0, 0, 0);  // K x Q^T, both K-major, e4m3
       constexpr uint32_t idO = idesc_f8(T, NP, 0, 1, 1, 1);  // V^T (e4m3) x weights^T (e5m2), both MN-major
       constexpr uint32_t SWZ = D < 128 ? 4 : 2;
@@ -790,7 +798,7 @@ __global__ void __launch_bounds__(C8<D, NR>::THR, 2)
       };
       bool ok = true;
 #pragma unroll 1
-      for (int n = -2; ok && n < total; ++n) {
+      for (int n = -2; ok && wv.left > 0; ++n) {
         if (n >= 0) {
           if (!wait(bar.p_full(), n & 1, abort_flag)) break;
           tc_fence_after();
@@ -811,7 +819,7 @@ __global__ void __launch_bounds__(C8<D, NR>::THR, 2)
           mma_commit(bar.o_done());
           wv.next();
         }
-        if (n + 2 < total) ok = issue_s(n + 2);  // the weights of tile n have been written: its scores' buffer is free
+        if (ws.left > 0) ok = issue_s(n + 2);  // the weights of tile n have been written: its scores' buffer is free
       }
       mma_commit(bar.drain());
       mbar_wait_drain(bar.drain(), 0);
@@ -821,7 +829,7 @@ __global__ void __launch_bounds__(C8<D, NR>::THR, 2)
     Walk w = first;
     Soft c;
     c.n = c.visit = 0;
-    if (total > 0) {
+    if (any) {
       load_scales(p, w, 32 * (warp & 3) + lane, c);
       if (warp - 2 < NR / 4)
         prepare_queries<D, NR>(p, w.head(), w.blk, min(NR, g.M - w.blk * NR), base + C::OFF_Q, qfac, warp - 2, lane);
@@ -830,7 +838,7 @@ __global__ void __launch_bounds__(C8<D, NR>::THR, 2)
     }
     const int group = (warp - 2) / 4;
     int2* plan = reinterpret_cast<int2*>(base + C::OFF_SMALL + group * C::SOFT + C::PLAN);
-    if ((warp & 3) == 0 && lane == 0) *plan = make_int2(0, total);
+    if ((warp & 3) == 0 && lane == 0) *plan = make_int2(0, first.left);
     tmem_sync<32 + 128 * C::GROUPS>();
     tc_fence_after();
     c.at = *tmem_slot + ((uint32_t)(32 * (warp & 3)) << 16);
@@ -842,16 +850,16 @@ __global__ void __launch_bounds__(C8<D, NR>::THR, 2)
     // ------------------------------------------------------------ the later visits' queries
     if (warp == C::HELPER && lane == 0) {  // for the merge
       int4 cut = make_int4(-1, 0, 0, 0);
-      if (total > 0 && first.t > 0) {
-        const int begin = u0 - first.t, c0 = runs.of(begin);
+      if (any && first.t > 0) {
+        const int begin = u0 - first.t, c0 = runs.of(begin);  // the segment's first tile
         cut = make_int4(first.head() * g.nmb + first.blk, runs.of(begin + first.nt - 1) - c0 + 1,
                         c0 * g.lanes + first.lane,
-                        2 * (c0 * g.lanes + first.lane) + (runs.start(c0) == begin ? 0 : 1));
+                        2 * (c0 * g.lanes + first.lane) + (runs.start(c0) >= begin - g.visit ? 0 : 1));
       }
       p.cuts[cta] = cut;
     }
     Walk w = first;
-    if (total > 0) w.skip();
+    if (any) w.skip();
     int filled = NR / 4 * 0x11;  // groups of rows of either buffer that may not be zero
 #pragma unroll 1
     for (int v = 1; w.left > 0; ++v) {
@@ -1106,7 +1114,7 @@ cudaError_t cache8_nr(const Cache8Geom& g, const Cache8Args& a, void* ws, int* s
 // Units (tiles of all segments) within 32 bits; 288 GB hold 18 million tiles, to be
 // multiplied by up to 27 row blocks each.
 bool cache8_fits(const Cache8Geom& g) {
-  const double units = (double)g.B * g.Hkv * g.nmb * ((g.rows + T - 1) / T);
+  const double units = (double)g.B * g.Hkv * g.nmb * ((g.rows + T - 1) / T + g.visit);
   return units < 5.0e8 && (double)g.B * g.Hkv * g.M < 1.0e9;
 }
 // Query rows of a block.  Up to 8 rows need one group of softmax warps (the 48.4 us
@@ -1124,6 +1132,9 @@ void cache8_split(Cache8Geom& g) {
   g.nr = g.M <= 8 ? 8 : g.M <= 16 || g.D > 128 || units < 6 * kCtas ? 16 : 32;
   g.nmb = (g.M + g.nr - 1) / g.nr;
   g.lanes = g.nmb < kCtas ? g.nmb : kCtas;
+  // (in tiles; 1, 2, 3 for all: 32 requests of 32 rows over up to 8,192 keys, D = 128, 41.8, 39.5, 38.2 us, and 47.8
+  // without; of 16 rows 28.0, 26.9, 27.3 and 31.3; 8 requests of 32 / 8 heads over up to 2,000 9.4, 9.6, 9.7 and 10.8)
+  g.visit = g.nr / 16 + 1;
 }
 size_t cache8_workspace_bytes(const Cache8Geom& g) { return c8_ws(g).total; }
 

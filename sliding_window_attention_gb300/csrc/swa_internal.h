@@ -462,6 +462,7 @@ cudaError_t launch_cache8_read(const Cache8ReadArgs& a, cudaStream_t s);
 struct Cache8Geom {
   int B, Hq, Hkv, G, Lq, M;       // M = G * Lq query rows of a request and kv head
   int nr, nmb;                    // in nmb blocks of up to nr
+  int visit;                      // units of a segment beside its tiles
   int lanes;                      // CTA (x, y) works on blocks x, x + lanes, ..: those of one key range are
                                   // neighbours' work at the same time, and meet in L2
   int rows, lb, nblk;             // cache rows, log2 of a scale's block, scales of a head
