@@ -25,8 +25,8 @@
 // number of query rows is.  A block has up to N = 8, 16 or 32 of the G * Lq rows of a
 // kv head; a softmax thread has one key of the tile and 8 rows at a time.  Blocks of 16
 // and 32 have two groups of four softmax warps, each with half of the rows and with
-// barriers of its own, so that one works while the other waits (32 requests over up to
-// 8,192 keys, D = 128, N = 32: 47.7 us, and 50.4 with one group).
+// barriers of its own, so that one works while the other waits (N = 32, 32 requests over
+// up to 8,192 keys, D = 128: 50.4 to 47.8 us).
 //
 // Work.  The unit is one tile of 128 keys of one segment (request, kv head, row
 // block), and some for each segment, since a CTA's visit of one takes as long as 1 to 3
@@ -36,14 +36,14 @@
 // O) for each run, and a second kernel merges those.  Where a kv head has several
 // row blocks, neighbouring CTAs have the same runs of different blocks, so that a
 // tile's later reads find it in L2 (16 requests of 32 rows over 4,096 keys, D =
-// 512: 52.7 us, and 83.9 with the blocks one after the other).
+// 512: 51.0 us, and 83.9 with the blocks one after the other).
 //
 // Tiles are aligned to the end of what a request's rows see: one that would
 // reach past it starts earlier (below key 0 the TMA fills zeros), so nothing
 // behind a request's length is loaded.
 //
-// Bounds.  Long caches by HBM: 32 requests of up to 16,384 tokens, D = 512, 151 us,
-// 7.1 TB/s of cache; 64 of up to 8,192, D = 128, 43.5 us, 6.2 TB/s, of which some 8
+// Bounds.  Long caches by HBM: 32 requests of up to 16,384 tokens, D = 512, 152 us,
+// 7.1 TB/s of cache; 64 of up to 8,192, D = 128, 43.4 us, 6.2 TB/s, of which some 8
 // are not the stream's: 0.7 lengths and split, 2.7 until the first tiles are there,
 // 1 from the last tile's arrival to a run's end, 1.0 until the merge may begin, 1.6
 // merge, 0.5 until the next call's lengths.  Those are what a short call takes (4
@@ -195,8 +195,8 @@ template <int D, int NR>
 struct C8 {
   static constexpr int GROUPS = NR > 8 ? 2 : 1;   // of four softmax warps, each with a part of the rows:
   static constexpr int NH = NR / 8 / GROUPS;      // so many eights, one after the other
-  // warps: TMA, MMA, softmax, and those that prepare queries (rows of 512: one warp is 40.1 us where two are 36.4, 16
-  // requests of 32 rows over up to 4,096 keys); two CTAs of 12 warps have 80 registers a thread
+  // warps: TMA, MMA, softmax, and those that prepare queries (rows of 512: one warp 40.1 us, two 36.4, 16 requests of
+  // 32 rows over up to 4,096 keys); two CTAs of 12 warps have 80 registers a thread
   static constexpr int HELPER = 2 + 4 * GROUPS, HELPERS = GROUPS, THR = 32 * (HELPER + HELPERS);
   static constexpr int NS = 2 * NR;               // columns of S^T: 8 rows' q in its first part, then in its second
   static constexpr int NP = NR > 8 ? 3 * NR : 32; // of O^T: weights' three parts (see o_col)
@@ -1117,16 +1117,15 @@ bool cache8_fits(const Cache8Geom& g) {
   const double units = (double)g.B * g.Hkv * g.nmb * ((g.rows + T - 1) / T + g.visit);
   return units < 5.0e8 && (double)g.B * g.Hkv * g.M < 1.0e9;
 }
-// Query rows of a block.  Up to 8 rows need one group of softmax warps (the 48.4 us
-// above are 59.2 with blocks of 16; D = 128, 43.5 and 45.4).  A tile costs blocks of 32
+// Query rows of a block.  Up to 8 rows need one group of softmax warps (the 48.5 us
+// above are 59.7 with blocks of 16; D = 128, 43.2 and 45.2).  A tile costs blocks of 32
 // nearly twice that of 16, and they read it once where two of 16 both do, one of them
 // from L2.  At D = 256 and 512, where HBM is what bounds the calls, that is as fast, and
 // the accumulators of 32 rows would not fit beside the scores of two CTAs; at D <= 128
-// it is what bounds them (32 requests over 8,192 keys, D = 128: 65 and 56 us).  With few
-// tiles a CTA the blocks of 16 spread better (16 requests, 2 kv heads, D = 64: 12.8 and
-// 14.5 us over 2,560 keys, 2.1 tiles of 32 rows a CTA; 17.1 and 15.9 over 5,120, but 15.3
-// and 17.1 over up to 5,001).  The host knows a cache's rows only; it is taken to be half
-// full.
+// it is what bounds them (32 requests over 8,192 keys, D = 128: 65.7 and 55.7 us).  With
+// few tiles a CTA the blocks of 16 spread better (16 requests, 2 kv heads, D = 64: 13.9
+// and 15.4 us over up to 5,001 keys, of a cache with 4.2 tiles of 32 rows a CTA; 17.6 and
+// 16.8 with 5,120 each).
 void cache8_split(Cache8Geom& g) {
   const long long units = (long long)g.B * g.Hkv * ((g.M + 31) / 32) * tiles_most(g);
   g.nr = g.M <= 8 ? 8 : g.M <= 16 || g.D > 128 || units < 6 * kCtas ? 16 : 32;
