@@ -206,7 +206,7 @@ struct C8 {
   static constexpr int QB = NS * D;               // a block of queries
   static constexpr int PB = NP * T;               // weights
   // the softmax groups' small arrays: [4][8] exchanged maxima / sums, references, rescale factors, row ranges, the
-  // visit's tiles and whether another follows; and the row factors of four visits
+  // visit's tiles; and the row factors of four visits
   static constexpr int RED = 0, REF = 128 * NH, ALPHA = REF + 32 * NH, RNG = ALPHA + 32 * NH, PLAN = RNG + 64 * NH, SOFT = PLAN + 16,
                        QFAC = GROUPS * SOFT, SMALL = QFAC + 16 * NR;
   static constexpr int BARS = 256;
@@ -358,8 +358,8 @@ __device__ __forceinline__ float finish_row(const float* sink, float ref, float 
 // Barrier of a group's four softmax warps; `any`: whether any of their threads says so.
 // Its wait needs no limit: the warps go through all of them whatever their bounded
 // waits on the other roles say, and how often is what one thread says to all (a
-// visit's tiles, whether another follows), so that lengths that a faulty program
-// changes while the kernel runs can make them no different.
+// visit's tiles), so that lengths that a faulty program changes while the kernel
+// runs can make them no different.
 __device__ __forceinline__ void soft_sync(int group) {
   if (group == 0) asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
   else asm volatile("barrier.cta.sync 3, 128;" ::: "memory");
@@ -387,17 +387,33 @@ struct Soft {
   uint32_t at;   // TMEM: this thread's lane
   int n;         // tiles so far: S^T(n) is in buffer n & 1
   int visit;
-  int2 plan;     // the visit's tiles, units of the visits behind it
+  int tiles;     // the visit's; none: the run is through
   float ks, vs;  // scales of this thread's key of tile n
 };
-__device__ __forceinline__ int2 plan_of(const Walk& w) {  // w at a visit's begin, or behind the run
-  const int tiles = min(w.left, w.nt - w.t);
-  return w.left > 0 ? make_int2(tiles, max(w.left - tiles - w.p->g.visit, 0)) : make_int2(0, 0);
-}
 __device__ __forceinline__ void load_scales(const C8Params& p, const Walk& w, int t, Soft& c) {
   const size_t at = (size_t)w.head() * p.g.nblk + (max(w.key0() + t, 0) >> p.g.lb);
   c.ks = p.ks[at];
   c.vs = p.vs[at];
+}
+
+// What a group's warps have to see before a visit (w at its begin, or behind the
+// run): the rows' visible keys, no references, the number of tiles.
+template <int D, int NR>
+__device__ __forceinline__ void plan_visit(const C8Params& p, unsigned char* small, const Walk& w, int t, int r0) {
+  using C = C8<D, NR>;
+  constexpr int R = 8 * C::NH;
+  const Cache8Geom& g = p.g;
+  if (t < R) {  // rows that are no query mask nothing: their columns are never read
+    const int row = w.blk * NR + r0 + t;
+    int lo = 0, hi = INT32_MAX;
+    if (row < g.M) {
+      hi = w.n - g.Lq + (g.Lq > 1 ? row % g.Lq : 0);
+      lo = g.W > 0 ? max(0, hi - g.W + 1) : 0;
+    }
+    reinterpret_cast<int2*>(small + C::RNG)[t] = make_int2(lo, hi);
+    reinterpret_cast<float*>(small + C::REF)[t] = -kUnset;  // (the references' negatives)
+  }
+  if (t == 0) *reinterpret_cast<int*>(small + C::PLAN) = w.left > 0 ? min(w.left, w.nt - w.t) : 0;
 }
 
 // One visit of a segment: its tiles' weights, then the result or the partial.
@@ -417,23 +433,10 @@ __device__ __forceinline__ void softmax_visit(const C8Params& p, unsigned char* 
   float* alp = reinterpret_cast<float*>(small + C::ALPHA);
   int2* rng = reinterpret_cast<int2*>(small + C::RNG);
   const float* fac = reinterpret_cast<const float*>(base + C::OFF_SMALL + C::QFAC) + (c.visit & 3) * NR + r0;
-  const int blk = w.blk, head = w.head(), len = w.n, row0 = blk * NR + r0, rows = min(R, g.M - row0);  // (rows < 1: none)
+  const int head = w.head(), len = w.n, row0 = w.blk * NR + r0, rows = min(R, g.M - row0);  // (rows < 1: none)
   const bool whole = w.t == 0 && w.left >= w.nt;  // the visit is of the whole segment
-  if (t < R) {  // row t's visible keys; rows that are no query mask nothing: their columns are never read
-    int lo = 0, hi = INT32_MAX;
-    if (t < rows) {
-      hi = len - g.Lq + (g.Lq > 1 ? (row0 + t) % g.Lq : 0);
-      lo = g.W > 0 ? max(0, hi - g.W + 1) : 0;
-    }
-    rng[t] = make_int2(lo, hi);
-    nref[t] = -kUnset;
-  }
   // every row sees the keys from lo_all to hi_all
   const int lo_all = g.W > 0 ? max(0, len - g.W) : 0, hi_all = len - g.Lq;
-  int2* plan = reinterpret_cast<int2*>(small + C::PLAN);
-  if (t == 0) *plan = plan_of(w);
-  soft_sync(group);
-  c.plan = *plan;
 
   uint64_t l_part[R / 2];  // pairs of rows
   float m_row = kUnset;    // thread t < R holds row t's reference
@@ -442,7 +445,7 @@ __device__ __forceinline__ void softmax_visit(const C8Params& p, unsigned char* 
 
   bool fresh = true;
 #pragma unroll 1
-  for (int k = 0; k < c.plan.x; ++k) {
+  for (int k = 0; k < c.tiles; ++k) {
     const int n = c.n, buf = n & 1, key0 = w.key0();
     const float vscale = fmaxf(c.vs, cache8_two_to(kCache8LeastExponent)), lv = __log2f(vscale);
     const uint64_t ks2 = f2_pack(c.ks, c.ks), lv2 = f2_pack(lv, lv), iv2 = f2_pack(__fdividef(1.f, vscale), __fdividef(1.f, vscale));
@@ -621,7 +624,9 @@ __device__ __forceinline__ void softmax_visit(const C8Params& p, unsigned char* 
       *reinterpret_cast<float2*>(p.ml + 2 * (slot + t)) = make_float2(m_row, l);
     }
   }
+  plan_visit<D, NR>(p, small, w, t, r0);  // the next one's, while the last product is under way
   soft_sync(group);
+  c.tiles = *reinterpret_cast<int*>(small + C::PLAN);
   wait(bar.o_done(), (c.n - 1) & 1, abort);
   __syncwarp();
   tc_fence_after();
@@ -837,15 +842,14 @@ __global__ void __launch_bounds__(C8<D, NR>::THR, 2)
       if (lane == 0) mbar_arrive(bar.q_full(0));
     }
     const int group = (warp - 2) / 4;
-    int2* plan = reinterpret_cast<int2*>(base + C::OFF_SMALL + group * C::SOFT + C::PLAN);
-    if ((warp & 3) == 0 && lane == 0) *plan = make_int2(0, first.left);
+    unsigned char* small = base + C::OFF_SMALL + group * C::SOFT;
+    plan_visit<D, NR>(p, small, w, 32 * (warp & 3) + lane, 8 * C::NH * group);
     tmem_sync<32 + 128 * C::GROUPS>();
     tc_fence_after();
     c.at = *tmem_slot + ((uint32_t)(32 * (warp & 3)) << 16);
-    c.plan = *plan;
-    soft_sync(group);  // (before the first visit's is written)
+    c.tiles = *reinterpret_cast<int*>(small + C::PLAN);
 #pragma unroll 1
-    while (c.plan.y > 0) softmax_visit<D, NR>(p, base, bar, abort_flag, w, c);
+    while (c.tiles > 0) softmax_visit<D, NR>(p, base, bar, abort_flag, w, c);
   } else {
     // ------------------------------------------------------------ the later visits' queries
     if (warp == C::HELPER && lane == 0) {  // for the merge
