@@ -26,6 +26,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "cache8_rows.h"
 #include "swa_internal.h"
 #include "tc_ptx.cuh"
 
@@ -89,15 +90,11 @@ __global__ void __launch_bounds__(GT > 256 ? GT : 256, GT > 256 ? 2 : (VPT > 4 ?
   const bool in = j < p.nj && bh < p.B * p.Hkv;
   const int b = in ? bh / p.Hkv : 0, h = in ? bh - b * p.Hkv : 0;
   const int n = in ? (p.kv_len ? p.kv_len[b] : p.L) : 0;
-  const long long from = (long long)n - p.L;  // row of token 0
-  const int row0 = from > 0 ? (int)from : 0, blk = (row0 >> p.lb) + j;
-  const long long lo = (long long)blk << p.lb, end = lo + (1 << p.lb);
-  const int a = (int)(lo > row0 ? lo : row0);  // the block's older tokens are rows lo .. a, its new ones a .. hi
-  int hi = n < p.rows ? n : p.rows;
-  if (end < hi) hi = (int)end;
-  const bool any = in && hi > a;
-  const int lv = p.ld - 3, vecs = any ? (hi - a) << lv : 0;  // vectors of the new rows
-  const uint16_t* x = p.x[which] + b * p.sb[which] + h * p.sh[which] + (any ? a - from : 0) * p.st[which];
+  const Cache8Rows r = cache8_rows(n, p.L, p.rows, p.lb, j);
+  const int blk = r.blk, lo = r.lo, a = r.a;
+  const bool any = in && r.any;
+  const int lv = p.ld - 3, vecs = any ? (r.hi - a) << lv : 0;  // vectors of the new rows
+  const uint16_t* x = p.x[which] + b * p.sb[which] + h * p.sh[which] + r.token * p.st[which];
   auto vector = [&](int e) { return x + (e >> lv) * p.st[which] + ((e & ((1 << lv) - 1)) << 3); };
   uint32_t most = 0;  // the larger magnitude of a pair
   auto look = [&](const uint4& u) {
@@ -166,7 +163,7 @@ __global__ void __launch_bounds__(GT > 256 ? GT : 256, GT > 256 ? 2 : (VPT > 4 ?
   if (tid == 0) *scale = now;
   if (older) {  // the older codes move to the new scale
     uint2* c = reinterpret_cast<uint2*>(codes + ((size_t)lo << p.ld));
-    const int old = (int)(a - lo) << lv;
+    const int old = (a - lo) << lv;
     const float f = was / now;
 #pragma unroll 1
     for (int e = tid; e < old; e += GT) {

@@ -178,6 +178,63 @@ def test_append_strides_and_one_tensor():
     assert torch.equal(d[0].cpu().double(), codes) and torch.equal(d[1].cpu().double(), scales)
 
 
+ROWS_MAIN = """
+#include <cstdio>
+#include "cache8_rows.h"
+int main() {
+  int n, L, rows, lb, j;
+  while (std::scanf("%d %d %d %d %d", &n, &L, &rows, &lb, &j) == 5) {
+    const swa::Cache8Rows r = swa::cache8_rows(n, L, rows, lb, j);
+    std::printf("%d %d %d %d %d %d\\n", (int)r.any, r.blk, r.lo, r.a, r.hi, r.token);
+  }
+}
+"""
+
+
+def test_rows_that_an_append_writes(tmp_path):
+    """The kernel's own arithmetic, compiled for the host: lengths over the whole range of an int, its ends among them."""
+    import random
+    import subprocess
+
+    from sliding_window_attention_gb300 import build
+
+    src, exe = tmp_path / "rows.cpp", tmp_path / "rows"
+    src.write_text(ROWS_MAIN)
+    subprocess.run(["g++", "-O1", "-std=c++17", "-fsanitize=undefined", "-fno-sanitize-recover=all", "-I", build.CSRC,
+                    str(src), "-o", str(exe)], check=True)
+    rng = random.Random(1)
+    top = 2 ** 31 - 1
+    cases = [(top, 2, 64, 4, 1), (top, 2, 64, 4, 0), (top, 40, 2_000_000_000, 4, 2), (-top - 1, 5, 64, 4, 0)]
+    for _ in range(4000):
+        lb, L = rng.choice((4, 5, 6, 7)), rng.choice((1, 2, 7, 64, 300, 5000, 2_000_000_000))
+        rows = rng.choice((1, 50, 64, 1000, 2_000_000_000))
+        n = rng.choice((rng.randint(-5, 400), rng.randint(rows - 200, rows + 400), rng.randint(top - 300, top),
+                        rng.randint(-top - 1, top), -top - 1 + rng.randint(0, 300)))
+        meets = min((L + 2 ** lb - 2) // 2 ** lb + 1, -(-rows // 2 ** lb))
+        cases.append((max(min(n, top), -top - 1), L, rows, lb, rng.randrange(meets)))
+    out = subprocess.run([str(exe)], input="\n".join(" ".join(map(str, c)) for c in cases), text=True, check=True,
+                         capture_output=True).stdout.splitlines()
+    assert len(out) == len(cases)
+    for c, line in zip(cases, out):
+        n, L, rows, lb, j = c
+        row0 = max(n - L, 0)
+        blk = (row0 >> lb) + j
+        a, hi = max(blk << lb, row0), min(n, rows, (blk + 1) << lb)
+        want = [1, blk, blk << lb, a, hi, a - (n - L)] if a < hi else [0] * 6
+        assert [int(x) for x in line.split()] == want, c
+
+
+@pytest.mark.gpu
+def test_append_at_the_largest_lengths():
+    """Lengths up to 2^31 - 1 lie behind the cache: nothing is written, by calls that meet several blocks too."""
+    top = 2 ** 31 - 1
+    for L, D, block in ((5, 64, 16), (40, 128, 16), (300, 64, 128)):
+        k = torch.randn(6, 2, L, D).to(BF)
+        kc, vc = filled(6, 2, 64, D, block, 14), filled(6, 2, 64, D, block, 15)
+        check_append(k, (2 * k.float()).to(BF), (kc[0], vc[0], kc[1], vc[1]), [top, top - 1, top - 15, 64 + L, -top - 1, 63],
+                     block)
+
+
 # ---------------------------------------------------------------- read
 
 
