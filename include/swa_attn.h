@@ -402,7 +402,8 @@ int swa_attn_cache8_read(const uint8_t* k_cache, const uint8_t* v_cache, const f
  * in fp32, as are the row sums and the partial outputs; o is rounded to bf16
  * once.  Within a request and head the values' scales that matter may lie up to
  * 2^100 apart; a value's scale below 2^-64 (the append writes none) counts as
- * 2^-64.  Scales are positive and finite; of rows within the lengths they
+ * 2^-64.  An infinite or NaN element of q makes its row's o and lse NaN, where the
+ * row sees a key.  Scales are positive and finite; of rows within the lengths they
  * and the codes must not be NaN, whatever stands behind is not used.  The
  * Hq / Hkv * Lq query rows of a kv head are taken in blocks of up to 8, 16 or 32,
  * each of which multiplies the whole cache (side by side, so that L2 serves all

@@ -340,7 +340,9 @@ __device__ __forceinline__ void prepare_queries(const C8Params& p, int head, int
     put(r + (r & ~7), hi);
     put(r + (r & ~7) + 8, lo);
   }
-  if (l8 == 0) fac[r] = fabsf(p.g.scale) * kLog2e * cache8_two_to(e);
+  // (an infinity's parts are 448, as a finite maximum's may be: its row's factor is
+  // NaN, scale + 0 * infinity)
+  if (l8 == 0) fac[r] = fmaf(amax, 0.f, fabsf(p.g.scale)) * kLog2e * cache8_two_to(e);
   fence_proxy_async_smem();
 }
 

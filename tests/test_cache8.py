@@ -462,6 +462,33 @@ def test_scales_of_the_softmax(scale):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128, 256, 512])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("sinks", [False, True])
+def test_queries_that_are_not_finite(D, bad, sinks):
+    """One such element makes its row's o and lse NaN, whole or cut, unless the row sees no key; the other rows' bits stay."""
+    g = torch.Generator().manual_seed(D)
+    B, Hq, Hkv, Lq, rows, block = 3, 8, 2, 3, 900, 32
+    lens = [900, 2, 130]  # the second request's first row sees no key
+    q = torch.randn(B, Hq, Lq, D, generator=g).to(BF)
+    kc, vc = filled(B, Hkv, rows, D, block, 61, 0.3), filled(B, Hkv, rows, D, block, 62)
+    s = torch.randn(Hq, generator=g) if sinks else None
+    hit = [(0, 1, 2), (0, 6, 0), (1, 3, 0), (1, 4, 1), (2, 7, 1)]
+    dirty, clean = q.clone(), q.clone()
+    for i, (b, h, l) in enumerate(hit):
+        dirty[b, h, l, (37 * i) % D] = bad
+        clean[b, h, l] = 0
+    got, want = attend(dirty, kc, vc, s, lens, 0, 0.1, block), attend(clean, kc, vc, s, lens, 0, 0.1, block)
+    live = torch.ones(B, Hq, Lq, dtype=torch.bool)
+    for b, h, l in hit:
+        if lens[b] - Lq + l >= 0:
+            live[b, h, l] = False
+    assert int((~live).sum()) == 4
+    assert bool(got[0][~live].isnan().all()) and bool(got[1][~live].isnan().all())
+    assert torch.equal(got[0][live], want[0][live]) and torch.equal(got[1][live], want[1][live])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("D,Lq,window", [(64, 4, 0), (128, 1, 100), (256, 5, 0), (512, 1, 0)])
 def test_what_stands_behind_the_lengths(D, Lq, window):
     """NaN codes and scales behind the lengths, and in empty places, change nothing; rows of empty places stay."""
