@@ -931,7 +931,8 @@ __device__ __forceinline__ void merge_pieces(const C8Params& p, const int4& cut,
   // pieces first, first + step, .. of `all` (the quotient of numbers below 2^12 is exact)
   const int all = rows * PIECES, first = kMergeSides * (apart - 1) + blockIdx.y, step = max(kMergeSides * (n - 1), 1);
   const int mine = n == 0 ? 4 : (first < all ? (int)__fdividef(all - first + step - 0.5f, (float)step) : 0);
-  const int sh = mine >= kMergeWarps ? 0 : 2 - (32 - __clz(mine - 1)), share = 1 << sh;  // warps on a piece
+  static_assert(kMergeWarps == 4, "the next line");
+  const int sh = mine > 2 ? 0 : (mine == 2 ? 1 : 2), share = 1 << sh;  // warps on a piece
   const int k = warp & (share - 1);
 #pragma unroll 1
   for (int i0 = 0; i0 < mine; i0 += kMergeWarps >> sh) {
