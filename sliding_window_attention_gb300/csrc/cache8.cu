@@ -126,6 +126,8 @@ __global__ void __launch_bounds__(GT > 256 ? GT : 256, GT > 256 ? 2 : (VPT > 4 ?
     __syncthreads();  // (also orders every thread's read of the old scale before it is written)
 #pragma unroll
     for (int i = 0; i < GT / 32; ++i) most = max(most, top[group * (GT / 32) + i]);
+  } else {
+    __syncwarp();  // the same order within a warp: the reduction orders no memory
   }
   if (!any) return;
   const float amax = __uint_as_float(min(most, 0x7F7Fu) << 16);  // (infinity and NaN count as the largest number)
