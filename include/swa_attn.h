@@ -368,8 +368,9 @@ int swa_attn_qk_rope_bwd(const swa_bf16* q, const swa_bf16* k, long long q_strid
  * swa_attn_cache8_read writes rows row0 .. row0 + rows - 1 of the cache as bf16
  * [B, Hkv, rows, D] (code * scale, rounded once; exact where the scale is a
  * power of two and nothing is subnormal), zeros for rows at or behind the
- * request's length (none with kv_len NULL).  k_out or v_out may be NULL.  With
- * it a prompt's next chunk runs through swa_attn_fwd_ex.
+ * request's length (none with kv_len NULL).  k_out or v_out may be NULL, with its
+ * codes and scales then not used.  With it a prompt's next chunk runs through
+ * swa_attn_fwd_ex.
  */
 int swa_attn_cache8_append(const swa_bf16* k, const swa_bf16* v, long long k_stride_b, long long k_stride_h,
                            long long k_stride_t, long long v_stride_b, long long v_stride_h, long long v_stride_t,

@@ -752,8 +752,8 @@ int swa_attn_cache8_append(const swa_bf16* k, const swa_bf16* v, long long k_str
       (v && !strides_ok(v_stride_b, v_stride_h, v_stride_t, B, Hkv, L, D)))
     return SWA_ERR_BAD_STRIDE;
   if ((double)B * Hkv * (L / block + 2.0) > 1.0e9) return SWA_ERR_TOO_LARGE;
-  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 4) ||
-      !aligned(v_scale, 4) || !aligned(kv_len, 4))
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(kv_len, 4) ||
+      (k && (!aligned(k_cache, 16) || !aligned(k_scale, 4))) || (v && (!aligned(v_cache, 16) || !aligned(v_scale, 4))))
     return SWA_ERR_MISALIGNED;
   if ((rc = check_device())) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -790,8 +790,9 @@ int swa_attn_cache8_read(const uint8_t* k_cache, const uint8_t* v_cache, const f
   if (rc) return rc;
   if (row0 < 0 || rows < 1 || (long long)row0 + rows > kv_rows) return SWA_ERR_BAD_CACHE;
   if ((double)B * Hkv * ((double)rows * D / 8192 + 1.0) > 2.0e9) return SWA_ERR_TOO_LARGE;
-  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_out, 16) || !aligned(v_out, 16) ||
-      !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(kv_len, 4))
+  if (!aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(kv_len, 4) ||
+      (k_out && (!aligned(k_cache, 16) || !aligned(k_scale, 4))) ||
+      (v_out && (!aligned(v_cache, 16) || !aligned(v_scale, 4))))
     return SWA_ERR_MISALIGNED;
   if ((rc = check_device())) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

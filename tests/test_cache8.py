@@ -235,6 +235,41 @@ def test_append_at_the_largest_lengths():
                      block)
 
 
+@pytest.mark.gpu
+def test_what_a_call_does_not_use_is_not_checked():
+    """With k or v alone the other's strides, codes and scales are anything (here: the middle of a tensor, oddly placed)."""
+    import sliding_window_attention_gb300 as swa
+
+    lib = swa.load()
+    B, H, L, D, rows, block = 2, 2, 3, 64, 40, 16
+    g = torch.Generator().manual_seed(17)
+    x = torch.randn(B, H, L, D, generator=g).to(BF)
+    n = torch.tensor([3, 20], dtype=torch.int32)
+    c0, s0 = filled(B, H, rows, D, block, 18)
+    want_c, want_s = c0.double(), s0.double()
+    ref_append(x, want_c, want_s, n, block)
+    dx, dn, rest = x.cuda(), n.cuda(), torch.full((4096,), 7, dtype=torch.uint8, device="cuda")
+    strides, odd = x.stride()[:3], rest.data_ptr() + 2049
+    for first in (True, False):
+        for other in (0, odd):
+            c, s = c0.cuda(), s0.cuda()
+            out = torch.empty(B, H, rows, D, dtype=BF, device="cuda")
+
+            def pair(mine, none=other):  # (k's, v's)
+                return (mine, none) if first else (none, mine)
+
+            sk, sv = pair(strides, (-1, 3, 5))
+            assert lib.swa_attn_cache8_append(*pair(dx.data_ptr(), None), *sk, *sv, dn.data_ptr(), *pair(c.data_ptr()),
+                                              *pair(s.data_ptr()), B, H, L, D, rows, block, None) == 0
+            assert lib.swa_attn_cache8_read(*pair(c.data_ptr()), *pair(s.data_ptr()), None, *pair(out.data_ptr(), None),
+                                            B, H, D, rows, block, 0, rows, None) == 0
+            status_ok()
+            assert torch.equal(c.cpu().double(), want_c) and torch.equal(s.cpu().double(), want_s)
+            per = want_s.float().repeat_interleave(block, 2)[:, :, :rows, None]
+            assert torch.equal(out.cpu(), (want_c.float() * per).to(BF))
+    assert bool((rest == 7).all())
+
+
 # ---------------------------------------------------------------- read
 
 
