@@ -822,11 +822,21 @@ def prefix_positions(B: int, L: int, prompt_len: int, chosen_len: int, device):
 # a cache in 8 bits: quantised as it is written, read back, and the attention over it
 
 
+def _scale_block(block) -> int:
+    block = _int32("block", block)
+    if block not in (16, 32, 64, 128):
+        raise ValueError(f"block must be 16, 32, 64 or 128 tokens, got {block}")
+    return block
+
+
 def make_cache8(B: int, Hkv: int, rows: int, D: int, block: int, device="cuda"):
     """An empty cache in 8 bits: (k_cache, v_cache) float8_e4m3fn
     [B,Hkv,rows,D] and (k_scale, v_scale) fp32 [B,Hkv,ceil(rows / block)]."""
     import torch
 
+    block = _scale_block(block)
+    if D not in (64, 128, 256, 512) or min(B, Hkv, rows) < 1:
+        raise ValueError(f"a cache has B, Hkv, rows >= 1 and D of 64, 128, 256 or 512, got {(B, Hkv, rows, D)}")
     codes = [torch.zeros((B, Hkv, rows, D), dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) for _ in range(2)]
     scales = [torch.ones((B, Hkv, -(-rows // block)), dtype=torch.float32, device=device) for _ in range(2)]
     return (*codes, *scales)
@@ -841,9 +851,7 @@ def _check_cache8(k_cache, v_cache, k_scale, v_scale, kv_len, block, optional_le
         raise ValueError("k_cache or v_cache is needed")
     if one.dim() != 4:
         raise ValueError("the caches must be [B, Hkv, rows, D]")
-    block = _int32("block", block)
-    if block not in (16, 32, 64, 128):
-        raise ValueError(f"block must be 16, 32, 64 or 128 tokens, got {block}")
+    block = _scale_block(block)
     dev = _current_device(one, "the cache")
     B, Hkv, rows, D = one.shape
     scales = (B, Hkv, -(-rows // block))
@@ -915,7 +923,10 @@ def swa_attn_cache8_read(k_cache, v_cache, k_scale, v_scale, kv_len, k_out, v_ou
                                                 k_scale, v_scale, kv_len, block, True)
     if (k_out is not None and k_cache is None) or (v_out is not None and v_cache is None):
         raise ValueError("k_out needs k_cache and v_out needs v_cache")
-    n = (k_out if k_out is not None else v_out).shape[2]
+    one = k_out if k_out is not None else v_out
+    if one.dim() != 4:
+        raise ValueError("the outputs must be [B, Hkv, rows, D]")
+    n = one.shape[2]
     _check(dev, [(name, t, torch.bfloat16, (B, Hkv, n, D)) for name, t in (("k_out", k_out), ("v_out", v_out))
                  if t is not None])
     rc = load().swa_attn_cache8_read(_addr(k_cache), _addr(v_cache), _addr(k_scale), _addr(v_scale), _addr(kv_len),

@@ -821,6 +821,29 @@ def test_binding_refuses_host_tensors(lib):
         swa.forward_cache8(torch.zeros(1, 4, 1, 64, dtype=BF), *cache, n, 16, 0, 0.1)
 
 
+def test_a_cache_that_no_call_takes_is_not_made():
+    import sliding_window_attention_gb300 as swa
+
+    for shape in ((1, 2, 32, 64, 0), (1, 2, 32, 64, 24), (1, 2, 32, 64, -16), (1, 2, 32, 96, 16), (0, 2, 32, 64, 16),
+                  (1, 0, 32, 64, 16), (1, 2, 0, 64, 16), (1, 2, -1, 64, 16)):
+        with pytest.raises(ValueError, match="block must be|a cache has"):
+            swa.make_cache8(*shape, device="cpu")
+    k8, v8, ks, vs = swa.make_cache8(2, 3, 33, 64, 16, device="cpu")
+    assert k8.shape == v8.shape == (2, 3, 33, 64) and ks.shape == vs.shape == (2, 3, 3) and k8.dtype is F8
+
+
+@pytest.mark.gpu
+def test_a_read_refuses_outputs_of_other_dimensions():
+    import sliding_window_attention_gb300 as swa
+
+    k8, v8, ks, vs = swa.make_cache8(2, 2, 48, 64, 16)
+    out = torch.zeros(2, 2, 48, 64, dtype=BF, device="cuda")
+    for k_out, v_out in ((out[0, 0], out), (out[0], None), (None, out[0, 0]), (out[None], out)):
+        with pytest.raises(ValueError):
+            swa.swa_attn_cache8_read(k8, v8, ks, vs, None, k_out, v_out, 16)
+    status_ok()
+
+
 @pytest.mark.gpu
 def test_binding_refuses_wrong_tensors():
     import sliding_window_attention_gb300 as swa
