@@ -95,11 +95,12 @@ struct C8Params {
   int* status;
 };
 
-// Key tiles of a request that any of its rows sees.
+// Key tiles of a request that any of its rows sees: of its last W + Lq - 1 keys at
+// most.  (A length may be any int: none is subtracted from.)
 __device__ __forceinline__ int tiles_of(const Cache8Geom& g, int len) {
-  const int n = min(len, g.rows);
-  const int lo = g.W > 0 ? max(0, n - g.Lq - g.W + 1) : 0;
-  return n > lo ? (n - lo + T - 1) / T : 0;
+  int n = min(len, g.rows);
+  if (g.W > 0) n = min(n, g.W + g.Lq - 1);
+  return n > 0 ? (n + T - 1) / T : 0;
 }
 
 // a / b, 0 <= a < 2^31, 0 < b: an estimate, the estimate of what it left, and the

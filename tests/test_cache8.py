@@ -560,6 +560,31 @@ def test_what_stands_behind_the_lengths(D, Lq, window):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D,Lq,window", [(64, 1, 0), (128, 3, 200), (512, 9, 37)])
+def test_attention_at_the_ends_of_the_lengths(D, Lq, window):
+    """-2^31 is an empty place like -1, 2^31 - 1 a full cache like its number of rows."""
+    import sliding_window_attention_gb300 as swa
+
+    g = torch.Generator().manual_seed(D)
+    B, Hq, Hkv, rows, block = 5, 4, 2, 300, 64
+    q = torch.randn(B, Hq, Lq, D, generator=g).to(BF).cuda()
+    kc, vc = filled(B, Hkv, rows, D, block, 63), filled(B, Hkv, rows, D, block, 64)
+    cache = [t.cuda() for t in (kc[0], vc[0], kc[1], vc[1])]
+    ws = torch.empty(swa.fwd_workspace_bytes_cache8(B, Hq, Hkv, Lq, rows, D, block, window), dtype=torch.uint8, device="cuda")
+    got = []
+    for lens in ([-2 ** 31, 200, 2 ** 31 - 1, -2 ** 31 + 5, 2 ** 31 - 200], [-1, 200, rows, -1, rows]):
+        o, lse = torch.full_like(q, 3), torch.full((B, Hq, Lq), 3.0, device="cuda")
+        n = torch.tensor(lens, dtype=torch.int32).cuda()
+        swa.swa_attn_fwd_cache8(q, *cache, n, None, o, lse, block, window, 0.1, ws)
+        kb, vb = swa.cache8_read(*cache, n, block)
+        status_ok()
+        got.append((o, lse, kb, vb))
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+    assert bool((got[0][0][[0, 3]] == 3).all()) and bool((got[0][1][[0, 3]] == 3).all())
+
+
+@pytest.mark.gpu
 def test_a_step_with_the_calls_around_it():
     """Rotation, append and attention, step after step, a request ending and a place reused: like
     forward_shared over bf16 caches that hold what the 8-bit cache's reads give."""
