@@ -358,9 +358,11 @@ int swa_attn_qk_rope_bwd(const swa_bf16* q, const swa_bf16* k, long long q_strid
  * to even.  A block that already has tokens (rows before the first new one)
  * keeps its scale if the new tokens fit, max |x| <= 448 s; otherwise it gets
  * the scale of the new tokens, and its older codes are written again for it.
- * That only moves their exponents: a value changes when it falls below 2^-6 s,
- * by at most 2^-10 s.  Older scales have to be positive and finite.  Rows behind the
- * last new one are left as they were.  A block in which no row is written
+ * Where the older scale is a power of two, as the append's are, that only moves
+ * their exponents: a value changes when it falls below 2^-6 s, by at most 2^-10 s.
+ * Codes under another quantiser's scale are rounded once more: a value changes by up
+ * to 2^-4 of itself, or 2^-10 s where that is more.  Older scales have to be positive
+ * and finite.  Codes behind the last new row are left as they were.  A block in which no row is written
  * keeps its scale; one that begins with a new token gets a new scale whatever
  * it held.  Tokens must be finite; magnitudes above 2^127 may read back as
  * infinity.  Equal calls give equal bits.

@@ -157,6 +157,38 @@ def test_append_with_scales_that_are_no_powers_of_two():
     check_append((k.float() * 0.1).to(BF), k, (kc[0], vc[0], ks, vs), [20, 45], 32)
 
 
+# L, D, block: one for each of the append's groups of threads and vectors a thread, in their order, by the min(L, block)
+# * D / 8 vectors that a block can get: up to 64, 128, 256, 512, 1,024, 2,048, 4,096 and more
+GROUPS = [(1, 512, 64), (4, 256, 64), (7, 256, 16), (70, 64, 64), (100, 256, 32), (300, 128, 128), (200, 256, 64),
+          (100, 512, 32), (300, 256, 128), (200, 512, 128)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("L,D,block", GROUPS)
+@pytest.mark.parametrize("times", [1.0, 1.2734375, 1.9921875])
+@pytest.mark.parametrize("size", [0.01, 1.0, 40.0])
+def test_append_behind_older_tokens(L, D, block, times, size):
+    """Each group's kernel behind a partial block of older tokens that fits the new ones, or has to grow for them; with
+    scales that are powers of two and another quantiser's.  A value that is written again changes by what the header
+    says: 2^-10 s of a power of two, and 2^-4 of itself where that is more with other scales."""
+    g = torch.Generator().manual_seed(L + D + block)
+    B, H = 2, 2
+    rows = L + block + 5
+    k, v = (size * torch.randn(B, H, L, D, generator=g)).to(BF), (3 * size * torch.randn(B, H, L, D, generator=g)).to(BF)
+    kc, vc = filled(B, H, rows, D, block, 71, 0.3), filled(B, H, rows, D, block, 72, 0.3)
+    ks, vs = kc[1] * times, vc[1] * times
+    lens = [L + 3, rows - 1]
+    d = check_append(k, v, (kc[0], vc[0], ks, vs), lens, block)
+    for was_c, was_s, now_c, now_s in ((kc[0], ks, d[0], d[2]), (vc[0], vs, d[1], d[3])):
+        for b, n in enumerate(lens):
+            j = torch.arange(n - L) // block
+            was = was_c[b, :, :n - L].double() * was_s[b][:, j, None].double()
+            s = now_s.cpu()[b][:, j, None].double()
+            change = (now_c.cpu()[b, :, :n - L].double() * s - was).abs()
+            most = s * 2.0 ** -10 if times == 1.0 else torch.maximum(s * 2.0 ** -10, was.abs() * 2.0 ** -4)
+            assert bool((change <= most).all())
+
+
 @pytest.mark.gpu
 def test_append_strides_and_one_tensor():
     """Slices of a projection's rows, and k alone."""
