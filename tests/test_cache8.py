@@ -445,6 +445,67 @@ def test_attention_of_many_tiles(B, Hq, Hkv, Lq, D, rows, window, block, spread)
     assert torch.equal(again[0], got_o) and torch.equal(again[1], got_lse)
 
 
+def rows_of_a_block(B, Hq, Hkv, Lq, rows, D, block, window):
+    """Query rows of a block, by the partials that the workspace holds (D + 2 floats a row, two slots for each of 304 CTAs)."""
+    import sliding_window_attention_gb300 as swa
+
+    return swa.fwd_workspace_bytes_cache8(B, Hq, Hkv, Lq, rows, D, block, window) // (608 * 4 * (D + 2))
+
+
+# B, Hq, Hkv, Lq, D, rows, window, sinks, block: more than 16 rows a kv head at D <= 128, over caches of more than 1,824
+# tiles, which are what blocks of 32 rows are taken for
+BLOCKS_OF_32 = [
+    (40, 16, 2, 4, 64, 4000, 3500, True, 16),     # a window and sinks
+    (40, 16, 2, 4, 128, 4000, 3500, True, 64),
+    (24, 20, 2, 4, 128, 3000, 0, True, 128),      # 40 rows: a block of 32 and one of 8
+    (24, 20, 2, 5, 64, 3000, 0, False, 16),       # 50: one of 32 and one of 18
+    (100, 16, 2, 3, 128, 2000, 1500, True, 32),   # 24 of 32
+    (1900, 17, 1, 1, 64, 300, 100, True, 64),     # 17; a window within a tile or two: many visits of one tile
+    (256, 32, 4, 4, 64, 400, 0, False, 32),       # many short requests
+    (256, 32, 4, 4, 128, 400, 130, True, 128),
+    (20, 32, 1, 4, 128, 4000, 0, True, 64),       # 128 rows: four whole blocks
+    (30, 25, 1, 4, 64, 8000, 2000, False, 128),   # 100: three and one of 4, over a long window
+]
+
+
+def test_which_blocks_are_tested():
+    """The cases above are of blocks of 32 rows, their likes with fewer tiles, few rows or longer heads of 16 or 8."""
+    for B, Hq, Hkv, Lq, D, rows, window, _, block in BLOCKS_OF_32:
+        assert rows_of_a_block(B, Hq, Hkv, Lq, rows, D, block, window) == (32 if Hq // Hkv * Lq > 32 else Hq // Hkv * Lq)
+        units = B * Hkv * -(-Hq // Hkv * Lq // 32) * -(-min(rows, window + Lq - 1 if window else rows) // 128)
+        assert units >= 1.02 * 6 * 304
+    assert rows_of_a_block(40, 20, 2, 4, 4000, 256, 16, 0) == 16 and rows_of_a_block(40, 20, 2, 4, 4000, 512, 16, 0) == 16
+    assert rows_of_a_block(2, 20, 2, 4, 4000, 64, 16, 0) == 16 and rows_of_a_block(40, 8, 2, 4, 4000, 64, 16, 0) == 16
+    assert rows_of_a_block(40, 8, 2, 2, 4000, 64, 16, 0) == 8
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,Hq,Hkv,Lq,D,rows,window,sinks,block", BLOCKS_OF_32)
+@pytest.mark.parametrize("equal", [False, True])
+def test_attention_in_blocks_of_32_rows(B, Hq, Hkv, Lq, D, rows, window, sinks, block, equal):
+    g = torch.Generator().manual_seed(rows + D + equal)
+    q = torch.randn(B, Hq, Lq, D, generator=g).to(BF)
+    x = torch.randint(0, 256, (2, B, Hkv, rows, D), generator=g, dtype=torch.uint8)
+    x &= 0xDF  # no NaN, 30 at most
+    kc, vc = (t.view(F8) for t in x)
+    sc = torch.exp2(torch.randint(-6, -2, (2, B, Hkv, -(-rows // block)), generator=g).float())
+    s = torch.randn(Hq, generator=g) if sinks else None
+    lens = [rows] * B if equal else torch.randint(0, rows + 1, (B,), generator=g).tolist()
+    if not equal:
+        lens[1:5] = [0, -1, 1, 2]  # no key, an empty place, rows without a key among others
+    some = [0, 1, 3, 4, B // 2, B - 1]
+    got_o, got_lse = attend(q, (kc, sc[0]), (vc, sc[1]), s, lens, window, 0.25 / math.sqrt(D), block)
+    o, tol, lse, ltol = attention(q[some], x[0][some].view(F8), x[1][some].view(F8), sc[0][some], sc[1][some], s,
+                                  [lens[b] for b in some], window, 0.25 / math.sqrt(D), block)
+    inf = lse == -math.inf
+    assert torch.equal(got_lse[some] == -math.inf, inf)
+    assert bool(((got_o[some] - o).abs() <= tol).all())
+    assert bool(((got_lse[some] - lse).masked_fill(inf, 0).abs() <= ltol).all())
+    again = attend(q, (kc, sc[0]), (vc, sc[1]), s, lens, window, 0.25 / math.sqrt(D), block)
+    live = torch.tensor(lens) >= 0
+    assert torch.equal(again[0][live], got_o[live]) and torch.equal(again[1][live], got_lse[live])
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("D,Hq,rising", [(64, 2, True), (128, 8, True), (256, 20, True), (512, 3, False)])
 def test_references_that_move(D, Hq, rising):
