@@ -98,8 +98,7 @@ struct C8Params {
 // Key tiles of a request that any of its rows sees: of its last W + Lq - 1 keys at
 // most.  (A length may be any int: none is subtracted from.)
 __device__ __forceinline__ int tiles_of(const Cache8Geom& g, int len) {
-  int n = min(len, g.rows);
-  if (g.W > 0) n = min(n, g.W + g.Lq - 1);
+  const int n = min(len, g.seen);
   return n > 0 ? (n + T - 1) / T : 0;
 }
 
@@ -1050,10 +1049,7 @@ struct C8Ws {
 };
 int slot_rows(const Cache8Geom& g) { return g.M < g.nr ? g.M : g.nr; }
 // Key tiles of a request, at most.
-long long tiles_most(const Cache8Geom& g) {
-  const long long keys = g.W > 0 && (long long)g.W + g.Lq - 1 < g.rows ? (long long)g.W + g.Lq - 1 : g.rows;
-  return (keys + T - 1) / T;
-}
+long long tiles_most(const Cache8Geom& g) { return ((long long)g.seen + T - 1) / T; }
 C8Ws c8_ws(const Cache8Geom& g) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   const size_t rows = (size_t)2 * kCtas * slot_rows(g);

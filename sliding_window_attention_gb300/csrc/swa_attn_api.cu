@@ -831,6 +831,7 @@ static int cache8_geom(swa::Cache8Geom& g, int B, int Hq, int Hkv, int Lq, int k
   g.nblk = (kv_rows + block - 1) / block;
   g.D = D;
   g.W = window >= kv_rows ? 0 : window;  // no two positions are further apart
+  g.seen = g.W > 0 && g.W + Lq - 1 < kv_rows ? g.W + Lq - 1 : kv_rows;
   g.scale = scale;
   swa::cache8_split(g);
   return swa::cache8_fits(g) ? SWA_OK : SWA_ERR_TOO_LARGE;

@@ -467,6 +467,7 @@ struct Cache8Geom {
                                   // neighbours' work at the same time, and meet in L2
   int rows, lb, nblk;             // cache rows, log2 of a scale's block, scales of a head
   int D, W;                       // W = 0: no window
+  int seen;                       // keys that any of a request's rows sees, at most
   float scale;
 };
 struct Cache8Args {
