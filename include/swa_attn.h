@@ -338,9 +338,10 @@ int swa_attn_qk_rope_bwd(const swa_bf16* q, const swa_bf16* k, long long q_strid
  * The value at row r is code * scale[r / block]; block is 16, 32, 64 or 128
  * tokens.  kv_len [B] int32 (device memory, read when the kernels run, so that
  * a captured call replays with the lengths of then) counts each request's
- * tokens; a negative length marks an empty place of the batch, one above
- * kv_rows counts as kv_rows.  D in {64, 128, 256, 512}; device pointers, data
- * 16-byte and scales 4-byte aligned.  Asynchronous on `stream`; errors as for
+ * tokens; a negative length marks an empty place of the batch.  The read and the
+ * attention take one above kv_rows as kv_rows; the append takes it as it is and
+ * leaves out the tokens whose rows the cache has not.  D in {64, 128, 256, 512};
+ * device pointers, data 16-byte and scales 4-byte aligned.  Asynchronous on `stream`; errors as for
  * swa_attn_fwd, and SWA_ERR_BAD_CACHE (kv_rows, block, rows), SWA_ERR_BAD_STRIDE.
  *
  * swa_attn_cache8_append quantises L new tokens a request and writes them:
@@ -362,10 +363,10 @@ int swa_attn_qk_rope_bwd(const swa_bf16* q, const swa_bf16* k, long long q_strid
  * their exponents: a value changes when it falls below 2^-6 s, by at most 2^-10 s.
  * Codes under another quantiser's scale are rounded once more: a value changes by up
  * to 2^-4 of itself, or 2^-10 s where that is more.  Older scales have to be positive
- * and finite.  Codes behind the last new row are left as they were.  A block in which no row is written
- * keeps its scale; one that begins with a new token gets a new scale whatever
- * it held.  Tokens must be finite; magnitudes above 2^127 may read back as
- * infinity.  Equal calls give equal bits.
+ * and finite.  Codes behind the last new row are left as they were.  A block in
+ * which no row is written keeps its scale; one that begins with a new token gets a
+ * new scale whatever it held.  Tokens must be finite; magnitudes above 2^127 may
+ * read back as infinity.  Equal calls give equal bits.
  *
  * swa_attn_cache8_read writes rows row0 .. row0 + rows - 1 of the cache as bf16
  * [B, Hkv, rows, D] (code * scale, rounded once; exact where the scale is a
@@ -403,14 +404,21 @@ int swa_attn_cache8_read(const uint8_t* k_cache, const uint8_t* v_cache, const f
  * times the values' scales, into three e5m2 parts of an fp16 number (2^-11,
  * and 2^-27 of the row's largest weight for those below).  Products are summed
  * in fp32, as are the row sums and the partial outputs; o is rounded to bf16
- * once.  Within a request and head the values' scales that matter may lie up to
- * 2^100 apart; a value's scale below 2^-64 (the append writes none) counts as
- * 2^-64.  An infinite or NaN element of q makes its row's o and lse NaN, where the
- * row sees a key.  Scales are positive and finite; of rows within the lengths they
- * and the codes must not be NaN, whatever stands behind is not used.  The
- * Hq / Hkv * Lq query rows of a kv head are taken in blocks of up to 8, 16 or 32,
- * each of which multiplies the whole cache (side by side, so that L2 serves all
- * but the first): a prompt's next chunk is better read back.
+ * once.  A weight counts by its block's scale, whatever the key's codes are: where
+ * one outlier has set a block's scale, values in blocks whose scales are 2^20 below
+ * it keep 6 bits.  Row sums (and lse) keep their precision while a request's and
+ * head's values' scales lie within 2^100 of each other; a value's scale below 2^-64
+ * (the append writes none) counts as 2^-64.  An infinite or NaN element of q makes
+ * its row's o and lse NaN, where the row sees a key.  Scales are positive and finite;
+ * of rows within the lengths they and the codes must not be NaN, whatever stands
+ * behind is not used.  The Hq / Hkv * Lq query rows of a kv head are taken in blocks
+ * of up to 8, 16 or 32, each of which multiplies the whole cache (side by side, so
+ * that L2 serves all but the first).  So a long chunk of a prompt is faster read back
+ * and run through swa_attn_fwd_ex: for one request from some 8,000 query rows
+ * (Hq * Lq), at D = 512 from some 4,000, over 4,096 as over 32,768 keys.
+ * The size of the blocks is chosen by kv_rows and the window, not by the lengths,
+ * which only the device knows: a cache made for many more rows than it holds gets the
+ * blocks that suit a full one.
  * The result does not depend on what else runs, but it does on the other
  * requests' lengths, in its last bits: they move the places where the key
  * ranges are split.  Equal calls give equal bits.
