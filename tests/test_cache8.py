@@ -578,6 +578,24 @@ def test_scales_far_apart(D):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D,Hq,Lq,sinks", [(64, 8, 1, False), (128, 8, 4, True), (256, 2, 5, False), (512, 4, 1, True)])
+@pytest.mark.parametrize("apart", [20, 100])
+def test_scales_as_far_apart_as_the_header_allows(D, Hq, Lq, sinks, apart):
+    """Values' scales 2^100 apart, the largest ones over codes of 0 (an outlier's block): lse keeps its
+    precision, and o is off by 2^-27 of the largest weight for each key, which at 2^20 leaves the small scales' values 6 bits."""
+    g = torch.Generator().manual_seed(D + apart)
+    B, Hkv, rows, block = 2, 2, 700, 32
+    nb = -(-rows // block)
+    q = torch.randn(B, Hq, Lq, D, generator=g).to(BF)
+    kc, vc = filled(B, Hkv, rows, D, block, 65, 0.2), filled(B, Hkv, rows, D, block, 66, 0.2)
+    low = torch.rand(B, Hkv, nb, generator=g) < 0.5
+    vs = torch.where(low, 2.0 ** -(apart // 2), 2.0 ** (apart - apart // 2))
+    codes = vc[0].float() * low.repeat_interleave(block, 2)[:, :, :rows, None]
+    s = torch.randn(Hq, generator=g) if sinks else None
+    check_attention(q, kc, (codes.to(F8), vs), s, [rows, 333], 0, 1.0 / math.sqrt(D), block)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("scale", [0.0, -0.125, 3.0])
 def test_scales_of_the_softmax(scale):
     g = torch.Generator().manual_seed(7)
