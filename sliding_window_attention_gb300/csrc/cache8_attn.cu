@@ -26,7 +26,8 @@
 // kv head; a softmax thread has one key of the tile and 8 rows at a time.  Blocks of 16
 // and 32 have two groups of four softmax warps, each with half of the rows and with
 // barriers of its own, so that one works while the other waits (N = 32, 32 requests over
-// up to 8,192 keys, D = 128: 50.4 to 47.8 us).
+// up to 8,192 keys, D = 128: 50.4 us with one group and 47.8 with two when they came,
+// 36.8 now).
 //
 // Work.  The unit is one tile of 128 keys of one segment (request, kv head, row
 // block), and some for each segment, since a CTA's visit of one takes as long as 1 to 3
@@ -35,22 +36,27 @@
 // one run is finished there; one that runs' ends cut leaves a partial (R, sum,
 // O) for each run, and a second kernel merges those.  Where a kv head has several
 // row blocks, neighbouring CTAs have the same runs of different blocks, so that a
-// tile's later reads find it in L2 (16 requests of 32 rows over 4,096 keys, D =
-// 512: 51.0 us, and 83.9 with the blocks one after the other).
+// tile's later reads find it in L2 (16 requests of 32 rows, each over 4,096 keys, D =
+// 512: 52.2 us, and 83.2 with the blocks one after the other).
 //
 // Tiles are aligned to the end of what a request's rows see: one that would
 // reach past it starts earlier (below key 0 the TMA fills zeros), so nothing
 // behind a request's length is loaded.
 //
-// Bounds.  Long caches by HBM: 32 requests of up to 16,384 tokens, D = 512, 152 us,
-// 7.1 TB/s of cache; 64 of up to 8,192, D = 128, 43.4 us, 6.2 TB/s, of which some 8
-// are not the stream's: 0.7 lengths and split, 2.7 until the first tiles are there,
-// 1 from the last tile's arrival to a run's end, 1.0 until the merge may begin, 1.6
-// merge, 0.5 until the next call's lengths.  Those are what a short call takes (4
-// requests of up to 1,024, D = 128: 7.5 us, and as much on the host).  At D = 64 the
+// Bounds.  Up to 8 rows over long caches by HBM: 32 requests of up to 16,384 tokens, D
+// = 512, 153 us, 7.0 TB/s of cache; 64 of up to 8,192, D = 128, 44.0 us, 6.1 TB/s, of
+// which some 8 are not the stream's: 0.7 lengths and split, 2.7 until the first tiles
+// are there, 1 from the last tile's arrival to a run's end, 1.0 until the merge may
+// begin, 1.6 merge, 0.5 until the next call's lengths.  Those are what a short call takes
+// (4 requests of up to 1,024, D = 128: 8.0 us, and as much on the host).  At D = 64 the
 // softmax of a tile, 0.7 us of a CTA for 8 rows, is as long as its stream (64
-// requests of 16 / 2 heads over 16,384 keys: 48.5 us, 5.5 TB/s; three CTAs an SM,
-// 46.2 us, would cost the other head dims 1 to 4 us).
+// requests of 16 / 2 heads over 16,384 keys: 48.8 us, 5.5 TB/s; three CTAs an SM were
+// 2.3 us faster there, and 1 to 4 us slower at the other head dims).  With 9 rows and
+// more neither HBM nor the tensor pipe is busy, but the chain of a tile's steps in the
+// softmax warps: 32 rows over 16,384 keys, D = 64, issue in 58 % of an SM's cycles with
+// DRAM at 31 %; two blocks of 16, D = 512, in 30 % with DRAM at 65 %, L2 at 42 %, half of
+// the stalls being on loads and scores (16 requests over 4,096 keys: 52.2 us for 40.2 of
+// bytes).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -195,8 +201,9 @@ template <int D, int NR>
 struct C8 {
   static constexpr int GROUPS = NR > 8 ? 2 : 1;   // of four softmax warps, each with a part of the rows:
   static constexpr int NH = NR / 8 / GROUPS;      // so many eights, one after the other
-  // warps: TMA, MMA, softmax, and those that prepare queries (rows of 512: one warp 40.1 us, two 36.4, 16 requests of
-  // 32 rows over up to 4,096 keys); two CTAs of 12 warps have 80 registers a thread
+  // warps: TMA, MMA, softmax, and those that prepare queries (rows of 512, 16 requests of 32 rows over up to 4,096 keys:
+  // one warp 40.1 us and two 36.4 when visits weighed nothing in the split; 33.0 and 33.7 since); two CTAs of 12 warps
+  // have 80 registers a thread, of which blocks of 32 rows spill 5
   static constexpr int HELPER = 2 + 4 * GROUPS, HELPERS = GROUPS, THR = 32 * (HELPER + HELPERS);
   static constexpr int NS = 2 * NR;               // columns of S^T: 8 rows' q in its first part, then in its second
   static constexpr int NP = NR > 8 ? 3 * NR : 32; // of O^T: weights' three parts (see o_col)
@@ -1121,22 +1128,23 @@ bool cache8_fits(const Cache8Geom& g) {
   const double units = (double)g.B * g.Hkv * g.nmb * ((g.rows + T - 1) / T + g.visit);
   return units < 5.0e8 && (double)g.B * g.Hkv * g.M < 1.0e9;
 }
-// Query rows of a block.  Up to 8 rows need one group of softmax warps (the 48.5 us
-// above are 59.7 with blocks of 16; D = 128, 43.2 and 45.2).  A tile costs blocks of 32
+// Query rows of a block.  Up to 8 rows need one group of softmax warps (the 48.8 us
+// above are 57.9 with blocks of 16; D = 128, 43.9 and 46.0).  A tile costs blocks of 32
 // nearly twice that of 16, and they read it once where two of 16 both do, one of them
-// from L2.  At D = 256 and 512, where HBM is what bounds the calls, that is as fast, and
-// the accumulators of 32 rows would not fit beside the scores of two CTAs; at D <= 128
-// it is what bounds them (32 requests over 8,192 keys, D = 128: 65.7 and 55.7 us).  With
-// few tiles a CTA the blocks of 16 spread better (16 requests, 2 kv heads, D = 64: 13.9
-// and 15.4 us over up to 5,001 keys, of a cache with 4.2 tiles of 32 rows a CTA; 17.6 and
-// 16.8 with 5,120 each).
+// from L2.  At D = 256 and 512 the accumulators of 32 rows do not fit beside the scores
+// of two CTAs.  At D <= 128 blocks of 32 are faster where CTAs have many tiles (32
+// requests of 32 rows over 8,192 keys each, D = 128: 56.4 us, and 64.8 with 16; over up
+// to 16,384, D = 64: 54.4 and 61.8).  With few the blocks of 16 spread better: 16
+// requests, 2 kv heads, D = 64, 13.4 us, and 14.8 with 32, over up to 5,001 keys, of a
+// cache with 4.2 tiles of 32 rows a CTA.  (The rule knows the cache's rows, not the
+// lengths: 17.4 and 16.5 with 5,120 keys each.)
 void cache8_split(Cache8Geom& g) {
   const long long units = (long long)g.B * g.Hkv * ((g.M + 31) / 32) * tiles_most(g);
   g.nr = g.M <= 8 ? 8 : g.M <= 16 || g.D > 128 || units < 6 * kCtas ? 16 : 32;
   g.nmb = (g.M + g.nr - 1) / g.nr;
   g.lanes = g.nmb < kCtas ? g.nmb : kCtas;
-  // (in tiles; 1, 2, 3 for all: 32 requests of 32 rows over up to 8,192 keys, D = 128, 41.8, 39.5, 38.2 us, and 47.8
-  // without; of 16 rows 28.0, 26.9, 27.3 and 31.3; 8 requests of 32 / 8 heads over up to 2,000 9.4, 9.6, 9.7 and 10.8)
+  // (in tiles; 0, 1, 2, 3 for all: 32 requests of 32 rows over up to 8,192 keys, D = 128, 43.2, 38.8, 37.5, 37.4 us; of
+  // 16 rows 29.3, 26.6, 26.4, 26.5; 8 requests of 32 / 8 heads over up to 2,000 10.9, 9.4, 9.6, 9.7)
   g.visit = g.nr / 16 + 1;
 }
 size_t cache8_workspace_bytes(const Cache8Geom& g) { return c8_ws(g).total; }
