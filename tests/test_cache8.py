@@ -468,7 +468,7 @@ BLOCKS_OF_32 = [
 ]
 
 
-def test_which_blocks_are_tested():
+def test_which_blocks_are_tested(lib):
     """The cases above are of blocks of 32 rows, their likes with fewer tiles, few rows or longer heads of 16 or 8."""
     for B, Hq, Hkv, Lq, D, rows, window, _, block in BLOCKS_OF_32:
         assert rows_of_a_block(B, Hq, Hkv, Lq, rows, D, block, window) == (32 if Hq // Hkv * Lq > 32 else Hq // Hkv * Lq)
